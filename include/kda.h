@@ -77,6 +77,12 @@ typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype; /* dtype of q, k, v and o 
 #define KDA_STATUS_TIMEOUT 8u     /* a tensor-core CTA waited more than 2 s for its own copies
                                      or MMAs and stopped early; its outputs are incomplete */
 
+#define KDA_STATUS_BAD_PAGE 16u  /* a page id >= n_pages, or a position past the page table, was
+                                    skipped */
+#define KDA_STATUS_BAD_TOKEN 32u /* draft verify: a drafted token outside [0, vocab) was refused */
+#define KDA_STATUS_BAD_POSITION 64u /* head norm: a position outside the rotation table; that
+                                       token was not rotated */
+
 /* Message for the most recent non-OK status returned on this thread ("" if none). */
 KDA_API const char* kda_last_error(void);
 
@@ -394,6 +400,160 @@ KDA_API kda_status kda_short_conv(kda_dtype dt, int n_seqs, int total_tokens,
                                   const int32_t* read_slots, const int32_t* write_slots,
                                   void* conv_state, int64_t n_slots, void* out,
                                   uint32_t* status, kda_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Serving operators next to the recurrence: the softmax-attention layers of a hybrid model and
+ * the verification of drafted tokens. Heads have d in {64, 128} channels; query head i reads
+ * key/value head i / (Hq / Hkv). The pages have no counterpart of these calls.
+ *
+ * The K/V cache. k_cache and v_cache are [n_pages, Hkv, 64, d] bytes, 16-byte aligned: e4m3
+ * codes (4 exponent bits, 3 mantissa bits, no infinities) of 64 consecutive tokens of one head.
+ * k_scale and v_scale are [n_pages, Hkv] fp32: a cached value is code * scale. A scale is a
+ * power of two in [2^-100, 2^120], so that dividing by it and multiplying by it are exact.
+ * page_table is device int32 [n, max_pages]: the token at position t of sequence s is in row
+ * t % 64 of page page_table[s, t / 64]. A negative id means that the page is absent: nothing is
+ * stored there, and it is not attended to. An id >= n_pages is treated the same way and sets
+ * KDA_STATUS_BAD_PAGE. A cache may exceed 4 GiB.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Bits of the `flags` argument of kda_head_norm_rope. */
+#define KDA_NORM_L2 1u          /* divide by the 2-norm instead of the root of the mean square */
+#define KDA_ROPE_INTERLEAVED 2u /* rotate pairs (2i, 2i+1) instead of (i, i + rot_dim/2) */
+
+/*
+ * kda_head_norm_rope: norms of queries and keys for each head, and the position rotation in the
+ * same pass. For each token and head, with x in R^d its channels and w the weights:
+ *     y = x / sqrt(mean(x^2) + eps) * w        (sum instead of mean with KDA_NORM_L2)
+ *     (a, b) -> (a cos - b sin, b cos + a sin) for the pairs among the first rot_dim channels,
+ * pair i with cos_sin[pos, i] and cos_sin[pos, rot_dim/2 + i]. All arithmetic is fp32; the result
+ * is rounded once.
+ *   q, k         [tokens, Hq, d] and [tokens, Hk, d] (dtype dt), heads contiguous, tokens
+ *                q_stride and k_stride elements apart (views of a fused projection's rows). Either
+ *                may be NULL with its head count 0.
+ *   q_weight, k_weight  [d] fp32, or NULL for ones.
+ *   cos_sin      [n_pos, rot_dim] fp32: rot_dim/2 cosines, then rot_dim/2 sines. Needed when
+ *                rot_dim > 0. rot_dim: a multiple of 16, 0 .. d (0: no rotation).
+ *   positions    device int32 [tokens], or NULL for 0 .. tokens - 1. A position outside
+ *                [0, n_pos) leaves its token unrotated and sets KDA_STATUS_BAD_POSITION.
+ *   q_out, k_out as q and k with their own strides. Writing in place (same pointer and stride)
+ *                is allowed; any other overlap is not.
+ *   q, k, outputs, weights and cos_sin 16-byte aligned, strides multiples of 16 bytes.
+ */
+KDA_API kda_status kda_head_norm_rope(kda_dtype dt, int tokens, int Hq, int Hk, int d,
+                                      const void* q, int64_t q_stride, const void* k,
+                                      int64_t k_stride, const float* q_weight,
+                                      const float* k_weight, float eps, unsigned flags,
+                                      const float* cos_sin, int64_t n_pos, int rot_dim,
+                                      const int32_t* positions, void* q_out, int64_t qo_stride,
+                                      void* k_out, int64_t ko_stride, uint32_t* status,
+                                      kda_stream_t stream);
+
+/*
+ * kda_cache_write: appends new keys and values to the paged 8-bit cache, quantising them on the
+ * way. Token i of sequence s (packed by cu_seqlens) goes to position start[s] + i.
+ * For each (page, head) that gets new tokens, with m the largest finite |x| among them:
+ *     s_new = 2^ceil(log2(m / 448)), at least 2^-100
+ *     s     = max(scale, s_new) if the page keeps earlier tokens (positions before start[s]),
+ *             else s_new
+ *     codes of the kept tokens become rn_e4m3(code * scale / s); new codes are rn_e4m3(x / s),
+ *     ties to even, saturating at +-448 (infinities too); NaN is stored as the NaN code.
+ * Rows of a page after the last new token hold no defined value.
+ *   k, v        [total_tokens, Hkv, d] (dtype dt), heads contiguous, tokens k_stride and v_stride
+ *               elements apart (multiples of 16 bytes; 16-byte aligned).
+ *   cu_seqlens  device int32 [n_seqs + 1], or NULL for one sequence of total_tokens.
+ *   start       device int32 [n_seqs]; a negative start skips the sequence.
+ *   lens        device int32 [n_seqs] or NULL: only the first lens[s] of the sequence's tokens
+ *               are stored (the rest is the padding of a ragged window).
+ *   A position of max_pages * 64 or more is not stored and sets KDA_STATUS_BAD_PAGE. No page may
+ *   be written through two sequences of one call.
+ *   status      optional device word (KDA_STATUS_BAD_PAGE, KDA_STATUS_BAD_OFFSETS).
+ */
+KDA_API kda_status kda_cache_write(kda_dtype dt, int n_seqs, int total_tokens,
+                                   const int32_t* cu_seqlens, const int32_t* start,
+                                   const int32_t* lens, int Hkv, int d, const void* k,
+                                   int64_t k_stride, const void* v, int64_t v_stride,
+                                   const int32_t* page_table, int max_pages, void* k_cache,
+                                   float* k_scale, void* v_cache, float* v_scale,
+                                   int64_t n_pages, uint32_t* status, kda_stream_t stream);
+
+/*
+ * kda_cache_read: the cached keys and values of positions start[s] .. start[s] + len_s - 1 of
+ * each sequence, packed by cu_seqlens (len_s = cu_seqlens[s+1] - cu_seqlens[s]), as code * scale
+ * in dtype dt. Tokens of absent pages, or of a sequence with a negative start, are zeros.
+ *   k, v  [total_tokens, Hkv, d] outputs, contiguous, 16-byte aligned; either may be NULL.
+ * Other arguments as for kda_cache_write.
+ */
+KDA_API kda_status kda_cache_read(kda_dtype dt, int n_seqs, int total_tokens,
+                                  const int32_t* cu_seqlens, const int32_t* start, int Hkv, int d,
+                                  const int32_t* page_table, int max_pages, const void* k_cache,
+                                  const float* k_scale, const void* v_cache,
+                                  const float* v_scale, int64_t n_pages, void* k, void* v,
+                                  uint32_t* status, kda_stream_t stream);
+
+/*
+ * kda_cache_attention: attention of one decoded token per row, or of a verify window of up to 16
+ * tokens, over the paged 8-bit cache (which already holds the window's own keys and values).
+ * The window's token j of row b is at position start[b] + j and sees positions 0 .. start[b] + j:
+ *     o = sum_t softmax_t(scale * q . k_t) v_t
+ *   q, o        [batch * window, Hq, d] (dtype dt), 16-byte aligned; token j of row b is row
+ *               b * window + j.
+ *   start       device int32 [batch]; a negative start marks a padding row: its o rows are zeros.
+ *   lens        device int32 [batch] or NULL: row b has lens[b] tokens (0 .. window); the o rows
+ *               of the others are zeros.
+ *   A query none of whose positions is present (absent pages, or positions past the page table)
+ *   gets zeros. Cached values that a query does not see do not reach its result, NaN included.
+ *   workspace   at least kda_cache_attention_workspace(...) bytes, 256-byte aligned; contents need
+ *               not be initialised.
+ *   window 1 .. 16 (0 is a no-op); Hq a multiple of Hkv; batch * Hkv at most 2^24;
+ *   max_pages at most 2^24.
+ * Scores, softmax statistics and sums are fp32. With bf16 queries the probabilities enter the
+ * second product rounded to 11 bits; with fp32 queries, queries and probabilities are carried in
+ * two 11-bit parts.
+ */
+KDA_API size_t kda_cache_attention_workspace(int batch, int window, int Hq, int Hkv, int d);
+KDA_API kda_status kda_cache_attention(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d,
+                                       float scale, const void* q, const int32_t* start,
+                                       const int32_t* lens, const int32_t* page_table,
+                                       int max_pages, const void* k_cache, const float* k_scale,
+                                       const void* v_cache, const float* v_scale, int64_t n_pages,
+                                       void* o, void* workspace, size_t ws_bytes,
+                                       uint32_t* status, kda_stream_t stream);
+
+/*
+ * kda_draft_verify: verification of drafted tokens against the target's probabilities, from given
+ * random numbers. Row b drafted lens[b] tokens x_0, x_1, ...; p_j is the target's distribution
+ * for the token at place j, q_j the one that x_j was drawn from. Tokens are taken in order while
+ *     u_accept[b, j] * q_j(x_j) < p_j(x_j)          (fp32)
+ * With n of them taken, one more token is sampled: from max(p_n - q_n, 0) if x_n was refused, from
+ * p_n if all were taken. Sampling uses integer weights, so that the sum's order does not matter:
+ *     w_i = floor(clamp(y_i, 0, 1) * 2^40), y the distribution sampled from (the difference in
+ *     fp32; NaN counts as 0); T = sum_i w_i; r = floor(T * floor(u_sample[b] * 2^24) / 2^24);
+ *     the token is the first i with w_0 + .. + w_i > r.
+ * If max(p_n - q_n, 0) has no weight, p_n is sampled; if p_n has none, the token is -1.
+ *   target_probs [batch, window + 1, vocab] and draft_probs [batch, window, vocab] (dtype dt), rows
+ *                target_stride and draft_stride elements apart, aligned to their element.
+ *                draft_probs NULL: the drafts were not sampled (q_j is 1 at x_j, 0 elsewhere).
+ *   draft_tokens device int32 [batch, window]. One outside [0, vocab) is refused, p_n sampled, and
+ *                KDA_STATUS_BAD_TOKEN set.
+ *   lens         device int32 [batch] or NULL (window for every row). Larger values count as
+ *                window; a negative one marks a padding row: n_accepted 0, tokens and slot -1.
+ *   u_accept     [batch, window], u_sample [batch] fp32 in [0, 1).
+ *   write_slots  device int32 [batch, window + 1] or NULL: the slot table of the
+ *                kda_decode_window call that ran the last token and the drafts.
+ *   tokens       [batch, window + 1] int32 output: the taken drafts, the sampled token, then -1.
+ *   n_accepted   [batch] int32 output.
+ *   resume_slots [batch] int32 output (needs write_slots) or NULL: write_slots[b, n], the slot that
+ *                holds the state after the taken tokens: the next window's read slot.
+ *   window 0 .. 16; vocab 1 .. 2^22.
+ */
+KDA_API kda_status kda_draft_verify(kda_dtype dt, int batch, int window, int vocab,
+                                    const void* target_probs, int64_t target_stride,
+                                    const void* draft_probs, int64_t draft_stride,
+                                    const int32_t* draft_tokens, const int32_t* lens,
+                                    const float* u_accept, const float* u_sample,
+                                    const int32_t* write_slots, int32_t* tokens,
+                                    int32_t* n_accepted, int32_t* resume_slots, uint32_t* status,
+                                    kda_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -66,6 +66,45 @@ kda_status chunked(const char* fn, const ChunkParams& p, kda_dtype dt, void* ws,
   return launch_chunk_tc(p, dt, ws, ws_bytes, s);
 }
 
+int elem_bytes(kda_dtype dt) { return dt == KDA_BF16 ? 2 : 4; }
+
+// A token stride that covers the token's heads and keeps every token 16-byte aligned.
+bool row_stride_ok(int64_t stride, int64_t row, int64_t per16) {
+  return stride >= row && stride % per16 == 0;
+}
+
+kda_status check_head(const char* fn, kda_dtype dt, int d) {
+  KDA_REQUIRE(dt == KDA_F32 || dt == KDA_BF16, KDA_ERR_UNSUPPORTED,
+              std::string(fn) + ": dtype must be KDA_F32 or KDA_BF16");
+  KDA_REQUIRE(d == 64 || d == 128, KDA_ERR_UNSUPPORTED, std::string(fn) + ": d must be 64 or 128");
+  return KDA_OK;
+}
+
+kda_status check_cache(const char* fn, kda_dtype dt, int n_seqs, int total, const int32_t* cu,
+                       const int32_t* start, const int32_t* lens, int Hkv, int d,
+                       const int32_t* table, int max_pages, const void* kc, const float* ks,
+                       const void* vc, const float* vs, int64_t n_pages, const uint32_t* status) {
+  kda_status st = check_head(fn, dt, d);
+  if (st != KDA_OK) return st;
+  const std::string f(fn);
+  KDA_REQUIRE(n_seqs >= 0 && total >= 0, KDA_ERR_INVALID_ARG, f + ": sizes must be >= 0");
+  KDA_REQUIRE(Hkv > 0 && Hkv <= 65535, KDA_ERR_INVALID_ARG, f + ": Hkv must be in 1 .. 65535");
+  KDA_REQUIRE(n_pages > 0 && max_pages > 0 && max_pages <= (1 << 24), KDA_ERR_INVALID_ARG,
+              f + ": n_pages must be > 0, max_pages in 1 .. 2^24");
+  KDA_REQUIRE(cu || n_seqs <= 1, KDA_ERR_INVALID_ARG,
+              f + ": cu_seqlens is required for more than one sequence");
+  KDA_REQUIRE((int64_t)total / kPage + 2 * (int64_t)n_seqs <= 0x7fffffffLL, KDA_ERR_INVALID_ARG,
+              f + ": too many tokens and sequences for one launch");
+  if (n_seqs == 0 || total == 0) return KDA_OK;
+  KDA_REQUIRE(start && table && (!kc || ks) && (!vc || vs), KDA_ERR_INVALID_ARG,
+              f + ": start, page_table and the scales must be non-null");
+  KDA_REQUIRE(aligned(kc, 16) && aligned(vc, 16) && aligned(ks, 4) && aligned(vs, 4) &&
+                  aligned(cu, 4) && aligned(start, 4) && aligned(lens, 4) && aligned(table, 4) &&
+                  aligned(status, 4),
+              KDA_ERR_INVALID_ARG, f + ": misaligned pointer");
+  return KDA_OK;
+}
+
 }  // namespace
 }  // namespace kda
 
@@ -428,6 +467,194 @@ kda_status kda_short_conv(kda_dtype dt, int n_seqs, int total_tokens, const int3
   return launch_short_conv(dt, n_seqs, total_tokens, cu_seqlens, channels, width, x, weight,
                            flags, slots ? read_slots : nullptr, slots ? write_slots : nullptr,
                            conv_state, slots ? n_slots : 0, out, status, (cudaStream_t)stream);
+}
+
+kda_status kda_head_norm_rope(kda_dtype dt, int tokens, int Hq, int Hk, int d, const void* q,
+                              int64_t q_stride, const void* k, int64_t k_stride,
+                              const float* q_weight, const float* k_weight, float eps,
+                              unsigned flags, const float* cos_sin, int64_t n_pos, int rot_dim,
+                              const int32_t* positions, void* q_out, int64_t qo_stride,
+                              void* k_out, int64_t ko_stride, uint32_t* status,
+                              kda_stream_t stream) {
+  kda_status st = check_head("kda_head_norm_rope", dt, d);
+  if (st != KDA_OK) return st;
+  KDA_REQUIRE(tokens >= 0 && Hq >= 0 && Hk >= 0 && (int64_t)Hq + Hk <= 65536,
+              KDA_ERR_INVALID_ARG,
+              "kda_head_norm_rope: tokens, Hq and Hk must be >= 0, Hq + Hk at most 65536");
+  KDA_REQUIRE(rot_dim >= 0 && rot_dim <= d && rot_dim % 16 == 0, KDA_ERR_UNSUPPORTED,
+              "kda_head_norm_rope: rot_dim must be a multiple of 16 in 0 .. d");
+  KDA_REQUIRE((flags & ~(KDA_NORM_L2 | KDA_ROPE_INTERLEAVED)) == 0, KDA_ERR_INVALID_ARG,
+              "kda_head_norm_rope: unknown flag bits");
+  KDA_REQUIRE(eps >= 0.0f, KDA_ERR_INVALID_ARG, "kda_head_norm_rope: eps must be >= 0");
+  if (tokens == 0 || Hq + Hk == 0) return KDA_OK;
+  KDA_REQUIRE((Hq == 0 || (q && q_out)) && (Hk == 0 || (k && k_out)), KDA_ERR_INVALID_ARG,
+              "kda_head_norm_rope: q, k and their outputs must be non-null");
+  KDA_REQUIRE(rot_dim == 0 || (cos_sin && n_pos > 0), KDA_ERR_INVALID_ARG,
+              "kda_head_norm_rope: a rotation needs cos_sin and n_pos > 0");
+  const int64_t per16 = 16 / elem_bytes(dt);
+  KDA_REQUIRE((Hq == 0 || (row_stride_ok(q_stride, (int64_t)Hq * d, per16) &&
+                           row_stride_ok(qo_stride, (int64_t)Hq * d, per16))) &&
+                  (Hk == 0 || (row_stride_ok(k_stride, (int64_t)Hk * d, per16) &&
+                               row_stride_ok(ko_stride, (int64_t)Hk * d, per16))),
+              KDA_ERR_INVALID_ARG,
+              "kda_head_norm_rope: token strides must cover the heads and be multiples of 16 bytes");
+  KDA_REQUIRE(aligned(q, 16) && aligned(k, 16) && aligned(q_out, 16) && aligned(k_out, 16) &&
+                  aligned(q_weight, 16) && aligned(k_weight, 16) && aligned(cos_sin, 16) &&
+                  aligned(positions, 4) && aligned(status, 4),
+              KDA_ERR_INVALID_ARG, "kda_head_norm_rope: misaligned pointer");
+  KDA_REQUIRE((q != q_out || q_stride == qo_stride) && (k != k_out || k_stride == ko_stride),
+              KDA_ERR_INVALID_ARG, "kda_head_norm_rope: in place needs equal strides");
+  HeadNormParams p{};
+  p.q.x = q; p.q.out = q_out; p.q.w = q_weight; p.q.H = Hq;
+  p.q.x_stride = q_stride; p.q.out_stride = qo_stride;
+  p.k.x = k; p.k.out = k_out; p.k.w = k_weight; p.k.H = Hk;
+  p.k.x_stride = k_stride; p.k.out_stride = ko_stride;
+  p.tokens = tokens; p.eps = eps; p.flags = flags; p.cos_sin = cos_sin; p.n_pos = n_pos;
+  p.rot = rot_dim; p.positions = positions; p.status = status;
+  return launch_head_norm(p, dt, d, (cudaStream_t)stream);
+}
+
+kda_status kda_cache_write(kda_dtype dt, int n_seqs, int total_tokens, const int32_t* cu_seqlens,
+                           const int32_t* start, const int32_t* lens, int Hkv, int d,
+                           const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           const int32_t* page_table, int max_pages, void* k_cache,
+                           float* k_scale, void* v_cache, float* v_scale, int64_t n_pages,
+                           uint32_t* status, kda_stream_t stream) {
+  const char* fn = "kda_cache_write";
+  kda_status st = check_cache(fn, dt, n_seqs, total_tokens, cu_seqlens, start, lens, Hkv, d,
+                              page_table, max_pages, k_cache, k_scale, v_cache, v_scale, n_pages,
+                              status);
+  if (st != KDA_OK || n_seqs == 0 || total_tokens == 0) return st;
+  KDA_REQUIRE(k && v && k_cache && v_cache, KDA_ERR_INVALID_ARG,
+              "kda_cache_write: k, v, k_cache and v_cache must be non-null");
+  const int64_t per16 = 16 / elem_bytes(dt);
+  KDA_REQUIRE(row_stride_ok(k_stride, (int64_t)Hkv * d, per16) &&
+                  row_stride_ok(v_stride, (int64_t)Hkv * d, per16) && aligned(k, 16) &&
+                  aligned(v, 16),
+              KDA_ERR_INVALID_ARG,
+              "kda_cache_write: k and v must be 16-byte aligned, their token strides must cover "
+              "the heads and be multiples of 16 bytes");
+  CacheParams p{};
+  p.n_seqs = n_seqs; p.total = total_tokens; p.cu = cu_seqlens; p.start = start; p.lens = lens;
+  p.H = Hkv; p.table = page_table; p.max_pages = max_pages; p.n_pages = n_pages;
+  p.x[0] = const_cast<void*>(k); p.x[1] = const_cast<void*>(v);
+  p.stride[0] = k_stride; p.stride[1] = v_stride;
+  p.code[0] = (uint8_t*)k_cache; p.code[1] = (uint8_t*)v_cache;
+  p.scale[0] = k_scale; p.scale[1] = v_scale; p.status = status;
+  return launch_cache_write(p, dt, d, (cudaStream_t)stream);
+}
+
+kda_status kda_cache_read(kda_dtype dt, int n_seqs, int total_tokens, const int32_t* cu_seqlens,
+                          const int32_t* start, int Hkv, int d, const int32_t* page_table,
+                          int max_pages, const void* k_cache, const float* k_scale,
+                          const void* v_cache, const float* v_scale, int64_t n_pages, void* k,
+                          void* v, uint32_t* status, kda_stream_t stream) {
+  const char* fn = "kda_cache_read";
+  kda_status st = check_cache(fn, dt, n_seqs, total_tokens, cu_seqlens, start, nullptr, Hkv, d,
+                              page_table, max_pages, k_cache, k_scale, v_cache, v_scale, n_pages,
+                              status);
+  if (st != KDA_OK || n_seqs == 0 || total_tokens == 0) return st;
+  KDA_REQUIRE((k || v) && (!k || k_cache) && (!v || v_cache), KDA_ERR_INVALID_ARG,
+              "kda_cache_read: k or v must be non-null, with its cache");
+  KDA_REQUIRE(aligned(k, 16) && aligned(v, 16), KDA_ERR_INVALID_ARG,
+              "kda_cache_read: k and v must be 16-byte aligned");
+  CacheParams p{};
+  p.n_seqs = n_seqs; p.total = total_tokens; p.cu = cu_seqlens; p.start = start;
+  p.H = Hkv; p.table = page_table; p.max_pages = max_pages; p.n_pages = n_pages;
+  p.x[0] = k; p.x[1] = v;
+  p.stride[0] = p.stride[1] = (int64_t)Hkv * d;
+  p.code[0] = (uint8_t*)const_cast<void*>(k_cache);
+  p.code[1] = (uint8_t*)const_cast<void*>(v_cache);
+  p.scale[0] = const_cast<float*>(k_scale); p.scale[1] = const_cast<float*>(v_scale);
+  p.status = status;
+  return launch_cache_read(p, dt, d, (cudaStream_t)stream);
+}
+
+size_t kda_cache_attention_workspace(int batch, int window, int Hq, int Hkv, int d) {
+  if (batch <= 0 || window <= 0 || window > kMaxWindow || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 ||
+      (d != 64 && d != 128))
+    return 0;
+  return cache_attn_workspace_bytes(batch, window, Hq, Hkv, d);
+}
+
+kda_status kda_cache_attention(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d,
+                               float scale, const void* q, const int32_t* start,
+                               const int32_t* lens, const int32_t* page_table, int max_pages,
+                               const void* k_cache, const float* k_scale, const void* v_cache,
+                               const float* v_scale, int64_t n_pages, void* o, void* workspace,
+                               size_t ws_bytes, uint32_t* status, kda_stream_t stream) {
+  const char* fn = "kda_cache_attention";
+  KDA_REQUIRE(window >= 0 && window <= kMaxWindow, KDA_ERR_UNSUPPORTED,
+              "kda_cache_attention: window must be in 0 .. 16");
+  KDA_REQUIRE(batch >= 0, KDA_ERR_INVALID_ARG, "kda_cache_attention: batch must be >= 0");
+  kda_status st = check_head(fn, dt, d);
+  if (st != KDA_OK) return st;
+  KDA_REQUIRE(Hkv > 0 && Hq > 0 && Hq % Hkv == 0, KDA_ERR_INVALID_ARG,
+              "kda_cache_attention: Hq must be a positive multiple of Hkv");
+  KDA_REQUIRE((int64_t)batch * Hkv <= (1 << 24) && (int64_t)batch * window * Hq <= (1 << 30),
+              KDA_ERR_INVALID_ARG,
+              "kda_cache_attention: batch * Hkv must not exceed 2^24, nor batch * window * Hq 2^30");
+  if (batch == 0 || window == 0) return KDA_OK;
+  KDA_REQUIRE(start, KDA_ERR_INVALID_ARG, "kda_cache_attention: start must be non-null");
+  st = check_cache(fn, dt, batch, batch, start, start, lens, Hkv, d, page_table, max_pages, k_cache,
+                   k_scale, v_cache, v_scale, n_pages, status);
+  if (st != KDA_OK) return st;
+  KDA_REQUIRE(q && o && k_cache && v_cache, KDA_ERR_INVALID_ARG,
+              "kda_cache_attention: q, o, k_cache and v_cache must be non-null");
+  KDA_REQUIRE(aligned(q, 16) && aligned(o, 16), KDA_ERR_INVALID_ARG,
+              "kda_cache_attention: q and o must be 16-byte aligned");
+  const size_t need = cache_attn_workspace_bytes(batch, window, Hq, Hkv, d);
+  KDA_REQUIRE(need == 0 || (workspace && ws_bytes >= need && aligned(workspace, 256)),
+              KDA_ERR_WORKSPACE,
+              "kda_cache_attention: workspace missing, too small or not 256-byte aligned (need " +
+                  std::to_string(need) + " bytes)");
+  CacheAttnParams p{};
+  p.batch = batch; p.window = window; p.Hq = Hq; p.Hkv = Hkv; p.scale = scale;
+  p.q = q; p.start = start; p.lens = lens; p.table = page_table; p.max_pages = max_pages;
+  p.n_pages = n_pages; p.kc = (const uint8_t*)k_cache; p.ks = k_scale;
+  p.vc = (const uint8_t*)v_cache; p.vs = v_scale; p.o = o; p.ws = workspace; p.status = status;
+  return launch_cache_attn(p, dt, d, (cudaStream_t)stream);
+}
+
+kda_status kda_draft_verify(kda_dtype dt, int batch, int window, int vocab,
+                            const void* target_probs, int64_t target_stride,
+                            const void* draft_probs, int64_t draft_stride,
+                            const int32_t* draft_tokens, const int32_t* lens,
+                            const float* u_accept, const float* u_sample,
+                            const int32_t* write_slots, int32_t* tokens, int32_t* n_accepted,
+                            int32_t* resume_slots, uint32_t* status, kda_stream_t stream) {
+  KDA_REQUIRE(dt == KDA_F32 || dt == KDA_BF16, KDA_ERR_UNSUPPORTED,
+              "kda_draft_verify: dtype must be KDA_F32 or KDA_BF16");
+  KDA_REQUIRE(window >= 0 && window <= kMaxWindow, KDA_ERR_UNSUPPORTED,
+              "kda_draft_verify: window must be in 0 .. 16");
+  KDA_REQUIRE(vocab >= 1 && vocab <= (1 << 22), KDA_ERR_UNSUPPORTED,
+              "kda_draft_verify: vocab must be in 1 .. 2^22");
+  KDA_REQUIRE(batch >= 0 && batch <= (1 << 24), KDA_ERR_INVALID_ARG,
+              "kda_draft_verify: batch must be in 0 .. 2^24");
+  if (batch == 0) return KDA_OK;
+  KDA_REQUIRE(target_probs && u_sample && tokens && n_accepted &&
+                  (window == 0 || (draft_tokens && u_accept)),
+              KDA_ERR_INVALID_ARG,
+              "kda_draft_verify: target_probs, draft_tokens, u_accept, u_sample, tokens and "
+              "n_accepted must be non-null");
+  KDA_REQUIRE(!resume_slots || write_slots, KDA_ERR_INVALID_ARG,
+              "kda_draft_verify: resume_slots needs write_slots");
+  KDA_REQUIRE(target_stride >= vocab && (!draft_probs || draft_stride >= vocab),
+              KDA_ERR_INVALID_ARG, "kda_draft_verify: row strides must be at least vocab");
+  const size_t eb = (size_t)elem_bytes(dt);
+  KDA_REQUIRE(aligned(target_probs, eb) && aligned(draft_probs, eb) && aligned(draft_tokens, 4) &&
+                  aligned(lens, 4) && aligned(u_accept, 4) && aligned(u_sample, 4) &&
+                  aligned(write_slots, 4) && aligned(tokens, 4) && aligned(n_accepted, 4) &&
+                  aligned(resume_slots, 4) && aligned(status, 4),
+              KDA_ERR_INVALID_ARG, "kda_draft_verify: misaligned pointer");
+  VerifyParams p{};
+  p.batch = batch; p.window = window; p.vocab = vocab;
+  p.target = target_probs; p.target_stride = target_stride;
+  p.draft = draft_probs; p.draft_stride = draft_stride;
+  p.drafts = draft_tokens; p.lens = lens; p.ua = u_accept; p.us = u_sample;
+  p.slots = write_slots; p.tokens = tokens; p.n_accepted = n_accepted; p.resume = resume_slots;
+  p.status = status;
+  return launch_verify(p, dt, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,144 @@
+// Norms of queries and keys for each head, with the position rotation in the same pass
+// (kda_head_norm_rope).
+//
+// For a (token, head) row x in R^d: y = x / sqrt(mean(x^2) + eps) * w (sum for the 2-norm), then
+// (a, b) -> (a cos - b sin, b cos + a sin) on the rotated pairs. Everything is fp32; the row is
+// rounded to its type once, after the rotation.
+//
+// The pass reads and writes each row once (2 d elements) for some 10 operations per element, so
+// it is HBM-bound. A row is held by d * sizeof(T) / 16 consecutive lanes, 16 bytes each, so its
+// sum of squares is a few shuffles and a half-split pair's partner one more; the 16-byte chunks
+// never straddle the halves because rot_dim is a multiple of 16. A warp takes kHeads heads of
+// one token, so that the token's cosines and sines are loaded once into registers for all of
+// them, and issues every row load before it reduces the first.
+#include "kda_internal.cuh"
+#include "kda_fp8.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kUnroll = 4;  // row loads in flight per lane
+
+template <class T, int D>
+__global__ void __launch_bounds__(kWarps * 32)
+head_norm_kernel(const HeadNormParams p, int groups) {
+  constexpr int N = Vec16<T>::N;
+  constexpr int LPR = D / N;        // lanes per row
+  constexpr int RPW = 32 / LPR;     // rows a warp loads at once
+  constexpr int HEADS = RPW * kUnroll;
+  const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
+  const int64_t tok = item / groups;
+  if (tok >= p.tokens) return;
+  const int h0 = (int)(item - tok * groups) * HEADS + sub;
+  const int H = p.q.H + p.k.H;
+  const int e0 = l * N;  // first channel of this lane
+
+  uint4 raw[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int h = h0 + u * RPW;
+    raw[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (h < H) {
+      const bool isq = h < p.q.H;
+      const HeadNormSide& s = isq ? p.q : p.k;
+      const T* x = (const T*)s.x + tok * s.x_stride + (int64_t)(isq ? h : h - p.q.H) * D + e0;
+      raw[u] = *reinterpret_cast<const uint4*>(x);
+    }
+  }
+
+  // this lane's cosines and sines
+  const int half = p.rot / 2;
+  const bool inter = (p.flags & KDA_ROPE_INTERLEAVED) != 0;
+  float cs[N], sn[N];
+  bool rotate = e0 < p.rot;
+  if (p.rot) {
+    const int64_t pos = p.positions ? (int64_t)p.positions[tok] : tok;
+    if (pos < 0 || pos >= p.n_pos) {
+      if (lane == 0 && h0 == 0 && p.status) atomicOr(p.status, KDA_STATUS_BAD_POSITION);
+      rotate = false;
+    }
+    if (rotate) {
+      const float* row = p.cos_sin + pos * p.rot;
+      if (inter) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+          cs[2 * i] = cs[2 * i + 1] = row[e0 / 2 + i];
+          sn[2 * i + 1] = row[half + e0 / 2 + i];
+          sn[2 * i] = -sn[2 * i + 1];
+        }
+      } else {
+        const int i0 = e0 < half ? e0 : e0 - half;
+        const float sign = e0 < half ? -1.0f : 1.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          cs[i] = row[i0 + i];
+          sn[i] = sign * row[half + i0 + i];
+        }
+      }
+    }
+  }
+  // lane that holds the partner chunk of a half-split pair (itself where nothing is rotated)
+  const int shift = half / N;
+  const int partner = (inter || !rotate) ? lane : (e0 < half ? lane + shift : lane - shift);
+
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int h = h0 + u * RPW;
+    float x[N];
+    Vec16<T>::unpack(raw[u], x);
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float r = rsqrtf(((p.flags & KDA_NORM_L2) ? ss : ss * (1.0f / D)) + p.eps);
+    const bool isq = h < p.q.H;
+    const HeadNormSide& s = isq ? p.q : p.k;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] *= r;
+    if (s.w && h < H) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] *= s.w[e0 + i];
+    }
+    float y[N];
+    if (inter) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) y[i] = x[i ^ 1];
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], partner);
+    }
+    if (rotate) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = fmaf(x[i], cs[i], y[i] * sn[i]);
+    }
+    if (h < H) {
+      T* out = (T*)s.out + tok * s.out_stride + (int64_t)(isq ? h : h - p.q.H) * D + e0;
+      *reinterpret_cast<uint4*>(out) = Vec16<T>::pack(x);
+    }
+  }
+}
+
+template <class T, int D>
+kda_status launch_t(const HeadNormParams& p, cudaStream_t s) {
+  constexpr int HEADS = 32 / (D / Vec16<T>::N) * kUnroll;
+  const int groups = (p.q.H + p.k.H + HEADS - 1) / HEADS;
+  const int64_t blocks = ((int64_t)p.tokens * groups + kWarps - 1) / kWarps;
+  if (blocks > 0x7fffffffLL)
+    return set_error(KDA_ERR_INVALID_ARG, "kda_head_norm_rope: too many tokens x heads");
+  head_norm_kernel<T, D><<<(unsigned)blocks, kWarps * 32, 0, s>>>(p, groups);
+  count_launches(1);
+  return check_launch("kda_head_norm_rope");
+}
+
+}  // namespace
+
+kda_status launch_head_norm(const HeadNormParams& p, kda_dtype dt, int d, cudaStream_t s) {
+  if (dt == KDA_BF16)
+    return d == 128 ? launch_t<__nv_bfloat16, 128>(p, s) : launch_t<__nv_bfloat16, 64>(p, s);
+  return d == 128 ? launch_t<float, 128>(p, s) : launch_t<float, 64>(p, s);
+}
+
+}  // namespace kda

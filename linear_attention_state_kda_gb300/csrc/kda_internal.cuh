@@ -107,6 +107,86 @@ kda_status launch_short_conv(kda_dtype dt, int n_seqs, int total, const int32_t*
                              const int32_t* read_slots, const int32_t* write_slots, void* hist,
                              int64_t n_slots, void* out, uint32_t* status, cudaStream_t s);
 
+// Per-head norm of q and k with the position rotation.
+struct HeadNormSide {
+  const void* x;
+  void* out;
+  const float* w;  // [d] or nullptr (ones)
+  int64_t x_stride, out_stride;  // elements between tokens
+  int H;
+};
+struct HeadNormParams {
+  HeadNormSide q, k;
+  int tokens;
+  float eps;
+  unsigned flags;
+  const float* cos_sin;  // [n_pos, rot]
+  const int32_t* positions;
+  int64_t n_pos;
+  int rot;
+  uint32_t* status;
+};
+kda_status launch_head_norm(const HeadNormParams& p, kda_dtype dt, int d, cudaStream_t s);
+
+// Paged 8-bit K/V cache: [n_pages, H, 64, d] e4m3 codes with an fp32 scale per (page, head).
+constexpr int kPage = 64;
+struct CacheParams {
+  int n_seqs, total;
+  const int32_t* cu;     // [n_seqs + 1] or nullptr (one sequence)
+  const int32_t* start;  // [n_seqs]
+  const int32_t* lens;   // [n_seqs] or nullptr
+  int H;
+  const int32_t* table;  // [n_seqs, max_pages]
+  int max_pages;
+  int64_t n_pages;
+  void* x[2];            // k, v: token rows read (write) or written (read)
+  int64_t stride[2];     // elements between tokens
+  uint8_t* code[2];
+  float* scale[2];
+  uint32_t* status;
+};
+kda_status launch_cache_write(const CacheParams& p, kda_dtype dt, int d, cudaStream_t s);
+kda_status launch_cache_read(const CacheParams& p, kda_dtype dt, int d, cudaStream_t s);
+
+// Attention of up to kMaxWindow query tokens per row over the cache.
+struct CacheAttnParams {
+  int batch, window, Hq, Hkv;
+  float scale;
+  const void* q;
+  const int32_t* start;
+  const int32_t* lens;
+  const int32_t* table;
+  int max_pages;
+  int64_t n_pages;
+  const uint8_t* kc;
+  const float* ks;
+  const uint8_t* vc;
+  const float* vs;
+  void* o;
+  void* ws;
+  uint32_t* status;
+};
+size_t cache_attn_workspace_bytes(int batch, int window, int Hq, int Hkv, int d);
+kda_status launch_cache_attn(const CacheAttnParams& p, kda_dtype dt, int d, cudaStream_t s);
+
+// Verification of drafted tokens.
+struct VerifyParams {
+  int batch, window, vocab;
+  const void* target;
+  const void* draft;  // or nullptr: one-hot drafts
+  int64_t target_stride, draft_stride;
+  const int32_t* drafts;
+  const int32_t* lens;
+  const float* ua;
+  const float* us;
+  const int32_t* slots;
+  int32_t* tokens;
+  int32_t* n_accepted;
+  int32_t* resume;
+  uint32_t* status;
+};
+kda_status launch_verify(const VerifyParams& p, kda_dtype dt, cudaStream_t s);
+
 // Package scan.
 size_t scan_workspace_bytes(int n_seqs, int max_segs, int H, int dk, int dv);
 kda_status launch_scan(int n_seqs, int n_segs, const int32_t* seq_seg_offsets, int max_segs,

@@ -18,7 +18,10 @@ KDA_F32, KDA_BF16 = 0, 1
 DECODE_BETA_LOGIT = 1
 CONV_SILU = 1
 MAX_WINDOW = 16
+NORM_L2, ROPE_INTERLEAVED = 1, 2
+PAGE = 64  # tokens of a page of the 8-bit cache
 STATUS_BAD_SLOT, STATUS_BAD_OFFSETS, STATUS_TIMEOUT = 1, 4, 8
+STATUS_BAD_PAGE, STATUS_BAD_TOKEN, STATUS_BAD_POSITION = 16, 32, 64
 
 _lib = None
 
@@ -82,6 +85,21 @@ def lib():
     L.kda_slot_copy.argtypes = [I, P, P, I64, P, P, I64, I64, P, P]
     L.kda_short_conv.restype = I
     L.kda_short_conv.argtypes = [I, I, I, P, I, I, P, P, ctypes.c_uint, P, P, P, I64, P, P, P]
+    L.kda_head_norm_rope.restype = I
+    L.kda_head_norm_rope.argtypes = [I, I, I, I, I, P, I64, P, I64, P, P, F, ctypes.c_uint, P, I64,
+                                     I, P, P, I64, P, I64, P, P]
+    L.kda_cache_write.restype = I
+    L.kda_cache_write.argtypes = [I, I, I, P, P, P, I, I, P, I64, P, I64, P, I, P, P, P, P, I64, P,
+                                  P]
+    L.kda_cache_read.restype = I
+    L.kda_cache_read.argtypes = [I, I, I, P, P, I, I, P, I, P, P, P, P, I64, P, P, P, P]
+    L.kda_cache_attention_workspace.restype = Z
+    L.kda_cache_attention_workspace.argtypes = [I, I, I, I, I]
+    L.kda_cache_attention.restype = I
+    L.kda_cache_attention.argtypes = [I, I, I, I, I, I, F, P, P, P, P, I, P, P, P, P, I64, P, P, Z,
+                                      P, P]
+    L.kda_draft_verify.restype = I
+    L.kda_draft_verify.argtypes = [I, I, I, I, P, I64, P, I64, P, P, P, P, P, P, P, P, P, P]
     _lib = L
     return L
 
@@ -421,3 +439,205 @@ def short_conv(x, weight, cu_seqlens=None, silu=False, read_slots=None, write_sl
                                 _stream(stream)))
     return out
 
+
+def _heads(t, name):
+    """Token stride of [tokens, H, d] rows whose heads are contiguous (any token stride)."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be [tokens, heads, d] with contiguous heads")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _same(dtype, *ts):
+    for t in ts:
+        if t is not None and t.dtype != dtype:
+            raise TypeError(f"expected {dtype} tensors")
+
+
+def _cache(k_cache, k_scale, v_cache, v_scale, page_table, rows):
+    """Checks a cache's four tensors and its page table; returns (n_pages, Hkv, d, max_pages)."""
+    _contig(k_cache, k_scale, v_cache, v_scale, page_table)
+    _int32(page_table)
+    _same(torch.float32, k_scale, v_scale)
+    if k_cache.dtype not in (torch.float8_e4m3fn, torch.uint8) or v_cache.dtype != k_cache.dtype:
+        raise TypeError("the caches must be float8_e4m3fn (or uint8 codes)")
+    n_pages, H, page, d = k_cache.shape
+    if page != PAGE or v_cache.shape != k_cache.shape:
+        raise ValueError("the caches must both be [n_pages, Hkv, 64, d]")
+    if k_scale.shape != (n_pages, H) or v_scale.shape != (n_pages, H):
+        raise ValueError("the scales must be [n_pages, Hkv]")
+    if page_table.dim() != 2 or page_table.shape[0] != rows:
+        raise ValueError("page_table must be [rows, max_pages], a row for each entry of start")
+    return n_pages, H, d, page_table.shape[1]
+
+
+def head_norm_rope(q, k, q_weight=None, k_weight=None, eps=1e-6, l2=False, cos_sin=None,
+                   positions=None, interleaved=False, q_out=None, k_out=None, status=None,
+                   stream=None):
+    """kda_head_norm_rope: RMS norm (2-norm with l2) of each head of q [T, Hq, d] and k [T, Hk, d]
+    with per-channel weights, then the rotation by row `positions[t]` of cos_sin [n_pos, rot_dim]
+    (none when cos_sin is None). q and k may be views of a fused projection's rows; either may be
+    None. q_out = q (k_out = k) works in place. Returns (q_out, k_out)."""
+    x = q if q is not None else k
+    T, _, d = x.shape
+    _contig(q_weight, k_weight, cos_sin, positions)
+    _int32(positions)
+    _same(torch.float32, q_weight, k_weight, cos_sin)
+    _same(x.dtype, q, k, q_out, k_out)
+    for t, w, name in ((q, q_weight, "q"), (k, k_weight, "k")):
+        if t is not None and (t.shape[0] != T or t.shape[2] != d):
+            raise ValueError("q and k must have the same tokens and head size")
+        if w is not None and w.numel() != d:
+            raise ValueError(f"{name}_weight must hold d values")
+    if positions is not None and positions.numel() != T:
+        raise ValueError("positions must hold one entry per token")
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    if (q is not None and q_out.shape != q.shape) or (k is not None and k_out.shape != k.shape):
+        raise ValueError("outputs must have the shapes of q and k")
+    Hq, qs, qos = (0, 0, 0) if q is None else (q.shape[1], _heads(q, "q"), _heads(q_out, "q_out"))
+    Hk, ks, kos = (0, 0, 0) if k is None else (k.shape[1], _heads(k, "k"), _heads(k_out, "k_out"))
+    n_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
+    flags = (NORM_L2 if l2 else 0) | (ROPE_INTERLEAVED if interleaved else 0)
+    _check(lib().kda_head_norm_rope(_dt(x), T, Hq, Hk, d, _ptr(q), qs, _ptr(k), ks,
+                                    _ptr(q_weight), _ptr(k_weight), float(eps), flags,
+                                    _ptr(cos_sin), n_pos, rot, _ptr(positions), _ptr(q_out), qos,
+                                    _ptr(k_out), kos, _ptr(status), _stream(stream)))
+    return q_out, k_out
+
+
+def cache_write(k, v, start, page_table, k_cache, k_scale, v_cache, v_scale, cu_seqlens=None,
+                lens=None, status=None, stream=None):
+    """kda_cache_write: quantises k and v [T, Hkv, d] (views of a fused projection's rows are fine)
+    into the paged cache [n_pages, Hkv, 64, d] with scales [n_pages, Hkv], token i of sequence s at
+    position start[s] + i. The caches and scales are updated in place."""
+    _contig(start, cu_seqlens, lens)
+    _int32(start, cu_seqlens, lens)
+    _same(k.dtype, v)
+    n = start.numel()
+    n_pages, H, d, max_pages = _cache(k_cache, k_scale, v_cache, v_scale, page_table, n)
+    if k.shape != v.shape or k.shape[1:] != (H, d):
+        raise ValueError("k and v must be [tokens, Hkv, d] of the cache")
+    if (cu_seqlens is not None and cu_seqlens.numel() != n + 1) or \
+            (lens is not None and lens.numel() != n):
+        raise ValueError("cu_seqlens must hold n + 1 and lens n entries")
+    _check(lib().kda_cache_write(_dt(k), n, k.shape[0], _ptr(cu_seqlens), _ptr(start), _ptr(lens),
+                                 H, d, _ptr(k), _heads(k, "k"), _ptr(v), _heads(v, "v"),
+                                 _ptr(page_table), max_pages, _ptr(k_cache), _ptr(k_scale),
+                                 _ptr(v_cache), _ptr(v_scale), n_pages, _ptr(status),
+                                 _stream(stream)))
+
+
+def cache_read(start, page_table, k_cache, k_scale, v_cache, v_scale, total_tokens,
+               cu_seqlens=None, dtype=torch.bfloat16, k=None, v=None, status=None, stream=None):
+    """kda_cache_read: cached keys and values of positions start[s] .. of each sequence, packed by
+    cu_seqlens (total_tokens rows in all). Returns (k, v), [total_tokens, Hkv, d] of `dtype`."""
+    _contig(start, cu_seqlens, k, v)
+    _int32(start, cu_seqlens)
+    n = start.numel()
+    n_pages, H, d, max_pages = _cache(k_cache, k_scale, v_cache, v_scale, page_table, n)
+    if cu_seqlens is not None and cu_seqlens.numel() != n + 1:
+        raise ValueError("cu_seqlens must hold n + 1 entries")
+    if k is None:
+        k = torch.empty(total_tokens, H, d, dtype=dtype, device=k_cache.device)
+    if v is None:
+        v = torch.empty(total_tokens, H, d, dtype=dtype, device=k_cache.device)
+    if k.shape != (total_tokens, H, d) or v.shape != k.shape:
+        raise ValueError("k and v must be [total_tokens, Hkv, d]")
+    _same(k.dtype, v)
+    _check(lib().kda_cache_read(_dt(k), n, int(total_tokens), _ptr(cu_seqlens), _ptr(start), H, d,
+                                _ptr(page_table), max_pages, _ptr(k_cache), _ptr(k_scale),
+                                _ptr(v_cache), _ptr(v_scale), n_pages, _ptr(k), _ptr(v),
+                                _ptr(status), _stream(stream)))
+    return k, v
+
+
+def cache_attention_workspace(batch, window, Hq, Hkv, d):
+    """kda_cache_attention_workspace: scratch bytes of cache_attention."""
+    return int(lib().kda_cache_attention_workspace(batch, window, Hq, Hkv, d))
+
+
+def cache_attention(q, start, page_table, k_cache, k_scale, v_cache, v_scale, scale=1.0, lens=None,
+                    o=None, workspace=None, status=None, stream=None):
+    """kda_cache_attention: q [batch*window, Hq, d] or [batch, window, Hq, d], the window's token j
+    of row b at position start[b] + j, seeing the cached positions 0 .. start[b] + j. Returns o,
+    shaped like q."""
+    _contig(q, start, lens, o)
+    _int32(start, lens)
+    B = start.numel()
+    n_pages, Hkv, d, max_pages = _cache(k_cache, k_scale, v_cache, v_scale, page_table, B)
+    Hq = q.shape[-2]
+    if q.shape[-1] != d:
+        raise ValueError("q and the cache differ in head size")
+    W = q.numel() // (B * Hq * d) if B else 0
+    if q.numel() != B * W * Hq * d:
+        raise ValueError("q must hold batch x window tokens")
+    if lens is not None and lens.numel() != B:
+        raise ValueError("lens must hold one entry per row")
+    if o is None:
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _same(q.dtype, o)
+    if o.numel() != q.numel():
+        raise ValueError("o must have the shape of q")
+    if workspace is None:
+        need = cache_attention_workspace(B, W, Hq, Hkv, d)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().kda_cache_attention(_dt(q), B, W, Hq, Hkv, d, float(scale), _ptr(q), _ptr(start),
+                                     _ptr(lens), _ptr(page_table), max_pages, _ptr(k_cache),
+                                     _ptr(k_scale), _ptr(v_cache), _ptr(v_scale), n_pages, _ptr(o),
+                                     _ptr(workspace), ws_bytes, _ptr(status), _stream(stream)))
+    return o
+
+
+def _rows3(t, name):
+    """Row stride of [batch, places, vocab] rows at one stride, entries contiguous."""
+    b, n, v = t.shape
+    s = t.stride(1) if n > 1 else (t.stride(0) if b > 1 else v)
+    if (v > 1 and t.stride(2) != 1) or (b > 1 and t.stride(0) != n * s):
+        raise ValueError(f"{name} must have contiguous entries and evenly spaced rows")
+    return s
+
+
+def draft_verify(target_probs, draft_tokens, u_accept, u_sample, draft_probs=None, lens=None,
+                 write_slots=None, tokens=None, n_accepted=None, resume_slots=None, status=None,
+                 stream=None):
+    """kda_draft_verify: takes the drafts [batch, window] in order while u * q(x) < p(x), then
+    samples one token from the rest of p (target_probs [batch, window+1, vocab], draft_probs
+    [batch, window, vocab] or None for drafts that were not sampled). Returns (n_accepted [batch],
+    tokens [batch, window+1] padded with -1, resume_slots [batch]: write_slots[b, n_accepted[b]],
+    the slot to resume the recurrent state from, or None without write_slots)."""
+    _contig(draft_tokens, u_accept, u_sample, lens, write_slots, tokens, n_accepted, resume_slots)
+    _int32(draft_tokens, lens, write_slots, tokens, n_accepted, resume_slots)
+    _same(torch.float32, u_accept, u_sample)
+    _same(target_probs.dtype, draft_probs)
+    B, W1, V = target_probs.shape
+    W = W1 - 1
+    if draft_tokens.shape != (B, W) or u_accept.shape != (B, W) or u_sample.shape != (B,):
+        raise ValueError("draft_tokens and u_accept must be [batch, window], u_sample [batch]")
+    if draft_probs is not None and draft_probs.shape != (B, W, V):
+        raise ValueError("draft_probs must be [batch, window, vocab]")
+    if lens is not None and lens.numel() != B:
+        raise ValueError("lens must hold one entry per row")
+    if write_slots is not None and write_slots.shape != (B, W1):
+        raise ValueError("write_slots must be [batch, window + 1]")
+    dev = target_probs.device
+    if tokens is None:
+        tokens = torch.empty(B, W1, dtype=torch.int32, device=dev)
+    if n_accepted is None:
+        n_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+    if resume_slots is None and write_slots is not None:
+        resume_slots = torch.empty(B, dtype=torch.int32, device=dev)
+    if tokens.shape != (B, W1) or n_accepted.numel() != B or \
+            (resume_slots is not None and resume_slots.numel() != B):
+        raise ValueError("outputs must be tokens [batch, window + 1], n_accepted and resume_slots "
+                         "[batch]")
+    ds = 0 if draft_probs is None or W == 0 else _rows3(draft_probs, "draft_probs")
+    _check(lib().kda_draft_verify(_dt(target_probs), B, W, V, _ptr(target_probs),
+                                  _rows3(target_probs, "target_probs"),
+                                  _ptr(draft_probs) if ds else None, ds, _ptr(draft_tokens),
+                                  _ptr(lens), _ptr(u_accept), _ptr(u_sample), _ptr(write_slots),
+                                  _ptr(tokens), _ptr(n_accepted), _ptr(resume_slots), _ptr(status),
+                                  _stream(stream)))
+    return n_accepted, tokens, resume_slots
