@@ -2,119 +2,728 @@
 // (kda_cache_attention): o = sum_t softmax_t(scale q . k_t) v_t in one pass over the cache with
 // the running maximum and sum of the softmax.
 //
-// One CTA per (query token, query head). Each of its warps walks every eighth key with its own
-// running maximum m, sum l and weighted sum of values (the lanes share the head's channels), and
-// the warps' results are joined at the end: o = sum_w e^{m_w - m} acc_w / sum_w e^{m_w - m} l_w.
+// What bounds it: the cache is read once, 2 d bytes per token and key/value head, so a single
+// decoded token per row is HBM-bound; the 4 d operations per (query row, key) are tensor-core
+// work. A "unit" is one (batch row, key/value head) with up to 16 MT query rows (the window's tokens
+// times the query heads of the group), so that the cache is read once for all of them.
+//
+// Arithmetic. e4m3 codes are exact in f16, so both products run as f16 x f16 -> fp32 warp MMAs
+// on codes; the page's power-of-two scales are applied around them. A query row is multiplied by
+// a power of two that puts its largest entry in [2^13, 2^14) and rounded to f16: exact for bf16
+// entries down to 2^-28 of the largest; fp32 queries are carried as the sum of two f16 parts (22
+// bits). With x_t the score in units of log2 and e_t the exponent of t's value scale, the row
+// keeps M = max_t (x_t + e_t) and accumulates
+//     P_t = 2^(x_t + e_t - M + 14) (f16; two parts for fp32),  O = sum_t P_t code_t,
+//     l = sum_t 2^(x_t - M + 14) = sum_t P_t 2^-e_t (fp32),    o = O / l.
+// P is at most 2^14 whatever the scales of the pages, and what f16 drops is below 2^-38 of the
+// row's largest term.
+//
+// Layout. Lane (g, t) = (lane / 4, lane % 4) of an m16n8k16 MMA. The order of the channels in the
+// first product and of the columns in the second is free as long as both operands agree, and is
+// chosen so that a lane reads 16-byte pieces of a cached row as they lie: channels 32 t .. 32 t +
+// 31 of key g for the scores, and channels 16 g .. 16 g + 15 of keys 2t, 2t+1, 2t+8, 2t+9 for the
+// values, whose bytes are interleaved pairwise to give two keys of one channel (d = 128; half of
+// that for d = 64). A lane's outputs are then 32 consecutive channels of its row.
+//
+// Every warp walks 16-key slices of its own through a private ring of kStages shared-memory
+// buffers filled with 16-byte asynchronous copies; nothing in the loop waits for another warp.
+// The warps' results are joined at the end of the unit.
+//
+// Work split. The rows' 64-key blocks are laid end to end (row, head, row group, block) and cut
+// into as many equal ranges as CTAs fit on the GPU, so that ragged lengths and few rows load
+// every SM alike. A unit that lies in one range is finished there; the pieces of a unit that is
+// cut go to the workspace (each CTA has at most two) and a second kernel, launched ahead of time
+// and released when the first ends, joins them in order: no atomics, the same bits every time.
 #include "kda_internal.cuh"
 #include "kda_fp8.cuh"
+#include "ptx.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kSlice = 16;     // keys per warp step
+constexpr int kStages = 3;     // slices in a warp's ring
+constexpr int kMaxCtas = 320;  // bound of the grid (sizes the workspace)
+constexpr int kMinBlocks = 2;  // 64-key blocks per CTA at least: a slice for every warp
+constexpr float kPBase = 14.0f;
+constexpr int kMinScaleExp = -60;  // clamp of e_t in M, so that l stays in range
 
-template <int N>
-__device__ __forceinline__ void load_codes(const uint8_t* p, float* f) {
-  uint32_t w;
-  if constexpr (N == 4) w = *reinterpret_cast<const uint32_t*>(p);
-  else w = *reinterpret_cast<const uint16_t*>(p);
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) {
-    const float2 a = f32x2_from_f16x2(f16x2_from_e4m3((w >> (16 * i)) & 0xffffu));
-    f[2 * i] = a.x;
-    f[2 * i + 1] = a.y;
-  }
+struct UnitDesc {  // a unit whose first piece is CTA c's last one
+  int32_t b, h, rg, pieces;
+};
+
+template <class T, int D, int MT>
+struct Shape {
+  static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;
+  static constexpr int ROWS = 16 * MT;
+  static constexpr int KSTEPS = D / 16;
+  static constexpr int NT = D / 8;                 // n-tiles of the second product
+  static constexpr int SLICE_BYTES = kSlice * D;   // one of K, V
+  static constexpr int STAGE = 2 * SLICE_BYTES;
+  static constexpr int RING = kWarps * kStages * STAGE;
+  static constexpr int MERGE = kWarps * ROWS * D * 4;
+  static constexpr int BUF = RING > MERGE ? RING : MERGE;
+  static constexpr int QFRAG = MT * PARTS * KSTEPS * 512;
+  static constexpr int SMEM = BUF + QFRAG;
+};
+
+// Byte of 16-byte chunk c of row r of a slice: chunks are permuted within the row so that both
+// access patterns above touch every bank once (d = 128).
+template <int D>
+__device__ __forceinline__ int chunk_at(int r, int c) {
+  if constexpr (D == 128) return r * 128 + ((c ^ (r & 7)) << 4);
+  else return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-template <class T, int D>
-__global__ void __launch_bounds__(kWarps * 32) attn_kernel(const CacheAttnParams p) {
-  constexpr int N = D / 32;  // channels per lane
-  __shared__ float acc_s[kWarps][D], m_s[kWarps], l_s[kWarps];
-  const int hq = blockIdx.x % p.Hq, tok = blockIdx.x / p.Hq;
-  const int b = tok / p.window, j = tok - b * p.window;
-  const int h = hq / (p.Hq / p.Hkv);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t n = 0;  // keys this query sees
-  if (p.start[b] >= 0 && (!p.lens || j < p.lens[b])) {
-    n = (int64_t)p.start[b] + j + 1;
-    const int64_t top = (int64_t)p.max_pages * kPage;
-    if (n > top) {
-      if (threadIdx.x == 0 && hq == 0 && p.status) atomicOr(p.status, KDA_STATUS_BAD_PAGE);
-      n = top;
-    }
-  }
-  float q[N], acc[N], m = -INFINITY, l = 0.0f;
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma_f16(float* d, const uint4& a, uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// The part of (lo, hi) that f16x2(lo, hi) = h dropped, rounded to f16.
+__device__ __forceinline__ uint32_t f16x2_rest(float lo, float hi, uint32_t h) {
+  const float2 f = f32x2_from_f16x2(h);
+  return f16x2(lo - f.x, hi - f.y);
+}
+
+// Query tokens of row b, and 64-key blocks that any of them sees.
+__device__ __forceinline__ int row_tokens(const CacheAttnParams& p, int b) {
+  if (p.start[b] < 0) return 0;
+  const int n = p.lens ? p.lens[b] : p.window;
+  return n < 0 ? 0 : (n > p.window ? p.window : n);
+}
+__device__ __forceinline__ int64_t row_blocks(const CacheAttnParams& p, int b, bool flag) {
+  const int n = row_tokens(p, b);
+  if (n == 0) return 0;
+  const int64_t blocks = ((int64_t)p.start[b] + n + kPage - 1) / kPage;
+  if (blocks <= p.max_pages) return blocks;
+  if (flag && p.status) atomicOr(p.status, KDA_STATUS_BAD_PAGE);
+  return p.max_pages;
+}
+
+struct Work {        // what a CTA knows of the list of blocks
+  int64_t pre[kThreads + 1];  // blocks before row base + i, from row `base` on
+  int64_t part[kWarps];
+};
+
+// pre[] of rows base .. base + 255. Every thread calls.
+__device__ __forceinline__ void scan_rows(const CacheAttnParams& p, Work& w, int base, bool flag) {
+  const int b = base + threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t v = b < p.batch ? row_blocks(p, b, flag) : 0;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    q[i] = ld_elem((const T*)p.q, ((int64_t)tok * p.Hq + hq) * D + lane * N + i) * p.scale;
-    acc[i] = 0.0f;
-  }
-  for (int64_t t = warp; t < n; t += kWarps) {
-    const int64_t page = p.table[(int64_t)b * p.max_pages + t / kPage];
-    if (page < 0) continue;
-    if (page >= p.n_pages) {
-      if (lane == 0 && p.status) atomicOr(p.status, KDA_STATUS_BAD_PAGE);
-      continue;
-    }
-    const int64_t slice = page * p.Hkv + h;
-    const int64_t at = (slice * kPage + t % kPage) * D + lane * N;
-    float f[N], s = 0.0f;
-    load_codes<N>(p.kc + at, f);
-#pragma unroll
-    for (int i = 0; i < N; ++i) s = fmaf(q[i], f[i], s);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= p.ks[slice];
-    const float mn = fmaxf(m, s);
-    const float c = mn == -INFINITY ? 0.0f : expf(m - mn);
-    const float e = mn == -INFINITY ? 0.0f : expf(s - mn);
-    m = mn;
-    l = l * c + e;
-    load_codes<N>(p.vc + at, f);
-    const float ev = e * p.vs[slice];
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = acc[i] * c + ev * f[i];
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) acc_s[warp][lane * N + i] = acc[i];
-  if (lane == 0) {
-    m_s[warp] = m;
-    l_s[warp] = l;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
   }
   __syncthreads();
-  float top = -INFINITY, sum = 0.0f;
+  if (lane == 31) w.part[warp] = v;
+  __syncthreads();
+  for (int i = 0; i < warp; ++i) v += w.part[i];
+  w.pre[threadIdx.x + 1] = v;
+  if (threadIdx.x == 0) w.pre[0] = 0;
+  __syncthreads();
+}
+
+template <class T, int D, int MT>
+struct WarpState {
+  float o[MT][D / 8][4];
+  float m[MT][2], l[MT][2];
+};
+
+// One 16-key slice: scores, softmax update, weighted values. `tail`: some key of the slice is
+// hidden from some row.
+template <class T, int D, int MT, bool kTail>
+__device__ __forceinline__ void slice_step(WarpState<T, D, MT>& st, const uint8_t* kb,
+                                           const uint8_t* vb, const uint4* qfrag, float ks, float vs,
+                                           const float (&rowf)[MT][2], const int (&seen)[MT][2],
+                                           int lane) {
+  using S = Shape<T, D, MT>;
+  const int g = lane >> 2, t = lane & 3;
+  float s[MT][2][4];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_s[w]);
-  float c[kWarps];
+  for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    c[w] = m_s[w] == -INFINITY ? 0.0f : expf(m_s[w] - top);
-    sum += c[w] * l_s[w];
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[mt][nt][i] = 0.0f;
+  uint32_t kw[2][D / 16];
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      const uint4 x = *reinterpret_cast<const uint4*>(
+          kb + chunk_at<D>(nt * 8 + g, (D / 64) * t + j));
+      kw[nt][4 * j] = x.x; kw[nt][4 * j + 1] = x.y;
+      kw[nt][4 * j + 2] = x.z; kw[nt][4 * j + 3] = x.w;
+    }
+#pragma unroll
+  for (int k = 0; k < S::KSTEPS; ++k) {
+    uint32_t b[2][2];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      b[nt][0] = f16x2_from_e4m3(kw[nt][k] & 0xffffu);
+      b[nt][1] = f16x2_from_e4m3(kw[nt][k] >> 16);
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int part = 0; part < S::PARTS; ++part) {
+        const uint4 a = qfrag[((mt * S::PARTS + part) * S::KSTEPS + k) * 32 + lane];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) mma_f16(s[mt][nt], a, b[nt][0], b[nt][1]);
+      }
   }
-  for (int i = threadIdx.x; i < D; i += kWarps * 32) {
-    float o = 0.0f;
+  // the value rows, while the scores finish
+  uint32_t vw[4][D / 32];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      if (c[w] != 0.0f) o += c[w] * acc_s[w][i];
-    st_elem((T*)p.o, ((int64_t)tok * p.Hq + hq) * D + i, sum == 0.0f ? 0.0f : o / sum);
+  for (int r = 0; r < 4; ++r) {
+    const int key = 2 * t + (r & 1) + (r >> 1) * 8;
+    if constexpr (D == 128) {
+      const uint4 x = *reinterpret_cast<const uint4*>(vb + chunk_at<D>(key, g));
+      vw[r][0] = x.x; vw[r][1] = x.y; vw[r][2] = x.z; vw[r][3] = x.w;
+    } else {
+      const uint2 x =
+          *reinterpret_cast<const uint2*>(vb + chunk_at<D>(key, g >> 1) + (g & 1) * 8);
+      vw[r][0] = x.x; vw[r][1] = x.y;
+    }
+  }
+  const int ve = (int)((__float_as_uint(vs) >> 23) & 255u) - 127;
+  const float vexp = (float)ve, vref = (float)(ve < kMinScaleExp ? kMinScaleExp : ve);
+  const float vinv = __uint_as_float((uint32_t)(127 - ve) << 23);  // 2^-e
+  bool grew = false;
+  float corr[MT][2];
+  uint4 pa[MT][S::PARTS];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const float f = rowf[mt][half] * ks;
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = s[mt][i >> 1][half * 2 + (i & 1)] * f;
+        if constexpr (kTail) {
+          if ((i >> 1) * 8 + 2 * t + (i & 1) >= seen[mt][half]) x[i] = -INFINITY;
+        }
+      }
+      float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float mo = st.m[mt][half];
+      const float mn = fmaxf(mo, top + vref);
+      grew |= mn > mo;
+      const float mu = mn == -INFINITY ? 0.0f : mn;
+      corr[mt][half] = ptx::ex2_approx(mo - mu);
+      st.m[mt][half] = mn;
+      const float c = vexp - mu + kPBase;
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = ptx::ex2_approx(x[i] + c);
+        sum += x[i];
+      }
+      st.l[mt][half] = st.l[mt][half] * corr[mt][half] + sum * vinv;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const uint32_t hi = f16x2(x[2 * nt], x[2 * nt + 1]);
+        (&pa[mt][0].x)[half + 2 * nt] = hi;
+        if constexpr (S::PARTS == 2)
+          (&pa[mt][1].x)[half + 2 * nt] = f16x2_rest(x[2 * nt], x[2 * nt + 1], hi);
+      }
+    }
+  }
+  if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int n = 0; n < S::NT; ++n) {
+        st.o[mt][n][0] *= corr[mt][0]; st.o[mt][n][1] *= corr[mt][0];
+        st.o[mt][n][2] *= corr[mt][1]; st.o[mt][n][3] *= corr[mt][1];
+      }
+  }
+  if constexpr (kTail) {
+    // Values of keys that some row does not see: a zero weight does not hide a NaN code (nor
+    // whatever lies after the last token), so NaN codes are taken out here and put back into
+    // the rows that see them.
+    uint32_t nan = 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w)
+        nan |= __vcmpeq4(vw[r][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+    if (__any_sync(0xffffffffu, nan != 0)) {
+      uint4 va[MT];  // 1 where the row sees the key
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            const int key = nt * 8 + 2 * t;
+            (&va[mt].x)[half + 2 * nt] = (key < seen[mt][half] ? 0x3c00u : 0u) |
+                                         (key + 1 < seen[mt][half] ? 0x3c000000u : 0u);
+          }
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) {
+        uint32_t ind[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t bad = __vcmpeq4(vw[r][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+          vw[r][w] &= ~bad;
+          ind[r] = bad & 0x38383838u;  // the code of 1.0
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t sel = q < 2 ? 0x5140u : 0x7362u;
+          const uint32_t c0 = __byte_perm(ind[0], ind[1], sel), c1 = __byte_perm(ind[2], ind[3], sel);
+          const uint32_t b0 = f16x2_from_e4m3((q & 1) ? c0 >> 16 : c0 & 0xffffu);
+          const uint32_t b1 = f16x2_from_e4m3((q & 1) ? c1 >> 16 : c1 & 0xffffu);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma_f16(hit, va[mt], b0, b1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (hit[i] > 0.0f) st.o[mt][4 * w + q][i] = __uint_as_float(0x7fffffffu);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < D / 32; ++w) {
+#pragma unroll
+    for (int q = 0; q < 4; q += 2) {
+      const uint32_t sel = q < 2 ? 0x5140u : 0x7362u;
+      const uint32_t c0 = __byte_perm(vw[0][w], vw[1][w], sel);
+      const uint32_t c1 = __byte_perm(vw[2][w], vw[3][w], sel);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t b0 = f16x2_from_e4m3(u ? c0 >> 16 : c0 & 0xffffu);
+        const uint32_t b1 = f16x2_from_e4m3(u ? c1 >> 16 : c1 & 0xffffu);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int part = 0; part < S::PARTS; ++part)
+            mma_f16(st.o[mt][4 * w + q + u], pa[mt][part], b0, b1);
+      }
+    }
   }
 }
 
-template <class T, int D>
+template <class T, int D, int MT>
+__global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1)
+attn_kernel(const CacheAttnParams p, float* ws_o, float2* ws_ml, UnitDesc* desc) {
+  using S = Shape<T, D, MT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Work work;
+  __shared__ float s_rowf[S::ROWS];
+  __shared__ int64_t s_seen[S::ROWS];
+  __shared__ float s_m[kWarps][S::ROWS], s_l[kWarps][S::ROWS];
+  __shared__ __align__(16) float s_scale[kWarps][kStages][4];  // k scale, v scale, present
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int G = p.Hq / p.Hkv, R = G * p.window;
+  const int nrg = (R + S::ROWS - 1) / S::ROWS;
+  const int U = p.Hkv * nrg;
+  const bool flag = blockIdx.x == 0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // rows without keys get their zeros here
+  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+    if (row_blocks(p, b, false) > 0) continue;
+    T* o = (T*)p.o + (int64_t)b * p.window * p.Hq * D;
+    for (int i = threadIdx.x; i < p.window * p.Hq * D; i += kThreads) st_elem(o, i, 0.0f);
+  }
+  if (threadIdx.x == 0) desc[blockIdx.x].pieces = 0;
+
+  // this CTA's range of the list of blocks
+  int64_t total = 0;
+  int base = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+    scan_rows(p, work, b0, flag);
+    total += work.pre[kThreads];
+    base = b0;
+  }
+  total *= U;
+  int64_t ctas = (total + kMinBlocks - 1) / kMinBlocks;
+  if (ctas > gridDim.x) ctas = gridDim.x;
+  if (blockIdx.x >= ctas) return;
+  const int64_t cta = blockIdx.x;
+  int64_t pos = total * cta / ctas;
+  const int64_t end = total * (cta + 1) / ctas;
+  int64_t before = 0;  // blocks (times U) before row `base`
+  if (p.batch > kThreads) {
+    base = 0;
+    for (;;) {
+      scan_rows(p, work, base, false);
+      if (before + work.pre[kThreads] * U > pos) break;
+      before += work.pre[kThreads] * U;
+      base += kThreads;
+    }
+  }
+  int row;  // within the scanned rows: the last one that starts at or before pos
+  {
+    int a = 0, z = kThreads - 1;
+    while (a < z) {
+      const int mid = (a + z + 1) >> 1;
+      if (before + work.pre[mid] * U <= pos) a = mid;
+      else z = mid - 1;
+    }
+    row = a;
+  }
+
+  while (pos < end) {
+    // the piece [blk0, blk1) of a unit
+    while (work.pre[row + 1] == work.pre[row] || before + work.pre[row + 1] * U <= pos) {
+      if (++row == kThreads) {
+        before += work.pre[kThreads] * U;
+        base += kThreads;
+        row = 0;
+        scan_rows(p, work, base, false);
+      }
+    }
+    const int b = base + row;
+    const int64_t nb = work.pre[row + 1] - work.pre[row];
+    const int64_t off = pos - before - work.pre[row] * U;
+    const int unit = (int)(off / nb);
+    const int64_t blk0 = off - unit * nb;
+    const int64_t blk1 = blk0 + (end - pos) < nb ? blk0 + (end - pos) : nb;
+    const int h = unit / nrg, rg = unit - h * nrg;
+    const int rows = R - rg * S::ROWS < S::ROWS ? R - rg * S::ROWS : S::ROWS;
+    const int n_tok = row_tokens(p, b);
+    const int64_t start = p.start[b];
+
+    // queries: scaled by a power of two, rounded to f16 parts, in the order of the MMA's operand
+    for (int r = warp; r < S::ROWS; r += kWarps) {
+      constexpr int N = D / 32;
+      float q[N];
+      uint32_t top = 0;
+      const int gr = rg * S::ROWS + r, j = gr / G;
+      const bool live = r < rows && j < n_tok;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        q[i] = 0.0f;
+        if (live)
+          q[i] = ld_elem((const T*)p.q, ((int64_t)(b * p.window + j) * p.Hq + h * G + (gr - j * G)) * D +
+                                            lane * N + i);
+        top = max(top, finite_abs_bits(q[i]));
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      int e = top ? 13 + 127 - (int)(top >> 23) : 0;
+      e = e > 100 ? 100 : (e < -100 ? -100 : e);
+      if (lane == 0) {
+        s_rowf[r] = p.scale * 1.44269504f * pow2f(-e);
+        // rows that are not live see everything: they force no mask, and are not stored
+        s_seen[r] = live ? start + j + 1 : (int64_t)1 << 60;
+      }
+      const float up = pow2f(e);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        // channels c, c + 1: lane quarter t', k-step k, register pair (c & 2)
+        const int c = lane * N + i, tt = c / (D / 4), k = (c % (D / 4)) / 4;
+        const int reg = (r & 15) / 8 + (c & 2);
+        const uint32_t hi = f16x2(q[i] * up, q[i + 1] * up);
+        uint32_t* f = reinterpret_cast<uint32_t*>(smem + S::BUF);
+        const int at = (((r / 16) * S::PARTS * S::KSTEPS + k) * 32 + (r & 7) * 4 + tt) * 4 + reg;
+        f[at] = hi;
+        if constexpr (S::PARTS == 2)
+          f[at + S::KSTEPS * 128] = f16x2_rest(q[i] * up, q[i + 1] * up, hi);
+      }
+    }
+    __syncthreads();
+
+    float rowf[MT][2];
+    int64_t seen[MT][2], least = (int64_t)1 << 60;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        rowf[mt][half] = s_rowf[mt * 16 + half * 8 + g];
+        seen[mt][half] = s_seen[mt * 16 + half * 8 + g];
+      }
+    for (int r = 0; r < S::ROWS; ++r) least = s_seen[r] < least ? s_seen[r] : least;
+
+    WarpState<T, D, MT> st;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int n = 0; n < S::NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st.o[mt][n][i] = 0.0f;
+      st.m[mt][0] = st.m[mt][1] = -INFINITY;
+      st.l[mt][0] = st.l[mt][1] = 0.0f;
+    }
+
+    // slices of this warp: blk0 * 4 + warp, + kWarps, ...
+    const int64_t first = blk0 * (kPage / kSlice) + warp, last = blk1 * (kPage / kSlice);
+    const int n_sl = last > first ? (int)((last - first + kWarps - 1) / kWarps) : 0;
+    uint8_t* ring = smem + warp * kStages * S::STAGE;
+    const int32_t* table = p.table + (int64_t)b * p.max_pages;
+    auto page_of = [&](int i) {
+      return i < n_sl ? table[(first + (int64_t)i * kWarps) / (kPage / kSlice)] : -1;
+    };
+    auto issue = [&](int i, int page) {
+      if (i < n_sl) {
+        const int stage = i % kStages;
+        float* sc = s_scale[warp][stage];
+        const bool present = page >= 0 && page < p.n_pages;
+        if (page >= p.n_pages && lane == 0 && p.status) atomicOr(p.status, KDA_STATUS_BAD_PAGE);
+        if (lane == 0) sc[2] = present ? 1.0f : 0.0f;
+        if (present) {
+          const int64_t slice = (int64_t)page * p.Hkv + h;
+          const int key = (int)((first + (int64_t)i * kWarps) % (kPage / kSlice)) * kSlice;
+          const int64_t at = (slice * kPage + key) * D;
+          const uint32_t dst = ptx::smem_u32(ring + stage * S::STAGE);
+#pragma unroll
+          for (int c = 0; c < S::SLICE_BYTES / 512; ++c) {
+            const int idx = c * 32 + lane, r = idx / (D / 16), ch = idx % (D / 16);
+            cp16(dst + chunk_at<D>(r, ch), p.kc + at + idx * 16);
+            cp16(dst + S::SLICE_BYTES + chunk_at<D>(r, ch), p.vc + at + idx * 16);
+          }
+          if (lane == 0) {
+            cp4(ptx::smem_u32(sc), p.ks + slice);
+            cp4(ptx::smem_u32(sc + 1), p.vs + slice);
+          }
+        }
+      }
+      cp_commit();
+    };
+    int next_page;
+    {
+      int pg[kStages];
+#pragma unroll
+      for (int i = 0; i < kStages; ++i) pg[i] = page_of(i);
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) issue(i, pg[i]);
+      next_page = pg[kStages - 1];
+    }
+    for (int i = 0; i < n_sl; ++i) {
+      cp_wait<kStages - 2>();
+      __syncwarp();
+      const int page = next_page;
+      next_page = page_of(i + kStages);
+      issue(i + kStages - 1, page);
+      const int stage = i % kStages;
+      const float* sc = s_scale[warp][stage];
+      if (sc[2] == 0.0f) continue;
+      const uint8_t* kb = ring + stage * S::STAGE;
+      const uint8_t* vb = kb + S::SLICE_BYTES;
+      const uint4* qf = reinterpret_cast<const uint4*>(smem + S::BUF);
+      const int64_t t0 = (first + (int64_t)i * kWarps) * kSlice;
+      int left[MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int64_t n = seen[mt][half] - t0;
+          left[mt][half] = n < 0 ? 0 : (n > kSlice ? kSlice : (int)n);
+        }
+      if (t0 + kSlice <= least)
+        slice_step<T, D, MT, false>(st, kb, vb, qf, sc[0], sc[1], rowf, left, lane);
+      else
+        slice_step<T, D, MT, true>(st, kb, vb, qf, sc[0], sc[1], rowf, left, lane);
+    }
+    cp_wait<0>();
+
+    // join the warps
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float l = st.l[mt][half];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if (t == 0) {
+          s_m[warp][mt * 16 + half * 8 + g] = st.m[mt][half];
+          s_l[warp][mt * 16 + half * 8 + g] = l;
+        }
+      }
+    __syncthreads();
+    float* acc = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float* o = acc + (warp * S::ROWS + mt * 16 + half * 8 + g) * D + t * (D / 4);
+#pragma unroll
+        for (int n = 0; n < S::NT; ++n) {  // channels t D/4 + n and t D/4 + D/8 + n
+          o[n] = st.o[mt][n][half * 2];
+          o[D / 8 + n] = st.o[mt][n][half * 2 + 1];
+        }
+      }
+    __syncthreads();
+    const bool whole = blk0 == 0 && blk1 == nb;
+    const int slot = 2 * blockIdx.x + (blk0 == 0 ? 1 : 0);
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+      float top = -INFINITY, l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (s_m[w][r] == -INFINITY && s_l[w][r] == 0.0f) continue;  // saw no key
+        const float f = ptx::ex2_approx(s_m[w][r] - (top == -INFINITY ? 0.0f : top));
+        const float4 x = *reinterpret_cast<const float4*>(acc + (w * S::ROWS + r) * D + c);
+        l += f * s_l[w][r];
+        o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
+      }
+      if (whole) {
+        const int gr = rg * S::ROWS + r, j = gr / G;
+        const bool live = j < n_tok;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        T* dst = (T*)p.o + ((int64_t)(b * p.window + j) * p.Hq + h * G + (gr - j * G)) * D + c;
+        st_elem(dst, 0, live ? o.x * inv : 0.0f);
+        st_elem(dst, 1, live ? o.y * inv : 0.0f);
+        st_elem(dst, 2, live ? o.z * inv : 0.0f);
+        st_elem(dst, 3, live ? o.w * inv : 0.0f);
+      } else {
+        *reinterpret_cast<float4*>(ws_o + ((int64_t)slot * S::ROWS + r) * D + c) = o;
+        if (c == 0) ws_ml[(int64_t)slot * S::ROWS + r] = make_float2(top, l);
+      }
+    }
+    if (!whole && blk0 == 0 && threadIdx.x == 0) {
+      // the pieces of this unit end in the CTA whose range holds its last block
+      const int64_t stop = pos + nb;
+      int pieces = 1;
+      while (total * (cta + pieces) / ctas < stop) ++pieces;
+      UnitDesc d;
+      d.b = b; d.h = h; d.rg = rg; d.pieces = pieces;
+      desc[blockIdx.x] = d;
+    }
+    __syncthreads();
+    pos += blk1 - blk0;
+  }
+}
+
+constexpr int kJoinRows = 4;
+
+// Joins the pieces of the unit that CTA c began and others went on with: c's second slot, then
+// the first slots of c + 1, c + 2, ...
+template <class T, int D, int MT>
+__global__ void __launch_bounds__(kJoinRows * 32)
+join_kernel(const CacheAttnParams p, const float* ws_o, const float2* ws_ml, const UnitDesc* desc) {
+  using S = Shape<T, D, MT>;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const UnitDesc d = desc[blockIdx.x];
+  if (d.pieces == 0) return;
+  const int G = p.Hq / p.Hkv, R = G * p.window;
+  const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int gr = d.rg * S::ROWS + r;
+  if (r >= S::ROWS || gr >= R) return;
+  const int j = gr / G;
+  constexpr int N = D / 32;
+  float top = -INFINITY;
+  for (int i = 0; i < d.pieces; ++i) {
+    const int64_t slot = i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i);
+    top = fmaxf(top, ws_ml[slot * S::ROWS + r].x);
+  }
+  float o[N], l = 0.0f;
+#pragma unroll
+  for (int c = 0; c < N; ++c) o[c] = 0.0f;
+  for (int i = 0; i < d.pieces; ++i) {
+    const int64_t slot = i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i);
+    const float2 ml = ws_ml[slot * S::ROWS + r];
+    if (ml.x == -INFINITY && ml.y == 0.0f) continue;
+    const float f = ptx::ex2_approx(ml.x - (top == -INFINITY ? 0.0f : top));
+    l += f * ml.y;
+#pragma unroll
+    for (int c = 0; c < N; ++c) o[c] += f * ws_o[(slot * S::ROWS + r) * D + lane * N + c];
+  }
+  const bool live = j < row_tokens(p, d.b);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  T* dst = (T*)p.o + ((int64_t)(d.b * p.window + j) * p.Hq + d.h * G + (gr - j * G)) * D + lane * N;
+#pragma unroll
+  for (int c = 0; c < N; ++c) st_elem(dst, c, live ? o[c] * inv : 0.0f);
+}
+
+size_t piece_bytes(int rows, int d) { return (size_t)2 * kMaxCtas * rows * d * sizeof(float); }
+size_t ml_bytes(int rows) { return (size_t)2 * kMaxCtas * rows * sizeof(float2); }
+
+template <class T, int D, int MT>
 kda_status launch_t(const CacheAttnParams& p, cudaStream_t s) {
-  attn_kernel<T, D><<<(unsigned)(p.batch * p.window * p.Hq), kWarps * 32, 0, s>>>(p);
-  count_launches(1);
+  using S = Shape<T, D, MT>;
+  static int ctas_of[64] = {};  // resident CTAs of each device, found once
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64)
+    return set_error(KDA_ERR_CUDA, "kda_cache_attention: no current device");
+  if (ctas_of[dev] == 0) {
+    int sms = 0, per = 0;
+    e = cudaFuncSetAttribute(attn_kernel<T, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             S::SMEM);
+    if (e == cudaSuccess)
+      e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, attn_kernel<T, D, MT>, kThreads,
+                                                        S::SMEM);
+    if (e != cudaSuccess || per < 1)
+      return set_error(KDA_ERR_CUDA, std::string("kda_cache_attention: ") + cudaGetErrorString(e));
+    ctas_of[dev] = sms * per < kMaxCtas ? sms * per : kMaxCtas;
+  }
+  const int G = p.Hq / p.Hkv, nrg = (G * p.window + S::ROWS - 1) / S::ROWS;
+  // no more CTAs than the page table allows ranges of kMinBlocks blocks
+  const int64_t most = ((int64_t)p.batch * p.Hkv * nrg * p.max_pages + kMinBlocks - 1) / kMinBlocks;
+  const int ctas = most < ctas_of[dev] ? (int)most : ctas_of[dev];
+  uint8_t* ws = (uint8_t*)p.ws;
+  float* ws_o = (float*)ws;
+  float2* ws_ml = (float2*)(ws + piece_bytes(S::ROWS, D));
+  UnitDesc* desc = (UnitDesc*)(ws + piece_bytes(S::ROWS, D) + ml_bytes(S::ROWS));
+  attn_kernel<T, D, MT><<<ctas, kThreads, S::SMEM, s>>>(p, ws_o, ws_ml, desc);
+  kda_status st = check_launch("kda_cache_attention");
+  if (st != KDA_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, S::ROWS / kJoinRows);
+  cfg.blockDim = dim3(kJoinRows * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, join_kernel<T, D, MT>, p, (const float*)ws_o, (const float2*)ws_ml,
+                     (const UnitDesc*)desc);
+  count_launches(2);
   return check_launch("kda_cache_attention");
 }
 
+// Rows of a unit: two MMA row tiles when the group and window fill them (bf16), else one.
+int row_tiles(kda_dtype dt, int rows) { return dt == KDA_BF16 && rows > 16 ? 2 : 1; }
+
 }  // namespace
 
-size_t cache_attn_workspace_bytes(int, int, int, int, int) { return 0; }
+size_t cache_attn_workspace_bytes(int, int window, int Hq, int Hkv, int d) {
+  const int rows = Hq / Hkv * window > 16 ? 32 : 16;
+  return piece_bytes(rows, d) + ml_bytes(rows) + (sizeof(UnitDesc) * kMaxCtas + 255) / 256 * 256;
+}
 
 kda_status launch_cache_attn(const CacheAttnParams& p, kda_dtype dt, int d, cudaStream_t s) {
-  if (dt == KDA_BF16)
-    return d == 128 ? launch_t<__nv_bfloat16, 128>(p, s) : launch_t<__nv_bfloat16, 64>(p, s);
-  return d == 128 ? launch_t<float, 128>(p, s) : launch_t<float, 64>(p, s);
+  if (dt == KDA_BF16) {
+    if (row_tiles(dt, p.Hq / p.Hkv * p.window) == 2)
+      return d == 128 ? launch_t<__nv_bfloat16, 128, 2>(p, s) : launch_t<__nv_bfloat16, 64, 2>(p, s);
+    return d == 128 ? launch_t<__nv_bfloat16, 128, 1>(p, s) : launch_t<__nv_bfloat16, 64, 1>(p, s);
+  }
+  return d == 128 ? launch_t<float, 128, 1>(p, s) : launch_t<float, 64, 1>(p, s);
 }
 
 }  // namespace kda
