@@ -41,13 +41,15 @@
 namespace kda {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kSlice = 16;     // keys per warp step
-constexpr int kStages = 3;     // slices in a warp's ring
+constexpr int kSlice = 32;     // keys per warp step
 constexpr int kMaxCtas = 320;  // bound of the grid (sizes the workspace)
-constexpr int kMinBlocks = 2;  // 64-key blocks per CTA at least: a slice for every warp
-constexpr float kPBase = 14.0f;
+// P is 2^kPBase for a term equal to the row's M, and M is raised only when a term exceeds it by
+// more than 2^kSlack: P <= 2^15 fits f16, and the accumulators are rescaled once or twice per
+// unit instead of in most steps.
+constexpr float kPBase = 7.0f, kSlack = 8.0f;
+constexpr int kUnitCost = 3;   // what beginning and joining a unit takes, in blocks
+constexpr int kMinCost = kUnitCost + 2;  // least work of a CTA: a unit of two blocks
+constexpr int kNoEnd = 1 << 30;    // beyond the positions of the largest page table
 constexpr int kMinScaleExp = -60;  // clamp of e_t in M, so that l stays in range
 
 struct UnitDesc {  // a unit whose first piece is CTA c's last one
@@ -58,12 +60,19 @@ template <class T, int D, int MT>
 struct Shape {
   static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;
   static constexpr int ROWS = 16 * MT;
+  static constexpr int WARPS = MT == 1 ? 6 : 8;
+  static constexpr int THREADS = WARPS * 32;
+  static constexpr int CTAS = MT == 1 ? 2 : 1;     // resident per SM
+  static constexpr int STAGES = D == 128 ? 2 : 3;  // slices in a warp's ring
   static constexpr int KSTEPS = D / 16;
   static constexpr int NT = D / 8;                 // n-tiles of the second product
   static constexpr int SLICE_BYTES = kSlice * D;   // one of K, V
   static constexpr int STAGE = 2 * SLICE_BYTES;
-  static constexpr int RING = kWarps * kStages * STAGE;
-  static constexpr int MERGE = kWarps * ROWS * D * 4;
+  static constexpr int RING = WARPS * STAGES * STAGE;
+  // A warp's results in shared memory: each lane's D / 4 channels of a row 4 floats further than
+  // the last lane's, so that 16-byte accesses of 8 lanes touch every bank once.
+  static constexpr int LANE_F = D / 4 + 4, ROW_F = 4 * LANE_F;
+  static constexpr int MERGE = WARPS * ROWS * ROW_F * 4;
   static constexpr int BUF = RING > MERGE ? RING : MERGE;
   static constexpr int QFRAG = MT * PARTS * KSTEPS * 512;
   static constexpr int SMEM = BUF + QFRAG;
@@ -79,9 +88,6 @@ __device__ __forceinline__ int chunk_at(int r, int c) {
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -121,15 +127,19 @@ __device__ __forceinline__ int64_t row_blocks(const CacheAttnParams& p, int b, b
   return p.max_pages;
 }
 
-struct Work {        // what a CTA knows of the list of blocks
-  int64_t pre[kThreads + 1];  // blocks before row base + i, from row `base` on
-  int64_t part[kWarps];
+template <int kThreads>
+struct Work {                 // what a CTA knows of the list of blocks
+  int64_t pre[kThreads + 1];  // cost of one unit of rows base .. base + i - 1, summed
+  int64_t part[kThreads / 32];
 };
 
-// pre[] of rows base .. base + 255. Every thread calls.
-__device__ __forceinline__ void scan_rows(const CacheAttnParams& p, Work& w, int base, bool flag) {
+// pre[] of rows base .. base + kThreads - 1. Every thread calls.
+template <int kThreads>
+__device__ __forceinline__ void scan_rows(const CacheAttnParams& p, Work<kThreads>& w, int base,
+                                          bool flag) {
   const int b = base + threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t v = b < p.batch ? row_blocks(p, b, flag) : 0;
+  if (v > 0) v += kUnitCost;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
@@ -150,197 +160,206 @@ struct WarpState {
   float m[MT][2], l[MT][2];
 };
 
-// One 16-key slice: scores, softmax update, weighted values. `tail`: some key of the slice is
-// hidden from some row.
+// One slice: scores, softmax update, weighted values. kTail: some key of the slice is hidden from
+// some row; `left` of its keys are seen by each of the lane's rows.
 template <class T, int D, int MT, bool kTail>
 __device__ __forceinline__ void slice_step(WarpState<T, D, MT>& st, const uint8_t* kb,
                                            const uint8_t* vb, const uint4* qfrag, float ks, float vs,
-                                           const float (&rowf)[MT][2], const int (&seen)[MT][2],
+                                           const float (&rowf)[MT][2], const int (&left)[MT][2],
                                            int lane) {
   using S = Shape<T, D, MT>;
+  constexpr int NK = kSlice / 8;  // key tiles of the first product
   const int g = lane >> 2, t = lane & 3;
-  float s[MT][2][4];
+  float s[MT][NK][4];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+    for (int nt = 0; nt < NK; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[mt][nt][i] = 0.0f;
-  uint32_t kw[2][D / 16];
+  // half of the lane's channels at a time
 #pragma unroll
-  for (int nt = 0; nt < 2; ++nt)
+  for (int j = 0; j < D / 64; ++j) {
+    uint4 kw[NK];
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-      const uint4 x = *reinterpret_cast<const uint4*>(
-          kb + chunk_at<D>(nt * 8 + g, (D / 64) * t + j));
-      kw[nt][4 * j] = x.x; kw[nt][4 * j + 1] = x.y;
-      kw[nt][4 * j + 2] = x.z; kw[nt][4 * j + 3] = x.w;
-    }
+    for (int nt = 0; nt < NK; ++nt)
+      kw[nt] = *reinterpret_cast<const uint4*>(kb + chunk_at<D>(nt * 8 + g, (D / 64) * t + j));
 #pragma unroll
-  for (int k = 0; k < S::KSTEPS; ++k) {
-    uint32_t b[2][2];
+    for (int k4 = 0; k4 < 4; ++k4) {
+      uint32_t b[NK][2];
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      b[nt][0] = f16x2_from_e4m3(kw[nt][k] & 0xffffu);
-      b[nt][1] = f16x2_from_e4m3(kw[nt][k] >> 16);
-    }
+      for (int nt = 0; nt < NK; ++nt) f16x4_from_e4m3((&kw[nt].x)[k4], b[nt][0], b[nt][1]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int part = 0; part < S::PARTS; ++part) {
-        const uint4 a = qfrag[((mt * S::PARTS + part) * S::KSTEPS + k) * 32 + lane];
+        for (int part = 0; part < S::PARTS; ++part) {
+          const uint4 a = qfrag[((mt * S::PARTS + part) * S::KSTEPS + 4 * j + k4) * 32 + lane];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) mma_f16(s[mt][nt], a, b[nt][0], b[nt][1]);
-      }
-  }
-  // the value rows, while the scores finish
-  uint32_t vw[4][D / 32];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int key = 2 * t + (r & 1) + (r >> 1) * 8;
-    if constexpr (D == 128) {
-      const uint4 x = *reinterpret_cast<const uint4*>(vb + chunk_at<D>(key, g));
-      vw[r][0] = x.x; vw[r][1] = x.y; vw[r][2] = x.z; vw[r][3] = x.w;
-    } else {
-      const uint2 x =
-          *reinterpret_cast<const uint2*>(vb + chunk_at<D>(key, g >> 1) + (g & 1) * 8);
-      vw[r][0] = x.x; vw[r][1] = x.y;
+          for (int nt = 0; nt < NK; ++nt) mma_f16(s[mt][nt], a, b[nt][0], b[nt][1]);
+        }
     }
   }
   const int ve = (int)((__float_as_uint(vs) >> 23) & 255u) - 127;
   const float vexp = (float)ve, vref = (float)(ve < kMinScaleExp ? kMinScaleExp : ve);
   const float vinv = __uint_as_float((uint32_t)(127 - ve) << 23);  // 2^-e
-  bool grew = false;
-  float corr[MT][2];
-  uint4 pa[MT][S::PARTS];
+  bool over = false;
+  float top[MT][2];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
+  for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const float f = rowf[mt][half] * ks;
-      float x[4];
+      top[mt][half] = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = s[mt][i >> 1][half * 2 + (i & 1)] * f;
-        if constexpr (kTail) {
-          if ((i >> 1) * 8 + 2 * t + (i & 1) >= seen[mt][half]) x[i] = -INFINITY;
+      for (int nt = 0; nt < NK; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float& x = s[mt][nt][half * 2 + i];
+          x *= f;
+          if constexpr (kTail) {
+            if (nt * 8 + 2 * t + i >= left[mt][half]) x = -INFINITY;
+          }
+          top[mt][half] = fmaxf(top[mt][half], x);
         }
-      }
-      float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float mo = st.m[mt][half];
-      const float mn = fmaxf(mo, top + vref);
-      grew |= mn > mo;
-      const float mu = mn == -INFINITY ? 0.0f : mn;
-      corr[mt][half] = ptx::ex2_approx(mo - mu);
-      st.m[mt][half] = mn;
-      const float c = vexp - mu + kPBase;
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = ptx::ex2_approx(x[i] + c);
-        sum += x[i];
-      }
-      st.l[mt][half] = st.l[mt][half] * corr[mt][half] + sum * vinv;
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const uint32_t hi = f16x2(x[2 * nt], x[2 * nt + 1]);
-        (&pa[mt][0].x)[half + 2 * nt] = hi;
-        if constexpr (S::PARTS == 2)
-          (&pa[mt][1].x)[half + 2 * nt] = f16x2_rest(x[2 * nt], x[2 * nt + 1], hi);
-      }
+      over |= top[mt][half] + vref > st.m[mt][half] + kSlack;
     }
-  }
-  if (__any_sync(0xffffffffu, grew)) {
+  if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
+      float corr[2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float x = top[mt][half];
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        const float mo = st.m[mt][half], mn = fmaxf(mo, x + vref);
+        st.m[mt][half] = mn;
+        corr[half] = ptx::ex2_approx(mo - (mn == -INFINITY ? 0.0f : mn));
+        st.l[mt][half] *= corr[half];
+      }
 #pragma unroll
       for (int n = 0; n < S::NT; ++n) {
-        st.o[mt][n][0] *= corr[mt][0]; st.o[mt][n][1] *= corr[mt][0];
-        st.o[mt][n][2] *= corr[mt][1]; st.o[mt][n][3] *= corr[mt][1];
-      }
-  }
-  if constexpr (kTail) {
-    // Values of keys that some row does not see: a zero weight does not hide a NaN code (nor
-    // whatever lies after the last token), so NaN codes are taken out here and put back into
-    // the rows that see them.
-    uint32_t nan = 0;
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w)
-        nan |= __vcmpeq4(vw[r][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-    if (__any_sync(0xffffffffu, nan != 0)) {
-      uint4 va[MT];  // 1 where the row sees the key
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            const int key = nt * 8 + 2 * t;
-            (&va[mt].x)[half + 2 * nt] = (key < seen[mt][half] ? 0x3c00u : 0u) |
-                                         (key + 1 < seen[mt][half] ? 0x3c000000u : 0u);
-          }
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
-        uint32_t ind[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t bad = __vcmpeq4(vw[r][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-          vw[r][w] &= ~bad;
-          ind[r] = bad & 0x38383838u;  // the code of 1.0
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t sel = q < 2 ? 0x5140u : 0x7362u;
-          const uint32_t c0 = __byte_perm(ind[0], ind[1], sel), c1 = __byte_perm(ind[2], ind[3], sel);
-          const uint32_t b0 = f16x2_from_e4m3((q & 1) ? c0 >> 16 : c0 & 0xffffu);
-          const uint32_t b1 = f16x2_from_e4m3((q & 1) ? c1 >> 16 : c1 & 0xffffu);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma_f16(hit, va[mt], b0, b1);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (hit[i] > 0.0f) st.o[mt][4 * w + q][i] = __uint_as_float(0x7fffffffu);
-          }
-        }
+        st.o[mt][n][0] *= corr[0]; st.o[mt][n][1] *= corr[0];
+        st.o[mt][n][2] *= corr[1]; st.o[mt][n][3] *= corr[1];
       }
     }
   }
+  uint4 pa[MT][S::PARTS][kSlice / 16];
 #pragma unroll
-  for (int w = 0; w < D / 32; ++w) {
+  for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int q = 0; q < 4; q += 2) {
-      const uint32_t sel = q < 2 ? 0x5140u : 0x7362u;
-      const uint32_t c0 = __byte_perm(vw[0][w], vw[1][w], sel);
-      const uint32_t c1 = __byte_perm(vw[2][w], vw[3][w], sel);
+    for (int half = 0; half < 2; ++half) {
+      const float m = st.m[mt][half];
+      const float c = vexp - (m == -INFINITY ? 0.0f : m) + kPBase;
+      float sum = 0.0f;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t b0 = f16x2_from_e4m3(u ? c0 >> 16 : c0 & 0xffffu);
-        const uint32_t b1 = f16x2_from_e4m3(u ? c1 >> 16 : c1 & 0xffffu);
+      for (int nt = 0; nt < NK; ++nt) {
+        const float x0 = ptx::ex2_approx(s[mt][nt][half * 2] + c);
+        const float x1 = ptx::ex2_approx(s[mt][nt][half * 2 + 1] + c);
+        sum += x0 + x1;
+        const uint32_t hi = f16x2(x0, x1);
+        (&pa[mt][0][nt >> 1].x)[half + 2 * (nt & 1)] = hi;
+        if constexpr (S::PARTS == 2)
+          (&pa[mt][1][nt >> 1].x)[half + 2 * (nt & 1)] = f16x2_rest(x0, x1, hi);
+      }
+      st.l[mt][half] = fmaf(sum, vinv, st.l[mt][half]);
+    }
+#pragma unroll
+  for (int kh = 0; kh < kSlice / 16; ++kh) {
+    uint32_t vw[4][D / 32];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int key = kh * 16 + 2 * t + (r & 1) + (r >> 1) * 8;
+      if constexpr (D == 128) {
+        const uint4 x = *reinterpret_cast<const uint4*>(vb + chunk_at<D>(key, g));
+        vw[r][0] = x.x; vw[r][1] = x.y; vw[r][2] = x.z; vw[r][3] = x.w;
+      } else {
+        const uint2 x =
+            *reinterpret_cast<const uint2*>(vb + chunk_at<D>(key, g >> 1) + (g & 1) * 8);
+        vw[r][0] = x.x; vw[r][1] = x.y;
+      }
+    }
+    if constexpr (kTail) {
+      // A zero weight does not hide a NaN code of a key that the row does not see (or of what
+      // lies after the last token): NaN codes are taken out here and put back into the rows
+      // that see them.
+      uint32_t nan = 0;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w)
+          nan |= __vcmpeq4(vw[r][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+      if (__any_sync(0xffffffffu, nan != 0)) {
+        uint4 va[MT];  // 1 where the row sees the key
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int part = 0; part < S::PARTS; ++part)
-            mma_f16(st.o[mt][4 * w + q + u], pa[mt][part], b0, b1);
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              const int key = kh * 16 + nt * 8 + 2 * t;
+              (&va[mt].x)[half + 2 * nt] = (key < left[mt][half] ? 0x3c00u : 0u) |
+                                           (key + 1 < left[mt][half] ? 0x3c000000u : 0u);
+            }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          uint32_t ind[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const uint32_t bad = __vcmpeq4(vw[r][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            vw[r][w] &= ~bad;
+            ind[r] = bad & 0x38383838u;  // the code of 1.0
+          }
+#pragma unroll
+          for (int q = 0; q < 4; q += 2) {
+            const uint32_t sel = q < 2 ? 0x5140u : 0x7362u;
+            uint32_t b0[2], b1[2];
+            f16x4_from_e4m3(__byte_perm(ind[0], ind[1], sel), b0[0], b0[1]);
+            f16x4_from_e4m3(__byte_perm(ind[2], ind[3], sel), b1[0], b1[1]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                mma_f16(hit, va[mt], b0[u], b1[u]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (hit[i] > 0.0f) st.o[mt][4 * w + q + u][i] = __uint_as_float(0x7fffffffu);
+              }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        const uint32_t sel = q < 2 ? 0x5140u : 0x7362u;
+        uint32_t b0[2], b1[2];
+        f16x4_from_e4m3(__byte_perm(vw[0][w], vw[1][w], sel), b0[0], b0[1]);
+        f16x4_from_e4m3(__byte_perm(vw[2][w], vw[3][w], sel), b1[0], b1[1]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int part = 0; part < S::PARTS; ++part)
+              mma_f16(st.o[mt][4 * w + q + u], pa[mt][part][kh], b0[u], b1[u]);
       }
     }
   }
 }
 
 template <class T, int D, int MT>
-__global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(Shape<T, D, MT>::THREADS, Shape<T, D, MT>::CTAS)
 attn_kernel(const CacheAttnParams p, float* ws_o, float2* ws_ml, UnitDesc* desc) {
   using S = Shape<T, D, MT>;
+  constexpr int kWarps = S::WARPS, kThreads = S::THREADS, kStages = S::STAGES;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Work work;
+  __shared__ Work<kThreads> work;
   __shared__ float s_rowf[S::ROWS];
-  __shared__ int64_t s_seen[S::ROWS];
+  __shared__ int s_seen[S::ROWS];
   __shared__ float s_m[kWarps][S::ROWS], s_l[kWarps][S::ROWS];
-  __shared__ __align__(16) float s_scale[kWarps][kStages][4];  // k scale, v scale, present
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int G = p.Hq / p.Hkv, R = G * p.window;
   const int nrg = (R + S::ROWS - 1) / S::ROWS;
@@ -365,7 +384,7 @@ attn_kernel(const CacheAttnParams p, float* ws_o, float2* ws_ml, UnitDesc* desc)
     base = b0;
   }
   total *= U;
-  int64_t ctas = (total + kMinBlocks - 1) / kMinBlocks;
+  int64_t ctas = (total + kMinCost - 1) / kMinCost;
   if (ctas > gridDim.x) ctas = gridDim.x;
   if (blockIdx.x >= ctas) return;
   const int64_t cta = blockIdx.x;
@@ -403,11 +422,16 @@ attn_kernel(const CacheAttnParams p, float* ws_o, float2* ws_ml, UnitDesc* desc)
       }
     }
     const int b = base + row;
-    const int64_t nb = work.pre[row + 1] - work.pre[row];
+    const int64_t cost = work.pre[row + 1] - work.pre[row], nb = cost - kUnitCost;
     const int64_t off = pos - before - work.pre[row] * U;
-    const int unit = (int)(off / nb);
-    const int64_t blk0 = off - unit * nb;
-    const int64_t blk1 = blk0 + (end - pos) < nb ? blk0 + (end - pos) : nb;
+    const int unit = (int)(off / cost);
+    const int64_t x0 = off - unit * cost;
+    const int64_t x1 = x0 + (end - pos) < cost ? x0 + (end - pos) : cost;
+    const int64_t stop = pos + (cost - x0);  // end of the unit
+    pos += x1 - x0;
+    const int64_t blk0 = x0 > kUnitCost ? x0 - kUnitCost : 0;
+    const int64_t blk1 = x1 > kUnitCost ? x1 - kUnitCost : 0;
+    if (blk0 == blk1) continue;  // the range ends before the unit's first block
     const int h = unit / nrg, rg = unit - h * nrg;
     const int rows = R - rg * S::ROWS < S::ROWS ? R - rg * S::ROWS : S::ROWS;
     const int n_tok = row_tokens(p, b);
@@ -434,7 +458,8 @@ attn_kernel(const CacheAttnParams p, float* ws_o, float2* ws_ml, UnitDesc* desc)
       if (lane == 0) {
         s_rowf[r] = p.scale * 1.44269504f * pow2f(-e);
         // rows that are not live see everything: they force no mask, and are not stored
-        s_seen[r] = live ? start + j + 1 : (int64_t)1 << 60;
+        const int64_t n = start + j + 1;
+        s_seen[r] = live && n < kNoEnd ? (int)n : kNoEnd;
       }
       const float up = pow2f(e);
 #pragma unroll
@@ -453,7 +478,7 @@ attn_kernel(const CacheAttnParams p, float* ws_o, float2* ws_ml, UnitDesc* desc)
     __syncthreads();
 
     float rowf[MT][2];
-    int64_t seen[MT][2], least = (int64_t)1 << 60;
+    int seen[MT][2], least = kNoEnd;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -461,7 +486,8 @@ attn_kernel(const CacheAttnParams p, float* ws_o, float2* ws_ml, UnitDesc* desc)
         rowf[mt][half] = s_rowf[mt * 16 + half * 8 + g];
         seen[mt][half] = s_seen[mt * 16 + half * 8 + g];
       }
-    for (int r = 0; r < S::ROWS; ++r) least = s_seen[r] < least ? s_seen[r] : least;
+    for (int r = lane; r < S::ROWS; r += 32) least = min(least, s_seen[r]);
+    least = __reduce_min_sync(0xffffffffu, least);
 
     WarpState<T, D, MT> st;
 #pragma unroll
@@ -474,74 +500,79 @@ attn_kernel(const CacheAttnParams p, float* ws_o, float2* ws_ml, UnitDesc* desc)
       st.l[mt][0] = st.l[mt][1] = 0.0f;
     }
 
-    // slices of this warp: blk0 * 4 + warp, + kWarps, ...
-    const int64_t first = blk0 * (kPage / kSlice) + warp, last = blk1 * (kPage / kSlice);
-    const int n_sl = last > first ? (int)((last - first + kWarps - 1) / kWarps) : 0;
+    // slices of this warp: warp, warp + kWarps, ... of the piece
+    const int first = (int)blk0 * (kPage / kSlice) + warp, last = (int)blk1 * (kPage / kSlice);
     uint8_t* ring = smem + warp * kStages * S::STAGE;
+    const uint32_t ring_u = ptx::smem_u32(ring);
     const int32_t* table = p.table + (int64_t)b * p.max_pages;
-    auto page_of = [&](int i) {
-      return i < n_sl ? table[(first + (int64_t)i * kWarps) / (kPage / kSlice)] : -1;
+    const uint4* qf = reinterpret_cast<const uint4*>(smem + S::BUF);
+    // 16-byte copies of a lane: chunk lane + 32 c, at rotated places of their rows
+    const int put0 = D == 128 ? (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4)
+                              : (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+    struct Pending {
+      float ks, vs;
+      bool present;
     };
-    auto issue = [&](int i, int page) {
-      if (i < n_sl) {
-        const int stage = i % kStages;
-        float* sc = s_scale[warp][stage];
-        const bool present = page >= 0 && page < p.n_pages;
-        if (page >= p.n_pages && lane == 0 && p.status) atomicOr(p.status, KDA_STATUS_BAD_PAGE);
-        if (lane == 0) sc[2] = present ? 1.0f : 0.0f;
-        if (present) {
-          const int64_t slice = (int64_t)page * p.Hkv + h;
-          const int key = (int)((first + (int64_t)i * kWarps) % (kPage / kSlice)) * kSlice;
-          const int64_t at = (slice * kPage + key) * D;
-          const uint32_t dst = ptx::smem_u32(ring + stage * S::STAGE);
+    auto page_of = [&](int sl) { return sl < last ? table[sl / (kPage / kSlice)] : -1; };
+    auto issue = [&](int sl, int page, int stage) {
+      Pending n = {0.0f, 0.0f, page >= 0 && page < p.n_pages};
+      if (n.present) {
+        const int64_t slice = (int64_t)page * p.Hkv + h;
+        const int64_t at =
+            slice * (kPage * D) + (sl % (kPage / kSlice)) * S::SLICE_BYTES + lane * 16;
+        const uint8_t* kp = p.kc + at;
+        const uint8_t* vp = p.vc + at;
+        const uint32_t dst = ring_u + stage * S::STAGE;
 #pragma unroll
-          for (int c = 0; c < S::SLICE_BYTES / 512; ++c) {
-            const int idx = c * 32 + lane, r = idx / (D / 16), ch = idx % (D / 16);
-            cp16(dst + chunk_at<D>(r, ch), p.kc + at + idx * 16);
-            cp16(dst + S::SLICE_BYTES + chunk_at<D>(r, ch), p.vc + at + idx * 16);
-          }
-          if (lane == 0) {
-            cp4(ptx::smem_u32(sc), p.ks + slice);
-            cp4(ptx::smem_u32(sc + 1), p.vs + slice);
-          }
-        }
+        for (int c = 0; c < S::SLICE_BYTES / 512; ++c)
+          cp16(dst + c * 512 + (D == 128 ? put0 ^ ((c & 1) * 64) : put0), kp + c * 512);
+#pragma unroll
+        for (int c = 0; c < S::SLICE_BYTES / 512; ++c)
+          cp16(dst + S::SLICE_BYTES + c * 512 + (D == 128 ? put0 ^ ((c & 1) * 64) : put0),
+               vp + c * 512);
+        n.ks = p.ks[slice];
+        n.vs = p.vs[slice];
+      } else if (page >= 0 && lane == 0 && p.status) {
+        atomicOr(p.status, KDA_STATUS_BAD_PAGE);
       }
       cp_commit();
+      return n;
     };
+    Pending pend[kStages - 1];
     int next_page;
     {
       int pg[kStages];
 #pragma unroll
-      for (int i = 0; i < kStages; ++i) pg[i] = page_of(i);
+      for (int i = 0; i < kStages; ++i) pg[i] = page_of(first + i * kWarps);
 #pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) issue(i, pg[i]);
+      for (int i = 0; i < kStages - 1; ++i) pend[i] = issue(first + i * kWarps, pg[i], i);
       next_page = pg[kStages - 1];
     }
-    for (int i = 0; i < n_sl; ++i) {
+    int stage = 0;
+#pragma unroll 1
+    for (int sl = first; sl < last; sl += kWarps) {
       cp_wait<kStages - 2>();
       __syncwarp();
-      const int page = next_page;
-      next_page = page_of(i + kStages);
-      issue(i + kStages - 1, page);
-      const int stage = i % kStages;
-      const float* sc = s_scale[warp][stage];
-      if (sc[2] == 0.0f) continue;
+      const Pending cur = pend[0];
+#pragma unroll
+      for (int i = 0; i < kStages - 2; ++i) pend[i] = pend[i + 1];
+      const int ahead = sl + (kStages - 1) * kWarps;
+      pend[kStages - 2] = issue(ahead, next_page, stage == 0 ? kStages - 1 : stage - 1);
+      next_page = page_of(ahead + kWarps);
       const uint8_t* kb = ring + stage * S::STAGE;
       const uint8_t* vb = kb + S::SLICE_BYTES;
-      const uint4* qf = reinterpret_cast<const uint4*>(smem + S::BUF);
-      const int64_t t0 = (first + (int64_t)i * kWarps) * kSlice;
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+      if (!cur.present) continue;
       int left[MT][2];
+      if (sl * kSlice + kSlice <= least) {
+        slice_step<T, D, MT, false>(st, kb, vb, qf, cur.ks, cur.vs, rowf, left, lane);
+      } else {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int64_t n = seen[mt][half] - t0;
-          left[mt][half] = n < 0 ? 0 : (n > kSlice ? kSlice : (int)n);
-        }
-      if (t0 + kSlice <= least)
-        slice_step<T, D, MT, false>(st, kb, vb, qf, sc[0], sc[1], rowf, left, lane);
-      else
-        slice_step<T, D, MT, true>(st, kb, vb, qf, sc[0], sc[1], rowf, left, lane);
+          for (int half = 0; half < 2; ++half) left[mt][half] = seen[mt][half] - sl * kSlice;
+        slice_step<T, D, MT, true>(st, kb, vb, qf, cur.ks, cur.vs, rowf, left, lane);
+      }
     }
     cp_wait<0>();
 
@@ -564,12 +595,14 @@ attn_kernel(const CacheAttnParams p, float* ws_o, float2* ws_ml, UnitDesc* desc)
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        float* o = acc + (warp * S::ROWS + mt * 16 + half * 8 + g) * D + t * (D / 4);
+        float* o = acc + (warp * S::ROWS + mt * 16 + half * 8 + g) * S::ROW_F + t * S::LANE_F;
 #pragma unroll
-        for (int n = 0; n < S::NT; ++n) {  // channels t D/4 + n and t D/4 + D/8 + n
-          o[n] = st.o[mt][n][half * 2];
-          o[D / 8 + n] = st.o[mt][n][half * 2 + 1];
-        }
+        for (int n = 0; n < S::NT; n += 4)  // channels t D/4 + n and t D/4 + D/8 + n
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            *reinterpret_cast<float4*>(o + u * (D / 8) + n) =
+                make_float4(st.o[mt][n][half * 2 + u], st.o[mt][n + 1][half * 2 + u],
+                            st.o[mt][n + 2][half * 2 + u], st.o[mt][n + 3][half * 2 + u]);
       }
     __syncthreads();
     const bool whole = blk0 == 0 && blk1 == nb;
@@ -584,7 +617,8 @@ attn_kernel(const CacheAttnParams p, float* ws_o, float2* ws_ml, UnitDesc* desc)
       for (int w = 0; w < kWarps; ++w) {
         if (s_m[w][r] == -INFINITY && s_l[w][r] == 0.0f) continue;  // saw no key
         const float f = ptx::ex2_approx(s_m[w][r] - (top == -INFINITY ? 0.0f : top));
-        const float4 x = *reinterpret_cast<const float4*>(acc + (w * S::ROWS + r) * D + c);
+        const float4 x = *reinterpret_cast<const float4*>(
+            acc + (w * S::ROWS + r) * S::ROW_F + (c / (D / 4)) * S::LANE_F + c % (D / 4));
         l += f * s_l[w][r];
         o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
       }
@@ -604,7 +638,6 @@ attn_kernel(const CacheAttnParams p, float* ws_o, float2* ws_ml, UnitDesc* desc)
     }
     if (!whole && blk0 == 0 && threadIdx.x == 0) {
       // the pieces of this unit end in the CTA whose range holds its last block
-      const int64_t stop = pos + nb;
       int pieces = 1;
       while (total * (cta + pieces) / ctas < stop) ++pieces;
       UnitDesc d;
@@ -612,49 +645,75 @@ attn_kernel(const CacheAttnParams p, float* ws_o, float2* ws_ml, UnitDesc* desc)
       desc[blockIdx.x] = d;
     }
     __syncthreads();
-    pos += blk1 - blk0;
   }
 }
 
-constexpr int kJoinRows = 4;
+constexpr int kJoinWarps = 8;
 
 // Joins the pieces of the unit that CTA c began and others went on with: c's second slot, then
-// the first slots of c + 1, c + 2, ...
+// the first slots of c + 1, c + 2, ... One CTA per (c, row): its warps sum every eighth piece, and
+// their sums are added in order.
 template <class T, int D, int MT>
-__global__ void __launch_bounds__(kJoinRows * 32)
+__global__ void __launch_bounds__(kJoinWarps * 32)
 join_kernel(const CacheAttnParams p, const float* ws_o, const float2* ws_ml, const UnitDesc* desc) {
   using S = Shape<T, D, MT>;
+  constexpr int N = D / 32;
+  __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps], s_top[kJoinWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const UnitDesc d = desc[blockIdx.x];
-  if (d.pieces == 0) return;
   const int G = p.Hq / p.Hkv, R = G * p.window;
-  const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int gr = d.rg * S::ROWS + r;
-  if (r >= S::ROWS || gr >= R) return;
-  const int j = gr / G;
-  constexpr int N = D / 32;
+  const int r = blockIdx.y, gr = d.rg * S::ROWS + r;
+  if (d.pieces == 0 || gr >= R) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto slot_row = [&](int i) {
+    return (int64_t)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * S::ROWS + r;
+  };
   float top = -INFINITY;
-  for (int i = 0; i < d.pieces; ++i) {
-    const int64_t slot = i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i);
-    top = fmaxf(top, ws_ml[slot * S::ROWS + r].x);
-  }
+  for (int i = threadIdx.x; i < d.pieces; i += kJoinWarps * 32) top = fmaxf(top, ws_ml[slot_row(i)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) s_top[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_top[w]);
+  const float mu = top == -INFINITY ? 0.0f : top;
   float o[N], l = 0.0f;
 #pragma unroll
   for (int c = 0; c < N; ++c) o[c] = 0.0f;
-  for (int i = 0; i < d.pieces; ++i) {
-    const int64_t slot = i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i);
-    const float2 ml = ws_ml[slot * S::ROWS + r];
-    if (ml.x == -INFINITY && ml.y == 0.0f) continue;
-    const float f = ptx::ex2_approx(ml.x - (top == -INFINITY ? 0.0f : top));
-    l += f * ml.y;
+#pragma unroll 4
+  for (int i = warp; i < d.pieces; i += kJoinWarps) {
+    const int64_t at = slot_row(i);
+    const float2 ml = ws_ml[at];
+    float x[N];
+    if constexpr (N == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(ws_o + at * D + lane * N);
+      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(ws_o + at * D + lane * N);
+      x[0] = v.x; x[1] = v.y;
+    }
+    // a piece in which the row saw no key has m = -inf and only zeros
+    const float f = ptx::ex2_approx(ml.x - mu);
+    l = fmaf(f, ml.y, l);
 #pragma unroll
-    for (int c = 0; c < N; ++c) o[c] += f * ws_o[(slot * S::ROWS + r) * D + lane * N + c];
+    for (int c = 0; c < N; ++c) o[c] = fmaf(f, x[c], o[c]);
   }
-  const bool live = j < row_tokens(p, d.b);
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  T* dst = (T*)p.o + ((int64_t)(d.b * p.window + j) * p.Hq + d.h * G + (gr - j * G)) * D + lane * N;
 #pragma unroll
-  for (int c = 0; c < N; ++c) st_elem(dst, c, live ? o[c] * inv : 0.0f);
+  for (int c = 0; c < N; ++c) s_o[warp][lane * N + c] = o[c];
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  float sum = 0.0f;
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    sum += s_o[w][threadIdx.x];
+    l += s_l[w];
+  }
+  const int j = gr / G;
+  const bool live = j < row_tokens(p, d.b);
+  T* dst = (T*)p.o + ((int64_t)(d.b * p.window + j) * p.Hq + d.h * G + (gr - j * G)) * D;
+  st_elem(dst, threadIdx.x, live && l != 0.0f ? sum / l : 0.0f);
 }
 
 size_t piece_bytes(int rows, int d) { return (size_t)2 * kMaxCtas * rows * d * sizeof(float); }
@@ -675,26 +734,28 @@ kda_status launch_t(const CacheAttnParams& p, cudaStream_t s) {
     if (e == cudaSuccess)
       e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, attn_kernel<T, D, MT>, kThreads,
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, attn_kernel<T, D, MT>, S::THREADS,
                                                         S::SMEM);
     if (e != cudaSuccess || per < 1)
       return set_error(KDA_ERR_CUDA, std::string("kda_cache_attention: ") + cudaGetErrorString(e));
     ctas_of[dev] = sms * per < kMaxCtas ? sms * per : kMaxCtas;
   }
   const int G = p.Hq / p.Hkv, nrg = (G * p.window + S::ROWS - 1) / S::ROWS;
-  // no more CTAs than the page table allows ranges of kMinBlocks blocks
-  const int64_t most = ((int64_t)p.batch * p.Hkv * nrg * p.max_pages + kMinBlocks - 1) / kMinBlocks;
+  // no more CTAs than the page table allows ranges of kMinCost
+  const int64_t most =
+      ((int64_t)p.batch * p.Hkv * nrg * (p.max_pages + kUnitCost) + kMinCost - 1) / kMinCost;
   const int ctas = most < ctas_of[dev] ? (int)most : ctas_of[dev];
   uint8_t* ws = (uint8_t*)p.ws;
   float* ws_o = (float*)ws;
   float2* ws_ml = (float2*)(ws + piece_bytes(S::ROWS, D));
   UnitDesc* desc = (UnitDesc*)(ws + piece_bytes(S::ROWS, D) + ml_bytes(S::ROWS));
-  attn_kernel<T, D, MT><<<ctas, kThreads, S::SMEM, s>>>(p, ws_o, ws_ml, desc);
+  attn_kernel<T, D, MT><<<ctas, S::THREADS, S::SMEM, s>>>(p, ws_o, ws_ml, desc);
   kda_status st = check_launch("kda_cache_attention");
   if (st != KDA_OK) return st;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, S::ROWS / kJoinRows);
-  cfg.blockDim = dim3(kJoinRows * 32);
+  const int rows = G * p.window < S::ROWS ? G * p.window : S::ROWS;
+  cfg.gridDim = dim3(ctas, rows);
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -18,6 +18,15 @@ __device__ __forceinline__ uint32_t f16x2_from_e4m3(uint32_t codes) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
   return r;
 }
+// The four codes of a word: (0, 1) to lo, (2, 3) to hi.
+__device__ __forceinline__ void f16x4_from_e4m3(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+}
 __device__ __forceinline__ float2 f32x2_from_f16x2(uint32_t h) {
   float2 r;
   asm("{\n\t.reg .b16 lo, hi;\n\t"
