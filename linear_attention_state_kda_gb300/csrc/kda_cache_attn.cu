@@ -12,10 +12,10 @@
 // a power of two that puts its largest entry in [2^13, 2^14) and rounded to f16: exact for bf16
 // entries down to 2^-28 of the largest; fp32 queries are carried as the sum of two f16 parts (22
 // bits). With x_t the score in units of log2 and e_t the exponent of t's value scale, the row
-// keeps M = max_t (x_t + e_t) and accumulates
-//     P_t = 2^(x_t + e_t - M + 14) (f16; two parts for fp32),  O = sum_t P_t code_t,
-//     l = sum_t 2^(x_t - M + 14) = sum_t P_t 2^-e_t (fp32),    o = O / l.
-// P is at most 2^14 whatever the scales of the pages, and what f16 drops is below 2^-38 of the
+// keeps M, at most 8 below max_t (x_t + e_t), and accumulates
+//     P_t = 2^(x_t + e_t - M + 7) (f16; two parts for fp32),  O = sum_t P_t code_t,
+//     l = sum_t 2^(x_t - M + 7) = sum_t P_t 2^-e_t (fp32),    o = O / l.
+// P is at most 2^15 whatever the scales of the pages, and what f16 drops is below 2^-32 of the
 // row's largest term.
 //
 // Layout. Lane (g, t) = (lane / 4, lane % 4) of an m16n8k16 MMA. The order of the channels in the
@@ -25,15 +25,15 @@
 // values, whose bytes are interleaved pairwise to give two keys of one channel (d = 128; half of
 // that for d = 64). A lane's outputs are then 32 consecutive channels of its row.
 //
-// Every warp walks 16-key slices of its own through a private ring of kStages shared-memory
-// buffers filled with 16-byte asynchronous copies; nothing in the loop waits for another warp.
-// The warps' results are joined at the end of the unit.
-//
-// Work split. The rows' 64-key blocks are laid end to end (row, head, row group, block) and cut
-// into as many equal ranges as CTAs fit on the GPU, so that ragged lengths and few rows load
-// every SM alike. A unit that lies in one range is finished there; the pieces of a unit that is
-// cut go to the workspace (each CTA has at most two) and a second kernel, launched ahead of time
-// and released when the first ends, joins them in order: no atomics, the same bits every time.
+// Work split. The rows' key slices (32 keys) are laid end to end (row, head, row group, slice) and
+// cut into as many equal ranges as warps fit on the GPU (8 per SM), so that ragged lengths and few
+// rows load every SM alike. A warp walks its range alone, through a private ring of shared-memory
+// buffers filled with 16-byte asynchronous copies: no barrier, and while one warp begins or ends
+// a unit the others keep the memory busy. (A CTA per unit, its warps joined at the unit's end,
+// left 4-8 us of latency per unit uncovered: 398 us against this split's on 128 rows of up to 16k
+// tokens.) A unit that lies in one range is finished there; the pieces of a unit that is cut go to
+// the workspace (each warp has at most two) and a second kernel, launched ahead of time and
+// released when the first ends, joins them in order: no atomics, the same bits every time.
 #include "kda_internal.cuh"
 #include "kda_fp8.cuh"
 #include "ptx.cuh"
@@ -41,41 +41,38 @@
 namespace kda {
 namespace {
 
-constexpr int kSlice = 32;     // keys per warp step
-constexpr int kMaxCtas = 320;  // bound of the grid (sizes the workspace)
+constexpr int kSlice = 32;    // keys per warp step
+constexpr int kWarps = 8;     // per CTA, one CTA per SM: up to 255 registers a thread
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxWorkers = 1280;  // warps that share the work, at most (sizes the workspace)
+constexpr int kWindows = 512;      // windows of rows in the search for a warp's first row
 // P is 2^kPBase for a term equal to the row's M, and M is raised only when a term exceeds it by
 // more than 2^kSlack: P <= 2^15 fits f16, and the accumulators are rescaled once or twice per
 // unit instead of in most steps.
 constexpr float kPBase = 7.0f, kSlack = 8.0f;
-constexpr int kUnitCost = 3;   // what beginning and joining a unit takes, in blocks
-constexpr int kMinCost = kUnitCost + 2;  // least work of a CTA: a unit of two blocks
+constexpr int kUnitCost = 2;  // what beginning and ending a unit takes, in slices
+constexpr int kMinCost = kUnitCost + 2;  // least work of a warp
 constexpr int kNoEnd = 1 << 30;    // beyond the positions of the largest page table
 constexpr int kMinScaleExp = -60;  // clamp of e_t in M, so that l stays in range
 
-struct UnitDesc {  // a unit whose first piece is CTA c's last one
-  int32_t b, h, rg, pieces;
+struct UnitDesc {  // of a unit that is cut: the warp that began it, and how many share it (else 0)
+  int32_t worker, pieces;
 };
 
 template <class T, int D, int MT>
 struct Shape {
   static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;
   static constexpr int ROWS = 16 * MT;
-  static constexpr int WARPS = MT == 1 ? 6 : 8;
-  static constexpr int THREADS = WARPS * 32;
-  static constexpr int CTAS = MT == 1 ? 2 : 1;     // resident per SM
-  static constexpr int STAGES = D == 128 ? 2 : 3;  // slices in a warp's ring
   static constexpr int KSTEPS = D / 16;
-  static constexpr int NT = D / 8;                 // n-tiles of the second product
-  static constexpr int SLICE_BYTES = kSlice * D;   // one of K, V
+  static constexpr int NT = D / 8;                // n-tiles of the second product
+  static constexpr int SLICE_BYTES = kSlice * D;  // one of K, V
   static constexpr int STAGE = 2 * SLICE_BYTES;
-  static constexpr int RING = WARPS * STAGES * STAGE;
-  // A warp's results in shared memory: each lane's D / 4 channels of a row 4 floats further than
-  // the last lane's, so that 16-byte accesses of 8 lanes touch every bank once.
-  static constexpr int LANE_F = D / 4 + 4, ROW_F = 4 * LANE_F;
-  static constexpr int MERGE = WARPS * ROWS * ROW_F * 4;
-  static constexpr int BUF = RING > MERGE ? RING : MERGE;
-  static constexpr int QFRAG = MT * PARTS * KSTEPS * 512;
-  static constexpr int SMEM = BUF + QFRAG;
+  static constexpr int STAGES = MT == 2 && D == 128 ? 2 : 3;
+  // Query operands: in registers for one row tile, in shared memory for two.
+  static constexpr bool QREG = MT == 1;
+  static constexpr int QFRAGS = MT * PARTS * KSTEPS;
+  static constexpr int QBYTES = QREG ? 0 : QFRAGS * 512;
+  static constexpr int SMEM = kWarps * (STAGES * STAGE + QBYTES);
 };
 
 // Byte of 16-byte chunk c of row r of a slice: chunks are permuted within the row so that both
@@ -118,40 +115,24 @@ __device__ __forceinline__ int row_tokens(const CacheAttnParams& p, int b) {
   const int n = p.lens ? p.lens[b] : p.window;
   return n < 0 ? 0 : (n > p.window ? p.window : n);
 }
-__device__ __forceinline__ int64_t row_blocks(const CacheAttnParams& p, int b, bool flag) {
+// Key slices that any query of row b sees (within the page table).
+__device__ __forceinline__ int row_slices(const CacheAttnParams& p, int b, bool flag) {
+  if (b >= p.batch) return 0;
   const int n = row_tokens(p, b);
   if (n == 0) return 0;
-  const int64_t blocks = ((int64_t)p.start[b] + n + kPage - 1) / kPage;
-  if (blocks <= p.max_pages) return blocks;
+  const int64_t keys = (int64_t)p.start[b] + n, most = (int64_t)p.max_pages * kPage;
+  if (keys <= most) return (int)((keys + kSlice - 1) / kSlice);
   if (flag && p.status) atomicOr(p.status, KDA_STATUS_BAD_PAGE);
-  return p.max_pages;
+  return (int)(most / kSlice);
 }
-
-template <int kThreads>
-struct Work {                 // what a CTA knows of the list of blocks
-  int64_t pre[kThreads + 1];  // cost of one unit of rows base .. base + i - 1, summed
-  int64_t part[kThreads / 32];
-};
-
-// pre[] of rows base .. base + kThreads - 1. Every thread calls.
-template <int kThreads>
-__device__ __forceinline__ void scan_rows(const CacheAttnParams& p, Work<kThreads>& w, int base,
-                                          bool flag) {
-  const int b = base + threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t v = b < p.batch ? row_blocks(p, b, flag) : 0;
-  if (v > 0) v += kUnitCost;
+__device__ __forceinline__ int row_cost(const CacheAttnParams& p, int b, bool flag) {
+  const int n = row_slices(p, b, flag);
+  return n > 0 ? n + kUnitCost : 0;
+}
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  __syncthreads();
-  if (lane == 31) w.part[warp] = v;
-  __syncthreads();
-  for (int i = 0; i < warp; ++i) v += w.part[i];
-  w.pre[threadIdx.x + 1] = v;
-  if (threadIdx.x == 0) w.pre[0] = 0;
-  __syncthreads();
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
 template <class T, int D, int MT>
@@ -164,7 +145,10 @@ struct WarpState {
 // some row; `left` of its keys are seen by each of the lane's rows.
 template <class T, int D, int MT, bool kTail>
 __device__ __forceinline__ void slice_step(WarpState<T, D, MT>& st, const uint8_t* kb,
-                                           const uint8_t* vb, const uint4* qfrag, float ks, float vs,
+                                           const uint8_t* vb,
+                                           const uint4 (&qreg)[Shape<T, D, MT>::QREG
+                                                                   ? Shape<T, D, MT>::QFRAGS : 1],
+                                           const uint4* qfrag, float ks, float vs,
                                            const float (&rowf)[MT][2], const int (&left)[MT][2],
                                            int lane) {
   using S = Shape<T, D, MT>;
@@ -193,7 +177,8 @@ __device__ __forceinline__ void slice_step(WarpState<T, D, MT>& st, const uint8_
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int part = 0; part < S::PARTS; ++part) {
-          const uint4 a = qfrag[((mt * S::PARTS + part) * S::KSTEPS + 4 * j + k4) * 32 + lane];
+          const int at = (mt * S::PARTS + part) * S::KSTEPS + 4 * j + k4;
+          const uint4 a = S::QREG ? qreg[S::QREG ? at : 0] : qfrag[at * 32 + lane];
 #pragma unroll
           for (int nt = 0; nt < NK; ++nt) mma_f16(s[mt][nt], a, b[nt][0], b[nt][1]);
         }
@@ -351,164 +336,103 @@ __device__ __forceinline__ void slice_step(WarpState<T, D, MT>& st, const uint8_
 }
 
 template <class T, int D, int MT>
-__global__ void __launch_bounds__(Shape<T, D, MT>::THREADS, Shape<T, D, MT>::CTAS)
-attn_kernel(const CacheAttnParams p, float* ws_o, float2* ws_ml, UnitDesc* desc) {
+__global__ void __launch_bounds__(kThreads, 1)
+attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml, UnitDesc* desc) {
   using S = Shape<T, D, MT>;
-  constexpr int kWarps = S::WARPS, kThreads = S::THREADS, kStages = S::STAGES;
+  constexpr int kStages = S::STAGES;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Work<kThreads> work;
-  __shared__ float s_rowf[S::ROWS];
-  __shared__ int s_seen[S::ROWS];
-  __shared__ float s_m[kWarps][S::ROWS], s_l[kWarps][S::ROWS];
+  __shared__ int64_t s_win[kWindows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int G = p.Hq / p.Hkv, R = G * p.window;
   const int nrg = (R + S::ROWS - 1) / S::ROWS;
   const int U = p.Hkv * nrg;
-  const bool flag = blockIdx.x == 0;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // rows without keys get their zeros here
-  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-    if (row_blocks(p, b, false) > 0) continue;
-    T* o = (T*)p.o + (int64_t)b * p.window * p.Hq * D;
-    for (int i = threadIdx.x; i < p.window * p.Hq * D; i += kThreads) st_elem(o, i, 0.0f);
+  // cost of each window of rows, then of all
+  const int per_win = (p.batch + 32 * kWindows - 1) / (32 * kWindows) * 32;
+  const int n_win = (p.batch + per_win - 1) / per_win;
+  for (int w = warp; w < n_win; w += kWarps) {
+    int64_t c = 0;
+    for (int i = lane; i < per_win; i += 32) c += row_cost(p, w * per_win + i, blockIdx.x == 0);
+    c = warp_sum(c);
+    if (lane == 0) s_win[w] = c;
   }
-  if (threadIdx.x == 0) desc[blockIdx.x].pieces = 0;
-
-  // this CTA's range of the list of blocks
+  __syncthreads();
   int64_t total = 0;
-  int base = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
-    scan_rows(p, work, b0, flag);
-    total += work.pre[kThreads];
-    base = b0;
+  for (int w = lane; w < n_win; w += 32) total += s_win[w];
+  total = warp_sum(total) * U;
+  // this warp's range; consecutive ranges are on different SMs
+  const int worker = warp * gridDim.x + blockIdx.x;
+  int64_t workers = (total + kMinCost - 1) / kMinCost;
+  if (workers > (int64_t)gridDim.x * kWarps) workers = gridDim.x * kWarps;
+  int64_t pos = 0, end = 0;
+  if (worker < workers) {
+    pos = total * worker / workers;
+    end = total * (worker + 1) / workers;
   }
-  total *= U;
-  int64_t ctas = (total + kMinCost - 1) / kMinCost;
-  if (ctas > gridDim.x) ctas = gridDim.x;
-  if (blockIdx.x >= ctas) return;
-  const int64_t cta = blockIdx.x;
-  int64_t pos = total * cta / ctas;
-  const int64_t end = total * (cta + 1) / ctas;
-  int64_t before = 0;  // blocks (times U) before row `base`
-  if (p.batch > kThreads) {
-    base = 0;
+
+  // the row that holds pos: its window, then the 32 rows, then the row
+  int base = 0, row = 0, cost_l = 0, cost = 0;
+  int64_t at = 0;  // where row base + row begins
+  if (pos < end) {
+    int w = 0;
+    for (;; w += 32) {
+      int64_t c = w + lane < n_win ? s_win[w + lane] * U : 0;
+      const int64_t mine = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) c += u;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, at + c <= pos);
+      const int k = __popc(past);  // windows that end at or before pos
+      if (k < 32) {
+        at += __shfl_sync(0xffffffffu, c - mine, k);
+        base = (w + k) * per_win;
+        break;
+      }
+      at += __shfl_sync(0xffffffffu, c, 31);
+    }
     for (;;) {
-      scan_rows(p, work, base, false);
-      if (before + work.pre[kThreads] * U > pos) break;
-      before += work.pre[kThreads] * U;
-      base += kThreads;
+      cost_l = row_cost(p, base + lane, false);
+      const int64_t c = warp_sum(cost_l) * U;
+      if (at + c > pos) break;
+      at += c;
+      base += 32;
     }
+    cost = __shfl_sync(0xffffffffu, cost_l, 0);
   }
-  int row;  // within the scanned rows: the last one that starts at or before pos
-  {
-    int a = 0, z = kThreads - 1;
-    while (a < z) {
-      const int mid = (a + z + 1) >> 1;
-      if (before + work.pre[mid] * U <= pos) a = mid;
-      else z = mid - 1;
-    }
-    row = a;
-  }
+
+  uint8_t* ring = smem + warp * (kStages * S::STAGE + S::QBYTES);
+  const uint32_t ring_u = ptx::smem_u32(ring);
+  uint4* qf = reinterpret_cast<uint4*>(ring + kStages * S::STAGE);
+  // 16-byte copies of a lane: chunk lane + 32 c, at rotated places of their rows
+  const int put0 = D == 128 ? (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4)
+                            : (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
 
   while (pos < end) {
-    // the piece [blk0, blk1) of a unit
-    while (work.pre[row + 1] == work.pre[row] || before + work.pre[row + 1] * U <= pos) {
-      if (++row == kThreads) {
-        before += work.pre[kThreads] * U;
-        base += kThreads;
+    while (at + (int64_t)cost * U <= pos) {
+      at += (int64_t)cost * U;
+      if (++row == 32) {
         row = 0;
-        scan_rows(p, work, base, false);
+        base += 32;
+        cost_l = row_cost(p, base + lane, false);
       }
+      cost = __shfl_sync(0xffffffffu, cost_l, row);
     }
-    const int b = base + row;
-    const int64_t cost = work.pre[row + 1] - work.pre[row], nb = cost - kUnitCost;
-    const int64_t off = pos - before - work.pre[row] * U;
-    const int unit = (int)(off / cost);
-    const int64_t x0 = off - unit * cost;
-    const int64_t x1 = x0 + (end - pos) < cost ? x0 + (end - pos) : cost;
+    // the piece [first, last) of a unit's slices
+    const int b = base + row, n_slices = cost - kUnitCost;
+    const int unit = (int)((pos - at) / cost);
+    const int x0 = (int)((pos - at) - (int64_t)unit * cost);
+    const int x1 = end - pos < cost - x0 ? x0 + (int)(end - pos) : cost;
     const int64_t stop = pos + (cost - x0);  // end of the unit
     pos += x1 - x0;
-    const int64_t blk0 = x0 > kUnitCost ? x0 - kUnitCost : 0;
-    const int64_t blk1 = x1 > kUnitCost ? x1 - kUnitCost : 0;
-    if (blk0 == blk1) continue;  // the range ends before the unit's first block
+    const int first = x0 > kUnitCost ? x0 - kUnitCost : 0;
+    const int last = x1 > kUnitCost ? x1 - kUnitCost : 0;
+    if (first == last) continue;  // the range ends before the unit's first slice
     const int h = unit / nrg, rg = unit - h * nrg;
-    const int rows = R - rg * S::ROWS < S::ROWS ? R - rg * S::ROWS : S::ROWS;
-    const int n_tok = row_tokens(p, b);
-    const int64_t start = p.start[b];
 
-    // queries: scaled by a power of two, rounded to f16 parts, in the order of the MMA's operand
-    for (int r = warp; r < S::ROWS; r += kWarps) {
-      constexpr int N = D / 32;
-      float q[N];
-      uint32_t top = 0;
-      const int gr = rg * S::ROWS + r, j = gr / G;
-      const bool live = r < rows && j < n_tok;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        q[i] = 0.0f;
-        if (live)
-          q[i] = ld_elem((const T*)p.q, ((int64_t)(b * p.window + j) * p.Hq + h * G + (gr - j * G)) * D +
-                                            lane * N + i);
-        top = max(top, finite_abs_bits(q[i]));
-      }
-      top = __reduce_max_sync(0xffffffffu, top);
-      int e = top ? 13 + 127 - (int)(top >> 23) : 0;
-      e = e > 100 ? 100 : (e < -100 ? -100 : e);
-      if (lane == 0) {
-        s_rowf[r] = p.scale * 1.44269504f * pow2f(-e);
-        // rows that are not live see everything: they force no mask, and are not stored
-        const int64_t n = start + j + 1;
-        s_seen[r] = live && n < kNoEnd ? (int)n : kNoEnd;
-      }
-      const float up = pow2f(e);
-#pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        // channels c, c + 1: lane quarter t', k-step k, register pair (c & 2)
-        const int c = lane * N + i, tt = c / (D / 4), k = (c % (D / 4)) / 4;
-        const int reg = (r & 15) / 8 + (c & 2);
-        const uint32_t hi = f16x2(q[i] * up, q[i + 1] * up);
-        uint32_t* f = reinterpret_cast<uint32_t*>(smem + S::BUF);
-        const int at = (((r / 16) * S::PARTS * S::KSTEPS + k) * 32 + (r & 7) * 4 + tt) * 4 + reg;
-        f[at] = hi;
-        if constexpr (S::PARTS == 2)
-          f[at + S::KSTEPS * 128] = f16x2_rest(q[i] * up, q[i + 1] * up, hi);
-      }
-    }
-    __syncthreads();
-
-    float rowf[MT][2];
-    int seen[MT][2], least = kNoEnd;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        rowf[mt][half] = s_rowf[mt * 16 + half * 8 + g];
-        seen[mt][half] = s_seen[mt * 16 + half * 8 + g];
-      }
-    for (int r = lane; r < S::ROWS; r += 32) least = min(least, s_seen[r]);
-    least = __reduce_min_sync(0xffffffffu, least);
-
-    WarpState<T, D, MT> st;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int n = 0; n < S::NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) st.o[mt][n][i] = 0.0f;
-      st.m[mt][0] = st.m[mt][1] = -INFINITY;
-      st.l[mt][0] = st.l[mt][1] = 0.0f;
-    }
-
-    // slices of this warp: warp, warp + kWarps, ... of the piece
-    const int first = (int)blk0 * (kPage / kSlice) + warp, last = (int)blk1 * (kPage / kSlice);
-    uint8_t* ring = smem + warp * kStages * S::STAGE;
-    const uint32_t ring_u = ptx::smem_u32(ring);
     const int32_t* table = p.table + (int64_t)b * p.max_pages;
-    const uint4* qf = reinterpret_cast<const uint4*>(smem + S::BUF);
-    // 16-byte copies of a lane: chunk lane + 32 c, at rotated places of their rows
-    const int put0 = D == 128 ? (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4)
-                              : (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
     struct Pending {
       float ks, vs;
       bool present;
@@ -518,10 +442,10 @@ attn_kernel(const CacheAttnParams p, float* ws_o, float2* ws_ml, UnitDesc* desc)
       Pending n = {0.0f, 0.0f, page >= 0 && page < p.n_pages};
       if (n.present) {
         const int64_t slice = (int64_t)page * p.Hkv + h;
-        const int64_t at =
+        const int64_t off =
             slice * (kPage * D) + (sl % (kPage / kSlice)) * S::SLICE_BYTES + lane * 16;
-        const uint8_t* kp = p.kc + at;
-        const uint8_t* vp = p.vc + at;
+        const uint8_t* kp = p.kc + off;
+        const uint8_t* vp = p.vc + off;
         const uint32_t dst = ring_u + stage * S::STAGE;
 #pragma unroll
         for (int c = 0; c < S::SLICE_BYTES / 512; ++c)
@@ -543,40 +467,114 @@ attn_kernel(const CacheAttnParams p, float* ws_o, float2* ws_ml, UnitDesc* desc)
     {
       int pg[kStages];
 #pragma unroll
-      for (int i = 0; i < kStages; ++i) pg[i] = page_of(first + i * kWarps);
+      for (int i = 0; i < kStages; ++i) pg[i] = page_of(first + i);
 #pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) pend[i] = issue(first + i * kWarps, pg[i], i);
+      for (int i = 0; i < kStages - 1; ++i) pend[i] = issue(first + i, pg[i], i);
       next_page = pg[kStages - 1];
+    }
+
+    // Queries: a lane loads its D / 4 channels of rows g and g + 8 of each row tile, scales them
+    // by a power of two and rounds them to the f16 parts of its MMA operands.
+    const int n_tok = row_tokens(p, b);
+    const int start = p.start[b];
+    float rowf[MT][2];
+    int seen[MT][2], least = kNoEnd;
+    uint4 qreg[S::QREG ? S::QFRAGS : 1];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      uint32_t frag[S::PARTS][S::KSTEPS][4];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int gr = rg * S::ROWS + mt * 16 + half * 8 + g, j = gr / G;
+        const bool live = gr < R && j < n_tok;
+        float q[D / 4];
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) q[i] = 0.0f;
+        if (live) {
+          const uint4* src = reinterpret_cast<const uint4*>(
+              (const T*)p.q + ((int64_t)(b * p.window + j) * p.Hq + h * G + (gr - j * G)) * D +
+              t * (D / 4));
+          constexpr int N = Vec16<T>::N;
+#pragma unroll
+          for (int i = 0; i < D / 4 / N; ++i) Vec16<T>::unpack(src[i], q + i * N);
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) top = max(top, finite_abs_bits(q[i]));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        int e = top ? 13 + 127 - (int)(top >> 23) : 0;
+        e = e > 100 ? 100 : (e < -100 ? -100 : e);
+        const float up = pow2f(e);
+        rowf[mt][half] = p.scale * 1.44269504f * pow2f(-e);
+        // rows that are not live see everything: they force no mask, and are not stored
+        const int64_t n = (int64_t)start + j + 1;
+        seen[mt][half] = live && n < kNoEnd ? (int)n : kNoEnd;
+        least = min(least, seen[mt][half]);
+#pragma unroll
+        for (int k = 0; k < S::KSTEPS; ++k)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float a0 = q[4 * k + 2 * c] * up, a1 = q[4 * k + 2 * c + 1] * up;
+            frag[0][k][half + 2 * c] = f16x2(a0, a1);
+            if constexpr (S::PARTS == 2)
+              frag[1][k][half + 2 * c] = f16x2_rest(a0, a1, frag[0][k][half + 2 * c]);
+          }
+      }
+#pragma unroll
+      for (int part = 0; part < S::PARTS; ++part)
+#pragma unroll
+        for (int k = 0; k < S::KSTEPS; ++k) {
+          const uint4 a = make_uint4(frag[part][k][0], frag[part][k][1], frag[part][k][2],
+                                     frag[part][k][3]);
+          const int i = (mt * S::PARTS + part) * S::KSTEPS + k;
+          if constexpr (S::QREG) qreg[i] = a;
+          else qf[i * 32 + lane] = a;
+        }
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+
+    WarpState<T, D, MT> st;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int n = 0; n < S::NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st.o[mt][n][i] = 0.0f;
+      st.m[mt][0] = st.m[mt][1] = -INFINITY;
+      st.l[mt][0] = st.l[mt][1] = 0.0f;
     }
     int stage = 0;
 #pragma unroll 1
-    for (int sl = first; sl < last; sl += kWarps) {
+    for (int sl = first; sl < last; ++sl) {
       cp_wait<kStages - 2>();
       __syncwarp();
       const Pending cur = pend[0];
 #pragma unroll
       for (int i = 0; i < kStages - 2; ++i) pend[i] = pend[i + 1];
-      const int ahead = sl + (kStages - 1) * kWarps;
-      pend[kStages - 2] = issue(ahead, next_page, stage == 0 ? kStages - 1 : stage - 1);
-      next_page = page_of(ahead + kWarps);
+      pend[kStages - 2] =
+          issue(sl + kStages - 1, next_page, stage == 0 ? kStages - 1 : stage - 1);
+      next_page = page_of(sl + kStages);
       const uint8_t* kb = ring + stage * S::STAGE;
       const uint8_t* vb = kb + S::SLICE_BYTES;
       stage = stage == kStages - 1 ? 0 : stage + 1;
       if (!cur.present) continue;
       int left[MT][2];
       if (sl * kSlice + kSlice <= least) {
-        slice_step<T, D, MT, false>(st, kb, vb, qf, cur.ks, cur.vs, rowf, left, lane);
+        slice_step<T, D, MT, false>(st, kb, vb, qreg, qf, cur.ks, cur.vs, rowf, left, lane);
       } else {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int half = 0; half < 2; ++half) left[mt][half] = seen[mt][half] - sl * kSlice;
-        slice_step<T, D, MT, true>(st, kb, vb, qf, cur.ks, cur.vs, rowf, left, lane);
+        slice_step<T, D, MT, true>(st, kb, vb, qreg, qf, cur.ks, cur.vs, rowf, left, lane);
       }
     }
     cp_wait<0>();
+    __syncwarp();
 
-    // join the warps
+    const bool whole = first == 0 && last == n_slices;
+    const int slot = 2 * worker + (first == 0 ? 1 : 0);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -584,177 +582,170 @@ attn_kernel(const CacheAttnParams p, float* ws_o, float2* ws_ml, UnitDesc* desc)
         float l = st.l[mt][half];
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
-        if (t == 0) {
-          s_m[warp][mt * 16 + half * 8 + g] = st.m[mt][half];
-          s_l[warp][mt * 16 + half * 8 + g] = l;
+        const int r = mt * 16 + half * 8 + g, gr = rg * S::ROWS + r, j = gr / G;
+        if (gr >= R) continue;
+        float o[D / 4];  // channels t D/4 + n and t D/4 + D/8 + n
+#pragma unroll
+        for (int n = 0; n < S::NT; ++n) {
+          o[n] = st.o[mt][n][half * 2];
+          o[D / 8 + n] = st.o[mt][n][half * 2 + 1];
+        }
+        if (whole) {
+          const bool live = j < n_tok;
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          uint4* dst = reinterpret_cast<uint4*>(
+              (T*)p.o + ((int64_t)(b * p.window + j) * p.Hq + h * G + (gr - j * G)) * D +
+              t * (D / 4));
+          constexpr int N = Vec16<T>::N;
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i) o[i] = live ? o[i] * inv : 0.0f;
+#pragma unroll
+          for (int i = 0; i < D / 4 / N; ++i) dst[i] = Vec16<T>::pack(o + i * N);
+        } else {
+          const int64_t to = (int64_t)slot * piece_rows + r;
+          float4* dst = reinterpret_cast<float4*>(ws_o + to * D + t * (D / 4));
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+            dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          if (t == 0) ws_ml[to] = make_float2(st.m[mt][half], l);
         }
       }
-    __syncthreads();
-    float* acc = reinterpret_cast<float*>(smem);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float* o = acc + (warp * S::ROWS + mt * 16 + half * 8 + g) * S::ROW_F + t * S::LANE_F;
-#pragma unroll
-        for (int n = 0; n < S::NT; n += 4)  // channels t D/4 + n and t D/4 + D/8 + n
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            *reinterpret_cast<float4*>(o + u * (D / 8) + n) =
-                make_float4(st.o[mt][n][half * 2 + u], st.o[mt][n + 1][half * 2 + u],
-                            st.o[mt][n + 2][half * 2 + u], st.o[mt][n + 3][half * 2 + u]);
+    if (first == 0 && lane == 0) {
+      UnitDesc d = {worker, 0};
+      if (!whole) {  // its last piece is in the range that holds the unit's end
+        d.pieces = 1;
+        while (total * (worker + d.pieces) / workers < stop) ++d.pieces;
       }
-    __syncthreads();
-    const bool whole = blk0 == 0 && blk1 == nb;
-    const int slot = 2 * blockIdx.x + (blk0 == 0 ? 1 : 0);
-    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
-      const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-      float top = -INFINITY, l = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
-      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (s_m[w][r] == -INFINITY && s_l[w][r] == 0.0f) continue;  // saw no key
-        const float f = ptx::ex2_approx(s_m[w][r] - (top == -INFINITY ? 0.0f : top));
-        const float4 x = *reinterpret_cast<const float4*>(
-            acc + (w * S::ROWS + r) * S::ROW_F + (c / (D / 4)) * S::LANE_F + c % (D / 4));
-        l += f * s_l[w][r];
-        o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
-      }
-      if (whole) {
-        const int gr = rg * S::ROWS + r, j = gr / G;
-        const bool live = j < n_tok;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        T* dst = (T*)p.o + ((int64_t)(b * p.window + j) * p.Hq + h * G + (gr - j * G)) * D + c;
-        st_elem(dst, 0, live ? o.x * inv : 0.0f);
-        st_elem(dst, 1, live ? o.y * inv : 0.0f);
-        st_elem(dst, 2, live ? o.z * inv : 0.0f);
-        st_elem(dst, 3, live ? o.w * inv : 0.0f);
-      } else {
-        *reinterpret_cast<float4*>(ws_o + ((int64_t)slot * S::ROWS + r) * D + c) = o;
-        if (c == 0) ws_ml[(int64_t)slot * S::ROWS + r] = make_float2(top, l);
-      }
+      desc[(int64_t)b * U + unit] = d;
     }
-    if (!whole && blk0 == 0 && threadIdx.x == 0) {
-      // the pieces of this unit end in the CTA whose range holds its last block
-      int pieces = 1;
-      while (total * (cta + pieces) / ctas < stop) ++pieces;
-      UnitDesc d;
-      d.b = b; d.h = h; d.rg = rg; d.pieces = pieces;
-      desc[blockIdx.x] = d;
-    }
-    __syncthreads();
+  }
+
+  // rows without keys
+  for (int b = worker; b < p.batch; b += gridDim.x * kWarps) {
+    if (row_slices(p, b, false) > 0) continue;
+    T* o = (T*)p.o + (int64_t)b * p.window * p.Hq * D;
+    for (int i = lane; i < p.window * p.Hq * D; i += 32) st_elem(o, i, 0.0f);
+    for (int i = lane; i < U; i += 32) desc[(int64_t)b * U + i] = {0, 0};
   }
 }
 
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 16;
 
-// Joins the pieces of the unit that CTA c began and others went on with: c's second slot, then
-// the first slots of c + 1, c + 2, ... One CTA per (c, row): its warps sum every eighth piece, and
+// Joins the pieces of a unit that was cut: the second slot of the warp that began it, then the
+// first slots of the next ones. `per_row` warps of the CTA sum every per_row-th piece of a row, and
 // their sums are added in order.
 template <class T, int D, int MT>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-join_kernel(const CacheAttnParams p, const float* ws_o, const float2* ws_ml, const UnitDesc* desc) {
+join_kernel(const CacheAttnParams p, int piece_rows, int per_row, const float* ws_o,
+            const float2* ws_ml, const UnitDesc* desc) {
   using S = Shape<T, D, MT>;
   constexpr int N = D / 32;
-  __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps], s_top[kJoinWarps];
+  __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps];
+  const int G = p.Hq / p.Hkv, R = G * p.window;
+  const int nrg = (R + S::ROWS - 1) / S::ROWS, U = p.Hkv * nrg;
+  const int b = blockIdx.x / U, unit = blockIdx.x - b * U, h = unit / nrg, rg = unit - h * nrg;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % per_row;
+  const int rows = kJoinWarps / per_row;
+  const int r = blockIdx.y * rows + warp / per_row, gr = rg * S::ROWS + r;
+  const bool mine = r < S::ROWS && gr < R;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const UnitDesc d = desc[blockIdx.x];
-  const int G = p.Hq / p.Hkv, R = G * p.window;
-  const int r = blockIdx.y, gr = d.rg * S::ROWS + r;
-  if (d.pieces == 0 || gr >= R) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (d.pieces == 0) return;
   auto slot_row = [&](int i) {
-    return (int64_t)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * S::ROWS + r;
+    return (int64_t)(i == 0 ? 2 * d.worker + 1 : 2 * (d.worker + i)) * piece_rows + r;
   };
-  float top = -INFINITY;
-  for (int i = threadIdx.x; i < d.pieces; i += kJoinWarps * 32) top = fmaxf(top, ws_ml[slot_row(i)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) s_top[warp] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_top[w]);
-  const float mu = top == -INFINITY ? 0.0f : top;
   float o[N], l = 0.0f;
 #pragma unroll
   for (int c = 0; c < N; ++c) o[c] = 0.0f;
-#pragma unroll 4
-  for (int i = warp; i < d.pieces; i += kJoinWarps) {
-    const int64_t at = slot_row(i);
-    const float2 ml = ws_ml[at];
-    float x[N];
-    if constexpr (N == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(ws_o + at * D + lane * N);
-      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(ws_o + at * D + lane * N);
-      x[0] = v.x; x[1] = v.y;
-    }
-    // a piece in which the row saw no key has m = -inf and only zeros
-    const float f = ptx::ex2_approx(ml.x - mu);
-    l = fmaf(f, ml.y, l);
+  if (mine) {
+    float top = -INFINITY;
+    for (int i = lane; i < d.pieces; i += 32) top = fmaxf(top, ws_ml[slot_row(i)].x);
 #pragma unroll
-    for (int c = 0; c < N; ++c) o[c] = fmaf(f, x[c], o[c]);
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float mu = top == -INFINITY ? 0.0f : top;
+#pragma unroll 8
+    for (int i = sub; i < d.pieces; i += per_row) {
+      const int64_t at = slot_row(i);
+      const float2 ml = ws_ml[at];
+      float x[N];
+      if constexpr (N == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(ws_o + at * D + lane * N);
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(ws_o + at * D + lane * N);
+        x[0] = v.x; x[1] = v.y;
+      }
+      // a piece in which the row saw no key has m = -inf and only zeros
+      const float f = ptx::ex2_approx(ml.x - mu);
+      l = fmaf(f, ml.y, l);
+#pragma unroll
+      for (int c = 0; c < N; ++c) o[c] = fmaf(f, x[c], o[c]);
+    }
   }
 #pragma unroll
   for (int c = 0; c < N; ++c) s_o[warp][lane * N + c] = o[c];
   if (lane == 0) s_l[warp] = l;
   __syncthreads();
-  if (threadIdx.x >= D) return;
-  float sum = 0.0f;
-  l = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    sum += s_o[w][threadIdx.x];
-    l += s_l[w];
+  for (int i = threadIdx.x; i < rows * D; i += kJoinWarps * 32) {
+    const int rr = i / D, c = i - rr * D;
+    const int gq = rg * S::ROWS + blockIdx.y * rows + rr, j = gq / G;
+    if (blockIdx.y * rows + rr >= S::ROWS || gq >= R) continue;
+    float sum = 0.0f, ls = 0.0f;
+    for (int w = 0; w < per_row; ++w) {
+      sum += s_o[rr * per_row + w][c];
+      ls += s_l[rr * per_row + w];
+    }
+    const bool live = j < row_tokens(p, b) && ls != 0.0f;
+    T* dst = (T*)p.o + ((int64_t)(b * p.window + j) * p.Hq + h * G + (gq - j * G)) * D;
+    st_elem(dst, c, live ? sum / ls : 0.0f);
   }
-  const int j = gr / G;
-  const bool live = j < row_tokens(p, d.b);
-  T* dst = (T*)p.o + ((int64_t)(d.b * p.window + j) * p.Hq + d.h * G + (gr - j * G)) * D;
-  st_elem(dst, threadIdx.x, live && l != 0.0f ? sum / l : 0.0f);
 }
 
-size_t piece_bytes(int rows, int d) { return (size_t)2 * kMaxCtas * rows * d * sizeof(float); }
-size_t ml_bytes(int rows) { return (size_t)2 * kMaxCtas * rows * sizeof(float2); }
+// Rows of a unit: two MMA row tiles when the group and window fill them (bf16), else one.
+int row_tiles(kda_dtype dt, int rows) { return dt == KDA_BF16 && rows > 16 ? 2 : 1; }
+
+// Workspace: the pieces' sums, their (m, l), then a descriptor per unit (of 16 rows at least).
+size_t piece_bytes(int rows, int d) { return (size_t)2 * kMaxWorkers * rows * d * sizeof(float); }
+size_t ml_bytes(int rows) { return (size_t)2 * kMaxWorkers * rows * sizeof(float2); }
 
 template <class T, int D, int MT>
 kda_status launch_t(const CacheAttnParams& p, cudaStream_t s) {
   using S = Shape<T, D, MT>;
-  static int ctas_of[64] = {};  // resident CTAs of each device, found once
+  static int sms_of[64] = {};  // SMs of each device, found once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || dev < 0 || dev >= 64)
     return set_error(KDA_ERR_CUDA, "kda_cache_attention: no current device");
-  if (ctas_of[dev] == 0) {
-    int sms = 0, per = 0;
+  if (sms_of[dev] == 0) {
+    int sms = 0;
     e = cudaFuncSetAttribute(attn_kernel<T, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              S::SMEM);
-    if (e == cudaSuccess)
-      e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, attn_kernel<T, D, MT>, S::THREADS,
-                                                        S::SMEM);
-    if (e != cudaSuccess || per < 1)
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess)
       return set_error(KDA_ERR_CUDA, std::string("kda_cache_attention: ") + cudaGetErrorString(e));
-    ctas_of[dev] = sms * per < kMaxCtas ? sms * per : kMaxCtas;
+    sms_of[dev] = sms * kWarps < kMaxWorkers ? sms : kMaxWorkers / kWarps;
   }
-  const int G = p.Hq / p.Hkv, nrg = (G * p.window + S::ROWS - 1) / S::ROWS;
+  const int G = p.Hq / p.Hkv, R = G * p.window, nrg = (R + S::ROWS - 1) / S::ROWS;
+  const int rows = R < S::ROWS ? R : S::ROWS;
   // no more CTAs than the page table allows ranges of kMinCost
+  const int64_t units = (int64_t)p.batch * p.Hkv * nrg;
   const int64_t most =
-      ((int64_t)p.batch * p.Hkv * nrg * (p.max_pages + kUnitCost) + kMinCost - 1) / kMinCost;
-  const int ctas = most < ctas_of[dev] ? (int)most : ctas_of[dev];
+      (units * ((int64_t)p.max_pages * (kPage / kSlice) + kUnitCost) + kMinCost - 1) / kMinCost;
+  const int ctas = most < sms_of[dev] ? (int)most : sms_of[dev];
   uint8_t* ws = (uint8_t*)p.ws;
   float* ws_o = (float*)ws;
-  float2* ws_ml = (float2*)(ws + piece_bytes(S::ROWS, D));
-  UnitDesc* desc = (UnitDesc*)(ws + piece_bytes(S::ROWS, D) + ml_bytes(S::ROWS));
-  attn_kernel<T, D, MT><<<ctas, S::THREADS, S::SMEM, s>>>(p, ws_o, ws_ml, desc);
+  float2* ws_ml = (float2*)(ws + piece_bytes(rows, D));
+  UnitDesc* desc = (UnitDesc*)(ws + piece_bytes(rows, D) + ml_bytes(rows));
+  attn_kernel<T, D, MT><<<ctas, kThreads, S::SMEM, s>>>(p, rows, ws_o, ws_ml, desc);
   kda_status st = check_launch("kda_cache_attention");
   if (st != KDA_OK) return st;
+  // few units have many pieces each: a CTA per row; many units: a CTA for as many rows as it has
+  // warps
+  int per_row = kJoinWarps;
+  if (units * rows > 4 * sms_of[dev])
+    while (per_row > 1 && kJoinWarps / per_row < rows) per_row >>= 1;
   cudaLaunchConfig_t cfg = {};
-  const int rows = G * p.window < S::ROWS ? G * p.window : S::ROWS;
-  cfg.gridDim = dim3(ctas, rows);
+  cfg.gridDim = dim3((unsigned)units, (unsigned)((rows * per_row + kJoinWarps - 1) / kJoinWarps));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -762,20 +753,18 @@ kda_status launch_t(const CacheAttnParams& p, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, join_kernel<T, D, MT>, p, (const float*)ws_o, (const float2*)ws_ml,
-                     (const UnitDesc*)desc);
+  cudaLaunchKernelEx(&cfg, join_kernel<T, D, MT>, p, rows, per_row, (const float*)ws_o,
+                     (const float2*)ws_ml, (const UnitDesc*)desc);
   count_launches(2);
   return check_launch("kda_cache_attention");
 }
 
-// Rows of a unit: two MMA row tiles when the group and window fill them (bf16), else one.
-int row_tiles(kda_dtype dt, int rows) { return dt == KDA_BF16 && rows > 16 ? 2 : 1; }
-
 }  // namespace
 
-size_t cache_attn_workspace_bytes(int, int window, int Hq, int Hkv, int d) {
-  const int rows = Hq / Hkv * window > 16 ? 32 : 16;
-  return piece_bytes(rows, d) + ml_bytes(rows) + (sizeof(UnitDesc) * kMaxCtas + 255) / 256 * 256;
+size_t cache_attn_workspace_bytes(int batch, int window, int Hq, int Hkv, int d) {
+  const int R = Hq / Hkv * window, rows = R < 32 ? R : 32;
+  const size_t units = (size_t)batch * Hkv * ((R + 15) / 16);
+  return piece_bytes(rows, d) + ml_bytes(rows) + (sizeof(UnitDesc) * units + 255) / 256 * 256;
 }
 
 kda_status launch_cache_attn(const CacheAttnParams& p, kda_dtype dt, int d, cudaStream_t s) {
