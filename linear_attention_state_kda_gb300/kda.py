@@ -136,7 +136,8 @@ def _dt(t):
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the raw handle of torch.cuda.current_stream(), without building the Stream object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -440,34 +441,62 @@ def short_conv(x, weight, cu_seqlens=None, silu=False, read_slots=None, write_sl
     return out
 
 
-def _heads(t, name):
+# The serving operators are called once or more per layer and token, so their checks are written
+# for few attribute reads: a call's host time is what bounds it at small sizes.
+
+_F32, _I32, _BF16 = torch.float32, torch.int32, torch.bfloat16
+_DTYPES = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
+
+
+def _code(dtype):
+    try:
+        return _DTYPES[dtype]
+    except KeyError:
+        raise TypeError(f"unsupported dtype {dtype}") from None
+
+
+def _vec(t, dtype, n, name):
+    """Pointer of a contiguous tensor of n entries of `dtype` (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and hold {n} entries")
+    return t.data_ptr()
+
+
+def _heads(t, shape, dtype, name):
     """Token stride of [tokens, H, d] rows whose heads are contiguous (any token stride)."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError(f"{name} must be [tokens, heads, d] with contiguous heads")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
-def _same(dtype, *ts):
-    for t in ts:
-        if t is not None and t.dtype != dtype:
-            raise TypeError(f"expected {dtype} tensors")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    st = t.stride()
+    if t.shape != shape or st[2] != 1 or (st[1] != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name} must be [tokens, heads, d] = {tuple(shape)} with contiguous heads")
+    return st[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def _cache(k_cache, k_scale, v_cache, v_scale, page_table, rows):
     """Checks a cache's four tensors and its page table; returns (n_pages, Hkv, d, max_pages)."""
-    _contig(k_cache, k_scale, v_cache, v_scale, page_table)
-    _int32(page_table)
-    _same(torch.float32, k_scale, v_scale)
-    if k_cache.dtype not in (torch.float8_e4m3fn, torch.uint8) or v_cache.dtype != k_cache.dtype:
+    shape = k_cache.shape
+    dtype = k_cache.dtype
+    if (dtype is not torch.float8_e4m3fn and dtype is not torch.uint8) or \
+            v_cache.dtype is not dtype:
         raise TypeError("the caches must be float8_e4m3fn (or uint8 codes)")
-    n_pages, H, page, d = k_cache.shape
-    if page != PAGE or v_cache.shape != k_cache.shape:
+    if k_scale.dtype is not _F32 or v_scale.dtype is not _F32 or page_table.dtype is not _I32:
+        raise TypeError("the scales must be float32 and page_table int32")
+    n_pages, H, page, d = shape
+    if page != PAGE or v_cache.shape != shape:
         raise ValueError("the caches must both be [n_pages, Hkv, 64, d]")
     if k_scale.shape != (n_pages, H) or v_scale.shape != (n_pages, H):
         raise ValueError("the scales must be [n_pages, Hkv]")
-    if page_table.dim() != 2 or page_table.shape[0] != rows:
+    n, max_pages = page_table.shape
+    if n != rows:
         raise ValueError("page_table must be [rows, max_pages], a row for each entry of start")
-    return n_pages, H, d, page_table.shape[1]
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous() and
+            v_scale.is_contiguous() and page_table.is_contiguous()):
+        raise ValueError("the cache's tensors and page_table must be contiguous")
+    return n_pages, H, d, max_pages
 
 
 def head_norm_rope(q, k, q_weight=None, k_weight=None, eps=1e-6, l2=False, cos_sin=None,
@@ -477,33 +506,46 @@ def head_norm_rope(q, k, q_weight=None, k_weight=None, eps=1e-6, l2=False, cos_s
     with per-channel weights, then the rotation by row `positions[t]` of cos_sin [n_pos, rot_dim]
     (none when cos_sin is None). q and k may be views of a fused projection's rows; either may be
     None. q_out = q (k_out = k) works in place. Returns (q_out, k_out)."""
-    x = q if q is not None else k
+    x = k if q is None else q
     T, _, d = x.shape
-    _contig(q_weight, k_weight, cos_sin, positions)
-    _int32(positions)
-    _same(torch.float32, q_weight, k_weight, cos_sin)
-    _same(x.dtype, q, k, q_out, k_out)
-    for t, w, name in ((q, q_weight, "q"), (k, k_weight, "k")):
-        if t is not None and (t.shape[0] != T or t.shape[2] != d):
+    dtype = x.dtype
+    code = _code(dtype)
+    qp = kp = qop = kop = cp = None
+    Hq = Hk = qs = ks = qos = kos = n_pos = rot = 0
+    if q is not None:
+        shape = q.shape
+        Hq = shape[1]
+        qs = _heads(q, shape, dtype, "q")
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=dtype, device=q.device)
+            qos = Hq * d
+        else:
+            qos = _heads(q_out, shape, dtype, "q_out")
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    if k is not None:
+        shape = k.shape
+        Hk = shape[1]
+        ks = _heads(k, shape, dtype, "k")
+        if shape[0] != T or shape[2] != d:
             raise ValueError("q and k must have the same tokens and head size")
-        if w is not None and w.numel() != d:
-            raise ValueError(f"{name}_weight must hold d values")
-    if positions is not None and positions.numel() != T:
-        raise ValueError("positions must hold one entry per token")
-    if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    if (q is not None and q_out.shape != q.shape) or (k is not None and k_out.shape != k.shape):
-        raise ValueError("outputs must have the shapes of q and k")
-    Hq, qs, qos = (0, 0, 0) if q is None else (q.shape[1], _heads(q, "q"), _heads(q_out, "q_out"))
-    Hk, ks, kos = (0, 0, 0) if k is None else (k.shape[1], _heads(k, "k"), _heads(k_out, "k_out"))
-    n_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
-    flags = (NORM_L2 if l2 else 0) | (ROPE_INTERLEAVED if interleaved else 0)
-    _check(lib().kda_head_norm_rope(_dt(x), T, Hq, Hk, d, _ptr(q), qs, _ptr(k), ks,
-                                    _ptr(q_weight), _ptr(k_weight), float(eps), flags,
-                                    _ptr(cos_sin), n_pos, rot, _ptr(positions), _ptr(q_out), qos,
-                                    _ptr(k_out), kos, _ptr(status), _stream(stream)))
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dtype, device=k.device)
+            kos = Hk * d
+        else:
+            kos = _heads(k_out, shape, dtype, "k_out")
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    if cos_sin is not None:
+        n_pos, rot = cos_sin.shape
+        cp = _vec(cos_sin, _F32, n_pos * rot, "cos_sin")
+    st = lib().kda_head_norm_rope(code, T, Hq, Hk, d, qp, qs, kp, ks,
+                                  _vec(q_weight, _F32, d, "q_weight"),
+                                  _vec(k_weight, _F32, d, "k_weight"), eps,
+                                  (NORM_L2 if l2 else 0) |
+                                  (ROPE_INTERLEAVED if interleaved else 0), cp, n_pos, rot,
+                                  _vec(positions, _I32, T, "positions"), qop, qos, kop, kos,
+                                  _ptr(status), _stream(stream))
+    if st:
+        _check(st)
     return q_out, k_out
 
 
@@ -512,44 +554,45 @@ def cache_write(k, v, start, page_table, k_cache, k_scale, v_cache, v_scale, cu_
     """kda_cache_write: quantises k and v [T, Hkv, d] (views of a fused projection's rows are fine)
     into the paged cache [n_pages, Hkv, 64, d] with scales [n_pages, Hkv], token i of sequence s at
     position start[s] + i. The caches and scales are updated in place."""
-    _contig(start, cu_seqlens, lens)
-    _int32(start, cu_seqlens, lens)
-    _same(k.dtype, v)
     n = start.numel()
     n_pages, H, d, max_pages = _cache(k_cache, k_scale, v_cache, v_scale, page_table, n)
-    if k.shape != v.shape or k.shape[1:] != (H, d):
+    shape, dtype = k.shape, k.dtype
+    if shape[1:] != (H, d):
         raise ValueError("k and v must be [tokens, Hkv, d] of the cache")
-    if (cu_seqlens is not None and cu_seqlens.numel() != n + 1) or \
-            (lens is not None and lens.numel() != n):
-        raise ValueError("cu_seqlens must hold n + 1 and lens n entries")
-    _check(lib().kda_cache_write(_dt(k), n, k.shape[0], _ptr(cu_seqlens), _ptr(start), _ptr(lens),
-                                 H, d, _ptr(k), _heads(k, "k"), _ptr(v), _heads(v, "v"),
-                                 _ptr(page_table), max_pages, _ptr(k_cache), _ptr(k_scale),
-                                 _ptr(v_cache), _ptr(v_scale), n_pages, _ptr(status),
-                                 _stream(stream)))
+    st = lib().kda_cache_write(_code(dtype), n, shape[0],
+                               _vec(cu_seqlens, _I32, n + 1, "cu_seqlens"),
+                               _vec(start, _I32, n, "start"), _vec(lens, _I32, n, "lens"), H, d,
+                               k.data_ptr(), _heads(k, shape, dtype, "k"), v.data_ptr(),
+                               _heads(v, shape, dtype, "v"), page_table.data_ptr(), max_pages,
+                               k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(),
+                               v_scale.data_ptr(), n_pages, _ptr(status), _stream(stream))
+    if st:
+        _check(st)
 
 
 def cache_read(start, page_table, k_cache, k_scale, v_cache, v_scale, total_tokens,
                cu_seqlens=None, dtype=torch.bfloat16, k=None, v=None, status=None, stream=None):
     """kda_cache_read: cached keys and values of positions start[s] .. of each sequence, packed by
     cu_seqlens (total_tokens rows in all). Returns (k, v), [total_tokens, Hkv, d] of `dtype`."""
-    _contig(start, cu_seqlens, k, v)
-    _int32(start, cu_seqlens)
     n = start.numel()
     n_pages, H, d, max_pages = _cache(k_cache, k_scale, v_cache, v_scale, page_table, n)
-    if cu_seqlens is not None and cu_seqlens.numel() != n + 1:
-        raise ValueError("cu_seqlens must hold n + 1 entries")
+    code = _code(dtype)
+    shape = (total_tokens, H, d)
     if k is None:
-        k = torch.empty(total_tokens, H, d, dtype=dtype, device=k_cache.device)
+        k = torch.empty(shape, dtype=dtype, device=k_cache.device)
     if v is None:
-        v = torch.empty(total_tokens, H, d, dtype=dtype, device=k_cache.device)
-    if k.shape != (total_tokens, H, d) or v.shape != k.shape:
+        v = torch.empty(shape, dtype=dtype, device=k_cache.device)
+    if k.shape != shape or v.shape != shape:
         raise ValueError("k and v must be [total_tokens, Hkv, d]")
-    _same(k.dtype, v)
-    _check(lib().kda_cache_read(_dt(k), n, int(total_tokens), _ptr(cu_seqlens), _ptr(start), H, d,
-                                _ptr(page_table), max_pages, _ptr(k_cache), _ptr(k_scale),
-                                _ptr(v_cache), _ptr(v_scale), n_pages, _ptr(k), _ptr(v),
-                                _ptr(status), _stream(stream)))
+    size = total_tokens * H * d
+    st = lib().kda_cache_read(code, n, total_tokens, _vec(cu_seqlens, _I32, n + 1, "cu_seqlens"),
+                              _vec(start, _I32, n, "start"), H, d, page_table.data_ptr(),
+                              max_pages, k_cache.data_ptr(), k_scale.data_ptr(),
+                              v_cache.data_ptr(), v_scale.data_ptr(), n_pages,
+                              _vec(k, dtype, size, "k"), _vec(v, dtype, size, "v"), _ptr(status),
+                              _stream(stream))
+    if st:
+        _check(st)
     return k, v
 
 
@@ -561,41 +604,48 @@ def cache_attention_workspace(batch, window, Hq, Hkv, d):
 def cache_attention(q, start, page_table, k_cache, k_scale, v_cache, v_scale, scale=1.0, lens=None,
                     o=None, workspace=None, status=None, stream=None):
     """kda_cache_attention: q [batch*window, Hq, d] or [batch, window, Hq, d], the window's token j
-    of row b at position start[b] + j, seeing the cached positions 0 .. start[b] + j. Returns o,
-    shaped like q."""
-    _contig(q, start, lens, o)
-    _int32(start, lens)
+    of row b at position start[b] + j, seeing the cached positions 0 .. start[b] + j. `workspace`
+    (uint8 device tensor of at least cache_attention_workspace(...) bytes) is allocated here when
+    not given. Returns o, shaped like q."""
     B = start.numel()
     n_pages, Hkv, d, max_pages = _cache(k_cache, k_scale, v_cache, v_scale, page_table, B)
-    Hq = q.shape[-2]
-    if q.shape[-1] != d:
+    L = lib()
+    shape, dtype, size = q.shape, q.dtype, q.numel()
+    Hq = shape[-2]
+    if shape[-1] != d:
         raise ValueError("q and the cache differ in head size")
-    W = q.numel() // (B * Hq * d) if B else 0
-    if q.numel() != B * W * Hq * d:
+    W = size // (B * Hq * d) if B else 0
+    if size != B * W * Hq * d:
         raise ValueError("q must hold batch x window tokens")
-    if lens is not None and lens.numel() != B:
-        raise ValueError("lens must hold one entry per row")
     if o is None:
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _same(q.dtype, o)
-    if o.numel() != q.numel():
-        raise ValueError("o must have the shape of q")
+        o = torch.empty(shape, dtype=dtype, device=q.device)
     if workspace is None:
-        need = cache_attention_workspace(B, W, Hq, Hkv, d)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().kda_cache_attention(_dt(q), B, W, Hq, Hkv, d, float(scale), _ptr(q), _ptr(start),
-                                     _ptr(lens), _ptr(page_table), max_pages, _ptr(k_cache),
-                                     _ptr(k_scale), _ptr(v_cache), _ptr(v_scale), n_pages, _ptr(o),
-                                     _ptr(workspace), ws_bytes, _ptr(status), _stream(stream)))
+        need = ws_bytes = L.kda_cache_attention_workspace(B, W, Hq, Hkv, d)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    st = L.kda_cache_attention(_code(dtype), B, W, Hq, Hkv, d, scale,
+                               _vec(q, dtype, size, "q"), _vec(start, _I32, B, "start"),
+                               _vec(lens, _I32, B, "lens"), page_table.data_ptr(), max_pages,
+                               k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(),
+                               v_scale.data_ptr(), n_pages, _vec(o, dtype, size, "o"),
+                               _ptr(workspace), ws_bytes, _ptr(status), _stream(stream))
+    if st:
+        _check(st)
     return o
 
 
-def _rows3(t, name):
+def _rows3(t, shape, dtype, name):
     """Row stride of [batch, places, vocab] rows at one stride, entries contiguous."""
-    b, n, v = t.shape
-    s = t.stride(1) if n > 1 else (t.stride(0) if b > 1 else v)
-    if (v > 1 and t.stride(2) != 1) or (b > 1 and t.stride(0) != n * s):
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}")
+    b, n, v = shape
+    s0, s1, s2 = t.stride()
+    s = s1 if n > 1 else (s0 if b > 1 else v)
+    if (s2 != 1 and v > 1) or (b > 1 and s0 != n * s):
         raise ValueError(f"{name} must have contiguous entries and evenly spaced rows")
     return s
 
@@ -608,36 +658,34 @@ def draft_verify(target_probs, draft_tokens, u_accept, u_sample, draft_probs=Non
     [batch, window, vocab] or None for drafts that were not sampled). Returns (n_accepted [batch],
     tokens [batch, window+1] padded with -1, resume_slots [batch]: write_slots[b, n_accepted[b]],
     the slot to resume the recurrent state from, or None without write_slots)."""
-    _contig(draft_tokens, u_accept, u_sample, lens, write_slots, tokens, n_accepted, resume_slots)
-    _int32(draft_tokens, lens, write_slots, tokens, n_accepted, resume_slots)
-    _same(torch.float32, u_accept, u_sample)
-    _same(target_probs.dtype, draft_probs)
-    B, W1, V = target_probs.shape
+    shape, dtype = target_probs.shape, target_probs.dtype
+    code = _code(dtype)
+    B, W1, V = shape
     W = W1 - 1
-    if draft_tokens.shape != (B, W) or u_accept.shape != (B, W) or u_sample.shape != (B,):
-        raise ValueError("draft_tokens and u_accept must be [batch, window], u_sample [batch]")
-    if draft_probs is not None and draft_probs.shape != (B, W, V):
-        raise ValueError("draft_probs must be [batch, window, vocab]")
-    if lens is not None and lens.numel() != B:
-        raise ValueError("lens must hold one entry per row")
-    if write_slots is not None and write_slots.shape != (B, W1):
-        raise ValueError("write_slots must be [batch, window + 1]")
+    if draft_tokens.shape != (B, W) or u_accept.shape != (B, W):
+        raise ValueError("draft_tokens and u_accept must be [batch, window]")
     dev = target_probs.device
     if tokens is None:
-        tokens = torch.empty(B, W1, dtype=torch.int32, device=dev)
+        tokens = torch.empty((B, W1), dtype=_I32, device=dev)
     if n_accepted is None:
-        n_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        n_accepted = torch.empty((B,), dtype=_I32, device=dev)
     if resume_slots is None and write_slots is not None:
-        resume_slots = torch.empty(B, dtype=torch.int32, device=dev)
-    if tokens.shape != (B, W1) or n_accepted.numel() != B or \
-            (resume_slots is not None and resume_slots.numel() != B):
-        raise ValueError("outputs must be tokens [batch, window + 1], n_accepted and resume_slots "
-                         "[batch]")
-    ds = 0 if draft_probs is None or W == 0 else _rows3(draft_probs, "draft_probs")
-    _check(lib().kda_draft_verify(_dt(target_probs), B, W, V, _ptr(target_probs),
-                                  _rows3(target_probs, "target_probs"),
-                                  _ptr(draft_probs) if ds else None, ds, _ptr(draft_tokens),
-                                  _ptr(lens), _ptr(u_accept), _ptr(u_sample), _ptr(write_slots),
-                                  _ptr(tokens), _ptr(n_accepted), _ptr(resume_slots), _ptr(status),
-                                  _stream(stream)))
+        resume_slots = torch.empty((B,), dtype=_I32, device=dev)
+    ds, dp = 0, None
+    if draft_probs is not None and W:
+        ds = _rows3(draft_probs, (B, W, V), dtype, "draft_probs")
+        dp = draft_probs.data_ptr()
+    st = lib().kda_draft_verify(code, B, W, V, target_probs.data_ptr(),
+                                _rows3(target_probs, shape, dtype, "target_probs"), dp, ds,
+                                _vec(draft_tokens, _I32, B * W, "draft_tokens"),
+                                _vec(lens, _I32, B, "lens"),
+                                _vec(u_accept, _F32, B * W, "u_accept"),
+                                _vec(u_sample, _F32, B, "u_sample"),
+                                _vec(write_slots, _I32, B * W1, "write_slots"),
+                                _vec(tokens, _I32, B * W1, "tokens"),
+                                _vec(n_accepted, _I32, B, "n_accepted"),
+                                _vec(resume_slots, _I32, B, "resume_slots"), _ptr(status),
+                                _stream(stream))
+    if st:
+        _check(st)
     return n_accepted, tokens, resume_slots
