@@ -20,6 +20,21 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kUnroll = 4;  // row loads in flight per lane
 
+// N floats from a 4 N-byte aligned address.
+template <int N>
+__device__ __forceinline__ void load_floats(const float* p, float* x) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
+      x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+    }
+  } else {
+    const float2 v = __ldg(reinterpret_cast<const float2*>(p));
+    x[0] = v.x; x[1] = v.y;
+  }
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(kWarps * 32)
 head_norm_kernel(const HeadNormParams p, int groups) {
@@ -44,7 +59,7 @@ head_norm_kernel(const HeadNormParams p, int groups) {
       const bool isq = h < p.q.H;
       const HeadNormSide& s = isq ? p.q : p.k;
       const T* x = (const T*)s.x + tok * s.x_stride + (int64_t)(isq ? h : h - p.q.H) * D + e0;
-      raw[u] = *reinterpret_cast<const uint4*>(x);
+      raw[u] = __ldcs(reinterpret_cast<const uint4*>(x));
     }
   }
 
@@ -62,23 +77,29 @@ head_norm_kernel(const HeadNormParams p, int groups) {
     if (rotate) {
       const float* row = p.cos_sin + pos * p.rot;
       if (inter) {
+        float c2[N / 2], s2[N / 2];
+        load_floats<N / 2>(row + e0 / 2, c2);
+        load_floats<N / 2>(row + half + e0 / 2, s2);
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-          cs[2 * i] = cs[2 * i + 1] = row[e0 / 2 + i];
-          sn[2 * i + 1] = row[half + e0 / 2 + i];
-          sn[2 * i] = -sn[2 * i + 1];
+          cs[2 * i] = cs[2 * i + 1] = c2[i];
+          sn[2 * i + 1] = s2[i];
+          sn[2 * i] = -s2[i];
         }
       } else {
         const int i0 = e0 < half ? e0 : e0 - half;
-        const float sign = e0 < half ? -1.0f : 1.0f;
+        load_floats<N>(row + i0, cs);
+        load_floats<N>(row + half + i0, sn);
+        if (e0 < half) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          cs[i] = row[i0 + i];
-          sn[i] = sign * row[half + i0 + i];
+          for (int i = 0; i < N; ++i) sn[i] = -sn[i];
         }
       }
     }
   }
+  // the weights of the side that the lane's heads are on (loaded again where k follows q)
+  float wt[N];
+  const float* have = nullptr;
   // lane that holds the partner chunk of a half-split pair (itself where nothing is rotated)
   const int shift = half / N;
   const int partner = (inter || !rotate) ? lane : (e0 < half ? lane + shift : lane - shift);
@@ -98,9 +119,13 @@ head_norm_kernel(const HeadNormParams p, int groups) {
     const HeadNormSide& s = isq ? p.q : p.k;
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] *= r;
-    if (s.w && h < H) {
+    if (s.w) {
+      if (s.w != have) {
+        load_floats<N>(s.w + e0, wt);
+        have = s.w;
+      }
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] *= s.w[e0 + i];
+      for (int i = 0; i < N; ++i) x[i] *= wt[i];
     }
     float y[N];
     if (inter) {
@@ -116,7 +141,7 @@ head_norm_kernel(const HeadNormParams p, int groups) {
     }
     if (h < H) {
       T* out = (T*)s.out + tok * s.out_stride + (int64_t)(isq ? h : h - p.q.H) * D + e0;
-      *reinterpret_cast<uint4*>(out) = Vec16<T>::pack(x);
+      __stcs(reinterpret_cast<uint4*>(out), Vec16<T>::pack(x));
     }
   }
 }

@@ -224,6 +224,21 @@ __device__ __forceinline__ bool wait_flag(const uint32_t* flag,
   }
 }
 
+// ---------------------------------------------------------------- clusters
+// Barrier of all threads of the cluster, ordering their shared-memory accesses.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The word at `p` (this CTA's shared memory) in the same place of the cluster's CTA `rank`.
+__device__ __forceinline__ uint64_t ld_cluster_u64(const uint64_t* p, uint32_t rank) {
+  uint32_t a;
+  uint64_t v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
+
 // ---------------------------------------------------------------- tcgen05
 // Allocates `ncols` TMEM columns (power of two >= 32); the base address lands in *dst.
 // Whole-warp instruction.
