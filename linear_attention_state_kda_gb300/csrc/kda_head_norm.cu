@@ -17,7 +17,7 @@
 namespace kda {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kUnroll = 4;  // row loads in flight per lane
 
 // N floats from a 4 N-byte aligned address.
@@ -36,8 +36,8 @@ __device__ __forceinline__ void load_floats(const float* p, float* x) {
 }
 
 template <class T, int D>
-__global__ void __launch_bounds__(kWarps * 32)
-head_norm_kernel(const HeadNormParams p, int groups) {
+__global__ void __launch_bounds__(kWarps * 32, 8)
+head_norm_kernel(const HeadNormParams p, int q_groups, int groups) {
   constexpr int N = Vec16<T>::N;
   constexpr int LPR = D / N;        // lanes per row
   constexpr int RPW = 32 / LPR;     // rows a warp loads at once
@@ -46,68 +46,74 @@ head_norm_kernel(const HeadNormParams p, int groups) {
   const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
   const int64_t tok = item / groups;
   if (tok >= p.tokens) return;
-  const int h0 = (int)(item - tok * groups) * HEADS + sub;
-  const int H = p.q.H + p.k.H;
+  const int group = (int)(item - tok * groups);
+  const HeadNormSide& s = group < q_groups ? p.q : p.k;
+  const int h0 = (group < q_groups ? group : group - q_groups) * HEADS + sub;
   const int e0 = l * N;  // first channel of this lane
+  int64_t pos = tok;
+  if (p.rot && p.positions) pos = __ldg(p.positions + tok);
 
+  const T* xr = (const T*)s.x + tok * s.x_stride + h0 * D + e0;
   uint4 raw[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const int h = h0 + u * RPW;
     raw[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (h < H) {
-      const bool isq = h < p.q.H;
-      const HeadNormSide& s = isq ? p.q : p.k;
-      const T* x = (const T*)s.x + tok * s.x_stride + (int64_t)(isq ? h : h - p.q.H) * D + e0;
-      raw[u] = __ldcs(reinterpret_cast<const uint4*>(x));
-    }
+    if (h0 + u * RPW < s.H) raw[u] = __ldcs(reinterpret_cast<const uint4*>(xr + u * RPW * D));
   }
 
-  // this lane's cosines and sines
+  // y_i = r (x_i a_i + x_partner b_i): weights and rotation in two factors per channel, the same
+  // for all heads. A channel that is not rotated is its own partner, with b = 0.
   const int half = p.rot / 2;
   const bool inter = (p.flags & KDA_ROPE_INTERLEAVED) != 0;
-  float cs[N], sn[N];
   bool rotate = e0 < p.rot;
-  if (p.rot) {
-    const int64_t pos = p.positions ? (int64_t)p.positions[tok] : tok;
-    if (pos < 0 || pos >= p.n_pos) {
-      if (lane == 0 && h0 == 0 && p.status) atomicOr(p.status, KDA_STATUS_BAD_POSITION);
-      rotate = false;
-    }
-    if (rotate) {
-      const float* row = p.cos_sin + pos * p.rot;
-      if (inter) {
-        float c2[N / 2], s2[N / 2];
-        load_floats<N / 2>(row + e0 / 2, c2);
-        load_floats<N / 2>(row + half + e0 / 2, s2);
+  if (rotate && (pos < 0 || pos >= p.n_pos)) {
+    if (group == 0 && lane == 0 && p.status) atomicOr(p.status, KDA_STATUS_BAD_POSITION);
+    rotate = false;
+  }
+  float a[N], b[N];
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-          cs[2 * i] = cs[2 * i + 1] = c2[i];
-          sn[2 * i + 1] = s2[i];
-          sn[2 * i] = -s2[i];
-        }
-      } else {
-        const int i0 = e0 < half ? e0 : e0 - half;
-        load_floats<N>(row + i0, cs);
-        load_floats<N>(row + half + i0, sn);
-        if (e0 < half) {
+  for (int i = 0; i < N; ++i) {
+    a[i] = 1.0f;
+    b[i] = 0.0f;
+  }
+  if (rotate) {
+    const float* row = p.cos_sin + pos * p.rot;
+    if (inter) {
+      float c2[N / 2], s2[N / 2];
+      load_floats<N / 2>(row + e0 / 2, c2);
+      load_floats<N / 2>(row + half + e0 / 2, s2);
 #pragma unroll
-          for (int i = 0; i < N; ++i) sn[i] = -sn[i];
-        }
+      for (int i = 0; i < N / 2; ++i) {
+        a[2 * i] = a[2 * i + 1] = c2[i];
+        b[2 * i + 1] = s2[i];
+        b[2 * i] = -s2[i];
+      }
+    } else {
+      const int i0 = e0 < half ? e0 : e0 - half;
+      load_floats<N>(row + i0, a);
+      load_floats<N>(row + half + i0, b);
+      if (e0 < half) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) b[i] = -b[i];
       }
     }
   }
-  // the weights of the side that the lane's heads are on (loaded again where k follows q)
-  float wt[N];
-  const float* have = nullptr;
-  // lane that holds the partner chunk of a half-split pair (itself where nothing is rotated)
-  const int shift = half / N;
-  const int partner = (inter || !rotate) ? lane : (e0 < half ? lane + shift : lane - shift);
+  // the chunk that holds the partners of a half-split pair
+  const int step = inter || !rotate ? 0 : (e0 < half ? half : -half);
+  const int partner = lane + step / N;
+  if (s.w) {
+    float w[N];
+    load_floats<N>(s.w + e0, w);
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] *= w[i];
+    if (!inter) load_floats<N>(s.w + e0 + step, w);
+#pragma unroll
+    for (int i = 0; i < N; ++i) b[i] *= inter ? w[i ^ 1] : w[i];
+  }
 
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const int h = h0 + u * RPW;
-    float x[N];
+    float x[N], y[N];
     Vec16<T>::unpack(raw[u], x);
     float ss = 0.0f;
 #pragma unroll
@@ -115,32 +121,22 @@ head_norm_kernel(const HeadNormParams p, int groups) {
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     const float r = rsqrtf(((p.flags & KDA_NORM_L2) ? ss : ss * (1.0f / D)) + p.eps);
-    const bool isq = h < p.q.H;
-    const HeadNormSide& s = isq ? p.q : p.k;
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] *= r;
-    if (s.w) {
-      if (s.w != have) {
-        load_floats<N>(s.w + e0, wt);
-        have = s.w;
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) x[i] *= wt[i];
-    }
-    float y[N];
-    if (inter) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) y[i] = x[i ^ 1];
+    if (p.rot && !inter) {
+      uint4 o;
+      o.x = __shfl_sync(0xffffffffu, raw[u].x, partner);
+      o.y = __shfl_sync(0xffffffffu, raw[u].y, partner);
+      o.z = __shfl_sync(0xffffffffu, raw[u].z, partner);
+      o.w = __shfl_sync(0xffffffffu, raw[u].w, partner);
+      Vec16<T>::unpack(o, y);
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], partner);
+      for (int i = 0; i < N; ++i) y[i] = rotate ? x[i ^ 1] : x[i];
     }
-    if (rotate) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = fmaf(x[i], cs[i], y[i] * sn[i]);
-    }
-    if (h < H) {
-      T* out = (T*)s.out + tok * s.out_stride + (int64_t)(isq ? h : h - p.q.H) * D + e0;
+    for (int i = 0; i < N; ++i) x[i] = fmaf(x[i], a[i], y[i] * b[i]) * r;
+    const int h = h0 + u * RPW;
+    if (h < s.H) {
+      T* out = (T*)s.out + tok * s.out_stride + h * D + e0;
       __stcs(reinterpret_cast<uint4*>(out), Vec16<T>::pack(x));
     }
   }
@@ -149,11 +145,12 @@ head_norm_kernel(const HeadNormParams p, int groups) {
 template <class T, int D>
 kda_status launch_t(const HeadNormParams& p, cudaStream_t s) {
   constexpr int HEADS = 32 / (D / Vec16<T>::N) * kUnroll;
-  const int groups = (p.q.H + p.k.H + HEADS - 1) / HEADS;
+  const int q_groups = (p.q.H + HEADS - 1) / HEADS;
+  const int groups = q_groups + (p.k.H + HEADS - 1) / HEADS;
   const int64_t blocks = ((int64_t)p.tokens * groups + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffffLL)
     return set_error(KDA_ERR_INVALID_ARG, "kda_head_norm_rope: too many tokens x heads");
-  head_norm_kernel<T, D><<<(unsigned)blocks, kWarps * 32, 0, s>>>(p, groups);
+  head_norm_kernel<T, D><<<(unsigned)blocks, kWarps * 32, 0, s>>>(p, q_groups, groups);
   count_launches(1);
   return check_launch("kda_head_norm_rope");
 }
