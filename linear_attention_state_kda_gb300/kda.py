@@ -1,17 +1,19 @@
 """Thin Python binding of libkda.so (include/kda.h): one function per C entry point.
 
-Argument marshalling only: tensors are passed as raw device pointers with their sizes, on
+Argument marshalling only (ctypes, or a compiled module for the serving operators): tensors are passed as raw device pointers with their sizes, on
 the current torch CUDA stream; every step of the computation runs in the library's CUDA
 kernels. Outputs that the caller does not supply are allocated with torch (plumbing).
 Loading fails loudly if the library was not built: there is no fallback.
 """
 import ctypes
+import importlib.util
 import os
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libkda.so")
+NATIVE_PATH = os.path.join(_HERE, "_build", "_kda_native.so")
 
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_WORKSPACE, KDA_ERR_CUDA = range(5)
 KDA_F32, KDA_BF16 = 0, 1
@@ -136,8 +138,7 @@ def _dt(t):
 
 def _stream(stream):
     if stream is None:
-        # the raw handle of torch.cuda.current_stream(), without building the Stream object
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
 
@@ -441,62 +442,30 @@ def short_conv(x, weight, cu_seqlens=None, silu=False, read_slots=None, write_sl
     return out
 
 
-# The serving operators are called once or more per layer and token, so their checks are written
-# for few attribute reads: a call's host time is what bounds it at small sizes.
+# The serving operators are called once or more per layer and token, and a call's host time is
+# what bounds it at small sizes: their checks and allocations run in a compiled module
+# (csrc/kda_binding.cpp) that calls the same C entry points.
 
-_F32, _I32, _BF16 = torch.float32, torch.int32, torch.bfloat16
-_DTYPES = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
-
-
-def _code(dtype):
-    try:
-        return _DTYPES[dtype]
-    except KeyError:
-        raise TypeError(f"unsupported dtype {dtype}") from None
+_native_module = None
 
 
-def _vec(t, dtype, n, name):
-    """Pointer of a contiguous tensor of n entries of `dtype` (None for None)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous and hold {n} entries")
-    return t.data_ptr()
+def _native():
+    """The compiled half of the binding. Raises if it has not been built."""
+    global _native_module
+    if _native_module is None:
+        lib()
+        if not os.path.exists(NATIVE_PATH):
+            raise RuntimeError(f"_kda_native.so not found at {NATIVE_PATH}: build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`")
+        spec = importlib.util.spec_from_file_location("_kda_native", NATIVE_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _native_module = module
+    return _native_module
 
 
-def _heads(t, shape, dtype, name):
-    """Token stride of [tokens, H, d] rows whose heads are contiguous (any token stride)."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    st = t.stride()
-    if t.shape != shape or st[2] != 1 or (st[1] != shape[2] and shape[1] > 1):
-        raise ValueError(f"{name} must be [tokens, heads, d] = {tuple(shape)} with contiguous heads")
-    return st[0] if shape[0] > 1 else shape[1] * shape[2]
-
-
-def _cache(k_cache, k_scale, v_cache, v_scale, page_table, rows):
-    """Checks a cache's four tensors and its page table; returns (n_pages, Hkv, d, max_pages)."""
-    shape = k_cache.shape
-    dtype = k_cache.dtype
-    if (dtype is not torch.float8_e4m3fn and dtype is not torch.uint8) or \
-            v_cache.dtype is not dtype:
-        raise TypeError("the caches must be float8_e4m3fn (or uint8 codes)")
-    if k_scale.dtype is not _F32 or v_scale.dtype is not _F32 or page_table.dtype is not _I32:
-        raise TypeError("the scales must be float32 and page_table int32")
-    n_pages, H, page, d = shape
-    if page != PAGE or v_cache.shape != shape:
-        raise ValueError("the caches must both be [n_pages, Hkv, 64, d]")
-    if k_scale.shape != (n_pages, H) or v_scale.shape != (n_pages, H):
-        raise ValueError("the scales must be [n_pages, Hkv]")
-    n, max_pages = page_table.shape
-    if n != rows:
-        raise ValueError("page_table must be [rows, max_pages], a row for each entry of start")
-    if not (k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous() and
-            v_scale.is_contiguous() and page_table.is_contiguous()):
-        raise ValueError("the cache's tensors and page_table must be contiguous")
-    return n_pages, H, d, max_pages
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def head_norm_rope(q, k, q_weight=None, k_weight=None, eps=1e-6, l2=False, cos_sin=None,
@@ -506,47 +475,12 @@ def head_norm_rope(q, k, q_weight=None, k_weight=None, eps=1e-6, l2=False, cos_s
     with per-channel weights, then the rotation by row `positions[t]` of cos_sin [n_pos, rot_dim]
     (none when cos_sin is None). q and k may be views of a fused projection's rows; either may be
     None. q_out = q (k_out = k) works in place. Returns (q_out, k_out)."""
-    x = k if q is None else q
-    T, _, d = x.shape
-    dtype = x.dtype
-    code = _code(dtype)
-    qp = kp = qop = kop = cp = None
-    Hq = Hk = qs = ks = qos = kos = n_pos = rot = 0
-    if q is not None:
-        shape = q.shape
-        Hq = shape[1]
-        qs = _heads(q, shape, dtype, "q")
-        if q_out is None:
-            q_out = torch.empty(shape, dtype=dtype, device=q.device)
-            qos = Hq * d
-        else:
-            qos = _heads(q_out, shape, dtype, "q_out")
-        qp, qop = q.data_ptr(), q_out.data_ptr()
-    if k is not None:
-        shape = k.shape
-        Hk = shape[1]
-        ks = _heads(k, shape, dtype, "k")
-        if shape[0] != T or shape[2] != d:
-            raise ValueError("q and k must have the same tokens and head size")
-        if k_out is None:
-            k_out = torch.empty(shape, dtype=dtype, device=k.device)
-            kos = Hk * d
-        else:
-            kos = _heads(k_out, shape, dtype, "k_out")
-        kp, kop = k.data_ptr(), k_out.data_ptr()
-    if cos_sin is not None:
-        n_pos, rot = cos_sin.shape
-        cp = _vec(cos_sin, _F32, n_pos * rot, "cos_sin")
-    st = lib().kda_head_norm_rope(code, T, Hq, Hk, d, qp, qs, kp, ks,
-                                  _vec(q_weight, _F32, d, "q_weight"),
-                                  _vec(k_weight, _F32, d, "k_weight"), eps,
-                                  (NORM_L2 if l2 else 0) |
-                                  (ROPE_INTERLEAVED if interleaved else 0), cp, n_pos, rot,
-                                  _vec(positions, _I32, T, "positions"), qop, qos, kop, kos,
-                                  _ptr(status), _stream(stream))
-    if st:
-        _check(st)
-    return q_out, k_out
+    r = (_native_module or _native()).head_norm_rope(
+        q, k, q_weight, k_weight, eps, l2, cos_sin, positions, interleaved, q_out, k_out, status,
+        _handle(stream))
+    if r.__class__ is int:
+        _check(r)
+    return r
 
 
 def cache_write(k, v, start, page_table, k_cache, k_scale, v_cache, v_scale, cu_seqlens=None,
@@ -554,46 +488,23 @@ def cache_write(k, v, start, page_table, k_cache, k_scale, v_cache, v_scale, cu_
     """kda_cache_write: quantises k and v [T, Hkv, d] (views of a fused projection's rows are fine)
     into the paged cache [n_pages, Hkv, 64, d] with scales [n_pages, Hkv], token i of sequence s at
     position start[s] + i. The caches and scales are updated in place."""
-    n = start.numel()
-    n_pages, H, d, max_pages = _cache(k_cache, k_scale, v_cache, v_scale, page_table, n)
-    shape, dtype = k.shape, k.dtype
-    if shape[1:] != (H, d):
-        raise ValueError("k and v must be [tokens, Hkv, d] of the cache")
-    st = lib().kda_cache_write(_code(dtype), n, shape[0],
-                               _vec(cu_seqlens, _I32, n + 1, "cu_seqlens"),
-                               _vec(start, _I32, n, "start"), _vec(lens, _I32, n, "lens"), H, d,
-                               k.data_ptr(), _heads(k, shape, dtype, "k"), v.data_ptr(),
-                               _heads(v, shape, dtype, "v"), page_table.data_ptr(), max_pages,
-                               k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(),
-                               v_scale.data_ptr(), n_pages, _ptr(status), _stream(stream))
-    if st:
-        _check(st)
+    r = (_native_module or _native()).cache_write(
+        k, v, start, page_table, k_cache, k_scale, v_cache, v_scale, cu_seqlens, lens, status,
+        _handle(stream))
+    if r is not None:
+        _check(r)
 
 
 def cache_read(start, page_table, k_cache, k_scale, v_cache, v_scale, total_tokens,
                cu_seqlens=None, dtype=torch.bfloat16, k=None, v=None, status=None, stream=None):
     """kda_cache_read: cached keys and values of positions start[s] .. of each sequence, packed by
     cu_seqlens (total_tokens rows in all). Returns (k, v), [total_tokens, Hkv, d] of `dtype`."""
-    n = start.numel()
-    n_pages, H, d, max_pages = _cache(k_cache, k_scale, v_cache, v_scale, page_table, n)
-    code = _code(dtype)
-    shape = (total_tokens, H, d)
-    if k is None:
-        k = torch.empty(shape, dtype=dtype, device=k_cache.device)
-    if v is None:
-        v = torch.empty(shape, dtype=dtype, device=k_cache.device)
-    if k.shape != shape or v.shape != shape:
-        raise ValueError("k and v must be [total_tokens, Hkv, d]")
-    size = total_tokens * H * d
-    st = lib().kda_cache_read(code, n, total_tokens, _vec(cu_seqlens, _I32, n + 1, "cu_seqlens"),
-                              _vec(start, _I32, n, "start"), H, d, page_table.data_ptr(),
-                              max_pages, k_cache.data_ptr(), k_scale.data_ptr(),
-                              v_cache.data_ptr(), v_scale.data_ptr(), n_pages,
-                              _vec(k, dtype, size, "k"), _vec(v, dtype, size, "v"), _ptr(status),
-                              _stream(stream))
-    if st:
-        _check(st)
-    return k, v
+    r = (_native_module or _native()).cache_read(
+        start, page_table, k_cache, k_scale, v_cache, v_scale, total_tokens, cu_seqlens, dtype, k,
+        v, status, _handle(stream))
+    if r.__class__ is int:
+        _check(r)
+    return r
 
 
 def cache_attention_workspace(batch, window, Hq, Hkv, d):
@@ -607,47 +518,12 @@ def cache_attention(q, start, page_table, k_cache, k_scale, v_cache, v_scale, sc
     of row b at position start[b] + j, seeing the cached positions 0 .. start[b] + j. `workspace`
     (uint8 device tensor of at least cache_attention_workspace(...) bytes) is allocated here when
     not given. Returns o, shaped like q."""
-    B = start.numel()
-    n_pages, Hkv, d, max_pages = _cache(k_cache, k_scale, v_cache, v_scale, page_table, B)
-    L = lib()
-    shape, dtype, size = q.shape, q.dtype, q.numel()
-    Hq = shape[-2]
-    if shape[-1] != d:
-        raise ValueError("q and the cache differ in head size")
-    W = size // (B * Hq * d) if B else 0
-    if size != B * W * Hq * d:
-        raise ValueError("q must hold batch x window tokens")
-    if o is None:
-        o = torch.empty(shape, dtype=dtype, device=q.device)
-    if workspace is None:
-        need = ws_bytes = L.kda_cache_attention_workspace(B, W, Hq, Hkv, d)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    else:
-        ws_bytes = workspace.numel() * workspace.element_size()
-    st = L.kda_cache_attention(_code(dtype), B, W, Hq, Hkv, d, scale,
-                               _vec(q, dtype, size, "q"), _vec(start, _I32, B, "start"),
-                               _vec(lens, _I32, B, "lens"), page_table.data_ptr(), max_pages,
-                               k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(),
-                               v_scale.data_ptr(), n_pages, _vec(o, dtype, size, "o"),
-                               _ptr(workspace), ws_bytes, _ptr(status), _stream(stream))
-    if st:
-        _check(st)
-    return o
-
-
-def _rows3(t, shape, dtype, name):
-    """Row stride of [batch, places, vocab] rows at one stride, entries contiguous."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}")
-    b, n, v = shape
-    s0, s1, s2 = t.stride()
-    s = s1 if n > 1 else (s0 if b > 1 else v)
-    if (s2 != 1 and v > 1) or (b > 1 and s0 != n * s):
-        raise ValueError(f"{name} must have contiguous entries and evenly spaced rows")
-    return s
+    r = (_native_module or _native()).cache_attention(
+        q, start, page_table, k_cache, k_scale, v_cache, v_scale, scale, lens, o, workspace, status,
+        _handle(stream))
+    if r.__class__ is int:
+        _check(r)
+    return r
 
 
 def draft_verify(target_probs, draft_tokens, u_accept, u_sample, draft_probs=None, lens=None,
@@ -658,34 +534,9 @@ def draft_verify(target_probs, draft_tokens, u_accept, u_sample, draft_probs=Non
     [batch, window, vocab] or None for drafts that were not sampled). Returns (n_accepted [batch],
     tokens [batch, window+1] padded with -1, resume_slots [batch]: write_slots[b, n_accepted[b]],
     the slot to resume the recurrent state from, or None without write_slots)."""
-    shape, dtype = target_probs.shape, target_probs.dtype
-    code = _code(dtype)
-    B, W1, V = shape
-    W = W1 - 1
-    if draft_tokens.shape != (B, W) or u_accept.shape != (B, W):
-        raise ValueError("draft_tokens and u_accept must be [batch, window]")
-    dev = target_probs.device
-    if tokens is None:
-        tokens = torch.empty((B, W1), dtype=_I32, device=dev)
-    if n_accepted is None:
-        n_accepted = torch.empty((B,), dtype=_I32, device=dev)
-    if resume_slots is None and write_slots is not None:
-        resume_slots = torch.empty((B,), dtype=_I32, device=dev)
-    ds, dp = 0, None
-    if draft_probs is not None and W:
-        ds = _rows3(draft_probs, (B, W, V), dtype, "draft_probs")
-        dp = draft_probs.data_ptr()
-    st = lib().kda_draft_verify(code, B, W, V, target_probs.data_ptr(),
-                                _rows3(target_probs, shape, dtype, "target_probs"), dp, ds,
-                                _vec(draft_tokens, _I32, B * W, "draft_tokens"),
-                                _vec(lens, _I32, B, "lens"),
-                                _vec(u_accept, _F32, B * W, "u_accept"),
-                                _vec(u_sample, _F32, B, "u_sample"),
-                                _vec(write_slots, _I32, B * W1, "write_slots"),
-                                _vec(tokens, _I32, B * W1, "tokens"),
-                                _vec(n_accepted, _I32, B, "n_accepted"),
-                                _vec(resume_slots, _I32, B, "resume_slots"), _ptr(status),
-                                _stream(stream))
-    if st:
-        _check(st)
-    return n_accepted, tokens, resume_slots
+    r = (_native_module or _native()).draft_verify(
+        target_probs, draft_tokens, u_accept, u_sample, draft_probs, lens, write_slots, tokens,
+        n_accepted, resume_slots, status, _handle(stream))
+    if r.__class__ is int:
+        _check(r)
+    return r
