@@ -51,7 +51,6 @@ constexpr int kWindows = 512;      // windows of rows in the search for a warp's
 // unit instead of in most steps.
 constexpr float kPBase = 7.0f, kSlack = 8.0f;
 constexpr int kUnitCost = 2;  // what beginning and ending a unit takes, in slices
-constexpr int kMinCost = kUnitCost + 2;  // least work of a warp
 constexpr int kNoEnd = 1 << 30;    // beyond the positions of the largest page table
 constexpr int kMinScaleExp = -60;  // clamp of e_t in M, so that l stays in range
 
@@ -125,9 +124,8 @@ __device__ __forceinline__ int row_slices(const CacheAttnParams& p, int b, bool 
   if (flag && p.status) atomicOr(p.status, KDA_STATUS_BAD_PAGE);
   return (int)(most / kSlice);
 }
-__device__ __forceinline__ int row_cost(const CacheAttnParams& p, int b, bool flag) {
-  const int n = row_slices(p, b, flag);
-  return n > 0 ? n + kUnitCost : 0;
+__device__ __forceinline__ int row_cost(int slices, int unit_cost) {
+  return slices > 0 ? slices + unit_cost : 0;
 }
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
@@ -342,65 +340,93 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
   constexpr int kStages = S::STAGES;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_win[kWindows];
+  __shared__ int s_rows[kWindows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int G = p.Hq / p.Hkv, R = G * p.window;
   const int nrg = (R + S::ROWS - 1) / S::ROWS;
   const int U = p.Hkv * nrg;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // cost of each window of rows, then of all
+  // Slices of each window of rows and rows that have any, then of all; up to 32 rows without
+  // leaving the warp.
   const int per_win = (p.batch + 32 * kWindows - 1) / (32 * kWindows) * 32;
   const int n_win = (p.batch + per_win - 1) / per_win;
-  for (int w = warp; w < n_win; w += kWarps) {
-    int64_t c = 0;
-    for (int i = lane; i < per_win; i += 32) c += row_cost(p, w * per_win + i, blockIdx.x == 0);
-    c = warp_sum(c);
-    if (lane == 0) s_win[w] = c;
+  int64_t slices = 0, live_rows = 0;
+  int slices_l = 0;  // lane's row of the 32 from `base` on
+  if (p.batch <= 32) {
+    slices_l = row_slices(p, lane, blockIdx.x == 0);
+    slices = warp_sum(slices_l);
+    live_rows = __popc(__ballot_sync(0xffffffffu, slices_l > 0));
+  } else {
+    for (int w = warp; w < n_win; w += kWarps) {
+      int64_t c = 0, r = 0;
+      for (int i = lane; i < per_win; i += 32) {
+        const int n = row_slices(p, w * per_win + i, blockIdx.x == 0);
+        c += n;
+        r += n > 0;
+      }
+      c = warp_sum(c);
+      r = warp_sum(r);
+      if (lane == 0) {
+        s_win[w] = c;
+        s_rows[w] = (int)r;
+      }
+    }
+    __syncthreads();
+    for (int w = lane; w < n_win; w += 32) {
+      slices += s_win[w];
+      live_rows += s_rows[w];
+    }
+    slices = warp_sum(slices);
+    live_rows = warp_sum(live_rows);
   }
-  __syncthreads();
-  int64_t total = 0;
-  for (int w = lane; w < n_win; w += 32) total += s_win[w];
-  total = warp_sum(total) * U;
-  // this warp's range; consecutive ranges are on different SMs
+  // This warp's range; consecutive ranges are on different SMs. With no more slices than warps,
+  // one each: there is no one to balance with.
   const int worker = warp * gridDim.x + blockIdx.x;
-  int64_t workers = (total + kMinCost - 1) / kMinCost;
-  if (workers > (int64_t)gridDim.x * kWarps) workers = gridDim.x * kWarps;
+  int64_t workers = (int64_t)gridDim.x * kWarps;
+  const bool few = slices * U <= workers;
+  const int unit_cost = few ? 0 : kUnitCost;
+  const int64_t total = (slices + live_rows * unit_cost) * U;
+  if (few) workers = total;
   int64_t pos = 0, end = 0;
   if (worker < workers) {
-    pos = total * worker / workers;
-    end = total * (worker + 1) / workers;
+    pos = few ? worker : total * worker / workers;
+    end = few ? worker + 1 : total * (worker + 1) / workers;
   }
 
   // the row that holds pos: its window, then the 32 rows, then the row
-  int base = 0, row = 0, cost_l = 0, cost = 0;
+  int base = 0, row = 0, cost = 0;
   int64_t at = 0;  // where row base + row begins
   if (pos < end) {
-    int w = 0;
-    for (;; w += 32) {
-      int64_t c = w + lane < n_win ? s_win[w + lane] * U : 0;
-      const int64_t mine = c;
+    if (p.batch > 32) {
+      int w = 0;
+      for (;; w += 32) {
+        int64_t c =
+            w + lane < n_win ? (s_win[w + lane] + (int64_t)s_rows[w + lane] * unit_cost) * U : 0;
+        const int64_t mine = c;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, c, o);
-        if (lane >= o) c += u;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t u = __shfl_up_sync(0xffffffffu, c, o);
+          if (lane >= o) c += u;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, at + c <= pos);
+        const int k = __popc(past);  // windows that end at or before pos
+        if (k < 32) {
+          at += __shfl_sync(0xffffffffu, c - mine, k);
+          base = (w + k) * per_win;
+          break;
+        }
+        at += __shfl_sync(0xffffffffu, c, 31);
       }
-      const unsigned past = __ballot_sync(0xffffffffu, at + c <= pos);
-      const int k = __popc(past);  // windows that end at or before pos
-      if (k < 32) {
-        at += __shfl_sync(0xffffffffu, c - mine, k);
-        base = (w + k) * per_win;
-        break;
+      for (;;) {
+        slices_l = row_slices(p, base + lane, false);
+        const int64_t c = warp_sum(row_cost(slices_l, unit_cost)) * U;
+        if (at + c > pos) break;
+        at += c;
+        base += 32;
       }
-      at += __shfl_sync(0xffffffffu, c, 31);
     }
-    for (;;) {
-      cost_l = row_cost(p, base + lane, false);
-      const int64_t c = warp_sum(cost_l) * U;
-      if (at + c > pos) break;
-      at += c;
-      base += 32;
-    }
-    cost = __shfl_sync(0xffffffffu, cost_l, 0);
+    cost = row_cost(__shfl_sync(0xffffffffu, slices_l, 0), unit_cost);
   }
 
   uint8_t* ring = smem + warp * (kStages * S::STAGE + S::QBYTES);
@@ -416,19 +442,19 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
       if (++row == 32) {
         row = 0;
         base += 32;
-        cost_l = row_cost(p, base + lane, false);
+        slices_l = row_slices(p, base + lane, false);
       }
-      cost = __shfl_sync(0xffffffffu, cost_l, row);
+      cost = row_cost(__shfl_sync(0xffffffffu, slices_l, row), unit_cost);
     }
     // the piece [first, last) of a unit's slices
-    const int b = base + row, n_slices = cost - kUnitCost;
+    const int b = base + row, n_slices = cost - unit_cost;
     const int unit = (int)((pos - at) / cost);
     const int x0 = (int)((pos - at) - (int64_t)unit * cost);
     const int x1 = end - pos < cost - x0 ? x0 + (int)(end - pos) : cost;
-    const int64_t stop = pos + (cost - x0);  // end of the unit
+    const int64_t pos0 = pos, stop = pos + (cost - x0);  // end of the unit
     pos += x1 - x0;
-    const int first = x0 > kUnitCost ? x0 - kUnitCost : 0;
-    const int last = x1 > kUnitCost ? x1 - kUnitCost : 0;
+    const int first = x0 > unit_cost ? x0 - unit_cost : 0;
+    const int last = x1 > unit_cost ? x1 - unit_cost : 0;
     if (first == last) continue;  // the range ends before the unit's first slice
     const int h = unit / nrg, rg = unit - h * nrg;
 
@@ -612,10 +638,9 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
       }
     if (first == 0 && lane == 0) {
       UnitDesc d = {worker, 0};
-      if (!whole) {  // its last piece is in the range that holds the unit's end
-        d.pieces = 1;
-        while (total * (worker + d.pieces) / workers < stop) ++d.pieces;
-      }
+      // its last piece is in the first range that ends at or after the unit's end
+      if (!whole)
+        d.pieces = (int)(few ? stop - pos0 : (stop * workers + total - 1) / total - worker);
       desc[(int64_t)b * U + unit] = d;
     }
   }
@@ -629,18 +654,16 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
   }
 }
 
-constexpr int kJoinWarps = 16;
-
 // Joins the pieces of a unit that was cut: the second slot of the warp that began it, then the
-// first slots of the next ones. `per_row` warps of the CTA sum every per_row-th piece of a row, and
-// their sums are added in order.
-template <class T, int D, int MT>
+// first slots of the next ones. `per_row` warps of the CTA sum every per_row-th piece of a row
+// relative to their own largest M, and their sums are added in order.
+template <class T, int D, int MT, int kJoinWarps, int kBatch>
 __global__ void __launch_bounds__(kJoinWarps * 32)
 join_kernel(const CacheAttnParams p, int piece_rows, int per_row, const float* ws_o,
             const float2* ws_ml, const UnitDesc* desc) {
   using S = Shape<T, D, MT>;
   constexpr int N = D / 32;
-  __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps];
+  __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps], s_m[kJoinWarps];
   const int G = p.Hq / p.Hkv, R = G * p.window;
   const int nrg = (R + S::ROWS - 1) / S::ROWS, U = p.Hkv * nrg;
   const int b = blockIdx.x / U, unit = blockIdx.x - b * U, h = unit / nrg, rg = unit - h * nrg;
@@ -651,49 +674,67 @@ join_kernel(const CacheAttnParams p, int piece_rows, int per_row, const float* w
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const UnitDesc d = desc[blockIdx.x];
   if (d.pieces == 0) return;
-  auto slot_row = [&](int i) {
-    return (int64_t)(i == 0 ? 2 * d.worker + 1 : 2 * (d.worker + i)) * piece_rows + r;
-  };
-  float o[N], l = 0.0f;
+  float o[N], l = 0.0f, m = -INFINITY;
 #pragma unroll
   for (int c = 0; c < N; ++c) o[c] = 0.0f;
-  if (mine) {
-    float top = -INFINITY;
-    for (int i = lane; i < d.pieces; i += 32) top = fmaxf(top, ws_ml[slot_row(i)].x);
+  for (int i0 = sub; mine && i0 < d.pieces; i0 += per_row * kBatch) {
+    float2 ml[kBatch];
+    float x[kBatch][N];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    const float mu = top == -INFINITY ? 0.0f : top;
-#pragma unroll 8
-    for (int i = sub; i < d.pieces; i += per_row) {
-      const int64_t at = slot_row(i);
-      const float2 ml = ws_ml[at];
-      float x[N];
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * per_row;
+      ml[k] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int c = 0; c < N; ++c) x[k][c] = 0.0f;
+      if (i >= d.pieces) continue;
+      const int64_t at =
+          (int64_t)(i == 0 ? 2 * d.worker + 1 : 2 * (d.worker + i)) * piece_rows + r;
+      ml[k] = ws_ml[at];
       if constexpr (N == 4) {
         const float4 v = *reinterpret_cast<const float4*>(ws_o + at * D + lane * N);
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+        x[k][0] = v.x; x[k][1] = v.y; x[k][2] = v.z; x[k][3] = v.w;
       } else {
         const float2 v = *reinterpret_cast<const float2*>(ws_o + at * D + lane * N);
-        x[0] = v.x; x[1] = v.y;
+        x[k][0] = v.x; x[k][1] = v.y;
       }
-      // a piece in which the row saw no key has m = -inf and only zeros
-      const float f = ptx::ex2_approx(ml.x - mu);
-      l = fmaf(f, ml.y, l);
+    }
+    float top = m;
 #pragma unroll
-      for (int c = 0; c < N; ++c) o[c] = fmaf(f, x[c], o[c]);
+    for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k].x);
+    const float mu = top == -INFINITY ? 0.0f : top;
+    const float keep = ptx::ex2_approx(m - mu);
+    m = top;
+    l *= keep;
+#pragma unroll
+    for (int c = 0; c < N; ++c) o[c] *= keep;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      // a piece in which the row saw no key has M = -inf and only zeros
+      const float f = ptx::ex2_approx(ml[k].x - mu);
+      l = fmaf(f, ml[k].y, l);
+#pragma unroll
+      for (int c = 0; c < N; ++c) o[c] = fmaf(f, x[k][c], o[c]);
     }
   }
 #pragma unroll
   for (int c = 0; c < N; ++c) s_o[warp][lane * N + c] = o[c];
-  if (lane == 0) s_l[warp] = l;
+  if (lane == 0) {
+    s_l[warp] = l;
+    s_m[warp] = m;
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < rows * D; i += kJoinWarps * 32) {
     const int rr = i / D, c = i - rr * D;
     const int gq = rg * S::ROWS + blockIdx.y * rows + rr, j = gq / G;
     if (blockIdx.y * rows + rr >= S::ROWS || gq >= R) continue;
+    float top = -INFINITY;
+    for (int w = 0; w < per_row; ++w) top = fmaxf(top, s_m[rr * per_row + w]);
+    const float mu = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f, ls = 0.0f;
     for (int w = 0; w < per_row; ++w) {
-      sum += s_o[rr * per_row + w][c];
-      ls += s_l[rr * per_row + w];
+      const float f = ptx::ex2_approx(s_m[rr * per_row + w] - mu);
+      sum = fmaf(f, s_o[rr * per_row + w][c], sum);
+      ls = fmaf(f, s_l[rr * per_row + w], ls);
     }
     const bool live = j < row_tokens(p, b) && ls != 0.0f;
     T* dst = (T*)p.o + ((int64_t)(b * p.window + j) * p.Hq + h * G + (gq - j * G)) * D;
@@ -720,6 +761,15 @@ kda_status launch_t(const CacheAttnParams& p, cudaStream_t s) {
     int sms = 0;
     e = cudaFuncSetAttribute(attn_kernel<T, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              S::SMEM);
+    // the same split of L1 and shared memory for both kernels: no SM is drained to change it
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(join_kernel<T, D, MT, 16, 8>,
+                               cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(join_kernel<T, D, MT, 4, 4>,
+                               cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
       return set_error(KDA_ERR_CUDA, std::string("kda_cache_attention: ") + cudaGetErrorString(e));
@@ -727,10 +777,9 @@ kda_status launch_t(const CacheAttnParams& p, cudaStream_t s) {
   }
   const int G = p.Hq / p.Hkv, R = G * p.window, nrg = (R + S::ROWS - 1) / S::ROWS;
   const int rows = R < S::ROWS ? R : S::ROWS;
-  // no more CTAs than the page table allows ranges of kMinCost
+  // no more CTAs than the page table allows slices
   const int64_t units = (int64_t)p.batch * p.Hkv * nrg;
-  const int64_t most =
-      (units * ((int64_t)p.max_pages * (kPage / kSlice) + kUnitCost) + kMinCost - 1) / kMinCost;
+  const int64_t most = units * p.max_pages * (kPage / kSlice);
   const int ctas = most < sms_of[dev] ? (int)most : sms_of[dev];
   uint8_t* ws = (uint8_t*)p.ws;
   float* ws_o = (float*)ws;
@@ -739,22 +788,21 @@ kda_status launch_t(const CacheAttnParams& p, cudaStream_t s) {
   attn_kernel<T, D, MT><<<ctas, kThreads, S::SMEM, s>>>(p, rows, ws_o, ws_ml, desc);
   kda_status st = check_launch("kda_cache_attention");
   if (st != KDA_OK) return st;
-  // few units have many pieces each: a CTA per row; many units: a CTA for as many rows as it has
-  // warps
-  int per_row = kJoinWarps;
-  if (units * rows > 4 * sms_of[dev])
-    while (per_row > 1 && kJoinWarps / per_row < rows) per_row >>= 1;
+  // Few units have many pieces each: 16 warps for a row of one. Many units have a few: a warp for a
+  // row, in small CTAs.
+  const bool few = units * rows <= 4 * sms_of[dev];
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)units, (unsigned)((rows * per_row + kJoinWarps - 1) / kJoinWarps));
-  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.gridDim = dim3((unsigned)units, (unsigned)(few ? rows : (rows + 3) / 4));
+  cfg.blockDim = dim3(few ? 512 : 128);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, join_kernel<T, D, MT>, p, rows, per_row, (const float*)ws_o,
-                     (const float2*)ws_ml, (const UnitDesc*)desc);
+  cudaLaunchKernelEx(&cfg, few ? join_kernel<T, D, MT, 16, 8> : join_kernel<T, D, MT, 4, 4>, p, rows,
+                     few ? 16 : 1, (const float*)ws_o, (const float2*)ws_ml,
+                     (const UnitDesc*)desc);
   count_launches(2);
   return check_launch("kda_cache_attention");
 }
