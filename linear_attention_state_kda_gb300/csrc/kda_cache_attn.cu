@@ -4,7 +4,7 @@
 //
 // What bounds it: the cache is read once, 2 d bytes per token and key/value head, so a single
 // decoded token per row is HBM-bound; the 4 d operations per (query row, key) are tensor-core
-// work. A "unit" is one (batch row, key/value head) with up to 16 MT query rows (the window's tokens
+// work. A "unit" is one (batch row, key/value head) with up to 64 query rows (the window's tokens
 // times the query heads of the group), so that the cache is read once for all of them.
 //
 // Arithmetic. e4m3 codes are exact in f16, so both products run as f16 x f16 -> fp32 warp MMAs
@@ -26,13 +26,15 @@
 // that for d = 64). A lane's outputs are then 32 consecutive channels of its row.
 //
 // Work split. The rows' key slices (32 keys) are laid end to end (row, head, row group, slice) and
-// cut into as many equal ranges as warps fit on the GPU (8 per SM), so that ragged lengths and few
-// rows load every SM alike. A warp walks its range alone, through a private ring of shared-memory
-// buffers filled with 16-byte asynchronous copies: no barrier, and while one warp begins or ends
-// a unit the others keep the memory busy. (A CTA per unit, its warps joined at the unit's end,
-// left 4-8 us of latency per unit uncovered: 398 us against this split's on 128 rows of up to 16k
-// tokens.) A unit that lies in one range is finished there; the pieces of a unit that is cut go to
-// the workspace (each warp has at most two) and a second kernel, launched ahead of time and
+// cut into as many equal ranges as workers fit on the GPU, so that ragged lengths and few rows load
+// every SM alike. A worker is one warp (8 per SM), or a team of 2 or 4 warps with 16 query rows
+// each (12 warps per SM); it walks its range through its own ring of shared-memory buffers filled
+// with 16-byte asynchronous copies, and while one begins or ends a unit the others keep the memory
+// busy. (A CTA per unit, its warps joined at the unit's end, left 4-8 us of latency per unit
+// uncovered: 398 us against 354 on 128 rows of up to 16k tokens. Two row tiles in one warp instead
+// of a team: 8 warps of 255 registers, 98 us against 74 on 32 windows of 32 rows. Teams in 16 warps
+// of 128 registers spill: 292 us against 149 on 64 windows.) A unit that lies in one range is finished there; the pieces of a unit that is cut go to
+// the workspace (each worker has at most two) and a second kernel, launched ahead of time and
 // released when the first ends, joins them in order: no atomics, the same bits every time.
 #include "kda_internal.cuh"
 #include "kda_fp8.cuh"
@@ -42,9 +44,7 @@ namespace kda {
 namespace {
 
 constexpr int kSlice = 32;    // keys per warp step
-constexpr int kWarps = 8;     // per CTA, one CTA per SM: up to 255 registers a thread
-constexpr int kThreads = kWarps * 32;
-constexpr int kMaxWorkers = 1280;  // warps that share the work, at most (sizes the workspace)
+constexpr int kMaxSms = 160;  // SMs used at most (sizes the workspace)
 constexpr int kWindows = 512;      // windows of rows in the search for a warp's first row
 // P is 2^kPBase for a term equal to the row's M, and M is raised only when a term exceeds it by
 // more than 2^kSlack: P <= 2^15 fits f16, and the accumulators are rescaled once or twice per
@@ -58,21 +58,33 @@ struct UnitDesc {  // of a unit that is cut: the warp that began it, and how man
   int32_t worker, pieces;
 };
 
-template <class T, int D, int MT>
+// TEAM warps walk a unit's slices together, 16 query rows each: the slice is copied once for all
+// of them.
+template <class T, int D, int TEAM>
 struct Shape {
   static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;
-  static constexpr int ROWS = 16 * MT;
+  static constexpr int WARPS = TEAM == 1 ? 8 : 12;  // one CTA per SM: 255 or 168 registers a thread
+  static constexpr int THREADS = WARPS * 32;
+  static constexpr int TEAMS = WARPS / TEAM;        // workers of a CTA
+  static constexpr int ROWS = 16 * TEAM;
   static constexpr int KSTEPS = D / 16;
   static constexpr int NT = D / 8;                // n-tiles of the second product
   static constexpr int SLICE_BYTES = kSlice * D;  // one of K, V
   static constexpr int STAGE = 2 * SLICE_BYTES;
-  static constexpr int STAGES = MT == 2 && D == 128 ? 2 : 3;
-  // Query operands: in registers for one row tile, in shared memory for two.
-  static constexpr bool QREG = MT == 1;
-  static constexpr int QFRAGS = MT * PARTS * KSTEPS;
-  static constexpr int QBYTES = QREG ? 0 : QFRAGS * 512;
-  static constexpr int SMEM = kWarps * (STAGES * STAGE + QBYTES);
+  static constexpr int STAGES = 3;
+  // Query operands: in registers where there are enough, else in shared memory.
+  static constexpr bool QREG = TEAM == 1;
+  static constexpr int QFRAGS = PARTS * KSTEPS;
+  static constexpr int QBYTES = QREG ? 0 : QFRAGS * 512;  // of a warp
+  static constexpr int SMEM = TEAMS * STAGES * STAGE + WARPS * QBYTES;
 };
+
+// Barrier of a team's warps.
+template <int TEAM>
+__device__ __forceinline__ void team_sync(int team) {
+  if constexpr (TEAM == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TEAM * 32) : "memory");
+}
 
 // Byte of 16-byte chunk c of row r of a slice: chunks are permuted within the row so that both
 // access patterns above touch every bank once (d = 128).
@@ -133,32 +145,27 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
   return v;
 }
 
-template <class T, int D, int MT>
+template <int D>
 struct WarpState {
-  float o[MT][D / 8][4];
-  float m[MT][2], l[MT][2];
+  float o[D / 8][4];
+  float m[2], l[2];
 };
 
 // One slice: scores, softmax update, weighted values. kTail: some key of the slice is hidden from
 // some row; `left` of its keys are seen by each of the lane's rows.
-template <class T, int D, int MT, bool kTail>
-__device__ __forceinline__ void slice_step(WarpState<T, D, MT>& st, const uint8_t* kb,
-                                           const uint8_t* vb,
-                                           const uint4 (&qreg)[Shape<T, D, MT>::QREG
-                                                                   ? Shape<T, D, MT>::QFRAGS : 1],
-                                           const uint4* qfrag, float ks, float vs,
-                                           const float (&rowf)[MT][2], const int (&left)[MT][2],
-                                           int lane) {
-  using S = Shape<T, D, MT>;
+template <class T, int D, int TEAM, bool kTail>
+__device__ __forceinline__ void slice_step(
+    WarpState<D>& st, const uint8_t* kb, const uint8_t* vb,
+    const uint4 (&qreg)[Shape<T, D, TEAM>::QREG ? Shape<T, D, TEAM>::QFRAGS : 1],
+    const uint4* qfrag, float ks, float vs, const float (&rowf)[2], const int (&left)[2], int lane) {
+  using S = Shape<T, D, TEAM>;
   constexpr int NK = kSlice / 8;  // key tiles of the first product
   const int g = lane >> 2, t = lane & 3;
-  float s[MT][NK][4];
+  float s[NK][4];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int nt = 0; nt < NK; ++nt)
 #pragma unroll
-    for (int nt = 0; nt < NK; ++nt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[mt][nt][i] = 0.0f;
+    for (int i = 0; i < 4; ++i) s[nt][i] = 0.0f;
   // half of the lane's channels at a time
 #pragma unroll
   for (int j = 0; j < D / 64; ++j) {
@@ -172,81 +179,72 @@ __device__ __forceinline__ void slice_step(WarpState<T, D, MT>& st, const uint8_
 #pragma unroll
       for (int nt = 0; nt < NK; ++nt) f16x4_from_e4m3((&kw[nt].x)[k4], b[nt][0], b[nt][1]);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int part = 0; part < S::PARTS; ++part) {
+        const int at = part * S::KSTEPS + 4 * j + k4;
+        const uint4 a = S::QREG ? qreg[S::QREG ? at : 0] : qfrag[at * 32 + lane];
 #pragma unroll
-        for (int part = 0; part < S::PARTS; ++part) {
-          const int at = (mt * S::PARTS + part) * S::KSTEPS + 4 * j + k4;
-          const uint4 a = S::QREG ? qreg[S::QREG ? at : 0] : qfrag[at * 32 + lane];
-#pragma unroll
-          for (int nt = 0; nt < NK; ++nt) mma_f16(s[mt][nt], a, b[nt][0], b[nt][1]);
-        }
+        for (int nt = 0; nt < NK; ++nt) mma_f16(s[nt], a, b[nt][0], b[nt][1]);
+      }
     }
   }
   const int ve = (int)((__float_as_uint(vs) >> 23) & 255u) - 127;
   const float vexp = (float)ve, vref = (float)(ve < kMinScaleExp ? kMinScaleExp : ve);
   const float vinv = __uint_as_float((uint32_t)(127 - ve) << 23);  // 2^-e
   bool over = false;
-  float top[MT][2];
+  float top[2];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int half = 0; half < 2; ++half) {
+    const float f = rowf[half] * ks;
+    top[half] = -INFINITY;
+#pragma unroll
+    for (int nt = 0; nt < NK; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float& x = s[nt][half * 2 + i];
+        x *= f;
+        if constexpr (kTail) {
+          if (nt * 8 + 2 * t + i >= left[half]) x = -INFINITY;
+        }
+        top[half] = fmaxf(top[half], x);
+      }
+    over |= top[half] + vref > st.m[half] + kSlack;
+  }
+  if (__any_sync(0xffffffffu, over)) {
+    float corr[2];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const float f = rowf[mt][half] * ks;
-      top[mt][half] = -INFINITY;
-#pragma unroll
-      for (int nt = 0; nt < NK; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float& x = s[mt][nt][half * 2 + i];
-          x *= f;
-          if constexpr (kTail) {
-            if (nt * 8 + 2 * t + i >= left[mt][half]) x = -INFINITY;
-          }
-          top[mt][half] = fmaxf(top[mt][half], x);
-        }
-      over |= top[mt][half] + vref > st.m[mt][half] + kSlack;
+      float x = top[half];
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+      const float mo = st.m[half], mn = fmaxf(mo, x + vref);
+      st.m[half] = mn;
+      corr[half] = ptx::ex2_approx(mo - (mn == -INFINITY ? 0.0f : mn));
+      st.l[half] *= corr[half];
     }
-  if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float corr[2];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float x = top[mt][half];
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        const float mo = st.m[mt][half], mn = fmaxf(mo, x + vref);
-        st.m[mt][half] = mn;
-        corr[half] = ptx::ex2_approx(mo - (mn == -INFINITY ? 0.0f : mn));
-        st.l[mt][half] *= corr[half];
-      }
-#pragma unroll
-      for (int n = 0; n < S::NT; ++n) {
-        st.o[mt][n][0] *= corr[0]; st.o[mt][n][1] *= corr[0];
-        st.o[mt][n][2] *= corr[1]; st.o[mt][n][3] *= corr[1];
-      }
+    for (int n = 0; n < S::NT; ++n) {
+      st.o[n][0] *= corr[0]; st.o[n][1] *= corr[0];
+      st.o[n][2] *= corr[1]; st.o[n][3] *= corr[1];
     }
   }
-  uint4 pa[MT][S::PARTS][kSlice / 16];
+  uint4 pa[S::PARTS][kSlice / 16];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int half = 0; half < 2; ++half) {
+    const float m = st.m[half];
+    const float c = vexp - (m == -INFINITY ? 0.0f : m) + kPBase;
+    float sum = 0.0f;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const float m = st.m[mt][half];
-      const float c = vexp - (m == -INFINITY ? 0.0f : m) + kPBase;
-      float sum = 0.0f;
-#pragma unroll
-      for (int nt = 0; nt < NK; ++nt) {
-        const float x0 = ptx::ex2_approx(s[mt][nt][half * 2] + c);
-        const float x1 = ptx::ex2_approx(s[mt][nt][half * 2 + 1] + c);
-        sum += x0 + x1;
-        const uint32_t hi = f16x2(x0, x1);
-        (&pa[mt][0][nt >> 1].x)[half + 2 * (nt & 1)] = hi;
-        if constexpr (S::PARTS == 2)
-          (&pa[mt][1][nt >> 1].x)[half + 2 * (nt & 1)] = f16x2_rest(x0, x1, hi);
-      }
-      st.l[mt][half] = fmaf(sum, vinv, st.l[mt][half]);
+    for (int nt = 0; nt < NK; ++nt) {
+      const float x0 = ptx::ex2_approx(s[nt][half * 2] + c);
+      const float x1 = ptx::ex2_approx(s[nt][half * 2 + 1] + c);
+      sum += x0 + x1;
+      const uint32_t hi = f16x2(x0, x1);
+      (&pa[0][nt >> 1].x)[half + 2 * (nt & 1)] = hi;
+      if constexpr (S::PARTS == 2)
+        (&pa[1][nt >> 1].x)[half + 2 * (nt & 1)] = f16x2_rest(x0, x1, hi);
     }
+    st.l[half] = fmaf(sum, vinv, st.l[half]);
+  }
 #pragma unroll
   for (int kh = 0; kh < kSlice / 16; ++kh) {
     uint32_t vw[4][D / 32];
@@ -273,17 +271,15 @@ __device__ __forceinline__ void slice_step(WarpState<T, D, MT>& st, const uint8_
         for (int w = 0; w < D / 32; ++w)
           nan |= __vcmpeq4(vw[r][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
       if (__any_sync(0xffffffffu, nan != 0)) {
-        uint4 va[MT];  // 1 where the row sees the key
+        uint4 va;  // 1 where the row sees the key
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              const int key = kh * 16 + nt * 8 + 2 * t;
-              (&va[mt].x)[half + 2 * nt] = (key < left[mt][half] ? 0x3c00u : 0u) |
-                                           (key + 1 < left[mt][half] ? 0x3c000000u : 0u);
-            }
+          for (int nt = 0; nt < 2; ++nt) {
+            const int key = kh * 16 + nt * 8 + 2 * t;
+            (&va.x)[half + 2 * nt] = (key < left[half] ? 0x3c00u : 0u) |
+                                     (key + 1 < left[half] ? 0x3c000000u : 0u);
+          }
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
           uint32_t ind[4];
@@ -300,15 +296,13 @@ __device__ __forceinline__ void slice_step(WarpState<T, D, MT>& st, const uint8_
             f16x4_from_e4m3(__byte_perm(ind[0], ind[1], sel), b0[0], b0[1]);
             f16x4_from_e4m3(__byte_perm(ind[2], ind[3], sel), b1[0], b1[1]);
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 2; ++u) {
+              float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              mma_f16(hit, va, b0[u], b1[u]);
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                float hit[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma_f16(hit, va[mt], b0[u], b1[u]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (hit[i] > 0.0f) st.o[mt][4 * w + q + u][i] = __uint_as_float(0x7fffffffu);
-              }
+              for (int i = 0; i < 4; ++i)
+                if (hit[i] > 0.0f) st.o[4 * w + q + u][i] = __uint_as_float(0x7fffffffu);
+            }
           }
         }
       }
@@ -324,24 +318,23 @@ __device__ __forceinline__ void slice_step(WarpState<T, D, MT>& st, const uint8_
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int part = 0; part < S::PARTS; ++part)
-              mma_f16(st.o[mt][4 * w + q + u], pa[mt][part][kh], b0[u], b1[u]);
+          for (int part = 0; part < S::PARTS; ++part)
+            mma_f16(st.o[4 * w + q + u], pa[part][kh], b0[u], b1[u]);
       }
     }
   }
 }
 
-template <class T, int D, int MT>
-__global__ void __launch_bounds__(kThreads, 1)
+template <class T, int D, int TEAM>
+__global__ void __launch_bounds__(Shape<T, D, TEAM>::THREADS, 1)
 attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml, UnitDesc* desc) {
-  using S = Shape<T, D, MT>;
-  constexpr int kStages = S::STAGES;
+  using S = Shape<T, D, TEAM>;
+  constexpr int kStages = S::STAGES, kWarps = S::WARPS;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_win[kWindows];
   __shared__ int s_rows[kWindows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int team = warp / TEAM, member = warp % TEAM;
   const int G = p.Hq / p.Hkv, R = G * p.window;
   const int nrg = (R + S::ROWS - 1) / S::ROWS;
   const int U = p.Hkv * nrg;
@@ -380,10 +373,10 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
     slices = warp_sum(slices);
     live_rows = warp_sum(live_rows);
   }
-  // This warp's range; consecutive ranges are on different SMs. With no more slices than warps,
+  // This team's range; consecutive ranges are on different SMs. With no more slices than teams,
   // one each: there is no one to balance with.
-  const int worker = warp * gridDim.x + blockIdx.x;
-  int64_t workers = (int64_t)gridDim.x * kWarps;
+  const int worker = team * gridDim.x + blockIdx.x;
+  int64_t workers = (int64_t)gridDim.x * S::TEAMS;
   const bool few = slices * U <= workers;
   const int unit_cost = few ? 0 : kUnitCost;
   const int64_t total = (slices + live_rows * unit_cost) * U;
@@ -429,10 +422,11 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
     cost = row_cost(__shfl_sync(0xffffffffu, slices_l, 0), unit_cost);
   }
 
-  uint8_t* ring = smem + warp * (kStages * S::STAGE + S::QBYTES);
+  uint8_t* ring = smem + team * (kStages * S::STAGE);
   const uint32_t ring_u = ptx::smem_u32(ring);
-  uint4* qf = reinterpret_cast<uint4*>(ring + kStages * S::STAGE);
-  // 16-byte copies of a lane: chunk lane + 32 c, at rotated places of their rows
+  uint4* qf = reinterpret_cast<uint4*>(smem + S::TEAMS * kStages * S::STAGE + warp * S::QBYTES);
+  // 16-byte copies of a lane: chunk lane + 32 c, at rotated places of their rows; the team's
+  // members take every TEAM-th c
   const int put0 = D == 128 ? (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4)
                             : (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
 
@@ -474,15 +468,19 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
         const uint8_t* vp = p.vc + off;
         const uint32_t dst = ring_u + stage * S::STAGE;
 #pragma unroll
-        for (int c = 0; c < S::SLICE_BYTES / 512; ++c)
+        for (int i = 0; i < S::SLICE_BYTES / 512 / TEAM; ++i) {
+          const int c = i * TEAM + member;
           cp16(dst + c * 512 + (D == 128 ? put0 ^ ((c & 1) * 64) : put0), kp + c * 512);
+        }
 #pragma unroll
-        for (int c = 0; c < S::SLICE_BYTES / 512; ++c)
+        for (int i = 0; i < S::SLICE_BYTES / 512 / TEAM; ++i) {
+          const int c = i * TEAM + member;
           cp16(dst + S::SLICE_BYTES + c * 512 + (D == 128 ? put0 ^ ((c & 1) * 64) : put0),
                vp + c * 512);
+        }
         n.ks = p.ks[slice];
         n.vs = p.vs[slice];
-      } else if (page >= 0 && lane == 0 && p.status) {
+      } else if (page >= 0 && lane == 0 && member == 0 && p.status) {
         atomicOr(p.status, KDA_STATUS_BAD_PAGE);
       }
       cp_commit();
@@ -503,15 +501,15 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
     // by a power of two and rounds them to the f16 parts of its MMA operands.
     const int n_tok = row_tokens(p, b);
     const int start = p.start[b];
-    float rowf[MT][2];
-    int seen[MT][2], least = kNoEnd;
+    const int row0 = rg * S::ROWS + member * 16;  // of this warp's rows
+    float rowf[2];
+    int seen[2], least = kNoEnd;
     uint4 qreg[S::QREG ? S::QFRAGS : 1];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    {
       uint32_t frag[S::PARTS][S::KSTEPS][4];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int gr = rg * S::ROWS + mt * 16 + half * 8 + g, j = gr / G;
+        const int gr = row0 + half * 8 + g, j = gr / G;
         const bool live = gr < R && j < n_tok;
         float q[D / 4];
 #pragma unroll
@@ -532,11 +530,11 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
         int e = top ? 13 + 127 - (int)(top >> 23) : 0;
         e = e > 100 ? 100 : (e < -100 ? -100 : e);
         const float up = pow2f(e);
-        rowf[mt][half] = p.scale * 1.44269504f * pow2f(-e);
+        rowf[half] = p.scale * 1.44269504f * pow2f(-e);
         // rows that are not live see everything: they force no mask, and are not stored
         const int64_t n = (int64_t)start + j + 1;
-        seen[mt][half] = live && n < kNoEnd ? (int)n : kNoEnd;
-        least = min(least, seen[mt][half]);
+        seen[half] = live && n < kNoEnd ? (int)n : kNoEnd;
+        least = min(least, seen[half]);
 #pragma unroll
         for (int k = 0; k < S::KSTEPS; ++k)
 #pragma unroll
@@ -553,28 +551,26 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
         for (int k = 0; k < S::KSTEPS; ++k) {
           const uint4 a = make_uint4(frag[part][k][0], frag[part][k][1], frag[part][k][2],
                                      frag[part][k][3]);
-          const int i = (mt * S::PARTS + part) * S::KSTEPS + k;
+          const int i = part * S::KSTEPS + k;
           if constexpr (S::QREG) qreg[i] = a;
           else qf[i * 32 + lane] = a;
         }
     }
     least = __reduce_min_sync(0xffffffffu, least);
 
-    WarpState<T, D, MT> st;
+    WarpState<D> st;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int n = 0; n < S::NT; ++n)
 #pragma unroll
-      for (int n = 0; n < S::NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) st.o[mt][n][i] = 0.0f;
-      st.m[mt][0] = st.m[mt][1] = -INFINITY;
-      st.l[mt][0] = st.l[mt][1] = 0.0f;
-    }
+      for (int i = 0; i < 4; ++i) st.o[n][i] = 0.0f;
+    st.m[0] = st.m[1] = -INFINITY;
+    st.l[0] = st.l[1] = 0.0f;
     int stage = 0;
 #pragma unroll 1
     for (int sl = first; sl < last; ++sl) {
+      // the copies of every member, and the end of every member's last step
       cp_wait<kStages - 2>();
-      __syncwarp();
+      team_sync<TEAM>(team);
       const Pending cur = pend[0];
 #pragma unroll
       for (int i = 0; i < kStages - 2; ++i) pend[i] = pend[i + 1];
@@ -585,58 +581,55 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
       const uint8_t* vb = kb + S::SLICE_BYTES;
       stage = stage == kStages - 1 ? 0 : stage + 1;
       if (!cur.present) continue;
-      int left[MT][2];
+      if (row0 >= R) continue;  // a member without rows only copies
+      int left[2];
       if (sl * kSlice + kSlice <= least) {
-        slice_step<T, D, MT, false>(st, kb, vb, qreg, qf, cur.ks, cur.vs, rowf, left, lane);
+        slice_step<T, D, TEAM, false>(st, kb, vb, qreg, qf, cur.ks, cur.vs, rowf, left, lane);
       } else {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) left[mt][half] = seen[mt][half] - sl * kSlice;
-        slice_step<T, D, MT, true>(st, kb, vb, qreg, qf, cur.ks, cur.vs, rowf, left, lane);
+        left[0] = seen[0] - sl * kSlice;
+        left[1] = seen[1] - sl * kSlice;
+        slice_step<T, D, TEAM, true>(st, kb, vb, qreg, qf, cur.ks, cur.vs, rowf, left, lane);
       }
     }
     cp_wait<0>();
-    __syncwarp();
+    team_sync<TEAM>(team);  // the ring is free for the next unit
 
     const bool whole = first == 0 && last == n_slices;
     const int slot = 2 * worker + (first == 0 ? 1 : 0);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int half = 0; half < 2; ++half) {
+      float l = st.l[half];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      const int gr = row0 + half * 8 + g, j = gr / G;
+      if (gr >= R) continue;
+      float o[D / 4];  // channels t D/4 + n and t D/4 + D/8 + n
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float l = st.l[mt][half];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        const int r = mt * 16 + half * 8 + g, gr = rg * S::ROWS + r, j = gr / G;
-        if (gr >= R) continue;
-        float o[D / 4];  // channels t D/4 + n and t D/4 + D/8 + n
-#pragma unroll
-        for (int n = 0; n < S::NT; ++n) {
-          o[n] = st.o[mt][n][half * 2];
-          o[D / 8 + n] = st.o[mt][n][half * 2 + 1];
-        }
-        if (whole) {
-          const bool live = j < n_tok;
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-          uint4* dst = reinterpret_cast<uint4*>(
-              (T*)p.o + ((int64_t)(b * p.window + j) * p.Hq + h * G + (gr - j * G)) * D +
-              t * (D / 4));
-          constexpr int N = Vec16<T>::N;
-#pragma unroll
-          for (int i = 0; i < D / 4; ++i) o[i] = live ? o[i] * inv : 0.0f;
-#pragma unroll
-          for (int i = 0; i < D / 4 / N; ++i) dst[i] = Vec16<T>::pack(o + i * N);
-        } else {
-          const int64_t to = (int64_t)slot * piece_rows + r;
-          float4* dst = reinterpret_cast<float4*>(ws_o + to * D + t * (D / 4));
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-            dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          if (t == 0) ws_ml[to] = make_float2(st.m[mt][half], l);
-        }
+      for (int n = 0; n < S::NT; ++n) {
+        o[n] = st.o[n][half * 2];
+        o[D / 8 + n] = st.o[n][half * 2 + 1];
       }
-    if (first == 0 && lane == 0) {
+      if (whole) {
+        const bool live = j < n_tok;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint4* dst = reinterpret_cast<uint4*>(
+            (T*)p.o + ((int64_t)(b * p.window + j) * p.Hq + h * G + (gr - j * G)) * D +
+            t * (D / 4));
+        constexpr int N = Vec16<T>::N;
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) o[i] = live ? o[i] * inv : 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 4 / N; ++i) dst[i] = Vec16<T>::pack(o + i * N);
+      } else {
+        const int64_t to = (int64_t)slot * piece_rows + (gr - rg * S::ROWS);
+        float4* dst = reinterpret_cast<float4*>(ws_o + to * D + t * (D / 4));
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        if (t == 0) ws_ml[to] = make_float2(st.m[half], l);
+      }
+    }
+    if (first == 0 && member == 0 && lane == 0) {
       UnitDesc d = {worker, 0};
       // its last piece is in the first range that ends at or after the unit's end
       if (!whole)
@@ -646,7 +639,7 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
   }
 
   // rows without keys
-  for (int b = worker; b < p.batch; b += gridDim.x * kWarps) {
+  for (int b = warp * gridDim.x + blockIdx.x; b < p.batch; b += gridDim.x * kWarps) {
     if (row_slices(p, b, false) > 0) continue;
     T* o = (T*)p.o + (int64_t)b * p.window * p.Hq * D;
     for (int i = lane; i < p.window * p.Hq * D; i += 32) st_elem(o, i, 0.0f);
@@ -657,20 +650,19 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
 // Joins the pieces of a unit that was cut: the second slot of the warp that began it, then the
 // first slots of the next ones. `per_row` warps of the CTA sum every per_row-th piece of a row
 // relative to their own largest M, and their sums are added in order.
-template <class T, int D, int MT, int kJoinWarps, int kBatch>
+template <class T, int D, int kJoinWarps, int kBatch>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-join_kernel(const CacheAttnParams p, int piece_rows, int per_row, const float* ws_o,
+join_kernel(const CacheAttnParams p, int unit_rows, int piece_rows, int per_row, const float* ws_o,
             const float2* ws_ml, const UnitDesc* desc) {
-  using S = Shape<T, D, MT>;
   constexpr int N = D / 32;
   __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps], s_m[kJoinWarps];
   const int G = p.Hq / p.Hkv, R = G * p.window;
-  const int nrg = (R + S::ROWS - 1) / S::ROWS, U = p.Hkv * nrg;
+  const int nrg = (R + unit_rows - 1) / unit_rows, U = p.Hkv * nrg;
   const int b = blockIdx.x / U, unit = blockIdx.x - b * U, h = unit / nrg, rg = unit - h * nrg;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % per_row;
   const int rows = kJoinWarps / per_row;
-  const int r = blockIdx.y * rows + warp / per_row, gr = rg * S::ROWS + r;
-  const bool mine = r < S::ROWS && gr < R;
+  const int r = blockIdx.y * rows + warp / per_row, gr = rg * unit_rows + r;
+  const bool mine = r < unit_rows && gr < R;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const UnitDesc d = desc[blockIdx.x];
   if (d.pieces == 0) return;
@@ -725,8 +717,8 @@ join_kernel(const CacheAttnParams p, int piece_rows, int per_row, const float* w
   __syncthreads();
   for (int i = threadIdx.x; i < rows * D; i += kJoinWarps * 32) {
     const int rr = i / D, c = i - rr * D;
-    const int gq = rg * S::ROWS + blockIdx.y * rows + rr, j = gq / G;
-    if (blockIdx.y * rows + rr >= S::ROWS || gq >= R) continue;
+    const int gq = rg * unit_rows + blockIdx.y * rows + rr, j = gq / G;
+    if (blockIdx.y * rows + rr >= unit_rows || gq >= R) continue;
     float top = -INFINITY;
     for (int w = 0; w < per_row; ++w) top = fmaxf(top, s_m[rr * per_row + w]);
     const float mu = top == -INFINITY ? 0.0f : top;
@@ -742,16 +734,17 @@ join_kernel(const CacheAttnParams p, int piece_rows, int per_row, const float* w
   }
 }
 
-// Rows of a unit: two MMA row tiles when the group and window fill them (bf16), else one.
-int row_tiles(kda_dtype dt, int rows) { return dt == KDA_BF16 && rows > 16 ? 2 : 1; }
+// Warps of a team: as many as the unit's query rows fill, up to four (bf16); more rows are cut into
+// groups that read the cache again. fp32 has too many operands for 128 registers.
+int team_of(kda_dtype dt, int rows) { return dt == KDA_F32 || rows <= 16 ? 1 : (rows <= 32 ? 2 : 4); }
 
-// Workspace: the pieces' sums, their (m, l), then a descriptor per unit (of 16 rows at least).
-size_t piece_bytes(int rows, int d) { return (size_t)2 * kMaxWorkers * rows * d * sizeof(float); }
-size_t ml_bytes(int rows) { return (size_t)2 * kMaxWorkers * rows * sizeof(float2); }
+// Workspace: the pieces' sums, their (m, l), then a descriptor per unit (of 16 rows at least). An
+// SM has 8 workers with units of up to 32 rows, or 4 with 64.
+size_t piece_rows_of(int R) { return (size_t)2 * kMaxSms * 8 * (R < 32 ? R : 32); }
 
-template <class T, int D, int MT>
+template <class T, int D, int TEAM>
 kda_status launch_t(const CacheAttnParams& p, cudaStream_t s) {
-  using S = Shape<T, D, MT>;
+  using S = Shape<T, D, TEAM>;
   static int sms_of[64] = {};  // SMs of each device, found once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -759,21 +752,21 @@ kda_status launch_t(const CacheAttnParams& p, cudaStream_t s) {
     return set_error(KDA_ERR_CUDA, "kda_cache_attention: no current device");
   if (sms_of[dev] == 0) {
     int sms = 0;
-    e = cudaFuncSetAttribute(attn_kernel<T, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(attn_kernel<T, D, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              S::SMEM);
     // the same split of L1 and shared memory for both kernels: no SM is drained to change it
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(join_kernel<T, D, MT, 16, 8>,
+      e = cudaFuncSetAttribute(join_kernel<T, D, 16, 8>,
                                cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(join_kernel<T, D, MT, 4, 4>,
+      e = cudaFuncSetAttribute(join_kernel<T, D, 4, 4>,
                                cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
       return set_error(KDA_ERR_CUDA, std::string("kda_cache_attention: ") + cudaGetErrorString(e));
-    sms_of[dev] = sms * kWarps < kMaxWorkers ? sms : kMaxWorkers / kWarps;
+    sms_of[dev] = sms < kMaxSms ? sms : kMaxSms;
   }
   const int G = p.Hq / p.Hkv, R = G * p.window, nrg = (R + S::ROWS - 1) / S::ROWS;
   const int rows = R < S::ROWS ? R : S::ROWS;
@@ -781,11 +774,10 @@ kda_status launch_t(const CacheAttnParams& p, cudaStream_t s) {
   const int64_t units = (int64_t)p.batch * p.Hkv * nrg;
   const int64_t most = units * p.max_pages * (kPage / kSlice);
   const int ctas = most < sms_of[dev] ? (int)most : sms_of[dev];
-  uint8_t* ws = (uint8_t*)p.ws;
-  float* ws_o = (float*)ws;
-  float2* ws_ml = (float2*)(ws + piece_bytes(rows, D));
-  UnitDesc* desc = (UnitDesc*)(ws + piece_bytes(rows, D) + ml_bytes(rows));
-  attn_kernel<T, D, MT><<<ctas, kThreads, S::SMEM, s>>>(p, rows, ws_o, ws_ml, desc);
+  float* ws_o = (float*)p.ws;
+  float2* ws_ml = (float2*)(ws_o + piece_rows_of(R) * D);
+  UnitDesc* desc = (UnitDesc*)(ws_ml + piece_rows_of(R));
+  attn_kernel<T, D, TEAM><<<ctas, S::THREADS, S::SMEM, s>>>(p, rows, ws_o, ws_ml, desc);
   kda_status st = check_launch("kda_cache_attention");
   if (st != KDA_OK) return st;
   // Few units have many pieces each: 16 warps for a row of one. Many units have a few: a warp for a
@@ -800,28 +792,34 @@ kda_status launch_t(const CacheAttnParams& p, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, few ? join_kernel<T, D, MT, 16, 8> : join_kernel<T, D, MT, 4, 4>, p, rows,
-                     few ? 16 : 1, (const float*)ws_o, (const float2*)ws_ml,
+  cudaLaunchKernelEx(&cfg, few ? join_kernel<T, D, 16, 8> : join_kernel<T, D, 4, 4>, p, S::ROWS,
+                     rows, few ? 16 : 1, (const float*)ws_o, (const float2*)ws_ml,
                      (const UnitDesc*)desc);
   count_launches(2);
   return check_launch("kda_cache_attention");
 }
 
+template <int D>
+kda_status dispatch(const CacheAttnParams& p, kda_dtype dt, cudaStream_t s) {
+  if (dt == KDA_F32) return launch_t<float, D, 1>(p, s);
+  switch (team_of(dt, p.Hq / p.Hkv * p.window)) {
+    case 1: return launch_t<__nv_bfloat16, D, 1>(p, s);
+    case 2: return launch_t<__nv_bfloat16, D, 2>(p, s);
+    default: return launch_t<__nv_bfloat16, D, 4>(p, s);
+  }
+}
+
 }  // namespace
 
 size_t cache_attn_workspace_bytes(int batch, int window, int Hq, int Hkv, int d) {
-  const int R = Hq / Hkv * window, rows = R < 32 ? R : 32;
+  const int R = Hq / Hkv * window;
   const size_t units = (size_t)batch * Hkv * ((R + 15) / 16);
-  return piece_bytes(rows, d) + ml_bytes(rows) + (sizeof(UnitDesc) * units + 255) / 256 * 256;
+  return piece_rows_of(R) * (d * sizeof(float) + sizeof(float2)) +
+         (sizeof(UnitDesc) * units + 255) / 256 * 256;
 }
 
 kda_status launch_cache_attn(const CacheAttnParams& p, kda_dtype dt, int d, cudaStream_t s) {
-  if (dt == KDA_BF16) {
-    if (row_tiles(dt, p.Hq / p.Hkv * p.window) == 2)
-      return d == 128 ? launch_t<__nv_bfloat16, 128, 2>(p, s) : launch_t<__nv_bfloat16, 64, 2>(p, s);
-    return d == 128 ? launch_t<__nv_bfloat16, 128, 1>(p, s) : launch_t<__nv_bfloat16, 64, 1>(p, s);
-  }
-  return d == 128 ? launch_t<float, 128, 1>(p, s) : launch_t<float, 64, 1>(p, s);
+  return d == 128 ? dispatch<128>(p, dt, s) : dispatch<64>(p, dt, s);
 }
 
 }  // namespace kda
