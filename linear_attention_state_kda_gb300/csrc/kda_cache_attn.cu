@@ -33,9 +33,11 @@
 // busy. (A CTA per unit, its warps joined at the unit's end, left 4-8 us of latency per unit
 // uncovered: 398 us against 354 on 128 rows of up to 16k tokens. Two row tiles in one warp instead
 // of a team: 8 warps of 255 registers, 98 us against 74 on 32 windows of 32 rows. Teams in 16 warps
-// of 128 registers spill: 292 us against 149 on 64 windows.) A unit that lies in one range is finished there; the pieces of a unit that is cut go to
-// the workspace (each worker has at most two) and a second kernel, launched ahead of time and
-// released when the first ends, joins them in order: no atomics, the same bits every time.
+// of 128 registers spill: 292 us against 149 on 64 windows.) A unit that lies in one range is
+// finished there; the pieces of a unit that is cut go to the workspace (each worker has at most
+// two) and a second kernel, placed ahead of time and released when the first ends, joins them in
+// order: no atomics, the same bits every time. (Only the second kernel is launched that way: the
+// launch costs some 2 us more on the host, which the first would not win back.)
 #include "kda_internal.cuh"
 #include "kda_fp8.cuh"
 #include "ptx.cuh"
