@@ -211,6 +211,8 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 8 : 1) verify_kerne
         all[i] = cluster > 1 ? ptx::ld_cluster_u64(from, i / kWarps) : *from;
       }
       __syncthreads();
+      // the other CTAs' sums are read: they may leave (or write them again) once all are here
+      if (cluster > 1) ptx::cluster_arrive();
       uint64_t total = 0, before = 0;
       for (int i = lane; i < chunks; i += 32) {
         total += all[i];
@@ -222,7 +224,8 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 8 : 1) verify_kerne
         if (!sub || round == 1) break;
         src.q = nullptr;
         src.hot = -1;
-        __syncthreads();  // all[] is written again
+        if (cluster > 1) ptx::cluster_wait();
+        else __syncthreads();  // all[] is written again
         continue;
       }
       const uint64_t limit = __umul64hi(total, u24 << 40);
@@ -232,8 +235,6 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 8 : 1) verify_kerne
                   : find_weight<1>(src, i0, i1, lane, before, limit);
       break;
     }
-    // no CTA leaves while another may read its sums
-    if (cluster > 1) ptx::cluster_sync();
   }
 
   if (owner && lane == 0 && !pad) p.tokens[(int64_t)b * (W + 1) + n] = tok;
@@ -245,6 +246,10 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 8 : 1) verify_kerne
       p.n_accepted[b] = taken;
       if (p.resume) p.resume[b] = pad ? -1 : p.slots[(int64_t)b * (W + 1) + n];
     }
+  }
+  if (!pad && cluster > 1) {
+    __syncwarp();
+    ptx::cluster_wait();
   }
 }
 

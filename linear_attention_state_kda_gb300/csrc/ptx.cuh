@@ -225,10 +225,16 @@ __device__ __forceinline__ bool wait_flag(const uint32_t* flag,
 }
 
 // ---------------------------------------------------------------- clusters
-// Barrier of all threads of the cluster, ordering their shared-memory accesses.
-__device__ __forceinline__ void cluster_sync() {
+// Barrier of all threads of the cluster, ordering their shared-memory accesses; its two halves.
+__device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
 }
 // The word at `p` (this CTA's shared memory) in the same place of the cluster's CTA `rank`.
 __device__ __forceinline__ uint64_t ld_cluster_u64(const uint64_t* p, uint32_t rank) {
