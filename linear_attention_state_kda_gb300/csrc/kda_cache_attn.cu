@@ -31,7 +31,7 @@
 // each (12 warps per SM); it walks its range through its own ring of shared-memory buffers filled
 // with 16-byte asynchronous copies, and while one begins or ends a unit the others keep the memory
 // busy. (A CTA per unit, its warps joined at the unit's end, left 4-8 us of latency per unit
-// uncovered: 398 us against 354 on 128 rows of up to 16k tokens. Two row tiles in one warp instead
+// uncovered: 398 us against 352 on 128 rows of up to 16k tokens. Two row tiles in one warp instead
 // of a team: 8 warps of 255 registers, 98 us against 74 on 32 windows of 32 rows. Teams in 16 warps
 // of 128 registers spill: 292 us against 149 on 64 windows.) A unit that lies in one range is
 // finished there; the pieces of a unit that is cut go to the workspace (each worker has at most
@@ -52,7 +52,7 @@ constexpr int kWindows = 512;      // windows of rows in the search for a warp's
 // more than 2^kSlack: P <= 2^15 fits f16, and the accumulators are rescaled once or twice per
 // unit instead of in most steps.
 constexpr float kPBase = 7.0f, kSlack = 8.0f;
-constexpr int kUnitCost = 2;  // what beginning and ending a unit takes, in slices
+constexpr int kUnitCost = 4;  // what beginning and ending a unit takes, in slices
 constexpr int kNoEnd = 1 << 30;    // beyond the positions of the largest page table
 constexpr int kMinScaleExp = -60;  // clamp of e_t in M, so that l stays in range
 
@@ -73,7 +73,7 @@ struct Shape {
   static constexpr int NT = D / 8;                // n-tiles of the second product
   static constexpr int SLICE_BYTES = kSlice * D;  // one of K, V
   static constexpr int STAGE = 2 * SLICE_BYTES;
-  static constexpr int STAGES = 3;
+  static constexpr int STAGES = D == 128 ? 2 : 3;
   // Query operands: in registers where there are enough, else in shared memory.
   static constexpr bool QREG = TEAM == 1;
   static constexpr int QFRAGS = PARTS * KSTEPS;
