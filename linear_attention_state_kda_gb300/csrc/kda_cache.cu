@@ -12,9 +12,10 @@
 // items are (page of a sequence, head, k or v): one CTA owns the page's slice, so that scale and
 // codes change without atomics, and holds all its new values in registers between the maximum
 // and the rounding (8 chunks of 16 bytes a thread), so that they are read once. 16384 tokens x 32
-// heads at d = 128 in bf16, one GB300: written in 66 us (6.1 TB/s, 89% of the copy rate; 69 with
-// codes stored without the streaming hint, 73 with 16 rows a pass in 256 threads), read back in
-// 63 us (6.4 TB/s, 95%; 65 with 128 threads).
+// heads at d = 128 in bf16, one GB300: written in 69 us (5.8 TB/s, 86% of the copy rate; 73 with
+// 16 rows a pass in 256 threads; with a streaming hint on the codes 66, but then what reads them
+// next finds fewer in L2 and the pair is 2 us slower), read back in 63 us (6.4 TB/s, 95%; 65
+// with 128 threads).
 #include "kda_internal.cuh"
 #include "kda_fp8.cuh"
 
@@ -162,9 +163,9 @@ cache_write_kernel(const CacheParams p) {
       w[j] = e4m3x2_from_f32(f[4 * j] * inv, f[4 * j + 1] * inv) |
              e4m3x2_from_f32(f[4 * j + 2] * inv, f[4 * j + 3] * inv) << 16;
     if constexpr (N == 8)
-      __stcs(reinterpret_cast<uint2*>(code + t * D + e0), make_uint2(w[0], w[1]));
+      *reinterpret_cast<uint2*>(code + t * D + e0) = make_uint2(w[0], w[1]);
     else
-      __stcs(reinterpret_cast<uint32_t*>(code + t * D + e0), w[0]);
+      *reinterpret_cast<uint32_t*>(code + t * D + e0) = w[0];
   }
   if (threadIdx.x == 0) *sp = s;
 }
