@@ -99,22 +99,29 @@ head_norm_kernel(const HeadNormParams p, int q_groups, int groups) {
   // the lane's two chunks
   const int half = p.rot / 2;
   bool rotate = 2 * CH * l < p.rot;
-  const bool split = !kInter && rotate;
-  const int c0 = split ? CH * l : 2 * CH * l, c1 = split ? half + CH * l : 2 * CH * l + CH;
+  int c0 = !kInter && rotate ? CH * l : 2 * CH * l;
+  int c1 = !kInter && rotate ? half + CH * l : 2 * CH * l + CH;
   const T* xr = (const T*)s.x + tok * s.x_stride + h0 * D;
   uint2 raw[kUnroll][2];
+  auto load = [&]() {
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    raw[u][0] = raw[u][1] = make_uint2(0u, 0u);
-    if (h0 + u * RPW < s.H) {
-      raw[u][0] = __ldcs(reinterpret_cast<const uint2*>(xr + u * RPW * D + c0));
-      raw[u][1] = __ldcs(reinterpret_cast<const uint2*>(xr + u * RPW * D + c1));
+    for (int u = 0; u < kUnroll; ++u) {
+      raw[u][0] = raw[u][1] = make_uint2(0u, 0u);
+      if (h0 + u * RPW < s.H) {
+        raw[u][0] = __ldcs(reinterpret_cast<const uint2*>(xr + u * RPW * D + c0));
+        raw[u][1] = __ldcs(reinterpret_cast<const uint2*>(xr + u * RPW * D + c1));
+      }
     }
-  }
+  };
+  load();
 
-  if (rotate && (pos < 0 || pos >= p.n_pos)) {
+  if (p.rot && (pos < 0 || pos >= p.n_pos)) {
+    // not rotated: as without a table, to the order of the sum
     if (group == 0 && lane == 0 && p.status) atomicOr(p.status, KDA_STATUS_BAD_POSITION);
     rotate = false;
+    c0 = 2 * CH * l;
+    c1 = c0 + CH;
+    load();
   }
   // Pairs: (chunk 0's k-th, chunk 1's k-th) channel, or adjacent channels when interleaved. The
   // weights in the same order, then the four factors.
