@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -129,6 +130,16 @@ struct Out {
       made = at::empty(shape, opts);
       t = &made;
     }
+  }
+  // A tensor made here belongs to the current stream: its memory is not handed out again before
+  // work on another stream that uses it is done.
+  void used_on(kda_stream_t s) const {
+    if (!made.defined()) return;
+    const auto current = c10::cuda::getCurrentCUDAStream();
+    if ((kda_stream_t)current.stream() == s) return;
+    c10::cuda::CUDACachingAllocator::recordStream(
+        made.storage().data_ptr(),
+        c10::cuda::getStreamFromExternal((cudaStream_t)s, made.device().index()));
   }
   PyObject* object() const {
     if (!given) return THPVariable_Wrap(made);
@@ -258,6 +269,7 @@ PyObject* head_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
                               out_stride[1], status, s);
   }();
   if (st != KDA_OK) return PyLong_FromLong(st);
+  for (const Out& o : out) o.used_on(s);
   return tuple_of({q ? out[0].object() : none(), k ? out[1].object() : none()});
   END_HANDLE_TH_ERRORS
 }
@@ -337,6 +349,7 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
                           c.vs, c.n_pages, dst[0], dst[1], status, s);
   }();
   if (st != KDA_OK) return PyLong_FromLong(st);
+  for (const Out& o : out) o.used_on(s);
   return tuple_of({out[0].object(), out[1].object()});
   END_HANDLE_TH_ERRORS
 }
@@ -381,7 +394,10 @@ PyObject* cache_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return kda_cache_attention(dt, b, w, hq, hkv, d, scale, qp, st0, lens, c.table, c.max_pages,
                                c.kc, c.ks, c.vc, c.vs, c.n_pages, op, wp, (size_t)bytes, status, s);
   }();
-  return st != KDA_OK ? PyLong_FromLong(st) : out.object();
+  if (st != KDA_OK) return PyLong_FromLong(st);
+  out.used_on(s);
+  ws.used_on(s);
+  return out.object();
   END_HANDLE_TH_ERRORS
 }
 
@@ -447,6 +463,7 @@ PyObject* draft_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
                             tp, np, rp, status, s);
   }();
   if (st != KDA_OK) return PyLong_FromLong(st);
+  for (const Out* o : {&tokens, &taken, &resume}) o->used_on(s);
   return tuple_of({taken.object(), tokens.object(), has_resume ? resume.object() : none()});
   END_HANDLE_TH_ERRORS
 }
