@@ -491,8 +491,8 @@ KDA_API kda_status kda_cache_read(kda_dtype dt, int n_seqs, int total_tokens,
                                   uint32_t* status, kda_stream_t stream);
 
 /*
- * kda_cache_attention: attention of one decoded token per row, or of a verify window of up to 16
- * tokens, over the paged 8-bit cache (which already holds the window's own keys and values).
+ * kda_cache_attention: attention of one decoded token per row, of a verify window, or of a chunk
+ * of a prompt, over the paged 8-bit cache (which already holds the window's own keys and values).
  * The window's token j of row b is at position start[b] + j and sees positions 0 .. start[b] + j:
  *     o = sum_t softmax_t(scale * q . k_t) v_t
  *   q, o        [batch * window, Hq, d] (dtype dt), 16-byte aligned; token j of row b is row
@@ -504,8 +504,11 @@ KDA_API kda_status kda_cache_read(kda_dtype dt, int n_seqs, int total_tokens,
  *   gets zeros. Cached values that a query does not see do not reach its result, NaN included.
  *   workspace   at least kda_cache_attention_workspace(...) bytes, 256-byte aligned; contents need
  *               not be initialised.
- *   window 1 .. 16 (0 is a no-op); Hq a multiple of Hkv; batch * Hkv at most 2^24;
- *   max_pages at most 2^24.
+ *   window 1 .. 65536 (0 is a no-op); Hq a multiple of Hkv; batch * Hkv at most 2^24, batch *
+ *   window * Hq at most 2^30; max_pages at most 2^24.
+ * The cache is read once per 64 query rows of a key/value head (16 in fp32), a query row being one
+ * token of one of the head's query heads: once for a decoded token or a verify window, many times
+ * (from L2 mostly) for a prompt's chunk.
  * Scores, softmax statistics and sums are fp32. With bf16 queries the probabilities enter the
  * second product rounded to 11 bits; with fp32 queries, queries and probabilities are carried in
  * two 11-bit parts.

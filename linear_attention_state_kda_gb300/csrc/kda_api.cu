@@ -571,7 +571,7 @@ kda_status kda_cache_read(kda_dtype dt, int n_seqs, int total_tokens, const int3
 }
 
 size_t kda_cache_attention_workspace(int batch, int window, int Hq, int Hkv, int d) {
-  if (batch <= 0 || window <= 0 || window > kMaxWindow || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 ||
+  if (batch <= 0 || window <= 0 || window > kMaxAttnWindow || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 ||
       (d != 64 && d != 128))
     return 0;
   return cache_attn_workspace_bytes(batch, window, Hq, Hkv, d);
@@ -584,8 +584,8 @@ kda_status kda_cache_attention(kda_dtype dt, int batch, int window, int Hq, int 
                                const float* v_scale, int64_t n_pages, void* o, void* workspace,
                                size_t ws_bytes, uint32_t* status, kda_stream_t stream) {
   const char* fn = "kda_cache_attention";
-  KDA_REQUIRE(window >= 0 && window <= kMaxWindow, KDA_ERR_UNSUPPORTED,
-              "kda_cache_attention: window must be in 0 .. 16");
+  KDA_REQUIRE(window >= 0 && window <= kMaxAttnWindow, KDA_ERR_UNSUPPORTED,
+              "kda_cache_attention: window must be in 0 .. 65536");
   KDA_REQUIRE(batch >= 0, KDA_ERR_INVALID_ARG, "kda_cache_attention: batch must be >= 0");
   kda_status st = check_head(fn, dt, d);
   if (st != KDA_OK) return st;

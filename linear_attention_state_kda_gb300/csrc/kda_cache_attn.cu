@@ -454,12 +454,19 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
     if (first == last) continue;  // the range ends before the unit's first slice
     const int h = unit / nrg, rg = unit - h * nrg;
 
+    // keys that any row of the team sees: a long window's first rows see fewer
+    const int n_tok = row_tokens(p, b);
+    const int start = p.start[b];
+    const int last_j = (rg * S::ROWS + S::ROWS - 1) / G;
+    const int64_t reach = (int64_t)start + (last_j < n_tok ? last_j + 1 : n_tok);
     const int32_t* table = p.table + (int64_t)b * p.max_pages;
     struct Pending {
       float ks, vs;
       bool present;
     };
-    auto page_of = [&](int sl) { return sl < last ? table[sl / (kPage / kSlice)] : -1; };
+    auto page_of = [&](int sl) {
+      return sl < last && (int64_t)sl * kSlice < reach ? table[sl / (kPage / kSlice)] : -1;
+    };
     auto issue = [&](int sl, int page, int stage) {
       Pending n = {0.0f, 0.0f, page >= 0 && page < p.n_pages};
       if (n.present) {
@@ -501,8 +508,6 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
 
     // Queries: a lane loads its D / 4 channels of rows g and g + 8 of each row tile, scales them
     // by a power of two and rounds them to the f16 parts of its MMA operands.
-    const int n_tok = row_tokens(p, b);
-    const int start = p.start[b];
     const int row0 = rg * S::ROWS + member * 16;  // of this warp's rows
     float rowf[2];
     int seen[2], least = kNoEnd;

@@ -148,7 +148,9 @@ struct CacheParams {
 kda_status launch_cache_write(const CacheParams& p, kda_dtype dt, int d, cudaStream_t s);
 kda_status launch_cache_read(const CacheParams& p, kda_dtype dt, int d, cudaStream_t s);
 
-// Attention of up to kMaxWindow query tokens per row over the cache.
+// Attention of a window of query tokens per row over the cache: one token, a verify window, or a
+// chunk of a prompt.
+constexpr int kMaxAttnWindow = 65536;
 struct CacheAttnParams {
   int batch, window, Hq, Hkv;
   float scale;

@@ -515,7 +515,8 @@ def cache_attention_workspace(batch, window, Hq, Hkv, d):
 def cache_attention(q, start, page_table, k_cache, k_scale, v_cache, v_scale, scale=1.0, lens=None,
                     o=None, workspace=None, status=None, stream=None):
     """kda_cache_attention: q [batch*window, Hq, d] or [batch, window, Hq, d], the window's token j
-    of row b at position start[b] + j, seeing the cached positions 0 .. start[b] + j. `workspace`
+    of row b at position start[b] + j, seeing the cached positions 0 .. start[b] + j: one decoded
+    token, a verify window, or a chunk of a prompt (any window up to 65536). `workspace`
     (uint8 device tensor of at least cache_attention_workspace(...) bytes) is allocated here when
     not given. Returns o, shaped like q."""
     r = (_native_module or _native()).cache_attention(

@@ -73,7 +73,7 @@ def _attn(L, dt=1, B=2, W=1, Hq=8, Hkv=2, d=128, q=P, start=P, table=P, cols=4, 
 def test_attention_refusals(L):
     from linear_attention_state_kda_gb300 import kda
     U, A = kda.KDA_ERR_UNSUPPORTED, kda.KDA_ERR_INVALID_ARG
-    assert _attn(L, dt=3) == U and _attn(L, d=80) == U and _attn(L, W=17) == U
+    assert _attn(L, dt=3) == U and _attn(L, d=80) == U and _attn(L, W=65537) == U
     assert _attn(L, W=-1) == U
     for bad in (dict(B=-1), dict(Hq=7), dict(Hkv=0), dict(Hq=0), dict(q=None), dict(start=None),
                 dict(table=None), dict(kc=None), dict(o=None), dict(pages=0), dict(cols=0),

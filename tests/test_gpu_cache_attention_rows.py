@@ -135,3 +135,25 @@ def test_table_entries_past_the_context_are_not_looked_at():
         status = torch.zeros(1, dtype=torch.int32, device=DEV)
         got = kda.cache_attention(q, _i32(start), wide, *pool, scale=0.05, status=status)
         assert torch.equal(got, want) and int(status) == 0
+
+
+@pytest.mark.parametrize("start,W,Hq,Hkv,d,dtype", [
+    ([0], 200, 4, 2, 128, "bf16"), ([37, 0], 130, 6, 2, 64, "bf16"), ([500], 333, 2, 1, 128, "bf16"),
+    ([0, 90], 65, 3, 3, 64, "f32"), ([64], 17, 2, 2, 128, "f32")])
+def test_chunks_of_a_prompt(start, W, Hq, Hkv, d, dtype):
+    """Windows longer than a verify window: many row groups, whose first rows see few keys; with a
+    ragged length, and a NaN value that only the last tokens see."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(W + d)
+    q, table, pool = _make(gen, start, W, Hq, Hkv, d, dtype)
+    lens = [W] + [W - 9] * (len(start) - 1)
+    scale = 0.3 * d ** -0.5
+    got = kda.cache_attention(q, _i32(start), table, *pool, scale=scale, lens=_i32(lens))
+    _check(q, start, lens, table, pool, scale, dtype, got)
+    at = start[0] + W - 3
+    pool[2][int(table[0, at // 64]), :, at % 64, 5] = 0x7f
+    one = kda.cache_attention(q, _i32(start), table, *pool, scale=scale, lens=_i32(lens))
+    assert torch.equal(one[:W - 3], got[:W - 3]) and torch.equal(one[W:], got[W:])
+    assert torch.isnan(one[W - 3:W, :, 5].float()).all()
+    rest = torch.arange(d, device=DEV) != 5
+    assert torch.equal(one[W - 3:W][..., rest], got[W - 3:W][..., rest])
