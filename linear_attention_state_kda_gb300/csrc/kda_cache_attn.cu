@@ -1,6 +1,7 @@
-// Attention of one decoded token, or of a verify window, over the paged 8-bit cache
-// (kda_cache_attention): o = sum_t softmax_t(scale q . k_t) v_t in one pass over the cache with
-// the running maximum and sum of the softmax.
+// Attention of one decoded token, of a verify window or of a chunk of a prompt over the paged 8-bit
+// cache (kda_cache_attention): o = sum_t softmax_t(scale q . k_t) v_t in one pass over the cache
+// with the running maximum and sum of the softmax. More than 64 bf16 query rows per key/value head
+// run on the kernel of kda_cache_attn_tc.cu.
 //
 // What bounds it: the cache is read once, 2 d bytes per token and key/value head, so a single
 // decoded token per row is HBM-bound; the 4 d operations per (query row, key) are tensor-core
@@ -38,27 +39,18 @@
 // two) and a second kernel, placed ahead of time and released when the first ends, joins them in
 // order: no atomics, the same bits every time. (Only the second kernel is launched that way: the
 // launch costs some 2 us more on the host, which the first would not win back.)
-#include "kda_internal.cuh"
+#include "kda_cache_attn.cuh"
 #include "kda_fp8.cuh"
 #include "ptx.cuh"
 
 namespace kda {
+
+using namespace attn;
+
 namespace {
 
 constexpr int kSlice = 32;    // keys per warp step
-constexpr int kMaxSms = 160;  // SMs used at most (sizes the workspace)
-constexpr int kWindows = 512;      // windows of rows in the search for a warp's first row
-// P is 2^kPBase for a term equal to the row's M, and M is raised only when a term exceeds it by
-// more than 2^kSlack: P <= 2^15 fits f16, and the accumulators are rescaled once or twice per
-// unit instead of in most steps.
-constexpr float kPBase = 7.0f, kSlack = 8.0f;
 constexpr int kUnitCost = 4;  // what beginning and ending a unit takes, in slices
-constexpr int kNoEnd = 1 << 30;    // beyond the positions of the largest page table
-constexpr int kMinScaleExp = -60;  // clamp of e_t in M, so that l stays in range
-
-struct UnitDesc {  // of a unit that is cut: the warp that began it, and how many share it (else 0)
-  int32_t worker, pieces;
-};
 
 // TEAM warps walk a unit's slices together, 16 query rows each: the slice is copied once for all
 // of them.
@@ -120,31 +112,6 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t f16x2_rest(float lo, float hi, uint32_t h) {
   const float2 f = f32x2_from_f16x2(h);
   return f16x2(lo - f.x, hi - f.y);
-}
-
-// Query tokens of row b, and 64-key blocks that any of them sees.
-__device__ __forceinline__ int row_tokens(const CacheAttnParams& p, int b) {
-  if (p.start[b] < 0) return 0;
-  const int n = p.lens ? p.lens[b] : p.window;
-  return n < 0 ? 0 : (n > p.window ? p.window : n);
-}
-// Key slices that any query of row b sees (within the page table).
-__device__ __forceinline__ int row_slices(const CacheAttnParams& p, int b, bool flag) {
-  if (b >= p.batch) return 0;
-  const int n = row_tokens(p, b);
-  if (n == 0) return 0;
-  const int64_t keys = (int64_t)p.start[b] + n, most = (int64_t)p.max_pages * kPage;
-  if (keys <= most) return (int)((keys + kSlice - 1) / kSlice);
-  if (flag && p.status) atomicOr(p.status, KDA_STATUS_BAD_PAGE);
-  return (int)(most / kSlice);
-}
-__device__ __forceinline__ int row_cost(int slices, int unit_cost) {
-  return slices > 0 ? slices + unit_cost : 0;
-}
-__device__ __forceinline__ int64_t warp_sum(int64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
 }
 
 template <int D>
@@ -338,91 +305,12 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int team = warp / TEAM, member = warp % TEAM;
   const int G = p.Hq / p.Hkv, R = G * p.window;
-  const int nrg = (R + S::ROWS - 1) / S::ROWS;
-  const int U = p.Hkv * nrg;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-  // Slices of each window of rows and rows that have any, then of all; up to 32 rows without
-  // leaving the warp.
-  const int per_win = (p.batch + 32 * kWindows - 1) / (32 * kWindows) * 32;
-  const int n_win = (p.batch + per_win - 1) / per_win;
-  int64_t slices = 0, live_rows = 0;
-  int slices_l = 0;  // lane's row of the 32 from `base` on
-  if (p.batch <= 32) {
-    slices_l = row_slices(p, lane, blockIdx.x == 0);
-    slices = warp_sum(slices_l);
-    live_rows = __popc(__ballot_sync(0xffffffffu, slices_l > 0));
-  } else {
-    for (int w = warp; w < n_win; w += kWarps) {
-      int64_t c = 0, r = 0;
-      for (int i = lane; i < per_win; i += 32) {
-        const int n = row_slices(p, w * per_win + i, blockIdx.x == 0);
-        c += n;
-        r += n > 0;
-      }
-      c = warp_sum(c);
-      r = warp_sum(r);
-      if (lane == 0) {
-        s_win[w] = c;
-        s_rows[w] = (int)r;
-      }
-    }
-    __syncthreads();
-    for (int w = lane; w < n_win; w += 32) {
-      slices += s_win[w];
-      live_rows += s_rows[w];
-    }
-    slices = warp_sum(slices);
-    live_rows = warp_sum(live_rows);
-  }
-  // This team's range; consecutive ranges are on different SMs. With no more slices than teams,
-  // one each: there is no one to balance with.
+  // consecutive ranges are on different SMs
   const int worker = team * gridDim.x + blockIdx.x;
-  int64_t workers = (int64_t)gridDim.x * S::TEAMS;
-  const bool few = slices * U <= workers;
-  const int unit_cost = few ? 0 : kUnitCost;
-  const int64_t total = (slices + live_rows * unit_cost) * U;
-  if (few) workers = total;
-  int64_t pos = 0, end = 0;
-  if (worker < workers) {
-    pos = few ? worker : total * worker / workers;
-    end = few ? worker + 1 : total * (worker + 1) / workers;
-  }
-
-  // the row that holds pos: its window, then the 32 rows, then the row
-  int base = 0, row = 0, cost = 0;
-  int64_t at = 0;  // where row base + row begins
-  if (pos < end) {
-    if (p.batch > 32) {
-      int w = 0;
-      for (;; w += 32) {
-        int64_t c =
-            w + lane < n_win ? (s_win[w + lane] + (int64_t)s_rows[w + lane] * unit_cost) * U : 0;
-        const int64_t mine = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t u = __shfl_up_sync(0xffffffffu, c, o);
-          if (lane >= o) c += u;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, at + c <= pos);
-        const int k = __popc(past);  // windows that end at or before pos
-        if (k < 32) {
-          at += __shfl_sync(0xffffffffu, c - mine, k);
-          base = (w + k) * per_win;
-          break;
-        }
-        at += __shfl_sync(0xffffffffu, c, 31);
-      }
-      for (;;) {
-        slices_l = row_slices(p, base + lane, false);
-        const int64_t c = warp_sum(row_cost(slices_l, unit_cost)) * U;
-        if (at + c > pos) break;
-        at += c;
-        base += 32;
-      }
-    }
-    cost = row_cost(__shfl_sync(0xffffffffu, slices_l, 0), unit_cost);
-  }
+  Ranges<kSlice> ranges;
+  ranges.plan(p, S::ROWS, kWarps, worker, (int64_t)gridDim.x * S::TEAMS, kUnitCost, s_win, s_rows,
+              blockIdx.x == 0);
 
   uint8_t* ring = smem + team * (kStages * S::STAGE);
   const uint32_t ring_u = ptx::smem_u32(ring);
@@ -432,40 +320,18 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
   const int put0 = D == 128 ? (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4)
                             : (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
 
-  while (pos < end) {
-    while (at + (int64_t)cost * U <= pos) {
-      at += (int64_t)cost * U;
-      if (++row == 32) {
-        row = 0;
-        base += 32;
-        slices_l = row_slices(p, base + lane, false);
-      }
-      cost = row_cost(__shfl_sync(0xffffffffu, slices_l, row), unit_cost);
-    }
-    // the piece [first, last) of a unit's slices
-    const int b = base + row, n_slices = cost - unit_cost;
-    const int unit = (int)((pos - at) / cost);
-    const int x0 = (int)((pos - at) - (int64_t)unit * cost);
-    const int x1 = end - pos < cost - x0 ? x0 + (int)(end - pos) : cost;
-    const int64_t pos0 = pos, stop = pos + (cost - x0);  // end of the unit
-    pos += x1 - x0;
-    const int first = x0 > unit_cost ? x0 - unit_cost : 0;
-    const int last = x1 > unit_cost ? x1 - unit_cost : 0;
-    if (first == last) continue;  // the range ends before the unit's first slice
-    const int h = unit / nrg, rg = unit - h * nrg;
-
-    // keys that any row of the team sees: a long window's first rows see fewer
+  Piece piece;
+  while (ranges.next(p, piece)) {
+    const int b = piece.b, h = piece.h, rg = piece.rg, first = piece.first, last = piece.last;
     const int n_tok = row_tokens(p, b);
     const int start = p.start[b];
-    const int last_j = (rg * S::ROWS + S::ROWS - 1) / G;
-    const int64_t reach = (int64_t)start + (last_j < n_tok ? last_j + 1 : n_tok);
     const int32_t* table = p.table + (int64_t)b * p.max_pages;
     struct Pending {
       float ks, vs;
       bool present;
     };
     auto page_of = [&](int sl) {
-      return sl < last && (int64_t)sl * kSlice < reach ? table[sl / (kPage / kSlice)] : -1;
+      return sl < last ? table[sl / (kPage / kSlice)] : -1;
     };
     auto issue = [&](int sl, int page, int stage) {
       Pending n = {0.0f, 0.0f, page >= 0 && page < p.n_pages};
@@ -601,7 +467,6 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
     cp_wait<0>();
     team_sync<TEAM>(team);  // the ring is free for the next unit
 
-    const bool whole = first == 0 && last == n_slices;
     const int slot = 2 * worker + (first == 0 ? 1 : 0);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -616,7 +481,7 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
         o[n] = st.o[n][half * 2];
         o[D / 8 + n] = st.o[n][half * 2 + 1];
       }
-      if (whole) {
+      if (piece.whole) {
         const bool live = j < n_tok;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         uint4* dst = reinterpret_cast<uint4*>(
@@ -636,22 +501,10 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
         if (t == 0) ws_ml[to] = make_float2(st.m[half], l);
       }
     }
-    if (first == 0 && member == 0 && lane == 0) {
-      UnitDesc d = {worker, 0};
-      // its last piece is in the first range that ends at or after the unit's end
-      if (!whole)
-        d.pieces = (int)(few ? stop - pos0 : (stop * workers + total - 1) / total - worker);
-      desc[(int64_t)b * U + unit] = d;
-    }
+    if (first == 0 && member == 0 && lane == 0)
+      desc[(int64_t)b * ranges.U + piece.unit] = piece.desc;
   }
-
-  // rows without keys
-  for (int b = warp * gridDim.x + blockIdx.x; b < p.batch; b += gridDim.x * kWarps) {
-    if (row_slices(p, b, false) > 0) continue;
-    T* o = (T*)p.o + (int64_t)b * p.window * p.Hq * D;
-    for (int i = lane; i < p.window * p.Hq * D; i += 32) st_elem(o, i, 0.0f);
-    for (int i = lane; i < U; i += 32) desc[(int64_t)b * U + i] = {0, 0};
-  }
+  ranges.zero_units<T>(p, D, warp * gridDim.x + blockIdx.x, gridDim.x * kWarps, desc);
 }
 
 // Joins the pieces of a unit that was cut: the second slot of the warp that began it, then the
@@ -742,54 +595,53 @@ join_kernel(const CacheAttnParams p, int unit_rows, int piece_rows, int per_row,
 }
 
 // Warps of a team: as many as the unit's query rows fill, up to four (bf16); more rows are cut into
-// groups that read the cache again. fp32 has too many operands for 128 registers.
+// groups that read the cache again. fp32 has too many operands for 168 registers.
 int team_of(kda_dtype dt, int rows) { return dt == KDA_F32 || rows <= 16 ? 1 : (rows <= 32 ? 2 : 4); }
 
-// Workspace: the pieces' sums, their (m, l), then a descriptor per unit (of 16 rows at least). An
-// SM has 8 workers with units of up to 32 rows, or 4 with 64.
-size_t piece_rows_of(int R) { return (size_t)2 * kMaxSms * 8 * (R < 32 ? R : 32); }
+// bf16 calls with at least this many query rows per key/value head go to the tcgen05 kernel: beyond
+// 64 rows the warps' units read and convert the codes again. 64 windows over contexts to 8k, 8
+// key/value heads, d = 128: 80 rows 283 us against 469, 128 rows 295 against 489, 256 rows 385
+// against 938 (d = 64, 80 rows: 223 against 306); one chunk of 512 tokens after 8192: 99 against 245.
+// Only the shortest contexts lose, to the longer start: 64 tokens after 100, 23 us against 17.
+constexpr int kTcMinRows = 65;
 
-template <class T, int D, int TEAM>
-kda_status launch_t(const CacheAttnParams& p, cudaStream_t s) {
-  using S = Shape<T, D, TEAM>;
-  static int sms_of[64] = {};  // SMs of each device, found once
+// SMs used on the current device (0: error, set).
+int sms_here() {
+  static int sms_of[64] = {};
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || dev < 0 || dev >= 64)
-    return set_error(KDA_ERR_CUDA, "kda_cache_attention: no current device");
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    set_error(KDA_ERR_CUDA, "kda_cache_attention: no current device");
+    return 0;
+  }
   if (sms_of[dev] == 0) {
     int sms = 0;
-    e = cudaFuncSetAttribute(attn_kernel<T, D, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             S::SMEM);
-    // the same split of L1 and shared memory for both kernels: no SM is drained to change it
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(join_kernel<T, D, 16, 8>,
-                               cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(join_kernel<T, D, 4, 4>,
-                               cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess)
-      return set_error(KDA_ERR_CUDA, std::string("kda_cache_attention: ") + cudaGetErrorString(e));
+    const cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess || sms < 1) {
+      set_error(KDA_ERR_CUDA, std::string("kda_cache_attention: ") + cudaGetErrorString(e));
+      return 0;
+    }
     sms_of[dev] = sms < kMaxSms ? sms : kMaxSms;
   }
-  const int G = p.Hq / p.Hkv, R = G * p.window, nrg = (R + S::ROWS - 1) / S::ROWS;
-  const int rows = R < S::ROWS ? R : S::ROWS;
-  // no more CTAs than the page table allows slices
-  const int64_t units = (int64_t)p.batch * p.Hkv * nrg;
-  const int64_t most = units * p.max_pages * (kPage / kSlice);
-  const int ctas = most < sms_of[dev] ? (int)most : sms_of[dev];
-  float* ws_o = (float*)p.ws;
-  float2* ws_ml = (float2*)(ws_o + piece_rows_of(R) * D);
-  UnitDesc* desc = (UnitDesc*)(ws_ml + piece_rows_of(R));
-  attn_kernel<T, D, TEAM><<<ctas, S::THREADS, S::SMEM, s>>>(p, rows, ws_o, ws_ml, desc);
-  kda_status st = check_launch("kda_cache_attention");
-  if (st != KDA_OK) return st;
-  // Few units have many pieces each: 16 warps for a row of one. Many units have a few: a warp for a
-  // row, in small CTAs.
-  const bool few = units * rows <= 4 * sms_of[dev];
+  return sms_of[dev];
+}
+
+// Few units have many pieces each: 16 warps for a row of one. Many units have a few: a warp for a
+// row, in small CTAs.
+template <class T, int D>
+kda_status launch_join(const CacheAttnParams& p, int unit_rows, int rows, int64_t units, int sms,
+                       const float* ws_o, const float2* ws_ml, const UnitDesc* desc,
+                       cudaStream_t s) {
+  const bool few = units * rows <= 4 * sms;
+  auto kernel = few ? join_kernel<T, D, 16, 8> : join_kernel<T, D, 4, 4>;
+  static bool set[2][64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && !set[few][dev]) {
+    // the same split of L1 and shared memory for both kernels: no SM is drained to change it
+    cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                         cudaSharedmemCarveoutMaxShared);
+    set[few][dev] = true;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)units, (unsigned)(few ? rows : (rows + 3) / 4));
   cfg.blockDim = dim3(few ? 512 : 128);
@@ -799,21 +651,54 @@ kda_status launch_t(const CacheAttnParams& p, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, few ? join_kernel<T, D, 16, 8> : join_kernel<T, D, 4, 4>, p, S::ROWS,
-                     rows, few ? 16 : 1, (const float*)ws_o, (const float2*)ws_ml,
-                     (const UnitDesc*)desc);
+  cudaLaunchKernelEx(&cfg, kernel, p, unit_rows, rows, few ? 16 : 1, ws_o, ws_ml, desc);
   count_launches(2);
   return check_launch("kda_cache_attention");
 }
 
-template <int D>
-kda_status dispatch(const CacheAttnParams& p, kda_dtype dt, cudaStream_t s) {
-  if (dt == KDA_F32) return launch_t<float, D, 1>(p, s);
-  switch (team_of(dt, p.Hq / p.Hkv * p.window)) {
-    case 1: return launch_t<__nv_bfloat16, D, 1>(p, s);
-    case 2: return launch_t<__nv_bfloat16, D, 2>(p, s);
-    default: return launch_t<__nv_bfloat16, D, 4>(p, s);
+template <class T, int D, int TEAM>
+kda_status launch_main(const CacheAttnParams& p, int ctas, int rows, float* ws_o, float2* ws_ml,
+                       UnitDesc* desc, cudaStream_t s) {
+  using S = Shape<T, D, TEAM>;
+  static bool set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && !set[dev]) {
+    cudaFuncSetAttribute(attn_kernel<T, D, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         S::SMEM);
+    set[dev] = true;
   }
+  attn_kernel<T, D, TEAM><<<ctas, S::THREADS, S::SMEM, s>>>(p, rows, ws_o, ws_ml, desc);
+  return check_launch("kda_cache_attention");
+}
+
+template <class T, int D>
+kda_status launch_t(const CacheAttnParams& p, kda_dtype dt, cudaStream_t s) {
+  const int sms = sms_here();
+  if (sms == 0) return KDA_ERR_CUDA;
+  const int R = p.Hq / p.Hkv * p.window, team = team_of(dt, R);
+  const bool tc = dt == KDA_BF16 && R >= kTcMinRows;
+  const int unit_rows = tc ? kTcRows : 16 * team;
+  const int nrg = (R + unit_rows - 1) / unit_rows, rows = R < unit_rows ? R : unit_rows;
+  // no more CTAs than the page table allows slices
+  const int64_t units = (int64_t)p.batch * p.Hkv * nrg;
+  const int64_t most = units * p.max_pages * (kPage / kSlice);
+  const int ctas = most < sms ? (int)most : sms;
+  float* ws_o = (float*)p.ws;
+  float2* ws_ml = (float2*)(ws_o + piece_rows_of(R) * D);
+  UnitDesc* desc = (UnitDesc*)(ws_ml + piece_rows_of(R));
+  kda_status st;
+  if (tc) {
+    st = launch_attn_tc(p, D, ctas, rows, ws_o, ws_ml, desc, s);
+  } else if constexpr (sizeof(T) == 4) {
+    st = launch_main<T, D, 1>(p, ctas, rows, ws_o, ws_ml, desc, s);
+  } else {
+    st = team == 1   ? launch_main<T, D, 1>(p, ctas, rows, ws_o, ws_ml, desc, s)
+         : team == 2 ? launch_main<T, D, 2>(p, ctas, rows, ws_o, ws_ml, desc, s)
+                     : launch_main<T, D, 4>(p, ctas, rows, ws_o, ws_ml, desc, s);
+  }
+  if (st != KDA_OK) return st;
+  return launch_join<T, D>(p, unit_rows, rows, units, sms, ws_o, ws_ml, desc, s);
 }
 
 }  // namespace
@@ -826,7 +711,8 @@ size_t cache_attn_workspace_bytes(int batch, int window, int Hq, int Hkv, int d)
 }
 
 kda_status launch_cache_attn(const CacheAttnParams& p, kda_dtype dt, int d, cudaStream_t s) {
-  return d == 128 ? dispatch<128>(p, dt, s) : dispatch<64>(p, dt, s);
+  if (dt == KDA_F32) return d == 128 ? launch_t<float, 128>(p, dt, s) : launch_t<float, 64>(p, dt, s);
+  return d == 128 ? launch_t<__nv_bfloat16, 128>(p, dt, s) : launch_t<__nv_bfloat16, 64>(p, dt, s);
 }
 
 }  // namespace kda
