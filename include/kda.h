@@ -506,9 +506,11 @@ KDA_API kda_status kda_cache_read(kda_dtype dt, int n_seqs, int total_tokens,
  *               not be initialised.
  *   window 1 .. 65536 (0 is a no-op); Hq a multiple of Hkv; batch * Hkv at most 2^24, batch *
  *   window * Hq at most 2^30; max_pages at most 2^24.
- * The cache is read once per 64 query rows of a key/value head (16 in fp32), a query row being one
- * token of one of the head's query heads: once for a decoded token or a verify window, many times
- * (from L2 mostly) for a prompt's chunk.
+ * The cache is read once for up to 64 query rows of a key/value head, a query row being one token of
+ * one of the head's query heads; for more, once per 256 (bf16; per 16 in fp32): once for a decoded
+ * token or a verify window, several times (from L2 mostly) for a prompt's chunk.
+ *   status      optional device word (KDA_STATUS_BAD_PAGE; KDA_STATUS_TIMEOUT if a wait inside the
+ *               kernel for more than 64 rows gave up: o is then undefined).
  * Scores, softmax statistics and sums are fp32. With bf16 queries the probabilities enter the
  * second product rounded to 11 bits; with fp32 queries, queries and probabilities are carried in
  * two 11-bit parts.

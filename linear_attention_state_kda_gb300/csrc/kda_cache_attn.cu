@@ -600,8 +600,8 @@ int team_of(kda_dtype dt, int rows) { return dt == KDA_F32 || rows <= 16 ? 1 : (
 
 // bf16 calls with at least this many query rows per key/value head go to the tcgen05 kernel: beyond
 // 64 rows the warps' units read and convert the codes again. 64 windows over contexts to 8k, 8
-// key/value heads, d = 128: 80 rows 283 us against 469, 128 rows 295 against 489, 256 rows 385
-// against 938 (d = 64, 80 rows: 223 against 306); one chunk of 512 tokens after 8192: 99 against 245.
+// key/value heads, d = 128: 80 rows 279 us against 469, 128 rows 296 against 489, 256 rows 363
+// against 938 (d = 64, 80 rows: 193 against 306); one chunk of 512 tokens after 8192: 93 against 245.
 // Only the shortest contexts lose, to the longer start: 64 tokens after 100, 23 us against 17.
 constexpr int kTcMinRows = 65;
 

@@ -4,6 +4,9 @@
 // The key slices that the row groups see are laid end to end (row, head, row group, slice) and cut
 // into equal ranges, one per worker. A "unit" is one (row, head, row group); a worker's "piece" is the part of a unit
 // in its range. Beginning and ending a unit counts as unit_cost slices more.
+//
+// The loops here run a few times per CTA and are kept rolled: unrolled, they were 30 KB of each
+// kernel's code, more than the loops over the keys, and pushed those out of the instruction cache.
 #pragma once
 
 #include "kda_internal.cuh"
@@ -75,6 +78,7 @@ struct Ranges {
     const int start = p.start[b];
     if (flag && p.status && (int64_t)start + n > (int64_t)p.max_pages * kPage)
       atomicOr(p.status, KDA_STATUS_BAD_PAGE);
+#pragma unroll 1
     for (int rg = 0; rg < nrg; ++rg) {
       const int c = group_slices(p, start, n, rg);
       s.slices += c;
@@ -107,9 +111,11 @@ struct Ranges {
         sums_l = row_sums(p, lane, flag);
       } else {
         // a warp sums a row, its lanes the groups
+#pragma unroll 1
         for (int b = warp; b < p.batch; b += n_warps) {
           const int n = row_tokens(p, b), start = p.start[b];
           int64_t c = 0, u = 0;
+#pragma unroll 1
           for (int rg = lane; rg < nrg; rg += 32) {
             const int x = group_slices(p, start, n, rg);
             c += x;
@@ -130,8 +136,10 @@ struct Ranges {
       slices = warp_sum(sums_l.slices);
       units = warp_sum(sums_l.units);
     } else {
+#pragma unroll 1
       for (int w = warp; w < n_win; w += n_warps) {
         int64_t c = 0, u = 0;
+#pragma unroll 1
         for (int i = lane; i < per_win; i += 32) {
           const Sums x = row_sums(p, w * per_win + i, flag);
           c += x.slices;
@@ -145,6 +153,7 @@ struct Ranges {
         }
       }
       __syncthreads();
+#pragma unroll 1
       for (int w = lane; w < n_win; w += 32) {
         slices += s_win[w];
         units += s_rows[w];
@@ -169,6 +178,7 @@ struct Ranges {
     if (pos >= end) return;
     // the row that holds pos: its window, then the 32 rows
     if (p.batch > 32) {
+#pragma unroll 1
       for (int w = 0;; w += 32) {
         int64_t c = w + lane < n_win
                         ? (s_win[w + lane] + (int64_t)s_rows[w + lane] * unit_cost) * p.Hkv
@@ -188,6 +198,7 @@ struct Ranges {
         }
         at += __shfl_sync(0xffffffffu, c, 31);
       }
+#pragma unroll 1
       for (;;) {
         cost_l = cost_of(row_sums(p, base + lane, false));
         const int64_t c = warp_sum(cost_l) * p.Hkv;
@@ -201,7 +212,9 @@ struct Ranges {
 
   __device__ __forceinline__ bool next(const CacheAttnParams& p, Piece& x) {
     const int lane = threadIdx.x & 31;
+#pragma unroll 1
     while (pos < end) {
+#pragma unroll 1
       while (at + cost * p.Hkv <= pos) {
         at += cost * p.Hkv;
         if (++row == 32) {
@@ -218,6 +231,7 @@ struct Ranges {
       int c = (int)cost;  // of the unit
       if (nrg > 1) {
         const int n = row_tokens(p, x.b), start = p.start[x.b];
+#pragma unroll 1
         for (; x.rg < nrg; x.rg += 32) {
           const int s = group_slices(p, start, n, x.rg + lane);
           const int mine = s > 0 ? s + unit_cost : 0;
@@ -264,16 +278,19 @@ struct Ranges {
     const int lane = threadIdx.x & 31;
     const int64_t units = (int64_t)p.batch * U;
     const int chunks = d * (int)sizeof(T) / 16;
+#pragma unroll 1
     for (int64_t i0 = (int64_t)first * 32; i0 < units; i0 += (int64_t)step * 32) {
       const int64_t i = i0 + lane;
       const int b = i < units ? (int)(i / U) : 0, unit = (int)(i - (int64_t)b * U);
       const bool dead = i < units && group_slices(p, p.start[b], row_tokens(p, b), unit % nrg) == 0;
       if (dead) desc[i] = {0, 0};
+#pragma unroll 1
       for (unsigned left = __ballot_sync(0xffffffffu, dead); left; left &= left - 1) {
         const int from = __ffs(left) - 1;
         const int zb = __shfl_sync(0xffffffffu, b, from), zu = __shfl_sync(0xffffffffu, unit, from);
         const int h = zu / nrg, r0 = (zu - h * nrg) * unit_rows;
         const int rows = min(unit_rows, G * p.window - r0);
+#pragma unroll 1
         for (int k = lane; k < rows * chunks; k += 32) {
           const int gr = r0 + k / chunks, j = gr / G;
           uint4* o = reinterpret_cast<uint4*>(

@@ -21,10 +21,20 @@
 //                 one thread, so these warps need no barrier among themselves
 //   warps 12-15   load the codes of a tile into registers while the tile before is in work, and
 //                 widen them into two stages of K and of V (128-byte swizzle)
-// The issuing warp stays converged and its operands are known to be the same in all lanes, with one
-// elected lane at the instruction: issued from a branch of lane 0, each MMA took four times as long
-// (530 TFLOP/s against 885 on 4 chunks of 1024 tokens after 16384, 32/8 heads).
-// Measured there: 994-1012 TFLOP/s; 320 with warp MMAs.
+//
+// What bounds it: the products take 2048 cycles per 256 x 128 scores, the exponentials as long at
+// their full rate, and waits of some 150 cycles lie between a row tile's scores, softmax and values;
+// measured 3.9 thousand. 4 chunks of 1024 tokens after 16384, 32/8 heads: 633 us, 1146 TFLOP/s (59%
+// of the measured bf16 rate); 321 TFLOP/s with warp MMAs. What it took, in TFLOP/s there:
+//   530 -> 885   the issuing warp stays converged and its operands are known to be the same in all
+//                lanes, with one lane elected at the instruction: from a branch of lane 0 each MMA
+//                took four times as long to issue
+//   885 -> 994   one rolled loop of steps for the issuing warp
+//   994 -> 1068  less code: the waits count tries, loops that run once a piece are rolled (the
+//                instruction cache missed on a third of its requests)
+//  1068 -> 1146  barriers that are due together are looked at together
+// Handing P over a page at a time gave 509 against 477 TFLOP/s where only one row tile has rows, and
+// 1090 against 1146 here; not kept.
 // Tensor memory: 128 columns of S and d of O per row tile.
 #include "kda_cache_attn.cuh"
 #include "kda_fp8.cuh"
@@ -173,18 +183,19 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);  // (known to be the same in all lanes)
   const uint32_t tmem_o = tmem + 2 * kTile;
 
-  // A wait that gives up records it and makes every role leave.
-  auto gave_up = [&]() {
+  // A wait of a whole warp (all lanes get the same answer). One that gives up records it, and the
+  // warp leaves; so do those that wait for it.
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, ptx::mbar_wait_tries(bar, parity))) return true;
     if (p.status) atomicOr(p.status, KDA_STATUS_TIMEOUT);
     *(volatile int*)&s_abort = 1;
+    return false;
   };
-  // For a whole warp: all lanes get the same answer.
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    const bool r = ptx::mbar_wait_lean_or(bar, parity, &s_abort);
-    if (!r) gave_up();
-    return (bool)__all_sync(0xffffffffu, r);
+  // Of two barriers, which are looked at together.
+  auto wait2 = [&](uint64_t* a, uint32_t parity_a, uint64_t* b, uint32_t parity_b) {
+    const bool ra = ptx::mbar_try_wait(a, parity_a), rb = ptx::mbar_try_wait(b, parity_b);
+    return __all_sync(0xffffffffu, ra && rb) || (wait(a, parity_a) && wait(b, parity_b));
   };
-
   // Positions that the first row of a piece's unit sees.
   auto unit_first_sees = [&](const Work& x) {
     return (int64_t)p.start[x.b] + x.rg * kTcRows / G + 1;
@@ -226,8 +237,7 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
           const int m = n + i, buf = m & 1;
           const bool final = g == halves - 1;  // frees the stages
           if (i >= 0) {
-            if (g == 0) ok = wait(&bars.v_full[buf], (m >> 1) & 1);
-            ok = ok && wait(&bars.p_full[g], parity >> g & 1);
+            ok = wait2(&bars.v_full[buf], (m >> 1) & 1, &bars.p_full[g], parity >> g & 1);
             if (!ok) break;
             ptx::tc_fence_after();
             if (ptx::elect_one()) {
@@ -242,8 +252,9 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
             __syncwarp();
           }
           if (i + 1 < tiles) {
-            if (g == 0) ok = wait(&bars.k_full[buf ^ 1], ((m + 1) >> 1) & 1);
-            if (i >= 0) ok = ok && wait(&bars.o_full[g], parity >> g & 1);
+            // (before the first tile the last product of the piece before is looked at: complete)
+            ok = wait2(&bars.k_full[buf ^ 1], ((m + 1) >> 1) & 1, &bars.o_full[g],
+                       (parity >> g & 1) ^ (i < 0));
             if (!ok) break;
             ptx::tc_fence_after();
             if (ptx::elect_one()) {
@@ -311,14 +322,14 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
       float rowf;
       {
         const uint4* src = reinterpret_cast<const uint4*>((const __nv_bfloat16*)p.q + at_row * D);
-        uint4 raw[D / 8];
+        // (rolled: this is run once a piece, and what it takes of the instruction cache is fetched
+        // each time)
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) raw[i] = live ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
+#pragma unroll 8
         for (int i = 0; i < D / 8; ++i) {
           float q[8];
-          Vec16<__nv_bfloat16>::unpack(raw[i], q);
+          Vec16<__nv_bfloat16>::unpack(live ? src[i] : zero, q);
 #pragma unroll
           for (int u = 0; u < 8; ++u) top = max(top, finite_abs_bits(q[u]));
         }
@@ -328,10 +339,10 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
         rowf = p.scale * 1.44269504f * pow2f(-e);
         const uint32_t dst =
             ptx::smem_u32(smem) + M::Q + g * M::QTILE + (r >> 3) * 1024 + (r & 7) * 128;
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < D / 8; ++i) {
           float q[8];
-          Vec16<__nv_bfloat16>::unpack(raw[i], q);
+          Vec16<__nv_bfloat16>::unpack(live ? src[i] : zero, q);
           st_shared(dst + (i >> 3) * (128 * 128) + (((i & 7) ^ (r & 7)) << 4),
                     make_uint4(pack_f16(q[0] * up, q[1] * up), pack_f16(q[2] * up, q[3] * up),
                                pack_f16(q[4] * up, q[5] * up), pack_f16(q[6] * up, q[7] * up)));
@@ -423,7 +434,7 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
           m = most;
           l *= corr;
           if (i > piece.first) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               float o[32];
               ptx::tmem_ld32(t_o + c * 32, o);
@@ -480,12 +491,12 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
       const int slot = 2 * (int)blockIdx.x + (piece.first == 0 ? 1 : 0);
       const int64_t to = (int64_t)slot * piece_rows + g * 128 + r;
       const float inv = live && l != 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float o[32];
         __syncwarp();
         ptx::tmem_ld32(t_o + c * 32, o);
-        const uint32_t bad = (&nan.x)[c];
+        const uint32_t bad = c < 2 ? (c == 0 ? nan.x : nan.y) : (c == 2 ? nan.z : nan.w);
         if (bad) {
 #pragma unroll
           for (int k = 0; k < 32; ++k)
@@ -510,14 +521,14 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
     // -------------------------------------------------------------------- K and V to f16
     regs_give<88>();
     const int tid = threadIdx.x - 384, w = warp - 12;
-    // chunk tid + 128 i of a tile: channels 16 c .. 16 c + 15 of key key0 + i (128 / CPK)
-    const int key0 = tid / CPK, c = tid % CPK;
-    // where a chunk's two 16-byte pieces go (128 / CPK is a multiple of 8, so every i has the same
-    // rotation of the row's pieces)
-    const bool odd = c >> 2;
+    // Channels 16 c .. 16 c + 15 of keys key0 + i (128 / CPK). Eight lanes take four chunks of two
+    // keys, so that the two 16-byte pieces of their f16 go to eight different places of a row.
+    const int c = D == 128 ? (tid & 3) + (tid >> 1 & 4) : tid & 3;
+    const int key0 = D == 128 ? (tid >> 2 & 1) + (tid >> 4) * 2 : tid >> 2;
+    // (128 / CPK is a multiple of 8: every i has the same rotation of the row's pieces)
     const uint32_t row0 = (c >> 2) * (kTile * 128) + (key0 >> 3) * 1024 + (key0 & 7) * 128;
-    const uint32_t put0 = row0 + (((2 * (c & 3) + odd) ^ (key0 & 7)) << 4);
-    const uint32_t put1 = row0 + (((2 * (c & 3) + !odd) ^ (key0 & 7)) << 4);
+    const uint32_t put0 = row0 + (((2 * (c & 3)) ^ (key0 & 7)) << 4);
+    const uint32_t put1 = row0 + (((2 * (c & 3) + 1) ^ (key0 & 7)) << 4);
     const uint32_t tiles_at = ptx::smem_u32(smem);
     bool ok = true;
     while (ok && take()) {
@@ -543,7 +554,7 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
           raw[i] = make_uint4(0u, 0u, 0u, 0u);
           if (pg >= 0 && pg < p.n_pages)
             raw[i] = *reinterpret_cast<const uint4*>(codes + ((int64_t)pg * p.Hkv + piece.h) * (kPage * D) +
-                                                     (tid + 128 * (i % (NL / 2))) * 16);
+                                                     (key0 * CPK + c + 128 * (i % (NL / 2))) * 16);
         }
       };
       Scales next;
@@ -561,17 +572,15 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
           }
         }
       };
-      // f16 of chunk i into a tile: two 16-byte pieces, in the order that keeps eight lanes on
-      // different banks
+      // f16 of chunk i into a tile
       auto put = [&](uint32_t tile, int i, const uint4& x) {
-        uint32_t f[8];
-        f16x4_from_e4m3(x.x, f[0], f[1]);
-        f16x4_from_e4m3(x.y, f[2], f[3]);
-        f16x4_from_e4m3(x.z, f[4], f[5]);
-        f16x4_from_e4m3(x.w, f[6], f[7]);
-        const uint4 a = make_uint4(f[0], f[1], f[2], f[3]), b = make_uint4(f[4], f[5], f[6], f[7]);
-        st_shared(tile + put0 + i * (128 / CPK) * 128, odd ? b : a);
-        st_shared(tile + put1 + i * (128 / CPK) * 128, odd ? a : b);
+        uint4 a, b;
+        f16x4_from_e4m3(x.x, a.x, a.y);
+        f16x4_from_e4m3(x.y, a.z, a.w);
+        f16x4_from_e4m3(x.z, b.x, b.y);
+        f16x4_from_e4m3(x.w, b.z, b.w);
+        st_shared(tile + put0 + i * (128 / CPK) * 128, a);
+        st_shared(tile + put1 + i * (128 / CPK) * 128, b);
       };
       look(piece.first);
       load(kraw, p.kc);

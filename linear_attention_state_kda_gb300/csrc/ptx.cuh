@@ -54,18 +54,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Whether the phase has completed, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // try_wait without acquire semantics (for completions of tcgen05 work, which the caller
 // orders with tcgen05.fence::after_thread_sync), so that it does not wait for this thread's
 // outstanding global loads.
@@ -114,19 +102,13 @@ __device__ __forceinline__ bool mbar_wait_or(uint64_t* bar, uint32_t parity, con
     if (globaltimer_ns() - t0 > limit_ns) return false;
   }
 }
-// mbar_wait_or for waits on a critical path: the clock and the abort word are read once in 64 tries.
-__device__ __forceinline__ bool mbar_wait_lean_or(uint64_t* bar, uint32_t parity, const int* abort,
-                                                  uint64_t limit_ns = 2000000000ull) {
-  uint64_t t0 = 0;
+// The same with a limit on the tries, in a few instructions: for kernels with many waits, whose
+// code must stay within the instruction cache. Some 30 ms at the least.
+__device__ __forceinline__ bool mbar_wait_tries(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
-  for (uint32_t i = 1;; ++i) {
+  for (uint32_t i = 0; i < (1u << 20); ++i)
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 0) {
-      const uint64_t t = globaltimer_ns();
-      if (t0 == 0) t0 = t;
-      if (*(const volatile int*)abort || t - t0 > limit_ns) return false;
-    }
-  }
+  return false;
 }
 __device__ __forceinline__ bool mbar_wait_relaxed_or(uint64_t* bar, uint32_t parity,
                                                      const int* abort,
