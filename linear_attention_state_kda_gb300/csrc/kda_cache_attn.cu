@@ -508,33 +508,38 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
 }
 
 // Joins the pieces of a unit that was cut: the second slot of the warp that began it, then the
-// first slots of the next ones. `per_row` warps of the CTA sum every per_row-th piece of a row
-// relative to their own largest M, and their sums are added in order.
-template <class T, int D, int kJoinWarps, int kBatch>
+// first slots of the next ones. kPerRow warps of the CTA sum every kPerRow-th piece of a row relative
+// to their own largest M, and their sums are added in order; one warp writes its row by itself.
+// blockIdx.x is the unit, or, with `cut`, the worker that began it: of many units of a prompt's chunk
+// at most one per worker is cut (4 chunks of 1024 tokens after 16384 have 512 units on 152 workers:
+// 616 us a call against 633; without a barrier for rows of one warp 604).
+template <class T, int D, int kJoinWarps, int kPerRow, int kBatch>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-join_kernel(const CacheAttnParams p, int unit_rows, int piece_rows, int per_row, const float* ws_o,
-            const float2* ws_ml, const UnitDesc* desc) {
+join_kernel(const CacheAttnParams p, int unit_rows, int piece_rows, const float* ws_o,
+            const float2* ws_ml, const UnitDesc* desc, const int32_t* cut) {
   constexpr int N = D / 32;
-  __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps], s_m[kJoinWarps];
   const int G = p.Hq / p.Hkv, R = G * p.window;
   const int nrg = (R + unit_rows - 1) / unit_rows, U = p.Hkv * nrg;
-  const int b = blockIdx.x / U, unit = blockIdx.x - b * U, h = unit / nrg, rg = unit - h * nrg;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % per_row;
-  const int rows = kJoinWarps / per_row;
-  const int r = blockIdx.y * rows + warp / per_row, gr = rg * unit_rows + r;
-  const bool mine = r < unit_rows && gr < R;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % kPerRow;
+  constexpr int kRows = kJoinWarps / kPerRow;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const UnitDesc d = desc[blockIdx.x];
+  const int at_unit = cut ? cut[blockIdx.x] : (int)blockIdx.x;
+  if (at_unit < 0) return;
+  const UnitDesc d = desc[at_unit];
+  const int b = at_unit / U, unit = at_unit - b * U, h = unit / nrg, rg = unit - h * nrg;
+  const int n_tok = row_tokens(p, b);
   if (d.pieces == 0) return;
+  const int r = blockIdx.y * kRows + warp / kPerRow, gr = rg * unit_rows + r;
+  const bool mine = r < unit_rows && gr < R;
   float o[N], l = 0.0f, m = -INFINITY;
 #pragma unroll
   for (int c = 0; c < N; ++c) o[c] = 0.0f;
-  for (int i0 = sub; mine && i0 < d.pieces; i0 += per_row * kBatch) {
+  for (int i0 = sub; mine && i0 < d.pieces; i0 += kPerRow * kBatch) {
     float2 ml[kBatch];
     float x[kBatch][N];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + k * per_row;
+      const int i = i0 + k * kPerRow;
       ml[k] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
       for (int c = 0; c < N; ++c) x[k][c] = 0.0f;
@@ -568,29 +573,39 @@ join_kernel(const CacheAttnParams p, int unit_rows, int piece_rows, int per_row,
       for (int c = 0; c < N; ++c) o[c] = fmaf(f, x[k][c], o[c]);
     }
   }
+  if constexpr (kPerRow == 1) {
+    const int j = gr / G;
+    if (!mine) return;
+    const bool live = j < n_tok && l != 0.0f;
+    T* dst = (T*)p.o + ((int64_t)(b * p.window + j) * p.Hq + h * G + (gr - j * G)) * D;
 #pragma unroll
-  for (int c = 0; c < N; ++c) s_o[warp][lane * N + c] = o[c];
-  if (lane == 0) {
-    s_l[warp] = l;
-    s_m[warp] = m;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < rows * D; i += kJoinWarps * 32) {
-    const int rr = i / D, c = i - rr * D;
-    const int gq = rg * unit_rows + blockIdx.y * rows + rr, j = gq / G;
-    if (blockIdx.y * rows + rr >= unit_rows || gq >= R) continue;
-    float top = -INFINITY;
-    for (int w = 0; w < per_row; ++w) top = fmaxf(top, s_m[rr * per_row + w]);
-    const float mu = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f, ls = 0.0f;
-    for (int w = 0; w < per_row; ++w) {
-      const float f = ptx::ex2_approx(s_m[rr * per_row + w] - mu);
-      sum = fmaf(f, s_o[rr * per_row + w][c], sum);
-      ls = fmaf(f, s_l[rr * per_row + w], ls);
+    for (int c = 0; c < N; ++c) st_elem(dst, lane * N + c, live ? o[c] / l : 0.0f);
+  } else {
+    __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps], s_m[kJoinWarps];
+#pragma unroll
+    for (int c = 0; c < N; ++c) s_o[warp][lane * N + c] = o[c];
+    if (lane == 0) {
+      s_l[warp] = l;
+      s_m[warp] = m;
     }
-    const bool live = j < row_tokens(p, b) && ls != 0.0f;
-    T* dst = (T*)p.o + ((int64_t)(b * p.window + j) * p.Hq + h * G + (gq - j * G)) * D;
-    st_elem(dst, c, live ? sum / ls : 0.0f);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kRows * D; i += kJoinWarps * 32) {
+      const int rr = i / D, c = i - rr * D;
+      const int gq = rg * unit_rows + blockIdx.y * kRows + rr, j = gq / G;
+      if (blockIdx.y * kRows + rr >= unit_rows || gq >= R) continue;
+      float top = -INFINITY;
+      for (int w = 0; w < kPerRow; ++w) top = fmaxf(top, s_m[rr * kPerRow + w]);
+      const float mu = top == -INFINITY ? 0.0f : top;
+      float sum = 0.0f, ls = 0.0f;
+      for (int w = 0; w < kPerRow; ++w) {
+        const float f = ptx::ex2_approx(s_m[rr * kPerRow + w] - mu);
+        sum = fmaf(f, s_o[rr * kPerRow + w][c], sum);
+        ls = fmaf(f, s_l[rr * kPerRow + w], ls);
+      }
+      const bool live = j < n_tok && ls != 0.0f;
+      T* dst = (T*)p.o + ((int64_t)(b * p.window + j) * p.Hq + h * G + (gq - j * G)) * D;
+      st_elem(dst, c, live ? sum / ls : 0.0f);
+    }
   }
 }
 
@@ -600,9 +615,9 @@ int team_of(kda_dtype dt, int rows) { return dt == KDA_F32 || rows <= 16 ? 1 : (
 
 // bf16 calls with at least this many query rows per key/value head go to the tcgen05 kernel: beyond
 // 64 rows the warps' units read and convert the codes again. 64 windows over contexts to 8k, 8
-// key/value heads, d = 128: 80 rows 279 us against 469, 128 rows 296 against 489, 256 rows 363
-// against 938 (d = 64, 80 rows: 193 against 306); one chunk of 512 tokens after 8192: 93 against 245.
-// Only the shortest contexts lose, to the longer start: 64 tokens after 100, 23 us against 17.
+// key/value heads, d = 128: 80 rows 270 us against 469, 128 rows 281 against 489, 256 rows 334
+// against 938 (d = 64, 80 rows: 186 against 306); one chunk of 512 tokens after 8192: 85 against 245.
+// Only the shortest contexts lose, to the longer start: 64 tokens after 100, 21 us against 17.
 constexpr int kTcMinRows = 65;
 
 // SMs used on the current device (0: error, set).
@@ -628,11 +643,13 @@ int sms_here() {
 // Few units have many pieces each: 16 warps for a row of one. Many units have a few: a warp for a
 // row, in small CTAs.
 template <class T, int D>
-kda_status launch_join(const CacheAttnParams& p, int unit_rows, int rows, int64_t units, int sms,
-                       const float* ws_o, const float2* ws_ml, const UnitDesc* desc,
-                       cudaStream_t s) {
+kda_status launch_join(const CacheAttnParams& p, int unit_rows, int rows, int64_t units, int workers,
+                       int sms, const float* ws_o, const float2* ws_ml, const UnitDesc* desc,
+                       const int32_t* cut, cudaStream_t s) {
+  if (cut && units > workers) units = workers;
+  else cut = nullptr;
   const bool few = units * rows <= 4 * sms;
-  auto kernel = few ? join_kernel<T, D, 16, 8> : join_kernel<T, D, 4, 4>;
+  auto kernel = few ? join_kernel<T, D, 16, 16, 8> : join_kernel<T, D, 4, 1, 4>;
   static bool set[2][64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -651,7 +668,7 @@ kda_status launch_join(const CacheAttnParams& p, int unit_rows, int rows, int64_
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kernel, p, unit_rows, rows, few ? 16 : 1, ws_o, ws_ml, desc);
+  cudaLaunchKernelEx(&cfg, kernel, p, unit_rows, rows, ws_o, ws_ml, desc, cut);
   count_launches(2);
   return check_launch("kda_cache_attention");
 }
@@ -687,9 +704,11 @@ kda_status launch_t(const CacheAttnParams& p, kda_dtype dt, cudaStream_t s) {
   float* ws_o = (float*)p.ws;
   float2* ws_ml = (float2*)(ws_o + piece_rows_of(R) * D);
   UnitDesc* desc = (UnitDesc*)(ws_ml + piece_rows_of(R));
+  int32_t* cut = nullptr;
   kda_status st;
   if (tc) {
-    st = launch_attn_tc(p, D, ctas, rows, ws_o, ws_ml, desc, s);
+    cut = (int32_t*)(desc + units);
+    st = launch_attn_tc(p, D, ctas, rows, ws_o, ws_ml, desc, cut, s);
   } else if constexpr (sizeof(T) == 4) {
     st = launch_main<T, D, 1>(p, ctas, rows, ws_o, ws_ml, desc, s);
   } else {
@@ -698,7 +717,7 @@ kda_status launch_t(const CacheAttnParams& p, kda_dtype dt, cudaStream_t s) {
                      : launch_main<T, D, 4>(p, ctas, rows, ws_o, ws_ml, desc, s);
   }
   if (st != KDA_OK) return st;
-  return launch_join<T, D>(p, unit_rows, rows, units, sms, ws_o, ws_ml, desc, s);
+  return launch_join<T, D>(p, unit_rows, rows, units, ctas, sms, ws_o, ws_ml, desc, cut, s);
 }
 
 }  // namespace
@@ -707,7 +726,7 @@ size_t cache_attn_workspace_bytes(int batch, int window, int Hq, int Hkv, int d)
   const int R = Hq / Hkv * window;
   const size_t units = (size_t)batch * Hkv * ((R + 15) / 16);
   return piece_rows_of(R) * (d * sizeof(float) + sizeof(float2)) +
-         (sizeof(UnitDesc) * units + 255) / 256 * 256;
+         (sizeof(UnitDesc) * units + sizeof(int32_t) * kMaxSms + 255) / 256 * 256;
 }
 
 kda_status launch_cache_attn(const CacheAttnParams& p, kda_dtype dt, int d, cudaStream_t s) {

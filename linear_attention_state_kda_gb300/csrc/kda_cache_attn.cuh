@@ -302,15 +302,15 @@ struct Ranges {
   }
 };
 
-// Workspace: the pieces' sums, their (M, l), then a descriptor per unit (of 16 rows at least). An
-// SM has up to 8 workers with units of up to 32 rows, or 4 with 64, or one with 256.
+// Workspace: the pieces' sums, their (M, l), then a descriptor per unit (of 16 rows at least) and, for
+// units of 256 rows, the unit that each worker began and did not end (-1: none). An SM has up to 8 workers with units of up to 32 rows, or 4 with 64, or one with 256.
 inline size_t piece_rows_of(int R) { return (size_t)2 * kMaxSms * 8 * (R < 32 ? R : 32); }
 
 // The tcgen05 kernel for bf16 queries: rows of its units, and its launch over the parts of the
 // workspace.
 constexpr int kTcRows = 256;
 kda_status launch_attn_tc(const CacheAttnParams& p, int d, int ctas, int piece_rows, float* ws_o,
-                          float2* ws_ml, UnitDesc* desc, cudaStream_t s);
+                          float2* ws_ml, UnitDesc* desc, int32_t* cut, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace kda

@@ -24,7 +24,7 @@
 //
 // What bounds it: the products take 2048 cycles per 256 x 128 scores, the exponentials as long at
 // their full rate, and waits of some 150 cycles lie between a row tile's scores, softmax and values;
-// measured 3.9 thousand. 4 chunks of 1024 tokens after 16384, 32/8 heads: 633 us, 1146 TFLOP/s (59%
+// measured 3.9 thousand. 4 chunks of 1024 tokens after 16384, 32/8 heads: 604 us, 1200 TFLOP/s (62%
 // of the measured bf16 rate); 321 TFLOP/s with warp MMAs. What it took, in TFLOP/s there:
 //   530 -> 885   the issuing warp stays converged and its operands are known to be the same in all
 //                lanes, with one lane elected at the instruction: from a branch of lane 0 each MMA
@@ -33,6 +33,7 @@
 //   994 -> 1068  less code: the waits count tries, loops that run once a piece are rolled (the
 //                instruction cache missed on a third of its requests)
 //  1068 -> 1146  barriers that are due together are looked at together
+//  1146 -> 1200  the join of the units that were cut (join_kernel)
 // Handing P over a page at a time gave 509 against 477 TFLOP/s where only one row tile has rows, and
 // 1090 against 1146 here; not kept.
 // Tensor memory: 128 columns of S and d of O per row tile.
@@ -129,7 +130,8 @@ __device__ __forceinline__ void tmem_loaded(uint32_t* r, int n) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml, UnitDesc* desc) {
+attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml, UnitDesc* desc,
+               int32_t* cut) {
   using M = Smem<D>;
   constexpr int CPK = D / 16;            // 16-code chunks of a key
   constexpr int NL = kTile * CPK / 128;  // chunks of a tile that a converter thread takes
@@ -287,10 +289,15 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
     } else if (warp == 3) {
       Piece x = {};
       bool ok = true;
+      int begun = -1;
       for (bool more = true; more; ++taken) {
         more = ranges.next(p, x);
         if (!more) x.first = x.last = 0;
-        else if (x.first == 0 && lane == 0) desc[(int64_t)x.b * ranges.U + x.unit] = x.desc;
+        else if (x.first == 0) {
+          const int at = x.b * ranges.U + x.unit;
+          if (lane == 0) desc[at] = x.desc;
+          if (!x.whole) begun = at;
+        }
         // (descriptors are written to the end also when the other roles have left)
         const uint32_t slot = taken % kPieces;
         ok = ok && wait(&bars.piece_empty[slot], ((taken / kPieces) & 1) ^ 1);
@@ -299,6 +306,7 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
           ptx::mbar_arrive(&bars.piece_full[slot]);
         }
       }
+      if (lane == 0) cut[blockIdx.x] = begun;
     }
   } else if (warp < 12) {
     // -------------------------------------------------------------------- softmax
@@ -651,7 +659,7 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
 
 template <int D>
 kda_status launch_d(const CacheAttnParams& p, int ctas, int piece_rows, float* ws_o, float2* ws_ml,
-                    UnitDesc* desc, cudaStream_t s) {
+                    UnitDesc* desc, int32_t* cut, cudaStream_t s) {
   constexpr int bytes = Smem<D>::BYTES + 1024;
   static bool set[64] = {};
   int dev = 0;
@@ -660,7 +668,7 @@ kda_status launch_d(const CacheAttnParams& p, int ctas, int piece_rows, float* w
     cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     set[dev] = true;
   }
-  attn_tc_kernel<D><<<ctas, kThreads, bytes, s>>>(p, piece_rows, ws_o, ws_ml, desc);
+  attn_tc_kernel<D><<<ctas, kThreads, bytes, s>>>(p, piece_rows, ws_o, ws_ml, desc, cut);
   return check_launch("kda_cache_attention");
 }
 
@@ -669,9 +677,9 @@ kda_status launch_d(const CacheAttnParams& p, int ctas, int piece_rows, float* w
 namespace attn {
 
 kda_status launch_attn_tc(const CacheAttnParams& p, int d, int ctas, int piece_rows, float* ws_o,
-                          float2* ws_ml, UnitDesc* desc, cudaStream_t s) {
-  return d == 128 ? launch_d<128>(p, ctas, piece_rows, ws_o, ws_ml, desc, s)
-                  : launch_d<64>(p, ctas, piece_rows, ws_o, ws_ml, desc, s);
+                          float2* ws_ml, UnitDesc* desc, int32_t* cut, cudaStream_t s) {
+  return d == 128 ? launch_d<128>(p, ctas, piece_rows, ws_o, ws_ml, desc, cut, s)
+                  : launch_d<64>(p, ctas, piece_rows, ws_o, ws_ml, desc, cut, s);
 }
 
 }  // namespace attn
