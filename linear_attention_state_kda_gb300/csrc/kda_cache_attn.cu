@@ -159,24 +159,27 @@ __device__ __forceinline__ void slice_step(
   const int ve = (int)((__float_as_uint(vs) >> 23) & 255u) - 127;
   const float vexp = (float)ve, vref = (float)(ve < kMinScaleExp ? kMinScaleExp : ve);
   const float vinv = __uint_as_float((uint32_t)(127 - ve) << 23);  // 2^-e
+  // s becomes log2 P relative to the row's M (0 for one without keys so far)
   bool over = false;
-  float top[2];
+  float top[2], c[2];
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const float f = rowf[half] * ks;
+    c[half] = vexp - (st.m[half] == -INFINITY ? 0.0f : st.m[half]) + kPBase;
+    const f32x2 f2 = pair(f, f), c2 = pair(c[half], c[half]);
     top[half] = -INFINITY;
 #pragma unroll
-    for (int nt = 0; nt < NK; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float& x = s[nt][half * 2 + i];
-        x *= f;
-        if constexpr (kTail) {
-          if (nt * 8 + 2 * t + i >= left[half]) x = -INFINITY;
-        }
-        top[half] = fmaxf(top[half], x);
+    for (int nt = 0; nt < NK; ++nt) {
+      float &y0 = s[nt][half * 2], &y1 = s[nt][half * 2 + 1];
+      split(fma2(pair(y0, y1), f2, c2), y0, y1);
+      if constexpr (kTail) {
+        if (nt * 8 + 2 * t >= left[half]) y0 = -INFINITY;
+        if (nt * 8 + 2 * t + 1 >= left[half]) y1 = -INFINITY;
       }
-    over |= top[half] + vref > st.m[half] + kSlack;
+      top[half] = fmaxf(top[half], fmaxf(y0, y1));
+    }
+    top[half] += vref - c[half];
+    over |= top[half] > st.m[half] + kSlack;
   }
   if (__any_sync(0xffffffffu, over)) {
     float corr[2];
@@ -185,10 +188,16 @@ __device__ __forceinline__ void slice_step(
       float x = top[half];
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-      const float mo = st.m[half], mn = fmaxf(mo, x + vref);
+      const float mo = st.m[half], mn = fmaxf(mo, x), ref = mn == -INFINITY ? 0.0f : mn;
       st.m[half] = mn;
-      corr[half] = ptx::ex2_approx(mo - (mn == -INFINITY ? 0.0f : mn));
+      corr[half] = ptx::ex2_approx(mo - ref);
       st.l[half] *= corr[half];
+      const float down = (mo == -INFINITY ? 0.0f : mo) - ref;
+#pragma unroll
+      for (int nt = 0; nt < NK; ++nt) {
+        s[nt][half * 2] += down;
+        s[nt][half * 2 + 1] += down;
+      }
     }
 #pragma unroll
     for (int n = 0; n < S::NT; ++n) {
@@ -199,20 +208,20 @@ __device__ __forceinline__ void slice_step(
   uint4 pa[S::PARTS][kSlice / 16];
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    const float m = st.m[half];
-    const float c = vexp - (m == -INFINITY ? 0.0f : m) + kPBase;
-    float sum = 0.0f;
+    f32x2 sums = 0ull;
 #pragma unroll
     for (int nt = 0; nt < NK; ++nt) {
-      const float x0 = ptx::ex2_approx(s[nt][half * 2] + c);
-      const float x1 = ptx::ex2_approx(s[nt][half * 2 + 1] + c);
-      sum += x0 + x1;
+      const float x0 = ptx::ex2_approx(s[nt][half * 2]);
+      const float x1 = ptx::ex2_approx(s[nt][half * 2 + 1]);
+      sums = add2(sums, pair(x0, x1));
       const uint32_t hi = f16x2(x0, x1);
       (&pa[0][nt >> 1].x)[half + 2 * (nt & 1)] = hi;
       if constexpr (S::PARTS == 2)
         (&pa[1][nt >> 1].x)[half + 2 * (nt & 1)] = f16x2_rest(x0, x1, hi);
     }
-    st.l[half] = fmaf(sum, vinv, st.l[half]);
+    float sum0, sum1;
+    split(sums, sum0, sum1);
+    st.l[half] = fmaf(sum0 + sum1, vinv, st.l[half]);
   }
 #pragma unroll
   for (int kh = 0; kh < kSlice / 16; ++kh) {

@@ -23,6 +23,27 @@ constexpr float kPBase = 7.0f, kSlack = 8.0f;
 constexpr int kNoEnd = 1 << 30;    // beyond the positions of the largest page table
 constexpr int kMinScaleExp = -60;  // clamp of e_t in M, so that l stays in range
 
+// Two fp32 values in one register pair, and the packed operations on them.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(f32x2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 struct UnitDesc {  // of a unit that is cut: the worker that began it, and how many share it (else 0)
   int32_t worker, pieces;
 };
