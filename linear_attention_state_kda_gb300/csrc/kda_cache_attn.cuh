@@ -2,8 +2,8 @@
 // what both keep per query row.
 //
 // The key slices that the row groups see are laid end to end (row, head, row group, slice) and cut
-// into equal ranges, one per worker. A "unit" is one (row, head, row group); a worker's "piece" is the part of a unit
-// in its range. Beginning and ending a unit counts as unit_cost slices more.
+// into equal ranges, one per worker. A "unit" is one (row, head, row group); a worker's "piece" is
+// the part of a unit in its range. Beginning and ending a unit counts as unit_cost slices more.
 //
 // The loops here run a few times per CTA and are kept rolled: unrolled, they were 30 KB of each
 // kernel's code, more than the loops over the keys, and pushed those out of the instruction cache.
@@ -324,7 +324,8 @@ struct Ranges {
 };
 
 // Workspace: the pieces' sums, their (M, l), then a descriptor per unit (of 16 rows at least) and, for
-// units of 256 rows, the unit that each worker began and did not end (-1: none). An SM has up to 8 workers with units of up to 32 rows, or 4 with 64, or one with 256.
+// units of 256 rows, the unit that each worker began and did not end (-1: none). An SM has up to 8
+// workers with units of up to 32 rows, or 4 with 64, or one with 256.
 inline size_t piece_rows_of(int R) { return (size_t)2 * kMaxSms * 8 * (R < 32 ? R : 32); }
 
 // The tcgen05 kernel for bf16 queries: rows of its units, and its launch over the parts of the

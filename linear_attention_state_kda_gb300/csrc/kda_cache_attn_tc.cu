@@ -542,8 +542,9 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
           const int pg = page[i / (NL / 2)];
           raw[i] = make_uint4(0u, 0u, 0u, 0u);
           if (pg >= 0 && pg < p.n_pages)
-            raw[i] = *reinterpret_cast<const uint4*>(codes + ((int64_t)pg * p.Hkv + piece.h) * (kPage * D) +
-                                                     (key0 * CPK + c + 128 * (i % (NL / 2))) * 16);
+            raw[i] = *reinterpret_cast<const uint4*>(
+                codes + ((int64_t)pg * p.Hkv + piece.h) * (kPage * D) +
+                (key0 * CPK + c + 128 * (i % (NL / 2))) * 16);
         }
       };
       Scales next;

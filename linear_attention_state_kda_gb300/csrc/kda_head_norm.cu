@@ -15,8 +15,8 @@
 // y_v = r (v w_v cos + u w_u sin), computed once for the heads of a token that a warp takes, and
 // applied with packed fp32 operations. Every row load is issued before the first is reduced: 55 us
 // for 16384 tokens of 32 + 8 heads at d = 128, 6.2 TB/s, 92% of the copy rate. (Four rows a lane
-// instead of eight 57, two 62. 16-byte chunks with the partner's fetched by shuffles took 67, with twice the
-// instructions; a persistent grid that loads a token ahead measured the same as that.)
+// instead of eight 57, two 62. 16-byte chunks with the partner's fetched by shuffles took 67, with
+// twice the instructions; a persistent grid that loads a token ahead measured the same as that.)
 #include "kda_internal.cuh"
 
 namespace kda {

@@ -150,7 +150,8 @@ __device__ __forceinline__ int find_weight(const Source<T>& s, int i0, int i1, i
 }
 
 template <class T, int kWarps>
-__global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 8 : 1) verify_kernel(const VerifyParams p, int cluster) {
+__global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 8 : 1)
+verify_kernel(const VerifyParams p, int cluster) {
   __shared__ uint64_t part[2][kWarps];
   __shared__ uint64_t all[kMaxCluster * kWarps];
   const int b = blockIdx.x / cluster, rank = blockIdx.x - b * cluster;
@@ -275,9 +276,9 @@ kda_status launch_t(const VerifyParams& p, int cluster, cudaStream_t s) {
 template <class T>
 kda_status dispatch(const VerifyParams& p, cudaStream_t s) {
   // Few rows (up to two large CTAs per SM): as many warps per row as a cluster has, so that each
-  // stretch is short: 16 us against 20 for 4 rows of 32003 entries with one CTA a row. Many rows:
-  // small CTAs, whose loads cover each other's waits: 57 us on 256 rows of 131072 entries (4.7
-  // TB/s, 69% of the copy rate) against 84 with 16 warps; clusters of 4 or 2 are 10-60% slower.
+  // stretch is short: 4 us less than one CTA a row for 4 rows of 32003 entries (a call takes 8.2).
+  // Many rows: small CTAs, whose loads cover each other's waits: 55 us on 256 rows of 131072 entries
+  // (4.9 TB/s, 72% of the copy rate) against 84 with 16 warps; clusters of 4 or 2 are 10-60% slower.
   if (p.batch <= 38) return launch_t<T, 16>(p, kMaxCluster, s);
   return launch_t<T, 4>(p, kMaxCluster, s);
 }
