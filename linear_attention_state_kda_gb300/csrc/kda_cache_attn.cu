@@ -624,8 +624,8 @@ int team_of(kda_dtype dt, int rows) { return dt == KDA_F32 || rows <= 16 ? 1 : (
 
 // bf16 calls with at least this many query rows per key/value head go to the tcgen05 kernel: beyond
 // 64 rows the warps' units read and convert the codes again. 64 windows over contexts to 8k, 8
-// key/value heads, d = 128: 80 rows 270 us against 469, 128 rows 281 against 489, 256 rows 334
-// against 938 (d = 64, 80 rows: 186 against 306); one chunk of 512 tokens after 8192: 85 against 245.
+// key/value heads, d = 128: 80 rows 262 us against 469, 128 rows 277 against 489, 256 rows 314
+// against 938 (d = 64, 80 rows: 185 against 306); one chunk of 512 tokens after 8192: 83 against 245.
 // Only the shortest contexts lose, to the longer start: 64 tokens after 100, 21 us against 17.
 constexpr int kTcMinRows = 65;
 

@@ -24,8 +24,10 @@
 //
 // What bounds it: the products take 2048 cycles per 256 x 128 scores, the exponentials as long at
 // their full rate, and waits of some 150 cycles lie between a row tile's scores, softmax and values;
-// measured 3.9 thousand. 4 chunks of 1024 tokens after 16384, 32/8 heads: 604 us, 1200 TFLOP/s (62%
-// of the measured bf16 rate); 321 TFLOP/s with warp MMAs. What it took, in TFLOP/s there:
+// measured 3.9 thousand. 4 chunks of 1024 tokens after 16384, 32/8 heads: 598 us, 1212 TFLOP/s (63%
+// of the measured bf16 rate, 70% of the sustained one); 321 TFLOP/s with warp MMAs. Taking out the
+// widening gains 2%, the loads of the codes 5%, the exponentials nothing. What it took, in TFLOP/s
+// there:
 //   530 -> 885   the issuing warp stays converged and its operands are known to be the same in all
 //                lanes, with one lane elected at the instruction: from a branch of lane 0 each MMA
 //                took four times as long to issue
@@ -35,7 +37,8 @@
 //  1068 -> 1146  barriers that are due together are looked at together
 //  1146 -> 1200  the join of the units that were cut (join_kernel)
 // Handing P over a page at a time gave 509 against 477 TFLOP/s where only one row tile has rows, and
-// 1090 against 1146 here; not kept.
+// 1090 against 1146 here; taking the exponentials while the largest score is looked for, and
+// beginning the tile again where it turns out too large, 1068 against 1213. Neither was kept.
 // Tensor memory: 128 columns of S and d of O per row tile.
 #include "kda_cache_attn.cuh"
 #include "kda_fp8.cuh"
@@ -49,7 +52,9 @@ namespace {
 
 constexpr int kTile = 128;  // keys per step: two pages
 constexpr int kThreads = 512;
-constexpr int kUnitCost = 4;  // what beginning and ending a unit takes, in tiles
+// What beginning and ending a unit takes, in tiles (2 measured 17% slower on 64 windows of 256 rows,
+// 6 and 10 within 3% either way).
+constexpr int kUnitCost = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kScales = 4;  // ring of the tiles' scales
 constexpr int kPieces = 4;  // ring of pieces
@@ -77,8 +82,9 @@ struct Scales {  // of a tile's two pages
   int there[2];
 };
 
-struct Work {  // a piece; tiles = 0: there are no more
+struct Work {  // a piece; without tiles: there are no more
   int b, h, rg, first, last, whole;
+  int start, tokens;  // of its row
 };
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -181,7 +187,7 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
   };
   // Positions that the first row of a piece's unit sees.
   auto unit_first_sees = [&](const Work& x) {
-    return (int64_t)p.start[x.b] + x.rg * kTcRows / G + 1;
+    return (int64_t)x.start + x.rg * kTcRows / G + 1;
   };
 
   int n = 0;           // tiles of the pieces so far
@@ -279,11 +285,12 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
           if (lane == 0) desc[at] = x.desc;
           if (!x.whole) begun = at;
         }
+        const int start = more ? p.start[x.b] : 0, tokens = more ? row_tokens(p, x.b) : 0;
         // (descriptors are written to the end also when the other roles have left)
         const uint32_t slot = taken % kPieces;
         ok = ok && wait(&bars.piece_empty[slot], ((taken / kPieces) & 1) ^ 1);
         if (ok && lane == 0) {
-          s_work[slot] = {x.b, x.h, x.rg, x.first, x.last, x.whole};
+          s_work[slot] = {x.b, x.h, x.rg, x.first, x.last, x.whole, start, tokens};
           ptx::mbar_arrive(&bars.piece_full[slot]);
         }
       }
@@ -304,7 +311,7 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
         n += tiles;
         continue;
       }
-      const int j = gr / G, n_tok = row_tokens(p, piece.b);
+      const int j = gr / G, n_tok = piece.tokens;
       const bool live = gr < R && j < n_tok;
       const int64_t at_row =
           ((int64_t)piece.b * p.window + j) * p.Hq + piece.h * G + (gr - j * G);  // of q and o
@@ -328,7 +335,7 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
         rowf = p.scale * 1.44269504f * pow2f(-e);
         const uint32_t dst =
             ptx::smem_u32(smem) + M::Q + g * M::QTILE + (r >> 3) * 1024 + (r & 7) * 128;
-#pragma unroll 2
+#pragma unroll 8
         for (int i = 0; i < D / 8; ++i) {
           float q[8];
           Vec16<__nv_bfloat16>::unpack(live ? src[i] : zero, q);
@@ -343,7 +350,7 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
       if (lane == 0) ptx::mbar_arrive(&bars.q_full[g]);
 
       // rows that are not live see everything: they force no mask, and are not stored
-      const int64_t sees = (int64_t)p.start[piece.b] + j + 1;
+      const int64_t sees = (int64_t)piece.start + j + 1;
       const int seen = live && sees < kNoEnd ? (int)sees : kNoEnd;
       const int64_t first_sees = unit_first_sees(piece);
       float m = -INFINITY, l = 0.0f;
@@ -522,7 +529,7 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
     bool ok = true;
     while (ok && take()) {
       const int32_t* table = p.table + (int64_t)piece.b * p.max_pages;
-      const int n_tok = row_tokens(p, piece.b), start = p.start[piece.b];
+      const int n_tok = piece.tokens, start = piece.start;
       const int j1 = (piece.rg * kTcRows + kTcRows - 1) / G;
       const int64_t first_sees = unit_first_sees(piece);
       // positions that some row of the unit sees
