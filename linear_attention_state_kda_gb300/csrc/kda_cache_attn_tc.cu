@@ -106,10 +106,7 @@ template <int N>
 __device__ __forceinline__ void regs_take() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
-// 32 columns of the lane's row; the empty statements keep every use behind the wait.
-__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t* r) {
-  ptx::tmem_ld32_nowait(at, r);
-}
+// Empty statements that keep every use of loaded columns behind the wait.
 __device__ __forceinline__ void tmem_loaded(uint32_t* r, int n) {
 #pragma unroll
   for (int i = 0; i < n; ++i) asm volatile("" : "+r"(r[i]));
@@ -266,11 +263,13 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
         }
         n += tiles;
       }
-      if (lane == 0 && *(volatile int*)&s_abort) {  // a role gave up: the MMAs in flight end first
-        ptx::mma_commit(&bars.drain);
-        ptx::mbar_wait(&bars.drain, 0, 100000000ull);
+      if (__any_sync(0xffffffffu, *(volatile int*)&s_abort)) {
+        // a role gave up: the MMAs in flight end first
+        if (ptx::elect_one()) ptx::mma_commit(&bars.drain);
+        __syncwarp();
+        ptx::mbar_wait_tries(&bars.drain, 0);
+        __syncwarp();
       }
-      __syncwarp();
     } else if (warp == 2) {
       ranges.zero_units<__nv_bfloat16>(p, D, blockIdx.x, gridDim.x, desc);
     } else if (warp == 3) {
@@ -377,7 +376,7 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
 #pragma unroll 1
         for (bool again = false;; again = true) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_load32(t_s + c * 32, s + c * 32);
+          for (int c = 0; c < 4; ++c) ptx::tmem_ld32_nowait(t_s + c * 32, s + c * 32);
           ptx::tmem_ld_wait();
           tmem_loaded(s, kTile);
           const float m0 = m == -INFINITY ? 0.0f : m;
