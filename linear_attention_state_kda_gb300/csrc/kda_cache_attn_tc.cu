@@ -68,6 +68,16 @@ struct Smem {  // offsets; every operand tile starts on 1024 bytes
   static constexpr int BYTES = V + 2 * KV;
 };
 
+// Every wait is by parity, which tells a phase only from the one before it. So a role may wait for a
+// phase only where the phase before is known to be complete and the one after it cannot be:
+//   k_full, v_full, by the MMAs: tiles in order; a stage's next tile waits for k_empty / v_empty of
+//     this one. v_full, by the softmax: once the scores of tile n are there, a converter warp has put
+//     V of n - 1 before K of n, and V of n + 2 waits for this row tile's P of n
+//   k_empty, v_empty: tiles in order, two behind
+//   q_full, s_full, p_full, o_full: of one row tile, each waited for by the other side in every tile
+//     (piece) that the row tile has rows in; S, P and O take turns
+//   scales: in order, by a row tile with rows in every piece; see there for one that skips some
+//   piece_full, piece_empty: every role takes every piece
 struct Bars {
   // codes widened (4 converter warps) and read by both row tiles' MMAs
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
@@ -302,12 +312,13 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
     const uint32_t lanes = (uint32_t)(w * 32) << 16;
     const uint32_t t_s = tmem + lanes + g * kTile, t_o = tmem_o + lanes + g * D;
     uint32_t use = 0;  // tiles of this row tile so far
-    bool ok = true;
+    bool ok = true, skipped = false;
     while (ok && take()) {
       const int tiles = piece.last - piece.first;
       const int gr = piece.rg * kTcRows + g * 128 + r;
       if (R - piece.rg * kTcRows <= g * 128) {  // no rows
         n += tiles;
+        skipped = true;
         continue;
       }
       const int j = gr / G, n_tok = piece.tokens;
@@ -354,9 +365,17 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
       const int64_t first_sees = unit_first_sees(piece);
       float m = -INFINITY, l = 0.0f;
       uint4 nan = make_uint4(0u, 0u, 0u, 0u);  // channels in which the row saw a NaN
+      // After a skipped piece, the first scores before the first scales. A wait by parity tells a
+      // phase only from the one before it, and the converters may still be many tiles behind: the
+      // ring's word is another tile's then, and its parity may let the wait pass. s_full counts this
+      // row tile's own tiles. With the scores of tile n there, tile n - 4's scales have been published,
+      // and tile n + 4's cannot be: they wait until the keys of n + 2 have been read, and so for this
+      // row tile's P of tile n. Without a skip the scores of the tile before say the same.
+      if (skipped) ok = wait(&bars.s_full[g], use & 1);
+      skipped = false;
 #pragma unroll 1
       for (int i = piece.first; i < piece.last; ++i, ++n, ++use) {
-        ok = wait(&bars.scales[n % kScales], (n / kScales) & 1);
+        ok = ok && wait(&bars.scales[n % kScales], (n / kScales) & 1);
         const Scales sc = s_scales[n % kScales];
         const int left = seen - i * kTile;
         const bool masked =
