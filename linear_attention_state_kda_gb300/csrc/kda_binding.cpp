@@ -384,6 +384,8 @@ PyObject* cache_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (bytes > 0 || a[10] != Py_None) {
     ws.set(a[10], {bytes}, at::TensorOptions().dtype(at::kByte).device(q.device()), "workspace");
     require(ws.t->is_contiguous(), "must be contiguous", "workspace");
+    dv.see(*ws.t);
+    dv.check();
     bytes = (int64_t)ws.t->nbytes();
     wp = ws.t->data_ptr();
   }

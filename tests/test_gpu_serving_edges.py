@@ -100,3 +100,19 @@ def test_cache_of_many_short_sequences():
         for s in range(n):
             a, _ = ref.gather(val, sc, host[s], int(back[s]), 2 * n)
             assert np.array_equal(x[rcu[s]:rcu[s + 1]], a), s
+
+
+def test_workspace_elsewhere_is_refused():
+    """A workspace in host memory is refused by the binding: nothing is launched with its pointer."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(4)
+    start = [300, 17]
+    q, table, pool = _make(gen, start, 2, 8, 2, 128, "bf16")
+    st = _i32(start)
+    ws = torch.zeros(kda.cache_attention_workspace(2, 2, 8, 2, 128) + 256, dtype=torch.uint8)
+    before = kda.launch_count()
+    with pytest.raises(ValueError, match="device"):
+        kda.cache_attention(q, st, table, *pool, scale=0.05, workspace=ws)
+    assert kda.launch_count() == before
+    kda.cache_attention(q, st, table, *pool, scale=0.05, workspace=ws.to(DEV))
+    assert kda.launch_count() > before
