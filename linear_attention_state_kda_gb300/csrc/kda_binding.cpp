@@ -13,11 +13,13 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <initializer_list>
+#include <optional>
 
 #include "../../include/kda.h"
 
@@ -92,12 +94,6 @@ int as_int(int64_t v, const char* name) {
   return (int)v;
 }
 
-kda_stream_t stream_of(PyObject* o) {
-  if (o == Py_None) return (kda_stream_t)c10::cuda::getCurrentCUDAStream().stream();
-  void* p = PyLong_AsVoidPtr(o);
-  if (PyErr_Occurred()) throw python_error();
-  return (kda_stream_t)p;
-}
 double as_double(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw python_error();
@@ -117,6 +113,26 @@ uint32_t* status_of(Devices& d, PyObject* o) {
   return static_cast<uint32_t*>(t->data_ptr());
 }
 
+// The stream of a call (None: the current one). While this lives, tensors are allocated on it: the
+// allocator orders the uses of a block by the stream that it was allocated on, so a block that was
+// freed while another stream still works on it is not written by this call ahead of that work.
+// Made once the tensors of the call are known to be on the current device.
+struct CallStream {
+  kda_stream_t s;
+  std::optional<c10::cuda::CUDAStream> caller;  // the current stream, where it is another one
+  std::optional<c10::cuda::CUDAStreamGuard> guard;
+  explicit CallStream(PyObject* o) {
+    const auto current = c10::cuda::getCurrentCUDAStream();
+    s = (kda_stream_t)current.stream();
+    if (o == Py_None) return;
+    s = (kda_stream_t)PyLong_AsVoidPtr(o);
+    if (PyErr_Occurred()) throw python_error();
+    if (s == (kda_stream_t)current.stream()) return;
+    caller = current;
+    guard.emplace(c10::cuda::getStreamFromExternal((cudaStream_t)s, current.device_index()));
+  }
+};
+
 // An output: the caller's tensor, or a new one.
 struct Out {
   PyObject* given = nullptr;
@@ -131,15 +147,11 @@ struct Out {
       t = &made;
     }
   }
-  // A tensor made here belongs to the current stream: its memory is not handed out again before
-  // work on another stream that uses it is done.
-  void used_on(kda_stream_t s) const {
-    if (!made.defined()) return;
-    const auto current = c10::cuda::getCurrentCUDAStream();
-    if ((kda_stream_t)current.stream() == s) return;
-    c10::cuda::CUDACachingAllocator::recordStream(
-        made.storage().data_ptr(),
-        c10::cuda::getStreamFromExternal((cudaStream_t)s, made.device().index()));
+  // A tensor made on the call's stream goes to the caller, whose current stream is the one that it
+  // is likely used on: its memory is not handed out again before that stream has come so far.
+  void handed_to(const CallStream& c) const {
+    if (c.caller && made.defined())
+      c10::cuda::CUDACachingAllocator::recordStream(made.storage().data_ptr(), *c.caller);
   }
   PyObject* object() const {
     if (!given) return THPVariable_Wrap(made);
@@ -244,6 +256,9 @@ PyObject* head_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float* qw = vec<float>(dv, opt(a[2], "q_weight"), at::kFloat, d, "q_weight");
   const float* kw = vec<float>(dv, opt(a[3], "k_weight"), at::kFloat, d, "k_weight");
   const int32_t* pos = vec<int32_t>(dv, opt(a[7], "positions"), at::kInt, T, "positions");
+  uint32_t* status = status_of(dv, a[11]);
+  dv.check();
+  const CallStream on(a[12]);
   for (int i = 0; i < 2; ++i) {
     if (!side[i]) continue;
     const Tensor& t = *side[i];
@@ -253,7 +268,6 @@ PyObject* head_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     src[i] = t.data_ptr();
     dst[i] = out[i].t->data_ptr();
   }
-  uint32_t* status = status_of(dv, a[11]);
   dv.check();
   const int tokens = as_int(T, "tokens"), hd = as_int(d, "d");
   const int rot = table ? as_int(table->size(1), "rot_dim") : 0;
@@ -261,15 +275,14 @@ PyObject* head_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float eps = (float)as_double(a[4]);
   const unsigned flags =
       (as_bool(a[5]) ? KDA_NORM_L2 : 0u) | (as_bool(a[8]) ? KDA_ROPE_INTERLEAVED : 0u);
-  const kda_stream_t s = stream_of(a[12]);
   const kda_status st = [&] {
     NoGil g;
     return kda_head_norm_rope(dt, tokens, H[0], H[1], hd, src[0], stride[0], src[1], stride[1], qw,
                               kw, eps, flags, cs, n_pos, rot, pos, dst[0], out_stride[0], dst[1],
-                              out_stride[1], status, s);
+                              out_stride[1], status, on.s);
   }();
   if (st != KDA_OK) return PyLong_FromLong(st);
-  for (const Out& o : out) o.used_on(s);
+  for (const Out& o : out) o.handed_to(on);
   return tuple_of({q ? out[0].object() : none(), k ? out[1].object() : none()});
   END_HANDLE_TH_ERRORS
 }
@@ -295,11 +308,11 @@ PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   dv.check();
   const int nr = as_int(rows, "rows"), T = as_int(k.size(0), "tokens"), H = as_int(c.H, "Hkv"),
             d = as_int(c.d, "d");
-  const kda_stream_t s = stream_of(a[11]);
+  const CallStream on(a[11]);
   const kda_status st = [&] {
     NoGil g;
     return kda_cache_write(dt, nr, T, cu, st0, lens, H, d, k.data_ptr(), ks, v.data_ptr(), vs,
-                           c.table, c.max_pages, c.kc, c.ks, c.vc, c.vs, c.n_pages, status, s);
+                           c.table, c.max_pages, c.kc, c.ks, c.vc, c.vs, c.n_pages, status, on.s);
   }();
   return st != KDA_OK ? PyLong_FromLong(st) : none();
   END_HANDLE_TH_ERRORS
@@ -330,6 +343,9 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const kda_dtype dt = code_of(type, "k and v");
   const int64_t shape[3] = {T, c.H, c.d};
   const auto opts = at::TensorOptions().dtype(type).device(start.device());
+  uint32_t* status = status_of(dv, a[11]);
+  dv.check();
+  const CallStream on(a[12]);
   Out out[2];
   void* dst[2];
   for (int i = 0; i < 2; ++i) {
@@ -338,18 +354,16 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
             i ? "v" : "k");
     dst[i] = vec(dv, out[i].t, type, T * c.H * c.d, i ? "v" : "k");
   }
-  uint32_t* status = status_of(dv, a[11]);
   dv.check();
   const int nr = as_int(rows, "rows"), total = as_int(T, "total_tokens"), H = as_int(c.H, "Hkv"),
             d = as_int(c.d, "d");
-  const kda_stream_t s = stream_of(a[12]);
   const kda_status st = [&] {
     NoGil g;
     return kda_cache_read(dt, nr, total, cu, st0, H, d, c.table, c.max_pages, c.kc, c.ks, c.vc,
-                          c.vs, c.n_pages, dst[0], dst[1], status, s);
+                          c.vs, c.n_pages, dst[0], dst[1], status, on.s);
   }();
   if (st != KDA_OK) return PyLong_FromLong(st);
-  for (const Out& o : out) o.used_on(s);
+  for (const Out& o : out) o.handed_to(on);
   return tuple_of({out[0].object(), out[1].object()});
   END_HANDLE_TH_ERRORS
 }
@@ -372,11 +386,12 @@ PyObject* cache_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const void* qp = vec(dv, &q, type, size, "q");
   const int32_t* st0 = vec<int32_t>(dv, &start, at::kInt, B, "start");
   const int32_t* lens = vec<int32_t>(dv, opt(a[8], "lens"), at::kInt, B, "lens");
+  uint32_t* status = status_of(dv, a[11]);
+  dv.check();
+  const CallStream on(a[12]);
   Out out, ws;
   out.set(a[9], q.sizes(), at::TensorOptions().dtype(type).device(q.device()), "o");
   void* op = vec(dv, out.t, type, size, "o");
-  uint32_t* status = status_of(dv, a[11]);
-  dv.check();
   const int b = as_int(B, "batch"), w = as_int(W, "window"), hq = as_int(Hq, "Hq"),
             hkv = as_int(c.H, "Hkv"), d = as_int(c.d, "d");
   int64_t bytes = (int64_t)kda_cache_attention_workspace(b, w, hq, hkv, d);
@@ -385,20 +400,19 @@ PyObject* cache_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     ws.set(a[10], {bytes}, at::TensorOptions().dtype(at::kByte).device(q.device()), "workspace");
     require(ws.t->is_contiguous(), "must be contiguous", "workspace");
     dv.see(*ws.t);
-    dv.check();
     bytes = (int64_t)ws.t->nbytes();
     wp = ws.t->data_ptr();
   }
+  dv.check();
   const float scale = (float)as_double(a[7]);
-  const kda_stream_t s = stream_of(a[12]);
   const kda_status st = [&] {
     NoGil g;
     return kda_cache_attention(dt, b, w, hq, hkv, d, scale, qp, st0, lens, c.table, c.max_pages,
-                               c.kc, c.ks, c.vc, c.vs, c.n_pages, op, wp, (size_t)bytes, status, s);
+                               c.kc, c.ks, c.vc, c.vs, c.n_pages, op, wp, (size_t)bytes, status,
+                               on.s);
   }();
   if (st != KDA_OK) return PyLong_FromLong(st);
-  out.used_on(s);
-  ws.used_on(s);
+  out.handed_to(on);
   return out.object();
   END_HANDLE_TH_ERRORS
 }
@@ -447,6 +461,9 @@ PyObject* draft_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t* slots =
       vec<int32_t>(dv, opt(a[6], "write_slots"), at::kInt, B * W1, "write_slots");
   const auto opts = at::TensorOptions().dtype(at::kInt).device(target.device());
+  uint32_t* status = status_of(dv, a[10]);
+  dv.check();
+  const CallStream on(a[11]);
   Out tokens, taken, resume;
   tokens.set(a[7], {B, W1}, opts, "tokens");
   taken.set(a[8], {B}, opts, "n_accepted");
@@ -455,17 +472,15 @@ PyObject* draft_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int32_t* tp = vec<int32_t>(dv, tokens.t, at::kInt, B * W1, "tokens");
   int32_t* np = vec<int32_t>(dv, taken.t, at::kInt, B, "n_accepted");
   int32_t* rp = vec<int32_t>(dv, resume.t, at::kInt, B, "resume_slots");
-  uint32_t* status = status_of(dv, a[10]);
   dv.check();
   const int b = as_int(B, "batch"), w = as_int(W, "window"), v = as_int(V, "vocab");
-  const kda_stream_t s = stream_of(a[11]);
   const kda_status st = [&] {
     NoGil g;
     return kda_draft_verify(dt, b, w, v, target.data_ptr(), ts, dp, ds, xp, lens, uap, usp, slots,
-                            tp, np, rp, status, s);
+                            tp, np, rp, status, on.s);
   }();
   if (st != KDA_OK) return PyLong_FromLong(st);
-  for (const Out* o : {&tokens, &taken, &resume}) o->used_on(s);
+  for (const Out* o : {&tokens, &taken, &resume}) o->handed_to(on);
   return tuple_of({taken.object(), tokens.object(), has_resume ? resume.object() : none()});
   END_HANDLE_TH_ERRORS
 }

@@ -116,3 +116,49 @@ def test_workspace_elsewhere_is_refused():
     assert kda.launch_count() == before
     kda.cache_attention(q, st, table, *pool, scale=0.05, workspace=ws.to(DEV))
     assert kda.launch_count() > before
+
+
+def _held_back(shape_bytes, call):
+    """Runs `call` on a stream of its own while the current stream still has to read a block of
+    `shape_bytes` bytes that was dropped just before; returns whether the reader got its data."""
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    blocks = [torch.full((n,), 37, dtype=torch.uint8, device=DEV) for n in shape_bytes]
+    copies = [torch.empty_like(b) for b in blocks]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # about a tenth of a second
+    for c, b in zip(copies, blocks):
+        c.copy_(b)
+    del blocks, b
+    out = call(side)
+    side.synchronize()
+    done = torch.cuda.current_stream().query()
+    torch.cuda.synchronize()
+    assert not done  # the reader was still waiting when the call had run
+    return out, all(bool((c == 37).all()) for c in copies)
+
+
+def test_memory_made_for_another_stream_is_not_taken_from_pending_work():
+    """Outputs and workspace of a call on another stream do not lie in memory that the current stream
+    has yet to read, though it is free for the current stream's next tensors."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(6)
+    start = [4000, 17, 900]
+    q, table, pool = _make(gen, start, 2, 8, 2, 128, "bf16")
+    st, zero, cu = _i32(start), _i32([0, 0, 0]), _i32([0, 100, 150, 500])
+    p = torch.softmax(torch.randn(300, 4, 50, generator=gen, device=DEV), -1)
+    toks = p[:, :3].argmax(-1).to(torch.int32).contiguous()
+    ua, us = torch.rand(300, 3, generator=gen, device=DEV), torch.zeros(300, device=DEV)
+    n = q.numel() * 2
+    need = kda.cache_attention_workspace(3, 2, 8, 2, 128)
+    for sizes, call in (
+            ([n], lambda s: kda.head_norm_rope(q, None, stream=s)[0]),
+            ([n, need], lambda s: kda.cache_attention(q, st, table, *pool, scale=0.05, stream=s)),
+            ([500 * 2 * 128 * 2] * 2,
+             lambda s: kda.cache_read(zero, table, *pool, 500, cu_seqlens=cu, stream=s)),
+            ([300 * 4 * 4, 300 * 4], lambda s: kda.draft_verify(p, toks, ua, us, stream=s)[1])):
+        want = call(None)
+        got, kept = _held_back(sizes, call)
+        assert kept
+        for x, y in zip(*((z,) if torch.is_tensor(z) else z for z in (got, want))):
+            assert torch.equal(x, y)
