@@ -74,9 +74,8 @@ typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype; /* dtype of q, k, v and o 
 #define KDA_STATUS_BAD_OFFSETS 4u /* an offset array was decreasing or out of range, or a
                                      sequence had more segments than max_segs_per_seq; the
                                      offending range was treated as empty */
-#define KDA_STATUS_TIMEOUT 8u     /* a tensor-core CTA waited too long (2 s; some 30 ms or more in
-                                     kda_cache_attention) for its own copies or MMAs and stopped
-                                     early; its outputs are incomplete */
+#define KDA_STATUS_TIMEOUT 8u     /* a tensor-core CTA waited more than 2 s for its own copies
+                                     or MMAs and stopped early; its outputs are incomplete */
 
 #define KDA_STATUS_BAD_PAGE 16u  /* a page id >= n_pages, or a position past the page table, was
                                     skipped */

@@ -58,6 +58,9 @@ constexpr int kUnitCost = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kScales = 4;  // ring of the tiles' scales
 constexpr int kPieces = 4;  // ring of pieces
+// Tries of a wait for a tile (2 s) and for a whole piece (63 s: the longest is 2^23 tiles, the keys of
+// the largest page table, some 17 s).
+constexpr uint32_t kTileTries = 1u << 19, kPieceTries = 1u << 24;
 
 template <int D>
 struct Smem {  // offsets; every operand tile starts on 1024 bytes
@@ -179,13 +182,21 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);  // (known to be the same in all lanes)
   const uint32_t tmem_o = tmem + 2 * kTile;
 
-  // A wait of a whole warp (all lanes get the same answer). One that gives up records it, and the
-  // warp leaves; so do those that wait for it.
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (__all_sync(0xffffffffu, ptx::mbar_wait_tries(bar, parity))) return true;
+  // A wait of a whole warp (all lanes get the same answer) for what another role does with a tile.
+  // One that gives up records it, and the warp leaves; so do those that wait for it.
+  auto outcome = [&](bool done) {
+    if (__all_sync(0xffffffffu, done)) return true;
     if (p.status) atomicOr(p.status, KDA_STATUS_TIMEOUT);
     *(volatile int*)&s_abort = 1;
     return false;
+  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return outcome(ptx::mbar_wait_tries(bar, parity, kTileTries));
+  };
+  // For what takes another role a whole piece, or the search for the next one: as long as that takes,
+  // and no longer than until a role gives up.
+  auto wait_long = [&](uint64_t* bar, uint32_t parity) {
+    return outcome(ptx::mbar_wait_tries_or(bar, parity, kPieceTries, &s_abort));
   };
   // Of two barriers, which are looked at together.
   auto wait2 = [&](uint64_t* a, uint32_t parity_a, uint64_t* b, uint32_t parity_b) {
@@ -203,7 +214,7 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
   Work piece;
   auto take = [&]() {
     const uint32_t slot = taken % kPieces;
-    if (!wait(&bars.piece_full[slot], (taken / kPieces) & 1)) return false;
+    if (!wait_long(&bars.piece_full[slot], (taken / kPieces) & 1)) return false;
     piece = s_work[slot];
     piece.first = __shfl_sync(0xffffffffu, piece.first, 0);
     piece.last = __shfl_sync(0xffffffffu, piece.last, 0);
@@ -277,7 +288,7 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
         // a role gave up: the MMAs in flight end first
         if (ptx::elect_one()) ptx::mma_commit(&bars.drain);
         __syncwarp();
-        ptx::mbar_wait_tries(&bars.drain, 0);
+        ptx::mbar_wait_tries(&bars.drain, 0, kTileTries);
         __syncwarp();
       }
     } else if (warp == 2) {
@@ -297,7 +308,7 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
         const int start = more ? p.start[x.b] : 0, tokens = more ? row_tokens(p, x.b) : 0;
         // (descriptors are written to the end also when the other roles have left)
         const uint32_t slot = taken % kPieces;
-        ok = ok && wait(&bars.piece_empty[slot], ((taken / kPieces) & 1) ^ 1);
+        ok = ok && wait_long(&bars.piece_empty[slot], ((taken / kPieces) & 1) ^ 1);
         if (ok && lane == 0) {
           s_work[slot] = {x.b, x.h, x.rg, x.first, x.last, x.whole, start, tokens};
           ptx::mbar_arrive(&bars.piece_full[slot]);
@@ -371,7 +382,7 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
       // row tile's own tiles. With the scores of tile n there, tile n - 4's scales have been published,
       // and tile n + 4's cannot be: they wait until the keys of n + 2 have been read, and so for this
       // row tile's P of tile n. Without a skip the scores of the tile before say the same.
-      if (skipped) ok = wait(&bars.s_full[g], use & 1);
+      if (skipped) ok = wait_long(&bars.s_full[g], use & 1);
       skipped = false;
 #pragma unroll 1
       for (int i = piece.first; i < piece.last; ++i, ++n, ++use) {

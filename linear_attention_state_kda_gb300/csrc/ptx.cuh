@@ -103,11 +103,21 @@ __device__ __forceinline__ bool mbar_wait_or(uint64_t* bar, uint32_t parity, con
   }
 }
 // The same with a limit on the tries, in a few instructions: for kernels with many waits, whose
-// code must stay within the instruction cache. Some 30 ms at the least.
-__device__ __forceinline__ bool mbar_wait_tries(uint64_t* bar, uint32_t parity) {
+// code must stay within the instruction cache. A try that fails blocks for 3.76 us (measured on a
+// GB300), so 2^19 of them are 2 s.
+__device__ __forceinline__ bool mbar_wait_tries(uint64_t* bar, uint32_t parity, uint32_t tries) {
 #pragma unroll 1
-  for (uint32_t i = 0; i < (1u << 20); ++i)
+  for (uint32_t i = 0; i < tries; ++i)
     if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+__device__ __forceinline__ bool mbar_wait_tries_or(uint64_t* bar, uint32_t parity, uint32_t tries,
+                                                   const int* abort) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < tries; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*(const volatile int*)abort) return false;
+  }
   return false;
 }
 __device__ __forceinline__ bool mbar_wait_relaxed_or(uint64_t* bar, uint32_t parity,

@@ -63,3 +63,36 @@ def test_from_a_short_row_group_into_the_next_unit(start, W, Hq, Hkv, d, absent)
     assert float(err.max()) <= 1, float(err.max())
     for _ in range(3):
         assert torch.equal(kda.cache_attention(q, _i32(start), table, *pool, scale=scale), got)
+
+
+def test_pieces_that_take_long():
+    """Contexts of 3.8 million tokens (two pages in turn), two heads on each SM: a row tile waits 30
+    thousand tiles for the other one's piece. No wait gives up, and the result is right.
+
+    Each of a row's sums is 30 thousand tiles of at most 8 additions in fp32, each of which may lose
+    2^-23 of the sum so far: 0.03 of the largest result, besides the usual 2^-10 of the largest value
+    and 2^-8 of the result."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(9)
+    B, W, Hq, Hkv, d, tiles = 76, 75, 16, 4, 64, 30000
+    start = [tiles * 128 - W] * B
+    q, _, pool = _make(gen, [100], 1, Hq, Hkv, d, "bf16", spare=0)
+    pool[2] &= 0x7f
+    q = torch.randn(B * W, Hq, d, generator=gen, device=DEV).bfloat16()
+    table = _i32([0, 1]).repeat(tiles).expand(B, -1).contiguous()
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    scale = 0.3 * d ** -0.5
+    got = kda.cache_attention(q, _i32(start), table, *pool, scale=scale, status=status)
+    assert int(status) == 0
+    code = torch.from_numpy(ref.code_values()).to(DEV)
+    t = torch.arange(128, device=DEV)
+    seen = start[0] + 1 + torch.arange(W, device=DEV)  # keys of the window's tokens
+    times = ((seen[:, None] - 1 - t) // 128 + 1).double()  # of each of the two pages' rows
+    x = q.double().reshape(B, W, Hkv, Hq // Hkv, d)
+    k, v = ((code[pool[i].long()] * pool[i + 1].double()[:, :, None, None])
+            .transpose(0, 1).reshape(Hkv, 128, d) for i in (0, 2))
+    s = scale * torch.einsum("bwhgd,htd->bwhgt", x, k) + times.log()[None, :, None, None]
+    want = torch.einsum("bwhgt,htd->bwhgd", torch.softmax(s, -1), v).reshape(q.shape)
+    top = 30 * float(pool[3].max())
+    tol = 0.03 * want.abs().max() + 2.0 ** -10 * top + 2.0 ** -8 * want.abs()
+    assert bool(((got.double() - want).abs() <= tol).all())
