@@ -514,6 +514,9 @@ KDA_API kda_status kda_cache_read(kda_dtype dt, int n_seqs, int total_tokens,
  * Scores, softmax statistics and sums are fp32. With bf16 queries the probabilities enter the
  * second product rounded to 11 bits; with fp32 queries, queries and probabilities are carried in
  * two 11-bit parts.
+ * A row that only sees values of scales below 2^-80 (2^e at the most) has its probabilities rounded to
+ * 2^-(111 + e) of the largest besides: 2^-11 where all scales are 2^-100. Where a row sees value scales
+ * more than 2^109 apart, probabilities of the smallest begin to be lost from the softmax's sum.
  */
 KDA_API size_t kda_cache_attention_workspace(int batch, int window, int Hq, int Hkv, int d);
 KDA_API kda_status kda_cache_attention(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d,

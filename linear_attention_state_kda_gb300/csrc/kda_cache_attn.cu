@@ -16,8 +16,11 @@
 // keeps M, at most 8 below max_t (x_t + e_t), and accumulates
 //     P_t = 2^(x_t + e_t - M + 7) (f16; two parts for fp32),  O = sum_t P_t code_t,
 //     l = sum_t 2^(x_t - M + 7) = sum_t P_t 2^-e_t (fp32),    o = O / l.
-// P is at most 2^15 whatever the scales of the pages, and what f16 drops is below 2^-32 of the
-// row's largest term.
+// P is at most 2^15 whatever the scales of the pages, and what f16 drops is below 2^-32 of the row's
+// largest term, as long as the row sees a value scale of 2^-80 or more. In M a smaller e_t counts as
+// -80, so that l stays in range; where all are smaller, 2^e at the most, what f16 drops is below
+// 2^-(112 + e) of the largest term: 2^-12 for the smallest scale, 2^-100. (l loses what is below 2^-126
+// as P: terms below 2^-24 of the largest where a row's value scales are 2^109 apart, larger ones beyond.)
 //
 // Layout. Lane (g, t) = (lane / 4, lane % 4) of an m16n8k16 MMA. The order of the channels in the
 // first product and of the columns in the second is free as long as both operands agree, and is

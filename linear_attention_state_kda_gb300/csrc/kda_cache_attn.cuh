@@ -21,7 +21,9 @@ constexpr int kWindows = 512;      // windows of rows in the search for a worker
 // unit instead of in most steps.
 constexpr float kPBase = 7.0f, kSlack = 8.0f;
 constexpr int kNoEnd = 1 << 30;    // beyond the positions of the largest page table
-constexpr int kMinScaleExp = -60;  // clamp of e_t in M, so that l stays in range
+// Value scales below 2^kMinScaleExp count as this one in M. l is then at most 2^(15 + 80) a key, in range
+// for 2^30 keys; P of a smaller scale 2^e starts at 2^(e + 87) instead of 2^7, 2^-13 for the smallest.
+constexpr int kMinScaleExp = -80;
 
 // Two fp32 values in one register pair, and the packed operations on them.
 typedef unsigned long long f32x2;
