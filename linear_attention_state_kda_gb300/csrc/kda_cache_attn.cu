@@ -413,7 +413,7 @@ attn_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_ml,
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         int e = top ? 13 + 127 - (int)(top >> 23) : 0;
-        e = e > 100 ? 100 : (e < -100 ? -100 : e);
+        e = e > 100 ? 100 : e;  // (-114 at the least)
         const float up = pow2f(e);
         rowf[half] = p.scale * 1.44269504f * pow2f(-e);
         // rows that are not live see everything: they force no mask, and are not stored

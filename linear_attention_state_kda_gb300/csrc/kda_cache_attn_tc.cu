@@ -351,7 +351,7 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
           for (int u = 0; u < 8; ++u) top = max(top, finite_abs_bits(q[u]));
         }
         int e = top ? 13 + 127 - (int)(top >> 23) : 0;
-        e = e > 100 ? 100 : (e < -100 ? -100 : e);
+        e = e > 100 ? 100 : e;  // (-114 at the least)
         const float up = pow2f(e);
         rowf = p.scale * 1.44269504f * pow2f(-e);
         const uint32_t dst =

@@ -42,3 +42,17 @@ def test_small_value_scales_fp32(e):
     pool[2] &= 0x7f
     got = kda.cache_attention(q, _i32(start), table, *pool, scale=0.01)
     _check(q, start, None, table, pool, 0.01, "f32", got)
+
+
+@pytest.mark.parametrize("W,Hq,Hkv,d,dtype", [s + ("bf16",) for s in SHAPES] +
+                         [(3, 6, 2, 128, "f32"), (2, 3, 3, 64, "f32")])
+def test_large_queries(W, Hq, Hkv, d, dtype):
+    """Query entries from 1 to 2^126, with a scale that leaves scores of a usual size."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(W + d)
+    start = [300, 40]
+    q, table, pool = _make(gen, start, W, Hq, Hkv, d, dtype)
+    q = q.clamp(-3.9, 3.9)
+    for up in (2.0 ** 112, 2.0 ** 118, 2.0 ** 124):
+        got = kda.cache_attention(q * up, _i32(start), table, *pool, scale=0.02 / up)
+        _check(q, start, None, table, pool, 0.02, dtype, got)
