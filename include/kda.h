@@ -502,8 +502,8 @@ KDA_API kda_status kda_cache_read(kda_dtype dt, int n_seqs, int total_tokens,
  *               of the others are zeros.
  *   A query none of whose positions is present (absent pages, or positions past the page table)
  *   gets zeros. Cached values that a query does not see do not reach its result, NaN included.
- *   workspace   at least kda_cache_attention_workspace(...) bytes, 256-byte aligned; contents need
- *               not be initialised.
+ *   workspace   at least kda_cache_attention_workspace(...) bytes (0 for sizes that are refused),
+ *               256-byte aligned; contents need not be initialised.
  *   window 1 .. 65536 (0 is a no-op); Hq a multiple of Hkv; batch * Hkv at most 2^24, batch *
  *   window * Hq at most 2^30; max_pages at most 2^24.
  * The cache is read once for up to 64 query rows of a key/value head, a query row being one token of

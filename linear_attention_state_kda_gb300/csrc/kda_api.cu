@@ -80,6 +80,13 @@ kda_status check_head(const char* fn, kda_dtype dt, int d) {
   return KDA_OK;
 }
 
+// Sizes for which the attention's row and unit numbers fit 32 bits. (A window of at most 2^16 times a
+// batch, and that times the heads: each product before its check fits 64 bits.)
+bool attn_sizes_ok(int batch, int window, int Hq, int Hkv) {
+  const int64_t tokens = (int64_t)batch * window;
+  return (int64_t)batch * Hkv <= (1 << 24) && tokens <= (1 << 30) && tokens * Hq <= (1 << 30);
+}
+
 kda_status check_cache(const char* fn, kda_dtype dt, int n_seqs, int total, const int32_t* cu,
                        const int32_t* start, const int32_t* lens, int Hkv, int d,
                        const int32_t* table, int max_pages, const void* kc, const float* ks,
@@ -572,7 +579,7 @@ kda_status kda_cache_read(kda_dtype dt, int n_seqs, int total_tokens, const int3
 
 size_t kda_cache_attention_workspace(int batch, int window, int Hq, int Hkv, int d) {
   if (batch <= 0 || window <= 0 || window > kMaxAttnWindow || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 ||
-      (d != 64 && d != 128))
+      (d != 64 && d != 128) || !attn_sizes_ok(batch, window, Hq, Hkv))
     return 0;
   return cache_attn_workspace_bytes(batch, window, Hq, Hkv, d);
 }
@@ -591,8 +598,7 @@ kda_status kda_cache_attention(kda_dtype dt, int batch, int window, int Hq, int 
   if (st != KDA_OK) return st;
   KDA_REQUIRE(Hkv > 0 && Hq > 0 && Hq % Hkv == 0, KDA_ERR_INVALID_ARG,
               "kda_cache_attention: Hq must be a positive multiple of Hkv");
-  KDA_REQUIRE((int64_t)batch * Hkv <= (1 << 24) && (int64_t)batch * window * Hq <= (1 << 30),
-              KDA_ERR_INVALID_ARG,
+  KDA_REQUIRE(attn_sizes_ok(batch, window, Hq, Hkv), KDA_ERR_INVALID_ARG,
               "kda_cache_attention: batch * Hkv must not exceed 2^24, nor batch * window * Hq 2^30");
   if (batch == 0 || window == 0) return KDA_OK;
   KDA_REQUIRE(start, KDA_ERR_INVALID_ARG, "kda_cache_attention: start must be non-null");

@@ -139,3 +139,15 @@ def test_binding_refusals(L):
         kda.draft_verify(t, torch.zeros(2, 3), torch.zeros(2, 3), torch.zeros(2))
     with pytest.raises(ValueError):
         kda.draft_verify(t[:, :, ::2], i32(2, 3), torch.zeros(2, 3), torch.zeros(2))
+
+
+def test_attention_workspace_of_refused_sizes(L):
+    """Sizes that the call refuses need no workspace: no overflow on the way to the answer."""
+    from linear_attention_state_kda_gb300 import kda
+    for B, W, Hq, Hkv in ((1, 65536, 65536, 1), (1, 65536, 1 << 30, 1), (1 << 24, 1, 2, 2),
+                          (1 << 30, 65536, 1 << 30, 1 << 30), (1, 65536, 16385, 1),
+                          (1 << 24, 65536, 1 << 30, 1)):
+        assert kda.cache_attention_workspace(B, W, Hq, Hkv, 128) == 0, (B, W, Hq, Hkv)
+        assert _attn(L, B=B, W=W, Hq=Hq, Hkv=Hkv, n=0) == kda.KDA_ERR_INVALID_ARG
+    most = kda.cache_attention_workspace(1, 65536, 16384, 1, 128)
+    assert 2 ** 29 < most < 2 ** 31
