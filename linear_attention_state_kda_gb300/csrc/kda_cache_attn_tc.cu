@@ -218,6 +218,7 @@ attn_tc_kernel(const CacheAttnParams p, int piece_rows, float* ws_o, float2* ws_
     piece = s_work[slot];
     piece.first = __shfl_sync(0xffffffffu, piece.first, 0);
     piece.last = __shfl_sync(0xffffffffu, piece.last, 0);
+    __syncwarp();  // every lane has read it (a shuffle orders no memory)
     if (lane == 0) ptx::mbar_arrive(&bars.piece_empty[slot]);
     ++taken;
     return piece.last > piece.first;
