@@ -458,6 +458,10 @@ KDA_API kda_status kda_head_norm_rope(kda_dtype dt, int tokens, int Hq, int Hk, 
  *     codes of the kept tokens become rn_e4m3(code * scale / s); new codes are rn_e4m3(x / s),
  *     ties to even, saturating at +-448 (infinities too); NaN is stored as the NaN code.
  * Rows of a page after the last new token hold no defined value.
+ * A scale only grows while a page keeps tokens. Tokens that are taken back later (refused drafts,
+ * overwritten by the next window) can have raised it, and the kept codes were rounded for it: what a
+ * page holds may depend on drafts that were refused, by the rounding of codes that the larger scale
+ * put among the format's subnormals.
  *   k, v        [total_tokens, Hkv, d] (dtype dt), heads contiguous, tokens k_stride and v_stride
  *               elements apart (multiples of 16 bytes; 16-byte aligned).
  *   cu_seqlens  device int32 [n_seqs + 1], or NULL for one sequence of total_tokens.
@@ -479,7 +483,9 @@ KDA_API kda_status kda_cache_write(kda_dtype dt, int n_seqs, int total_tokens,
 /*
  * kda_cache_read: the cached keys and values of positions start[s] .. start[s] + len_s - 1 of
  * each sequence, packed by cu_seqlens (len_s = cu_seqlens[s+1] - cu_seqlens[s]), as code * scale
- * in dtype dt. Tokens of absent pages, or of a sequence with a negative start, are zeros.
+ * in dtype dt. Tokens of absent pages, or of a sequence with a negative start, are zeros. Rows that
+ * no sequence covers (before cu_seqlens[0], from cu_seqlens[n_seqs] on, those of a malformed range)
+ * are not written.
  *   k, v  [total_tokens, Hkv, d] outputs, contiguous, 16-byte aligned; either may be NULL.
  * Other arguments as for kda_cache_write.
  */
@@ -514,9 +520,10 @@ KDA_API kda_status kda_cache_read(kda_dtype dt, int n_seqs, int total_tokens,
  * Scores, softmax statistics and sums are fp32. With bf16 queries the probabilities enter the
  * second product rounded to 11 bits; with fp32 queries, queries and probabilities are carried in
  * two 11-bit parts.
- * A row that only sees values of scales below 2^-80 (2^e at the most) has its probabilities rounded to
- * 2^-(111 + e) of the largest besides: 2^-11 where all scales are 2^-100. Where a row sees value scales
- * more than 2^109 apart, probabilities of the smallest begin to be lost from the softmax's sum.
+ * A row that only sees values of scales below 2^-80 (2^e at the most) has its probabilities rounded
+ * to 2^-(111 + e) of the largest besides: 2^-11 where all scales are 2^-100. Where a row sees value
+ * scales more than 2^109 apart, probabilities of the smallest begin to be lost from the softmax's
+ * sum.
  */
 KDA_API size_t kda_cache_attention_workspace(int batch, int window, int Hq, int Hkv, int d);
 KDA_API kda_status kda_cache_attention(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d,

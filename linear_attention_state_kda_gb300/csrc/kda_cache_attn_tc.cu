@@ -24,7 +24,7 @@
 //
 // What bounds it: the products take 2048 cycles per 256 x 128 scores, the exponentials as long at
 // their full rate, and waits of some 150 cycles lie between a row tile's scores, softmax and values;
-// measured 3.9 thousand. 4 chunks of 1024 tokens after 16384, 32/8 heads: 598 us, 1212 TFLOP/s (63%
+// measured 3.9 thousand. 4 chunks of 1024 tokens after 16384, 32/8 heads: 602 us, 1203 TFLOP/s (62%
 // of the measured bf16 rate, 70% of the sustained one); 321 TFLOP/s with warp MMAs. Taking out the
 // widening gains 2%, the loads of the codes 5%, the exponentials nothing. What it took, in TFLOP/s
 // there:
@@ -36,8 +36,9 @@
 //                instruction cache missed on a third of its requests)
 //  1068 -> 1146  barriers that are due together are looked at together
 //  1146 -> 1200  the join of the units that were cut (join_kernel)
+//  1212 -> 1203  waits for a whole piece, which look whether another role gave up
 // Handing P over a page at a time gave 509 against 477 TFLOP/s where only one row tile has rows, and
-// 1090 against 1146 here; taking the exponentials while the largest score is looked for, and
+// 1090 against 1146 there; taking the exponentials while the largest score is looked for, and
 // beginning the tile again where it turns out too large, 1068 against 1213. Neither was kept.
 // Tensor memory: 128 columns of S and d of O per row tile.
 #include "kda_cache_attn.cuh"

@@ -13,10 +13,11 @@
 // because rot_dim is a multiple of 16). So a lane needs each angle once, and no shuffles but the
 // sum of squares'. Weights and rotation are two factors per channel, y_u = r (u w_u cos - v w_v sin),
 // y_v = r (v w_v cos + u w_u sin), computed once for the heads of a token that a warp takes, and
-// applied with packed fp32 operations. Every row load is issued before the first is reduced: 55 us
-// for 16384 tokens of 32 + 8 heads at d = 128, 6.2 TB/s, 92% of the copy rate. (Four rows a lane
-// instead of eight 57, two 62. 16-byte chunks with the partner's fetched by shuffles took 67, with
-// twice the instructions; a persistent grid that loads a token ahead measured the same as that.)
+// applied with packed fp32 operations. Every row load is issued before the first is reduced: 57.5 us
+// for 16384 tokens of 32 + 8 heads at d = 128, 6.0 TB/s, 88% of the copy rate. (In a run in which it
+// took 55: four rows a lane instead of eight 57, two 62. 16-byte chunks with the partner's fetched by
+// shuffles took 67, with twice the instructions; a persistent grid that loads a token ahead measured
+// the same as that.)
 #include "kda_internal.cuh"
 
 namespace kda {

@@ -1,8 +1,9 @@
 """Thin Python binding of libkda.so (include/kda.h): one function per C entry point.
 
-Argument marshalling only (ctypes, or a compiled module for the serving operators): tensors are passed as raw device pointers with their sizes, on
-the current torch CUDA stream; every step of the computation runs in the library's CUDA
-kernels. Outputs that the caller does not supply are allocated with torch (plumbing).
+Argument marshalling only (ctypes, or a compiled module for the serving operators): tensors are
+passed as raw device pointers with their sizes, on the current torch CUDA stream; every step of
+the computation runs in the library's CUDA kernels. Outputs that the caller does not supply are
+allocated with torch (plumbing).
 Loading fails loudly if the library was not built: there is no fallback.
 """
 import ctypes
@@ -487,7 +488,8 @@ def cache_write(k, v, start, page_table, k_cache, k_scale, v_cache, v_scale, cu_
                 lens=None, status=None, stream=None):
     """kda_cache_write: quantises k and v [T, Hkv, d] (views of a fused projection's rows are fine)
     into the paged cache [n_pages, Hkv, 64, d] with scales [n_pages, Hkv], token i of sequence s at
-    position start[s] + i. The caches and scales are updated in place."""
+    position start[s] + i. The caches and scales are updated in place. A page's scale only grows
+    while it keeps tokens, also for drafted tokens that are refused later."""
     r = (_native_module or _native()).cache_write(
         k, v, start, page_table, k_cache, k_scale, v_cache, v_scale, cu_seqlens, lens, status,
         _handle(stream))
@@ -498,7 +500,8 @@ def cache_write(k, v, start, page_table, k_cache, k_scale, v_cache, v_scale, cu_
 def cache_read(start, page_table, k_cache, k_scale, v_cache, v_scale, total_tokens,
                cu_seqlens=None, dtype=torch.bfloat16, k=None, v=None, status=None, stream=None):
     """kda_cache_read: cached keys and values of positions start[s] .. of each sequence, packed by
-    cu_seqlens (total_tokens rows in all). Returns (k, v), [total_tokens, Hkv, d] of `dtype`."""
+    cu_seqlens (total_tokens rows in all; rows that no sequence covers are not written). Returns
+    (k, v), [total_tokens, Hkv, d] of `dtype`."""
     r = (_native_module or _native()).cache_read(
         start, page_table, k_cache, k_scale, v_cache, v_scale, total_tokens, cu_seqlens, dtype, k,
         v, status, _handle(stream))
@@ -518,7 +521,8 @@ def cache_attention(q, start, page_table, k_cache, k_scale, v_cache, v_scale, sc
     of row b at position start[b] + j, seeing the cached positions 0 .. start[b] + j: one decoded
     token, a verify window, or a chunk of a prompt (any window up to 65536). `workspace`
     (uint8 device tensor of at least cache_attention_workspace(...) bytes) is allocated here when
-    not given. Returns o, shaped like q."""
+    not given. Returns o, shaped like q. `status` (int32) tells of pages that were skipped, and of a
+    wait inside the kernel that gave up, which leaves o undefined."""
     r = (_native_module or _native()).cache_attention(
         q, start, page_table, k_cache, k_scale, v_cache, v_scale, scale, lens, o, workspace, status,
         _handle(stream))
