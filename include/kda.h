@@ -570,6 +570,117 @@ KDA_API kda_status kda_draft_verify(kda_dtype dt, int batch, int window, int voc
                                     int32_t* n_accepted, int32_t* resume_slots, uint32_t* status,
                                     kda_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Contexts of any length in bounded memory: linear-attention layers whose decay is one number per
+ * head (no delta rule), with the same packed sequences and state pools as the KDA calls, and the
+ * eviction of cached tokens by accumulated attention weight. The pages have no counterpart of these
+ * calls.
+ *
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t     per sequence and head
+ *
+ *   q, k        [tokens, Hk, d] (dtype dt); v, o [tokens, H, d], H a multiple of Hk: head h reads
+ *               q and k of head h / (H / Hk). Heads contiguous, tokens q_stride, k_stride and
+ *               v_stride elements apart (views of a fused projection's rows; multiples of 16
+ *               bytes); o contiguous. All 16-byte aligned.
+ *   g           fp32 log-decays, g <= 0: [tokens, H] rows g_stride elements apart, or, with
+ *               g_stride 0, [H]: one constant decay per head. Minus infinity (a reset) is allowed;
+ *               a decay below e^-277 counts as that.
+ *   d           64 or 128. States are [.., H, d, d] fp32 (row = key channel), 16-byte aligned.
+ * States and sums are fp32. Infinities and NaN in a token's inputs reach the outputs of their own
+ * sequence and heads only, from the first token of the 64-token chunk on that holds the token
+ * (chunks are counted from the sequence's start).
+ * ------------------------------------------------------------------------------------------ */
+
+/*
+ * kda_decay_prefill: packed prompts in chunks.
+ *   cu_seqlens  device int32 [n_seqs + 1], or NULL for one sequence of total_tokens. Rows of o that
+ *               no sequence covers are not written.
+ *   init_state  [n_seqs, H, d, d] entry states or NULL for zeros; final_state the exit states or
+ *               NULL (not the same buffer). An empty sequence passes its state through.
+ *   workspace   at least kda_decay_prefill_workspace(...) bytes (0 for sizes that are refused or
+ *               need none), 256-byte aligned; contents need not be initialised.
+ *   n_seqs at most 2^24, H at most 65535.
+ *   status      optional device word (KDA_STATUS_BAD_OFFSETS, KDA_STATUS_TIMEOUT).
+ * bf16 runs on the tensor cores (KDA_ERR_UNSUPPORTED when the driver lacks cuTensorMapEncodeTiled),
+ * fp32 on CUDA cores. With bf16 the state enters the outputs as two bf16 parts (16 bits), as do
+ * the products q.k, and new keys and values enter the state as three (24 bits).
+ */
+KDA_API size_t kda_decay_prefill_workspace(kda_dtype dt, int n_seqs, int total_tokens, int H, int d);
+KDA_API kda_status kda_decay_prefill(kda_dtype dt, int n_seqs, int total_tokens,
+                                     const int32_t* cu_seqlens, int H, int Hk, int d, float scale,
+                                     const void* q, int64_t q_stride, const void* k,
+                                     int64_t k_stride, const void* v, int64_t v_stride,
+                                     const float* g, int64_t g_stride, const float* init_state,
+                                     void* o, float* final_state, void* workspace, size_t ws_bytes,
+                                     uint32_t* status, kda_stream_t stream);
+
+/*
+ * kda_decay_window: one token, or a verify window of up to 16, per row over the slot pool. Row b
+ * reads its state from slot read_slots[b]; the state after token j (row b * window + j of the token
+ * arrays) is stored into slot write_slots[b, j]. Slots, padding rows, columns that store nothing
+ * and the pool are as for kda_decode_window; window 1 with write_slots = read_slots is a decode
+ * step in place.
+ */
+KDA_API kda_status kda_decay_window(kda_dtype dt, int batch, int window, int H, int Hk, int d,
+                                    float scale, const void* q, int64_t q_stride, const void* k,
+                                    int64_t k_stride, const void* v, int64_t v_stride,
+                                    const float* g, int64_t g_stride, const int32_t* read_slots,
+                                    const int32_t* write_slots, float* state_pool, int64_t n_slots,
+                                    void* o, uint32_t* status, kda_stream_t stream);
+
+/*
+ * kda_cache_weigh: adds the attention weights of a window of queries to a weight per cached token
+ * and head. With p_i the softmax over positions of query row i of kda_cache_attention (same
+ * arguments: token j of row b sees positions 0 .. start[b] + j), for every present position
+ * t < start[b] + (tokens of row b):
+ *     weights[page, head, t % 64] = keep * weights[..] + sum_i p_i(t)
+ * over the window's tokens and the query heads of the key/value head. Positions from start[b] on
+ * (the window's own tokens) begin at the sum alone, and so does everything with keep = 0: what
+ * their entries held does not matter.
+ *   weights     [n_pages, Hkv, 64] fp32, 16-byte aligned, updated in place. Other entries are not
+ *               touched. No page may be named by two rows of one call.
+ *   A query none of whose positions is present adds nothing. Codes that a query does not see do not
+ *   reach its weights, NaN included.
+ *   Other arguments, limits and status as for kda_cache_attention. No workspace.
+ * Scores and sums are fp32 and the same on every run. bf16 queries enter at full precision, fp32
+ * ones as two 11-bit parts.
+ */
+KDA_API kda_status kda_cache_weigh(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d,
+                                   float scale, float keep, const void* q, const int32_t* start,
+                                   const int32_t* lens, const int32_t* page_table, int max_pages,
+                                   const void* k_cache, const float* k_scale, float* weights,
+                                   int64_t n_pages, uint32_t* status, kda_stream_t stream);
+
+/*
+ * kda_cache_evict: cuts the cached tokens of each row down to a budget, per head, and moves what is
+ * kept into new pages. Of the positions 0 .. length[b] - 1 of present pages a head keeps
+ *     the first `sinks` positions and the last `recent` ones, then
+ *     of the rest those with the largest weights, of equal weights the earliest,
+ * at most `budget` in all, or everything if there are no more. (NaN is the smallest weight.)
+ * The kept tokens, in order, are positions 0, 1, .. of new_table[b]: codes, weights, and per new
+ * page and head a scale that is the largest of the scales the page's tokens had; codes of smaller
+ * scales become rn_e4m3(code * old / new). Rows of a new page after the last kept token hold no
+ * defined codes, and weight 0.
+ *   length      device int32 [batch]; negative marks a padding row: nothing is moved, its
+ *               new_length is the same negative number. Positions past the page table are not kept
+ *               and set KDA_STATUS_BAD_PAGE.
+ *   new_table   device int32 [batch, new_max_pages], at least ceil(budget / 64) columns: pages of
+ *               the same pool. None of them may hold tokens of any row of the call, and none may be
+ *               named twice. A negative id drops its 64 tokens (kept still lists them).
+ *   new_length  [batch] int32 output: tokens kept.
+ *   kept        [batch, Hkv, budget] int32 output: the kept positions in ascending order, then -1.
+ *               (Keys that were rotated by their position before they were cached stay so.)
+ *   budget 0 .. 2^24; sinks + recent at most budget; batch * Hkv at most 2^24.
+ *   status      optional device word (KDA_STATUS_BAD_PAGE).
+ */
+KDA_API kda_status kda_cache_evict(int batch, int Hkv, int d, const int32_t* length,
+                                   const int32_t* page_table, int max_pages,
+                                   const int32_t* new_table, int new_max_pages, void* k_cache,
+                                   float* k_scale, void* v_cache, float* v_scale, float* weights,
+                                   int64_t n_pages, int budget, int sinks, int recent,
+                                   int32_t* new_length, int32_t* kept, uint32_t* status,
+                                   kda_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -112,6 +112,32 @@ kda_status check_cache(const char* fn, kda_dtype dt, int n_seqs, int total, cons
   return KDA_OK;
 }
 
+// What the calls of linear attention with one decay per head share.
+kda_status check_decay_heads(const char* fn, kda_dtype dt, int H, int Hk, int d) {
+  kda_status st = check_head(fn, dt, d);
+  if (st != KDA_OK) return st;
+  KDA_REQUIRE(Hk > 0 && H > 0 && H <= 65535 && H % Hk == 0, KDA_ERR_INVALID_ARG,
+              std::string(fn) + ": H must be a positive multiple of Hk, at most 65535");
+  return KDA_OK;
+}
+kda_status check_decay(const char* fn, kda_dtype dt, int d, const DecayParams& p) {
+  const std::string f(fn);
+  KDA_REQUIRE(p.q && p.k && p.v && p.g && p.o, KDA_ERR_INVALID_ARG,
+              f + ": q, k, v, g and o must be non-null");
+  const int64_t per16 = 16 / elem_bytes(dt);
+  KDA_REQUIRE(row_stride_ok(p.qs, (int64_t)p.Hk * d, per16) &&
+                  row_stride_ok(p.ks, (int64_t)p.Hk * d, per16) &&
+                  row_stride_ok(p.vs, (int64_t)p.H * d, per16),
+              KDA_ERR_INVALID_ARG,
+              f + ": token strides must cover the heads and be multiples of 16 bytes");
+  KDA_REQUIRE(p.gs == 0 || p.gs >= p.H, KDA_ERR_INVALID_ARG,
+              f + ": g_stride must be 0 (one decay per head) or at least H");
+  KDA_REQUIRE(aligned(p.q, 16) && aligned(p.k, 16) && aligned(p.v, 16) && aligned(p.o, 16) &&
+                  aligned(p.g, 4) && aligned(p.status, 4),
+              KDA_ERR_INVALID_ARG, f + ": misaligned pointer");
+  return KDA_OK;
+}
+
 }  // namespace
 }  // namespace kda
 
@@ -661,6 +687,147 @@ kda_status kda_draft_verify(kda_dtype dt, int batch, int window, int vocab,
   p.slots = write_slots; p.tokens = tokens; p.n_accepted = n_accepted; p.resume = resume_slots;
   p.status = status;
   return launch_verify(p, dt, (cudaStream_t)stream);
+}
+
+size_t kda_decay_prefill_workspace(kda_dtype dt, int n_seqs, int total_tokens, int H, int d) {
+  if ((dt != KDA_F32 && dt != KDA_BF16) || n_seqs <= 0 || total_tokens <= 0 || H <= 0 ||
+      H > 65535 || (d != 64 && d != 128))
+    return 0;
+  return decay_prefill_workspace_bytes(dt, total_tokens, H, d);
+}
+
+kda_status kda_decay_prefill(kda_dtype dt, int n_seqs, int total_tokens, const int32_t* cu_seqlens,
+                             int H, int Hk, int d, float scale, const void* q, int64_t q_stride,
+                             const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             const float* g, int64_t g_stride, const float* init_state, void* o,
+                             float* final_state, void* workspace, size_t ws_bytes,
+                             uint32_t* status, kda_stream_t stream) {
+  const char* fn = "kda_decay_prefill";
+  kda_status st = check_decay_heads(fn, dt, H, Hk, d);
+  if (st != KDA_OK) return st;
+  KDA_REQUIRE(n_seqs >= 0 && n_seqs <= (1 << 24) && total_tokens >= 0, KDA_ERR_INVALID_ARG,
+              "kda_decay_prefill: n_seqs must be in 0 .. 2^24, total_tokens >= 0");
+  KDA_REQUIRE(cu_seqlens || n_seqs <= 1, KDA_ERR_INVALID_ARG,
+              "kda_decay_prefill: cu_seqlens is required for more than one sequence");
+  if (n_seqs == 0 || (total_tokens == 0 && !final_state)) return KDA_OK;
+  DecayParams p{};
+  p.q = q; p.k = k; p.v = v; p.qs = q_stride; p.ks = k_stride; p.vs = v_stride;
+  p.g = g; p.gs = g_stride; p.H = H; p.Hk = Hk; p.scale = scale; p.o = o; p.status = status;
+  p.n_seqs = n_seqs; p.total = total_tokens; p.cu = cu_seqlens;
+  p.init = init_state; p.final_state = final_state;
+  if (total_tokens > 0 && (st = check_decay(fn, dt, d, p)) != KDA_OK) return st;
+  KDA_REQUIRE(aligned(init_state, 16) && aligned(final_state, 16) && aligned(cu_seqlens, 4) &&
+                  aligned(status, 4),
+              KDA_ERR_INVALID_ARG, "kda_decay_prefill: states must be 16-byte aligned");
+  KDA_REQUIRE(!final_state || final_state != init_state, KDA_ERR_INVALID_ARG,
+              "kda_decay_prefill: final_state must not alias init_state");
+  const size_t need = kda_decay_prefill_workspace(dt, n_seqs, total_tokens, H, d);
+  KDA_REQUIRE(need == 0 || (workspace && ws_bytes >= need && aligned(workspace, 256)),
+              KDA_ERR_WORKSPACE,
+              "kda_decay_prefill: workspace missing, too small or not 256-byte aligned (need " +
+                  std::to_string(need) + " bytes)");
+  p.ws = need ? workspace : nullptr;
+  return launch_decay_prefill(p, dt, d, (cudaStream_t)stream);
+}
+
+kda_status kda_decay_window(kda_dtype dt, int batch, int window, int H, int Hk, int d, float scale,
+                            const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const float* g, int64_t g_stride,
+                            const int32_t* read_slots, const int32_t* write_slots,
+                            float* state_pool, int64_t n_slots, void* o, uint32_t* status,
+                            kda_stream_t stream) {
+  const char* fn = "kda_decay_window";
+  kda_status st = check_decay_heads(fn, dt, H, Hk, d);
+  if (st != KDA_OK) return st;
+  KDA_REQUIRE(batch >= 0, KDA_ERR_INVALID_ARG, "kda_decay_window: batch must be >= 0");
+  KDA_REQUIRE(window >= 0 && window <= kMaxWindow, KDA_ERR_UNSUPPORTED,
+              "kda_decay_window: window must be in 0 .. 16");
+  KDA_REQUIRE(n_slots > 0, KDA_ERR_INVALID_ARG, "kda_decay_window: n_slots must be > 0");
+  if (batch == 0 || window == 0) return KDA_OK;
+  DecayParams p{};
+  p.q = q; p.k = k; p.v = v; p.qs = q_stride; p.ks = k_stride; p.vs = v_stride;
+  p.g = g; p.gs = g_stride; p.H = H; p.Hk = Hk; p.scale = scale; p.o = o; p.status = status;
+  p.batch = batch; p.window = window; p.read_slots = read_slots; p.write_slots = write_slots;
+  p.pool = state_pool; p.n_slots = n_slots;
+  st = check_decay(fn, dt, d, p);
+  if (st != KDA_OK) return st;
+  KDA_REQUIRE(read_slots && write_slots && state_pool, KDA_ERR_INVALID_ARG,
+              "kda_decay_window: slots and state_pool must be non-null");
+  KDA_REQUIRE((int64_t)batch * window * H <= (1LL << 30), KDA_ERR_INVALID_ARG,
+              "kda_decay_window: batch * window * H must not exceed 2^30");
+  KDA_REQUIRE(aligned(state_pool, 16) && aligned(read_slots, 4) && aligned(write_slots, 4),
+              KDA_ERR_INVALID_ARG, "kda_decay_window: misaligned pointer");
+  return launch_decay_window(p, dt, d, (cudaStream_t)stream);
+}
+
+kda_status kda_cache_weigh(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d, float scale,
+                           float keep, const void* q, const int32_t* start, const int32_t* lens,
+                           const int32_t* page_table, int max_pages, const void* k_cache,
+                           const float* k_scale, float* weights, int64_t n_pages, uint32_t* status,
+                           kda_stream_t stream) {
+  const char* fn = "kda_cache_weigh";
+  KDA_REQUIRE(window >= 0 && window <= kMaxAttnWindow, KDA_ERR_UNSUPPORTED,
+              "kda_cache_weigh: window must be in 0 .. 65536");
+  KDA_REQUIRE(batch >= 0, KDA_ERR_INVALID_ARG, "kda_cache_weigh: batch must be >= 0");
+  kda_status st = check_head(fn, dt, d);
+  if (st != KDA_OK) return st;
+  KDA_REQUIRE(Hkv > 0 && Hq > 0 && Hq % Hkv == 0, KDA_ERR_INVALID_ARG,
+              "kda_cache_weigh: Hq must be a positive multiple of Hkv");
+  KDA_REQUIRE(attn_sizes_ok(batch, window, Hq, Hkv), KDA_ERR_INVALID_ARG,
+              "kda_cache_weigh: batch * Hkv must not exceed 2^24, nor batch * window * Hq 2^30");
+  if (batch == 0 || window == 0) return KDA_OK;
+  KDA_REQUIRE(start, KDA_ERR_INVALID_ARG, "kda_cache_weigh: start must be non-null");
+  st = check_cache(fn, dt, batch, batch, start, start, lens, Hkv, d, page_table, max_pages, k_cache,
+                   k_scale, nullptr, nullptr, n_pages, status);
+  if (st != KDA_OK) return st;
+  KDA_REQUIRE(q && k_cache && weights, KDA_ERR_INVALID_ARG,
+              "kda_cache_weigh: q, k_cache and weights must be non-null");
+  KDA_REQUIRE(aligned(q, 16) && aligned(weights, 16), KDA_ERR_INVALID_ARG,
+              "kda_cache_weigh: q and weights must be 16-byte aligned");
+  WeighParams p{};
+  p.batch = batch; p.window = window; p.Hq = Hq; p.Hkv = Hkv; p.scale = scale; p.keep = keep;
+  p.q = q; p.start = start; p.lens = lens; p.table = page_table; p.max_pages = max_pages;
+  p.n_pages = n_pages; p.kc = (const uint8_t*)k_cache; p.ks = k_scale; p.weights = weights;
+  p.status = status;
+  return launch_cache_weigh(p, dt, d, (cudaStream_t)stream);
+}
+
+kda_status kda_cache_evict(int batch, int Hkv, int d, const int32_t* length,
+                           const int32_t* page_table, int max_pages, const int32_t* new_table,
+                           int new_max_pages, void* k_cache, float* k_scale, void* v_cache,
+                           float* v_scale, float* weights, int64_t n_pages, int budget, int sinks,
+                           int recent, int32_t* new_length, int32_t* kept, uint32_t* status,
+                           kda_stream_t stream) {
+  const char* fn = "kda_cache_evict";
+  KDA_REQUIRE(budget >= 0 && budget <= (1 << 24) && sinks >= 0 && recent >= 0 &&
+                  (int64_t)sinks + recent <= budget,
+              KDA_ERR_INVALID_ARG,
+              "kda_cache_evict: budget must be in 0 .. 2^24, sinks and recent >= 0 and at most "
+              "budget together");
+  kda_status st = check_cache(fn, KDA_F32, batch, batch, length, length, nullptr, Hkv, d, page_table,
+                              max_pages, k_cache, k_scale, v_cache, v_scale, n_pages, status);
+  if (st != KDA_OK || batch == 0) return st;
+  const int width = (budget + kPage - 1) / kPage;
+  KDA_REQUIRE((int64_t)batch * Hkv <= (1 << 24) && (int64_t)batch * width <= 0x7fffffffLL,
+              KDA_ERR_INVALID_ARG,
+              "kda_cache_evict: batch * Hkv must not exceed 2^24, nor batch * new pages 2^31");
+  KDA_REQUIRE(k_cache && v_cache && weights && new_length && (budget == 0 || (kept && new_table)),
+              KDA_ERR_INVALID_ARG,
+              "kda_cache_evict: caches, weights, new_table, new_length and kept must be non-null");
+  KDA_REQUIRE(new_max_pages >= width, KDA_ERR_INVALID_ARG,
+              "kda_cache_evict: new_table must have a column for every page of the budget");
+  KDA_REQUIRE(aligned(weights, 16) && aligned(new_table, 4) && aligned(new_length, 4) &&
+                  aligned(kept, 4) && new_length != length,
+              KDA_ERR_INVALID_ARG,
+              "kda_cache_evict: misaligned pointer, or new_length in place of length");
+  EvictParams p{};
+  p.batch = batch; p.Hkv = Hkv; p.length = length; p.table = page_table; p.max_pages = max_pages;
+  p.new_table = new_table; p.new_max_pages = new_max_pages; p.n_pages = n_pages;
+  p.code[0] = (uint8_t*)k_cache; p.code[1] = (uint8_t*)v_cache;
+  p.scale[0] = k_scale; p.scale[1] = v_scale; p.weights = weights;
+  p.budget = budget; p.sinks = sinks; p.recent = recent;
+  p.new_length = new_length; p.kept = kept; p.status = status;
+  return launch_cache_evict(p, d, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -485,11 +485,222 @@ PyObject* draft_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// q, k, v, g of linear attention with one decay per head.
+struct DecayIn {
+  const Tensor &q, &k, &v, &g;
+  at::ScalarType type;
+  kda_dtype dt;
+  int H, Hk, d;
+  int64_t T, qs, ks, vs, gs;
+  const float* gp;
+  DecayIn(Devices& dv, PyObject* const* a)
+      : q(need(a[0], "q")), k(need(a[1], "k")), v(need(a[2], "v")), g(need(a[3], "g")) {
+    type = v.scalar_type();
+    dt = code_of(type, "q, k and v");
+    require(q.dim() == 3 && v.dim() == 3 && q.sizes() == k.sizes() && q.size(0) == v.size(0) &&
+                q.size(2) == v.size(2),
+            "must be [tokens, Hk, d], [tokens, Hk, d] and [tokens, H, d]", "q, k and v");
+    T = v.size(0);
+    Hk = as_int(q.size(1), "Hk");
+    H = as_int(v.size(1), "H");
+    d = as_int(v.size(2), "d");
+    qs = heads(dv, q, q.sizes(), type, "q");
+    ks = heads(dv, k, q.sizes(), type, "k");
+    vs = heads(dv, v, v.sizes(), type, "v");
+    require_type(g.scalar_type() == at::kFloat, "must be float32", "g");
+    const bool constant = g.dim() == 1;
+    require((constant ? g.size(0) == H : g.dim() == 2 && g.size(0) == T && g.size(1) == H) &&
+                (g.stride(-1) == 1 || H <= 1),
+            "must be [tokens, H] or [H] with contiguous heads", "g");
+    gs = constant ? 0 : T > 1 ? g.stride(0) : H;
+    dv.see(g);
+    gp = static_cast<const float*>(g.data_ptr());
+  }
+};
+
+// q, k, v, g, cu_seqlens, init_state, scale, o, final_state, want_final, status, workspace, stream
+PyObject* decay_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 13);
+  Devices dv;
+  const DecayIn x(dv, a);
+  const Tensor* cu = opt(a[4], "cu_seqlens");
+  require(!cu || cu->numel() >= 1, "must hold n + 1 offsets", "cu_seqlens");
+  const int64_t N = cu ? cu->numel() - 1 : 1;
+  const int32_t* cup = vec<int32_t>(dv, cu, at::kInt, N + 1, "cu_seqlens");
+  const int64_t states = N * x.H * x.d * x.d;
+  const float* init = vec<float>(dv, opt(a[5], "init_state"), at::kFloat, states, "init_state");
+  uint32_t* status = status_of(dv, a[10]);
+  dv.check();
+  const CallStream on(a[12]);
+  const auto opts = at::TensorOptions().dtype(x.type).device(x.v.device());
+  Out o, fin, ws;
+  o.set(a[7], x.v.sizes(), opts, "o");
+  void* op = vec(dv, o.t, x.type, x.v.numel(), "o");
+  const bool has_final = a[8] != Py_None || as_bool(a[9]);
+  if (has_final) fin.set(a[8], {N, x.H, x.d, x.d}, opts.dtype(at::kFloat), "final_state");
+  float* fp = vec<float>(dv, fin.t, at::kFloat, states, "final_state");
+  const int ns = as_int(N, "n_seqs"), T = as_int(x.T, "tokens");
+  int64_t bytes = (int64_t)kda_decay_prefill_workspace(x.dt, ns, T, x.H, x.d);
+  void* wp = nullptr;
+  if (bytes > 0 || a[11] != Py_None) {
+    ws.set(a[11], {bytes}, opts.dtype(at::kByte), "workspace");
+    require(ws.t->is_contiguous(), "must be contiguous", "workspace");
+    dv.see(*ws.t);
+    bytes = (int64_t)ws.t->nbytes();
+    wp = ws.t->data_ptr();
+  }
+  dv.check();
+  const float scale = (float)as_double(a[6]);
+  const kda_status st = [&] {
+    NoGil g;
+    return kda_decay_prefill(x.dt, ns, T, cup, x.H, x.Hk, x.d, scale, x.q.data_ptr(), x.qs,
+                             x.k.data_ptr(), x.ks, x.v.data_ptr(), x.vs, x.gp, x.gs, init, op, fp,
+                             wp, (size_t)bytes, status, on.s);
+  }();
+  if (st != KDA_OK) return PyLong_FromLong(st);
+  o.handed_to(on);
+  fin.handed_to(on);
+  return tuple_of({o.object(), has_final ? fin.object() : none()});
+  END_HANDLE_TH_ERRORS
+}
+
+// q, k, v, g, read_slots, write_slots, state_pool, scale, o, status, stream
+PyObject* decay_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 11);
+  Devices dv;
+  const DecayIn x(dv, a);
+  const Tensor &rs = need(a[4], "read_slots"), &ws = need(a[5], "write_slots"),
+               &pool = need(a[6], "state_pool");
+  const int64_t B = rs.numel(), W = B ? ws.numel() / B : 0;
+  require(x.T == B * W, "must be [batch, window] with a column for each token of a row",
+          "write_slots");
+  const int32_t* rp = vec<int32_t>(dv, &rs, at::kInt, B, "read_slots");
+  const int32_t* wp = vec<int32_t>(dv, &ws, at::kInt, x.T, "write_slots");
+  require(pool.dim() == 4 && pool.size(1) == x.H && pool.size(2) == x.d && pool.size(3) == x.d,
+          "must be [n_slots, H, d, d]", "state_pool");
+  float* pp = vec<float>(dv, &pool, at::kFloat, pool.numel(), "state_pool");
+  uint32_t* status = status_of(dv, a[9]);
+  dv.check();
+  const CallStream on(a[10]);
+  Out o;
+  o.set(a[8], x.v.sizes(), at::TensorOptions().dtype(x.type).device(x.v.device()), "o");
+  void* op = vec(dv, o.t, x.type, x.v.numel(), "o");
+  dv.check();
+  const int b = as_int(B, "batch"), w = as_int(W, "window");
+  const int64_t slots = pool.size(0);
+  const float scale = (float)as_double(a[7]);
+  const kda_status st = [&] {
+    NoGil g;
+    return kda_decay_window(x.dt, b, w, x.H, x.Hk, x.d, scale, x.q.data_ptr(), x.qs, x.k.data_ptr(),
+                            x.ks, x.v.data_ptr(), x.vs, x.gp, x.gs, rp, wp, pp, slots, op, status,
+                            on.s);
+  }();
+  if (st != KDA_OK) return PyLong_FromLong(st);
+  o.handed_to(on);
+  return o.object();
+  END_HANDLE_TH_ERRORS
+}
+
+// Weights of the cached tokens.
+float* weights_of(Devices& dv, PyObject* o, int64_t n_pages, int64_t H) {
+  const Tensor& t = need(o, "weights");
+  require(t.dim() == 3 && t.size(0) == n_pages && t.size(1) == H && t.size(2) == kPage,
+          "must be [n_pages, Hkv, 64]", "weights");
+  return vec<float>(dv, &t, at::kFloat, t.numel(), "weights");
+}
+
+// q, start, page_table, k_cache, k_scale, weights, scale, lens, keep, status, stream
+PyObject* cache_weigh(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 11);
+  const Tensor &q = need(a[0], "q"), &start = need(a[1], "start");
+  Devices dv;
+  const int64_t B = start.numel();
+  // the keys' side alone
+  PyObject* const side[5] = {a[2], a[3], a[4], a[3], a[4]};
+  const Cache c = cache_of(dv, side, B);
+  const auto type = q.scalar_type();
+  const kda_dtype dt = code_of(type, "q");
+  require(q.dim() >= 3 && q.size(-1) == c.d, "must be [.., Hq, d] with the cache's head size", "q");
+  const int64_t Hq = q.size(-2), size = q.numel(), per = B * Hq * c.d;
+  const int64_t W = per ? size / per : 0;
+  require(W * per == size, "must hold batch x window tokens", "q");
+  const void* qp = vec(dv, &q, type, size, "q");
+  const int32_t* st0 = vec<int32_t>(dv, &start, at::kInt, B, "start");
+  float* wp = weights_of(dv, a[5], c.n_pages, c.H);
+  const int32_t* lens = vec<int32_t>(dv, opt(a[7], "lens"), at::kInt, B, "lens");
+  uint32_t* status = status_of(dv, a[9]);
+  dv.check();
+  const int b = as_int(B, "batch"), w = as_int(W, "window"), hq = as_int(Hq, "Hq"),
+            hkv = as_int(c.H, "Hkv"), d = as_int(c.d, "d");
+  const float scale = (float)as_double(a[6]), keep = (float)as_double(a[8]);
+  const CallStream on(a[10]);
+  const kda_status st = [&] {
+    NoGil g;
+    return kda_cache_weigh(dt, b, w, hq, hkv, d, scale, keep, qp, st0, lens, c.table, c.max_pages,
+                           c.kc, c.ks, wp, c.n_pages, status, on.s);
+  }();
+  if (st != KDA_OK) return PyLong_FromLong(st);
+  Py_INCREF(a[5]);
+  return a[5];
+  END_HANDLE_TH_ERRORS
+}
+
+// length, page_table, new_table, k_cache, k_scale, v_cache, v_scale, weights, budget, sinks, recent,
+// new_length, kept, status, stream
+PyObject* cache_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 15);
+  const Tensor &length = need(a[0], "length"), &table = need(a[2], "new_table");
+  Devices dv;
+  const int64_t B = length.numel();
+  PyObject* const side[5] = {a[1], a[3], a[4], a[5], a[6]};
+  const Cache c = cache_of(dv, side, B);
+  const int32_t* lp = vec<int32_t>(dv, &length, at::kInt, B, "length");
+  require(table.dim() == 2 && table.size(0) == B, "must be [rows, pages], a row for each length",
+          "new_table");
+  const int32_t* tp = vec<int32_t>(dv, &table, at::kInt, table.numel(), "new_table");
+  const int width = as_int(table.size(1), "new_table");
+  float* wp = weights_of(dv, a[7], c.n_pages, c.H);
+  int value[3];
+  const char* name[3] = {"budget", "sinks", "recent"};
+  for (int i = 0; i < 3; ++i) {
+    const int64_t v = PyLong_AsLongLong(a[8 + i]);
+    if (v == -1 && PyErr_Occurred()) throw python_error();
+    value[i] = as_int(v, name[i]);
+  }
+  uint32_t* status = status_of(dv, a[13]);
+  dv.check();
+  const CallStream on(a[14]);
+  const auto opts = at::TensorOptions().dtype(at::kInt).device(length.device());
+  Out taken, kept;
+  taken.set(a[11], {B}, opts, "new_length");
+  kept.set(a[12], {B, c.H, value[0]}, opts, "kept");
+  int32_t* np = vec<int32_t>(dv, taken.t, at::kInt, B, "new_length");
+  int32_t* kp = vec<int32_t>(dv, kept.t, at::kInt, B * c.H * value[0], "kept");
+  dv.check();
+  const int b = as_int(B, "batch"), hkv = as_int(c.H, "Hkv"), d = as_int(c.d, "d");
+  const kda_status st = [&] {
+    NoGil g;
+    return kda_cache_evict(b, hkv, d, lp, c.table, c.max_pages, tp, width, c.kc, c.ks, c.vc, c.vs,
+                           wp, c.n_pages, value[0], value[1], value[2], np, kp, status, on.s);
+  }();
+  if (st != KDA_OK) return PyLong_FromLong(st);
+  taken.handed_to(on);
+  kept.handed_to(on);
+  return tuple_of({taken.object(), kept.object()});
+  END_HANDLE_TH_ERRORS
+}
+
 #define KDA_METHOD(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {KDA_METHOD(head_norm_rope), KDA_METHOD(cache_write),
                          KDA_METHOD(cache_read),     KDA_METHOD(cache_attention),
-                         KDA_METHOD(draft_verify),   {nullptr, nullptr, 0, nullptr}};
+                         KDA_METHOD(draft_verify),   KDA_METHOD(decay_prefill),
+                         KDA_METHOD(decay_window),   KDA_METHOD(cache_weigh),
+                         KDA_METHOD(cache_evict),    {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_native", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,381 @@
+// Linear attention with one decay per head,
+//     S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,
+// for tokens and verify windows over the slot-addressed state pool, and, on CUDA cores, for
+// prompts in chunks. (Prompts in bf16 run on the tensor cores, kda_decay_tc.cu.)
+#include "kda_decay.cuh"
+#include "kda_fp8.cuh"
+
+namespace kda {
+namespace {
+
+using namespace decay;
+
+// ---------------------------------------------------------------- windows
+//
+// HBM-bound: a state is read once and stored once per token. As in the KDA decode kernel a CTA
+// owns 64 columns of one (row, head)'s state in registers: 8 warps own D/8 rows each, a lane two
+// columns, so that every warp moves 256-byte row segments. A column evolves on its own; the only
+// exchange is the sum over the key channels in o, one barrier a token (two sets of partial sums
+// take turns).
+constexpr int kWarps = 8;
+constexpr int kCols = 64;
+
+template <int D, class T>
+__global__ void __launch_bounds__(kWarps * 32, 4) decay_window_kernel(const DecayParams p) {
+  constexpr int NSPLIT = D / kCols;
+  constexpr int RPW = D / kWarps;
+  const int part = blockIdx.x % NSPLIT;
+  const int bh = blockIdx.x / NSPLIT;
+  const int b = bh / p.H, h = bh - b * p.H;
+  const int hk = h / (p.H / p.Hk);
+  const int W = p.window;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r0 = warp * RPW, c0 = lane * 2, cg = part * kCols + c0;
+
+  extern __shared__ float win[];  // [W][D] q, k; [W][64] v; [W] decays
+  float* s_q = win;
+  float* s_k = s_q + W * D;
+  float* s_v = s_k + W * D;
+  float* s_a = s_v + W * kCols;
+  __shared__ float red[2][kWarps][kCols];
+
+  const int64_t tok0 = (int64_t)b * W;
+  T* o = (T*)p.o;
+  const int slot = p.read_slots[b];
+  if (slot < 0 || (int64_t)slot >= p.n_slots) {
+    if ((int64_t)slot >= p.n_slots && threadIdx.x == 0 && h == 0 && part == 0 && p.status)
+      atomicOr(p.status, KDA_STATUS_BAD_SLOT);
+    for (int i = threadIdx.x; i < W * kCols; i += blockDim.x)
+      st_elem(o, ((tok0 + i / kCols) * p.H + h) * D + part * kCols + i % kCols, 0.0f);
+    return;
+  }
+  const float* S = p.pool + ((int64_t)slot * p.H + h) * (int64_t)(D * D);
+  float2 st[RPW];
+#pragma unroll
+  for (int i = 0; i < RPW; ++i)
+    st[i] = __ldcs(reinterpret_cast<const float2*>(S + (int64_t)(r0 + i) * D + cg));
+
+  const T *q = (const T*)p.q + (int64_t)hk * D, *k = (const T*)p.k + (int64_t)hk * D,
+          *v = (const T*)p.v + (int64_t)h * D + part * kCols;
+  for (int i = threadIdx.x; i < W * D; i += blockDim.x) {
+    const int64_t t = tok0 + i / D;
+    s_q[i] = ld_elem(q, t * p.qs + i % D);
+    s_k[i] = ld_elem(k, t * p.ks + i % D);
+  }
+  for (int i = threadIdx.x; i < W * kCols; i += blockDim.x)
+    s_v[i] = ld_elem(v, (tok0 + i / kCols) * p.vs + i % kCols);
+  for (int j = threadIdx.x; j < W; j += blockDim.x) s_a[j] = expf(p.g[(tok0 + j) * p.gs + h]);
+  __syncthreads();
+
+  for (int j = 0; j < W; ++j) {
+    const float* kr = s_k + j * D + r0;
+    const float* qr = s_q + j * D + r0;
+    const float a = s_a[j], v0 = s_v[j * kCols + c0], v1 = s_v[j * kCols + c0 + 1];
+    float y0 = 0.0f, y1 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < RPW; ++i) {
+      st[i].x = fmaf(kr[i], v0, st[i].x * a);
+      st[i].y = fmaf(kr[i], v1, st[i].y * a);
+      y0 = fmaf(qr[i], st[i].x, y0);
+      y1 = fmaf(qr[i], st[i].y, y1);
+    }
+    *reinterpret_cast<float2*>(&red[j & 1][warp][c0]) = make_float2(y0, y1);
+    const int ws = p.write_slots[tok0 + j];
+    if ((int64_t)ws >= p.n_slots) {
+      if (threadIdx.x == 0 && h == 0 && part == 0 && p.status)
+        atomicOr(p.status, KDA_STATUS_BAD_SLOT);
+    } else if (ws >= 0) {
+      float* out = p.pool + ((int64_t)ws * p.H + h) * (int64_t)(D * D);
+#pragma unroll
+      for (int i = 0; i < RPW; ++i)
+        __stcs(reinterpret_cast<float2*>(out + (int64_t)(r0 + i) * D + cg), st[i]);
+    }
+    __syncthreads();
+    if (threadIdx.x < kCols) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s += red[j & 1][w][threadIdx.x];
+      st_elem(o, ((tok0 + j) * p.H + h) * D + part * kCols + threadIdx.x, p.scale * s);
+    }
+  }
+}
+
+template <int D, class T>
+kda_status launch_window_t(const DecayParams& p, cudaStream_t s) {
+  const size_t smem = (size_t)p.window * (2 * D + kCols + 1) * sizeof(float);
+  const dim3 grid((unsigned)p.batch * (unsigned)p.H * (unsigned)(D / kCols));
+  decay_window_kernel<D, T><<<grid, kWarps * 32, smem, s>>>(p);
+  count_launches(1);
+  return check_launch("kda_decay_window");
+}
+
+// ---------------------------------------------------------------- prompts on CUDA cores
+//
+// fp32 throughout. A CTA walks one segment of one head for 64 value columns in chunks of 32
+// tokens. With gamma the running sum of g in the chunk,
+//     o_i = e^{gamma_i} scale S^T q_i + sum_{j <= i} e^{gamma_i - gamma_j} scale (q_i . k_j) v_j
+//     S'  = e^{gamma_C} S + sum_j e^{gamma_C - gamma_j} k_j v_j^T
+// The state is in registers (D/16 x 4 a thread), copied to shared memory for the first sum.
+constexpr int kC = 32;
+constexpr int kSimtThreads = 256;
+
+template <int D>
+struct SimtShape {
+  static constexpr int DP = D + 4, VP = kCols + 4, PP = kC + 1;
+  static constexpr int floats = 2 * kC * DP + kC * VP + D * VP + kC * PP;
+};
+
+template <int D, class T, bool kStates>
+__global__ void __launch_bounds__(kSimtThreads)
+decay_chunk_kernel(const DecayParams p, int seg, float* added, float* added_log) {
+  using S = SimtShape<D>;
+  constexpr int RPT = D / 16, N = Vec16<T>::N;
+  extern __shared__ float smem[];
+  float* sq = smem;
+  float* sk = sq + kC * S::DP;
+  float* sv = sk + kC * S::DP;
+  float* ss = sv + kC * S::VP;
+  float* sp = ss + D * S::VP;
+  __shared__ float2 gam[kC];
+  __shared__ float s_in[kC], s_out[kC];  // e^gamma_i, e^(gamma_C - gamma_i)
+  __shared__ float s_total;
+  __shared__ int64_t s_sum;
+
+  const int h = blockIdx.y, col0 = blockIdx.z * kCols, tid = threadIdx.x;
+  Segment x;
+  if (!find_segment(p, seg, blockIdx.x, tid == 0 && h == 0 && blockIdx.z == 0, x)) return;
+  if (kStates && x.last) return;
+  const int hk = h / (p.H / p.Hk);
+  const int ty = tid >> 4, tx = tid & 15;
+  const int r0 = ty * RPT, c0 = col0 + tx * 4;
+
+  float st[RPT][4];
+  const float* entry = nullptr;
+  if (!kStates)
+    entry = !x.first ? added + ((x.place - 1) * p.H + h) * (int64_t)(D * D)
+            : p.init ? p.init + ((int64_t)x.seq * p.H + h) * (D * D) : nullptr;
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (entry) f = *reinterpret_cast<const float4*>(entry + (int64_t)(r0 + i) * D + c0);
+    st[i][0] = f.x; st[i][1] = f.y; st[i][2] = f.z; st[i][3] = f.w;
+  }
+  int64_t log_sum = 0;  // thread 0
+
+  const T *q = (const T*)p.q + (int64_t)hk * D, *k = (const T*)p.k + (int64_t)hk * D,
+          *v = (const T*)p.v + (int64_t)h * D + col0;
+  for (int64_t t0 = x.lo; t0 < x.hi; t0 += kC) {
+    const int n = (int)(x.hi - t0 < kC ? x.hi - t0 : kC);
+    __syncthreads();
+    // rows of the chunk, zeros past its end
+    for (int i = tid; i < kC * (D / N); i += kSimtThreads) {
+      const int t = i / (D / N), c = (i % (D / N)) * N;
+      uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+      if (t < n) {
+        if (!kStates) a = *reinterpret_cast<const uint4*>(q + (t0 + t) * p.qs + c);
+        b = *reinterpret_cast<const uint4*>(k + (t0 + t) * p.ks + c);
+      }
+      float f[N];
+      if (!kStates) {
+        Vec16<T>::unpack(a, f);
+#pragma unroll
+        for (int e = 0; e < N; ++e) sq[t * S::DP + c + e] = f[e];
+      }
+      Vec16<T>::unpack(b, f);
+#pragma unroll
+      for (int e = 0; e < N; ++e) sk[t * S::DP + c + e] = f[e];
+    }
+    for (int i = tid; i < kC * (kCols / N); i += kSimtThreads) {
+      const int t = i / (kCols / N), c = (i % (kCols / N)) * N;
+      uint4 a = make_uint4(0u, 0u, 0u, 0u);
+      if (t < n) a = *reinterpret_cast<const uint4*>(v + (t0 + t) * p.vs + c);
+      float f[N];
+      Vec16<T>::unpack(a, f);
+#pragma unroll
+      for (int e = 0; e < N; ++e) sv[t * S::VP + c + e] = f[e];
+    }
+    if (!kStates) {
+#pragma unroll
+      for (int i = 0; i < RPT; ++i)
+        *reinterpret_cast<float4*>(&ss[(r0 + i) * S::VP + tx * 4]) =
+            make_float4(st[i][0], st[i][1], st[i][2], st[i][3]);
+    }
+    if (tid < 32) {
+      const float g = tid < n ? p.g[(t0 + tid) * p.gs + h] : 0.0f;
+      int64_t u = log_units(g);
+      const bool nan = __any_sync(0xffffffffu, g != g);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t w = __shfl_up_sync(0xffffffffu, u, o);
+        if (tid >= o) u += w;
+      }
+      const int64_t all = __shfl_sync(0xffffffffu, u, 31);
+      const float bad = nan ? __int_as_float(0x7fffffff) : 0.0f;  // a NaN decay spoils its chunk
+      gam[tid] = log_pair(u);
+      gam[tid].x += bad;
+      s_in[tid] = exp2f(gam[tid].x + gam[tid].y);
+      s_out[tid] = exp2f(log_pair(all - u).x + bad);
+      if (tid == 0) {
+        s_total = exp2f(log_pair(all).x + bad);
+        log_sum += all;
+      }
+    }
+    __syncthreads();
+    if (!kStates) {
+      const int i = tid >> 3;
+      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int c = 0; c < D; c += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(&sq[i * S::DP + c]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const float4 b = *reinterpret_cast<const float4*>(&sk[((tid & 7) + 8 * m) * S::DP + c]);
+          acc[m] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, acc[m]))));
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int j = (tid & 7) + 8 * m;
+        sp[i * S::PP + j] = j <= i ? acc[m] * decay_between(gam[i], gam[j]) : 0.0f;
+      }
+      __syncthreads();
+      const int i0 = ty * 2;
+      float out[2][4] = {};
+      for (int r = 0; r < D; r += 4) {
+        const float4 qa = *reinterpret_cast<const float4*>(&sq[i0 * S::DP + r]);
+        const float4 qb = *reinterpret_cast<const float4*>(&sq[(i0 + 1) * S::DP + r]);
+        const float a[4] = {qa.x, qa.y, qa.z, qa.w}, b[4] = {qb.x, qb.y, qb.z, qb.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 f = *reinterpret_cast<const float4*>(&ss[(r + e) * S::VP + tx * 4]);
+          out[0][0] = fmaf(a[e], f.x, out[0][0]); out[0][1] = fmaf(a[e], f.y, out[0][1]);
+          out[0][2] = fmaf(a[e], f.z, out[0][2]); out[0][3] = fmaf(a[e], f.w, out[0][3]);
+          out[1][0] = fmaf(b[e], f.x, out[1][0]); out[1][1] = fmaf(b[e], f.y, out[1][1]);
+          out[1][2] = fmaf(b[e], f.z, out[1][2]); out[1][3] = fmaf(b[e], f.w, out[1][3]);
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int row = i0 + m;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) out[m][c] *= s_in[row];
+        for (int j = 0; j <= row; ++j) {  // later rows do not reach it, NaN included
+          const float w = sp[row * S::PP + j];
+          const float4 f = *reinterpret_cast<const float4*>(&sv[j * S::VP + tx * 4]);
+          out[m][0] = fmaf(w, f.x, out[m][0]); out[m][1] = fmaf(w, f.y, out[m][1]);
+          out[m][2] = fmaf(w, f.z, out[m][2]); out[m][3] = fmaf(w, f.w, out[m][3]);
+        }
+        if (row < n) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            st_elem((T*)p.o, ((t0 + row) * p.H + h) * D + c0 + c, p.scale * out[m][c]);
+        }
+      }
+    }
+    const float a = s_total;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) st[i][c] *= a;
+    for (int j = 0; j < n; ++j) {
+      const float w = s_out[j];
+      const float4 f = *reinterpret_cast<const float4*>(&sv[j * S::VP + tx * 4]);
+      const float vv[4] = {f.x * w, f.y * w, f.z * w, f.w * w};
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        const float kk = sk[j * S::DP + r0 + i];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) st[i][c] = fmaf(kk, vv[c], st[i][c]);
+      }
+    }
+  }
+  float* exit_state = nullptr;
+  if (kStates) {
+    exit_state = added + (x.place * p.H + h) * (int64_t)(D * D);
+    if (tid == 0 && blockIdx.z == 0) added_log[x.place * p.H + h] = log_pair(log_sum).x;
+  } else if (x.last && p.final_state) {
+    exit_state = p.final_state + ((int64_t)x.seq * p.H + h) * (D * D);
+  }
+  if (exit_state) {
+#pragma unroll
+    for (int i = 0; i < RPT; ++i)
+      *reinterpret_cast<float4*>(exit_state + (int64_t)(r0 + i) * D + c0) =
+          make_float4(st[i][0], st[i][1], st[i][2], st[i][3]);
+  }
+}
+
+// The scan: place j of a sequence goes from the state that segment j adds to the state after it,
+// which is the entry state of segment j + 1. One thread per four elements of a (sequence, head).
+template <int D>
+__global__ void __launch_bounds__(256)
+decay_scan_kernel(const DecayParams p, int seg, float* added, const float* added_log) {
+  constexpr int kParts = D * D / 1024;
+  const int s = blockIdx.x / kParts, h = blockIdx.y;
+  const int64_t c0 = p.cu ? p.cu[s] : 0, c1 = p.cu ? p.cu[s + 1] : p.total;
+  if (c0 < 0 || c1 > p.total || c1 - c0 <= seg) return;
+  const int e = (blockIdx.x % kParts * 256 + threadIdx.x) * 4;
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (p.init)
+    x = *reinterpret_cast<const float4*>(p.init + ((int64_t)s * p.H + h) * (D * D) + e);
+  const int64_t first = c0 / seg, n = (c1 - c0 + seg - 1) / seg - 1;
+  for (int64_t j = first; j < first + n; ++j) {
+    const float a = exp2f(added_log[j * p.H + h]);
+    float4* y = reinterpret_cast<float4*>(added + (j * p.H + h) * (int64_t)(D * D) + e);
+    const float4 f = *y;
+    x = make_float4(fmaf(a, x.x, f.x), fmaf(a, x.y, f.y), fmaf(a, x.z, f.z), fmaf(a, x.w, f.w));
+    *y = x;
+  }
+}
+
+int segment_tokens(kda_dtype, int total, int H, int d) {
+  // about two segments per SM and head column tile
+  const int64_t units = (int64_t)H * (d / kCols);
+  int64_t seg = ((int64_t)total * units / 304 + 63) / 64 * 64;
+  return (int)(seg < 256 ? 256 : seg);
+}
+
+template <int D, class T>
+kda_status launch_simt_t(const DecayParams& p, kda_dtype dt, cudaStream_t s) {
+  const int seg = segment_tokens(dt, p.total, p.H, D);
+  const int places = p.total / seg;
+  const size_t smem = SimtShape<D>::floats * sizeof(float);
+  const dim3 grid((unsigned)(places + p.n_seqs), (unsigned)p.H, D / kCols);
+  float* added = (float*)p.ws;
+  float* added_log = added ? added + (int64_t)places * p.H * (D * D) : nullptr;
+  cudaFuncSetAttribute(decay_chunk_kernel<D, T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       (int)smem);
+  cudaFuncSetAttribute(decay_chunk_kernel<D, T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       (int)smem);
+  if (p.total > seg) {
+    decay_chunk_kernel<D, T, true><<<grid, kSimtThreads, smem, s>>>(p, seg, added, added_log);
+    decay_scan_kernel<D><<<dim3((unsigned)p.n_seqs * (D * D / 1024), (unsigned)p.H), 256, 0, s>>>(
+        p, seg, added, added_log);
+    count_launches(2);
+  }
+  decay_chunk_kernel<D, T, false><<<grid, kSimtThreads, smem, s>>>(p, seg, added, added_log);
+  count_launches(1);
+  return check_launch("kda_decay_prefill");
+}
+
+}  // namespace
+
+size_t decay_prefill_workspace_bytes(kda_dtype dt, int total, int H, int d) {
+  const int seg = segment_tokens(dt, total, H, d);
+  if (total <= seg) return 0;
+  return (size_t)(total / seg) * H * ((size_t)d * d + 1) * sizeof(float);
+}
+
+kda_status launch_decay_prefill(const DecayParams& p, kda_dtype dt, int d, cudaStream_t s) {
+  if (dt == KDA_BF16)
+    return d == 128 ? launch_simt_t<128, __nv_bfloat16>(p, dt, s)
+                    : launch_simt_t<64, __nv_bfloat16>(p, dt, s);
+  return d == 128 ? launch_simt_t<128, float>(p, dt, s) : launch_simt_t<64, float>(p, dt, s);
+}
+
+kda_status launch_decay_window(const DecayParams& p, kda_dtype dt, int d, cudaStream_t s) {
+  if (dt == KDA_BF16)
+    return d == 128 ? launch_window_t<128, __nv_bfloat16>(p, s)
+                    : launch_window_t<64, __nv_bfloat16>(p, s);
+  return d == 128 ? launch_window_t<128, float>(p, s) : launch_window_t<64, float>(p, s);
+}
+
+}  // namespace kda

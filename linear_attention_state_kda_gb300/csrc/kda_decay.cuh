@@ -1,0 +1,73 @@
+// Shared by the kernels of linear attention with one decay per head: how packed sequences are cut
+// into segments, and the decays inside a chunk.
+//
+// A prompt is cut into segments of `seg` tokens (a multiple of the chunk) that are walked side by
+// side: the state that a segment adds is summed first (from zero), a scan over a sequence's
+// segments gives each its entry state (elementwise, since a segment's decay is one number), and
+// the segments then run with their outputs. Lengths live on the device, so segments are numbered
+// from the packed offsets: segment j of sequence s is in slot floor(cu[s] / seg) + s + j. All but
+// a sequence's last are full, and their added states are in place floor(cu[s] / seg) + j of a
+// workspace of floor(total / seg) places: sequence s + 1 begins at least that many places on.
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+namespace decay {
+
+struct Segment {
+  int seq;
+  int64_t lo, hi;      // tokens
+  int64_t place;       // of the state that it adds; the entry state is in place - 1
+  bool first, last;    // of its sequence
+};
+
+// The segment in a slot; false: none. `flag`: report malformed offsets.
+__device__ __forceinline__ bool find_segment(const DecayParams& p, int seg, int slot, bool flag,
+                                             Segment& x) {
+  int a = 0, b = p.n_seqs - 1;  // the last sequence whose first slot is <= slot
+  if (p.cu) {
+    while (a < b) {
+      const int m = (a + b + 1) >> 1;
+      if ((int64_t)p.cu[m] / seg + m <= slot) a = m;
+      else b = m - 1;
+    }
+  }
+  int64_t c0 = p.cu ? p.cu[a] : 0, c1 = p.cu ? p.cu[a + 1] : p.total;
+  const int64_t j = slot - (c0 / seg + a);
+  if (j < 0) return false;
+  if (c0 < 0 || c1 > p.total || c1 < c0) {
+    if (flag && p.status) atomicOr(p.status, KDA_STATUS_BAD_OFFSETS);
+    if (j > 0) return false;
+    c0 = c1 = 0;  // an empty sequence
+  }
+  x.seq = a;
+  x.lo = c0 + j * seg;
+  x.hi = x.lo + seg < c1 ? x.lo + seg : c1;
+  x.first = j == 0;
+  x.last = x.hi == c1;
+  x.place = c0 / seg + j;
+  return x.first || x.lo < c1;
+}
+
+// Log-decays in units of 2^-40 of a base-2 exponent, as integers: sums of any number of them are
+// exact, so the decay between two tokens does not lose bits to a strong decay before both. A
+// token's decay below 2^-400 counts as that: no fp32 state survives it either way.
+constexpr double kLogUnit = 1099511627776.0 * 1.4426950408889634;  // 2^40 / ln 2
+__device__ __forceinline__ int64_t log_units(float g) {
+  g = g < -277.0f ? -277.0f : g;  // (a NaN stays)
+  return __double2ll_rn((double)g * kLogUnit);
+}
+// A sum of log units as a pair of floats, hi + lo, in base-2 exponents.
+__device__ __forceinline__ float2 log_pair(int64_t u) {
+  const double x = (double)u * 9.094947017729282e-13;  // 2^-40
+  const float hi = (float)x;
+  return make_float2(hi, (float)(x - (double)hi));
+}
+// 2^(a - b).
+__device__ __forceinline__ float decay_between(float2 a, float2 b) {
+  return exp2f((a.x - b.x) + (a.y - b.y));
+}
+
+}  // namespace decay
+}  // namespace kda

@@ -1,0 +1,633 @@
+// Eviction from the paged 8-bit cache by accumulated attention weight: adding a window's softmax
+// weights to a weight per cached token and head (kda_cache_weigh), and keeping a budget of tokens
+// by these weights, moved into new pages (kda_cache_evict).
+#include <cuda_fp16.h>
+
+#include "kda_internal.cuh"
+#include "kda_fp8.cuh"
+#include "ptx.cuh"
+
+namespace kda {
+namespace {
+
+// ---------------------------------------------------------------- weighing
+//
+//     weight[t] = keep * weight[t] + sum_i exp(s_it - lse_i),   s_it = scale q_i . k_t
+// over the query rows i (tokens of the window x query heads of the group) that see position t.
+//
+// Bound by the K codes, d bytes a key. A cluster owns one (row, key/value head) and its CTAs
+// contiguous ranges of its pages, so that the codes are read once: the scores stay in shared
+// memory while the row statistics (running maximum and sum) are joined over the cluster, and become
+// weights there. Keys beyond the room for scores are scored again.
+//
+// Scores are warp-level f16 MMAs with the keys as the rows: 16 keys x 16 channels times 16 channels
+// x 8 query rows. The sum over the channels is in any order, so lane (g, t) takes channels
+// 32 t .. (d = 128) of keys g and g + 8 from global memory in 16-byte loads, which are the A
+// fragments after widening (e4m3 to f16 is exact). Query rows are scaled by a power of two into
+// f16's upper range: bf16 entries down to 2^-30 of the row's largest are exact, fp32 entries are
+// two f16 parts.
+constexpr int kWThreads = 256;
+constexpr int kWWarps = kWThreads / 32;
+constexpr int kGroupRows = 64;  // query rows scored at once
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The 64-bit word at `p` of the cluster's CTA `rank` holds two floats.
+__device__ __forceinline__ float2 ld_cluster_f2(const float2* p, uint32_t rank) {
+  const uint64_t v = ptx::ld_cluster_u64(reinterpret_cast<const uint64_t*>(p), rank);
+  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+
+// (m, l) of two parts of a row's keys.
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  if (m == -INFINITY) return make_float2(m, a.y + b.y);
+  return make_float2(m, a.y * exp2f(a.x - m) + b.y * exp2f(b.x - m));
+}
+
+// NT: tiles of 8 query rows scored at once. P: f16 parts of a query.
+template <int D, int NT, int P, class T>
+__global__ void __launch_bounds__(kWThreads) weigh_kernel(const WeighParams p, int cs, int cap_keys) {
+  constexpr int KC = D / 16;      // 16-channel steps
+  constexpr int LB = D / 4;       // bytes of a key per lane
+  constexpr int ROWS = NT * 8;
+  extern __shared__ __align__(16) unsigned char wsm[];
+  // query fragments [P][NT][KC][32 lanes] x 8 bytes, then the scores [cap_keys][rows]
+  uint2* frag = reinterpret_cast<uint2*>(wsm);
+  float* score = reinterpret_cast<float*>(wsm + (size_t)P * NT * KC * 256);
+  __shared__ float row_mul[ROWS];          // scale * log2 e * 2^e of a query row
+  __shared__ float2 part[kWWarps][ROWS];
+  __shared__ float2 cta_ml[ROWS];
+  __shared__ float row_lse[ROWS];
+
+  const int rank = blockIdx.x % cs, bh = blockIdx.x / cs;
+  const int b = bh / p.Hkv, h = bh - b * p.Hkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  const int start = p.start[b];
+  int n = start < 0 ? 0 : p.lens ? p.lens[b] : p.window;
+  n = n < 0 ? 0 : n > p.window ? p.window : n;
+  if (n == 0) return;  // the whole cluster
+  const int G = p.Hq / p.Hkv, R = n * G;
+  const int64_t most = (int64_t)p.max_pages * kPage;
+  const int64_t keys = (int64_t)start + n < most ? (int64_t)start + n : most;
+  if (rank == 0 && tid == 0 && h == 0 && p.status && (int64_t)start + n > most)
+    atomicOr(p.status, KDA_STATUS_BAD_PAGE);
+  const int pages = (int)((keys + kPage - 1) / kPage);
+  const int per = (pages + cs - 1) / cs;
+  const int pg0 = min(pages, rank * per), pg1 = min(pages, pg0 + per);
+  const int32_t* table = p.table + (int64_t)b * p.max_pages;
+
+  for (int r0 = 0; r0 < R; r0 += ROWS) {
+    const int rows = min(ROWS, R - r0);
+    __syncthreads();
+    // the group's query rows: scale, then fragments. A warp takes a row.
+    for (int r = warp; r < ROWS; r += kWWarps) {
+      float f[D / 32];
+      float m = 0.0f;
+      const int row = r0 + r;
+      const int j = row / G, gh = row - j * G;
+      const T* q = (const T*)p.q + (((int64_t)b * p.window + j) * p.Hq + h * G + gh) * D;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        f[i] = r < rows ? ld_elem(q, lane * (D / 32) + i) : 0.0f;
+        m = fmaxf(m, __uint_as_float(finite_abs_bits(f[i])));
+      }
+      m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+      // 2^e with m 2^-e in [2^14, 2^15); e from the bits, m = 0 counts as 2^-126
+      const int ex = (int)(__float_as_uint(m) >> 23);
+      const int e = (ex ? ex : 1) - 127 - 14;  // -140 .. 113
+      const float down = e > 0 ? pow2f(-e) : 1.0f;
+      const float up1 = e < 0 ? pow2f(-e < 126 ? -e : 126) : 1.0f;
+      const float up2 = e < -126 ? pow2f(-e - 126) : 1.0f;
+      // channel c of the row: in lane quarter c / (D/4), step (c % (D/4)) / 4
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const float x = f[i] * down * up1 * up2;
+        const int c = lane * (D / 32) + i;
+        const int tq = c / LB, kc = (c % LB) / 4, el = c % 4;
+        __half hi = __float2half_rn(x);
+        __half* dst = reinterpret_cast<__half*>(
+            &frag[(((r >> 3) * KC) + kc) * 32 + (r & 7) * 4 + tq]);
+        dst[el] = hi;
+        if (P == 2) {
+          float lo = x - __half2float(hi);
+          if (!(fabsf(lo) <= 64.0f)) lo = 0.0f;  // of an infinity or NaN
+          dst[(size_t)NT * KC * 128 + el] = __float2half_rn(lo);
+        }
+      }
+      if (lane == 0) {
+        // scale and 2^e in two factors: e may be below the normal range
+        row_mul[r] = p.scale * kLog2e * pow2f(e < -126 ? -126 : e) * (e < -126 ? pow2f(e + 126) : 1.0f);
+      }
+    }
+    __syncthreads();
+
+    // the last token of the group sees the most; the page range of this CTA is fixed
+    const int j_last = (r0 + rows - 1) / G;
+    const int64_t seen = (int64_t)start + j_last + 1;
+    // the lane's rows 2 t4, 2 t4 + 1 of each tile: how far they see, and their statistics
+    int64_t vis[NT][2];
+    float2 ml[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = i * 8 + t4 * 2 + e;
+        vis[i][e] = r < rows ? (int64_t)start + (r0 + r) / G + 1 : 0;  // positions below
+        if (vis[i][e] > keys) vis[i][e] = keys;
+        ml[i][e] = make_float2(-INFINITY, 0.0f);
+      }
+
+    // Scores of 16 keys (rows of tile `tile` of page `page`) in base-2 exponents, masked.
+    auto score_tile = [&](int page_id, float ks, int64_t pos0, float acc[NT][4]) {
+      const uint8_t* base = p.kc + ((int64_t)page_id * p.Hkv + h) * (int64_t)(kPage * D) +
+                            (int)(pos0 & (kPage - 1)) * D;
+      uint32_t w[2][LB / 4];
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int i = 0; i < LB / 16; ++i)
+          *reinterpret_cast<uint4*>(&w[half][4 * i]) = __ldcs(reinterpret_cast<const uint4*>(
+              base + (g + 8 * half) * D + t4 * LB + 16 * i));
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+#pragma unroll
+      for (int kc = 0; kc < KC; ++kc) {
+        uint32_t a[4];
+        f16x4_from_e4m3(w[0][kc], a[0], a[2]);
+        f16x4_from_e4m3(w[1][kc], a[1], a[3]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+#pragma unroll
+          for (int part_i = 0; part_i < P; ++part_i) {
+            const uint2 q2 = frag[((part_i * NT + i) * KC + kc) * 32 + lane];
+            mma16816(acc[i], a, q2.x, q2.y);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t pos = pos0 + g + 8 * (e >> 1);
+          acc[i][e] = pos < vis[i][e & 1]
+                          ? acc[i][e] * ks * row_mul[i * 8 + t4 * 2 + (e & 1)] : -INFINITY;
+        }
+    };
+
+    for (int pg = pg0 + warp; pg < pg1; pg += kWWarps) {
+      if ((int64_t)pg * kPage >= seen) break;
+      int id = table[pg];
+      if (id >= p.n_pages) {
+        if (lane == 0 && h == 0 && p.status) atomicOr(p.status, KDA_STATUS_BAD_PAGE);
+        id = -1;
+      }
+      if (id < 0) continue;
+      const float ks = p.ks[(int64_t)id * p.Hkv + h];
+      const int local = (pg - pg0) * kPage;
+#pragma unroll 1
+      for (int tile = 0; tile < kPage / 16; ++tile) {
+        float acc[NT][4];
+        score_tile(id, ks, (int64_t)pg * kPage + tile * 16, acc);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float2& s = ml[i][e];
+            const float m = fmaxf(s.x, fmaxf(acc[i][e], acc[i][e + 2]));
+            const float mm = m == -INFINITY ? 0.0f : m;
+            s.y = s.y * exp2f(s.x - mm) + exp2f(acc[i][e] - mm) + exp2f(acc[i][e + 2] - mm);
+            s.x = m;
+          }
+        if (local < cap_keys) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = i * 8 + t4 * 2 + (e & 1);
+              if (r < rows) score[(local + tile * 16 + g + 8 * (e >> 1)) * rows + r] = acc[i][e];
+            }
+        }
+      }
+    }
+    // row statistics: lanes of a row, warps, CTAs
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float2 s = ml[i][e];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1)
+          s = join(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o),
+                                  __shfl_xor_sync(0xffffffffu, s.y, o)));
+        if (g == 0) part[warp][i * 8 + t4 * 2 + e] = s;
+      }
+    __syncthreads();
+    if (tid < ROWS) {
+      float2 s = part[0][tid];
+#pragma unroll
+      for (int w = 1; w < kWWarps; ++w) s = join(s, part[w][tid]);
+      cta_ml[tid] = s;
+    }
+    ptx::cluster_sync();
+    if (tid < ROWS) {
+      float2 s = ld_cluster_f2(&cta_ml[tid], 0);
+      for (int c = 1; c < cs; ++c) s = join(s, ld_cluster_f2(&cta_ml[tid], c));
+      // a row that sees nothing adds nothing
+      row_lse[tid] = s.x == -INFINITY && !(s.y != s.y) ? INFINITY : s.x + log2f(s.y);
+    }
+    ptx::cluster_sync();  // (also: the statistics are read before the next group's are written)
+
+    // weights: from the scores in shared memory, else scored again
+    const bool fresh = r0 == 0;
+    for (int pg = pg0 + warp; pg < pg1; pg += kWWarps) {
+      int id = table[pg];
+      if (id < 0 || id >= p.n_pages) continue;
+      const int local = (pg - pg0) * kPage;
+      const bool reached = (int64_t)pg * kPage < seen;
+      if (!reached && !fresh) continue;
+      float* wp = p.weights + ((int64_t)id * p.Hkv + h) * kPage;
+      if (local < cap_keys || !reached) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int at = lane + 32 * half;
+          const int64_t pos = (int64_t)pg * kPage + at;
+          if (pos >= keys) continue;
+          float sum = 0.0f;
+          if (reached)
+            for (int r = 0; r < rows; ++r)
+              sum += exp2f(score[(local + at) * rows + r] - row_lse[r]);
+          const float old = !fresh ? wp[at] : pos < start && p.keep != 0.0f ? p.keep * wp[at] : 0.0f;
+          wp[at] = old + sum;
+        }
+      } else {
+        const float ks = p.ks[(int64_t)id * p.Hkv + h];
+#pragma unroll 1
+        for (int tile = 0; tile < kPage / 16; ++tile) {
+          float acc[NT][4];
+          score_tile(id, ks, (int64_t)pg * kPage + tile * 16, acc);
+          float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              sum[e >> 1] += exp2f(acc[i][e] - row_lse[i * 8 + t4 * 2 + (e & 1)]);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 1);
+            sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 2);
+            const int at = tile * 16 + g + 8 * half;
+            const int64_t pos = (int64_t)pg * kPage + at;
+            if (t4 == 0 && pos < keys) {
+              const float old = !fresh ? wp[at] : pos < start && p.keep != 0.0f ? p.keep * wp[at] : 0.0f;
+              wp[at] = old + sum[half];
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+template <int D, int NT, int P, class T>
+kda_status launch_weigh_nt(const WeighParams& p, cudaStream_t s) {
+  const int64_t units = (int64_t)p.batch * p.Hkv;
+  const int G = p.Hq / p.Hkv;
+  const int64_t rows64 = (int64_t)G * p.window;
+  const int rows = rows64 < NT * 8 ? (int)rows64 : NT * 8;
+  // about 2048 keys per CTA, more CTAs where the units are few
+  int cs = 1;
+  while (cs < 8 && ((int64_t)p.max_pages * kPage > (int64_t)cs * 2048 ||
+                    (units * cs < 152 && p.max_pages > cs)))
+    cs *= 2;
+  const int64_t per = (p.max_pages + cs - 1) / cs;
+  const size_t frag = (size_t)P * NT * (D / 16) * 256;
+  const size_t room = 100 * 1024 - frag;
+  int64_t cap = (int64_t)(room / ((size_t)rows * 4)) / kPage;
+  if (cap > per) cap = per;
+  const size_t smem = frag + (size_t)cap * kPage * rows * 4;
+  auto kernel = weigh_kernel<D, NT, P, T>;
+  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * cs));
+  cfg.blockDim = dim3(kWThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cs;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, p, cs, (int)(cap * kPage));
+  count_launches(1);
+  return check_launch("kda_cache_weigh");
+}
+template <int D, int P, class T>
+kda_status launch_weigh_t(const WeighParams& p, cudaStream_t s) {
+  const int64_t rows = (int64_t)(p.Hq / p.Hkv) * p.window;
+  if (rows <= 8) return launch_weigh_nt<D, 1, P, T>(p, s);
+  if (rows <= 16) return launch_weigh_nt<D, 2, P, T>(p, s);
+  return launch_weigh_nt<D, 4, P, T>(p, s);
+}
+
+// ---------------------------------------------------------------- eviction
+//
+// Two kernels. The first keeps, for each (row, head), the budget's positions: a cluster holds the
+// candidates' weights as order-preserving integers in shared memory and finds the smallest one that
+// is kept by four rounds of 256-bin counts, then writes the kept positions in order. The second
+// moves the kept tokens, one CTA per (new page, head).
+constexpr int kEThreads = 512;
+constexpr int kEWarps = kEThreads / 32;
+
+// Orders like the weights; NaN lowest, zeros of both signs equal. 0 is no candidate.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 1u;
+  const uint32_t b = w == 0.0f ? 0u : __float_as_uint(w);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* p, uint32_t rank) {
+  uint32_t a, v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kEThreads) evict_select_kernel(const EvictParams p, int cs, int cap) {
+  extern __shared__ uint32_t s_key[];
+  __shared__ uint32_t hist[256], total[256];
+  __shared__ uint32_t s_count[2], s_pick[2];
+  __shared__ uint32_t warp_gt[kEWarps], warp_eq[kEWarps];
+  const int rank = blockIdx.x % cs, bh = blockIdx.x / cs;
+  const int b = bh / p.Hkv, h = bh % p.Hkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int raw = p.length[b];
+  int32_t* kept = p.kept + ((int64_t)b * p.Hkv + h) * p.budget;
+  if (raw < 0) {  // a padding row: the whole cluster
+    for (int i = rank * kEThreads + tid; i < p.budget; i += cs * kEThreads) kept[i] = -1;
+    if (rank == 0 && tid == 0 && h == 0) p.new_length[b] = raw;
+    return;
+  }
+  const int64_t most = (int64_t)p.max_pages * kPage;
+  if (raw > most && rank == 0 && tid == 0 && h == 0 && p.status)
+    atomicOr(p.status, KDA_STATUS_BAD_PAGE);
+  const int64_t len = raw < most ? raw : most;
+  const int pages = (int)((len + kPage - 1) / kPage), per = (pages + cs - 1) / cs;
+  const int pg0 = min(pages, rank * per), pg1 = min(pages, pg0 + per);
+  const int64_t first = (int64_t)pg0 * kPage;
+  const int n = (int)((int64_t)pg1 * kPage < len ? (pg1 - pg0) * kPage : len - first > 0 ? len - first : 0);
+  const int32_t* table = p.table + (int64_t)b * p.max_pages;
+
+  auto key_at = [&](int i) -> uint32_t {
+    const int64_t pos = first + i;
+    const int id = table[pos / kPage];
+    if (id < 0 || id >= p.n_pages) return 0u;
+    if (pos < p.sinks || pos >= len - p.recent) return 0xffffffffu;
+    return weight_key(p.weights[((int64_t)id * p.Hkv + h) * kPage + (pos & (kPage - 1))]);
+  };
+  auto get = [&](int i) -> uint32_t { return i < cap ? s_key[i] : key_at(i); };
+
+  // keys, and how many candidates there are
+  if (tid < 2) s_count[tid] = 0;
+  __syncthreads();
+  uint32_t mine = 0;
+  for (int i = tid; i < n; i += kEThreads) {
+    const uint32_t k = key_at(i);
+    if (i < cap) s_key[i] = k;
+    mine += k != 0u;
+    if (k == 0u && (i & (kPage - 1)) == 0 && h == 0 && p.status &&
+        table[(first + i) / kPage] >= p.n_pages)
+      atomicOr(p.status, KDA_STATUS_BAD_PAGE);
+  }
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) atomicAdd(&s_count[0], mine);
+  ptx::cluster_sync();
+  uint32_t all = 0;
+  for (int c = 0; c < cs; ++c) all += ld_cluster_u32(&s_count[0], c);
+  const uint32_t want = min(all, (uint32_t)p.budget);
+
+  // the smallest kept key, and how many of that value are kept: digits from the top
+  uint32_t prefix = 0, left = want;
+  if (want > 0) {
+#pragma unroll 1
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      const uint32_t above = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
+      if (tid < 256) hist[tid] = 0;
+      __syncthreads();
+      for (int i0 = 0; i0 < n; i0 += kEThreads) {
+        const int i = i0 + tid;
+        const uint32_t k = i < n ? get(i) : 0u;
+        const bool in = k != 0u && ((k ^ prefix) & above) == 0u;
+        // one addition per distinct digit of the warp
+        const uint32_t digit = in ? (k >> shift) & 255u : 256u;
+        const uint32_t same = __match_any_sync(0xffffffffu, digit);
+        if (in && (int)(__ffs(same) - 1) == lane) atomicAdd(&hist[digit], __popc(same));
+      }
+      ptx::cluster_sync();
+      if (tid < 256) {
+        uint32_t sum = 0;
+        for (int c = 0; c < cs; ++c) sum += ld_cluster_u32(&hist[tid], c);
+        total[tid] = sum;
+      }
+      __syncthreads();
+      if (warp == 0) {
+        // lane l owns digits 255 - 8 l .. 248 - 8 l
+        uint32_t sum = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += total[255 - 8 * lane - i];
+        uint32_t upto = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t u = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += u;
+        }
+        const uint32_t before = upto - sum;
+        if (before < left && left <= upto) {
+          uint32_t c = before;
+          int d = 255 - 8 * lane;
+          while (c + total[d] < left) c += total[d--];
+          s_pick[0] = (uint32_t)d;
+          s_pick[1] = left - c;
+        }
+      }
+      ptx::cluster_sync();  // counts are read before they are cleared
+      prefix |= s_pick[0] << shift;
+      left = s_pick[1];
+      __syncthreads();
+    }
+  }
+  // `prefix` is the smallest kept key; `left` of its positions are kept, the earliest ones.
+  // Where this CTA's positions begin among the kept: counts of the CTAs before it.
+  uint32_t gt = 0, eq = 0;
+  for (int i = tid; i < n; i += kEThreads) {
+    const uint32_t k = get(i);
+    gt += want > 0 && k > prefix;
+    eq += want > 0 && k == prefix;
+  }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  if (lane == 0) {
+    warp_gt[warp] = gt;
+    warp_eq[warp] = eq;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    gt = eq = 0;
+    for (int w = 0; w < kEWarps; ++w) {
+      gt += warp_gt[w];
+      eq += warp_eq[w];
+    }
+    s_count[0] = gt;
+    s_count[1] = eq;
+  }
+  ptx::cluster_sync();
+  uint32_t gt0 = 0, eq0 = 0;
+  for (int c = 0; c < rank; ++c) {
+    gt0 += ld_cluster_u32(&s_count[0], c);
+    eq0 += ld_cluster_u32(&s_count[1], c);
+  }
+  for (int i0 = 0; i0 < n && want > 0; i0 += kEThreads) {
+    const int i = i0 + tid;
+    const uint32_t k = i < n ? get(i) : 0u;
+    const bool is_gt = k > prefix, is_eq = k == prefix && k != 0u;
+    const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
+    __syncthreads();
+    if (lane == 0) {
+      warp_gt[warp] = __popc(bg);
+      warp_eq[warp] = __popc(be);
+    }
+    __syncthreads();
+    uint32_t g1 = gt0, e1 = eq0;
+    for (int w = 0; w < kEWarps; ++w) {
+      if (w < warp) {
+        g1 += warp_gt[w];
+        e1 += warp_eq[w];
+      }
+      gt0 += warp_gt[w];
+      eq0 += warp_eq[w];
+    }
+    const uint32_t below = (1u << lane) - 1u;
+    g1 += __popc(bg & below);
+    e1 += __popc(be & below);
+    if (is_gt || (is_eq && e1 < left)) kept[g1 + min(e1, left)] = (int32_t)(first + i);
+  }
+  for (int64_t i = (int64_t)want + rank * kEThreads + tid; i < p.budget; i += cs * kEThreads)
+    kept[i] = -1;
+  if (rank == 0 && tid == 0 && h == 0) p.new_length[b] = (int32_t)want;
+  ptx::cluster_sync();  // no CTA leaves while its counts are read
+}
+
+// Moves 64 kept tokens of a head into a new page. The page's scale is the largest of the tokens'
+// pages', so a code moves as it is where its page had that scale, else by an exact power of two
+// (rounded again only among the format's subnormals).
+constexpr int kMThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kMThreads) evict_move_kernel(const EvictParams p) {
+  __shared__ int64_t src[kPage];      // row of the caches, -1: none
+  __shared__ float ratio[2][kPage];
+  const int width = (p.budget + kPage - 1) / kPage;
+  const int pg = blockIdx.x % width, h = blockIdx.y, b = blockIdx.x / width;
+  const int count = p.new_length[b];
+  if (count < 0 || (int64_t)pg * kPage >= count) return;
+  const int tid = threadIdx.x;
+  int dst = -1;
+  if (pg < p.new_max_pages) dst = p.new_table[(int64_t)b * p.new_max_pages + pg];
+  if (pg >= p.new_max_pages || dst >= p.n_pages) {
+    if (tid == 0 && h == 0 && p.status) atomicOr(p.status, KDA_STATUS_BAD_PAGE);
+    return;
+  }
+  if (dst < 0) return;
+  if (tid < 64) {
+    const int i = pg * kPage + tid;
+    int64_t row = -1;
+    float s[2] = {0.0f, 0.0f}, w = 0.0f;
+    if (i < count) {
+      const int pos = p.kept[((int64_t)b * p.Hkv + h) * p.budget + i];
+      const int64_t slice =
+          (int64_t)p.table[(int64_t)b * p.max_pages + pos / kPage] * p.Hkv + h;
+      row = slice * kPage + (pos & (kPage - 1));
+      s[0] = p.scale[0][slice];
+      s[1] = p.scale[1][slice];
+      w = p.weights[row];
+    }
+    src[tid] = row;
+    ratio[0][tid] = s[0];
+    ratio[1][tid] = s[1];
+    p.weights[((int64_t)dst * p.Hkv + h) * kPage + tid] = w;
+  }
+  __syncthreads();
+  float top[2] = {0.0f, 0.0f};
+  for (int i = 0; i < kPage; ++i) {
+    top[0] = fmaxf(top[0], ratio[0][i]);
+    top[1] = fmaxf(top[1], ratio[1][i]);
+  }
+  constexpr int LPR = D / 16, ROWS = kMThreads / LPR;
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    uint8_t* out = p.code[side] + ((int64_t)dst * p.Hkv + h) * (int64_t)(kPage * D);
+#pragma unroll
+    for (int r = tid / LPR; r < kPage; r += ROWS) {
+      if (src[r] < 0) continue;
+      uint4 c = *reinterpret_cast<const uint4*>(p.code[side] + src[r] * D + (tid % LPR) * 16);
+      const float f = ratio[side][r] == top[side] ? 1.0f : ratio[side][r] / top[side];
+      if (f != 1.0f) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(&c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = f32x2_from_f16x2(f16x2_from_e4m3(w[j] & 0xffffu));
+          const float2 y = f32x2_from_f16x2(f16x2_from_e4m3(w[j] >> 16));
+          w[j] = e4m3x2_from_f32(x.x * f, x.y * f) | e4m3x2_from_f32(y.x * f, y.y * f) << 16;
+        }
+      }
+      *reinterpret_cast<uint4*>(out + r * D + (tid % LPR) * 16) = c;
+    }
+  }
+  if (tid < 2) p.scale[tid][(int64_t)dst * p.Hkv + h] = top[tid];
+}
+
+}  // namespace
+
+kda_status launch_cache_weigh(const WeighParams& p, kda_dtype dt, int d, cudaStream_t s) {
+  if (dt == KDA_BF16)
+    return d == 128 ? launch_weigh_t<128, 1, __nv_bfloat16>(p, s)
+                    : launch_weigh_t<64, 1, __nv_bfloat16>(p, s);
+  return d == 128 ? launch_weigh_t<128, 2, float>(p, s) : launch_weigh_t<64, 2, float>(p, s);
+}
+
+kda_status launch_cache_evict(const EvictParams& p, int d, cudaStream_t s) {
+  const int64_t units = (int64_t)p.batch * p.Hkv;
+  int cs = 1;
+  while (cs < 8 && (int64_t)p.max_pages * kPage > (int64_t)cs * 8192) cs *= 2;
+  const int64_t per = ((int64_t)p.max_pages + cs - 1) / cs * kPage;
+  const int cap = (int)(per < 49152 ? per : 49152);
+  cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, cap * 4);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * cs));
+  cfg.blockDim = dim3(kEThreads);
+  cfg.dynamicSmemBytes = (size_t)cap * 4;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cs;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, evict_select_kernel, p, cs, cap);
+  const dim3 grid((unsigned)p.batch * ((p.budget + kPage - 1) / kPage), (unsigned)p.Hkv);
+  if (grid.x > 0) {
+    if (d == 128) evict_move_kernel<128><<<grid, kMThreads, 0, s>>>(p);
+    else evict_move_kernel<64><<<grid, kMThreads, 0, s>>>(p);
+  }
+  count_launches(grid.x > 0 ? 2 : 1);
+  return check_launch("kda_cache_evict");
+}
+
+}  // namespace kda

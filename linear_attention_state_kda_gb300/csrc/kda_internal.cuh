@@ -189,6 +189,66 @@ struct VerifyParams {
 };
 kda_status launch_verify(const VerifyParams& p, kda_dtype dt, cudaStream_t s);
 
+// Linear attention with one decay per head: S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.
+struct DecayParams {
+  const void *q, *k, *v;  // token rows; q and k have Hk heads, v has H
+  int64_t qs, ks, vs;     // elements between tokens
+  const float* g;
+  int64_t gs;             // H, or 0: one value per head
+  int H, Hk;
+  float scale;
+  void* o;
+  uint32_t* status;
+  // prompts
+  int n_seqs, total;
+  const int32_t* cu;      // [n_seqs + 1] or nullptr (one sequence)
+  const float* init;      // [n_seqs, H, d, d] or nullptr (zeros)
+  float* final_state;     // [n_seqs, H, d, d] or nullptr
+  void* ws;
+  // windows over a slot pool
+  int batch, window;
+  const int32_t *read_slots, *write_slots;
+  float* pool;
+  int64_t n_slots;
+};
+size_t decay_prefill_workspace_bytes(kda_dtype dt, int total, int H, int d);
+kda_status launch_decay_prefill(const DecayParams& p, kda_dtype dt, int d, cudaStream_t s);
+kda_status launch_decay_window(const DecayParams& p, kda_dtype dt, int d, cudaStream_t s);
+
+// Eviction from the cache by accumulated attention weight.
+struct WeighParams {
+  int batch, window, Hq, Hkv;
+  float scale, keep;
+  const void* q;
+  const int32_t* start;
+  const int32_t* lens;
+  const int32_t* table;
+  int max_pages;
+  int64_t n_pages;
+  const uint8_t* kc;
+  const float* ks;
+  float* weights;  // [n_pages, Hkv, 64]
+  uint32_t* status;
+};
+kda_status launch_cache_weigh(const WeighParams& p, kda_dtype dt, int d, cudaStream_t s);
+struct EvictParams {
+  int batch, Hkv;
+  const int32_t* length;
+  const int32_t* table;
+  int max_pages;
+  const int32_t* new_table;
+  int new_max_pages;
+  int64_t n_pages;
+  uint8_t* code[2];
+  float* scale[2];
+  float* weights;
+  int budget, sinks, recent;
+  int32_t* new_length;
+  int32_t* kept;  // [batch, Hkv, budget]
+  uint32_t* status;
+};
+kda_status launch_cache_evict(const EvictParams& p, int d, cudaStream_t s);
+
 // Package scan.
 size_t scan_workspace_bytes(int n_seqs, int max_segs, int H, int dk, int dv);
 kda_status launch_scan(int n_seqs, int n_segs, const int32_t* seq_seg_offsets, int max_segs,

@@ -103,6 +103,18 @@ def lib():
                                       P, P]
     L.kda_draft_verify.restype = I
     L.kda_draft_verify.argtypes = [I, I, I, I, P, I64, P, I64, P, P, P, P, P, P, P, P, P, P]
+    L.kda_decay_prefill_workspace.restype = Z
+    L.kda_decay_prefill_workspace.argtypes = [I, I, I, I, I]
+    L.kda_decay_prefill.restype = I
+    L.kda_decay_prefill.argtypes = [I, I, I, P, I, I, I, F, P, I64, P, I64, P, I64, P, I64, P, P, P,
+                                    P, Z, P, P]
+    L.kda_decay_window.restype = I
+    L.kda_decay_window.argtypes = [I, I, I, I, I, I, F, P, I64, P, I64, P, I64, P, I64, P, P, P, I64,
+                                   P, P, P]
+    L.kda_cache_weigh.restype = I
+    L.kda_cache_weigh.argtypes = [I, I, I, I, I, I, F, F, P, P, P, P, I, P, P, P, I64, P, P]
+    L.kda_cache_evict.restype = I
+    L.kda_cache_evict.argtypes = [I, I, I, P, P, I, P, I, P, P, P, P, P, I64, I, I, I, P, P, P, P]
     _lib = L
     return L
 
@@ -542,6 +554,69 @@ def draft_verify(target_probs, draft_tokens, u_accept, u_sample, draft_probs=Non
     r = (_native_module or _native()).draft_verify(
         target_probs, draft_tokens, u_accept, u_sample, draft_probs, lens, write_slots, tokens,
         n_accepted, resume_slots, status, _handle(stream))
+    if r.__class__ is int:
+        _check(r)
+    return r
+
+
+def decay_prefill_workspace(dtype, n_seqs, total_tokens, H, d):
+    """kda_decay_prefill_workspace: scratch bytes of decay_prefill."""
+    dt = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    return int(lib().kda_decay_prefill_workspace(dt, n_seqs, total_tokens, H, d))
+
+
+def decay_prefill(q, k, v, g, cu_seqlens=None, init_state=None, scale=1.0, o=None,
+                  final_state=None, want_final=True, status=None, workspace=None, stream=None):
+    """kda_decay_prefill: linear attention with one decay per head over packed prompts. q, k
+    [T, Hk, d] and v [T, H, d] may be views of a fused projection's rows, each q and k head shared by
+    H / Hk heads; g is [T, H] fp32 log-decays, or [H] for a constant decay per head. `workspace`
+    (uint8 device tensor of at least decay_prefill_workspace(...) bytes) is allocated here when not
+    given. Returns (o [T, H, d], final_state [n, H, d, d] or None)."""
+    r = (_native_module or _native()).decay_prefill(
+        q, k, v, g, cu_seqlens, init_state, scale, o, final_state, want_final, status, workspace,
+        _handle(stream))
+    if r.__class__ is int:
+        _check(r)
+    return r
+
+
+def decay_window(q, k, v, g, read_slots, write_slots, state_pool, scale=1.0, o=None, status=None,
+                 stream=None):
+    """kda_decay_window: linear attention with one decay per head for rows of `window` tokens
+    (write_slots is [batch, window]; q, k [batch*window, Hk, d], v [batch*window, H, d], g
+    [batch*window, H] or [H]). Row b reads slot read_slots[b] of state_pool [n_slots, H, d, d] and
+    stores its state after token j into slot write_slots[b, j]; one token with write_slots =
+    read_slots is a decode step in place. Returns o, shaped like v."""
+    r = (_native_module or _native()).decay_window(
+        q, k, v, g, read_slots, write_slots, state_pool, scale, o, status, _handle(stream))
+    if r.__class__ is int:
+        _check(r)
+    return r
+
+
+def cache_weigh(q, start, page_table, k_cache, k_scale, weights, scale=1.0, lens=None, keep=1.0,
+                status=None, stream=None):
+    """kda_cache_weigh: adds to weights [n_pages, Hkv, 64] the softmax weights with which the
+    window's queries (as for cache_attention) see each cached token, summed over the window's
+    tokens and the head's query heads; what the tokens before the window had counts `keep` times.
+    Returns weights, updated in place."""
+    r = (_native_module or _native()).cache_weigh(
+        q, start, page_table, k_cache, k_scale, weights, scale, lens, keep, status, _handle(stream))
+    if r.__class__ is int:
+        _check(r)
+    return r
+
+
+def cache_evict(length, page_table, new_table, k_cache, k_scale, v_cache, v_scale, weights, budget,
+                sinks=0, recent=0, new_length=None, kept=None, status=None, stream=None):
+    """kda_cache_evict: keeps `budget` of each row's length[b] cached tokens, per head: the first
+    `sinks`, the last `recent`, and of the rest those of the largest weights. They move, in order,
+    into the pages of new_table [n, pages], which hold no tokens of any row yet; the old pages can
+    be reused after the call. Returns (new_length [n], kept [n, Hkv, budget]: the positions kept,
+    then -1)."""
+    r = (_native_module or _native()).cache_evict(
+        length, page_table, new_table, k_cache, k_scale, v_cache, v_scale, weights, budget, sinks,
+        recent, new_length, kept, status, _handle(stream))
     if r.__class__ is int:
         _check(r)
     return r
