@@ -599,7 +599,7 @@ KDA_API kda_status kda_draft_verify(kda_dtype dt, int batch, int window, int voc
  *               NULL (not the same buffer). An empty sequence passes its state through.
  *   workspace   at least kda_decay_prefill_workspace(...) bytes (0 for sizes that are refused or
  *               need none), 256-byte aligned; contents need not be initialised.
- *   n_seqs at most 2^24, H at most 65535.
+ *   n_seqs at most 2^24, total_tokens 2^30, H 65535, (total_tokens / 256 + n_seqs) * H below 2^31.
  *   status      optional device word (KDA_STATUS_BAD_OFFSETS, KDA_STATUS_TIMEOUT).
  * bf16 runs on the tensor cores (KDA_ERR_UNSUPPORTED when the driver lacks cuTensorMapEncodeTiled),
  * fp32 on CUDA cores. With bf16 the state enters the outputs as two bf16 parts (16 bits), as do

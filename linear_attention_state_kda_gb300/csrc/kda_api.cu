@@ -690,8 +690,8 @@ kda_status kda_draft_verify(kda_dtype dt, int batch, int window, int vocab,
 }
 
 size_t kda_decay_prefill_workspace(kda_dtype dt, int n_seqs, int total_tokens, int H, int d) {
-  if ((dt != KDA_F32 && dt != KDA_BF16) || n_seqs <= 0 || total_tokens <= 0 || H <= 0 ||
-      H > 65535 || (d != 64 && d != 128))
+  if ((dt != KDA_F32 && dt != KDA_BF16) || n_seqs <= 0 || total_tokens <= 0 ||
+      total_tokens > (1 << 30) || H <= 0 || H > 65535 || (d != 64 && d != 128))
     return 0;
   return decay_prefill_workspace_bytes(dt, total_tokens, H, d);
 }
@@ -705,8 +705,11 @@ kda_status kda_decay_prefill(kda_dtype dt, int n_seqs, int total_tokens, const i
   const char* fn = "kda_decay_prefill";
   kda_status st = check_decay_heads(fn, dt, H, Hk, d);
   if (st != KDA_OK) return st;
-  KDA_REQUIRE(n_seqs >= 0 && n_seqs <= (1 << 24) && total_tokens >= 0, KDA_ERR_INVALID_ARG,
-              "kda_decay_prefill: n_seqs must be in 0 .. 2^24, total_tokens >= 0");
+  KDA_REQUIRE(n_seqs >= 0 && n_seqs <= (1 << 24) && total_tokens >= 0 && total_tokens <= (1 << 30) &&
+                  ((int64_t)total_tokens / 256 + n_seqs) * H <= 0x7fffffffLL,
+              KDA_ERR_INVALID_ARG,
+              "kda_decay_prefill: n_seqs must be in 0 .. 2^24, total_tokens in 0 .. 2^30, "
+              "(total_tokens / 256 + n_seqs) * H below 2^31");
   KDA_REQUIRE(cu_seqlens || n_seqs <= 1, KDA_ERR_INVALID_ARG,
               "kda_decay_prefill: cu_seqlens is required for more than one sequence");
   if (n_seqs == 0 || (total_tokens == 0 && !final_state)) return KDA_OK;

@@ -1,7 +1,7 @@
 // Linear attention with one decay per head,
 //     S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,
 // for tokens and verify windows over the slot-addressed state pool, and, on CUDA cores, for
-// prompts in chunks. (Prompts in bf16 run on the tensor cores, kda_decay_tc.cu.)
+// fp32 prompts in chunks. (Prompts in bf16 run on the tensor cores, kda_decay_tc.cu.)
 #include "kda_decay.cuh"
 #include "kda_fp8.cuh"
 
@@ -125,10 +125,11 @@ struct SimtShape {
   static constexpr int floats = 2 * kC * DP + kC * VP + D * VP + kC * PP;
 };
 
-template <int D, class T, bool kStates>
+template <int D, bool kStates>
 __global__ void __launch_bounds__(kSimtThreads)
 decay_chunk_kernel(const DecayParams p, int seg, float* added, float* added_log) {
   using S = SimtShape<D>;
+  using T = float;
   constexpr int RPT = D / 16, N = Vec16<T>::N;
   extern __shared__ float smem[];
   float* sq = smem;
@@ -139,7 +140,6 @@ decay_chunk_kernel(const DecayParams p, int seg, float* added, float* added_log)
   __shared__ float2 gam[kC];
   __shared__ float s_in[kC], s_out[kC];  // e^gamma_i, e^(gamma_C - gamma_i)
   __shared__ float s_total;
-  __shared__ int64_t s_sum;
 
   const int h = blockIdx.y, col0 = blockIdx.z * kCols, tid = threadIdx.x;
   Segment x;
@@ -326,37 +326,47 @@ decay_scan_kernel(const DecayParams p, int seg, float* added, const float* added
   }
 }
 
-int segment_tokens(kda_dtype, int total, int H, int d) {
-  // about two segments per SM and head column tile
-  const int64_t units = (int64_t)H * (d / kCols);
-  int64_t seg = ((int64_t)total * units / 304 + 63) / 64 * 64;
-  return (int)(seg < 256 ? 256 : seg);
+// Tokens of a segment: so that the segments of all heads are at most two per SM, and no fewer than
+// a few chunks' worth of work outweighs the state that a segment has to write and read.
+int segment_tokens(kda_dtype dt, int total, int H, int d) {
+  const int64_t units = (int64_t)H * (dt == KDA_BF16 ? 1 : d / kCols);
+  const int64_t want = units < 304 ? 304 / units : 1;
+  const int64_t seg = ((total + want - 1) / want + 63) / 64 * 64, least = dt == KDA_BF16 ? 512 : 256;
+  return (int)(seg < least ? least : seg);
 }
 
-template <int D, class T>
-kda_status launch_simt_t(const DecayParams& p, kda_dtype dt, cudaStream_t s) {
-  const int seg = segment_tokens(dt, p.total, p.H, D);
-  const int places = p.total / seg;
+template <int D>
+kda_status launch_simt(const DecayParams& p, int seg, float* added, float* added_log,
+                       cudaStream_t s) {
   const size_t smem = SimtShape<D>::floats * sizeof(float);
-  const dim3 grid((unsigned)(places + p.n_seqs), (unsigned)p.H, D / kCols);
-  float* added = (float*)p.ws;
-  float* added_log = added ? added + (int64_t)places * p.H * (D * D) : nullptr;
-  cudaFuncSetAttribute(decay_chunk_kernel<D, T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const dim3 grid((unsigned)(p.total / seg + p.n_seqs), (unsigned)p.H, D / kCols);
+  cudaFuncSetAttribute(decay_chunk_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        (int)smem);
-  cudaFuncSetAttribute(decay_chunk_kernel<D, T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaFuncSetAttribute(decay_chunk_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        (int)smem);
   if (p.total > seg) {
-    decay_chunk_kernel<D, T, true><<<grid, kSimtThreads, smem, s>>>(p, seg, added, added_log);
-    decay_scan_kernel<D><<<dim3((unsigned)p.n_seqs * (D * D / 1024), (unsigned)p.H), 256, 0, s>>>(
-        p, seg, added, added_log);
-    count_launches(2);
+    decay_chunk_kernel<D, true><<<grid, kSimtThreads, smem, s>>>(p, seg, added, added_log);
+    launch_decay_scan(p, D, seg, added, added_log, s);
+    count_launches(1);
   }
-  decay_chunk_kernel<D, T, false><<<grid, kSimtThreads, smem, s>>>(p, seg, added, added_log);
+  decay_chunk_kernel<D, false><<<grid, kSimtThreads, smem, s>>>(p, seg, added, added_log);
   count_launches(1);
   return check_launch("kda_decay_prefill");
 }
 
 }  // namespace
+
+namespace decay {
+
+void launch_decay_scan(const DecayParams& p, int d, int seg, float* added, const float* added_log,
+                       cudaStream_t s) {
+  const dim3 grid((unsigned)p.n_seqs * (unsigned)(d * d / 1024), (unsigned)p.H);
+  if (d == 128) decay_scan_kernel<128><<<grid, 256, 0, s>>>(p, seg, added, added_log);
+  else decay_scan_kernel<64><<<grid, 256, 0, s>>>(p, seg, added, added_log);
+  count_launches(1);
+}
+
+}  // namespace decay
 
 size_t decay_prefill_workspace_bytes(kda_dtype dt, int total, int H, int d) {
   const int seg = segment_tokens(dt, total, H, d);
@@ -365,10 +375,12 @@ size_t decay_prefill_workspace_bytes(kda_dtype dt, int total, int H, int d) {
 }
 
 kda_status launch_decay_prefill(const DecayParams& p, kda_dtype dt, int d, cudaStream_t s) {
-  if (dt == KDA_BF16)
-    return d == 128 ? launch_simt_t<128, __nv_bfloat16>(p, dt, s)
-                    : launch_simt_t<64, __nv_bfloat16>(p, dt, s);
-  return d == 128 ? launch_simt_t<128, float>(p, dt, s) : launch_simt_t<64, float>(p, dt, s);
+  const int seg = segment_tokens(dt, p.total, p.H, d);
+  float* added = (float*)p.ws;
+  float* added_log = added ? added + (int64_t)(p.total / seg) * p.H * (d * d) : nullptr;
+  if (dt == KDA_BF16) return launch_tc(p, d, seg, added, added_log, s);
+  return d == 128 ? launch_simt<128>(p, seg, added, added_log, s)
+                  : launch_simt<64>(p, seg, added, added_log, s);
 }
 
 kda_status launch_decay_window(const DecayParams& p, kda_dtype dt, int d, cudaStream_t s) {

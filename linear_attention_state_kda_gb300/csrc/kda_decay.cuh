@@ -69,5 +69,11 @@ __device__ __forceinline__ float decay_between(float2 a, float2 b) {
   return exp2f((a.x - b.x) + (a.y - b.y));
 }
 
+// The scan over the segments' added states, and the tensor-core kernels for bf16.
+void launch_decay_scan(const DecayParams& p, int d, int seg, float* added, const float* added_log,
+                       cudaStream_t s);
+kda_status launch_tc(const DecayParams& p, int d, int seg, float* added, float* added_log,
+                     cudaStream_t s);
+
 }  // namespace decay
 }  // namespace kda

@@ -28,7 +28,6 @@ namespace {
 // two f16 parts.
 constexpr int kWThreads = 256;
 constexpr int kWWarps = kWThreads / 32;
-constexpr int kGroupRows = 64;  // query rows scored at once
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {

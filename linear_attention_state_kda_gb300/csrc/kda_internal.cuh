@@ -74,6 +74,10 @@ bool chunk_tc_available();
 // box [box_rows][box_cols]; false when the driver lacks the encoder or rejects the layout.
 bool make_map_rows(CUtensorMap* m, const void* ptr, bool f32, uint64_t cols, uint64_t rows,
                    uint32_t box_cols, uint32_t box_rows);
+// A bf16 array of `rows` rows of `cols` contiguous entries, row_bytes apart (a multiple of 16), as a
+// 2-D tensor map, box [box_rows][box_cols], plain or with the 128-byte swizzle (box_cols 64).
+bool make_map_tokens(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows,
+                     uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows, bool swizzle);
 // phases: kPhasePrep writes the records, kPhaseState walks them; both = one chunked call.
 // kPhaseFlags (with kPhaseState alone) makes the walk wait for each record's ready flag in
 // the workspace, as the fused launch's walk does (the flag-wait diagnostic).
