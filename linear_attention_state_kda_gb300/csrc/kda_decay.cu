@@ -317,12 +317,25 @@ decay_scan_kernel(const DecayParams p, int seg, float* added, const float* added
   if (p.init)
     x = *reinterpret_cast<const float4*>(p.init + ((int64_t)s * p.H + h) * (D * D) + e);
   const int64_t first = c0 / seg, n = (c1 - c0 + seg - 1) / seg - 1;
-  for (int64_t j = first; j < first + n; ++j) {
-    const float a = exp2f(added_log[j * p.H + h]);
-    float4* y = reinterpret_cast<float4*>(added + (j * p.H + h) * (int64_t)(D * D) + e);
-    const float4 f = *y;
-    x = make_float4(fmaf(a, x.x, f.x), fmaf(a, x.y, f.y), fmaf(a, x.z, f.z), fmaf(a, x.w, f.w));
-    *y = x;
+  // four places at a time: their loads do not wait for one another
+  for (int64_t j0 = first; j0 < first + n; j0 += 4) {
+    const int m = (int)(first + n - j0 < 4 ? first + n - j0 : 4);
+    float4 f[4];
+    float a[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= m) break;
+      a[i] = added_log[(j0 + i) * p.H + h];
+      f[i] = *reinterpret_cast<const float4*>(added + ((j0 + i) * p.H + h) * (int64_t)(D * D) + e);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= m) break;
+      const float b = exp2f(a[i]);
+      x = make_float4(fmaf(b, x.x, f[i].x), fmaf(b, x.y, f[i].y), fmaf(b, x.z, f[i].z),
+                      fmaf(b, x.w, f[i].w));
+      *reinterpret_cast<float4*>(added + ((j0 + i) * p.H + h) * (int64_t)(D * D) + e) = x;
+    }
   }
 }
 

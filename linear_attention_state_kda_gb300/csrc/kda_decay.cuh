@@ -52,17 +52,20 @@ __device__ __forceinline__ bool find_segment(const DecayParams& p, int seg, int 
 
 // Log-decays in units of 2^-40 of a base-2 exponent, as integers: sums of any number of them are
 // exact, so the decay between two tokens does not lose bits to a strong decay before both. A
-// token's decay below 2^-400 counts as that: no fp32 state survives it either way.
-constexpr double kLogUnit = 1099511627776.0 * 1.4426950408889634;  // 2^40 / ln 2
+// token's decay below e^-277 (2^-400) counts as that: no fp32 state survives it either way.
+// (In fp32 pairs: double precision runs at 1/64 of the rate and took 2500 cycles a chunk.)
 __device__ __forceinline__ int64_t log_units(float g) {
   g = g < -277.0f ? -277.0f : g;  // (a NaN stays)
-  return __double2ll_rn((double)g * kLogUnit);
+  // g / ln 2 as the sum of two floats
+  const float c0 = 1.4426950216293335f, c1 = 1.9259629911266175e-8f;
+  const float a = g * c0, b = fmaf(g, c1, fmaf(g, c0, -a));
+  return __float2ll_rn(a * 1099511627776.0f) + __float2ll_rn(b * 1099511627776.0f);
 }
 // A sum of log units as a pair of floats, hi + lo, in base-2 exponents.
 __device__ __forceinline__ float2 log_pair(int64_t u) {
-  const double x = (double)u * 9.094947017729282e-13;  // 2^-40
-  const float hi = (float)x;
-  return make_float2(hi, (float)(x - (double)hi));
+  const float hi = __ll2float_rn(u);
+  const float lo = __ll2float_rn(u - __float2ll_rn(hi));
+  return make_float2(hi * 9.094947017729282e-13f, lo * 9.094947017729282e-13f);  // 2^-40
 }
 // 2^(a - b).
 __device__ __forceinline__ float decay_between(float2 a, float2 b) {

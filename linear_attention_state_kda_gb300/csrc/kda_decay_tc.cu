@@ -10,10 +10,11 @@
 // them stays for the rest of the sequence). The two sums of O have accumulators of their own and
 // meet in fp32, so that Q needs no decayed copy.
 //
-// Roles of a CTA (one segment of one head, 16 warps): one warp loads (TMA) and sums the decays; one
-// issues the products; 4 build V'; 2 turn q.k into P; 4 split and decay the state; 4 write outputs.
-// Order of the products per chunk: q.k of the next chunk; V'^T K, whose result the next chunk's
-// state waits for; then S^T Q^T and V^T P^T, which run while the state is split again.
+// Roles of a CTA (one segment of one head, 24 warps): one warp loads (TMA) and sums the decays; one
+// issues the products; 8 put V and V' into TMEM, transposed on the way; 2 turn q.k into P; 8 split
+// and decay the state; 4 write outputs. Order of the products per chunk: V'^T K, whose result the
+// next chunk's state waits for; then S^T Q^T, V^T P^T and the next chunk's q.k, which run while the
+// state is decayed and split again.
 #include "kda_decay.cuh"
 #include "kda_fp8.cuh"
 #include "ptx.cuh"
@@ -24,8 +25,9 @@ namespace {
 using namespace decay;
 
 constexpr int kC = 64;
-constexpr int kStages = 3;
-constexpr int kThreads = 512;
+constexpr int kStages = 4;
+constexpr int kThreads = 768;
+constexpr int kAhead = 3;
 constexpr uint32_t kTries = 1u << 19;  // of a wait inside a CTA: 2 s
 
 struct Maps {
@@ -33,33 +35,34 @@ struct Maps {
 };
 
 // Offsets in shared memory. Operand tiles are [64 tokens][64 channels] blocks of 8 KB (128-byte
-// swizzle), D / 64 of them side by side. Products with M = 128 read the 64 rows or channels after
-// a tile's own, into accumulator lanes that no one reads: the order Q, V, K keeps those reads inside
-// the stage, and V' before P inside the operands.
+// swizzle), D / 64 of them side by side. q.k is a product with M = 128 on 64 rows: it reads the 64
+// rows after its own, into accumulator lanes that no one reads. The order Q, K, V keeps that inside
+// the stage.
 template <int D>
 struct Out {
   static constexpr int TILE = kC * D * 2, STAGE = 3 * TILE;
-  static constexpr int Q = 0, V = TILE, K = 2 * TILE;
-  static constexpr int VP = kStages * STAGE;      // three parts
-  static constexpr int P = VP + 3 * TILE;         // two parts of 8 KB
-  static constexpr int O = P + 2 * 8192;          // [64][D] bf16
+  static constexpr int Q = 0, K = TILE, V = 2 * TILE;
+  static constexpr int P = kStages * STAGE;  // two parts of 8 KB
+  static constexpr int O = P + 2 * 8192;     // outputs, as Q
   static constexpr int SMALL = O + TILE;
 };
 struct OutSmall {
   uint64_t full[kStages], empty[kStages];
-  uint64_t sc_full[2], sc_empty[2];
-  uint64_t p_full, v_full, st_full, kv_done, o_full, o_empty, drain;
-  alignas(16) float2 gam[kStages][kC];  // running sums of log2 decays, as pairs
-  float ein[kStages][kC];   // 2^gamma
+  uint64_t sc_full, sc_empty, p_full, v_full, vt_full, s_full, part_full;
+  uint64_t kv_done, sq_done, x_full, o_full, o_empty, drain;
+  float g[kAhead][kC];                       // log-decays of the next chunks
+  float ghi[kStages][kC], glo[kStages][kC];  // running sums of log2 decays, high and low parts
   float2 total[kStages];
   uint32_t tmem;
   int abort;
 };
-// TMEM columns
+// TMEM columns: the state (fp32) and its two parts, V' in three parts and V (transposed, two tokens a
+// column), the scores, and the outputs, all 512 at D = 128.
 template <int D>
 struct Tm {
-  static constexpr int S = 0, HI = D, LO = HI + D / 2, SC = LO + D / 2, OI = SC + 128, OA = OI + 64;
-  static_assert(OA + 64 <= 512, "TMEM");
+  static constexpr int S = 0, HI = D, LO = HI + D / 2, VP = LO + D / 2, VT = VP + 96, SC = VT + 32,
+                       O = SC + 64;
+  static_assert(O + 64 <= 512, "TMEM");
 };
 
 __device__ __forceinline__ void st_shared(uint32_t at, const uint4& v) {
@@ -87,26 +90,30 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Two values in two bf16 parts: the first truncated, the rest rounded (2^-16 in all). An infinity or
-// NaN stays one: its rest is NaN.
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = tops(a, b);
-  lo = pack_bf16(a - top(a), b - top(b));
+// The bf16 of a pair by truncation, and the exact rest.
+__device__ __forceinline__ uint32_t take_top(ptx::f32x2& x) {
+  float a, b;
+  ptx::unpack2(x, a, b);
+  x = ptx::fma2(ptx::pack2(top(a), top(b)), ptx::pack2(-1.0f, -1.0f), x);
+  return tops(a, b);
 }
-// Eight values in three parts: 8 bits each, exact.
-__device__ __forceinline__ void split3(const float* x, uint4& hi, uint4& mid, uint4& lo) {
-  uint32_t h[4], m[4], l[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = x[2 * i], b = x[2 * i + 1];
-    h[i] = tops(a, b);
-    const float ra = a - top(a), rb = b - top(b);
-    m[i] = tops(ra, rb);
-    l[i] = tops(ra - top(ra), rb - top(rb));
-  }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  mid = make_uint4(m[0], m[1], m[2], m[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
+// A pair in two bf16 parts: the first truncated, the rest rounded (2^-16 in all). An infinity or NaN
+// stays one: its rest is NaN.
+__device__ __forceinline__ void split2(ptx::f32x2 x, uint32_t& hi, uint32_t& lo) {
+  hi = take_top(x);
+  float a, b;
+  ptx::unpack2(x, a, b);
+  lo = pack_bf16(a, b);
+}
+// Two bf16 values times two weights in three parts of 8 bits: the fp32 products exactly.
+__device__ __forceinline__ void weigh3(uint32_t v, ptx::f32x2 w, uint32_t part[3]) {
+  ptx::f32x2 f =
+      ptx::mul2(ptx::pack2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)), w);
+  part[0] = take_top(f);
+  part[1] = take_top(f);
+  float a, b;
+  ptx::unpack2(f, a, b);
+  part[2] = tops(a, b);
 }
 
 // D x 64 tile of a head's rows from token t0.
@@ -118,19 +125,17 @@ __device__ __forceinline__ void load_tile(void* dst, const CUtensorMap* m, uint6
     ptx::tma_load_2d((uint8_t*)dst + i * 8192, m, bar, head * D + i * 64, t0);
 }
 
-// V'^T K of a chunk into the state: three parts of V' (MN-major), K (MN-major).
+// V'^T K of a chunk into the state: three parts of V' (TMEM), K (MN-major).
 template <int D>
 __device__ __forceinline__ void issue_kv(uint32_t tmem_s, uint32_t vp, uint32_t k, bool fresh) {
-  const uint32_t id = ptx::idesc_make(ptx::kFmtBF16, 128, D, true, true);
+  const uint32_t id = ptx::idesc_make(ptx::kFmtBF16, 128, D, false, true);
   const uint64_t b = ptx::sdesc_sw128(k, 8192, 1024);
 #pragma unroll
-  for (int part = 0; part < 3; ++part) {
-    const uint64_t a = ptx::sdesc_sw128(vp + part * (kC * D * 2), 8192, 1024);
+  for (int part = 0; part < 3; ++part)
 #pragma unroll
     for (int i = 0; i < kC / 16; ++i)
-      ptx::mma_f16(tmem_s, ptx::desc_add(a, i * 2048), ptx::desc_add(b, i * 2048), id,
-                   !fresh || part > 0 || i > 0);
-  }
+      ptx::mma_f16_ts(tmem_s, vp + part * 32 + i * 8, ptx::desc_add(b, i * 2048), id,
+                      !fresh || part > 0 || i > 0);
 }
 
 // 16 bytes (8 channels) number i of a tile: row i / (D / 8), swizzled place.
@@ -138,6 +143,40 @@ template <int D>
 __device__ __forceinline__ uint32_t tile_at(int i) {
   const int t = i / (D / 8), c = i % (D / 8);
   return (uint32_t)((c >> 3) * 8192 + t * 128 + (((c & 7) ^ (t & 7)) << 4));
+}
+// A ring of the next chunks' log-decays: lane l has tokens 2 l and 2 l + 1. Loaded kAhead chunks
+// before their use: the latency of one load is as long as a chunk.
+struct DecayRing {
+  float (*ring)[kC];
+  const float* g;
+  int64_t stride;
+  int lane;
+  // Asks for the tokens from t0 on (those at or after t_end count as 0); every call is a group.
+  __device__ __forceinline__ void ask(int n, int64_t t0, int64_t t_end) const {
+    float* dst = &ring[n % kAhead][2 * lane];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t t = t0 + 2 * lane + i;
+      if (t < t_end) ptx::cp_async4(dst + i, g + t * stride);
+      else dst[i] = 0.0f;
+    }
+    ptx::cp_async_commit();
+  }
+  // Chunk n's, once all but the latest kAhead - 1 groups have arrived.
+  __device__ __forceinline__ float2 take(int n) const {
+    ptx::cp_async_wait<kAhead - 1>();
+    return *reinterpret_cast<const float2*>(&ring[n % kAhead][2 * lane]);
+  }
+};
+
+// 16 channels x 32 tokens of V, transposed: words 2 i + c hold tokens 8 i + 2 t, + 1 (t = lane % 4) of
+// channel 8 c + lane / 4.
+__device__ __forceinline__ void load_vt(uint32_t v, int ch, int tok, int lane, uint32_t* r) {
+  // lane's row: token tok + (lane >> 4) * 8 + (lane & 7), channels ch + ((lane >> 3) & 1) * 8 ..
+  const int t = tok + (lane >> 4) * 8 + (lane & 7), c = (ch + ((lane >> 3) & 1) * 8) >> 3;
+  const uint32_t at = v + (c >> 3) * 8192 + t * 128 + (((c & 7) ^ (t & 7)) << 4);
+  ptx::ld_matrix4_trans(at, r);
+  ptx::ld_matrix4_trans(at + 16 * 128, r + 4);  // (16 tokens on: the same swizzle)
 }
 __device__ __forceinline__ float nan_f() { return __int_as_float(0x7fffffff); }
 
@@ -151,6 +190,21 @@ struct Waiter {
     if (status) atomicOr(status, KDA_STATUS_TIMEOUT);
     *(volatile int*)abort = 1;
     return false;
+  }
+  // Of several barriers: they are looked at together first, since a look takes some 200 cycles beside
+  // the traffic of the products.
+  template <int N>
+  __device__ __forceinline__ bool all(uint64_t* const (&bar)[N], const uint32_t (&parity)[N]) const {
+    bool seen[N], every = true;
+#pragma unroll
+    for (int i = 0; i < N; ++i) seen[i] = ptx::mbar_test(bar[i], parity[i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) every = every && seen[i];
+    if (__all_sync(0xffffffffu, every)) return true;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (!(*this)(bar[i], parity[i])) return false;
+    return true;
   }
 };
 // Barrier of `threads` threads with the conjunction of their answers.
@@ -186,23 +240,25 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&sm.full[i], 2);
-      ptx::mbar_init(&sm.empty[i], 1 + 4 + 2 + 2 * NQ);
+      ptx::mbar_init(&sm.empty[i], 1 + 2 + 5 * NQ);
     }
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&sm.sc_full[i], 1);
-      ptx::mbar_init(&sm.sc_empty[i], 2);
-    }
+    ptx::mbar_init(&sm.sc_full, 1);
+    ptx::mbar_init(&sm.sc_empty, 2);
     ptx::mbar_init(&sm.p_full, 2);
-    ptx::mbar_init(&sm.v_full, 4);
-    ptx::mbar_init(&sm.st_full, NQ);
+    ptx::mbar_init(&sm.v_full, 2 * NQ);
+    ptx::mbar_init(&sm.vt_full, 2 * NQ);
+    ptx::mbar_init(&sm.s_full, 2 * NQ);
+    ptx::mbar_init(&sm.part_full, 2 * NQ);
     ptx::mbar_init(&sm.kv_done, 1);
+    ptx::mbar_init(&sm.sq_done, 1);
+    ptx::mbar_init(&sm.x_full, NQ);
     ptx::mbar_init(&sm.o_full, 1);
     ptx::mbar_init(&sm.o_empty, NQ);
     ptx::mbar_init(&sm.drain, 1);
     ptx::fence_mbar_init();
     sm.abort = 0;
   }
-  if (warp == 1) {
+  if (warp == 3) {
     ptx::tmem_alloc(&sm.tmem, 512);
     ptx::tmem_relinquish();
   }
@@ -217,168 +273,17 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
     if (lane == 0) ptx::mbar_arrive(bar);
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ loads and decays
-    float g0 = 0.0f, g1 = 0.0f;
-    auto load_g = [&](int n) {
-      const int t = t_first + n * kC + 2 * lane;
-      g0 = t < t_end ? __ldg(p.g + t * p.gs + h) : 0.0f;
-      g1 = t + 1 < t_end ? __ldg(p.g + (t + 1) * p.gs + h) : 0.0f;
-    };
-    load_g(0);
-    int n = 0;
-#pragma unroll 1
-    for (; n < N; ++n) {
-      const int s = n % kStages;
-      if (n >= kStages && !wait(&sm.empty[s], ((n / kStages) - 1) & 1)) break;
-      if (lane == 0) {
-        uint8_t* st = smem + s * M::STAGE;
-        const int t = t_first + n * kC;
-        ptx::mbar_arrive_expect_tx(&sm.full[s], M::STAGE);
-        load_tile<D>(st + M::K, &maps.k, &sm.full[s], hk, t);
-        load_tile<D>(st + M::Q, &maps.q, &sm.full[s], hk, t);
-        load_tile<D>(st + M::V, &maps.v, &sm.full[s], h, t);
-      }
-      const bool nan = __any_sync(0xffffffffu, g0 != g0 || g1 != g1);
-      const int64_t u0 = log_units(g0), u1 = log_units(g1);
-      if (n + 1 < N) load_g(n + 1);
-      int64_t sum = u0 + u1;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t w = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += w;
-      }
-      float2 a = log_pair(sum - u1), b = log_pair(sum);
-      if (nan) a.x = b.x = nan_f();  // a NaN decay spoils its chunk
-      *reinterpret_cast<float4*>(&sm.gam[s][2 * lane]) = make_float4(a.x, a.y, b.x, b.y);
-      *reinterpret_cast<float2*>(&sm.ein[s][2 * lane]) =
-          make_float2(ptx::ex2_approx(a.x + a.y), ptx::ex2_approx(b.x + b.y));
-      if (lane == 31) sm.total[s] = b;
-      arrive(&sm.full[s]);
-    }
-    if (*(volatile int*)&sm.abort) {  // the loads in flight land before the CTA leaves
-      for (int i = n > kStages ? n - kStages : 0; i < n; ++i)
-        ptx::mbar_wait_tries(&sm.full[i % kStages], (i / kStages) & 1, kTries);
-      __syncwarp();
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ products
-    const uint32_t id_qk = ptx::idesc_make(ptx::kFmtBF16, 128, kC, false, false);
-    const uint32_t id_pv = ptx::idesc_make(ptx::kFmtBF16, 128, kC, true, false);
-    auto issue_qk = [&](int n) {
-      const uint32_t st = base + (n % kStages) * M::STAGE;
-      if (ptx::elect_one()) {
-        const uint64_t a = ptx::sdesc_sw128(st + M::Q, 16, 1024);
-        const uint64_t b = ptx::sdesc_sw128(st + M::K, 16, 1024);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint32_t off = (i >> 2) * 8192 + (i & 3) * 32;
-          ptx::mma_f16(tmem + T::SC + (n & 1) * 64, ptx::desc_add(a, off), ptx::desc_add(b, off),
-                       id_qk, i > 0);
-        }
-        ptx::mma_commit(&sm.sc_full[n & 1]);
-      }
-      __syncwarp();
-    };
-    bool ok = N == 0 || wait(&sm.full[0], 0);
-    if (ok && N > 0) issue_qk(0);
-#pragma unroll 1
-    for (int n = 0; ok && n < N; ++n) {
-      const int s = n % kStages;
-      const uint32_t st = base + s * M::STAGE;
-      if (n + 1 < N) {
-        ok = wait(&sm.full[(n + 1) % kStages], ((n + 1) / kStages) & 1) &&
-             (n < 1 || wait(&sm.sc_empty[(n + 1) & 1], (((n + 1) >> 1) - 1) & 1));
-        if (!ok) break;
-        ptx::tc_fence_after();
-        issue_qk(n + 1);
-      }
-      ok = wait(&sm.v_full, n & 1) && wait(&sm.st_full, n & 1);
-      if (!ok) break;
-      ptx::tc_fence_after();
-      if (ptx::elect_one()) {
-        issue_kv<D>(tmem + T::S, base + M::VP, st + M::K, false);
-        ptx::mma_commit(&sm.kv_done);
-      }
-      __syncwarp();
-      if (n > 0 && !(ok = wait(&sm.o_empty, (n - 1) & 1))) break;
-      ptx::tc_fence_after();
-      if (ptx::elect_one()) {
-        const uint64_t b = ptx::sdesc_sw128(st + M::Q, 16, 1024);
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-            ptx::mma_f16_ts(tmem + T::OI, tmem + (part ? T::LO : T::HI) + i * 8,
-                            ptx::desc_add(b, (i >> 2) * 8192 + (i & 3) * 32),
-                            ptx::idesc_make(ptx::kFmtBF16, 128, kC, false, false), part > 0 || i > 0);
-      }
-      __syncwarp();
-      if (!(ok = wait(&sm.p_full, n & 1))) break;
-      ptx::tc_fence_after();
-      if (ptx::elect_one()) {
-        const uint64_t a = ptx::sdesc_sw128(st + M::V, 8192, 1024);
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          const uint64_t b = ptx::sdesc_sw128(base + M::P + part * 8192, 16, 1024);
-#pragma unroll
-          for (int i = 0; i < kC / 16; ++i)
-            ptx::mma_f16(tmem + T::OA, ptx::desc_add(a, i * 2048), ptx::desc_add(b, i * 32), id_pv,
-                         part > 0 || i > 0);
-        }
-        ptx::mma_commit(&sm.o_full);
-        ptx::mma_commit(&sm.empty[s]);
-      }
-      __syncwarp();
-    }
-    if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort)) {  // the products in flight end first
-      if (ptx::elect_one()) ptx::mma_commit(&sm.drain);
-      __syncwarp();
-      ptx::mbar_wait_tries(&sm.drain, 0, kTries);
-      __syncwarp();
-    }
-  } else if (warp < 4 || warp >= 14) {
-    // ------------------------------------------------------------------ V'
-    const int tid = (warp < 4 ? warp - 2 : warp - 12) * 32 + lane;
-#pragma unroll 1
-    for (int n = 0; n < N; ++n) {
-      const int s = n % kStages;
-      const uint32_t st = base + s * M::STAGE;
-      const int m = t_end - (t_first + n * kC);  // tokens left
-      if (!wait(&sm.full[s], (n / kStages) & 1)) break;
-      if (n > 0 && !wait(&sm.kv_done, (n - 1) & 1)) break;
-      const float2 total = sm.total[s];
-#pragma unroll
-      for (int i = 0; i < kC * D / 8 / 128; ++i) {
-        const int at = i * 128 + tid, t = at / (D / 8);
-        const uint32_t off = tile_at<D>(at);
-        const float2 gt = sm.gam[s][t];
-        const float w = ptx::ex2_approx((total.x - gt.x) + (total.y - gt.y));
-        float f[8];
-        Vec16<__nv_bfloat16>::unpack(ld_shared(st + M::V + off), f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] *= w;
-        uint4 part[3];
-        split3(f, part[0], part[1], part[2]);
-        if (t >= m) {  // rows of the next sequence, whatever they hold
-          const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-          part[0] = part[1] = part[2] = z;
-          st_shared(st + M::V + off, z);
-          st_shared(st + M::K + off, z);
-        }
-#pragma unroll
-        for (int j = 0; j < 3; ++j) st_shared(base + M::VP + j * M::TILE + off, part[j]);
-      }
-      ptx::fence_proxy_async_smem();
-      arrive(&sm.v_full);
-      if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
-    }
-  } else if (warp < 8) {
+  // registers of the six warpgroups: 64 + 112 + 112 + 64 + 64 + 64 = 6 x 80
+  if (warp >= 4 && warp < 12) {
+    ptx::regs_take<112>();
     // ------------------------------------------------------------------ the state
-    const int w = warp - 4;
+    const int w = warp & 3, half = (warp - 4) >> 2;  // 32 value channels, half of the key channels
     if (w < NQ) {
+      constexpr int CB = D / 64;  // blocks of 32 key channels
       const uint32_t lanes = (uint32_t)(w * 32) << 16;
-      const int dv = w * 32 + lane;
+      const uint32_t t_s = tmem + lanes + T::S + half * (D / 2);
+      const uint32_t t_part = tmem + lanes + half * (D / 4);
+      const int64_t at = (int64_t)half * (D / 2) * D + w * 32 + lane;  // of the state's matrix
       const float* entry = !x.first ? added + ((x.place - 1) * p.H + h) * (int64_t)(D * D)
                            : p.init ? p.init + ((int64_t)x.seq * p.H + h) * (D * D) : nullptr;
       float* exit_state =
@@ -387,165 +292,440 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
 #pragma unroll 1
       for (int n = 0; n < N; ++n) {
         const int s = n % kStages;
-        ok = wait(&sm.full[s], (n / kStages) & 1) &&
-             (n == 0 || (wait(&sm.kv_done, (n - 1) & 1) && wait(&sm.o_full, (n - 1) & 1)));
+        ok = wait(&sm.full[s], (n / kStages) & 1) && (n == 0 || wait(&sm.kv_done, (n - 1) & 1));
         if (!ok) break;
         ptx::tc_fence_after();
         const float a = ptx::ex2_approx(sm.total[s].x + sm.total[s].y);
+        const ptx::f32x2 aa = ptx::pack2(a, a);
+        // decayed for the next sum first, which is what the products wait for
+        float hi[CB][16], lo[CB][16];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < CB; ++c) {
           float f[32];
           if (n > 0) {
-            ptx::tmem_ld32(tmem + lanes + T::S + c * 32, f);
+            ptx::tmem_ld32(t_s + c * 32, f);
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = entry ? entry[(c * 32 + i) * D + dv] : 0.0f;
+            for (int i = 0; i < 32; ++i) f[i] = entry ? entry[at + (c * 32 + i) * D] : 0.0f;
           }
-          float hi[16], lo[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
+            const ptx::f32x2 y = ptx::pack2(f[2 * i], f[2 * i + 1]);
             uint32_t u, v;
-            split2(f[2 * i], f[2 * i + 1], u, v);
-            hi[i] = __uint_as_float(u);
-            lo[i] = __uint_as_float(v);
-            f[2 * i] *= a;
-            f[2 * i + 1] *= a;
+            split2(y, u, v);
+            hi[c][i] = __uint_as_float(u);
+            lo[c][i] = __uint_as_float(v);
+            ptx::unpack2(ptx::mul2(y, aa), f[2 * i], f[2 * i + 1]);
           }
-          ptx::tmem_st16(tmem + lanes + T::HI + c * 16, hi);
-          ptx::tmem_st16(tmem + lanes + T::LO + c * 16, lo);
-          ptx::tmem_st32_nowait(tmem + lanes + T::S + c * 32, f);
+          ptx::tmem_st32_nowait(t_s + c * 32, f);
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
-        arrive(&sm.st_full);
+        arrive(&sm.s_full);
         if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
+        if (n > 0 && !(ok = wait(&sm.sq_done, (n - 1) & 1))) break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+          ptx::tmem_st16(t_part + T::HI + c * 16, hi[c]);
+          ptx::tmem_st16(t_part + T::LO + c * 16, lo[c]);
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        arrive(&sm.part_full);
       }
       if (ok && exit_state) {
         if (N > 0) ok = wait(&sm.kv_done, (N - 1) & 1);
         ptx::tc_fence_after();
         if (ok) {
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c < CB; ++c) {
             float f[32];
             if (N > 0) {
-              ptx::tmem_ld32(tmem + lanes + T::S + c * 32, f);
+              ptx::tmem_ld32(t_s + c * 32, f);
             } else {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) f[i] = entry ? entry[(c * 32 + i) * D + dv] : 0.0f;
+              for (int i = 0; i < 32; ++i) f[i] = entry ? entry[at + (c * 32 + i) * D] : 0.0f;
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) exit_state[(c * 32 + i) * D + dv] = f[i];
+            for (int i = 0; i < 32; ++i) exit_state[at + (c * 32 + i) * D] = f[i];
           }
         }
       }
     }
-  } else if (warp < 12) {
-    // ------------------------------------------------------------------ outputs
-    const int w = warp - 8;
-    if (w < NQ) {
+  } else {
+    ptx::regs_give<64>();
+    if (warp == 2) {
+      // ------------------------------------------------------------------ loads and decays
+      const DecayRing ring{sm.g, p.g + h, p.gs, lane};
+      auto load = [&](int n) {
+        if (lane != 0) return;
+        const int s = n % kStages, t = t_first + n * kC;
+        uint8_t* st = smem + s * M::STAGE;
+        ptx::mbar_arrive_expect_tx(&sm.full[s], M::STAGE);
+        load_tile<D>(st + M::K, &maps.k, &sm.full[s], hk, t);
+        load_tile<D>(st + M::Q, &maps.q, &sm.full[s], hk, t);
+        load_tile<D>(st + M::V, &maps.v, &sm.full[s], h, t);
+      };
+      for (int i = 0; i < kAhead; ++i) ring.ask(i, t_first + (int64_t)i * kC, t_end);
+      for (int i = 0; i < kStages && i < N; ++i) load(i);
+      int n = 0;
+#pragma unroll 1
+      for (; n < N; ++n) {
+        const int s = n % kStages;
+        // the decays, while the stage is still in use
+        const float2 g = ring.take(n);
+        const bool nan = __any_sync(0xffffffffu, g.x != g.x || g.y != g.y);
+        const int64_t u0 = log_units(g.x), u1 = log_units(g.y);
+        ring.ask(n + kAhead, t_first + (int64_t)(n + kAhead) * kC, t_end);
+        int64_t sum = u0 + u1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t w = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += w;
+        }
+        float2 a = log_pair(sum - u1), b = log_pair(sum);
+        if (nan) a.x = b.x = nan_f();  // a NaN decay spoils its chunk
+        if (n >= kStages) {
+          if (!wait(&sm.empty[s], ((n / kStages) - 1) & 1)) break;
+          load(n);
+        }
+        *reinterpret_cast<float2*>(&sm.ghi[s][2 * lane]) = make_float2(a.x, b.x);
+        *reinterpret_cast<float2*>(&sm.glo[s][2 * lane]) = make_float2(a.y, b.y);
+        if (lane == 31) sm.total[s] = b;
+        arrive(&sm.full[s]);
+      }
+      if (*(volatile int*)&sm.abort) {  // the loads in flight land before the CTA leaves
+        for (int i = n > kStages ? n - kStages : 0; i < n; ++i)
+          ptx::mbar_wait_tries(&sm.full[i % kStages], (i / kStages) & 1, kTries);
+        __syncwarp();
+      }
+      ptx::cp_async_wait<0>();
+    } else if (warp == 3) {
+      // ------------------------------------------------------------------ products
+      const uint32_t id64 = ptx::idesc_make(ptx::kFmtBF16, 128, kC, false, false);
+      auto issue_qk = [&](int n) {
+        const uint32_t st = base + (n % kStages) * M::STAGE;
+        if (ptx::elect_one()) {
+          const uint64_t a = ptx::sdesc_sw128(st + M::Q, 16, 1024);
+          const uint64_t b = ptx::sdesc_sw128(st + M::K, 16, 1024);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t off = (i >> 2) * 8192 + (i & 3) * 32;
+            ptx::mma_f16(tmem + T::SC, ptx::desc_add(a, off), ptx::desc_add(b, off), id64, i > 0);
+          }
+          ptx::mma_commit(&sm.sc_full);
+        }
+        __syncwarp();
+      };
+      bool ok = N == 0 || wait(&sm.full[0], 0);
+      if (ok && N > 0) issue_qk(0);
+#pragma unroll 1
+      for (int n = 0; ok && n < N; ++n) {
+        const int s = n % kStages;
+        const uint32_t st = base + s * M::STAGE;
+        const uint32_t ph = n & 1;
+        ok = wait.all({&sm.s_full, &sm.v_full}, {ph, ph});
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          issue_kv<D>(tmem + T::S, tmem + T::VP, st + M::K, false);
+          ptx::mma_commit(&sm.kv_done);
+        }
+        __syncwarp();
+        ok = n == 0 ? wait(&sm.part_full, 0)
+                    : wait.all({&sm.part_full, &sm.o_empty}, {ph, ph ^ 1});
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          const uint64_t b = ptx::sdesc_sw128(st + M::Q, 16, 1024);
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+              ptx::mma_f16_ts(tmem + T::O, tmem + (part ? T::LO : T::HI) + i * 8,
+                              ptx::desc_add(b, (i >> 2) * 8192 + (i & 3) * 32), id64,
+                              part > 0 || i > 0);
+          ptx::mma_commit(&sm.sq_done);
+          ptx::mma_commit(&sm.empty[s]);
+        }
+        __syncwarp();
+        if (n + 1 < N) {
+          ok = wait.all({&sm.full[(n + 1) % kStages], &sm.sc_empty},
+                        {(uint32_t)((n + 1) / kStages) & 1, ph});
+          if (!ok) break;
+          ptx::tc_fence_after();
+          issue_qk(n + 1);
+        }
+        ok = wait.all({&sm.p_full, &sm.vt_full, &sm.x_full}, {ph, ph, ph});
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            const uint64_t b = ptx::sdesc_sw128(base + M::P + part * 8192, 16, 1024);
+#pragma unroll
+            for (int i = 0; i < kC / 16; ++i)
+              ptx::mma_f16_ts(tmem + T::O, tmem + T::VT + i * 8, ptx::desc_add(b, i * 32), id64, 1);
+          }
+          ptx::mma_commit(&sm.o_full);
+        }
+        __syncwarp();
+      }
+      if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort)) {  // the products in flight end first
+        if (ptx::elect_one()) ptx::mma_commit(&sm.drain);
+        __syncwarp();
+        ptx::mbar_wait_tries(&sm.drain, 0, kTries);
+        __syncwarp();
+      }
+    } else if (warp >= 16) {
+      // ------------------------------------------------------------------ V and V', transposed
+      const int w = warp & 3, tok = ((warp - 16) >> 2) * 32;  // 32 channels, half of the tokens
+      if (w < NQ) {
+        const uint32_t lanes = (uint32_t)(w * 32) << 16;
+#pragma unroll 1
+        for (int n = 0; n < N; ++n) {
+          const int s = n % kStages;
+          const uint32_t st = base + s * M::STAGE;
+          const int m = t_end - (t_first + n * kC);  // tokens left
+          if (!wait(&sm.full[s], (n / kStages) & 1)) break;
+          const float2 total = sm.total[s];
+          ptx::f32x2 weight[4];
+          uint32_t raw[2][8];
+          load_vt(st + M::V, w * 32, tok, lane, raw[0]);
+          load_vt(st + M::V, w * 32 + 16, tok, lane, raw[1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = tok + i * 8 + 2 * (lane & 3);
+            const float2 h2 = *reinterpret_cast<const float2*>(&sm.ghi[s][t]);
+            const float2 l2 = *reinterpret_cast<const float2*>(&sm.glo[s][t]);
+            weight[i] = ptx::pack2(ptx::ex2_approx((total.x - h2.x) + (total.y - l2.x)),
+                                   ptx::ex2_approx((total.x - h2.y) + (total.y - l2.y)));
+          }
+          if (m < kC) {  // rows of the next sequence, whatever they hold: zeros, in K too
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int t = tok + i * 8 + 2 * (lane & 3);
+              const uint32_t keep = (t < m ? 0xffffu : 0u) | (t + 1 < m ? 0xffff0000u : 0u);
+              raw[0][2 * i] &= keep;
+              raw[0][2 * i + 1] &= keep;
+              raw[1][2 * i] &= keep;
+              raw[1][2 * i + 1] &= keep;
+            }
+            for (int i = (warp - 16) / 4 * (NQ * 32) + w * 32 + lane; i < kC * D / 8;
+                 i += 2 * NQ * 32)
+              if (i / (D / 8) >= m) st_shared(st + M::K + tile_at<D>(i), make_uint4(0u, 0u, 0u, 0u));
+            ptx::fence_proxy_async_smem();
+          }
+          arrive(&sm.empty[s]);
+          if (n > 0 && !wait(&sm.kv_done, (n - 1) & 1)) break;
+          ptx::tc_fence_after();
+#pragma unroll 1
+          for (int b = 0; b < 2; ++b) {
+            uint32_t part[3][8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              uint32_t x[3];
+              weigh3(b ? raw[1][i] : raw[0][i], weight[i >> 1], x);
+              part[0][i] = x[0];
+              part[1][i] = x[1];
+              part[2][i] = x[2];
+            }
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+              ptx::tmem_st_rows16_nowait(
+                  tmem + lanes + ((uint32_t)(b * 16) << 16) + T::VP + j * 32 + tok / 2, part[j]);
+          }
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+          arrive(&sm.v_full);
+          if (n > 0 && !wait(&sm.o_full, (n - 1) & 1)) break;
+          ptx::tc_fence_after();
+          ptx::tmem_st_rows16_nowait(tmem + lanes + T::VT + tok / 2, raw[0]);
+          ptx::tmem_st_rows16_nowait(tmem + lanes + (16u << 16) + T::VT + tok / 2, raw[1]);
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+          arrive(&sm.vt_full);
+        }
+      }
+    } else if (warp >= 12) {
+      // ------------------------------------------------------------------ outputs
+      const int w = warp - 12;
+      if (w < NQ) {
+        const uint32_t lanes = (uint32_t)(w * 32) << 16;
+        const int tid = w * 32 + lane;
+        const uint32_t stage = base + M::O + (w >> 1) * 8192;  // its block of 64 channels
+        const uint32_t t_o = tmem + lanes + T::O;
+        const ptx::f32x2 scale = ptx::pack2(p.scale, p.scale);
+        bool ok = true;
+#pragma unroll 1
+        for (int n = 0; n < N; ++n) {
+          const int s = n % kStages;
+          const int t0 = t_first + n * kC;
+          // S^T Q^T gets the decays from the chunk's start in place, and V^T P^T is added to it
+          ok = wait(&sm.full[s], (n / kStages) & 1) && wait(&sm.sq_done, n & 1);
+          if (ok) {
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int tok = 0; tok < kC; tok += 32) {
+              ptx::f32x2 ee[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int t = tok + i * 8 + 2 * (lane & 3);
+                const float2 h2 = *reinterpret_cast<const float2*>(&sm.ghi[s][t]);
+                const float2 l2 = *reinterpret_cast<const float2*>(&sm.glo[s][t]);
+                ee[i] = ptx::pack2(ptx::ex2_approx(h2.x + l2.x), ptx::ex2_approx(h2.y + l2.y));
+              }
+              uint32_t x[2][16];  // 16 channels x 32 tokens each
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                ptx::tmem_ld_frag32_nowait(t_o + ((uint32_t)(16 * c) << 16) + tok, x[c]);
+              ptx::tmem_ld_wait();
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[c][i]));
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                  float y0, y1;
+                  ptx::unpack2(ptx::mul2(ee[j >> 2], ptx::pack2(__uint_as_float(x[c][j]),
+                                                                __uint_as_float(x[c][j + 1]))),
+                               y0, y1);
+                  x[c][j] = __float_as_uint(y0);
+                  x[c][j + 1] = __float_as_uint(y1);
+                }
+                ptx::tmem_st_frag32_nowait(t_o + ((uint32_t)(16 * c) << 16) + tok, x[c]);
+              }
+            }
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            arrive(&sm.x_full);
+            if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
+            ok = wait(&sm.o_full, n & 1);
+          }
+          if (tid == 0) ptx::bulk_wait_read0();  // the last chunk's rows have left
+          ok = group_and(1, NQ * 32, ok);
+          if (!ok) break;
+          ptx::tc_fence_after();
+#pragma unroll 1
+          for (int tok = 0; tok < kC; tok += 32) {
+            uint32_t x[2][16];
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              ptx::tmem_ld_frag32_nowait(t_o + ((uint32_t)(16 * c) << 16) + tok, x[c]);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[c][i]));
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t o[8];
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                float y0, y1;
+                ptx::unpack2(ptx::mul2(scale, ptx::pack2(__uint_as_float(x[c][j]),
+                                                         __uint_as_float(x[c][j + 1]))),
+                             y0, y1);
+                o[j >> 1] = pack_bf16(y0, y1);
+              }
+              // matrices (channels 0-7, 8-15) x (two groups of 8 tokens): row = token
+              const int ch = ((w & 1) * 32 + c * 16) / 8 + ((lane >> 3) & 1);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int t = tok + i * 16 + (lane >> 4) * 8 + (lane & 7);
+                ptx::st_matrix4_trans(stage + t * 128 + ((ch ^ (t & 7)) << 4), o[4 * i],
+                                      o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              }
+            }
+          }
+          ptx::tc_fence_before();
+          arrive(&sm.o_empty);
+          ptx::fence_proxy_async_smem();
+          ok = group_and(1, NQ * 32, true);
+          const int m = t_end - t0;
+          if (m >= kC) {
+            if (tid == 0) {
+#pragma unroll
+              for (int i = 0; i < D / 64; ++i)
+                ptx::tma_store_2d(&maps.o, smem + M::O + i * 8192, h * D + i * 64, t0);
+              ptx::bulk_commit();
+            }
+          } else {  // the rows after the segment belong to another one
+            for (int i = tid; i < m * (D / 8); i += NQ * 32) {
+              const int t = i / (D / 8), c = i % (D / 8);
+              *reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + ((int64_t)(t0 + t) * p.H + h) * D + c * 8) =
+                  ld_shared(base + M::O + tile_at<D>(i));
+            }
+          }
+        }
+        if (tid == 0) ptx::bulk_wait0();
+      }
+    } else {
+      // ------------------------------------------------------------------ P (warps 0, 1)
+      const int w = warp, i = w * 32 + lane;  // the row
       const uint32_t lanes = (uint32_t)(w * 32) << 16;
-      const int dv = w * 32 + lane, tid = dv;
-      __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(smem + M::O);
-      bool ok = true;
 #pragma unroll 1
       for (int n = 0; n < N; ++n) {
         const int s = n % kStages;
-        const int t0 = t_first + n * kC;
-        ok = wait(&sm.o_full, n & 1) && wait(&sm.full[s], (n / kStages) & 1);
-        if (tid == 0) ptx::bulk_wait_read0();  // the last chunk's rows have left
-        ok = group_and(1, NQ * 32, ok);
-        if (!ok) break;
+        if (!(wait(&sm.full[s], (n / kStages) & 1) && wait(&sm.sc_full, n & 1) &&
+              (n == 0 || wait(&sm.o_full, (n - 1) & 1))))
+          break;
         ptx::tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t a[32], b[32];
-          ptx::tmem_ld32_nowait(tmem + lanes + T::OI + c * 32, a);
-          ptx::tmem_ld32_nowait(tmem + lanes + T::OA + c * 32, b);
-          ptx::tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(a[i]), "+r"(b[i]));
-          if (c == 1) {
-            ptx::tc_fence_before();
-            arrive(&sm.o_empty);
-          }
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 e = *reinterpret_cast<const float2*>(&sm.ein[s][c * 32 + i]);
-            const uint32_t r = pack_bf16(
-                p.scale * fmaf(e.x, __uint_as_float(a[i]), __uint_as_float(b[i])),
-                p.scale * fmaf(e.y, __uint_as_float(a[i + 1]), __uint_as_float(b[i + 1])));
-            stage[(c * 32 + i) * D + dv] = __ushort_as_bfloat16((unsigned short)r);
-            stage[(c * 32 + i + 1) * D + dv] = __ushort_as_bfloat16((unsigned short)(r >> 16));
-          }
-        }
-        arrive(&sm.empty[s]);
-        ptx::fence_proxy_async_smem();
-        ok = group_and(1, NQ * 32, true);
-        const int m = t_end - t0;
-        if (m >= kC) {
-          if (tid == 0) {
-            ptx::tma_store_2d(&maps.o, stage, h * D, t0);
-            ptx::bulk_commit();
-          }
-        } else {  // the rows after the segment belong to another one
-          for (int i = tid; i < m * (D / 8); i += NQ * 32) {
-            const int t = i / (D / 8), c = i % (D / 8);
-            *reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + ((int64_t)(t0 + t) * p.H + h) * D + c * 8) =
-                *reinterpret_cast<const uint4*>(stage + t * D + c * 8);
-          }
-        }
-      }
-      if (tid == 0) ptx::bulk_wait0();
-    }
-  } else {
-    // ------------------------------------------------------------------ P (warps 12, 13)
-    const int w = warp - 12, i = w * 32 + lane;  // the row
-    const uint32_t lanes = (uint32_t)(w * 32) << 16;
+        const ptx::f32x2 gh = ptx::pack2(sm.ghi[s][i], sm.ghi[s][i]),
+                         gl = ptx::pack2(sm.glo[s][i], sm.glo[s][i]), minus = ptx::pack2(-1.0f, -1.0f);
 #pragma unroll 1
-    for (int n = 0; n < N; ++n) {
-      const int s = n % kStages;
-      if (!(wait(&sm.full[s], (n / kStages) & 1) && wait(&sm.sc_full[n & 1], (n >> 1) & 1) &&
-            (n == 0 || wait(&sm.o_full, (n - 1) & 1))))
-        break;
-      ptx::tc_fence_after();
-      const float2 gi = sm.gam[s][i];
+        for (int c = 0; c < kC; c += 16) {
+          uint32_t hi[8], lo[8];
+          if (c < 32 * w + 32) {
+            uint32_t r[16];
+            ptx::tmem_ld16_nowait(tmem + lanes + T::SC + c, r);
+            ptx::tmem_ld_wait();
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float f[32];
-        if (c <= w) ptx::tmem_ld32(tmem + lanes + T::SC + (n & 1) * 64 + c * 32, f);
-        if (c == w) {
-          ptx::tc_fence_before();
-          arrive(&sm.sc_empty[n & 1]);
-        }
-        if (c <= w) {
+            for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(r[j]));
+            if (c == 32 * w + 16) {  // all of them read
+              ptx::tc_fence_before();
+              arrive(&sm.sc_empty);
+            }
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float2 gj = sm.gam[s][c * 32 + j];
-            const float d = ptx::ex2_approx((gi.x - gj.x) + (gi.y - gj.y));
-            f[j] = c * 32 + j <= i ? f[j] * d : 0.0f;
+            for (int j = 0; j < 16; j += 2) {
+              const float2 h2 = *reinterpret_cast<const float2*>(&sm.ghi[s][c + j]);
+              const float2 l2 = *reinterpret_cast<const float2*>(&sm.glo[s][c + j]);
+              float d0, d1;
+              ptx::unpack2(ptx::add2(ptx::fma2(ptx::pack2(h2.x, h2.y), minus, gh),
+                                     ptx::fma2(ptx::pack2(l2.x, l2.y), minus, gl)),
+                           d0, d1);
+              const ptx::f32x2 y =
+                  ptx::mul2(ptx::pack2(ptx::ex2_approx(d0), ptx::ex2_approx(d1)),
+                            ptx::pack2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])));
+              float y0, y1;
+              ptx::unpack2(y, y0, y1);
+              y0 = c + j <= i ? y0 : 0.0f;
+              y1 = c + j < i ? y1 : 0.0f;
+              split2(ptx::pack2(y0, y1), hi[j >> 1], lo[j >> 1]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) hi[j] = lo[j] = 0u;
           }
-        } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) f[j] = 0.0f;
+          for (int b = 0; b < 2; ++b) {
+            const uint32_t off = base + M::P + i * 128 + ((((c >> 3) + b) ^ (i & 7)) << 4);
+            st_shared(off, make_uint4(hi[4 * b], hi[4 * b + 1], hi[4 * b + 2], hi[4 * b + 3]));
+            st_shared(off + 8192, make_uint4(lo[4 * b], lo[4 * b + 1], lo[4 * b + 2], lo[4 * b + 3]));
+          }
         }
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) split2(f[b * 8 + 2 * e], f[b * 8 + 2 * e + 1], hi[e], lo[e]);
-          const uint32_t off = base + M::P + i * 128 + (((c * 4 + b) ^ (i & 7)) << 4);
-          st_shared(off, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-          st_shared(off + 8192, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-        }
+        ptx::fence_proxy_async_smem();
+        arrive(&sm.p_full);
+        if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
       }
-      ptx::fence_proxy_async_smem();
-      arrive(&sm.p_full);
-      if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
     }
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 1) ptx::tmem_dealloc(tmem, 512);
+  if (warp == 3) ptx::tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------- what a segment adds
@@ -555,27 +735,28 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
 // rows that the outputs' kernel reads first are the ones that this one read last.
 template <int D>
 struct Add {
-  static constexpr int TILE = kC * D * 2, STAGE = 2 * TILE;
+  static constexpr int TILE = kC * D * 2, STAGE = 2 * TILE, STAGES = D == 128 ? 6 : 8;
   static constexpr int V = 0, K = TILE;
-  static constexpr int VP = kStages * STAGE;  // two sets of three parts, then one tile of slack for D = 64
-  static constexpr int SMALL = VP + 6 * TILE + (D == 64 ? TILE : 0);
+  static constexpr int SMALL = STAGES * STAGE;
 };
 struct AddSmall {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[8], empty[8];
   uint64_t v_full[2], v_empty[2], done, drain;
-  float w[kStages][kC];
+  float w[8][kC];
+  float g[kAhead][kC];
   uint32_t tmem;
   int abort;
 };
-constexpr int kAddThreads = 320;  // 2 + 8 warps
-
+constexpr int kAddThreads = 576;  // 16 + 2 warps
 template <int D>
 __global__ void __launch_bounds__(kAddThreads, 1)
 decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg, float* added,
                  float* added_log) {
   using M = Add<D>;
   constexpr int NQ = D / 32;
-  constexpr uint32_t kCols = D;
+  constexpr int kStages = M::STAGES;
+  constexpr int VP = 128;  // TMEM: the sum, then two sets of three parts of V'
+  constexpr uint32_t kCols = 512;
   extern __shared__ __align__(1024) uint8_t smem[];
   AddSmall& sm = *reinterpret_cast<AddSmall*>(smem + M::SMALL);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -589,10 +770,10 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&sm.full[i], 2);
-      ptx::mbar_init(&sm.empty[i], 1 + 8);
+      ptx::mbar_init(&sm.empty[i], 1 + 4 * NQ);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&sm.v_full[i], 8);
+      ptx::mbar_init(&sm.v_full[i], 2 * NQ);
       ptx::mbar_init(&sm.v_empty[i], 1);
     }
     ptx::mbar_init(&sm.done, 1);
@@ -600,7 +781,7 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
     ptx::fence_mbar_init();
     sm.abort = 0;
   }
-  if (warp == 1) {
+  if (warp == 17) {
     ptx::tmem_alloc(&sm.tmem, kCols);
     ptx::tmem_relinquish();
   }
@@ -615,30 +796,29 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
     if (lane == 0) ptx::mbar_arrive(bar);
   };
 
-  if (warp == 0) {
-    float g0 = 0.0f, g1 = 0.0f;
-    auto load_g = [&](int n) {
-      const int t = t_first + (N - 1 - n) * kC + 2 * lane;
-      g0 = __ldg(p.g + t * p.gs + h);
-      g1 = __ldg(p.g + (t + 1) * p.gs + h);
+  if (warp == 16) {
+    const DecayRing ring{sm.g, p.g + h, p.gs, lane};
+    auto first = [&](int n) { return t_first + (N - 1 - n) * kC; };
+    auto load = [&](int n) {
+      if (lane != 0) return;
+      const int s = n % kStages;
+      uint8_t* st = smem + s * M::STAGE;
+      ptx::mbar_arrive_expect_tx(&sm.full[s], M::STAGE);
+      load_tile<D>(st + M::V, &maps.v, &sm.full[s], h, first(n));
+      load_tile<D>(st + M::K, &maps.k, &sm.full[s], hk, first(n));
     };
-    load_g(0);
+    auto ask = [&](int n) { ring.ask(n, n < N ? first(n) : 0, n < N ? first(n) + kC : 0); };
+    for (int i = 0; i < kAhead; ++i) ask(i);
+    for (int i = 0; i < kStages && i < N; ++i) load(i);
     int64_t later = 0;
     int n = 0;
 #pragma unroll 1
     for (; n < N; ++n) {
       const int s = n % kStages;
-      if (n >= kStages && !wait(&sm.empty[s], ((n / kStages) - 1) & 1)) break;
-      if (lane == 0) {
-        uint8_t* st = smem + s * M::STAGE;
-        const int t = t_first + (N - 1 - n) * kC;
-        ptx::mbar_arrive_expect_tx(&sm.full[s], M::STAGE);
-        load_tile<D>(st + M::V, &maps.v, &sm.full[s], h, t);
-        load_tile<D>(st + M::K, &maps.k, &sm.full[s], hk, t);
-      }
-      const bool nan = __any_sync(0xffffffffu, g0 != g0 || g1 != g1);
-      const int64_t u0 = log_units(g0), u1 = log_units(g1);
-      if (n + 1 < N) load_g(n + 1);
+      const float2 g = ring.take(n);
+      const bool nan = __any_sync(0xffffffffu, g.x != g.x || g.y != g.y);
+      const int64_t u0 = log_units(g.x), u1 = log_units(g.y);
+      ask(n + kAhead);
       int64_t sum = u0 + u1;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -649,8 +829,12 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
       const float2 a = log_pair(later + all - (sum - u1)), b = log_pair(later + all - sum);
       float wa = ptx::ex2_approx(a.x + a.y), wb = ptx::ex2_approx(b.x + b.y);
       if (nan) wa = wb = nan_f();
-      *reinterpret_cast<float2*>(&sm.w[s][2 * lane]) = make_float2(wa, wb);
       later += all;
+      if (n >= kStages) {
+        if (!wait(&sm.empty[s], ((n / kStages) - 1) & 1)) break;
+        load(n);
+      }
+      *reinterpret_cast<float2*>(&sm.w[s][2 * lane]) = make_float2(wa, wb);
       arrive(&sm.full[s]);
     }
     if (lane == 0) added_log[x.place * p.H + h] = log_pair(later).x;
@@ -659,7 +843,8 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
         ptx::mbar_wait_tries(&sm.full[i % kStages], (i / kStages) & 1, kTries);
       __syncwarp();
     }
-  } else if (warp == 1) {
+    ptx::cp_async_wait<0>();
+  } else if (warp == 17) {
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; ok && n < N; ++n) {
@@ -668,7 +853,7 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
       if (!ok) break;
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
-        issue_kv<D>(tmem, base + M::VP + b * 3 * M::TILE, base + s * M::STAGE + M::K, n == 0);
+        issue_kv<D>(tmem, tmem + VP + b * 96, base + s * M::STAGE + M::K, n == 0);
         ptx::mma_commit(&sm.v_empty[b]);
         ptx::mma_commit(&sm.empty[s]);
         if (n == N - 1) ptx::mma_commit(&sm.done);
@@ -682,42 +867,59 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
       __syncwarp();
     }
   } else {
-    const int tid = (warp - 2) * 32 + lane;
-    bool ok = true;
+    // two sets of 8 warps take chunks in turn: 32 channels, half of the tokens each
+    const int w = warp & 3, tok = ((warp >> 2) & 1) * 32, b = warp >> 3;
+    bool ok = w < NQ;
+    const uint32_t lanes = (uint32_t)(w * 32) << 16;
 #pragma unroll 1
-    for (int n = 0; n < N; ++n) {
-      const int s = n % kStages, b = n & 1;
-      const uint32_t st = base + s * M::STAGE, vp = base + M::VP + b * 3 * M::TILE;
-      ok = wait(&sm.full[s], (n / kStages) & 1) &&
-           (n < 2 || wait(&sm.v_empty[b], ((n >> 1) - 1) & 1));
-      if (!ok) break;
-#pragma unroll
-      for (int i = 0; i < kC * D / 8 / 256; ++i) {
-        const int at = i * 256 + tid;
-        const uint32_t off = tile_at<D>(at);
-        const float w = sm.w[s][at / (D / 8)];
-        float f[8];
-        Vec16<__nv_bfloat16>::unpack(ld_shared(st + M::V + off), f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] *= w;
-        uint4 part[3];
-        split3(f, part[0], part[1], part[2]);
-#pragma unroll
-        for (int j = 0; j < 3; ++j) st_shared(vp + j * M::TILE + off, part[j]);
+    for (int n = 0; ok && n < N; ++n) {
+      const int s = n % kStages;
+      const uint32_t st = base + s * M::STAGE;
+      if (!(ok = wait(&sm.full[s], (n / kStages) & 1))) break;
+      if ((n & 1) != b) {  // (every warp sees every phase of a stage: parities do not run ahead)
+        arrive(&sm.empty[s]);
+        continue;
       }
-      ptx::fence_proxy_async_smem();
+      uint32_t raw[2][8];
+      load_vt(st + M::V, w * 32, tok, lane, raw[0]);
+      load_vt(st + M::V, w * 32 + 16, tok, lane, raw[1]);
+      ptx::f32x2 weight[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = *reinterpret_cast<const float2*>(&sm.w[s][tok + i * 8 + 2 * (lane & 3)]);
+        weight[i] = ptx::pack2(f.x, f.y);
+      }
+      arrive(&sm.empty[s]);
+      if (n >= 2 && !(ok = wait(&sm.v_empty[b], ((n >> 1) - 1) & 1))) break;
+      ptx::tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        uint32_t part[3][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint32_t x[3];
+          weigh3(c ? raw[1][i] : raw[0][i], weight[i >> 1], x);
+          part[0][i] = x[0];
+          part[1][i] = x[1];
+          part[2][i] = x[2];
+        }
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          ptx::tmem_st_rows16_nowait(
+              tmem + lanes + ((uint32_t)(c * 16) << 16) + VP + b * 96 + j * 32 + tok / 2, part[j]);
+      }
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before();
       arrive(&sm.v_full[b]);
-      if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
     }
-    // warps 4 .. 7 hold the accumulator's rows
-    const int w = warp & 3;
-    if (ok && warp >= 4 && warp < 8 && w < NQ && wait(&sm.done, 0)) {
+    // the first four warps hold the accumulator's rows
+    if (ok && warp < 4 && wait(&sm.done, 0)) {
       ptx::tc_fence_after();
       float* out = added + (x.place * p.H + h) * (int64_t)(D * D) + w * 32 + lane;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float f[32];
-        ptx::tmem_ld32(tmem + ((uint32_t)(w * 32) << 16) + c * 32, f);
+        ptx::tmem_ld32(tmem + lanes + c * 32, f);
 #pragma unroll
         for (int i = 0; i < 32; ++i) out[(c * 32 + i) * D] = f[i];
       }
@@ -725,7 +927,7 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 1) ptx::tmem_dealloc(tmem, kCols);
+  if (warp == 17) ptx::tmem_dealloc(tmem, kCols);
 }
 
 template <int D>
@@ -737,7 +939,7 @@ kda_status launch_d(const DecayParams& p, int seg, float* added, float* added_lo
       !(make_map_tokens(&m.q, p.q, (uint64_t)p.Hk * D, rows, (uint64_t)p.qs * 2, 64, kC, true) &&
         make_map_tokens(&m.k, p.k, (uint64_t)p.Hk * D, rows, (uint64_t)p.ks * 2, 64, kC, true) &&
         make_map_tokens(&m.v, p.v, (uint64_t)p.H * D, rows, (uint64_t)p.vs * 2, 64, kC, true) &&
-        make_map_tokens(&m.o, p.o, (uint64_t)p.H * D, rows, (uint64_t)p.H * D * 2, D, kC, false)))
+        make_map_tokens(&m.o, p.o, (uint64_t)p.H * D, rows, (uint64_t)p.H * D * 2, 64, kC, true)))
     return set_error(KDA_ERR_CUDA, "kda_decay_prefill: cuTensorMapEncodeTiled failed");
   constexpr int out_bytes = Out<D>::SMALL + (int)sizeof(OutSmall);
   constexpr int add_bytes = Add<D>::SMALL + (int)sizeof(AddSmall);
