@@ -27,12 +27,21 @@ using namespace decay;
 constexpr int kC = 64;
 constexpr int kStages = 4;
 constexpr int kThreads = 768;
-constexpr int kAhead = 3;
+constexpr int kAhead = 2;
 constexpr uint32_t kTries = 1u << 19;  // of a wait inside a CTA: 2 s
 
 struct Maps {
   CUtensorMap q, k, v, o;
 };
+
+// What the roles know of a stage's chunk.
+struct Chunk {
+  const float* entry;  // of the unit's first chunk: the state before it, or nullptr (zeros)
+  float* exit;         // of a unit's last chunk: where the state after it goes, or nullptr
+  int t0, tokens;      // first token, and how many of the 64 belong to the segment
+  int head, kind;
+};
+constexpr int kFirst = 1, kStop = 2;  // kinds: begins a unit; no chunk, the roles leave
 
 // Offsets in shared memory. Operand tiles are [64 tokens][64 channels] blocks of 8 KB (128-byte
 // swizzle), D / 64 of them side by side. q.k is a product with M = 128 on 64 rows: it reads the 64
@@ -48,11 +57,12 @@ struct Out {
 };
 struct OutSmall {
   uint64_t full[kStages], empty[kStages];
-  uint64_t sc_full, sc_empty, p_full, v_full, vt_full, s_full, part_full;
+  uint64_t sc_full, sc_empty, p_full, v_full, vt_full, s_full;
   uint64_t kv_done, sq_done, x_full, o_full, o_empty, drain;
-  float g[kAhead][kC];                       // log-decays of the next chunks
   float ghi[kStages][kC], glo[kStages][kC];  // running sums of log2 decays, high and low parts
+  float g[kAhead][kC];                       // log-decays of the next chunks
   float2 total[kStages];
+  Chunk chunk[kStages];
   uint32_t tmem;
   int abort;
 };
@@ -130,12 +140,12 @@ template <int D>
 __device__ __forceinline__ void issue_kv(uint32_t tmem_s, uint32_t vp, uint32_t k, bool fresh) {
   const uint32_t id = ptx::idesc_make(ptx::kFmtBF16, 128, D, false, true);
   const uint64_t b = ptx::sdesc_sw128(k, 8192, 1024);
+#pragma unroll 1
+  for (uint32_t part = 0; part < 3; ++part)
 #pragma unroll
-  for (int part = 0; part < 3; ++part)
-#pragma unroll
-    for (int i = 0; i < kC / 16; ++i)
+    for (uint32_t i = 0; i < kC / 16; ++i)
       ptx::mma_f16_ts(tmem_s, vp + part * 32 + i * 8, ptx::desc_add(b, i * 2048), id,
-                      !fresh || part > 0 || i > 0);
+                      !fresh || part + i > 0);
 }
 
 // 16 bytes (8 channels) number i of a tile: row i / (D / 8), swizzled place.
@@ -223,19 +233,14 @@ __device__ __forceinline__ bool group_and(int id, int threads, bool ok) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg, const float* added) {
+decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg, int slots,
+                const float* added) {
   using M = Out<D>;
   using T = Tm<D>;
   constexpr int NQ = D / 32;  // warps that hold the accumulators' rows
   extern __shared__ __align__(1024) uint8_t smem[];
   OutSmall& sm = *reinterpret_cast<OutSmall*>(smem + M::SMALL);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.x % p.H;
-  Segment x;
-  if (!find_segment(p, seg, blockIdx.x / p.H, threadIdx.x == 0 && h == 0, x)) return;
-  const int hk = h / (p.H / p.Hk);
-  const int N = (int)((x.hi - x.lo + kC - 1) / kC);
-  const int t_first = (int)x.lo, t_end = (int)x.hi;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -248,7 +253,6 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
     ptx::mbar_init(&sm.v_full, 2 * NQ);
     ptx::mbar_init(&sm.vt_full, 2 * NQ);
     ptx::mbar_init(&sm.s_full, 2 * NQ);
-    ptx::mbar_init(&sm.part_full, 2 * NQ);
     ptx::mbar_init(&sm.kv_done, 1);
     ptx::mbar_init(&sm.sq_done, 1);
     ptx::mbar_init(&sm.x_full, NQ);
@@ -272,6 +276,12 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(bar);
   };
+  // The next chunk n, for every role but the one that loads it; false: none, or a wait gave up.
+  auto take = [&](int n, Chunk& c) {
+    if (!wait(&sm.full[n % kStages], (n / kStages) & 1)) return false;
+    c = sm.chunk[n % kStages];
+    return __shfl_sync(0xffffffffu, c.kind, 0) != kStop;
+  };
 
   // registers of the six warpgroups: 64 + 112 + 112 + 64 + 64 + 64 = 6 x 80
   if (warp >= 4 && warp < 12) {
@@ -279,121 +289,131 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
     // ------------------------------------------------------------------ the state
     const int w = warp & 3, half = (warp - 4) >> 2;  // 32 value channels, half of the key channels
     if (w < NQ) {
-      constexpr int CB = D / 64;  // blocks of 32 key channels
       const uint32_t lanes = (uint32_t)(w * 32) << 16;
       const uint32_t t_s = tmem + lanes + T::S + half * (D / 2);
       const uint32_t t_part = tmem + lanes + half * (D / 4);
-      const int64_t at = (int64_t)half * (D / 2) * D + w * 32 + lane;  // of the state's matrix
-      const float* entry = !x.first ? added + ((x.place - 1) * p.H + h) * (int64_t)(D * D)
-                           : p.init ? p.init + ((int64_t)x.seq * p.H + h) * (D * D) : nullptr;
-      float* exit_state =
-          x.last && p.final_state ? p.final_state + ((int64_t)x.seq * p.H + h) * (D * D) : nullptr;
-      bool ok = true;
+      const int at = half * (D / 2) * D + w * 32 + lane;  // of the state's matrix
+      float* exit_state = nullptr;
+      Chunk c;
 #pragma unroll 1
-      for (int n = 0; n < N; ++n) {
+      for (int n = 0;; ++n) {
         const int s = n % kStages;
-        ok = wait(&sm.full[s], (n / kStages) & 1) && (n == 0 || wait(&sm.kv_done, (n - 1) & 1));
+        bool ok = wait(&sm.full[s], (n / kStages) & 1) &&
+                  (n == 0 || wait.all({&sm.kv_done, &sm.sq_done},
+                                      {(uint32_t)(n - 1) & 1, (uint32_t)(n - 1) & 1}));
         if (!ok) break;
         ptx::tc_fence_after();
+        c = sm.chunk[s];
+        const int kind = __shfl_sync(0xffffffffu, c.kind, 0);
+        if (kind != 0 && exit_state) {  // the unit before ends
+#pragma unroll 1
+          for (int b = 0; b < D / 2; b += 32) {
+            float f[32];
+            ptx::tmem_ld32(t_s + b, f);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) exit_state[at + (b + i) * D] = f[i];
+          }
+        }
+        if (kind == kStop) break;
+        exit_state = c.exit;
         const float a = ptx::ex2_approx(sm.total[s].x + sm.total[s].y);
         const ptx::f32x2 aa = ptx::pack2(a, a);
-        // decayed for the next sum first, which is what the products wait for
-        float hi[CB][16], lo[CB][16];
-#pragma unroll
-        for (int c = 0; c < CB; ++c) {
+#pragma unroll 1
+        for (int b = 0; b < D / 2; b += 32) {
           float f[32];
-          if (n > 0) {
-            ptx::tmem_ld32(t_s + c * 32, f);
-          } else {
+          if (kind == kFirst) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = entry ? entry[at + (c * 32 + i) * D] : 0.0f;
+            for (int i = 0; i < 32; ++i) f[i] = c.entry ? __ldg(c.entry + at + (b + i) * D) : 0.0f;
+          } else {
+            ptx::tmem_ld32(t_s + b, f);
           }
+          float hi[16], lo[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const ptx::f32x2 y = ptx::pack2(f[2 * i], f[2 * i + 1]);
             uint32_t u, v;
             split2(y, u, v);
-            hi[c][i] = __uint_as_float(u);
-            lo[c][i] = __uint_as_float(v);
+            hi[i] = __uint_as_float(u);
+            lo[i] = __uint_as_float(v);
             ptx::unpack2(ptx::mul2(y, aa), f[2 * i], f[2 * i + 1]);
           }
-          ptx::tmem_st32_nowait(t_s + c * 32, f);
+          ptx::tmem_st32_nowait(t_s + b, f);
+          ptx::tmem_st16(t_part + T::HI + b / 2, hi);
+          ptx::tmem_st16(t_part + T::LO + b / 2, lo);
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         arrive(&sm.s_full);
         if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
-        if (n > 0 && !(ok = wait(&sm.sq_done, (n - 1) & 1))) break;
-        ptx::tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < CB; ++c) {
-          ptx::tmem_st16(t_part + T::HI + c * 16, hi[c]);
-          ptx::tmem_st16(t_part + T::LO + c * 16, lo[c]);
-        }
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        arrive(&sm.part_full);
-      }
-      if (ok && exit_state) {
-        if (N > 0) ok = wait(&sm.kv_done, (N - 1) & 1);
-        ptx::tc_fence_after();
-        if (ok) {
-#pragma unroll 1
-          for (int c = 0; c < CB; ++c) {
-            float f[32];
-            if (N > 0) {
-              ptx::tmem_ld32(t_s + c * 32, f);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) f[i] = entry ? entry[at + (c * 32 + i) * D] : 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) exit_state[at + (c * 32 + i) * D] = f[i];
-          }
-        }
       }
     }
   } else {
     ptx::regs_give<64>();
     if (warp == 2) {
       // ------------------------------------------------------------------ loads and decays
-      const DecayRing ring{sm.g, p.g + h, p.gs, lane};
-      auto load = [&](int n) {
-        if (lane != 0) return;
-        const int s = n % kStages, t = t_first + n * kC;
-        uint8_t* st = smem + s * M::STAGE;
-        ptx::mbar_arrive_expect_tx(&sm.full[s], M::STAGE);
-        load_tile<D>(st + M::K, &maps.k, &sm.full[s], hk, t);
-        load_tile<D>(st + M::Q, &maps.q, &sm.full[s], hk, t);
-        load_tile<D>(st + M::V, &maps.v, &sm.full[s], h, t);
-      };
-      for (int i = 0; i < kAhead; ++i) ring.ask(i, t_first + (int64_t)i * kC, t_end);
-      for (int i = 0; i < kStages && i < N; ++i) load(i);
       int n = 0;
+      bool ok = true;
 #pragma unroll 1
-      for (; n < N; ++n) {
-        const int s = n % kStages;
-        // the decays, while the stage is still in use
-        const float2 g = ring.take(n);
-        const bool nan = __any_sync(0xffffffffu, g.x != g.x || g.y != g.y);
-        const int64_t u0 = log_units(g.x), u1 = log_units(g.y);
-        ring.ask(n + kAhead, t_first + (int64_t)(n + kAhead) * kC, t_end);
-        int64_t sum = u0 + u1;
+      for (int unit = blockIdx.x; ok && unit < slots * p.H; unit += gridDim.x) {
+        const int h = unit % p.H;
+        Segment x;
+        if (!find_segment(p, seg, unit / p.H, lane == 0 && h == 0, x)) continue;
+        if (x.hi == x.lo && !p.final_state) continue;
+        const int hk = h / (p.H / p.Hk);
+        const int t_end = (int)x.hi;
+        const int N = x.hi > x.lo ? (int)((x.hi - x.lo + kC - 1) / kC) : 1;
+        Chunk c;
+        c.entry = !x.first ? added + ((x.place - 1) * p.H + h) * (int64_t)(D * D)
+                  : p.init ? p.init + ((int64_t)x.seq * p.H + h) * (D * D) : nullptr;
+        c.exit = nullptr;
+        c.head = h;
+        if (lane == 0 && c.entry) ptx::bulk_prefetch_l2(c.entry, D * D * 4);
+        const DecayRing ring{sm.g, p.g + h, p.gs, lane};
+        for (int i = 0; i < kAhead; ++i) ring.ask(i, x.lo + (int64_t)i * kC, t_end);
+#pragma unroll 1
+        for (int i = 0; i < N; ++i, ++n) {
+          const int s = n % kStages;
+          c.t0 = (int)x.lo + i * kC;
+          c.tokens = t_end - c.t0 < kC ? t_end - c.t0 : kC;
+          c.kind = i == 0 ? kFirst : 0;
+          if (i == N - 1 && x.last && p.final_state)
+            c.exit = p.final_state + ((int64_t)x.seq * p.H + h) * (D * D);
+          if (n >= kStages && !(ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1))) break;
+          if (lane == 0) {
+            uint8_t* st = smem + s * M::STAGE;
+            if (c.tokens > 0) {
+              ptx::mbar_arrive_expect_tx(&sm.full[s], M::STAGE);
+              load_tile<D>(st + M::K, &maps.k, &sm.full[s], hk, c.t0);
+              load_tile<D>(st + M::Q, &maps.q, &sm.full[s], hk, c.t0);
+              load_tile<D>(st + M::V, &maps.v, &sm.full[s], h, c.t0);
+            } else {  // an empty sequence: all rows are cleared, the state passes through
+              ptx::mbar_arrive(&sm.full[s]);
+            }
+            sm.chunk[s] = c;
+          }
+          const float2 g = ring.take(i);
+          const bool nan = __any_sync(0xffffffffu, g.x != g.x || g.y != g.y);
+          const int64_t u0 = log_units(g.x), u1 = log_units(g.y);
+          ring.ask(i + kAhead, x.lo + (int64_t)(i + kAhead) * kC, t_end);
+          int64_t sum = u0 + u1;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t w = __shfl_up_sync(0xffffffffu, sum, o);
-          if (lane >= o) sum += w;
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t w = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += w;
+          }
+          float2 a = log_pair(sum - u1), b = log_pair(sum);
+          if (nan) a.x = b.x = nan_f();  // a NaN decay spoils its chunk
+          *reinterpret_cast<float2*>(&sm.ghi[s][2 * lane]) = make_float2(a.x, b.x);
+          *reinterpret_cast<float2*>(&sm.glo[s][2 * lane]) = make_float2(a.y, b.y);
+          if (lane == 31) sm.total[s] = b;
+          arrive(&sm.full[s]);
         }
-        float2 a = log_pair(sum - u1), b = log_pair(sum);
-        if (nan) a.x = b.x = nan_f();  // a NaN decay spoils its chunk
-        if (n >= kStages) {
-          if (!wait(&sm.empty[s], ((n / kStages) - 1) & 1)) break;
-          load(n);
-        }
-        *reinterpret_cast<float2*>(&sm.ghi[s][2 * lane]) = make_float2(a.x, b.x);
-        *reinterpret_cast<float2*>(&sm.glo[s][2 * lane]) = make_float2(a.y, b.y);
-        if (lane == 31) sm.total[s] = b;
-        arrive(&sm.full[s]);
+      }
+      if (ok && n >= kStages) ok = wait(&sm.empty[n % kStages], ((n / kStages) - 1) & 1);
+      if (ok && lane == 0) {
+        sm.chunk[n % kStages].kind = kStop;
+        ptx::mbar_arrive(&sm.full[n % kStages]);
+        ptx::mbar_arrive(&sm.full[n % kStages]);
       }
       if (*(volatile int*)&sm.abort) {  // the loads in flight land before the CTA leaves
         for (int i = n > kStages ? n - kStages : 0; i < n; ++i)
@@ -403,74 +423,73 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
       ptx::cp_async_wait<0>();
     } else if (warp == 3) {
       // ------------------------------------------------------------------ products
+      // (loops rolled: unrolled, this role's code alone did not fit the instruction cache)
       const uint32_t id64 = ptx::idesc_make(ptx::kFmtBF16, 128, kC, false, false);
       auto issue_qk = [&](int n) {
         const uint32_t st = base + (n % kStages) * M::STAGE;
         if (ptx::elect_one()) {
           const uint64_t a = ptx::sdesc_sw128(st + M::Q, 16, 1024);
           const uint64_t b = ptx::sdesc_sw128(st + M::K, 16, 1024);
+#pragma unroll 1
+          for (uint32_t i = 0; i < D / 64; ++i)
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint32_t off = (i >> 2) * 8192 + (i & 3) * 32;
-            ptx::mma_f16(tmem + T::SC, ptx::desc_add(a, off), ptx::desc_add(b, off), id64, i > 0);
-          }
+            for (uint32_t j = 0; j < 4; ++j)
+              ptx::mma_f16(tmem + T::SC, ptx::desc_add(a, i * 8192 + j * 32),
+                           ptx::desc_add(b, i * 8192 + j * 32), id64, i + j > 0);
           ptx::mma_commit(&sm.sc_full);
         }
         __syncwarp();
       };
-      bool ok = N == 0 || wait(&sm.full[0], 0);
-      if (ok && N > 0) issue_qk(0);
+      Chunk c;
+      bool ok = take(0, c);
+      if (ok) issue_qk(0);
 #pragma unroll 1
-      for (int n = 0; ok && n < N; ++n) {
+      for (int n = 0; ok; ++n) {
         const int s = n % kStages;
-        const uint32_t st = base + s * M::STAGE;
-        const uint32_t ph = n & 1;
-        ok = wait.all({&sm.s_full, &sm.v_full}, {ph, ph});
-        if (!ok) break;
+        const uint32_t st = base + s * M::STAGE, ph = n & 1;
+        if (!wait.all({&sm.s_full, &sm.v_full}, {ph, ph})) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           issue_kv<D>(tmem + T::S, tmem + T::VP, st + M::K, false);
           ptx::mma_commit(&sm.kv_done);
         }
         __syncwarp();
-        ok = n == 0 ? wait(&sm.part_full, 0)
-                    : wait.all({&sm.part_full, &sm.o_empty}, {ph, ph ^ 1});
-        if (!ok) break;
+        if (n > 0 && !wait(&sm.o_empty, ph ^ 1)) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           const uint64_t b = ptx::sdesc_sw128(st + M::Q, 16, 1024);
+#pragma unroll 1
+          for (uint32_t i = 0; i < 2 * (D / 64); ++i) {  // both parts: they are side by side
+            const uint32_t g = i % (D / 64);
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-              ptx::mma_f16_ts(tmem + T::O, tmem + (part ? T::LO : T::HI) + i * 8,
-                              ptx::desc_add(b, (i >> 2) * 8192 + (i & 3) * 32), id64,
-                              part > 0 || i > 0);
+            for (uint32_t j = 0; j < 4; ++j)
+              ptx::mma_f16_ts(tmem + T::O, tmem + T::HI + i * 32 + j * 8,
+                              ptx::desc_add(b, g * 8192 + j * 32), id64, i + j > 0);
+          }
           ptx::mma_commit(&sm.sq_done);
           ptx::mma_commit(&sm.empty[s]);
         }
         __syncwarp();
-        if (n + 1 < N) {
-          ok = wait.all({&sm.full[(n + 1) % kStages], &sm.sc_empty},
-                        {(uint32_t)((n + 1) / kStages) & 1, ph});
-          if (!ok) break;
+        const bool more = take(n + 1, c);
+        if (more) {
+          if (!wait(&sm.sc_empty, ph)) break;
           ptx::tc_fence_after();
           issue_qk(n + 1);
         }
-        ok = wait.all({&sm.p_full, &sm.vt_full, &sm.x_full}, {ph, ph, ph});
-        if (!ok) break;
+        if (!wait.all({&sm.p_full, &sm.vt_full, &sm.x_full}, {ph, ph, ph})) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
+          const uint64_t b = ptx::sdesc_sw128(base + M::P, 16, 1024);
+#pragma unroll 1
+          for (uint32_t part = 0; part < 2; ++part)
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            const uint64_t b = ptx::sdesc_sw128(base + M::P + part * 8192, 16, 1024);
-#pragma unroll
-            for (int i = 0; i < kC / 16; ++i)
-              ptx::mma_f16_ts(tmem + T::O, tmem + T::VT + i * 8, ptx::desc_add(b, i * 32), id64, 1);
-          }
+            for (uint32_t i = 0; i < kC / 16; ++i)
+              ptx::mma_f16_ts(tmem + T::O, tmem + T::VT + i * 8,
+                              ptx::desc_add(b, part * 8192 + i * 32), id64, 1);
           ptx::mma_commit(&sm.o_full);
         }
         __syncwarp();
+        ok = more;
       }
       if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort)) {  // the products in flight end first
         if (ptx::elect_one()) ptx::mma_commit(&sm.drain);
@@ -483,12 +502,11 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
       const int w = warp & 3, tok = ((warp - 16) >> 2) * 32;  // 32 channels, half of the tokens
       if (w < NQ) {
         const uint32_t lanes = (uint32_t)(w * 32) << 16;
+        Chunk c;
 #pragma unroll 1
-        for (int n = 0; n < N; ++n) {
-          const int s = n % kStages;
+        for (int n = 0; take(n, c); ++n) {
+          const int s = n % kStages, m = c.tokens;
           const uint32_t st = base + s * M::STAGE;
-          const int m = t_end - (t_first + n * kC);  // tokens left
-          if (!wait(&sm.full[s], (n / kStages) & 1)) break;
           const float2 total = sm.total[s];
           ptx::f32x2 weight[4];
           uint32_t raw[2][8];
@@ -552,18 +570,20 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
       // ------------------------------------------------------------------ outputs
       const int w = warp - 12;
       if (w < NQ) {
-        const uint32_t lanes = (uint32_t)(w * 32) << 16;
         const int tid = w * 32 + lane;
         const uint32_t stage = base + M::O + (w >> 1) * 8192;  // its block of 64 channels
-        const uint32_t t_o = tmem + lanes + T::O;
+        const uint32_t t_o = tmem + ((uint32_t)(w * 32) << 16) + T::O;
         const ptx::f32x2 scale = ptx::pack2(p.scale, p.scale);
-        bool ok = true;
+        Chunk c;
 #pragma unroll 1
-        for (int n = 0; n < N; ++n) {
+        for (int n = 0;; ++n) {
           const int s = n % kStages;
-          const int t0 = t_first + n * kC;
           // S^T Q^T gets the decays from the chunk's start in place, and V^T P^T is added to it
-          ok = wait(&sm.full[s], (n / kStages) & 1) && wait(&sm.sq_done, n & 1);
+          bool ok = wait(&sm.full[s], (n / kStages) & 1);
+          if (ok) {
+            c = sm.chunk[s];
+            ok = __shfl_sync(0xffffffffu, c.kind, 0) != kStop && wait(&sm.sq_done, n & 1);
+          }
           if (ok) {
             ptx::tc_fence_after();
 #pragma unroll 1
@@ -576,27 +596,23 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
                 const float2 l2 = *reinterpret_cast<const float2*>(&sm.glo[s][t]);
                 ee[i] = ptx::pack2(ptx::ex2_approx(h2.x + l2.x), ptx::ex2_approx(h2.y + l2.y));
               }
-              uint32_t x[2][16];  // 16 channels x 32 tokens each
+#pragma unroll 1
+              for (uint32_t ch = 0; ch < 32; ch += 16) {  // 16 channels x 32 tokens
+                uint32_t x[16];
+                ptx::tmem_ld_frag32_nowait(t_o + (ch << 16) + tok, x);
+                ptx::tmem_ld_wait();
 #pragma unroll
-              for (int c = 0; c < 2; ++c)
-                ptx::tmem_ld_frag32_nowait(t_o + ((uint32_t)(16 * c) << 16) + tok, x[c]);
-              ptx::tmem_ld_wait();
-#pragma unroll
-              for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[c][i]));
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
+                for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[i]));
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {
                   float y0, y1;
-                  ptx::unpack2(ptx::mul2(ee[j >> 2], ptx::pack2(__uint_as_float(x[c][j]),
-                                                                __uint_as_float(x[c][j + 1]))),
+                  ptx::unpack2(ptx::mul2(ee[j >> 2], ptx::pack2(__uint_as_float(x[j]),
+                                                                __uint_as_float(x[j + 1]))),
                                y0, y1);
-                  x[c][j] = __float_as_uint(y0);
-                  x[c][j + 1] = __float_as_uint(y1);
+                  x[j] = __float_as_uint(y0);
+                  x[j + 1] = __float_as_uint(y1);
                 }
-                ptx::tmem_st_frag32_nowait(t_o + ((uint32_t)(16 * c) << 16) + tok, x[c]);
+                ptx::tmem_st_frag32_nowait(t_o + (ch << 16) + tok, x);
               }
             }
             ptx::tmem_st_wait();
@@ -610,54 +626,47 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
           if (!ok) break;
           ptx::tc_fence_after();
 #pragma unroll 1
-          for (int tok = 0; tok < kC; tok += 32) {
-            uint32_t x[2][16];
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              ptx::tmem_ld_frag32_nowait(t_o + ((uint32_t)(16 * c) << 16) + tok, x[c]);
+          for (int b = 0; b < 4; ++b) {
+            const int ch0 = (b & 1) * 16, tok = (b >> 1) * 32;
+            uint32_t x[16];
+            ptx::tmem_ld_frag32_nowait(t_o + ((uint32_t)ch0 << 16) + tok, x);
             ptx::tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[i]));
+            uint32_t o[8];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[c][i]));
+            for (int j = 0; j < 16; j += 2) {
+              float y0, y1;
+              ptx::unpack2(
+                  ptx::mul2(scale, ptx::pack2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]))), y0,
+                  y1);
+              o[j >> 1] = pack_bf16(y0, y1);
+            }
+            // matrices (channels 0-7, 8-15) x (two groups of 8 tokens): row = token
+            const int ch = ((w & 1) * 32 + ch0) / 8 + ((lane >> 3) & 1);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t o[8];
-#pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                float y0, y1;
-                ptx::unpack2(ptx::mul2(scale, ptx::pack2(__uint_as_float(x[c][j]),
-                                                         __uint_as_float(x[c][j + 1]))),
-                             y0, y1);
-                o[j >> 1] = pack_bf16(y0, y1);
-              }
-              // matrices (channels 0-7, 8-15) x (two groups of 8 tokens): row = token
-              const int ch = ((w & 1) * 32 + c * 16) / 8 + ((lane >> 3) & 1);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int t = tok + i * 16 + (lane >> 4) * 8 + (lane & 7);
-                ptx::st_matrix4_trans(stage + t * 128 + ((ch ^ (t & 7)) << 4), o[4 * i],
-                                      o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-              }
+            for (int i = 0; i < 2; ++i) {
+              const int t = tok + i * 16 + (lane >> 4) * 8 + (lane & 7);
+              ptx::st_matrix4_trans(stage + t * 128 + ((ch ^ (t & 7)) << 4), o[4 * i], o[4 * i + 1],
+                                    o[4 * i + 2], o[4 * i + 3]);
             }
           }
           ptx::tc_fence_before();
           arrive(&sm.o_empty);
           ptx::fence_proxy_async_smem();
-          ok = group_and(1, NQ * 32, true);
-          const int m = t_end - t0;
-          if (m >= kC) {
+          group_and(1, NQ * 32, true);
+          if (c.tokens >= kC) {
             if (tid == 0) {
 #pragma unroll
               for (int i = 0; i < D / 64; ++i)
-                ptx::tma_store_2d(&maps.o, smem + M::O + i * 8192, h * D + i * 64, t0);
+                ptx::tma_store_2d(&maps.o, smem + M::O + i * 8192, c.head * D + i * 64, c.t0);
               ptx::bulk_commit();
             }
           } else {  // the rows after the segment belong to another one
-            for (int i = tid; i < m * (D / 8); i += NQ * 32) {
-              const int t = i / (D / 8), c = i % (D / 8);
-              *reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + ((int64_t)(t0 + t) * p.H + h) * D + c * 8) =
-                  ld_shared(base + M::O + tile_at<D>(i));
+            for (int i = tid; i < c.tokens * (D / 8); i += NQ * 32) {
+              const int t = c.t0 + i / (D / 8);
+              *reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + ((int64_t)t * p.H + c.head) * D +
+                                        i % (D / 8) * 8) = ld_shared(base + M::O + tile_at<D>(i));
             }
           }
         }
@@ -667,32 +676,31 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
       // ------------------------------------------------------------------ P (warps 0, 1)
       const int w = warp, i = w * 32 + lane;  // the row
       const uint32_t lanes = (uint32_t)(w * 32) << 16;
+      Chunk c;
 #pragma unroll 1
-      for (int n = 0; n < N; ++n) {
+      for (int n = 0; take(n, c); ++n) {
         const int s = n % kStages;
-        if (!(wait(&sm.full[s], (n / kStages) & 1) && wait(&sm.sc_full, n & 1) &&
-              (n == 0 || wait(&sm.o_full, (n - 1) & 1))))
-          break;
+        if (!wait(&sm.sc_full, n & 1) || (n > 0 && !wait(&sm.o_full, (n - 1) & 1))) break;
         ptx::tc_fence_after();
         const ptx::f32x2 gh = ptx::pack2(sm.ghi[s][i], sm.ghi[s][i]),
                          gl = ptx::pack2(sm.glo[s][i], sm.glo[s][i]), minus = ptx::pack2(-1.0f, -1.0f);
 #pragma unroll 1
-        for (int c = 0; c < kC; c += 16) {
+        for (int c0 = 0; c0 < kC; c0 += 16) {
           uint32_t hi[8], lo[8];
-          if (c < 32 * w + 32) {
+          if (c0 < 32 * w + 32) {
             uint32_t r[16];
-            ptx::tmem_ld16_nowait(tmem + lanes + T::SC + c, r);
+            ptx::tmem_ld16_nowait(tmem + lanes + T::SC + c0, r);
             ptx::tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(r[j]));
-            if (c == 32 * w + 16) {  // all of them read
+            if (c0 == 32 * w + 16) {  // all of them read
               ptx::tc_fence_before();
               arrive(&sm.sc_empty);
             }
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
-              const float2 h2 = *reinterpret_cast<const float2*>(&sm.ghi[s][c + j]);
-              const float2 l2 = *reinterpret_cast<const float2*>(&sm.glo[s][c + j]);
+              const float2 h2 = *reinterpret_cast<const float2*>(&sm.ghi[s][c0 + j]);
+              const float2 l2 = *reinterpret_cast<const float2*>(&sm.glo[s][c0 + j]);
               float d0, d1;
               ptx::unpack2(ptx::add2(ptx::fma2(ptx::pack2(h2.x, h2.y), minus, gh),
                                      ptx::fma2(ptx::pack2(l2.x, l2.y), minus, gl)),
@@ -702,8 +710,8 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
                             ptx::pack2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])));
               float y0, y1;
               ptx::unpack2(y, y0, y1);
-              y0 = c + j <= i ? y0 : 0.0f;
-              y1 = c + j < i ? y1 : 0.0f;
+              y0 = c0 + j <= i ? y0 : 0.0f;
+              y1 = c0 + j < i ? y1 : 0.0f;
               split2(ptx::pack2(y0, y1), hi[j >> 1], lo[j >> 1]);
             }
           } else {
@@ -712,7 +720,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
           }
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            const uint32_t off = base + M::P + i * 128 + ((((c >> 3) + b) ^ (i & 7)) << 4);
+            const uint32_t off = base + M::P + i * 128 + ((((c0 >> 3) + b) ^ (i & 7)) << 4);
             st_shared(off, make_uint4(hi[4 * b], hi[4 * b + 1], hi[4 * b + 2], hi[4 * b + 3]));
             st_shared(off + 8192, make_uint4(lo[4 * b], lo[4 * b + 1], lo[4 * b + 2], lo[4 * b + 3]));
           }
@@ -741,48 +749,46 @@ struct Add {
 };
 struct AddSmall {
   uint64_t full[8], empty[8];
-  uint64_t v_full[2], v_empty[2], done, drain;
+  uint64_t v_full[2], v_empty[2], acc_full[2], acc_empty[2], drain;
   float w[8][kC];
   float g[kAhead][kC];
+  float* out[8];  // of a chunk's unit
+  int kind[8];
   uint32_t tmem;
   int abort;
 };
-constexpr int kAddThreads = 576;  // 16 + 2 warps
+constexpr int kLast = 4;           // a kind: ends a unit
+constexpr int kAddThreads = 704;  // 16 + 2 + 4 warps
+
 template <int D>
 __global__ void __launch_bounds__(kAddThreads, 1)
-decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg, float* added,
-                 float* added_log) {
+decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg, int slots,
+                 float* added, float* added_log) {
   using M = Add<D>;
-  constexpr int NQ = D / 32;
-  constexpr int kStages = M::STAGES;
-  constexpr int VP = 128;  // TMEM: the sum, then two sets of three parts of V'
-  constexpr uint32_t kCols = 512;
+  constexpr int NQ = D / 32, kStages = M::STAGES;
+  constexpr int VP = 256;  // TMEM: two sums in turn, then two sets of three parts of V'
   extern __shared__ __align__(1024) uint8_t smem[];
   AddSmall& sm = *reinterpret_cast<AddSmall*>(smem + M::SMALL);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.x % p.H;
-  Segment x;
-  if (!find_segment(p, seg, blockIdx.x / p.H, false, x) || x.last) return;
-  const int hk = h / (p.H / p.Hk);
   const int N = seg / kC;  // segments that are not their sequence's last are whole
-  const int t_first = (int)x.lo;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&sm.full[i], 2);
-      ptx::mbar_init(&sm.empty[i], 1 + 4 * NQ);
+      ptx::mbar_init(&sm.empty[i], 1 + 4 * NQ + NQ);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sm.v_full[i], 2 * NQ);
       ptx::mbar_init(&sm.v_empty[i], 1);
+      ptx::mbar_init(&sm.acc_full[i], 1);
+      ptx::mbar_init(&sm.acc_empty[i], NQ);
     }
-    ptx::mbar_init(&sm.done, 1);
     ptx::mbar_init(&sm.drain, 1);
     ptx::fence_mbar_init();
     sm.abort = 0;
   }
   if (warp == 17) {
-    ptx::tmem_alloc(&sm.tmem, kCols);
+    ptx::tmem_alloc(&sm.tmem, 512);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
@@ -795,49 +801,65 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(bar);
   };
+  auto take = [&](int n, int& kind) {
+    if (!wait(&sm.full[n % kStages], (n / kStages) & 1)) return false;
+    kind = __shfl_sync(0xffffffffu, sm.kind[n % kStages], 0);
+    return kind != kStop;
+  };
 
   if (warp == 16) {
-    const DecayRing ring{sm.g, p.g + h, p.gs, lane};
-    auto first = [&](int n) { return t_first + (N - 1 - n) * kC; };
-    auto load = [&](int n) {
-      if (lane != 0) return;
-      const int s = n % kStages;
-      uint8_t* st = smem + s * M::STAGE;
-      ptx::mbar_arrive_expect_tx(&sm.full[s], M::STAGE);
-      load_tile<D>(st + M::V, &maps.v, &sm.full[s], h, first(n));
-      load_tile<D>(st + M::K, &maps.k, &sm.full[s], hk, first(n));
-    };
-    auto ask = [&](int n) { ring.ask(n, n < N ? first(n) : 0, n < N ? first(n) + kC : 0); };
-    for (int i = 0; i < kAhead; ++i) ask(i);
-    for (int i = 0; i < kStages && i < N; ++i) load(i);
-    int64_t later = 0;
+    // ------------------------------------------------------------------ loads and decays
     int n = 0;
+    bool ok = true;
 #pragma unroll 1
-    for (; n < N; ++n) {
-      const int s = n % kStages;
-      const float2 g = ring.take(n);
-      const bool nan = __any_sync(0xffffffffu, g.x != g.x || g.y != g.y);
-      const int64_t u0 = log_units(g.x), u1 = log_units(g.y);
-      ask(n + kAhead);
-      int64_t sum = u0 + u1;
+    for (int unit = blockIdx.x; ok && unit < slots * p.H; unit += gridDim.x) {
+      const int h = unit % p.H;
+      Segment x;
+      if (!find_segment(p, seg, unit / p.H, false, x) || x.last) continue;
+      const int hk = h / (p.H / p.Hk);
+      const DecayRing ring{sm.g, p.g + h, p.gs, lane};
+      auto first = [&](int i) { return (int)x.lo + (N - 1 - i) * kC; };
+      auto ask = [&](int i) { ring.ask(i, i < N ? first(i) : 0, i < N ? first(i) + kC : 0); };
+      for (int i = 0; i < kAhead; ++i) ask(i);
+      int64_t later = 0;
+#pragma unroll 1
+      for (int i = 0; i < N; ++i, ++n) {
+        const int s = n % kStages;
+        if (n >= kStages && !(ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1))) break;
+        if (lane == 0) {
+          uint8_t* st = smem + s * M::STAGE;
+          ptx::mbar_arrive_expect_tx(&sm.full[s], M::STAGE);
+          load_tile<D>(st + M::V, &maps.v, &sm.full[s], h, first(i));
+          load_tile<D>(st + M::K, &maps.k, &sm.full[s], hk, first(i));
+          sm.kind[s] = (i == 0 ? kFirst : 0) | (i == N - 1 ? kLast : 0);
+          sm.out[s] = added + (x.place * p.H + h) * (int64_t)(D * D);
+        }
+        const float2 g = ring.take(i);
+        const bool nan = __any_sync(0xffffffffu, g.x != g.x || g.y != g.y);
+        const int64_t u0 = log_units(g.x), u1 = log_units(g.y);
+        ask(i + kAhead);
+        int64_t sum = u0 + u1;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t w = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += w;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t w = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += w;
+        }
+        const int64_t all = __shfl_sync(0xffffffffu, sum, 31);
+        const float2 a = log_pair(later + all - (sum - u1)), b = log_pair(later + all - sum);
+        float wa = ptx::ex2_approx(a.x + a.y), wb = ptx::ex2_approx(b.x + b.y);
+        if (nan) wa = wb = nan_f();
+        later += all;
+        *reinterpret_cast<float2*>(&sm.w[s][2 * lane]) = make_float2(wa, wb);
+        arrive(&sm.full[s]);
       }
-      const int64_t all = __shfl_sync(0xffffffffu, sum, 31);
-      const float2 a = log_pair(later + all - (sum - u1)), b = log_pair(later + all - sum);
-      float wa = ptx::ex2_approx(a.x + a.y), wb = ptx::ex2_approx(b.x + b.y);
-      if (nan) wa = wb = nan_f();
-      later += all;
-      if (n >= kStages) {
-        if (!wait(&sm.empty[s], ((n / kStages) - 1) & 1)) break;
-        load(n);
-      }
-      *reinterpret_cast<float2*>(&sm.w[s][2 * lane]) = make_float2(wa, wb);
-      arrive(&sm.full[s]);
+      if (lane == 0) added_log[x.place * p.H + h] = log_pair(later).x;
     }
-    if (lane == 0) added_log[x.place * p.H + h] = log_pair(later).x;
+    if (ok && n >= kStages) ok = wait(&sm.empty[n % kStages], ((n / kStages) - 1) & 1);
+    if (ok && lane == 0) {
+      sm.kind[n % kStages] = kStop;
+      ptx::mbar_arrive(&sm.full[n % kStages]);
+      ptx::mbar_arrive(&sm.full[n % kStages]);
+    }
     if (*(volatile int*)&sm.abort) {
       for (int i = n > kStages ? n - kStages : 0; i < n; ++i)
         ptx::mbar_wait_tries(&sm.full[i % kStages], (i / kStages) & 1, kTries);
@@ -845,20 +867,23 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
     }
     ptx::cp_async_wait<0>();
   } else if (warp == 17) {
-    bool ok = true;
+    // ------------------------------------------------------------------ products
+    int kind;
+    uint32_t unit = 0;
 #pragma unroll 1
-    for (int n = 0; ok && n < N; ++n) {
-      const int s = n % kStages, b = n & 1;
-      ok = wait(&sm.full[s], (n / kStages) & 1) && wait(&sm.v_full[b], (n >> 1) & 1);
-      if (!ok) break;
+    for (int n = 0; take(n, kind); ++n) {
+      const int s = n % kStages, b = n & 1, acc = unit & 1;
+      if ((kind & kFirst) && unit >= 2 && !wait(&sm.acc_empty[acc], ((unit >> 1) - 1) & 1)) break;
+      if (!wait(&sm.v_full[b], (n >> 1) & 1)) break;
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
-        issue_kv<D>(tmem, tmem + VP + b * 96, base + s * M::STAGE + M::K, n == 0);
+        issue_kv<D>(tmem + acc * 128, tmem + VP + b * 96, base + s * M::STAGE + M::K, kind & kFirst);
         ptx::mma_commit(&sm.v_empty[b]);
         ptx::mma_commit(&sm.empty[s]);
-        if (n == N - 1) ptx::mma_commit(&sm.done);
+        if (kind & kLast) ptx::mma_commit(&sm.acc_full[acc]);
       }
       __syncwarp();
+      if (kind & kLast) ++unit;
     }
     if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort)) {
       if (ptx::elect_one()) ptx::mma_commit(&sm.drain);
@@ -866,68 +891,85 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
       ptx::mbar_wait_tries(&sm.drain, 0, kTries);
       __syncwarp();
     }
-  } else {
+  } else if (warp < 16) {
+    // ------------------------------------------------------------------ V'
     // two sets of 8 warps take chunks in turn: 32 channels, half of the tokens each
     const int w = warp & 3, tok = ((warp >> 2) & 1) * 32, b = warp >> 3;
-    bool ok = w < NQ;
-    const uint32_t lanes = (uint32_t)(w * 32) << 16;
+    if (w < NQ) {
+      const uint32_t lanes = (uint32_t)(w * 32) << 16;
+      int kind;
 #pragma unroll 1
-    for (int n = 0; ok && n < N; ++n) {
-      const int s = n % kStages;
-      const uint32_t st = base + s * M::STAGE;
-      if (!(ok = wait(&sm.full[s], (n / kStages) & 1))) break;
-      if ((n & 1) != b) {  // (every warp sees every phase of a stage: parities do not run ahead)
-        arrive(&sm.empty[s]);
-        continue;
-      }
-      uint32_t raw[2][8];
-      load_vt(st + M::V, w * 32, tok, lane, raw[0]);
-      load_vt(st + M::V, w * 32 + 16, tok, lane, raw[1]);
-      ptx::f32x2 weight[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = *reinterpret_cast<const float2*>(&sm.w[s][tok + i * 8 + 2 * (lane & 3)]);
-        weight[i] = ptx::pack2(f.x, f.y);
-      }
-      arrive(&sm.empty[s]);
-      if (n >= 2 && !(ok = wait(&sm.v_empty[b], ((n >> 1) - 1) & 1))) break;
-      ptx::tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        uint32_t part[3][8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint32_t x[3];
-          weigh3(c ? raw[1][i] : raw[0][i], weight[i >> 1], x);
-          part[0][i] = x[0];
-          part[1][i] = x[1];
-          part[2][i] = x[2];
+      for (int n = 0; take(n, kind); ++n) {
+        const int s = n % kStages;
+        if ((n & 1) != b) {  // (every warp sees every phase of a stage: parities do not run ahead)
+          arrive(&sm.empty[s]);
+          continue;
         }
+        const uint32_t st = base + s * M::STAGE;
+        uint32_t raw[2][8];
+        load_vt(st + M::V, w * 32, tok, lane, raw[0]);
+        load_vt(st + M::V, w * 32 + 16, tok, lane, raw[1]);
+        ptx::f32x2 weight[4];
 #pragma unroll
-        for (int j = 0; j < 3; ++j)
-          ptx::tmem_st_rows16_nowait(
-              tmem + lanes + ((uint32_t)(c * 16) << 16) + VP + b * 96 + j * 32 + tok / 2, part[j]);
-      }
-      ptx::tmem_st_wait();
-      ptx::tc_fence_before();
-      arrive(&sm.v_full[b]);
-    }
-    // the first four warps hold the accumulator's rows
-    if (ok && warp < 4 && wait(&sm.done, 0)) {
-      ptx::tc_fence_after();
-      float* out = added + (x.place * p.H + h) * (int64_t)(D * D) + w * 32 + lane;
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = *reinterpret_cast<const float2*>(&sm.w[s][tok + i * 8 + 2 * (lane & 3)]);
+          weight[i] = ptx::pack2(f.x, f.y);
+        }
+        arrive(&sm.empty[s]);
+        if (n >= 2 && !wait(&sm.v_empty[b], ((n >> 1) - 1) & 1)) break;
+        ptx::tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        float f[32];
-        ptx::tmem_ld32(tmem + lanes + c * 32, f);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t part[3][8];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) out[(c * 32 + i) * D] = f[i];
+          for (int i = 0; i < 8; ++i) {
+            uint32_t x[3];
+            weigh3(c ? raw[1][i] : raw[0][i], weight[i >> 1], x);
+            part[0][i] = x[0];
+            part[1][i] = x[1];
+            part[2][i] = x[2];
+          }
+#pragma unroll
+          for (int j = 0; j < 3; ++j)
+            ptx::tmem_st_rows16_nowait(
+                tmem + lanes + ((uint32_t)(c * 16) << 16) + VP + b * 96 + j * 32 + tok / 2, part[j]);
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        arrive(&sm.v_full[b]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ sums out (warps 18 .. 21)
+    const int w = warp & 3;
+    if (w < NQ) {
+      int kind;
+      uint32_t unit = 0;
+#pragma unroll 1
+      for (int n = 0; take(n, kind); ++n) {
+        const int s = n % kStages;
+        float* out = sm.out[s] + w * 32 + lane;
+        arrive(&sm.empty[s]);
+        if (!(kind & kLast)) continue;
+        const uint32_t acc = unit & 1;
+        if (!wait(&sm.acc_full[acc], (unit >> 1) & 1)) break;
+        ptx::tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float f[32];
+          ptx::tmem_ld32(tmem + ((uint32_t)(w * 32) << 16) + acc * 128 + c, f);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) out[(c + i) * D] = f[i];
+        }
+        ptx::tc_fence_before();
+        arrive(&sm.acc_empty[acc]);
+        ++unit;
       }
     }
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 17) ptx::tmem_dealloc(tmem, kCols);
+  if (warp == 17) ptx::tmem_dealloc(tmem, 512);
 }
 
 template <int D>
@@ -944,21 +986,24 @@ kda_status launch_d(const DecayParams& p, int seg, float* added, float* added_lo
   constexpr int out_bytes = Out<D>::SMALL + (int)sizeof(OutSmall);
   constexpr int add_bytes = Add<D>::SMALL + (int)sizeof(AddSmall);
   static_assert(out_bytes <= 232448 && add_bytes <= 232448, "shared memory");
-  static bool set[64] = {};
-  int dev = 0;
+  static int sms_of[64] = {};  // by device: SMs, once the kernels are set up there
+  int dev = 0, sms = 0;
   cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !set[dev]) {
+  if (dev >= 0 && dev < 64) sms = sms_of[dev];
+  if (sms == 0) {
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     cudaFuncSetAttribute(decay_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, out_bytes);
     cudaFuncSetAttribute(decay_add_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, add_bytes);
-    if (dev >= 0 && dev < 64) set[dev] = true;
+    if (dev >= 0 && dev < 64) sms_of[dev] = sms;
   }
-  const unsigned grid = (unsigned)((p.total / seg + p.n_seqs) * p.H);
+  const int slots = p.total / seg + p.n_seqs;
+  const unsigned grid = (unsigned)(slots * p.H < sms ? slots * p.H : sms);
   if (p.total > seg) {
-    decay_add_kernel<D><<<grid, kAddThreads, add_bytes, s>>>(m, p, seg, added, added_log);
+    decay_add_kernel<D><<<grid, kAddThreads, add_bytes, s>>>(m, p, seg, slots, added, added_log);
     launch_decay_scan(p, D, seg, added, added_log, s);
     count_launches(1);
   }
-  decay_tc_kernel<D><<<grid, kThreads, out_bytes, s>>>(m, p, seg, added);
+  decay_tc_kernel<D><<<grid, kThreads, out_bytes, s>>>(m, p, seg, slots, added);
   count_launches(1);
   return check_launch("kda_decay_prefill");
 }
