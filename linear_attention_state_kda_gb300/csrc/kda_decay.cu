@@ -160,7 +160,7 @@ decay_chunk_kernel(const DecayParams p, int seg, float* added, float* added_log)
     if (entry) f = *reinterpret_cast<const float4*>(entry + (int64_t)(r0 + i) * D + c0);
     st[i][0] = f.x; st[i][1] = f.y; st[i][2] = f.z; st[i][3] = f.w;
   }
-  int64_t log_sum = 0;  // thread 0
+  float2 log_sum = make_float2(0.0f, 0.0f);  // thread 0
 
   const T *q = (const T*)p.q + (int64_t)hk * D, *k = (const T*)p.k + (int64_t)hk * D,
           *v = (const T*)p.v + (int64_t)h * D + col0;
@@ -202,22 +202,17 @@ decay_chunk_kernel(const DecayParams p, int seg, float* added, float* added_log)
     }
     if (tid < 32) {
       const float g = tid < n ? p.g[(t0 + tid) * p.gs + h] : 0.0f;
-      int64_t u = log_units(g);
       const bool nan = __any_sync(0xffffffffu, g != g);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t w = __shfl_up_sync(0xffffffffu, u, o);
-        if (tid >= o) u += w;
-      }
-      const int64_t all = __shfl_sync(0xffffffffu, u, 31);
-      const float bad = nan ? __int_as_float(0x7fffffff) : 0.0f;  // a NaN decay spoils its chunk
-      gam[tid] = log_pair(u);
-      gam[tid].x += bad;
-      s_in[tid] = exp2f(gam[tid].x + gam[tid].y);
-      s_out[tid] = exp2f(log_pair(all - u).x + bad);
+      float2 u = log_scan(log_pair(g), tid);
+      const float2 all = make_float2(__shfl_sync(0xffffffffu, u.x, 31),
+                                     __shfl_sync(0xffffffffu, u.y, 31));
+      if (nan) u.x = __int_as_float(0x7fffffff);  // a NaN decay spoils its chunk
+      gam[tid] = u;
+      s_in[tid] = exp2f(u.x + u.y);
+      s_out[tid] = decay_between(all, u);
       if (tid == 0) {
-        s_total = exp2f(log_pair(all).x + bad);
-        log_sum += all;
+        s_total = decay_between(all, make_float2(nan ? u.x : 0.0f, 0.0f));
+        log_sum = log_add(log_sum, all);
       }
     }
     __syncthreads();
@@ -291,7 +286,7 @@ decay_chunk_kernel(const DecayParams p, int seg, float* added, float* added_log)
   float* exit_state = nullptr;
   if (kStates) {
     exit_state = added + (x.place * p.H + h) * (int64_t)(D * D);
-    if (tid == 0 && blockIdx.z == 0) added_log[x.place * p.H + h] = log_pair(log_sum).x;
+    if (tid == 0 && blockIdx.z == 0) added_log[x.place * p.H + h] = log_sum.x;
   } else if (x.last && p.final_state) {
     exit_state = p.final_state + ((int64_t)x.seq * p.H + h) * (D * D);
   }

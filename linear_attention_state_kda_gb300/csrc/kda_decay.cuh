@@ -50,22 +50,36 @@ __device__ __forceinline__ bool find_segment(const DecayParams& p, int seg, int 
   return x.first || x.lo < c1;
 }
 
-// Log-decays in units of 2^-40 of a base-2 exponent, as integers: sums of any number of them are
-// exact, so the decay between two tokens does not lose bits to a strong decay before both. A
-// token's decay below e^-277 (2^-400) counts as that: no fp32 state survives it either way.
-// (In fp32 pairs: double precision runs at 1/64 of the rate and took 2500 cycles a chunk.)
-__device__ __forceinline__ int64_t log_units(float g) {
+// Sums of log-decays, in base-2 exponents, as pairs of floats (high + low part): their error stays
+// below 2^-30 however strong the decays, so the decay between two tokens does not lose bits to a
+// strong decay before both. A token's decay below e^-277 (2^-400) counts as that: no fp32 state
+// survives it either way. (As 64-bit integers or in double precision the conversions alone took
+// 2000 cycles a chunk.)
+__device__ __forceinline__ float2 log_pair(float g) {
   g = g < -277.0f ? -277.0f : g;  // (a NaN stays)
-  // g / ln 2 as the sum of two floats
-  const float c0 = 1.4426950216293335f, c1 = 1.9259629911266175e-8f;
-  const float a = g * c0, b = fmaf(g, c1, fmaf(g, c0, -a));
-  return __float2ll_rn(a * 1099511627776.0f) + __float2ll_rn(b * 1099511627776.0f);
+  const float c0 = 1.4426950216293335f, c1 = 1.9259629911266175e-8f;  // 1 / ln 2
+  const float a = g * c0;
+  return make_float2(a, fmaf(g, c1, fmaf(g, c0, -a)));
 }
-// A sum of log units as a pair of floats, hi + lo, in base-2 exponents.
-__device__ __forceinline__ float2 log_pair(int64_t u) {
-  const float hi = __ll2float_rn(u);
-  const float lo = __ll2float_rn(u - __float2ll_rn(hi));
-  return make_float2(hi * 9.094947017729282e-13f, lo * 9.094947017729282e-13f);  // 2^-40
+__device__ __forceinline__ float2 log_add(float2 a, float2 b) {
+  const float s = __fadd_rn(a.x, b.x), t = __fsub_rn(s, a.x);
+  float e = __fadd_rn(__fsub_rn(a.x, __fsub_rn(s, t)), __fsub_rn(b.x, t));  // s + e = a.x + b.x
+  e = __fadd_rn(e, __fadd_rn(a.y, b.y));
+  const float hi = __fadd_rn(s, e);
+  return make_float2(hi, __fsub_rn(e, __fsub_rn(hi, s)));
+}
+__device__ __forceinline__ float2 log_sub(float2 a, float2 b) {
+  return log_add(a, make_float2(-b.x, -b.y));
+}
+// Sums over the lanes up to each.
+__device__ __forceinline__ float2 log_scan(float2 v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float2 w = make_float2(__shfl_up_sync(0xffffffffu, v.x, o),
+                                 __shfl_up_sync(0xffffffffu, v.y, o));
+    if (lane >= o) v = log_add(v, w);
+  }
+  return v;
 }
 // 2^(a - b).
 __device__ __forceinline__ float decay_between(float2 a, float2 b) {

@@ -4,11 +4,12 @@
 // the state before it (fp32, kept transposed in TMEM: lanes are value channels),
 //     O^T = e^gamma_t * (S^T Q^T) + V^T P^T,   P_ts = [s <= t] e^(gamma_t - gamma_s) q_t . k_s
 //     S'^T = e^Gamma S^T + V'^T K,             V'_s = e^(Gamma - gamma_s) v_s
-// Every product is a tcgen05 bf16 product with fp32 sums. Operands that are not inputs are carried in
-// several bf16 parts, so that a product is as exact as its user needs: S and P in two (16 bits, under
-// the rounding of the bf16 outputs), V' in three (24 bits: states are fp32, and what a token adds to
-// them stays for the rest of the sequence). The two sums of O have accumulators of their own and
-// meet in fp32, so that Q needs no decayed copy.
+// Every product is a tcgen05 bf16 product with fp32 sums. S and P enter theirs rounded to bf16, which
+// costs an output as much as its own rounding to bf16 (together 1.4 times the latter alone; in two
+// parts each they cost half of the issue slots, which bound the kernel then). What a token adds to
+// the state stays for the rest of the sequence, and states are fp32: V' is carried in three bf16
+// parts (24 bits). The two sums of O have accumulators of their own and meet in fp32, so that Q
+// needs no decayed copy.
 //
 // Roles of a CTA (one segment of one head, 24 warps): one warp loads (TMA) and sums the decays; one
 // issues the products; 8 put V and V' into TMEM, transposed on the way; 2 turn q.k into P; 8 split
@@ -51,14 +52,14 @@ template <int D>
 struct Out {
   static constexpr int TILE = kC * D * 2, STAGE = 3 * TILE;
   static constexpr int Q = 0, K = TILE, V = 2 * TILE;
-  static constexpr int P = kStages * STAGE;  // two parts of 8 KB
+  static constexpr int P = kStages * STAGE;  // two of 8 KB, in turn
   static constexpr int O = P + 2 * 8192;     // outputs, as Q
   static constexpr int SMALL = O + TILE;
 };
 struct OutSmall {
   uint64_t full[kStages], empty[kStages];
-  uint64_t sc_full, sc_empty, p_full, v_full, vt_full, s_full;
-  uint64_t kv_done, sq_done, x_full, o_full, o_empty, drain;
+  uint64_t sc_full, sc_empty, p_full, p_empty[2], v_full, vt_full, s_full;
+  uint64_t kv_done, sq_done, o_full, o_empty, drain;
   float ghi[kStages][kC], glo[kStages][kC];  // running sums of log2 decays, high and low parts
   float g[kAhead][kC];                       // log-decays of the next chunks
   float2 total[kStages];
@@ -66,13 +67,13 @@ struct OutSmall {
   uint32_t tmem;
   int abort;
 };
-// TMEM columns: the state (fp32) and its two parts, V' in three parts and V (transposed, two tokens a
-// column), the scores, and the outputs, all 512 at D = 128.
+// TMEM columns: the state (fp32) and its bf16 rounding, V' in three parts and V (transposed, two tokens
+// a column), the scores, and the two sums of O, all 512 at D = 128.
 template <int D>
 struct Tm {
-  static constexpr int S = 0, HI = D, LO = HI + D / 2, VP = LO + D / 2, VT = VP + 96, SC = VT + 32,
-                       O = SC + 64;
-  static_assert(O + 64 <= 512, "TMEM");
+  static constexpr int S = 0, HI = D, VP = HI + D / 2, VT = VP + 96, SC = VT + 32, OI = SC + 64,
+                       OA = OI + 64;
+  static_assert(OA + 64 <= 512, "TMEM");
 };
 
 __device__ __forceinline__ void st_shared(uint32_t at, const uint4& v) {
@@ -106,14 +107,6 @@ __device__ __forceinline__ uint32_t take_top(ptx::f32x2& x) {
   ptx::unpack2(x, a, b);
   x = ptx::fma2(ptx::pack2(top(a), top(b)), ptx::pack2(-1.0f, -1.0f), x);
   return tops(a, b);
-}
-// A pair in two bf16 parts: the first truncated, the rest rounded (2^-16 in all). An infinity or NaN
-// stays one: its rest is NaN.
-__device__ __forceinline__ void split2(ptx::f32x2 x, uint32_t& hi, uint32_t& lo) {
-  hi = take_top(x);
-  float a, b;
-  ptx::unpack2(x, a, b);
-  lo = pack_bf16(a, b);
 }
 // Two bf16 values times two weights in three parts of 8 bits: the fp32 products exactly.
 __device__ __forceinline__ void weigh3(uint32_t v, ptx::f32x2 w, uint32_t part[3]) {
@@ -250,12 +243,13 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
     ptx::mbar_init(&sm.sc_full, 1);
     ptx::mbar_init(&sm.sc_empty, 2);
     ptx::mbar_init(&sm.p_full, 2);
+    ptx::mbar_init(&sm.p_empty[0], 1);
+    ptx::mbar_init(&sm.p_empty[1], 1);
     ptx::mbar_init(&sm.v_full, 2 * NQ);
     ptx::mbar_init(&sm.vt_full, 2 * NQ);
     ptx::mbar_init(&sm.s_full, 2 * NQ);
     ptx::mbar_init(&sm.kv_done, 1);
     ptx::mbar_init(&sm.sq_done, 1);
-    ptx::mbar_init(&sm.x_full, NQ);
     ptx::mbar_init(&sm.o_full, 1);
     ptx::mbar_init(&sm.o_empty, NQ);
     ptx::mbar_init(&sm.drain, 1);
@@ -327,19 +321,14 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
           } else {
             ptx::tmem_ld32(t_s + b, f);
           }
-          float hi[16], lo[16];
+          float r[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const ptx::f32x2 y = ptx::pack2(f[2 * i], f[2 * i + 1]);
-            uint32_t u, v;
-            split2(y, u, v);
-            hi[i] = __uint_as_float(u);
-            lo[i] = __uint_as_float(v);
-            ptx::unpack2(ptx::mul2(y, aa), f[2 * i], f[2 * i + 1]);
+            r[i] = __uint_as_float(pack_bf16(f[2 * i], f[2 * i + 1]));
+            ptx::unpack2(ptx::mul2(ptx::pack2(f[2 * i], f[2 * i + 1]), aa), f[2 * i], f[2 * i + 1]);
           }
           ptx::tmem_st32_nowait(t_s + b, f);
-          ptx::tmem_st16(t_part + T::HI + b / 2, hi);
-          ptx::tmem_st16(t_part + T::LO + b / 2, lo);
+          ptx::tmem_st16(t_part + T::HI + b / 2, r);
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
@@ -393,15 +382,9 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
           }
           const float2 g = ring.take(i);
           const bool nan = __any_sync(0xffffffffu, g.x != g.x || g.y != g.y);
-          const int64_t u0 = log_units(g.x), u1 = log_units(g.y);
+          const float2 second = log_pair(g.y);
+          float2 b = log_scan(log_add(log_pair(g.x), second), lane), a = log_sub(b, second);
           ring.ask(i + kAhead, x.lo + (int64_t)(i + kAhead) * kC, t_end);
-          int64_t sum = u0 + u1;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int64_t w = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += w;
-          }
-          float2 a = log_pair(sum - u1), b = log_pair(sum);
           if (nan) a.x = b.x = nan_f();  // a NaN decay spoils its chunk
           *reinterpret_cast<float2*>(&sm.ghi[s][2 * lane]) = make_float2(a.x, b.x);
           *reinterpret_cast<float2*>(&sm.glo[s][2 * lane]) = make_float2(a.y, b.y);
@@ -459,13 +442,11 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
         if (ptx::elect_one()) {
           const uint64_t b = ptx::sdesc_sw128(st + M::Q, 16, 1024);
 #pragma unroll 1
-          for (uint32_t i = 0; i < 2 * (D / 64); ++i) {  // both parts: they are side by side
-            const uint32_t g = i % (D / 64);
+          for (uint32_t i = 0; i < D / 64; ++i)
 #pragma unroll
             for (uint32_t j = 0; j < 4; ++j)
-              ptx::mma_f16_ts(tmem + T::O, tmem + T::HI + i * 32 + j * 8,
-                              ptx::desc_add(b, g * 8192 + j * 32), id64, i + j > 0);
-          }
+              ptx::mma_f16_ts(tmem + T::OI, tmem + T::HI + i * 32 + j * 8,
+                              ptx::desc_add(b, i * 8192 + j * 32), id64, i + j > 0);
           ptx::mma_commit(&sm.sq_done);
           ptx::mma_commit(&sm.empty[s]);
         }
@@ -476,17 +457,15 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
           ptx::tc_fence_after();
           issue_qk(n + 1);
         }
-        if (!wait.all({&sm.p_full, &sm.vt_full, &sm.x_full}, {ph, ph, ph})) break;
+        if (!wait.all({&sm.p_full, &sm.vt_full}, {ph, ph})) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
-          const uint64_t b = ptx::sdesc_sw128(base + M::P, 16, 1024);
-#pragma unroll 1
-          for (uint32_t part = 0; part < 2; ++part)
+          const uint64_t b = ptx::sdesc_sw128(base + M::P + ph * 8192, 16, 1024);
 #pragma unroll
-            for (uint32_t i = 0; i < kC / 16; ++i)
-              ptx::mma_f16_ts(tmem + T::O, tmem + T::VT + i * 8,
-                              ptx::desc_add(b, part * 8192 + i * 32), id64, 1);
+          for (uint32_t i = 0; i < kC / 16; ++i)
+            ptx::mma_f16_ts(tmem + T::OA, tmem + T::VT + i * 8, ptx::desc_add(b, i * 32), id64, i > 0);
           ptx::mma_commit(&sm.o_full);
+          ptx::mma_commit(&sm.p_empty[ph]);
         }
         __syncwarp();
         ok = more;
@@ -572,87 +551,63 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
       if (w < NQ) {
         const int tid = w * 32 + lane;
         const uint32_t stage = base + M::O + (w >> 1) * 8192;  // its block of 64 channels
-        const uint32_t t_o = tmem + ((uint32_t)(w * 32) << 16) + T::O;
+        const uint32_t t_o = tmem + ((uint32_t)(w * 32) << 16);
         const ptx::f32x2 scale = ptx::pack2(p.scale, p.scale);
         Chunk c;
 #pragma unroll 1
         for (int n = 0;; ++n) {
           const int s = n % kStages;
-          // S^T Q^T gets the decays from the chunk's start in place, and V^T P^T is added to it
           bool ok = wait(&sm.full[s], (n / kStages) & 1);
           if (ok) {
             c = sm.chunk[s];
-            ok = __shfl_sync(0xffffffffu, c.kind, 0) != kStop && wait(&sm.sq_done, n & 1);
-          }
-          if (ok) {
-            ptx::tc_fence_after();
-#pragma unroll 1
-            for (int tok = 0; tok < kC; tok += 32) {
-              ptx::f32x2 ee[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int t = tok + i * 8 + 2 * (lane & 3);
-                const float2 h2 = *reinterpret_cast<const float2*>(&sm.ghi[s][t]);
-                const float2 l2 = *reinterpret_cast<const float2*>(&sm.glo[s][t]);
-                ee[i] = ptx::pack2(ptx::ex2_approx(h2.x + l2.x), ptx::ex2_approx(h2.y + l2.y));
-              }
-#pragma unroll 1
-              for (uint32_t ch = 0; ch < 32; ch += 16) {  // 16 channels x 32 tokens
-                uint32_t x[16];
-                ptx::tmem_ld_frag32_nowait(t_o + (ch << 16) + tok, x);
-                ptx::tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[i]));
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                  float y0, y1;
-                  ptx::unpack2(ptx::mul2(ee[j >> 2], ptx::pack2(__uint_as_float(x[j]),
-                                                                __uint_as_float(x[j + 1]))),
-                               y0, y1);
-                  x[j] = __float_as_uint(y0);
-                  x[j + 1] = __float_as_uint(y1);
-                }
-                ptx::tmem_st_frag32_nowait(t_o + (ch << 16) + tok, x);
-              }
-            }
-            ptx::tmem_st_wait();
-            ptx::tc_fence_before();
-            arrive(&sm.x_full);
-            if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
-            ok = wait(&sm.o_full, n & 1);
+            ok = __shfl_sync(0xffffffffu, c.kind, 0) != kStop && wait(&sm.o_full, n & 1);
           }
           if (tid == 0) ptx::bulk_wait_read0();  // the last chunk's rows have left
           ok = group_and(1, NQ * 32, ok);
           if (!ok) break;
           ptx::tc_fence_after();
 #pragma unroll 1
-          for (int b = 0; b < 4; ++b) {
-            const int ch0 = (b & 1) * 16, tok = (b >> 1) * 32;
-            uint32_t x[16];
-            ptx::tmem_ld_frag32_nowait(t_o + ((uint32_t)ch0 << 16) + tok, x);
-            ptx::tmem_ld_wait();
+          for (int tok = 0; tok < kC; tok += 32) {
+            ptx::f32x2 ee[4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[i]));
-            uint32_t o[8];
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              float y0, y1;
-              ptx::unpack2(
-                  ptx::mul2(scale, ptx::pack2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]))), y0,
-                  y1);
-              o[j >> 1] = pack_bf16(y0, y1);
+            for (int i = 0; i < 4; ++i) {
+              const int t = tok + i * 8 + 2 * (lane & 3);
+              const float2 h2 = *reinterpret_cast<const float2*>(&sm.ghi[s][t]);
+              const float2 l2 = *reinterpret_cast<const float2*>(&sm.glo[s][t]);
+              ee[i] = ptx::pack2(ptx::ex2_approx(h2.x + l2.x), ptx::ex2_approx(h2.y + l2.y));
             }
-            // matrices (channels 0-7, 8-15) x (two groups of 8 tokens): row = token
-            const int ch = ((w & 1) * 32 + ch0) / 8 + ((lane >> 3) & 1);
+#pragma unroll 1
+            for (uint32_t ch0 = 0; ch0 < 32; ch0 += 16) {  // 16 channels x 32 tokens
+              uint32_t x[16], y[16];
+              ptx::tmem_ld_frag32_nowait(t_o + (ch0 << 16) + T::OI + tok, x);
+              ptx::tmem_ld_frag32_nowait(t_o + (ch0 << 16) + T::OA + tok, y);
+              ptx::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int t = tok + i * 16 + (lane >> 4) * 8 + (lane & 7);
-              ptx::st_matrix4_trans(stage + t * 128 + ((ch ^ (t & 7)) << 4), o[4 * i], o[4 * i + 1],
-                                    o[4 * i + 2], o[4 * i + 3]);
+              for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[i]), "+r"(y[i]));
+              uint32_t o[8];
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                const ptx::f32x2 inter =
+                    ptx::pack2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+                const ptx::f32x2 intra =
+                    ptx::pack2(__uint_as_float(y[j]), __uint_as_float(y[j + 1]));
+                float y0, y1;
+                ptx::unpack2(ptx::mul2(ptx::fma2(ee[j >> 2], inter, intra), scale), y0, y1);
+                o[j >> 1] = pack_bf16(y0, y1);
+              }
+              // matrices (channels 0-7, 8-15) x (two groups of 8 tokens): row = token
+              const int ch = ((w & 1) * 32 + (int)ch0) / 8 + ((lane >> 3) & 1);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int t = tok + i * 16 + (lane >> 4) * 8 + (lane & 7);
+                ptx::st_matrix4_trans(stage + t * 128 + ((ch ^ (t & 7)) << 4), o[4 * i], o[4 * i + 1],
+                                      o[4 * i + 2], o[4 * i + 3]);
+              }
             }
           }
           ptx::tc_fence_before();
           arrive(&sm.o_empty);
+          if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
           ptx::fence_proxy_async_smem();
           group_and(1, NQ * 32, true);
           if (c.tokens >= kC) {
@@ -680,13 +635,15 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
 #pragma unroll 1
       for (int n = 0; take(n, c); ++n) {
         const int s = n % kStages;
-        if (!wait(&sm.sc_full, n & 1) || (n > 0 && !wait(&sm.o_full, (n - 1) & 1))) break;
+        if (!wait(&sm.sc_full, n & 1) ||
+            (n >= 2 && !wait(&sm.p_empty[n & 1], ((n >> 1) - 1) & 1)))
+          break;
         ptx::tc_fence_after();
         const ptx::f32x2 gh = ptx::pack2(sm.ghi[s][i], sm.ghi[s][i]),
                          gl = ptx::pack2(sm.glo[s][i], sm.glo[s][i]), minus = ptx::pack2(-1.0f, -1.0f);
 #pragma unroll 1
         for (int c0 = 0; c0 < kC; c0 += 16) {
-          uint32_t hi[8], lo[8];
+          uint32_t o[8];
           if (c0 < 32 * w + 32) {
             uint32_t r[16];
             ptx::tmem_ld16_nowait(tmem + lanes + T::SC + c0, r);
@@ -712,17 +669,16 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
               ptx::unpack2(y, y0, y1);
               y0 = c0 + j <= i ? y0 : 0.0f;
               y1 = c0 + j < i ? y1 : 0.0f;
-              split2(ptx::pack2(y0, y1), hi[j >> 1], lo[j >> 1]);
+              o[j >> 1] = pack_bf16(y0, y1);
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) hi[j] = lo[j] = 0u;
+            for (int j = 0; j < 8; ++j) o[j] = 0u;
           }
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            const uint32_t off = base + M::P + i * 128 + ((((c0 >> 3) + b) ^ (i & 7)) << 4);
-            st_shared(off, make_uint4(hi[4 * b], hi[4 * b + 1], hi[4 * b + 2], hi[4 * b + 3]));
-            st_shared(off + 8192, make_uint4(lo[4 * b], lo[4 * b + 1], lo[4 * b + 2], lo[4 * b + 3]));
+            st_shared(base + M::P + (n & 1) * 8192 + i * 128 + ((((c0 >> 3) + b) ^ (i & 7)) << 4),
+                      make_uint4(o[4 * b], o[4 * b + 1], o[4 * b + 2], o[4 * b + 3]));
           }
         }
         ptx::fence_proxy_async_smem();
@@ -821,7 +777,7 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
       auto first = [&](int i) { return (int)x.lo + (N - 1 - i) * kC; };
       auto ask = [&](int i) { ring.ask(i, i < N ? first(i) : 0, i < N ? first(i) + kC : 0); };
       for (int i = 0; i < kAhead; ++i) ask(i);
-      int64_t later = 0;
+      float2 later = make_float2(0.0f, 0.0f);
 #pragma unroll 1
       for (int i = 0; i < N; ++i, ++n) {
         const int s = n % kStages;
@@ -836,23 +792,19 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
         }
         const float2 g = ring.take(i);
         const bool nan = __any_sync(0xffffffffu, g.x != g.x || g.y != g.y);
-        const int64_t u0 = log_units(g.x), u1 = log_units(g.y);
+        const float2 second = log_pair(g.y);
+        const float2 sum = log_scan(log_add(log_pair(g.x), second), lane);
         ask(i + kAhead);
-        int64_t sum = u0 + u1;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t w = __shfl_up_sync(0xffffffffu, sum, o);
-          if (lane >= o) sum += w;
-        }
-        const int64_t all = __shfl_sync(0xffffffffu, sum, 31);
-        const float2 a = log_pair(later + all - (sum - u1)), b = log_pair(later + all - sum);
+        const float2 all = make_float2(__shfl_sync(0xffffffffu, sum.x, 31),
+                                       __shfl_sync(0xffffffffu, sum.y, 31));
+        const float2 upto = log_add(later, all), b = log_sub(upto, sum), a = log_add(b, second);
         float wa = ptx::ex2_approx(a.x + a.y), wb = ptx::ex2_approx(b.x + b.y);
         if (nan) wa = wb = nan_f();
-        later += all;
+        later = upto;
         *reinterpret_cast<float2*>(&sm.w[s][2 * lane]) = make_float2(wa, wb);
         arrive(&sm.full[s]);
       }
-      if (lane == 0) added_log[x.place * p.H + h] = log_pair(later).x;
+      if (lane == 0) added_log[x.place * p.H + h] = later.x;
     }
     if (ok && n >= kStages) ok = wait(&sm.empty[n % kStages], ((n / kStages) - 1) & 1);
     if (ok && lane == 0) {

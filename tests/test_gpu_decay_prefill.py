@@ -1,11 +1,14 @@
 """kda_decay_prefill against the recurrence in 64 bits.
 
 Tolerances, element by element, relative to the same sums with every term's absolute value (A for
-outputs, B for states). bf16: the state and the products q.k are carried in two bf16 parts, off by at
-most 2^-8 of 2^-8 each (2^-16 A in all, the two cover different terms); the fp32 sums of at most 2^9
-terms in a chunk, or of that many chunks, are off by 2^-15 A in the worst case; exponentials a few
-2^-22. So 2^-14 A, and the output's own rounding, 2^-8 of it. fp32: 2^-14 A covers the same sums.
-States: parts of 24 bits and sums of at most 64 terms a chunk and a few hundred chunks: 2^-15 B."""
+outputs, B for states). bf16: the state and the weighted products q.k enter the outputs rounded to
+bf16, each term by at most 2^-8 of itself: 2^-8 A; the fp32 sums of at most 2^9 terms in a chunk, or of
+that many chunks, are off by 2^-15 A in the worst case, exponentials by a few 2^-22: 2^-14 A in all;
+and the output's own rounding, 2^-8 of it. Over a whole tensor these roundings are independent, each
+at most 2^-8 and 2^-8 / sqrt(3) in the root mean square, and the terms of random inputs add up like
+the outputs: the two together stay below 2^-8 sqrt(2 / 3) of the outputs in the 2-norm, 2^-8 of them
+with the rest. fp32: 2^-14 A covers the sums. States: parts of 24 bits and sums of at most 64 terms a
+chunk and a few hundred chunks: 2^-15 B."""
 import numpy as np
 import pytest
 import torch
@@ -44,7 +47,11 @@ def check(q, k, v, g, cu, s0, scale, o, fin, dtype):
     gg = np.broadcast_to(f64(g), (T, H))
     want, st, a, b = ref.decay_prefill(f64(q), f64(k), f64(v), gg, cu.tolist(), init, scale)
     n = int(cu[-1])
-    tol = 2.0 ** -14 * a + (2.0 ** -8 * np.abs(want) if dtype == "bf16" else 0)
+    tol = 2.0 ** -14 * a
+    if dtype == "bf16":
+        tol = tol + 2.0 ** -8 * (a + np.abs(want))
+        off = np.linalg.norm((f64(o) - want)[:n])
+        assert off <= 2.0 ** -8 * np.linalg.norm(want[:n]), off / np.linalg.norm(want[:n])
     err = np.abs(f64(o) - want)[:n]
     assert (err <= tol[:n] + 1e-30).all(), float((err / (tol[:n] + 1e-30)).max())
     err = np.abs(f64(fin) - st)
