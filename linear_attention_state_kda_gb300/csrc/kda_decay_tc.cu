@@ -11,11 +11,12 @@
 // parts (24 bits). The two sums of O have accumulators of their own and meet in fp32, so that Q
 // needs no decayed copy.
 //
-// Roles of a CTA (one segment of one head, 24 warps): one warp loads (TMA) and sums the decays; one
-// issues the products; 8 put V and V' into TMEM, transposed on the way; 2 turn q.k into P; 8 split
-// and decay the state; 4 write outputs. Order of the products per chunk: V'^T K, whose result the
-// next chunk's state waits for; then S^T Q^T, V^T P^T and the next chunk's q.k, which run while the
-// state is decayed and split again.
+// Roles of a CTA (28 warps): one takes the units of work (segments of a head), one loads (TMA), one sums
+// the decays, one issues the products; 8 put V and V' into TMEM, transposed on the way; 4 turn q.k
+// into P; 8 round and decay the state; 4 write outputs. The chunks of all units run through them as
+// one stream, so that a unit's ends are covered by its neighbours. Order of the products per chunk:
+// V'^T K, whose result the next chunk's state waits for; then the next chunk's q.k, S^T Q^T and
+// V^T P^T, which run while the state is decayed and rounded again.
 #include "kda_decay.cuh"
 #include "kda_fp8.cuh"
 #include "ptx.cuh"
@@ -27,7 +28,7 @@ using namespace decay;
 
 constexpr int kC = 64;
 constexpr int kStages = 4;
-constexpr int kThreads = 768;
+constexpr int kThreads = 896;
 constexpr int kAhead = 2;
 constexpr uint32_t kTries = 1u << 19;  // of a wait inside a CTA: 2 s
 
@@ -39,15 +40,31 @@ struct Maps {
 struct Chunk {
   const float* entry;  // of the unit's first chunk: the state before it, or nullptr (zeros)
   float* exit;         // of a unit's last chunk: where the state after it goes, or nullptr
-  int t0, tokens;      // first token, and how many of the 64 belong to the segment
-  int head, kind;
+  int t0;              // first token
+  int head;
+  short tokens;        // how many of the 64 belong to the segment
+  short kind;
 };
-constexpr int kFirst = 1, kStop = 2;  // kinds: begins a unit; no chunk, the roles leave
+constexpr int kFirst = 1, kStop = 2, kLast = 4;  // kinds: begins or ends a unit; none, the roles leave
+
+// A unit of the work: a segment of one head. The scheduling warp takes the units that this CTA runs
+// (its own block's, then those of blocks that were not launched yet: a long unit holds no one up) and
+// finds their segments; the warps that load and that sum decays follow it through a ring.
+constexpr int kUnits = 2;
+struct Unit {
+  const float* entry;
+  float* exit;
+  int lo, hi, head;
+  int place;  // -1: there are no more units
+};
+struct UnitRing {
+  uint64_t full[kUnits], empty[kUnits], clc;
+  alignas(16) uint32_t response[4];
+  Unit unit[kUnits];
+};
 
 // Offsets in shared memory. Operand tiles are [64 tokens][64 channels] blocks of 8 KB (128-byte
-// swizzle), D / 64 of them side by side. q.k is a product with M = 128 on 64 rows: it reads the 64
-// rows after its own, into accumulator lanes that no one reads. The order Q, K, V keeps that inside
-// the stage.
+// swizzle), D / 64 of them side by side.
 template <int D>
 struct Out {
   static constexpr int TILE = kC * D * 2, STAGE = 3 * TILE;
@@ -56,9 +73,15 @@ struct Out {
   static constexpr int O = P + 2 * 8192;     // outputs, as Q
   static constexpr int SMALL = O + TILE;
 };
+// Every wait is by parity, which tells a phase only from the one before it, so none may be two phases
+// behind. Each barrier's next phase needs, at some remove, what its waiters do after this one: a
+// stage's chunk is refilled once every role has left it; the next scores wait for sc_empty, the next
+// state and V' for kv_done, the next rounded state for sq_done, the next V for o_full, the next
+// outputs for o_empty. P runs up to two chunks ahead of the products, so its barriers are by place.
 struct OutSmall {
+  UnitRing units;
   uint64_t full[kStages], empty[kStages];
-  uint64_t sc_full, sc_empty, p_full, p_empty[2], v_full, vt_full, s_full;
+  uint64_t sc_full, sc_empty, p_full[2], p_empty[2], v_full, vt_full, s_full, hi_full;
   uint64_t kv_done, sq_done, o_full, o_empty, drain;
   float ghi[kStages][kC], glo[kStages][kC];  // running sums of log2 decays, high and low parts
   float g[kAhead][kC];                       // log-decays of the next chunks
@@ -210,6 +233,52 @@ struct Waiter {
     return true;
   }
 };
+// The scheduling warp. find(block, unit): the unit of a block; false where it has none.
+template <class Find>
+__device__ __forceinline__ void schedule(UnitRing& ring, const Waiter& wait, int lane,
+                                         const Find& find) {
+  int block = blockIdx.x;
+  uint32_t asked = 0, n = 0;
+  bool ok = true;
+#pragma unroll 1
+  while (ok) {
+    const bool more = block >= 0;
+    if (more && lane == 0) {  // the next one, while this one's segment is found
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive_expect_tx(&ring.clc, 16);
+      ptx::clc_try_cancel(ring.response, &ring.clc);
+    }
+    Unit u;
+    u.place = -1;
+    if (!more || find(block, u)) {
+      const uint32_t at = n % kUnits;
+      ok = n < kUnits || wait(&ring.empty[at], ((n / kUnits) - 1) & 1);
+      if (ok && lane == 0) {
+        ring.unit[at] = u;
+        ptx::mbar_arrive(&ring.full[at]);
+      }
+      ++n;
+    }
+    if (!more) break;
+    if (!wait(&ring.clc, asked++ & 1)) {
+      ok = false;
+      break;
+    }
+    block = ptx::clc_block(ring.response);
+    __syncwarp();
+  }
+}
+// The next unit, for the warps that follow; false: none, or a wait gave up.
+__device__ __forceinline__ bool next_unit(UnitRing& ring, const Waiter& wait, int lane, uint32_t& n,
+                                          Unit& u) {
+  const uint32_t at = n % kUnits;
+  if (!wait(&ring.full[at], (n / kUnits) & 1)) return false;
+  u = ring.unit[at];
+  __syncwarp();  // every lane has read it
+  if (lane == 0) ptx::mbar_arrive(&ring.empty[at]);
+  ++n;
+  return __shfl_sync(0xffffffffu, u.place, 0) >= 0;
+}
 // Barrier of `threads` threads with the conjunction of their answers.
 __device__ __forceinline__ bool group_and(int id, int threads, bool ok) {
   uint32_t r;
@@ -226,8 +295,7 @@ __device__ __forceinline__ bool group_and(int id, int threads, bool ok) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg, int slots,
-                const float* added) {
+decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg, const float* added) {
   using M = Out<D>;
   using T = Tm<D>;
   constexpr int NQ = D / 32;  // warps that hold the accumulators' rows
@@ -238,16 +306,23 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&sm.full[i], 2);
-      ptx::mbar_init(&sm.empty[i], 1 + 2 + 5 * NQ);
+      ptx::mbar_init(&sm.empty[i], 1 + 4 + 5 * NQ);
     }
+    for (int i = 0; i < kUnits; ++i) {
+      ptx::mbar_init(&sm.units.full[i], 1);
+      ptx::mbar_init(&sm.units.empty[i], 2);
+    }
+    ptx::mbar_init(&sm.units.clc, 1);
     ptx::mbar_init(&sm.sc_full, 1);
-    ptx::mbar_init(&sm.sc_empty, 2);
-    ptx::mbar_init(&sm.p_full, 2);
-    ptx::mbar_init(&sm.p_empty[0], 1);
-    ptx::mbar_init(&sm.p_empty[1], 1);
+    ptx::mbar_init(&sm.sc_empty, 4);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&sm.p_full[i], 4);
+      ptx::mbar_init(&sm.p_empty[i], 1);
+    }
     ptx::mbar_init(&sm.v_full, 2 * NQ);
     ptx::mbar_init(&sm.vt_full, 2 * NQ);
     ptx::mbar_init(&sm.s_full, 2 * NQ);
+    ptx::mbar_init(&sm.hi_full, 2 * NQ);
     ptx::mbar_init(&sm.kv_done, 1);
     ptx::mbar_init(&sm.sq_done, 1);
     ptx::mbar_init(&sm.o_full, 1);
@@ -256,7 +331,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
     ptx::fence_mbar_init();
     sm.abort = 0;
   }
-  if (warp == 3) {
+  if (warp == 25) {
     ptx::tmem_alloc(&sm.tmem, 512);
     ptx::tmem_relinquish();
   }
@@ -277,9 +352,9 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
     return __shfl_sync(0xffffffffu, c.kind, 0) != kStop;
   };
 
-  // registers of the six warpgroups: 64 + 112 + 112 + 64 + 64 + 64 = 6 x 80
+  // registers of the seven warpgroups: 64 + 96 + 96 + 64 + 64 + 64 + 56 = 7 x 72
   if (warp >= 4 && warp < 12) {
-    ptx::regs_take<112>();
+    ptx::regs_take<96>();
     // ------------------------------------------------------------------ the state
     const int w = warp & 3, half = (warp - 4) >> 2;  // 32 value channels, half of the key channels
     if (w < NQ) {
@@ -292,14 +367,11 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
 #pragma unroll 1
       for (int n = 0;; ++n) {
         const int s = n % kStages;
-        bool ok = wait(&sm.full[s], (n / kStages) & 1) &&
-                  (n == 0 || wait.all({&sm.kv_done, &sm.sq_done},
-                                      {(uint32_t)(n - 1) & 1, (uint32_t)(n - 1) & 1}));
-        if (!ok) break;
+        if (!wait(&sm.full[s], (n / kStages) & 1) || (n > 0 && !wait(&sm.kv_done, (n - 1) & 1))) break;
         ptx::tc_fence_after();
         c = sm.chunk[s];
         const int kind = __shfl_sync(0xffffffffu, c.kind, 0);
-        if (kind != 0 && exit_state) {  // the unit before ends
+        if ((kind & (kFirst | kStop)) && exit_state) {  // the unit before ends
 #pragma unroll 1
           for (int b = 0; b < D / 2; b += 32) {
             float f[32];
@@ -312,102 +384,142 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
         exit_state = c.exit;
         const float a = ptx::ex2_approx(sm.total[s].x + sm.total[s].y);
         const ptx::f32x2 aa = ptx::pack2(a, a);
-#pragma unroll 1
-        for (int b = 0; b < D / 2; b += 32) {
-          float f[32];
-          if (kind == kFirst) {
+        // decayed first, which is what the next sum waits for
+        float r[D / 64][16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = c.entry ? __ldg(c.entry + at + (b + i) * D) : 0.0f;
+        for (int b = 0; b < D / 64; ++b) {
+          float f[32];
+          if (kind & kFirst) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              f[i] = c.entry ? __ldg(c.entry + at + (b * 32 + i) * D) : 0.0f;
           } else {
-            ptx::tmem_ld32(t_s + b, f);
+            ptx::tmem_ld32(t_s + b * 32, f);
           }
-          float r[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            r[i] = __uint_as_float(pack_bf16(f[2 * i], f[2 * i + 1]));
+            r[b][i] = __uint_as_float(pack_bf16(f[2 * i], f[2 * i + 1]));
             ptx::unpack2(ptx::mul2(ptx::pack2(f[2 * i], f[2 * i + 1]), aa), f[2 * i], f[2 * i + 1]);
           }
-          ptx::tmem_st32_nowait(t_s + b, f);
-          ptx::tmem_st16(t_part + T::HI + b / 2, r);
+          ptx::tmem_st32_nowait(t_s + b * 32, f);
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         arrive(&sm.s_full);
+        if (n > 0 && !wait(&sm.sq_done, (n - 1) & 1)) break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b) ptx::tmem_st16(t_part + T::HI + b * 16, r[b]);
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        arrive(&sm.hi_full);
         if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
       }
     }
-  } else {
-    ptx::regs_give<64>();
-    if (warp == 2) {
-      // ------------------------------------------------------------------ loads and decays
+  } else if (warp >= 24) {
+    ptx::regs_give<56>();
+    if (warp == 24) {
+      // ------------------------------------------------------------------ loads
       int n = 0;
+      uint32_t unit = 0;
+      Unit u;
       bool ok = true;
 #pragma unroll 1
-      for (int unit = blockIdx.x; ok && unit < slots * p.H; unit += gridDim.x) {
-        const int h = unit % p.H;
-        Segment x;
-        if (!find_segment(p, seg, unit / p.H, lane == 0 && h == 0, x)) continue;
-        if (x.hi == x.lo && !p.final_state) continue;
-        const int hk = h / (p.H / p.Hk);
-        const int t_end = (int)x.hi;
-        const int N = x.hi > x.lo ? (int)((x.hi - x.lo + kC - 1) / kC) : 1;
+      while (ok && next_unit(sm.units, wait, lane, unit, u)) {
+        const int hk = u.head / (p.H / p.Hk);
+        if (lane == 0 && u.entry) ptx::bulk_prefetch_l2(u.entry, D * D * 4);
         Chunk c;
-        c.entry = !x.first ? added + ((x.place - 1) * p.H + h) * (int64_t)(D * D)
-                  : p.init ? p.init + ((int64_t)x.seq * p.H + h) * (D * D) : nullptr;
-        c.exit = nullptr;
-        c.head = h;
-        if (lane == 0 && c.entry) ptx::bulk_prefetch_l2(c.entry, D * D * 4);
-        const DecayRing ring{sm.g, p.g + h, p.gs, lane};
-        for (int i = 0; i < kAhead; ++i) ring.ask(i, x.lo + (int64_t)i * kC, t_end);
+        c.entry = u.entry;
+        c.head = u.head;
+        int t = u.lo;
 #pragma unroll 1
-        for (int i = 0; i < N; ++i, ++n) {
+        do {
           const int s = n % kStages;
-          c.t0 = (int)x.lo + i * kC;
-          c.tokens = t_end - c.t0 < kC ? t_end - c.t0 : kC;
-          c.kind = i == 0 ? kFirst : 0;
-          if (i == N - 1 && x.last && p.final_state)
-            c.exit = p.final_state + ((int64_t)x.seq * p.H + h) * (D * D);
+          c.t0 = t;
+          c.tokens = (short)(u.hi - t < kC ? u.hi - t : kC);
+          c.kind = (short)((t == u.lo ? kFirst : 0) | (u.hi - t <= kC ? kLast : 0));
+          c.exit = c.kind & kLast ? u.exit : nullptr;
           if (n >= kStages && !(ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1))) break;
           if (lane == 0) {
+            sm.chunk[s] = c;
             uint8_t* st = smem + s * M::STAGE;
             if (c.tokens > 0) {
               ptx::mbar_arrive_expect_tx(&sm.full[s], M::STAGE);
-              load_tile<D>(st + M::K, &maps.k, &sm.full[s], hk, c.t0);
-              load_tile<D>(st + M::Q, &maps.q, &sm.full[s], hk, c.t0);
-              load_tile<D>(st + M::V, &maps.v, &sm.full[s], h, c.t0);
+              load_tile<D>(st + M::K, &maps.k, &sm.full[s], hk, t);
+              load_tile<D>(st + M::Q, &maps.q, &sm.full[s], hk, t);
+              load_tile<D>(st + M::V, &maps.v, &sm.full[s], u.head, t);
             } else {  // an empty sequence: all rows are cleared, the state passes through
               ptx::mbar_arrive(&sm.full[s]);
             }
-            sm.chunk[s] = c;
           }
+          ++n;
+          t += kC;
+        } while (t < u.hi);
+      }
+      const int s = n % kStages;
+      if (ok && n >= kStages) ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1);
+      if (ok && lane == 0) {
+        sm.chunk[s].kind = kStop;
+        ptx::mbar_arrive(&sm.full[s]);
+      }
+      if (*(volatile int*)&sm.abort) {  // the loads in flight land before the CTA leaves
+        __nanosleep(1000000);
+        __syncwarp();
+      }
+    } else if (warp == 26) {
+      // ------------------------------------------------------------------ sums of the decays
+      int n = 0;
+      uint32_t unit = 0;
+      Unit u;
+      bool ok = true;
+#pragma unroll 1
+      while (ok && next_unit(sm.units, wait, lane, unit, u)) {
+        const DecayRing ring{sm.g, p.g + u.head, p.gs, lane};
+        for (int i = 0; i < kAhead; ++i) ring.ask(i, u.lo + (int64_t)i * kC, u.hi);
+        int i = 0;
+#pragma unroll 1
+        do {
+          const int s = n % kStages;
           const float2 g = ring.take(i);
           const bool nan = __any_sync(0xffffffffu, g.x != g.x || g.y != g.y);
           const float2 second = log_pair(g.y);
           float2 b = log_scan(log_add(log_pair(g.x), second), lane), a = log_sub(b, second);
-          ring.ask(i + kAhead, x.lo + (int64_t)(i + kAhead) * kC, t_end);
+          ring.ask(i + kAhead, u.lo + (int64_t)(i + kAhead) * kC, u.hi);
           if (nan) a.x = b.x = nan_f();  // a NaN decay spoils its chunk
+          if (n >= kStages && !(ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1))) break;
           *reinterpret_cast<float2*>(&sm.ghi[s][2 * lane]) = make_float2(a.x, b.x);
           *reinterpret_cast<float2*>(&sm.glo[s][2 * lane]) = make_float2(a.y, b.y);
           if (lane == 31) sm.total[s] = b;
           arrive(&sm.full[s]);
-        }
+          ++n;
+          ++i;
+        } while (u.lo + (int64_t)i * kC < u.hi);
       }
-      if (ok && n >= kStages) ok = wait(&sm.empty[n % kStages], ((n / kStages) - 1) & 1);
-      if (ok && lane == 0) {
-        sm.chunk[n % kStages].kind = kStop;
-        ptx::mbar_arrive(&sm.full[n % kStages]);
-        ptx::mbar_arrive(&sm.full[n % kStages]);
-      }
-      if (*(volatile int*)&sm.abort) {  // the loads in flight land before the CTA leaves
-        for (int i = n > kStages ? n - kStages : 0; i < n; ++i)
-          ptx::mbar_wait_tries(&sm.full[i % kStages], (i / kStages) & 1, kTries);
-        __syncwarp();
-      }
+      const int s = n % kStages;
+      if (ok && n >= kStages) ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1);
+      if (ok) arrive(&sm.full[s]);
       ptx::cp_async_wait<0>();
-    } else if (warp == 3) {
+    } else if (warp == 27) {
+      // ------------------------------------------------------------------ the units
+      schedule(sm.units, wait, lane, [&](int block, Unit& u) {
+        const int h = block % p.H;
+        Segment x;
+        if (!find_segment(p, seg, block / p.H, lane == 0 && h == 0, x)) return false;
+        u.lo = (int)x.lo;
+        u.hi = (int)x.hi;
+        u.head = h;
+        u.place = 0;
+        u.entry = !x.first ? added + ((x.place - 1) * p.H + h) * (int64_t)(D * D)
+                  : p.init ? p.init + ((int64_t)x.seq * p.H + h) * (D * D) : nullptr;
+        u.exit = x.last && p.final_state ? p.final_state + ((int64_t)x.seq * p.H + h) * (D * D)
+                                         : nullptr;
+        return x.hi > x.lo || u.exit != nullptr;
+      });
+    } else {
       // ------------------------------------------------------------------ products
       // (loops rolled: unrolled, this role's code alone did not fit the instruction cache)
-      const uint32_t id64 = ptx::idesc_make(ptx::kFmtBF16, 128, kC, false, false);
+      const uint32_t id_o = ptx::idesc_make(ptx::kFmtBF16, 128, kC, false, false);
+      const uint32_t id_sc = ptx::idesc_make(ptx::kFmtBF16, kC, kC, false, false);
       auto issue_qk = [&](int n) {
         const uint32_t st = base + (n % kStages) * M::STAGE;
         if (ptx::elect_one()) {
@@ -418,7 +530,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
 #pragma unroll
             for (uint32_t j = 0; j < 4; ++j)
               ptx::mma_f16(tmem + T::SC, ptx::desc_add(a, i * 8192 + j * 32),
-                           ptx::desc_add(b, i * 8192 + j * 32), id64, i + j > 0);
+                           ptx::desc_add(b, i * 8192 + j * 32), id_sc, i + j > 0);
           ptx::mma_commit(&sm.sc_full);
         }
         __syncwarp();
@@ -437,7 +549,13 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
           ptx::mma_commit(&sm.kv_done);
         }
         __syncwarp();
-        if (n > 0 && !wait(&sm.o_empty, ph ^ 1)) break;
+        const bool more = take(n + 1, c);
+        if (more) {  // (once this chunk's have been read)
+          if (!wait(&sm.sc_empty, ph)) break;
+          ptx::tc_fence_after();
+          issue_qk(n + 1);
+        }
+        if (n == 0 ? !wait(&sm.hi_full, 0) : !wait.all({&sm.hi_full, &sm.o_empty}, {ph, ph ^ 1})) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           const uint64_t b = ptx::sdesc_sw128(st + M::Q, 16, 1024);
@@ -446,24 +564,18 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
 #pragma unroll
             for (uint32_t j = 0; j < 4; ++j)
               ptx::mma_f16_ts(tmem + T::OI, tmem + T::HI + i * 32 + j * 8,
-                              ptx::desc_add(b, i * 8192 + j * 32), id64, i + j > 0);
+                              ptx::desc_add(b, i * 8192 + j * 32), id_o, i + j > 0);
           ptx::mma_commit(&sm.sq_done);
           ptx::mma_commit(&sm.empty[s]);
         }
         __syncwarp();
-        const bool more = take(n + 1, c);
-        if (more) {
-          if (!wait(&sm.sc_empty, ph)) break;
-          ptx::tc_fence_after();
-          issue_qk(n + 1);
-        }
-        if (!wait.all({&sm.p_full, &sm.vt_full}, {ph, ph})) break;
+        if (!wait.all({&sm.p_full[ph], &sm.vt_full}, {(uint32_t)(n >> 1) & 1, ph})) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           const uint64_t b = ptx::sdesc_sw128(base + M::P + ph * 8192, 16, 1024);
 #pragma unroll
           for (uint32_t i = 0; i < kC / 16; ++i)
-            ptx::mma_f16_ts(tmem + T::OA, tmem + T::VT + i * 8, ptx::desc_add(b, i * 32), id64, i > 0);
+            ptx::mma_f16_ts(tmem + T::OA, tmem + T::VT + i * 8, ptx::desc_add(b, i * 32), id_o, i > 0);
           ptx::mma_commit(&sm.o_full);
           ptx::mma_commit(&sm.p_empty[ph]);
         }
@@ -476,220 +588,236 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
         ptx::mbar_wait_tries(&sm.drain, 0, kTries);
         __syncwarp();
       }
-    } else if (warp >= 16) {
-      // ------------------------------------------------------------------ V and V', transposed
-      const int w = warp & 3, tok = ((warp - 16) >> 2) * 32;  // 32 channels, half of the tokens
-      if (w < NQ) {
-        const uint32_t lanes = (uint32_t)(w * 32) << 16;
-        Chunk c;
+    }
+  } else if (warp >= 16) {
+    ptx::regs_give<64>();
+    // ------------------------------------------------------------------ V and V', transposed
+    const int w = warp & 3, tok = ((warp - 16) >> 2) * 32;  // 32 channels, half of the tokens
+    if (w < NQ) {
+      const uint32_t lanes = (uint32_t)(w * 32) << 16;
+      Chunk c;
 #pragma unroll 1
-        for (int n = 0; take(n, c); ++n) {
-          const int s = n % kStages, m = c.tokens;
-          const uint32_t st = base + s * M::STAGE;
-          const float2 total = sm.total[s];
-          ptx::f32x2 weight[4];
-          uint32_t raw[2][8];
-          load_vt(st + M::V, w * 32, tok, lane, raw[0]);
-          load_vt(st + M::V, w * 32 + 16, tok, lane, raw[1]);
+      for (int n = 0; take(n, c); ++n) {
+        const int s = n % kStages, m = c.tokens;
+        const uint32_t st = base + s * M::STAGE;
+        const float2 total = sm.total[s];
+        ptx::f32x2 weight[4];
+        uint32_t raw[2][8];
+        load_vt(st + M::V, w * 32, tok, lane, raw[0]);
+        load_vt(st + M::V, w * 32 + 16, tok, lane, raw[1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = tok + i * 8 + 2 * (lane & 3);
+          const float2 h2 = *reinterpret_cast<const float2*>(&sm.ghi[s][t]);
+          const float2 l2 = *reinterpret_cast<const float2*>(&sm.glo[s][t]);
+          weight[i] = ptx::pack2(ptx::ex2_approx((total.x - h2.x) + (total.y - l2.x)),
+                                 ptx::ex2_approx((total.x - h2.y) + (total.y - l2.y)));
+        }
+        if (m < kC) {  // rows of the next sequence, whatever they hold: zeros, in K too
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = tok + i * 8 + 2 * (lane & 3);
+            const uint32_t keep = (t < m ? 0xffffu : 0u) | (t + 1 < m ? 0xffff0000u : 0u);
+            raw[0][2 * i] &= keep;
+            raw[0][2 * i + 1] &= keep;
+            raw[1][2 * i] &= keep;
+            raw[1][2 * i + 1] &= keep;
+          }
+          for (int i = (warp - 16) / 4 * (NQ * 32) + w * 32 + lane; i < kC * D / 8;
+               i += 2 * NQ * 32)
+            if (i / (D / 8) >= m) st_shared(st + M::K + tile_at<D>(i), make_uint4(0u, 0u, 0u, 0u));
+          ptx::fence_proxy_async_smem();
+        }
+        arrive(&sm.empty[s]);
+        if (n > 0 && !wait(&sm.kv_done, (n - 1) & 1)) break;
+        ptx::tc_fence_after();
+#pragma unroll 1
+        for (int b = 0; b < 2; ++b) {
+          uint32_t part[3][8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t x[3];
+            weigh3(b ? raw[1][i] : raw[0][i], weight[i >> 1], x);
+            part[0][i] = x[0];
+            part[1][i] = x[1];
+            part[2][i] = x[2];
+          }
+#pragma unroll
+          for (int j = 0; j < 3; ++j)
+            ptx::tmem_st_rows16_nowait(
+                tmem + lanes + ((uint32_t)(b * 16) << 16) + T::VP + j * 32 + tok / 2, part[j]);
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        arrive(&sm.v_full);
+        if (n > 0 && !wait(&sm.o_full, (n - 1) & 1)) break;
+        ptx::tc_fence_after();
+        ptx::tmem_st_rows16_nowait(tmem + lanes + T::VT + tok / 2, raw[0]);
+        ptx::tmem_st_rows16_nowait(tmem + lanes + (16u << 16) + T::VT + tok / 2, raw[1]);
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        arrive(&sm.vt_full);
+      }
+    }
+  } else if (warp >= 12) {
+    ptx::regs_give<64>();
+    // ------------------------------------------------------------------ outputs
+    const int w = warp - 12;
+    if (w < NQ) {
+      const int tid = w * 32 + lane;
+      const uint32_t stage = base + M::O + (w >> 1) * 8192;  // its block of 64 channels
+      const uint32_t t_o = tmem + ((uint32_t)(w * 32) << 16);
+      const ptx::f32x2 scale = ptx::pack2(p.scale, p.scale);
+      Chunk c;
+#pragma unroll 1
+      for (int n = 0;; ++n) {
+        const int s = n % kStages;
+        bool ok = wait(&sm.full[s], (n / kStages) & 1);
+        if (ok) {
+          c = sm.chunk[s];
+          ok = __shfl_sync(0xffffffffu, c.kind, 0) != kStop && wait(&sm.o_full, n & 1);
+        }
+        if (tid == 0) ptx::bulk_wait_read0();  // the last chunk's rows have left
+        ok = group_and(1, NQ * 32, ok);
+        if (!ok) break;
+        ptx::tc_fence_after();
+#pragma unroll 1
+        for (int tok = 0; tok < kC; tok += 32) {
+          ptx::f32x2 ee[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int t = tok + i * 8 + 2 * (lane & 3);
             const float2 h2 = *reinterpret_cast<const float2*>(&sm.ghi[s][t]);
             const float2 l2 = *reinterpret_cast<const float2*>(&sm.glo[s][t]);
-            weight[i] = ptx::pack2(ptx::ex2_approx((total.x - h2.x) + (total.y - l2.x)),
-                                   ptx::ex2_approx((total.x - h2.y) + (total.y - l2.y)));
+            ee[i] = ptx::pack2(ptx::ex2_approx(h2.x + l2.x), ptx::ex2_approx(h2.y + l2.y));
           }
-          if (m < kC) {  // rows of the next sequence, whatever they hold: zeros, in K too
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int t = tok + i * 8 + 2 * (lane & 3);
-              const uint32_t keep = (t < m ? 0xffffu : 0u) | (t + 1 < m ? 0xffff0000u : 0u);
-              raw[0][2 * i] &= keep;
-              raw[0][2 * i + 1] &= keep;
-              raw[1][2 * i] &= keep;
-              raw[1][2 * i + 1] &= keep;
-            }
-            for (int i = (warp - 16) / 4 * (NQ * 32) + w * 32 + lane; i < kC * D / 8;
-                 i += 2 * NQ * 32)
-              if (i / (D / 8) >= m) st_shared(st + M::K + tile_at<D>(i), make_uint4(0u, 0u, 0u, 0u));
-            ptx::fence_proxy_async_smem();
-          }
-          arrive(&sm.empty[s]);
-          if (n > 0 && !wait(&sm.kv_done, (n - 1) & 1)) break;
-          ptx::tc_fence_after();
 #pragma unroll 1
-          for (int b = 0; b < 2; ++b) {
-            uint32_t part[3][8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              uint32_t x[3];
-              weigh3(b ? raw[1][i] : raw[0][i], weight[i >> 1], x);
-              part[0][i] = x[0];
-              part[1][i] = x[1];
-              part[2][i] = x[2];
-            }
-#pragma unroll
-            for (int j = 0; j < 3; ++j)
-              ptx::tmem_st_rows16_nowait(
-                  tmem + lanes + ((uint32_t)(b * 16) << 16) + T::VP + j * 32 + tok / 2, part[j]);
-          }
-          ptx::tmem_st_wait();
-          ptx::tc_fence_before();
-          arrive(&sm.v_full);
-          if (n > 0 && !wait(&sm.o_full, (n - 1) & 1)) break;
-          ptx::tc_fence_after();
-          ptx::tmem_st_rows16_nowait(tmem + lanes + T::VT + tok / 2, raw[0]);
-          ptx::tmem_st_rows16_nowait(tmem + lanes + (16u << 16) + T::VT + tok / 2, raw[1]);
-          ptx::tmem_st_wait();
-          ptx::tc_fence_before();
-          arrive(&sm.vt_full);
-        }
-      }
-    } else if (warp >= 12) {
-      // ------------------------------------------------------------------ outputs
-      const int w = warp - 12;
-      if (w < NQ) {
-        const int tid = w * 32 + lane;
-        const uint32_t stage = base + M::O + (w >> 1) * 8192;  // its block of 64 channels
-        const uint32_t t_o = tmem + ((uint32_t)(w * 32) << 16);
-        const ptx::f32x2 scale = ptx::pack2(p.scale, p.scale);
-        Chunk c;
-#pragma unroll 1
-        for (int n = 0;; ++n) {
-          const int s = n % kStages;
-          bool ok = wait(&sm.full[s], (n / kStages) & 1);
-          if (ok) {
-            c = sm.chunk[s];
-            ok = __shfl_sync(0xffffffffu, c.kind, 0) != kStop && wait(&sm.o_full, n & 1);
-          }
-          if (tid == 0) ptx::bulk_wait_read0();  // the last chunk's rows have left
-          ok = group_and(1, NQ * 32, ok);
-          if (!ok) break;
-          ptx::tc_fence_after();
-#pragma unroll 1
-          for (int tok = 0; tok < kC; tok += 32) {
-            ptx::f32x2 ee[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int t = tok + i * 8 + 2 * (lane & 3);
-              const float2 h2 = *reinterpret_cast<const float2*>(&sm.ghi[s][t]);
-              const float2 l2 = *reinterpret_cast<const float2*>(&sm.glo[s][t]);
-              ee[i] = ptx::pack2(ptx::ex2_approx(h2.x + l2.x), ptx::ex2_approx(h2.y + l2.y));
-            }
-#pragma unroll 1
-            for (uint32_t ch0 = 0; ch0 < 32; ch0 += 16) {  // 16 channels x 32 tokens
-              uint32_t x[16], y[16];
-              ptx::tmem_ld_frag32_nowait(t_o + (ch0 << 16) + T::OI + tok, x);
-              ptx::tmem_ld_frag32_nowait(t_o + (ch0 << 16) + T::OA + tok, y);
-              ptx::tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[i]), "+r"(y[i]));
-              uint32_t o[8];
-#pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                const ptx::f32x2 inter =
-                    ptx::pack2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-                const ptx::f32x2 intra =
-                    ptx::pack2(__uint_as_float(y[j]), __uint_as_float(y[j + 1]));
-                float y0, y1;
-                ptx::unpack2(ptx::mul2(ptx::fma2(ee[j >> 2], inter, intra), scale), y0, y1);
-                o[j >> 1] = pack_bf16(y0, y1);
-              }
-              // matrices (channels 0-7, 8-15) x (two groups of 8 tokens): row = token
-              const int ch = ((w & 1) * 32 + (int)ch0) / 8 + ((lane >> 3) & 1);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int t = tok + i * 16 + (lane >> 4) * 8 + (lane & 7);
-                ptx::st_matrix4_trans(stage + t * 128 + ((ch ^ (t & 7)) << 4), o[4 * i], o[4 * i + 1],
-                                      o[4 * i + 2], o[4 * i + 3]);
-              }
-            }
-          }
-          ptx::tc_fence_before();
-          arrive(&sm.o_empty);
-          if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
-          ptx::fence_proxy_async_smem();
-          group_and(1, NQ * 32, true);
-          if (c.tokens >= kC) {
-            if (tid == 0) {
-#pragma unroll
-              for (int i = 0; i < D / 64; ++i)
-                ptx::tma_store_2d(&maps.o, smem + M::O + i * 8192, c.head * D + i * 64, c.t0);
-              ptx::bulk_commit();
-            }
-          } else {  // the rows after the segment belong to another one
-            for (int i = tid; i < c.tokens * (D / 8); i += NQ * 32) {
-              const int t = c.t0 + i / (D / 8);
-              *reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + ((int64_t)t * p.H + c.head) * D +
-                                        i % (D / 8) * 8) = ld_shared(base + M::O + tile_at<D>(i));
-            }
-          }
-        }
-        if (tid == 0) ptx::bulk_wait0();
-      }
-    } else {
-      // ------------------------------------------------------------------ P (warps 0, 1)
-      const int w = warp, i = w * 32 + lane;  // the row
-      const uint32_t lanes = (uint32_t)(w * 32) << 16;
-      Chunk c;
-#pragma unroll 1
-      for (int n = 0; take(n, c); ++n) {
-        const int s = n % kStages;
-        if (!wait(&sm.sc_full, n & 1) ||
-            (n >= 2 && !wait(&sm.p_empty[n & 1], ((n >> 1) - 1) & 1)))
-          break;
-        ptx::tc_fence_after();
-        const ptx::f32x2 gh = ptx::pack2(sm.ghi[s][i], sm.ghi[s][i]),
-                         gl = ptx::pack2(sm.glo[s][i], sm.glo[s][i]), minus = ptx::pack2(-1.0f, -1.0f);
-#pragma unroll 1
-        for (int c0 = 0; c0 < kC; c0 += 16) {
-          uint32_t o[8];
-          if (c0 < 32 * w + 32) {
-            uint32_t r[16];
-            ptx::tmem_ld16_nowait(tmem + lanes + T::SC + c0, r);
+          for (uint32_t ch0 = 0; ch0 < 32; ch0 += 16) {  // 16 channels x 32 tokens
+            uint32_t x[16], y[16];
+            ptx::tmem_ld_frag32_nowait(t_o + (ch0 << 16) + T::OI + tok, x);
+            ptx::tmem_ld_frag32_nowait(t_o + (ch0 << 16) + T::OA + tok, y);
             ptx::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(r[j]));
-            if (c0 == 32 * w + 16) {  // all of them read
-              ptx::tc_fence_before();
-              arrive(&sm.sc_empty);
-            }
+            for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[i]), "+r"(y[i]));
+            uint32_t o[8];
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
-              const float2 h2 = *reinterpret_cast<const float2*>(&sm.ghi[s][c0 + j]);
-              const float2 l2 = *reinterpret_cast<const float2*>(&sm.glo[s][c0 + j]);
-              float d0, d1;
-              ptx::unpack2(ptx::add2(ptx::fma2(ptx::pack2(h2.x, h2.y), minus, gh),
-                                     ptx::fma2(ptx::pack2(l2.x, l2.y), minus, gl)),
-                           d0, d1);
-              const ptx::f32x2 y =
-                  ptx::mul2(ptx::pack2(ptx::ex2_approx(d0), ptx::ex2_approx(d1)),
-                            ptx::pack2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])));
+              const ptx::f32x2 inter =
+                  ptx::pack2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+              const ptx::f32x2 intra =
+                  ptx::pack2(__uint_as_float(y[j]), __uint_as_float(y[j + 1]));
               float y0, y1;
-              ptx::unpack2(y, y0, y1);
-              y0 = c0 + j <= i ? y0 : 0.0f;
-              y1 = c0 + j < i ? y1 : 0.0f;
+              ptx::unpack2(ptx::mul2(ptx::fma2(ee[j >> 2], inter, intra), scale), y0, y1);
               o[j >> 1] = pack_bf16(y0, y1);
             }
-          } else {
+            // matrices (channels 0-7, 8-15) x (two groups of 8 tokens): row = token
+            const int ch = ((w & 1) * 32 + (int)ch0) / 8 + ((lane >> 3) & 1);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = 0u;
-          }
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            st_shared(base + M::P + (n & 1) * 8192 + i * 128 + ((((c0 >> 3) + b) ^ (i & 7)) << 4),
-                      make_uint4(o[4 * b], o[4 * b + 1], o[4 * b + 2], o[4 * b + 3]));
+            for (int i = 0; i < 2; ++i) {
+              const int t = tok + i * 16 + (lane >> 4) * 8 + (lane & 7);
+              ptx::st_matrix4_trans(stage + t * 128 + ((ch ^ (t & 7)) << 4), o[4 * i], o[4 * i + 1],
+                                    o[4 * i + 2], o[4 * i + 3]);
+            }
           }
         }
-        ptx::fence_proxy_async_smem();
-        arrive(&sm.p_full);
+        ptx::tc_fence_before();
+        arrive(&sm.o_empty);
         if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
+        ptx::fence_proxy_async_smem();
+        group_and(1, NQ * 32, true);
+        if (c.tokens >= kC) {
+          if (tid == 0) {
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i)
+              ptx::tma_store_2d(&maps.o, smem + M::O + i * 8192, c.head * D + i * 64, c.t0);
+            ptx::bulk_commit();
+          }
+        } else {  // the rows after the segment belong to another one
+          for (int i = tid; i < c.tokens * (D / 8); i += NQ * 32) {
+            const int t = c.t0 + i / (D / 8);
+            *reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + ((int64_t)t * p.H + c.head) * D +
+                                      i % (D / 8) * 8) = ld_shared(base + M::O + tile_at<D>(i));
+          }
+        }
       }
+      if (tid == 0) ptx::bulk_wait0();
+    }
+  } else {
+    ptx::regs_give<64>();
+    // ------------------------------------------------------------------ P (warps 0 .. 3)
+    // The scores are a product with M = 64: rows 16 w .. 16 w + 15 are in the first lanes of
+    // quarter w. A lane has two columns of every eight of rows g and g + 8.
+    const int w = warp, g = lane >> 2, t4 = lane & 3;
+    const uint32_t t_sc = tmem + ((uint32_t)(w * 32) << 16) + T::SC;
+    // columns that the rows never reach stay zeros
+    for (int i = lane; i < 2 * 16 * 4; i += 32) {
+      const int row = w * 16 + (i >> 2 & 15);
+      st_shared(base + M::P + (i >> 6) * 8192 + row * 128 + (((4 + (i & 3)) ^ (row & 7)) << 4),
+                make_uint4(0u, 0u, 0u, 0u));
+    }
+    __syncwarp();
+    const ptx::f32x2 minus = ptx::pack2(-1.0f, -1.0f);
+    Chunk c;
+#pragma unroll 1
+    for (int n = 0; take(n, c); ++n) {
+      const int s = n % kStages;
+      if (!wait(&sm.sc_full, n & 1) || (n >= 2 && !wait(&sm.p_empty[n & 1], ((n >> 1) - 1) & 1)))
+        break;
+      ptx::tc_fence_after();
+      const int row = w * 16 + g;
+      const ptx::f32x2 gh[2] = {ptx::pack2(sm.ghi[s][row], sm.ghi[s][row]),
+                                ptx::pack2(sm.ghi[s][row + 8], sm.ghi[s][row + 8])};
+      const ptx::f32x2 gl[2] = {ptx::pack2(sm.glo[s][row], sm.glo[s][row]),
+                                ptx::pack2(sm.glo[s][row + 8], sm.glo[s][row + 8])};
+#pragma unroll 1
+      for (int c0 = 0; c0 <= w * 16; c0 += 32) {
+        uint32_t r[16];
+        ptx::tmem_ld_frag32_nowait(t_sc + c0, r);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(r[j]));
+        if (c0 + 32 > w * 16) {  // all of them read
+          ptx::tc_fence_before();
+          arrive(&sm.sc_empty);
+        }
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int col = c0 + 8 * i + 2 * t4;
+          const float2 h2 = *reinterpret_cast<const float2*>(&sm.ghi[s][col]);
+          const float2 l2 = *reinterpret_cast<const float2*>(&sm.glo[s][col]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float d0, d1, y0, y1;
+            ptx::unpack2(ptx::add2(ptx::fma2(ptx::pack2(h2.x, h2.y), minus, gh[e]),
+                                   ptx::fma2(ptx::pack2(l2.x, l2.y), minus, gl[e])),
+                         d0, d1);
+            ptx::unpack2(ptx::mul2(ptx::pack2(ptx::ex2_approx(d0), ptx::ex2_approx(d1)),
+                                   ptx::pack2(__uint_as_float(r[4 * i + 2 * e]),
+                                              __uint_as_float(r[4 * i + 2 * e + 1]))),
+                         y0, y1);
+            y0 = col <= row + 8 * e ? y0 : 0.0f;
+            y1 = col < row + 8 * e ? y1 : 0.0f;
+            o[2 * i + e] = pack_bf16(y0, y1);
+          }
+        }
+        // matrices (rows 0-7, 8-15) x (two groups of 8 columns)
+        const int at = w * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int blk = c0 / 8 + 2 * i + (lane >> 4);
+          ptx::st_matrix4(base + M::P + (n & 1) * 8192 + at * 128 + ((blk ^ (at & 7)) << 4), o[4 * i],
+                          o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      }
+      ptx::fence_proxy_async_smem();
+      arrive(&sm.p_full[n & 1]);
+      if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
     }
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 3) ptx::tmem_dealloc(tmem, 512);
+  if (warp == 25) ptx::tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------- what a segment adds
@@ -704,6 +832,7 @@ struct Add {
   static constexpr int SMALL = STAGES * STAGE;
 };
 struct AddSmall {
+  UnitRing units;
   uint64_t full[8], empty[8];
   uint64_t v_full[2], v_empty[2], acc_full[2], acc_empty[2], drain;
   float w[8][kC];
@@ -713,13 +842,12 @@ struct AddSmall {
   uint32_t tmem;
   int abort;
 };
-constexpr int kLast = 4;           // a kind: ends a unit
-constexpr int kAddThreads = 704;  // 16 + 2 + 4 warps
+constexpr int kAddThreads = 768;  // 16 + 2 + 4 + 2 warps
 
 template <int D>
 __global__ void __launch_bounds__(kAddThreads, 1)
-decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg, int slots,
-                 float* added, float* added_log) {
+decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg, float* added,
+                 float* added_log) {
   using M = Add<D>;
   constexpr int NQ = D / 32, kStages = M::STAGES;
   constexpr int VP = 256;  // TMEM: two sums in turn, then two sets of three parts of V'
@@ -733,6 +861,11 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
       ptx::mbar_init(&sm.full[i], 2);
       ptx::mbar_init(&sm.empty[i], 1 + 4 * NQ + NQ);
     }
+    for (int i = 0; i < kUnits; ++i) {
+      ptx::mbar_init(&sm.units.full[i], 1);
+      ptx::mbar_init(&sm.units.empty[i], 2);
+    }
+    ptx::mbar_init(&sm.units.clc, 1);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sm.v_full[i], 2 * NQ);
       ptx::mbar_init(&sm.v_empty[i], 1);
@@ -764,32 +897,56 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
   };
 
   if (warp == 16) {
-    // ------------------------------------------------------------------ loads and decays
+    // ------------------------------------------------------------------ loads
     int n = 0;
+    uint32_t unit = 0;
+    Unit u;
     bool ok = true;
 #pragma unroll 1
-    for (int unit = blockIdx.x; ok && unit < slots * p.H; unit += gridDim.x) {
-      const int h = unit % p.H;
-      Segment x;
-      if (!find_segment(p, seg, unit / p.H, false, x) || x.last) continue;
-      const int hk = h / (p.H / p.Hk);
-      const DecayRing ring{sm.g, p.g + h, p.gs, lane};
-      auto first = [&](int i) { return (int)x.lo + (N - 1 - i) * kC; };
-      auto ask = [&](int i) { ring.ask(i, i < N ? first(i) : 0, i < N ? first(i) + kC : 0); };
+    while (ok && next_unit(sm.units, wait, lane, unit, u)) {
+      const int hk = u.head / (p.H / p.Hk);
+#pragma unroll 1
+      for (int i = 0; i < N; ++i, ++n) {
+        const int s = n % kStages, t = u.lo + (N - 1 - i) * kC;
+        if (n >= kStages && !(ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1))) break;
+        if (lane == 0) {
+          uint8_t* st = smem + s * M::STAGE;
+          sm.kind[s] = (i == 0 ? kFirst : 0) | (i == N - 1 ? kLast : 0);
+          sm.out[s] = u.exit;
+          ptx::mbar_arrive_expect_tx(&sm.full[s], M::STAGE);
+          load_tile<D>(st + M::V, &maps.v, &sm.full[s], u.head, t);
+          load_tile<D>(st + M::K, &maps.k, &sm.full[s], hk, t);
+        }
+      }
+    }
+    const int s = n % kStages;
+    if (ok && n >= kStages) ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1);
+    if (ok && lane == 0) {
+      sm.kind[s] = kStop;
+      ptx::mbar_arrive(&sm.full[s]);
+    }
+    if (*(volatile int*)&sm.abort) {  // the loads in flight land before the CTA leaves
+      __nanosleep(1000000);
+      __syncwarp();
+    }
+  } else if (warp == 22) {
+    // ------------------------------------------------------------------ sums of the decays
+    int n = 0;
+    uint32_t unit = 0;
+    Unit u;
+    bool ok = true;
+#pragma unroll 1
+    while (ok && next_unit(sm.units, wait, lane, unit, u)) {
+      const DecayRing ring{sm.g, p.g + u.head, p.gs, lane};
+      auto ask = [&](int i) {
+        const int t = i < N ? u.lo + (N - 1 - i) * kC : 0;
+        ring.ask(i, t, i < N ? t + kC : 0);
+      };
       for (int i = 0; i < kAhead; ++i) ask(i);
       float2 later = make_float2(0.0f, 0.0f);
 #pragma unroll 1
       for (int i = 0; i < N; ++i, ++n) {
         const int s = n % kStages;
-        if (n >= kStages && !(ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1))) break;
-        if (lane == 0) {
-          uint8_t* st = smem + s * M::STAGE;
-          ptx::mbar_arrive_expect_tx(&sm.full[s], M::STAGE);
-          load_tile<D>(st + M::V, &maps.v, &sm.full[s], h, first(i));
-          load_tile<D>(st + M::K, &maps.k, &sm.full[s], hk, first(i));
-          sm.kind[s] = (i == 0 ? kFirst : 0) | (i == N - 1 ? kLast : 0);
-          sm.out[s] = added + (x.place * p.H + h) * (int64_t)(D * D);
-        }
         const float2 g = ring.take(i);
         const bool nan = __any_sync(0xffffffffu, g.x != g.x || g.y != g.y);
         const float2 second = log_pair(g.y);
@@ -801,23 +958,29 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
         float wa = ptx::ex2_approx(a.x + a.y), wb = ptx::ex2_approx(b.x + b.y);
         if (nan) wa = wb = nan_f();
         later = upto;
+        if (n >= kStages && !(ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1))) break;
         *reinterpret_cast<float2*>(&sm.w[s][2 * lane]) = make_float2(wa, wb);
         arrive(&sm.full[s]);
       }
-      if (lane == 0) added_log[x.place * p.H + h] = later.x;
+      if (lane == 0) added_log[u.place] = later.x;
     }
-    if (ok && n >= kStages) ok = wait(&sm.empty[n % kStages], ((n / kStages) - 1) & 1);
-    if (ok && lane == 0) {
-      sm.kind[n % kStages] = kStop;
-      ptx::mbar_arrive(&sm.full[n % kStages]);
-      ptx::mbar_arrive(&sm.full[n % kStages]);
-    }
-    if (*(volatile int*)&sm.abort) {
-      for (int i = n > kStages ? n - kStages : 0; i < n; ++i)
-        ptx::mbar_wait_tries(&sm.full[i % kStages], (i / kStages) & 1, kTries);
-      __syncwarp();
-    }
+    const int s = n % kStages;
+    if (ok && n >= kStages) ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1);
+    if (ok) arrive(&sm.full[s]);
     ptx::cp_async_wait<0>();
+  } else if (warp == 23) {
+    // ------------------------------------------------------------------ the units
+    schedule(sm.units, wait, lane, [&](int block, Unit& u) {
+      Segment x;
+      if (!find_segment(p, seg, block / p.H, false, x) || x.last) return false;
+      u.lo = (int)x.lo;
+      u.hi = (int)x.hi;
+      u.head = block % p.H;
+      u.place = (int)(x.place * p.H) + u.head;
+      u.entry = nullptr;
+      u.exit = added + (int64_t)u.place * (D * D);
+      return true;
+    });
   } else if (warp == 17) {
     // ------------------------------------------------------------------ products
     int kind;
@@ -938,24 +1101,22 @@ kda_status launch_d(const DecayParams& p, int seg, float* added, float* added_lo
   constexpr int out_bytes = Out<D>::SMALL + (int)sizeof(OutSmall);
   constexpr int add_bytes = Add<D>::SMALL + (int)sizeof(AddSmall);
   static_assert(out_bytes <= 232448 && add_bytes <= 232448, "shared memory");
-  static int sms_of[64] = {};  // by device: SMs, once the kernels are set up there
-  int dev = 0, sms = 0;
+  static bool set[64] = {};
+  int dev = 0;
   cudaGetDevice(&dev);
-  if (dev >= 0 && dev < 64) sms = sms_of[dev];
-  if (sms == 0) {
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (dev < 0 || dev >= 64 || !set[dev]) {
     cudaFuncSetAttribute(decay_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, out_bytes);
     cudaFuncSetAttribute(decay_add_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, add_bytes);
-    if (dev >= 0 && dev < 64) sms_of[dev] = sms;
+    if (dev >= 0 && dev < 64) set[dev] = true;
   }
   const int slots = p.total / seg + p.n_seqs;
-  const unsigned grid = (unsigned)(slots * p.H < sms ? slots * p.H : sms);
   if (p.total > seg) {
-    decay_add_kernel<D><<<grid, kAddThreads, add_bytes, s>>>(m, p, seg, slots, added, added_log);
+    decay_add_kernel<D><<<(unsigned)(slots * p.H), kAddThreads, add_bytes, s>>>(m, p, seg, added,
+                                                                               added_log);
     launch_decay_scan(p, D, seg, added, added_log, s);
     count_launches(1);
   }
-  decay_tc_kernel<D><<<grid, kThreads, out_bytes, s>>>(m, p, seg, slots, added);
+  decay_tc_kernel<D><<<(unsigned)(slots * p.H), kThreads, out_bytes, s>>>(m, p, seg, added);
   count_launches(1);
   return check_launch("kda_decay_prefill");
 }

@@ -300,6 +300,32 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(const uint64_t* p, uint32_t r
   return v;
 }
 
+// ---------------------------------------------------------------- cluster launch control
+// Asks for a block of this grid that has not been launched, to run it here: 16 bytes at `response`
+// (16-byte aligned), which complete on `bar` as transaction bytes.
+__device__ __forceinline__ void clc_try_cancel(void* response, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+      ::"r"(smem_u32(response)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// The first block's x index of the response, -1 where there was none left.
+__device__ __forceinline__ int clc_block(const void* response) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, r;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(response))
+      : "memory");
+  return ok ? (int)x : -1;
+}
+
 // ---------------------------------------------------------------- tcgen05
 // Allocates `ncols` TMEM columns (power of two >= 32); the base address lands in *dst.
 // Whole-warp instruction.
@@ -517,6 +543,13 @@ __device__ __forceinline__ void st_matrix4_trans(uint32_t addr, uint32_t a, uint
                : "memory");
 }
 
+// The same, stored as they are: row j of matrix m (16 bytes) to the address of lane 8 m + j.
+__device__ __forceinline__ void st_matrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                           uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a),
+               "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
 // Four 8 x 8 matrices of 16-bit elements, loaded transposed: lane 8 m + j gives the address of row j
 // (16 bytes) of matrix m; a lane gets, of each, column lane / 4 of rows 2 t and 2 t + 1.
 __device__ __forceinline__ void ld_matrix4_trans(uint32_t addr, uint32_t* r) {
