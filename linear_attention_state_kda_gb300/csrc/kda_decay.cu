@@ -152,7 +152,7 @@ decay_chunk_kernel(const DecayParams p, int seg, float* added, float* added_log)
   float st[RPT][4];
   const float* entry = nullptr;
   if (!kStates)
-    entry = !x.first ? added + ((x.place - 1) * p.H + h) * (int64_t)(D * D)
+    entry = !x.first ? added + ((int64_t)(x.place - 1) * p.H + h) * (D * D)
             : p.init ? p.init + ((int64_t)x.seq * p.H + h) * (D * D) : nullptr;
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
@@ -285,7 +285,7 @@ decay_chunk_kernel(const DecayParams p, int seg, float* added, float* added_log)
   }
   float* exit_state = nullptr;
   if (kStates) {
-    exit_state = added + (x.place * p.H + h) * (int64_t)(D * D);
+    exit_state = added + ((int64_t)x.place * p.H + h) * (D * D);
     if (tid == 0 && blockIdx.z == 0) added_log[x.place * p.H + h] = log_sum.x;
   } else if (x.last && p.final_state) {
     exit_state = p.final_state + ((int64_t)x.seq * p.H + h) * (D * D);

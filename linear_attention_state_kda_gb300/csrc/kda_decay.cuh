@@ -17,33 +17,35 @@ namespace decay {
 
 struct Segment {
   int seq;
-  int64_t lo, hi;      // tokens
-  int64_t place;       // of the state that it adds; the entry state is in place - 1
+  int lo, hi;          // tokens
+  int place;           // of the state that it adds; the entry state is in place - 1
   bool first, last;    // of its sequence
 };
 
-// The segment in a slot; false: none. `flag`: report malformed offsets.
+// The segment in a slot; false: none. `flag`: report malformed offsets. (Offsets are at most 2^30, so
+// that 32 bits do; a negative one is malformed.)
 __device__ __forceinline__ bool find_segment(const DecayParams& p, int seg, int slot, bool flag,
                                              Segment& x) {
   int a = 0, b = p.n_seqs - 1;  // the last sequence whose first slot is <= slot
   if (p.cu) {
     while (a < b) {
       const int m = (a + b + 1) >> 1;
-      if ((int64_t)p.cu[m] / seg + m <= slot) a = m;
+      if (p.cu[m] / seg + m <= slot) a = m;
       else b = m - 1;
     }
   }
-  int64_t c0 = p.cu ? p.cu[a] : 0, c1 = p.cu ? p.cu[a + 1] : p.total;
-  const int64_t j = slot - (c0 / seg + a);
+  int c0 = p.cu ? p.cu[a] : 0, c1 = p.cu ? p.cu[a + 1] : p.total;
+  const int j = slot - (c0 / seg + a);
   if (j < 0) return false;
   if (c0 < 0 || c1 > p.total || c1 < c0) {
     if (flag && p.status) atomicOr(p.status, KDA_STATUS_BAD_OFFSETS);
     if (j > 0) return false;
     c0 = c1 = 0;  // an empty sequence
   }
+  if (j > (c1 - c0) / seg) return false;
   x.seq = a;
   x.lo = c0 + j * seg;
-  x.hi = x.lo + seg < c1 ? x.lo + seg : c1;
+  x.hi = c1 - x.lo > seg ? x.lo + seg : c1;
   x.first = j == 0;
   x.last = x.hi == c1;
   x.place = c0 / seg + j;

@@ -178,11 +178,11 @@ struct DecayRing {
   int64_t stride;
   int lane;
   // Asks for the tokens from t0 on (those at or after t_end count as 0); every call is a group.
-  __device__ __forceinline__ void ask(int n, int64_t t0, int64_t t_end) const {
+  __device__ __forceinline__ void ask(int n, int t0, int t_end) const {
     float* dst = &ring[n % kAhead][2 * lane];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int64_t t = t0 + 2 * lane + i;
+      const int t = t0 + 2 * lane + i;
       if (t < t_end) ptx::cp_async4(dst + i, g + t * stride);
       else dst[i] = 0.0f;
     }
@@ -206,31 +206,22 @@ __device__ __forceinline__ void load_vt(uint32_t v, int ch, int tok, int lane, u
 }
 __device__ __forceinline__ float nan_f() { return __int_as_float(0x7fffffff); }
 
-// What every role needs to wait: gives up after kTries or when another role did.
+// What every role needs to wait: gives up after kTries or when another role did. (The roles' code has
+// to stay within the instruction cache: the caller's status is set once, at the kernel's end.)
 struct Waiter {
   int* abort;
-  uint32_t* status;
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    const bool done = ptx::mbar_wait_tries_or(bar, parity, kTries, abort);
-    if (__all_sync(0xffffffffu, done)) return true;
-    if (status) atomicOr(status, KDA_STATUS_TIMEOUT);
-    *(volatile int*)abort = 1;
-    return false;
+    const bool done =
+        __all_sync(0xffffffffu, ptx::mbar_wait_short(bar, parity, kTries, abort));
+    if (!done) *(volatile int*)abort = 1;
+    return done;
   }
-  // Of several barriers: they are looked at together first, since a look takes some 200 cycles beside
-  // the traffic of the products.
-  template <int N>
-  __device__ __forceinline__ bool all(uint64_t* const (&bar)[N], const uint32_t (&parity)[N]) const {
-    bool seen[N], every = true;
-#pragma unroll
-    for (int i = 0; i < N; ++i) seen[i] = ptx::mbar_test(bar[i], parity[i]);
-#pragma unroll
-    for (int i = 0; i < N; ++i) every = every && seen[i];
-    if (__all_sync(0xffffffffu, every)) return true;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (!(*this)(bar[i], parity[i])) return false;
-    return true;
+  // Of two barriers, which are looked at together: a look takes some 200 cycles beside the traffic of
+  // the products.
+  __device__ __forceinline__ bool both(uint64_t* a, uint32_t parity_a, uint64_t* b,
+                                       uint32_t parity_b) const {
+    const bool ra = ptx::mbar_test(a, parity_a), rb = ptx::mbar_test(b, parity_b);
+    return __all_sync(0xffffffffu, ra && rb) || ((*this)(a, parity_a) && (*this)(b, parity_b));
   }
 };
 // The scheduling warp. find(block, unit): the unit of a block; false where it has none.
@@ -340,7 +331,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
   const uint32_t base = ptx::smem_u32(smem);
-  const Waiter wait{&sm.abort, p.status};
+  const Waiter wait{&sm.abort};
   auto arrive = [&](uint64_t* bar) {  // of a warp, after all its lanes
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(bar);
@@ -371,37 +362,50 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
         ptx::tc_fence_after();
         c = sm.chunk[s];
         const int kind = __shfl_sync(0xffffffffu, c.kind, 0);
-        if ((kind & (kFirst | kStop)) && exit_state) {  // the unit before ends
+        if (kind & (kFirst | kStop)) {
+          // the unit before ends: its state goes out, and the next one's comes in
+          if (exit_state) {
 #pragma unroll 1
-          for (int b = 0; b < D / 2; b += 32) {
-            float f[32];
-            ptx::tmem_ld32(t_s + b, f);
+            for (int b = 0; b < D / 2; b += 16) {
+              uint32_t f[16];
+              ptx::tmem_ld16_nowait(t_s + b, f);
+              ptx::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) exit_state[at + (b + i) * D] = f[i];
+              for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(f[i]));
+#pragma unroll
+              for (int i = 0; i < 16; ++i) exit_state[at + (b + i) * D] = __uint_as_float(f[i]);
+            }
           }
+          if (kind == kStop) break;
+#pragma unroll 1
+          for (int b = 0; b < D / 2; b += 16) {
+            float f[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[i] = c.entry ? __ldg(c.entry + at + (b + i) * D) : 0.0f;
+            ptx::tmem_st16(t_s + b, f);
+          }
+          ptx::tmem_st_wait();
         }
-        if (kind == kStop) break;
         exit_state = c.exit;
         const float a = ptx::ex2_approx(sm.total[s].x + sm.total[s].y);
         const ptx::f32x2 aa = ptx::pack2(a, a);
         // decayed first, which is what the next sum waits for
-        float r[D / 64][16];
+        float r[D / 32][8];
 #pragma unroll
-        for (int b = 0; b < D / 64; ++b) {
-          float f[32];
-          if (kind & kFirst) {
+        for (int b = 0; b < D / 32; ++b) {
+          uint32_t f[16];
+          ptx::tmem_ld16_nowait(t_s + b * 16, f);
+          ptx::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              f[i] = c.entry ? __ldg(c.entry + at + (b * 32 + i) * D) : 0.0f;
-          } else {
-            ptx::tmem_ld32(t_s + b * 32, f);
+          for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(f[i]));
+          float y[16];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float lo = __uint_as_float(f[2 * i]), hi = __uint_as_float(f[2 * i + 1]);
+            r[b][i] = __uint_as_float(pack_bf16(lo, hi));
+            ptx::unpack2(ptx::mul2(ptx::pack2(lo, hi), aa), y[2 * i], y[2 * i + 1]);
           }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            r[b][i] = __uint_as_float(pack_bf16(f[2 * i], f[2 * i + 1]));
-            ptx::unpack2(ptx::mul2(ptx::pack2(f[2 * i], f[2 * i + 1]), aa), f[2 * i], f[2 * i + 1]);
-          }
-          ptx::tmem_st32_nowait(t_s + b * 32, f);
+          ptx::tmem_st16(t_s + b * 16, y);
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
@@ -409,7 +413,12 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
         if (n > 0 && !wait(&sm.sq_done, (n - 1) & 1)) break;
         ptx::tc_fence_after();
 #pragma unroll
-        for (int b = 0; b < D / 64; ++b) ptx::tmem_st16(t_part + T::HI + b * 16, r[b]);
+        for (int b = 0; b < D / 32; b += 2) {
+          float h[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) h[i] = r[b + i / 8][i % 8];
+          ptx::tmem_st16(t_part + T::HI + b * 8, h);
+        }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         arrive(&sm.hi_full);
@@ -475,7 +484,8 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
 #pragma unroll 1
       while (ok && next_unit(sm.units, wait, lane, unit, u)) {
         const DecayRing ring{sm.g, p.g + u.head, p.gs, lane};
-        for (int i = 0; i < kAhead; ++i) ring.ask(i, u.lo + (int64_t)i * kC, u.hi);
+#pragma unroll 1
+        for (int i = 0; i < kAhead; ++i) ring.ask(i, u.lo + i * kC, u.hi);
         int i = 0;
 #pragma unroll 1
         do {
@@ -484,7 +494,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
           const bool nan = __any_sync(0xffffffffu, g.x != g.x || g.y != g.y);
           const float2 second = log_pair(g.y);
           float2 b = log_scan(log_add(log_pair(g.x), second), lane), a = log_sub(b, second);
-          ring.ask(i + kAhead, u.lo + (int64_t)(i + kAhead) * kC, u.hi);
+          ring.ask(i + kAhead, u.lo + (i + kAhead) * kC, u.hi);
           if (nan) a.x = b.x = nan_f();  // a NaN decay spoils its chunk
           if (n >= kStages && !(ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1))) break;
           *reinterpret_cast<float2*>(&sm.ghi[s][2 * lane]) = make_float2(a.x, b.x);
@@ -493,7 +503,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
           arrive(&sm.full[s]);
           ++n;
           ++i;
-        } while (u.lo + (int64_t)i * kC < u.hi);
+        } while (u.lo + i * kC < u.hi);
       }
       const int s = n % kStages;
       if (ok && n >= kStages) ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1);
@@ -509,7 +519,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
         u.hi = (int)x.hi;
         u.head = h;
         u.place = 0;
-        u.entry = !x.first ? added + ((x.place - 1) * p.H + h) * (int64_t)(D * D)
+        u.entry = !x.first ? added + ((int64_t)(x.place - 1) * p.H + h) * (D * D)
                   : p.init ? p.init + ((int64_t)x.seq * p.H + h) * (D * D) : nullptr;
         u.exit = x.last && p.final_state ? p.final_state + ((int64_t)x.seq * p.H + h) * (D * D)
                                          : nullptr;
@@ -542,7 +552,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
       for (int n = 0; ok; ++n) {
         const int s = n % kStages;
         const uint32_t st = base + s * M::STAGE, ph = n & 1;
-        if (!wait.all({&sm.s_full, &sm.v_full}, {ph, ph})) break;
+        if (!wait.both(&sm.s_full, ph, &sm.v_full, ph)) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           issue_kv<D>(tmem + T::S, tmem + T::VP, st + M::K, false);
@@ -555,7 +565,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
           ptx::tc_fence_after();
           issue_qk(n + 1);
         }
-        if (n == 0 ? !wait(&sm.hi_full, 0) : !wait.all({&sm.hi_full, &sm.o_empty}, {ph, ph ^ 1})) break;
+        if (n == 0 ? !wait(&sm.hi_full, 0) : !wait.both(&sm.hi_full, ph, &sm.o_empty, ph ^ 1)) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           const uint64_t b = ptx::sdesc_sw128(st + M::Q, 16, 1024);
@@ -569,7 +579,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
           ptx::mma_commit(&sm.empty[s]);
         }
         __syncwarp();
-        if (!wait.all({&sm.p_full[ph], &sm.vt_full}, {(uint32_t)(n >> 1) & 1, ph})) break;
+        if (!wait.both(&sm.p_full[ph], (n >> 1) & 1, &sm.vt_full, ph)) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           const uint64_t b = ptx::sdesc_sw128(base + M::P + ph * 8192, 16, 1024);
@@ -817,6 +827,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
   }
   ptx::tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && sm.abort && p.status) atomicOr(p.status, KDA_STATUS_TIMEOUT);
   if (warp == 25) ptx::tmem_dealloc(tmem, 512);
 }
 
@@ -885,7 +896,7 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
   const uint32_t base = ptx::smem_u32(smem);
-  const Waiter wait{&sm.abort, p.status};
+  const Waiter wait{&sm.abort};
   auto arrive = [&](uint64_t* bar) {
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(bar);
@@ -942,6 +953,7 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
         const int t = i < N ? u.lo + (N - 1 - i) * kC : 0;
         ring.ask(i, t, i < N ? t + kC : 0);
       };
+#pragma unroll 1
       for (int i = 0; i < kAhead; ++i) ask(i);
       float2 later = make_float2(0.0f, 0.0f);
 #pragma unroll 1
@@ -976,7 +988,7 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
       u.lo = (int)x.lo;
       u.hi = (int)x.hi;
       u.head = block % p.H;
-      u.place = (int)(x.place * p.H) + u.head;
+      u.place = x.place * p.H + u.head;
       u.entry = nullptr;
       u.exit = added + (int64_t)u.place * (D * D);
       return true;
@@ -1084,6 +1096,7 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
   }
   ptx::tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && sm.abort && p.status) atomicOr(p.status, KDA_STATUS_TIMEOUT);
   if (warp == 17) ptx::tmem_dealloc(tmem, 512);
 }
 

@@ -132,6 +132,28 @@ __device__ __forceinline__ bool mbar_wait_tries_or(uint64_t* bar, uint32_t parit
   }
   return false;
 }
+// mbar_wait_tries_or as one block of ten instructions, for kernels with very many waits.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, uint32_t tries,
+                                                const int* abort) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n, x;\n\t"
+      "mov.u32 n, %3;\n\t"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "ld.volatile.shared.u32 x, [%4];\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "setp.eq.and.u32 q, x, 0, q;\n\t"
+      "@q bra AGAIN;\n\t"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(tries), "r"(smem_u32(abort))
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool mbar_wait_relaxed_or(uint64_t* bar, uint32_t parity,
                                                      const int* abort,
                                                      uint64_t limit_ns = 2000000000ull) {
