@@ -1695,6 +1695,18 @@ bool make_map_tokens(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t ro
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_map_pages(CUtensorMap* m, const void* ptr, uint64_t d, uint64_t slices) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)kPage, (cuuint64_t)slices};
+  cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)(d * kPage)};
+  cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)kPage, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 kda_status launch_chunk_tc(const ChunkParams& p, kda_dtype dt, void* workspace, size_t ws_bytes,
                            cudaStream_t s, int phases) {
   (void)dt;

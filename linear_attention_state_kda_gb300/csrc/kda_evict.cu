@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kWThreads) weigh_kernel(const WeighParams p, i
         for (int e = 0; e < 4; ++e) {
           const int64_t pos = pos0 + g + 8 * (e >> 1);
           acc[i][e] = pos < vis[i][e & 1]
-                          ? acc[i][e] * ks * row_mul[i * 8 + t4 * 2 + (e & 1)] : -INFINITY;
+                          ? acc[i][e] * (ks * row_mul[i * 8 + t4 * 2 + (e & 1)]) : -INFINITY;
         }
     };
 
@@ -595,6 +595,8 @@ __global__ void __launch_bounds__(kMThreads) evict_move_kernel(const EvictParams
 }  // namespace
 
 kda_status launch_cache_weigh(const WeighParams& p, kda_dtype dt, int d, cudaStream_t s) {
+  if (dt == KDA_BF16 && d == 128 && (int64_t)p.window * (p.Hq / p.Hkv) > 64)
+    return launch_cache_weigh_tc(p, s);
   if (dt == KDA_BF16)
     return d == 128 ? launch_weigh_t<128, 1, __nv_bfloat16>(p, s)
                     : launch_weigh_t<64, 1, __nv_bfloat16>(p, s);

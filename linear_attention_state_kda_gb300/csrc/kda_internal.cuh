@@ -78,6 +78,9 @@ bool make_map_rows(CUtensorMap* m, const void* ptr, bool f32, uint64_t cols, uin
 // 2-D tensor map, box [box_rows][box_cols], plain or with the 128-byte swizzle (box_cols 64).
 bool make_map_tokens(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows,
                      uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows, bool swizzle);
+// The codes of a paged cache, [slices = n_pages * Hkv][64][d = 128] bytes, box one slice, with the
+// 128-byte swizzle.
+bool make_map_pages(CUtensorMap* m, const void* ptr, uint64_t d, uint64_t slices);
 // phases: kPhasePrep writes the records, kPhaseState walks them; both = one chunked call.
 // kPhaseFlags (with kPhaseState alone) makes the walk wait for each record's ready flag in
 // the workspace, as the fused launch's walk does (the flag-wait diagnostic).
@@ -235,6 +238,8 @@ struct WeighParams {
   uint32_t* status;
 };
 kda_status launch_cache_weigh(const WeighParams& p, kda_dtype dt, int d, cudaStream_t s);
+// bf16 at d = 128 with more than 64 query rows per key/value head: on the tensor cores' 8-bit path.
+kda_status launch_cache_weigh_tc(const WeighParams& p, cudaStream_t s);
 struct EvictParams {
   int batch, Hkv;
   const int32_t* length;

@@ -1,0 +1,460 @@
+// Weights of cached tokens for windows of many queries (bf16, d = 128, more than 64 query rows per
+// key/value head): the end of a prompt weighing the whole of it.
+//
+//     weight[t] = keep * weight[t] + sum_i 2^(x_it - lse_i),   x_it = scale log2(e) q_i . k_t
+//
+// A cluster owns one (row, key/value head), its CTAs contiguous ranges of its pages. Twice over its
+// keys, 256 query rows at a time: first the rows' statistics, then, once the cluster has joined them,
+// the sums over the rows. Both times the products are tcgen05 kind::f8f6f4 on the codes as they lie
+// (TMA), with the operands swapped: the first has a query row per accumulator lane, so that running
+// maximum and sum stay in one thread; the second a key per lane, so that the sum over rows does.
+//
+// A query row enters as three 8-bit parts: x = q / 2^e in [-448, 448], e4m3(x), e4m3 of the rest, and
+// e5m2 of the rest of that. bf16 has 8 significant bits, two e4m3 parts hold 8 where their exponents
+// reach; the third brings the error of entries below 2^-11 of the row's largest to 2^-22 of it.
+//
+// Bound by the exponentials (two for each query row and key, 16 a cycle and SM), then by the products
+// (three parts).
+#include "kda_internal.cuh"
+#include "kda_fp8.cuh"
+#include "ptx.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int D = 128;
+constexpr int kRows = 256;          // query rows at a time
+constexpr int kTile = 128;          // keys of a step: two pages
+constexpr int kStages = 4;
+constexpr int kParts = 3;
+constexpr int kThreads = 384;       // loads, products, two idle; 8 warps of exponentials
+constexpr uint32_t kTries = 1u << 19;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Smem {
+  static constexpr int Q = 0;                               // [part][row tile][128 rows][128 B]
+  static constexpr int K = Q + kParts * kRows * D;          // [stage][128 keys][128 B]
+  static constexpr int SMALL = K + kStages * kTile * D;
+};
+struct Small {
+  uint64_t full[kStages], empty[kStages], d_full[2], d_empty[2], drain;
+  float ks[kStages][2];             // of a step's pages; 0 where there is none
+  int page[kStages][2];             // -1: none
+  alignas(16) float2 ml[kRows];     // statistics of this CTA's keys
+  alignas(16) float2 row[kRows];    // scale log2(e) 2^e, and minus lse
+  float part[2][kTile];             // sums over the second half of the rows
+  uint32_t tmem;
+  int abort;
+};
+
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, int* abort) {
+  const bool done = __all_sync(0xffffffffu, ptx::mbar_wait_short(bar, parity, kTries, abort));
+  if (!done) *(volatile int*)abort = 1;
+  return done;
+}
+__device__ __forceinline__ uint32_t e5m2x2_from_f32(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(const float2* p, uint32_t rank) {
+  const uint64_t v = ptx::ld_cluster_u64(reinterpret_cast<const uint64_t*>(p), rank);
+  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, int cs) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Small& sm = *reinterpret_cast<Small*>(smem + Smem::SMALL);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % cs, bh = blockIdx.x / cs;
+  const int b = bh / p.Hkv, h = bh - b * p.Hkv;
+  const int start = p.start[b];
+  int n = start < 0 ? 0 : p.lens ? p.lens[b] : p.window;
+  n = n < 0 ? 0 : n > p.window ? p.window : n;
+  if (n == 0) return;  // the whole cluster
+  const int G = p.Hq / p.Hkv, R = n * G;
+  const int64_t most = (int64_t)p.max_pages * kPage;
+  const int64_t keys = (int64_t)start + n < most ? (int64_t)start + n : most;
+  if (rank == 0 && threadIdx.x == 0 && h == 0 && p.status && (int64_t)start + n > most)
+    atomicOr(p.status, KDA_STATUS_BAD_PAGE);
+  // steps of two pages; a contiguous range of them for each CTA
+  const int steps = (int)((keys + kTile - 1) / kTile);
+  const int per = (steps + cs - 1) / cs;
+  const int s0 = min(steps, rank * per), s1 = min(steps, s0 + per);
+  const int32_t* table = p.table + (int64_t)b * p.max_pages;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      ptx::mbar_init(&sm.full[i], 1);
+      ptx::mbar_init(&sm.empty[i], 1 + 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&sm.d_full[i], 1);
+      ptx::mbar_init(&sm.d_empty[i], 8);
+    }
+    ptx::mbar_init(&sm.drain, 1);
+    ptx::fence_mbar_init();
+    sm.abort = 0;
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&sm.tmem, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
+  const uint32_t base = ptx::smem_u32(smem);
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_all(bar, parity, &sm.abort); };
+
+  int step = 0;  // steps of both passes and all groups so far: stages and accumulators take turns
+  for (int r0 = 0; r0 < R; r0 += kRows) {
+    const int rows = min(kRows, R - r0);
+    const int tiles = rows > 128 ? 2 : 1;
+    // the group's query rows: a warp takes a row, a lane four channels
+    for (int r = warp; r < tiles * 128; r += kThreads / 32) {
+      const int at = r0 + r, j = at / G;
+      float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (r < rows) {
+        const uint2 v = *reinterpret_cast<const uint2*>(
+            (const __nv_bfloat16*)p.q +
+            (((int64_t)b * p.window + j) * p.Hq + h * G + (at - j * G)) * D + lane * 4);
+        f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
+        f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
+      }
+      uint32_t m = 0;
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        m = max(m, finite_abs_bits(f[i]));
+        bad |= !(fabsf(f[i]) < INFINITY);
+      }
+      m = __reduce_max_sync(0xffffffffu, m);
+      bad = __any_sync(0xffffffffu, bad);
+      // 2^e, the smallest power of two with m <= 448 2^e (e >= -100: smaller rows count as zeros
+      // below 2^-109 of an entry)
+      const int e = scale_exponent(m);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] *= pow2f(-e);
+      const uint32_t off = base + Smem::Q + (r >> 7) * (128 * D) + (r & 127) * D +
+                           (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+#pragma unroll
+      for (int part = 0; part < kParts; ++part) {
+        uint32_t code;
+        if (part < 2) {
+          const uint32_t lo = e4m3x2_from_f32(f[0], f[1]), hi = e4m3x2_from_f32(f[2], f[3]);
+          const float2 a = f32x2_from_f16x2(f16x2_from_e4m3(lo));
+          const float2 c = f32x2_from_f16x2(f16x2_from_e4m3(hi));
+          f[0] -= a.x; f[1] -= a.y; f[2] -= c.x; f[3] -= c.y;
+          code = lo | hi << 16;
+        } else {
+          code = e5m2x2_from_f32(f[0], f[1]) | e5m2x2_from_f32(f[2], f[3]) << 16;
+        }
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(off + part * (kRows * D)), "r"(code) : "memory");
+      }
+      // a row with an infinity or NaN has no weights but NaN; one past the last adds nothing
+      if (lane == 0)
+        sm.row[r] = make_float2(
+            bad ? __int_as_float(0x7fffffff) : p.scale * kLog2e * pow2f(e), 0.0f);
+    }
+    ptx::fence_proxy_async_smem();
+    __syncthreads();
+    // positions that some row of the group sees
+    const int64_t seen = (int64_t)start + (r0 + rows - 1) / G + 1;
+    const int last = (int)min((int64_t)s1, (seen + kTile - 1) / kTile);
+    const int count = last > s0 ? last - s0 : 0;  // steps of a pass
+
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      if (warp == 0) {
+        // ---------------------------------------------------------------- loads
+        int id = -1;  // of page 2 i + lane, and its scale, 16 steps ahead
+        float ks = 0.0f;
+#pragma unroll 1
+        for (int i = 0; i < count; ++i) {
+          const int at = step + i, s = at % kStages, from = (i & 15) * 2;
+          if (from == 0) {
+            const int pg = (s0 + i) * 2 + lane;
+            // (a step's second page also where no row of this group sees it: its weights begin here)
+            id = (int64_t)pg * kPage < keys && pg < 2 * s1 ? table[pg] : -1;
+            if (id >= p.n_pages) {
+              if (p.status) atomicOr(p.status, KDA_STATUS_BAD_PAGE);
+              id = -1;
+            }
+            ks = id < 0 ? 0.0f : p.ks[(int64_t)id * p.Hkv + h];
+          }
+          const int a = __shfl_sync(0xffffffffu, id, from), c = __shfl_sync(0xffffffffu, id, from + 1);
+          const float ka = __shfl_sync(0xffffffffu, ks, from), kc = __shfl_sync(0xffffffffu, ks, from + 1);
+          if (at >= kStages && !wait(&sm.empty[s], ((at / kStages) - 1) & 1)) break;
+          if (lane == 0) {
+            sm.page[s][0] = a < 0 ? -1 : a;
+            sm.page[s][1] = c < 0 ? -1 : c;
+            sm.ks[s][0] = ka;
+            sm.ks[s][1] = kc;
+            uint8_t* dst = smem + Smem::K + s * (kTile * D);
+            ptx::mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(((a >= 0) + (c >= 0)) * kPage * D));
+            if (a >= 0) ptx::tma_load_3d(dst, &map, &sm.full[s], 0, 0, a * p.Hkv + h);
+            if (c >= 0) ptx::tma_load_3d(dst + kPage * D, &map, &sm.full[s], 0, 0, c * p.Hkv + h);
+          }
+          __syncwarp();
+        }
+      } else if (warp == 1) {
+        // ---------------------------------------------------------------- products
+        for (int i = 0; i < count; ++i) {
+          const int at = step + i, s = at % kStages, buf = at & 1;
+          if (!wait(&sm.full[s], (at / kStages) & 1) ||
+              (at >= 2 && !wait(&sm.d_empty[buf], ((at >> 1) - 1) & 1)))
+            break;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            const uint64_t k = ptx::sdesc_sw128(base + Smem::K + s * (kTile * D), 16, 1024);
+            const uint64_t q = ptx::sdesc_sw128(base + Smem::Q, 16, 1024);
+            const uint32_t d = tmem + buf * kRows;
+#pragma unroll 1
+            for (int part = 0; part < kParts; ++part) {
+              const uint32_t fmt = part < 2 ? ptx::kFmtE4M3 : ptx::kFmtE5M2;
+              if (pass == 0) {
+                const uint32_t id = ptx::idesc_make2(fmt, ptx::kFmtE4M3, 128, kTile);
+                for (int t = 0; t < tiles; ++t)
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    ptx::mma_f8(d + t * kTile, ptx::desc_add(q, part * (kRows * D) + t * 128 * D + j * 32),
+                                ptx::desc_add(k, j * 32), id, part + j > 0);
+              } else {
+                const uint32_t id = ptx::idesc_make2(ptx::kFmtE4M3, fmt, 128, (uint32_t)tiles * 128);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  ptx::mma_f8(d, ptx::desc_add(k, j * 32), ptx::desc_add(q, part * (kRows * D) + j * 32),
+                              id, part + j > 0);
+              }
+            }
+            ptx::mma_commit(&sm.empty[s]);
+            ptx::mma_commit(&sm.d_full[buf]);
+          }
+          __syncwarp();
+        }
+      } else if (warp >= 4) {
+        // ---------------------------------------------------------------- exponentials
+        const int w = warp & 3, g = (warp - 4) >> 2;
+        const uint32_t lanes = (uint32_t)(w * 32) << 16;
+        if (pass == 0) {
+          // a query row: row tile g, lane
+          const int r = g * 128 + w * 32 + lane;
+          const float c = g < tiles ? sm.row[r].x : 0.0f;
+          const int64_t vis = r < rows ? min(keys, (int64_t)start + (r0 + r) / G + 1) : 0;
+          float m = -INFINITY, l = 0.0f;
+          for (int i = 0; i < count; ++i) {
+            const int at = step + i, s = at % kStages, buf = at & 1;
+            if (!wait(&sm.d_full[buf], (at >> 1) & 1)) break;
+            ptx::tc_fence_after();
+            if (g < tiles) {
+              const int64_t pos0 = (int64_t)(s0 + i) * kTile;
+#pragma unroll 1
+              for (int q4 = 0; q4 < 4; ++q4) {  // 32 keys
+                float x[32];
+                ptx::tmem_ld32(tmem + lanes + buf * kRows + g * kTile + q4 * 32, x);
+                const float f = c * sm.ks[s][q4 >> 1];
+                const int64_t left = sm.page[s][q4 >> 1] < 0 ? 0 : vis - (pos0 + q4 * 32);
+                const ptx::f32x2 ff = ptx::pack2(f, f);
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 32; j += 2)
+                  ptx::unpack2(ptx::mul2(ptx::pack2(x[j], x[j + 1]), ff), x[j], x[j + 1]);
+                if (__any_sync(0xffffffffu, left < 32)) {
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) x[j] = j < left ? x[j] : -INFINITY;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) top = fmaxf(top, fmaxf(x[j], x[j + 1]));
+                if (top > m) {
+                  l *= ptx::ex2_approx(m - top);
+                  m = top;
+                }
+                const float mm = m == -INFINITY ? 0.0f : m;
+                const ptx::f32x2 nm = ptx::pack2(-mm, -mm);
+                ptx::f32x2 sum = ptx::pack2(0.0f, 0.0f);
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                  float a, e;
+                  ptx::unpack2(ptx::add2(ptx::pack2(x[j], x[j + 1]), nm), a, e);
+                  sum = ptx::add2(sum, ptx::pack2(ptx::ex2_approx(a), ptx::ex2_approx(e)));
+                }
+                float a, e;
+                ptx::unpack2(sum, a, e);
+                l += a + e;
+              }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              ptx::mbar_arrive(&sm.d_empty[buf]);
+              ptx::mbar_arrive(&sm.empty[s]);
+            }
+          }
+          if (g < tiles) sm.ml[r] = make_float2(m, l);
+        } else {
+          // a key: half g of the query rows
+          for (int i = 0; i < count; ++i) {
+            const int at = step + i, s = at % kStages, buf = at & 1;
+            const bool ok = wait(&sm.d_full[buf], (at >> 1) & 1);
+            ptx::tc_fence_after();
+            const int64_t pos0 = (int64_t)(s0 + i) * kTile, pos = pos0 + w * 32 + lane;
+            const int id = sm.page[s][w >> 1];
+            const float ks = sm.ks[s][w >> 1];
+            const ptx::f32x2 kk = ptx::pack2(ks, ks);
+            // rows from `from` on see this key
+            const int64_t hidden = (pos - start) * G - r0;
+            const int from = pos >= keys ? kRows : hidden > 0 ? (int)min(hidden, (int64_t)kRows) : 0;
+            const bool all = __all_sync(0xffffffffu, from == 0);
+            ptx::f32x2 sum = ptx::pack2(0.0f, 0.0f);
+            if (ok && g < tiles) {
+#pragma unroll 1
+              for (int q4 = 0; q4 < 4; ++q4) {  // 32 rows
+                float x[32];
+                ptx::tmem_ld32(tmem + lanes + buf * kRows + g * 128 + q4 * 32, x);
+                const int rr = g * 128 + q4 * 32;
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                  // (c, -lse) of two rows
+                  const float4 t = *reinterpret_cast<const float4*>(&sm.row[rr + j]);
+                  float a, e;
+                  ptx::unpack2(ptx::fma2(ptx::pack2(x[j], x[j + 1]),
+                                         ptx::mul2(ptx::pack2(t.x, t.z), kk), ptx::pack2(t.y, t.w)),
+                               a, e);
+                  a = ptx::ex2_approx(a);
+                  e = ptx::ex2_approx(e);
+                  if (!all) {
+                    a = rr + j >= from ? a : 0.0f;
+                    e = rr + j + 1 >= from ? e : 0.0f;
+                  }
+                  sum = ptx::add2(sum, ptx::pack2(a, e));
+                }
+              }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              ptx::mbar_arrive(&sm.d_empty[buf]);
+              ptx::mbar_arrive(&sm.empty[s]);
+            }
+            float a, e;
+            ptx::unpack2(sum, a, e);
+            a += e;
+            if (g == 1) sm.part[at & 1][w * 32 + lane] = a;
+            // both halves' warps of these keys
+            asm volatile("bar.sync %0, 64;" ::"r"(2 + w) : "memory");
+            if (g == 0 && ok && id >= 0 && pos < keys) {
+              a += sm.part[at & 1][w * 32 + lane];
+              float* wp = p.weights + ((int64_t)id * p.Hkv + h) * kPage + (pos & (kPage - 1));
+              const float old = r0 > 0 ? *wp : pos < start && p.keep != 0.0f ? p.keep * *wp : 0.0f;
+              *wp = old + a;
+            }
+          }
+          // (a part is written again two steps on, behind the next step's barrier)
+          if (r0 == 0 && g == 0) {
+            // positions that the window holds, but no row of this group sees, begin at zero
+            for (int i = count; s0 + i < s1; ++i) {
+              const int64_t pos = (int64_t)(s0 + i) * kTile + w * 32 + lane;
+              const int pg = (int)(pos / kPage);
+              const int id = pos < keys ? table[pg] : -1;
+              if (id >= 0 && id < p.n_pages) {
+                float* wp = p.weights + ((int64_t)id * p.Hkv + h) * kPage + (pos & (kPage - 1));
+                *wp = pos < start && p.keep != 0.0f ? p.keep * *wp : 0.0f;
+              }
+            }
+          }
+        }
+      }
+      step += count;
+      if (pass == 0) {
+        // the rows' statistics over the cluster
+        __syncwarp();
+        ptx::cluster_sync();
+        if (warp >= 4) {
+          const int r = threadIdx.x - 128;
+          if (r < tiles * 128) {
+            float m = -INFINITY;
+            for (int c = 0; c < cs; ++c) m = fmaxf(m, ld_cluster_f2(&sm.ml[r], c).x);
+            const float mm = m == -INFINITY ? 0.0f : m;
+            float l = 0.0f;
+            for (int c = 0; c < cs; ++c) {
+              const float2 v = ld_cluster_f2(&sm.ml[r], c);
+              l += v.y * exp2f(v.x - mm);
+            }
+            // a row that sees nothing adds nothing
+            const bool none = m == -INFINITY && !(l != l);
+            sm.row[r].y = r >= rows || none ? -INFINITY : -(mm + log2f(l));
+            if (r >= rows || none) sm.row[r].x = 0.0f;
+          }
+        }
+        __syncwarp();
+        ptx::cluster_sync();
+      } else {
+        __syncthreads();
+      }
+    }
+  }
+  if (warp == 1 && __any_sync(0xffffffffu, *(volatile int*)&sm.abort)) {
+    if (ptx::elect_one()) ptx::mma_commit(&sm.drain);
+    __syncwarp();
+    ptx::mbar_wait_tries(&sm.drain, 0, kTries);
+    __syncwarp();
+  }
+  if (warp == 0 && *(volatile int*)&sm.abort) __nanosleep(1000000);  // loads in flight land
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && sm.abort && p.status) atomicOr(p.status, KDA_STATUS_TIMEOUT);
+  if (warp == 1) ptx::tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+kda_status launch_cache_weigh_tc(const WeighParams& p, cudaStream_t s) {
+  CUtensorMap map;
+  if (!chunk_tc_available())
+    return set_error(KDA_ERR_UNSUPPORTED,
+                     "kda_cache_weigh: the CUDA driver does not provide cuTensorMapEncodeTiled, which "
+                     "windows of many queries need");
+  if (!make_map_pages(&map, p.kc, D, (uint64_t)p.n_pages * p.Hkv))
+    return set_error(KDA_ERR_CUDA, "kda_cache_weigh: cuTensorMapEncodeTiled failed");
+  constexpr int bytes = Smem::SMALL + (int)sizeof(Small);
+  static_assert(bytes <= 232448, "shared memory");
+  static bool set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !set[dev]) {
+    cudaFuncSetAttribute(weigh_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaFuncSetAttribute(weigh_tc_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (dev >= 0 && dev < 64) set[dev] = true;
+  }
+  // one CTA per SM: as many to a cluster as fill the SMs
+  const int64_t units = (int64_t)p.batch * p.Hkv;
+  int cs = 1;
+  while (cs < 16 && units * cs < 128 && (int64_t)p.max_pages > 2 * cs) cs *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * cs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cs;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cs == 16) {  // more than the portable eight: where the GPU takes them
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, weigh_tc_kernel, &cfg) != cudaSuccess || clusters < 1) {
+      cudaGetLastError();
+      cs = 8;
+      cfg.gridDim = dim3((unsigned)(units * cs));
+      at[0].val.clusterDim.x = (unsigned)cs;
+    }
+  }
+  cudaLaunchKernelEx(&cfg, weigh_tc_kernel, map, p, cs);
+  count_launches(1);
+  return check_launch("kda_cache_weigh");
+}
+
+}  // namespace kda
