@@ -641,15 +641,21 @@ KDA_API kda_status kda_decay_window(kda_dtype dt, int batch, int window, int H, 
  *               touched. No page may be named by two rows of one call.
  *   A query none of whose positions is present adds nothing. Codes that a query does not see do not
  *   reach its weights, NaN included.
- *   Other arguments, limits and status as for kda_cache_attention. No workspace.
- * Scores and sums are fp32 and the same on every run. bf16 queries enter at full precision, fp32
- * ones as two 11-bit parts.
+ *   workspace   at least kda_cache_weigh_workspace(...) bytes (0 for sizes that are refused or need
+ *               none: up to 64 query rows per key/value head), 256-byte aligned; contents need not be
+ *               initialised.
+ *   Other arguments, limits and status as for kda_cache_attention.
+ * Scores and sums are fp32 and the same on every run. bf16 queries enter at full precision (in windows
+ * of more than 64 query rows per key/value head at d = 128: to 2^-20 of the query's largest entry),
+ * fp32 ones as two 11-bit parts.
  */
+KDA_API size_t kda_cache_weigh_workspace(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d);
 KDA_API kda_status kda_cache_weigh(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d,
                                    float scale, float keep, const void* q, const int32_t* start,
                                    const int32_t* lens, const int32_t* page_table, int max_pages,
                                    const void* k_cache, const float* k_scale, float* weights,
-                                   int64_t n_pages, uint32_t* status, kda_stream_t stream);
+                                   int64_t n_pages, void* workspace, size_t ws_bytes,
+                                   uint32_t* status, kda_stream_t stream);
 
 /*
  * kda_cache_evict: cuts the cached tokens of each row down to a budget, per head, and moves what is

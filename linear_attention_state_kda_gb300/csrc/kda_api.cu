@@ -763,11 +763,19 @@ kda_status kda_decay_window(kda_dtype dt, int batch, int window, int H, int Hk, 
   return launch_decay_window(p, dt, d, (cudaStream_t)stream);
 }
 
+size_t kda_cache_weigh_workspace(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d) {
+  if ((dt != KDA_F32 && dt != KDA_BF16) || batch <= 0 || window <= 0 || window > kMaxAttnWindow ||
+      Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || (d != 64 && d != 128) ||
+      !attn_sizes_ok(batch, window, Hq, Hkv))
+    return 0;
+  return cache_weigh_workspace_bytes(dt, batch, window, Hq, Hkv, d);
+}
+
 kda_status kda_cache_weigh(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d, float scale,
                            float keep, const void* q, const int32_t* start, const int32_t* lens,
                            const int32_t* page_table, int max_pages, const void* k_cache,
-                           const float* k_scale, float* weights, int64_t n_pages, uint32_t* status,
-                           kda_stream_t stream) {
+                           const float* k_scale, float* weights, int64_t n_pages, void* workspace,
+                           size_t ws_bytes, uint32_t* status, kda_stream_t stream) {
   const char* fn = "kda_cache_weigh";
   KDA_REQUIRE(window >= 0 && window <= kMaxAttnWindow, KDA_ERR_UNSUPPORTED,
               "kda_cache_weigh: window must be in 0 .. 65536");
@@ -787,11 +795,16 @@ kda_status kda_cache_weigh(kda_dtype dt, int batch, int window, int Hq, int Hkv,
               "kda_cache_weigh: q, k_cache and weights must be non-null");
   KDA_REQUIRE(aligned(q, 16) && aligned(weights, 16), KDA_ERR_INVALID_ARG,
               "kda_cache_weigh: q and weights must be 16-byte aligned");
+  const size_t need = cache_weigh_workspace_bytes(dt, batch, window, Hq, Hkv, d);
+  KDA_REQUIRE(need == 0 || (workspace && ws_bytes >= need && aligned(workspace, 256)),
+              KDA_ERR_WORKSPACE,
+              "kda_cache_weigh: workspace missing, too small or not 256-byte aligned (need " +
+                  std::to_string(need) + " bytes)");
   WeighParams p{};
   p.batch = batch; p.window = window; p.Hq = Hq; p.Hkv = Hkv; p.scale = scale; p.keep = keep;
   p.q = q; p.start = start; p.lens = lens; p.table = page_table; p.max_pages = max_pages;
   p.n_pages = n_pages; p.kc = (const uint8_t*)k_cache; p.ks = k_scale; p.weights = weights;
-  p.status = status;
+  p.stats = (float2*)workspace; p.status = status;
   return launch_cache_weigh(p, dt, d, (cudaStream_t)stream);
 }
 

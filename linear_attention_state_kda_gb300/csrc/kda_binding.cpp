@@ -611,10 +611,10 @@ float* weights_of(Devices& dv, PyObject* o, int64_t n_pages, int64_t H) {
   return vec<float>(dv, &t, at::kFloat, t.numel(), "weights");
 }
 
-// q, start, page_table, k_cache, k_scale, weights, scale, lens, keep, status, stream
+// q, start, page_table, k_cache, k_scale, weights, scale, lens, keep, workspace, status, stream
 PyObject* cache_weigh(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  count(n, 11);
+  count(n, 12);
   const Tensor &q = need(a[0], "q"), &start = need(a[1], "start");
   Devices dv;
   const int64_t B = start.numel();
@@ -631,16 +631,27 @@ PyObject* cache_weigh(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t* st0 = vec<int32_t>(dv, &start, at::kInt, B, "start");
   float* wp = weights_of(dv, a[5], c.n_pages, c.H);
   const int32_t* lens = vec<int32_t>(dv, opt(a[7], "lens"), at::kInt, B, "lens");
-  uint32_t* status = status_of(dv, a[9]);
+  uint32_t* status = status_of(dv, a[10]);
   dv.check();
   const int b = as_int(B, "batch"), w = as_int(W, "window"), hq = as_int(Hq, "Hq"),
             hkv = as_int(c.H, "Hkv"), d = as_int(c.d, "d");
   const float scale = (float)as_double(a[6]), keep = (float)as_double(a[8]);
-  const CallStream on(a[10]);
+  const CallStream on(a[11]);
+  int64_t bytes = (int64_t)kda_cache_weigh_workspace(dt, b, w, hq, hkv, d);
+  Out ws;
+  void* sp = nullptr;
+  if (bytes > 0 || a[9] != Py_None) {
+    ws.set(a[9], {bytes}, at::TensorOptions().dtype(at::kByte).device(q.device()), "workspace");
+    require(ws.t->is_contiguous(), "must be contiguous", "workspace");
+    dv.see(*ws.t);
+    bytes = (int64_t)ws.t->nbytes();
+    sp = ws.t->data_ptr();
+  }
+  dv.check();
   const kda_status st = [&] {
     NoGil g;
     return kda_cache_weigh(dt, b, w, hq, hkv, d, scale, keep, qp, st0, lens, c.table, c.max_pages,
-                           c.kc, c.ks, wp, c.n_pages, status, on.s);
+                           c.kc, c.ks, wp, c.n_pages, sp, (size_t)bytes, status, on.s);
   }();
   if (st != KDA_OK) return PyLong_FromLong(st);
   Py_INCREF(a[5]);

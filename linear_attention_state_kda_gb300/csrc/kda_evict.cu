@@ -594,9 +594,12 @@ __global__ void __launch_bounds__(kMThreads) evict_move_kernel(const EvictParams
 
 }  // namespace
 
+size_t cache_weigh_workspace_bytes(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d) {
+  return weigh_tc_applies(dt, window, Hq, Hkv, d) ? cache_weigh_tc_workspace(batch, window, Hq, Hkv) : 0;
+}
+
 kda_status launch_cache_weigh(const WeighParams& p, kda_dtype dt, int d, cudaStream_t s) {
-  if (dt == KDA_BF16 && d == 128 && (int64_t)p.window * (p.Hq / p.Hkv) > 64)
-    return launch_cache_weigh_tc(p, s);
+  if (weigh_tc_applies(dt, p.window, p.Hq, p.Hkv, d)) return launch_cache_weigh_tc(p, s);
   if (dt == KDA_BF16)
     return d == 128 ? launch_weigh_t<128, 1, __nv_bfloat16>(p, s)
                     : launch_weigh_t<64, 1, __nv_bfloat16>(p, s);

@@ -3,11 +3,13 @@
 //
 //     weight[t] = keep * weight[t] + sum_i 2^(x_it - lse_i),   x_it = scale log2(e) q_i . k_t
 //
-// A cluster owns one (row, key/value head), its CTAs contiguous ranges of its pages. Twice over its
-// keys, 256 query rows at a time: first the rows' statistics, then, once the cluster has joined them,
-// the sums over the rows. Both times the products are tcgen05 kind::f8f6f4 on the codes as they lie
-// (TMA), with the operands swapped: the first has a query row per accumulator lane, so that running
-// maximum and sum stay in one thread; the second a key per lane, so that the sum over rows does.
+// Two kernels over the keys, 256 query rows at a time: the first takes the rows' statistics (running
+// maximum and sum) of ranges of keys into the workspace, the second joins them and sums the weights
+// over the rows. In both the products are tcgen05 kind::f8f6f4 on the codes as they lie (TMA), with
+// the operands swapped: the first has a query row per accumulator lane, so that maximum and sum stay
+// in one thread; the second a key per lane, so that the sum over the rows does. (One kernel with the
+// statistics joined over a cluster per key/value head measured 117 us on one row of 32k keys and 8
+// heads: clusters of 8 use 64 SMs, and of clusters of 16 only 7 run at once.)
 //
 // A query row enters as three 8-bit parts: x = q / 2^e in [-448, 448], e4m3(x), e4m3 of the rest, and
 // e5m2 of the rest of that. bf16 has 8 significant bits, two e4m3 parts hold 8 where their exponents
@@ -28,6 +30,7 @@ constexpr int kTile = 128;          // keys of a step: two pages
 constexpr int kStages = 4;
 constexpr int kParts = 3;
 constexpr int kThreads = 384;       // loads, products, two idle; 8 warps of exponentials
+constexpr int kSms = 152;           // ranges of keys are made for
 constexpr uint32_t kTries = 1u << 19;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -40,7 +43,6 @@ struct Small {
   uint64_t full[kStages], empty[kStages], d_full[2], d_empty[2], drain;
   float ks[kStages][2];             // of a step's pages; 0 where there is none
   int page[kStages][2];             // -1: none
-  alignas(16) float2 ml[kRows];     // statistics of this CTA's keys
   alignas(16) float2 row[kRows];    // scale log2(e) 2^e, and minus lse
   float part[2][kTile];             // sums over the second half of the rows
   uint32_t tmem;
@@ -57,32 +59,38 @@ __device__ __forceinline__ uint32_t e5m2x2_from_f32(float a, float b) {
   asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
-__device__ __forceinline__ float2 ld_cluster_f2(const float2* p, uint32_t rank) {
-  const uint64_t v = ptx::ld_cluster_u64(reinterpret_cast<const uint64_t*>(p), rank);
-  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
-}
+// How the work is cut: statistics by (unit, 256 rows, range of keys), weights by (unit, range of keys),
+// a unit being a row's key/value head.
+struct Cut {
+  int groups, stat_ranges, ranges;
+};
 
+template <bool kStats>
 __global__ void __launch_bounds__(kThreads, 1)
-weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, int cs) {
+weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, const Cut cut) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Small& sm = *reinterpret_cast<Small*>(smem + Smem::SMALL);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.x % cs, bh = blockIdx.x / cs;
+  const int ranges = kStats ? cut.stat_ranges : cut.ranges;
+  const int range = blockIdx.x % ranges;
+  const int first_group = kStats ? blockIdx.x / ranges % cut.groups : 0;
+  const int bh = kStats ? blockIdx.x / ranges / cut.groups : blockIdx.x / ranges;
   const int b = bh / p.Hkv, h = bh - b * p.Hkv;
   const int start = p.start[b];
   int n = start < 0 ? 0 : p.lens ? p.lens[b] : p.window;
   n = n < 0 ? 0 : n > p.window ? p.window : n;
-  if (n == 0) return;  // the whole cluster
   const int G = p.Hq / p.Hkv, R = n * G;
+  if (first_group * kRows >= R) return;
   const int64_t most = (int64_t)p.max_pages * kPage;
   const int64_t keys = (int64_t)start + n < most ? (int64_t)start + n : most;
-  if (rank == 0 && threadIdx.x == 0 && h == 0 && p.status && (int64_t)start + n > most)
+  if (kStats && range == 0 && first_group == 0 && threadIdx.x == 0 && h == 0 && p.status &&
+      (int64_t)start + n > most)
     atomicOr(p.status, KDA_STATUS_BAD_PAGE);
-  // steps of two pages; a contiguous range of them for each CTA
-  const int steps = (int)((keys + kTile - 1) / kTile);
-  const int per = (steps + cs - 1) / cs;
-  const int s0 = min(steps, rank * per), s1 = min(steps, s0 + per);
   const int32_t* table = p.table + (int64_t)b * p.max_pages;
+  // weights: a contiguous range of steps (two pages each)
+  const int steps = (int)((keys + kTile - 1) / kTile);
+  const int per = (steps + ranges - 1) / ranges;
+  const int w0 = min(steps, range * per), w1 = min(steps, w0 + per);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -108,65 +116,100 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, in
   const uint32_t base = ptx::smem_u32(smem);
   auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_all(bar, parity, &sm.abort); };
 
-  int step = 0;  // steps of both passes and all groups so far: stages and accumulators take turns
-  for (int r0 = 0; r0 < R; r0 += kRows) {
-    const int rows = min(kRows, R - r0);
+  int step = 0;  // steps of all groups so far: stages and accumulators take turns
+  const int last_group = kStats ? first_group + 1 : (R + kRows - 1) / kRows;
+#pragma unroll 1
+  for (int group = first_group; group < last_group; ++group) {
+    const int r0 = group * kRows, rows = min(kRows, R - r0);
     const int tiles = rows > 128 ? 2 : 1;
-    // the group's query rows: a warp takes a row, a lane four channels
-    for (int r = warp; r < tiles * 128; r += kThreads / 32) {
-      const int at = r0 + r, j = at / G;
-      float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (r < rows) {
-        const uint2 v = *reinterpret_cast<const uint2*>(
-            (const __nv_bfloat16*)p.q +
-            (((int64_t)b * p.window + j) * p.Hq + h * G + (at - j * G)) * D + lane * 4);
-        f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
-        f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
-      }
-      uint32_t m = 0;
-      bool bad = false;
+    // positions that some row of the group sees, and the steps that this CTA takes of them
+    const int64_t seen = min(keys, (int64_t)start + (r0 + rows - 1) / G + 1);
+    const int all_steps = (int)((seen + kTile - 1) / kTile);
+    const int stat_per = (all_steps + ranges - 1) / ranges;
+    const int s0 = kStats ? min(all_steps, range * stat_per) : w0;
+    const int s1 = kStats ? min(all_steps, s0 + stat_per) : max(w0, min(w1, all_steps));
+    const int count = s1 - s0;
+    // the group's query rows: a warp takes four at a time, a lane four channels
+    constexpr int kWarps = kThreads / 32;
+#pragma unroll 1
+    for (int q4 = warp; q4 < tiles * 128; q4 += 4 * kWarps) {
+      uint2 v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        m = max(m, finite_abs_bits(f[i]));
-        bad |= !(fabsf(f[i]) < INFINITY);
+        const int r = q4 + i * kWarps, at = r0 + r, j = at / G;
+        v[i] = make_uint2(0u, 0u);
+        if (r < rows)
+          v[i] = *reinterpret_cast<const uint2*>(
+              (const __nv_bfloat16*)p.q +
+              (((int64_t)b * p.window + j) * p.Hq + h * G + (at - j * G)) * D + lane * 4);
       }
-      m = __reduce_max_sync(0xffffffffu, m);
-      bad = __any_sync(0xffffffffu, bad);
-      // 2^e, the smallest power of two with m <= 448 2^e (e >= -100: smaller rows count as zeros
-      // below 2^-109 of an entry)
-      const int e = scale_exponent(m);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] *= pow2f(-e);
-      const uint32_t off = base + Smem::Q + (r >> 7) * (128 * D) + (r & 127) * D +
-                           (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+      for (int i = 0; i < 4; ++i) {
+        const int r = q4 + i * kWarps;
+        if (r >= tiles * 128) break;
+        float f[4] = {__uint_as_float(v[i].x << 16), __uint_as_float(v[i].x & 0xffff0000u),
+                      __uint_as_float(v[i].y << 16), __uint_as_float(v[i].y & 0xffff0000u)};
+        uint32_t m = 0;
+        bool bad = false;
 #pragma unroll
-      for (int part = 0; part < kParts; ++part) {
-        uint32_t code;
-        if (part < 2) {
-          const uint32_t lo = e4m3x2_from_f32(f[0], f[1]), hi = e4m3x2_from_f32(f[2], f[3]);
-          const float2 a = f32x2_from_f16x2(f16x2_from_e4m3(lo));
-          const float2 c = f32x2_from_f16x2(f16x2_from_e4m3(hi));
-          f[0] -= a.x; f[1] -= a.y; f[2] -= c.x; f[3] -= c.y;
-          code = lo | hi << 16;
-        } else {
-          code = e5m2x2_from_f32(f[0], f[1]) | e5m2x2_from_f32(f[2], f[3]) << 16;
+        for (int c = 0; c < 4; ++c) {
+          m = max(m, finite_abs_bits(f[c]));
+          bad |= !(fabsf(f[c]) < INFINITY);
         }
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(off + part * (kRows * D)), "r"(code) : "memory");
+        m = __reduce_max_sync(0xffffffffu, m);
+        bad = __any_sync(0xffffffffu, bad);
+        // 2^e, the smallest power of two with m <= 448 2^e, at least 2^-100
+        const int e = scale_exponent(m);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) f[c] *= pow2f(-e);
+        const uint32_t off = base + Smem::Q + (r >> 7) * (128 * D) + (r & 127) * D +
+                             (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+          uint32_t code;
+          if (part < 2) {
+            const uint32_t lo = e4m3x2_from_f32(f[0], f[1]), hi = e4m3x2_from_f32(f[2], f[3]);
+            const float2 a = f32x2_from_f16x2(f16x2_from_e4m3(lo));
+            const float2 c = f32x2_from_f16x2(f16x2_from_e4m3(hi));
+            f[0] -= a.x; f[1] -= a.y; f[2] -= c.x; f[3] -= c.y;
+            code = lo | hi << 16;
+          } else {
+            code = e5m2x2_from_f32(f[0], f[1]) | e5m2x2_from_f32(f[2], f[3]) << 16;
+          }
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(off + part * (kRows * D)), "r"(code)
+                       : "memory");
+        }
+        // a row with an infinity or NaN has no weights but NaN
+        if (lane == 0)
+          sm.row[r].x = bad ? __int_as_float(0x7fffffff) : p.scale * kLog2e * pow2f(e);
       }
-      // a row with an infinity or NaN has no weights but NaN; one past the last adds nothing
-      if (lane == 0)
-        sm.row[r] = make_float2(
-            bad ? __int_as_float(0x7fffffff) : p.scale * kLog2e * pow2f(e), 0.0f);
+    }
+    float lse = 0.0f;
+    bool none = false;  // a row past the last, or that sees nothing, adds nothing
+    const int mine = (int)threadIdx.x - 128;
+    if (!kStats && mine >= 0 && mine < tiles * 128) {
+      const float2* ml =
+          p.stats + ((int64_t)bh * cut.groups + group) * cut.stat_ranges * kRows + mine;
+      float m = -INFINITY, l = 0.0f;
+#pragma unroll 4
+      for (int i = 0; i < cut.stat_ranges; ++i) {
+        const float2 x = ml[(int64_t)i * kRows];
+        const float top = fmaxf(m, x.x), at = top == -INFINITY ? 0.0f : top;
+        l = l * exp2f(m - at) + x.y * exp2f(x.x - at);
+        m = top;
+      }
+      none = mine >= rows || (m == -INFINITY && !(l != l));
+      lse = none ? INFINITY : (m == -INFINITY ? 0.0f : m) + log2f(l);
+    }
+    __syncthreads();
+    if (!kStats && mine >= 0 && mine < tiles * 128) {
+      sm.row[mine].y = -lse;
+      if (none) sm.row[mine].x = 0.0f;
     }
     ptx::fence_proxy_async_smem();
     __syncthreads();
-    // positions that some row of the group sees
-    const int64_t seen = (int64_t)start + (r0 + rows - 1) / G + 1;
-    const int last = (int)min((int64_t)s1, (seen + kTile - 1) / kTile);
-    const int count = last > s0 ? last - s0 : 0;  // steps of a pass
 
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
+    {
       if (warp == 0) {
         // ---------------------------------------------------------------- loads
         int id = -1;  // of page 2 i + lane, and its scale, 16 steps ahead
@@ -214,7 +257,7 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, in
 #pragma unroll 1
             for (int part = 0; part < kParts; ++part) {
               const uint32_t fmt = part < 2 ? ptx::kFmtE4M3 : ptx::kFmtE5M2;
-              if (pass == 0) {
+              if (kStats) {
                 const uint32_t id = ptx::idesc_make2(fmt, ptx::kFmtE4M3, 128, kTile);
                 for (int t = 0; t < tiles; ++t)
 #pragma unroll
@@ -238,7 +281,7 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, in
         // ---------------------------------------------------------------- exponentials
         const int w = warp & 3, g = (warp - 4) >> 2;
         const uint32_t lanes = (uint32_t)(w * 32) << 16;
-        if (pass == 0) {
+        if (kStats) {
           // a query row: row tile g, lane
           const int r = g * 128 + w * 32 + lane;
           const float c = g < tiles ? sm.row[r].x : 0.0f;
@@ -292,7 +335,9 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, in
               ptx::mbar_arrive(&sm.empty[s]);
             }
           }
-          if (g < tiles) sm.ml[r] = make_float2(m, l);
+          if (g < tiles)
+            p.stats[(((int64_t)bh * cut.groups + group) * ranges + range) * kRows + r] =
+                make_float2(m, l);
         } else {
           // a key: half g of the query rows
           for (int i = 0; i < count; ++i) {
@@ -354,8 +399,8 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, in
           // (a part is written again two steps on, behind the next step's barrier)
           if (r0 == 0 && g == 0) {
             // positions that the window holds, but no row of this group sees, begin at zero
-            for (int i = count; s0 + i < s1; ++i) {
-              const int64_t pos = (int64_t)(s0 + i) * kTile + w * 32 + lane;
+            for (int i = s1; i < w1; ++i) {
+              const int64_t pos = (int64_t)i * kTile + w * 32 + lane;
               const int pg = (int)(pos / kPage);
               const int id = pos < keys ? table[pg] : -1;
               if (id >= 0 && id < p.n_pages) {
@@ -367,33 +412,8 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, in
         }
       }
       step += count;
-      if (pass == 0) {
-        // the rows' statistics over the cluster
-        __syncwarp();
-        ptx::cluster_sync();
-        if (warp >= 4) {
-          const int r = threadIdx.x - 128;
-          if (r < tiles * 128) {
-            float m = -INFINITY;
-            for (int c = 0; c < cs; ++c) m = fmaxf(m, ld_cluster_f2(&sm.ml[r], c).x);
-            const float mm = m == -INFINITY ? 0.0f : m;
-            float l = 0.0f;
-            for (int c = 0; c < cs; ++c) {
-              const float2 v = ld_cluster_f2(&sm.ml[r], c);
-              l += v.y * exp2f(v.x - mm);
-            }
-            // a row that sees nothing adds nothing
-            const bool none = m == -INFINITY && !(l != l);
-            sm.row[r].y = r >= rows || none ? -INFINITY : -(mm + log2f(l));
-            if (r >= rows || none) sm.row[r].x = 0.0f;
-          }
-        }
-        __syncwarp();
-        ptx::cluster_sync();
-      } else {
-        __syncthreads();
-      }
     }
+    __syncthreads();
   }
   if (warp == 1 && __any_sync(0xffffffffu, *(volatile int*)&sm.abort)) {
     if (ptx::elect_one()) ptx::mma_commit(&sm.drain);
@@ -410,6 +430,26 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, in
 
 }  // namespace
 
+static Cut cut_of(int batch, int window, int Hq, int Hkv) {
+  const int64_t units = (int64_t)batch * Hkv, rows = (int64_t)(Hq / Hkv) * window;
+  Cut c;
+  c.groups = (int)((rows + kRows - 1) / kRows);
+  // about one range per SM
+  const int64_t stats = units * c.groups;
+  c.stat_ranges = (int)(stats < kSms ? kSms / stats : 1);
+  c.ranges = (int)(units < kSms ? kSms / units : 1);
+  return c;
+}
+
+bool weigh_tc_applies(kda_dtype dt, int window, int Hq, int Hkv, int d) {
+  return dt == KDA_BF16 && d == 128 && (int64_t)window * (Hq / Hkv) > 64;
+}
+
+size_t cache_weigh_tc_workspace(int batch, int window, int Hq, int Hkv) {
+  const Cut c = cut_of(batch, window, Hq, Hkv);
+  return (size_t)batch * Hkv * c.groups * c.stat_ranges * kRows * sizeof(float2);
+}
+
 kda_status launch_cache_weigh_tc(const WeighParams& p, cudaStream_t s) {
   CUtensorMap map;
   if (!chunk_tc_available())
@@ -424,36 +464,15 @@ kda_status launch_cache_weigh_tc(const WeighParams& p, cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !set[dev]) {
-    cudaFuncSetAttribute(weigh_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    cudaFuncSetAttribute(weigh_tc_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaFuncSetAttribute(weigh_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaFuncSetAttribute(weigh_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  // one CTA per SM: as many to a cluster as fill the SMs
+  const Cut c = cut_of(p.batch, p.window, p.Hq, p.Hkv);
   const int64_t units = (int64_t)p.batch * p.Hkv;
-  int cs = 1;
-  while (cs < 16 && units * cs < 128 && (int64_t)p.max_pages > 2 * cs) cs *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * cs));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)cs;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cs == 16) {  // more than the portable eight: where the GPU takes them
-    int clusters = 0;
-    if (cudaOccupancyMaxActiveClusters(&clusters, weigh_tc_kernel, &cfg) != cudaSuccess || clusters < 1) {
-      cudaGetLastError();
-      cs = 8;
-      cfg.gridDim = dim3((unsigned)(units * cs));
-      at[0].val.clusterDim.x = (unsigned)cs;
-    }
-  }
-  cudaLaunchKernelEx(&cfg, weigh_tc_kernel, map, p, cs);
-  count_launches(1);
+  weigh_tc_kernel<true><<<(unsigned)(units * c.groups * c.stat_ranges), kThreads, bytes, s>>>(map, p, c);
+  weigh_tc_kernel<false><<<(unsigned)(units * c.ranges), kThreads, bytes, s>>>(map, p, c);
+  count_launches(2);
   return check_launch("kda_cache_weigh");
 }
 

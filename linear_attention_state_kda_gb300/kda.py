@@ -112,7 +112,9 @@ def lib():
     L.kda_decay_window.argtypes = [I, I, I, I, I, I, F, P, I64, P, I64, P, I64, P, I64, P, P, P, I64,
                                    P, P, P]
     L.kda_cache_weigh.restype = I
-    L.kda_cache_weigh.argtypes = [I, I, I, I, I, I, F, F, P, P, P, P, I, P, P, P, I64, P, P]
+    L.kda_cache_weigh.argtypes = [I, I, I, I, I, I, F, F, P, P, P, P, I, P, P, P, I64, P, Z, P, P]
+    L.kda_cache_weigh_workspace.restype = Z
+    L.kda_cache_weigh_workspace.argtypes = [I, I, I, I, I, I]
     L.kda_cache_evict.restype = I
     L.kda_cache_evict.argtypes = [I, I, I, P, P, I, P, I, P, P, P, P, P, I64, I, I, I, P, P, P, P]
     _lib = L
@@ -594,14 +596,23 @@ def decay_window(q, k, v, g, read_slots, write_slots, state_pool, scale=1.0, o=N
     return r
 
 
+def cache_weigh_workspace(dtype, batch, window, Hq, Hkv, d):
+    """kda_cache_weigh_workspace: scratch bytes of cache_weigh (0 for up to 64 query rows per
+    key/value head)."""
+    dt = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    return int(lib().kda_cache_weigh_workspace(dt, batch, window, Hq, Hkv, d))
+
+
 def cache_weigh(q, start, page_table, k_cache, k_scale, weights, scale=1.0, lens=None, keep=1.0,
-                status=None, stream=None):
+                workspace=None, status=None, stream=None):
     """kda_cache_weigh: adds to weights [n_pages, Hkv, 64] the softmax weights with which the
     window's queries (as for cache_attention) see each cached token, summed over the window's
     tokens and the head's query heads; what the tokens before the window had counts `keep` times.
-    Returns weights, updated in place."""
+    `workspace` (uint8 device tensor of at least cache_weigh_workspace(...) bytes) is allocated here
+    when not given. Returns weights, updated in place."""
     r = (_native_module or _native()).cache_weigh(
-        q, start, page_table, k_cache, k_scale, weights, scale, lens, keep, status, _handle(stream))
+        q, start, page_table, k_cache, k_scale, weights, scale, lens, keep, workspace, status,
+        _handle(stream))
     if r.__class__ is int:
         _check(r)
     return r

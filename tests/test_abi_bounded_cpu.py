@@ -64,9 +64,9 @@ def test_window_refusals(L):
 
 
 def _weigh(L, dt=1, B=2, W=1, Hq=8, Hkv=2, d=128, q=P, start=P, table=P, cols=4, kc=P, ks=P, w=P,
-           pages=8):
+           pages=8, ws=None, ws_bytes=0):
     return L.kda_cache_weigh(dt, B, W, Hq, Hkv, d, 1.0, 1.0, q, start, None, table, cols, kc, ks, w,
-                             pages, None, None)
+                             pages, ws, ws_bytes, None, None)
 
 
 def test_weigh_refusals(L):
@@ -79,6 +79,14 @@ def test_weigh_refusals(L):
                 dict(cols=0), dict(q=P + 4), dict(w=P + 4), dict(kc=P + 1), dict(B=1 << 24)):
         assert _weigh(L, **bad) == A, bad
     assert "kda_cache_weigh" in kda.last_error()
+    need = kda.cache_weigh_workspace(torch.bfloat16, 2, 40, 8, 2, 128)
+    assert need > 0 and kda.cache_weigh_workspace(torch.bfloat16, 2, 16, 8, 2, 128) == 0
+    assert kda.cache_weigh_workspace(torch.float32, 2, 40, 8, 2, 128) == 0
+    for x in (dict(), dict(ws=P + 16, ws_bytes=need), dict(ws=P, ws_bytes=need - 1)):
+        assert _weigh(L, W=40, **x) == kda.KDA_ERR_WORKSPACE
+    for x in ((1, 0, 40, 8, 2, 128), (1, 2, 70000, 8, 2, 128), (1, 2, 40, 7, 2, 128),
+              (1, 2, 40, 8, 2, 96), (3, 2, 40, 8, 2, 128)):
+        assert L.kda_cache_weigh_workspace(*x) == 0
     assert _weigh(L, B=0) == kda.KDA_OK and _weigh(L, W=0) == kda.KDA_OK
 
 
