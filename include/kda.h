@@ -642,14 +642,14 @@ KDA_API kda_status kda_decay_window(kda_dtype dt, int batch, int window, int H, 
  *   A query none of whose positions is present adds nothing. Codes that a query does not see do not
  *   reach its weights, NaN included.
  *   workspace   at least kda_cache_weigh_workspace(...) bytes (0 for sizes that are refused or need
- *               none: up to 64 query rows per key/value head), 256-byte aligned; contents need not be
- *               initialised.
+ *               none), 256-byte aligned; contents need not be initialised.
  *   Other arguments, limits and status as for kda_cache_attention.
  * Scores and sums are fp32 and the same on every run. bf16 queries enter at full precision (in windows
  * of more than 64 query rows per key/value head at d = 128: to 2^-20 of the query's largest entry),
  * fp32 ones as two 11-bit parts.
  */
-KDA_API size_t kda_cache_weigh_workspace(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d);
+KDA_API size_t kda_cache_weigh_workspace(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d,
+                                         int max_pages);
 KDA_API kda_status kda_cache_weigh(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d,
                                    float scale, float keep, const void* q, const int32_t* start,
                                    const int32_t* lens, const int32_t* page_table, int max_pages,

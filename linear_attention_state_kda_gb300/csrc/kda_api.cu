@@ -763,12 +763,13 @@ kda_status kda_decay_window(kda_dtype dt, int batch, int window, int H, int Hk, 
   return launch_decay_window(p, dt, d, (cudaStream_t)stream);
 }
 
-size_t kda_cache_weigh_workspace(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d) {
+size_t kda_cache_weigh_workspace(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d,
+                                 int max_pages) {
   if ((dt != KDA_F32 && dt != KDA_BF16) || batch <= 0 || window <= 0 || window > kMaxAttnWindow ||
       Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || (d != 64 && d != 128) ||
-      !attn_sizes_ok(batch, window, Hq, Hkv))
+      !attn_sizes_ok(batch, window, Hq, Hkv) || max_pages <= 0 || max_pages > (1 << 24))
     return 0;
-  return cache_weigh_workspace_bytes(dt, batch, window, Hq, Hkv, d);
+  return cache_weigh_workspace_bytes(dt, batch, window, Hq, Hkv, d, max_pages);
 }
 
 kda_status kda_cache_weigh(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d, float scale,
@@ -795,7 +796,7 @@ kda_status kda_cache_weigh(kda_dtype dt, int batch, int window, int Hq, int Hkv,
               "kda_cache_weigh: q, k_cache and weights must be non-null");
   KDA_REQUIRE(aligned(q, 16) && aligned(weights, 16), KDA_ERR_INVALID_ARG,
               "kda_cache_weigh: q and weights must be 16-byte aligned");
-  const size_t need = cache_weigh_workspace_bytes(dt, batch, window, Hq, Hkv, d);
+  const size_t need = cache_weigh_workspace_bytes(dt, batch, window, Hq, Hkv, d, max_pages);
   KDA_REQUIRE(need == 0 || (workspace && ws_bytes >= need && aligned(workspace, 256)),
               KDA_ERR_WORKSPACE,
               "kda_cache_weigh: workspace missing, too small or not 256-byte aligned (need " +
@@ -804,7 +805,7 @@ kda_status kda_cache_weigh(kda_dtype dt, int batch, int window, int Hq, int Hkv,
   p.batch = batch; p.window = window; p.Hq = Hq; p.Hkv = Hkv; p.scale = scale; p.keep = keep;
   p.q = q; p.start = start; p.lens = lens; p.table = page_table; p.max_pages = max_pages;
   p.n_pages = n_pages; p.kc = (const uint8_t*)k_cache; p.ks = k_scale; p.weights = weights;
-  p.stats = (float2*)workspace; p.status = status;
+  p.stats = (float2*)workspace; p.max_rows = Hq / Hkv * window; p.status = status;
   return launch_cache_weigh(p, dt, d, (cudaStream_t)stream);
 }
 

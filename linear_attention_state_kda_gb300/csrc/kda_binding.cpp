@@ -637,7 +637,7 @@ PyObject* cache_weigh(PyObject*, PyObject* const* a, Py_ssize_t n) {
             hkv = as_int(c.H, "Hkv"), d = as_int(c.d, "d");
   const float scale = (float)as_double(a[6]), keep = (float)as_double(a[8]);
   const CallStream on(a[11]);
-  int64_t bytes = (int64_t)kda_cache_weigh_workspace(dt, b, w, hq, hkv, d);
+  int64_t bytes = (int64_t)kda_cache_weigh_workspace(dt, b, w, hq, hkv, d, c.max_pages);
   Out ws;
   void* sp = nullptr;
   if (bytes > 0 || a[9] != Py_None) {

@@ -13,21 +13,31 @@ namespace {
 // ---------------------------------------------------------------- weighing
 //
 //     weight[t] = keep * weight[t] + sum_i exp(s_it - lse_i),   s_it = scale q_i . k_t
-// over the query rows i (tokens of the window x query heads of the group) that see position t.
+//
+// over the query rows i (tokens of the window x query heads of the group) that see position t, for
+// up to 64 rows (or fp32, or d = 64; else kda_weigh_tc.cu).
 //
 // Bound by the K codes, d bytes a key. A cluster owns one (row, key/value head) and its CTAs
 // contiguous ranges of its pages, so that the codes are read once: the scores stay in shared
 // memory while the row statistics (running maximum and sum) are joined over the cluster, and become
-// weights there. Keys beyond the room for scores are scored again.
+// weights there. Keys beyond the room for scores are scored again. (Clusters do not fill the GPU
+// where there are few of them: 8 clusters of 16 CTAs land on 64 SMs. There the statistics are taken
+// by one launch and the weights by a second that scores again, mostly from L2: one row of 131072
+// tokens and 8 heads took 286 us as clusters of 8, 66 us so.)
 //
-// Scores are warp-level f16 MMAs with the keys as the rows: 16 keys x 16 channels times 16 channels
-// x 8 query rows. The sum over the channels is in any order, so lane (g, t) takes channels
-// 32 t .. (d = 128) of keys g and g + 8 from global memory in 16-byte loads, which are the A
-// fragments after widening (e4m3 to f16 is exact). Query rows are scaled by a power of two into
-// f16's upper range: bf16 entries down to 2^-30 of the row's largest are exact, fp32 entries are
-// two f16 parts.
-constexpr int kWThreads = 256;
-constexpr int kWWarps = kWThreads / 32;
+// A warp takes a page, 32 keys in flight at once (with 64, 341 us where 32 take 280: fewer CTAs per
+// SM); its id and scale are fetched with those of the warp's next pages. Scores are warp-level f16
+// MMAs with the keys as the rows: 16 keys x 16 channels times 16 channels x 8 query rows. The sum
+// over the channels is in any order, so lane (g, t) takes channels 16 t .. and 64 + 16 t .. of keys
+// g and g + 8 from global memory in 16-byte loads (four lanes read 64 bytes on end: whole sectors),
+// which are the A fragments after widening (e4m3 to f16 is exact). Query rows are scaled by a power
+// of two into f16's upper range: bf16 entries down to 2^-30 of the row's largest are exact, fp32
+// entries are two f16 parts.
+//
+// Measured, Hq 32, Hkv 8, d 128: 128 rows of 16384 tokens, one query token each, 280 us (4.6 TB/s
+// of codes); 16 rows of 8192 with 4 query tokens 48 us; the same with 2 in fp32 35 us; 2 rows of 100
+// 8.9 us, which is latency: ids, codes, the cluster's two barriers.
+constexpr int kWThreads = 128, kWMaxWarps = kWThreads / 32;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -46,48 +56,74 @@ __device__ __forceinline__ float2 ld_cluster_f2(const float2* p, uint32_t rank) 
 
 // (m, l) of two parts of a row's keys.
 __device__ __forceinline__ float2 join(float2 a, float2 b) {
-  const float m = fmaxf(a.x, b.x);
-  if (m == -INFINITY) return make_float2(m, a.y + b.y);
-  return make_float2(m, a.y * exp2f(a.x - m) + b.y * exp2f(b.x - m));
+  const float m = fmaxf(a.x, b.x), at = m == -INFINITY ? 0.0f : m;
+  return make_float2(m, a.y * ptx::ex2_approx(a.x - at) + b.y * ptx::ex2_approx(b.x - at));
 }
 
-// NT: tiles of 8 query rows scored at once. P: f16 parts of a query.
-template <int D, int NT, int P, class T>
-__global__ void __launch_bounds__(kWThreads) weigh_kernel(const WeighParams p, int cs, int cap_keys) {
+// NT: tiles of 8 query rows scored at once. P: f16 parts of a query. How a unit's keys are shared:
+// by a cluster of `cs` CTAs, or by `cs` CTAs of a launch that takes the statistics and of one that sums
+// the weights.
+enum Share { kCluster, kStats, kWeights };
+template <int D, int NT, int P, class T, Share kShare>
+__global__ void __launch_bounds__(kWThreads, NT == 1 ? 6 : 4)
+weigh_kernel(const WeighParams p, int cs, int cap_keys) {
   constexpr int KC = D / 16;      // 16-channel steps
   constexpr int LB = D / 4;       // bytes of a key per lane
   constexpr int ROWS = NT * 8;
+  constexpr int BT = 2;           // tiles of 16 keys in flight: half a page
   extern __shared__ __align__(16) unsigned char wsm[];
-  // query fragments [P][NT][KC][32 lanes] x 8 bytes, then the scores [cap_keys][rows]
+  // query fragments [P][NT][KC][32 lanes] x 8 bytes, then the scores [rows][cap_keys + 4] (a row
+  // begins 4 banks on: the 8 keys x 4 rows of an accumulator register fall into distinct banks)
   uint2* frag = reinterpret_cast<uint2*>(wsm);
   float* score = reinterpret_cast<float*>(wsm + (size_t)P * NT * KC * 256);
+  const int stride = cap_keys + 4;
   __shared__ float row_mul[ROWS];          // scale * log2 e * 2^e of a query row
-  __shared__ float2 part[kWWarps][ROWS];
+  __shared__ float2 part[kWMaxWarps][ROWS];
   __shared__ float2 cta_ml[ROWS];
   __shared__ float row_lse[ROWS];
 
   const int rank = blockIdx.x % cs, bh = blockIdx.x / cs;
   const int b = bh / p.Hkv, h = bh - b * p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  constexpr int warps = kWMaxWarps;
   const int start = p.start[b];
   int n = start < 0 ? 0 : p.lens ? p.lens[b] : p.window;
   n = n < 0 ? 0 : n > p.window ? p.window : n;
   if (n == 0) return;  // the whole cluster
   const int G = p.Hq / p.Hkv, R = n * G;
-  const int64_t most = (int64_t)p.max_pages * kPage;
-  const int64_t keys = (int64_t)start + n < most ? (int64_t)start + n : most;
-  if (rank == 0 && tid == 0 && h == 0 && p.status && (int64_t)start + n > most)
+  const int64_t most = (int64_t)p.max_pages * kPage;  // at most 2^30
+  const int keys = (int)((int64_t)start + n < most ? (int64_t)start + n : most);
+  if (kShare != kWeights && rank == 0 && tid == 0 && h == 0 && p.status && (int64_t)start + n > most)
     atomicOr(p.status, KDA_STATUS_BAD_PAGE);
-  const int pages = (int)((keys + kPage - 1) / kPage);
+  const int pages = (keys + kPage - 1) / kPage;
   const int per = (pages + cs - 1) / cs;
   const int pg0 = min(pages, rank * per), pg1 = min(pages, pg0 + per);
   const int32_t* table = p.table + (int64_t)b * p.max_pages;
+
+  // Ids and scales of the warp's pages pg0 + warp + warps * k: lane l has those of k = base + l.
+  int id_l = -1, have = -1;
+  float ks_l = 0.0f;
+  auto fetch = [&](int k) {  // (k the same in all lanes)
+    if (have >= 0 && k >= have && k < have + 32) return;
+    have = k & ~31;
+    const int pg = pg0 + warp + warps * (have + lane);
+    id_l = pg < pg1 ? table[pg] : -1;
+    if (id_l >= p.n_pages) {
+      if (p.status) atomicOr(p.status, KDA_STATUS_BAD_PAGE);
+      id_l = -1;
+    }
+    ks_l = id_l < 0 ? 0.0f : p.ks[(int64_t)id_l * p.Hkv + h];
+  };
+  {  // (the first pages' ids on their way before the queries)
+    const int pg = pg0 + warp + warps * lane;
+    if (pg < pg1) asm volatile("prefetch.global.L1 [%0];" ::"l"(table + pg));
+  }
 
   for (int r0 = 0; r0 < R; r0 += ROWS) {
     const int rows = min(ROWS, R - r0);
     __syncthreads();
     // the group's query rows: scale, then fragments. A warp takes a row.
-    for (int r = warp; r < ROWS; r += kWWarps) {
+    for (int r = warp; r < ROWS; r += warps) {
       float f[D / 32];
       float m = 0.0f;
       const int row = r0 + r;
@@ -105,12 +141,12 @@ __global__ void __launch_bounds__(kWThreads) weigh_kernel(const WeighParams p, i
       const float down = e > 0 ? pow2f(-e) : 1.0f;
       const float up1 = e < 0 ? pow2f(-e < 126 ? -e : 126) : 1.0f;
       const float up2 = e < -126 ? pow2f(-e - 126) : 1.0f;
-      // channel c of the row: in lane quarter c / (D/4), step (c % (D/4)) / 4
+      // channel c of the row: in 16-byte piece c / 16, of lane c / 16 % 4 and its load c / 64
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const float x = f[i] * down * up1 * up2;
         const int c = lane * (D / 32) + i;
-        const int tq = c / LB, kc = (c % LB) / 4, el = c % 4;
+        const int tq = c / 16 % 4, kc = c / 64 * 4 + c % 16 / 4, el = c % 4;
         __half hi = __float2half_rn(x);
         __half* dst = reinterpret_cast<__half*>(
             &frag[(((r >> 3) * KC) + kc) * 32 + (r & 7) * 4 + tq]);
@@ -128,204 +164,305 @@ __global__ void __launch_bounds__(kWThreads) weigh_kernel(const WeighParams p, i
     }
     __syncthreads();
 
-    // the last token of the group sees the most; the page range of this CTA is fixed
-    const int j_last = (r0 + rows - 1) / G;
-    const int64_t seen = (int64_t)start + j_last + 1;
-    // the lane's rows 2 t4, 2 t4 + 1 of each tile: how far they see, and their statistics
-    int64_t vis[NT][2];
+    // the last token of the group sees the most, its first token the least
+    const int seen = (int)min((int64_t)keys, (int64_t)start + (r0 + rows - 1) / G + 1);
+    const int64_t seen_by_all = (int64_t)start + r0 / G + 1;
+    // the lane's rows 2 t4, 2 t4 + 1 of each tile: how far they see, their factors and statistics
+    int vis[NT][2];
+    float mul[NT][2];
     float2 ml[NT][2];
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = i * 8 + t4 * 2 + e;
-        vis[i][e] = r < rows ? (int64_t)start + (r0 + r) / G + 1 : 0;  // positions below
-        if (vis[i][e] > keys) vis[i][e] = keys;
+        vis[i][e] = r < rows ? (int)min((int64_t)keys, (int64_t)start + (r0 + r) / G + 1) : 0;
+        mul[i][e] = row_mul[r];
         ml[i][e] = make_float2(-INFINITY, 0.0f);
       }
 
-    // Scores of 16 keys (rows of tile `tile` of page `page`) in base-2 exponents, masked.
-    auto score_tile = [&](int page_id, float ks, int64_t pos0, float acc[NT][4]) {
-      const uint8_t* base = p.kc + ((int64_t)page_id * p.Hkv + h) * (int64_t)(kPage * D) +
-                            (int)(pos0 & (kPage - 1)) * D;
-      uint32_t w[2][LB / 4];
+    // Scores of tiles t0 .. t0 + BT - 1 (16 keys each) of a page in base-2 exponents, masked.
+    auto score_tiles = [&](int id, float ks, int page, int t0, float (&acc)[BT][NT][4]) {
+      const uint8_t* base =
+          p.kc + ((int64_t)id * p.Hkv + h) * (int64_t)(kPage * D) + (t0 * 16 + g) * D + t4 * 16;
+      uint32_t w[BT][2][LB / 4];
 #pragma unroll
-      for (int half = 0; half < 2; ++half)
+      for (int t = 0; t < BT; ++t)
 #pragma unroll
-        for (int i = 0; i < LB / 16; ++i)
-          *reinterpret_cast<uint4*>(&w[half][4 * i]) = __ldcs(reinterpret_cast<const uint4*>(
-              base + (g + 8 * half) * D + t4 * LB + 16 * i));
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+          for (int i = 0; i < LB / 16; ++i)
+            *reinterpret_cast<uint4*>(&w[t][half][4 * i]) = __ldcs(
+                reinterpret_cast<const uint4*>(base + (t * 16 + 8 * half) * D + 64 * i));
 #pragma unroll
-      for (int kc = 0; kc < KC; ++kc) {
-        uint32_t a[4];
-        f16x4_from_e4m3(w[0][kc], a[0], a[2]);
-        f16x4_from_e4m3(w[1][kc], a[1], a[3]);
+      for (int t = 0; t < BT; ++t) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
+        for (int i = 0; i < NT; ++i) acc[t][i][0] = acc[t][i][1] = acc[t][i][2] = acc[t][i][3] = 0.0f;
 #pragma unroll
-          for (int part_i = 0; part_i < P; ++part_i) {
-            const uint2 q2 = frag[((part_i * NT + i) * KC + kc) * 32 + lane];
-            mma16816(acc[i], a, q2.x, q2.y);
-          }
+        for (int kc = 0; kc < KC; ++kc) {
+          uint32_t a[4];
+          f16x4_from_e4m3(w[t][0][kc], a[0], a[2]);
+          f16x4_from_e4m3(w[t][1][kc], a[1], a[3]);
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int part_i = 0; part_i < P; ++part_i) {
+              const uint2 q2 = frag[((part_i * NT + i) * KC + kc) * 32 + lane];
+              mma16816(acc[t][i], a, q2.x, q2.y);
+            }
         }
       }
+      const bool whole = (int64_t)(page + 1) * kPage <= seen_by_all;
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int t = 0; t < BT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int64_t pos = pos0 + g + 8 * (e >> 1);
-          acc[i][e] = pos < vis[i][e & 1]
-                          ? acc[i][e] * (ks * row_mul[i * 8 + t4 * 2 + (e & 1)]) : -INFINITY;
-        }
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[t][i][e] *= ks * mul[i][e & 1];
+      if (!whole) {
+#pragma unroll
+        for (int t = 0; t < BT; ++t)
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int pos = page * kPage + (t0 + t) * 16 + g + 8 * (e >> 1);
+              acc[t][i][e] = pos < vis[i][e & 1] ? acc[t][i][e] : -INFINITY;
+            }
+      }
     };
 
-    for (int pg = pg0 + warp; pg < pg1; pg += kWWarps) {
+    for (int k = 0, pg = pg0 + warp; kShare != kWeights && pg < pg1; ++k, pg += warps) {
       if ((int64_t)pg * kPage >= seen) break;
-      int id = table[pg];
-      if (id >= p.n_pages) {
-        if (lane == 0 && h == 0 && p.status) atomicOr(p.status, KDA_STATUS_BAD_PAGE);
-        id = -1;
-      }
+      fetch(k);
+      const int id = __shfl_sync(0xffffffffu, id_l, k & 31);
       if (id < 0) continue;
-      const float ks = p.ks[(int64_t)id * p.Hkv + h];
+      const float ks = __shfl_sync(0xffffffffu, ks_l, k & 31);
       const int local = (pg - pg0) * kPage;
+      if (kShare == kCluster && lane < 2)  // the page's weights, for later
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.weights + ((int64_t)id * p.Hkv + h) * kPage +
+                                                      32 * lane));
 #pragma unroll 1
-      for (int tile = 0; tile < kPage / 16; ++tile) {
-        float acc[NT][4];
-        score_tile(id, ks, (int64_t)pg * kPage + tile * 16, acc);
+      for (int t0 = 0; t0 < kPage / 16; t0 += BT) {
+        float acc[BT][NT][4];
+        score_tiles(id, ks, pg, t0, acc);
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float2& s = ml[i][e];
-            const float m = fmaxf(s.x, fmaxf(acc[i][e], acc[i][e + 2]));
-            const float mm = m == -INFINITY ? 0.0f : m;
-            s.y = s.y * exp2f(s.x - mm) + exp2f(acc[i][e] - mm) + exp2f(acc[i][e + 2] - mm);
-            s.x = m;
+            float m = s.x;
+#pragma unroll
+            for (int t = 0; t < BT; ++t) m = fmaxf(m, fmaxf(acc[t][i][e], acc[t][i][e + 2]));
+            const float at = m == -INFINITY ? 0.0f : m;
+            float l = s.y * ptx::ex2_approx(s.x - at);
+#pragma unroll
+            for (int t = 0; t < BT; ++t)
+              l += ptx::ex2_approx(acc[t][i][e] - at) + ptx::ex2_approx(acc[t][i][e + 2] - at);
+            s = make_float2(m, l);
           }
         if (local < cap_keys) {
 #pragma unroll
           for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int r = i * 8 + t4 * 2 + (e & 1);
-              if (r < rows) score[(local + tile * 16 + g + 8 * (e >> 1)) * rows + r] = acc[i][e];
+            for (int e = 0; e < 2; ++e) {
+              const int r = i * 8 + t4 * 2 + e;
+              if (r < rows) {
+                float* dst = score + r * stride + local + t0 * 16 + g;
+#pragma unroll
+                for (int t = 0; t < BT; ++t) {
+                  dst[t * 16] = acc[t][i][e];
+                  dst[t * 16 + 8] = acc[t][i][e + 2];
+                }
+              }
             }
         }
       }
     }
-    // row statistics: lanes of a row, warps, CTAs
+    // row statistics: lanes of a row, warps, CTAs (16 lanes to a row)
+    auto of_row = [&](float2 s) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+      for (int o = 8; o > 0; o >>= 1)
+        s = join(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o),
+                                __shfl_xor_sync(0xffffffffu, s.y, o)));
+      return s;
+    };
+    // a row that sees nothing adds nothing, nor does one past the last
+    auto set_lse = [&](int r, float2 s) {
+      const bool none = r >= rows || (s.x == -INFINITY && !(s.y != s.y));
+      row_lse[r] = none ? INFINITY : (s.x == -INFINITY ? 0.0f : s.x) + log2f(s.y);
+    };
+    float2* stats = kShare == kCluster ? nullptr : p.stats + (int64_t)bh * cs * p.max_rows + r0;
+    if (kShare != kWeights) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float2 s = ml[i][e];
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1)
-          s = join(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o),
-                                  __shfl_xor_sync(0xffffffffu, s.y, o)));
-        if (g == 0) part[warp][i * 8 + t4 * 2 + e] = s;
+        for (int e = 0; e < 2; ++e) {
+          float2 s = ml[i][e];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1)
+            s = join(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o),
+                                    __shfl_xor_sync(0xffffffffu, s.y, o)));
+          if (g == 0) part[warp][i * 8 + t4 * 2 + e] = s;
+        }
+      __syncthreads();
+      for (int i = tid; i < ROWS * 16; i += kWThreads) {
+        const int r = i >> 4, w = i & 15;
+        const float2 s = of_row(w < kWMaxWarps ? part[w][r] : make_float2(-INFINITY, 0.0f));
+        if (w == 0) {
+          if (kShare == kCluster) cta_ml[r] = s;
+          else if (r < rows) stats[(int64_t)rank * p.max_rows + r] = s;
+        }
       }
-    __syncthreads();
-    if (tid < ROWS) {
-      float2 s = part[0][tid];
-#pragma unroll
-      for (int w = 1; w < kWWarps; ++w) s = join(s, part[w][tid]);
-      cta_ml[tid] = s;
     }
-    ptx::cluster_sync();
-    if (tid < ROWS) {
-      float2 s = ld_cluster_f2(&cta_ml[tid], 0);
-      for (int c = 1; c < cs; ++c) s = join(s, ld_cluster_f2(&cta_ml[tid], c));
-      // a row that sees nothing adds nothing
-      row_lse[tid] = s.x == -INFINITY && !(s.y != s.y) ? INFINITY : s.x + log2f(s.y);
+    if (kShare == kStats) continue;
+    if (kShare == kCluster) {
+      ptx::cluster_sync();
+      for (int i = tid; i < ROWS * 16; i += kWThreads) {
+        const int r = i >> 4, c = i & 15;
+        const float2 s = of_row(c < cs ? ld_cluster_f2(&cta_ml[r], c) : make_float2(-INFINITY, 0.0f));
+        if (c == 0) set_lse(r, s);
+      }
+      __syncthreads();
+      ptx::cluster_arrive();  // this CTA has read the others' statistics; waited for below
+    } else {
+      for (int i = tid; i < ROWS * 16; i += kWThreads) {
+        const int r = i >> 4;
+        float2 s = make_float2(-INFINITY, 0.0f);
+        for (int c = i & 15; c < cs && r < rows; c += 16)
+          s = join(s, stats[(int64_t)c * p.max_rows + r]);
+        s = of_row(s);
+        if ((i & 15) == 0) set_lse(r, s);
+      }
+      __syncthreads();
     }
-    ptx::cluster_sync();  // (also: the statistics are read before the next group's are written)
 
     // weights: from the scores in shared memory, else scored again
     const bool fresh = r0 == 0;
-    for (int pg = pg0 + warp; pg < pg1; pg += kWWarps) {
-      int id = table[pg];
-      if (id < 0 || id >= p.n_pages) continue;
+    for (int k = 0, pg = pg0 + warp; pg < pg1; ++k, pg += warps) {
+      fetch(k);
+      const int id = __shfl_sync(0xffffffffu, id_l, k & 31);
+      if (id < 0) continue;
       const int local = (pg - pg0) * kPage;
       const bool reached = (int64_t)pg * kPage < seen;
       if (!reached && !fresh) continue;
       float* wp = p.weights + ((int64_t)id * p.Hkv + h) * kPage;
       if (local < cap_keys || !reached) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int at = lane + 32 * half;
-          const int64_t pos = (int64_t)pg * kPage + at;
-          if (pos >= keys) continue;
-          float sum = 0.0f;
-          if (reached)
-            for (int r = 0; r < rows; ++r)
-              sum += exp2f(score[(local + at) * rows + r] - row_lse[r]);
-          const float old = !fresh ? wp[at] : pos < start && p.keep != 0.0f ? p.keep * wp[at] : 0.0f;
-          wp[at] = old + sum;
+        // lane l: keys 2 l and 2 l + 1 of the page
+        const int at = 2 * lane, pos = pg * kPage + at;
+        float2 sum = make_float2(0.0f, 0.0f), old = sum;
+        if (pos < keys && (!fresh || (pos < start && p.keep != 0.0f)))
+          old = *reinterpret_cast<const float2*>(wp + at);
+        if (reached)
+          for (int r = 0; r < rows; ++r) {
+            const float2 x = *reinterpret_cast<const float2*>(&score[r * stride + local + at]);
+            sum.x += ptx::ex2_approx(x.x - row_lse[r]);
+            sum.y += ptx::ex2_approx(x.y - row_lse[r]);
+          }
+        if (fresh) {
+          old.x = pos < start && p.keep != 0.0f ? p.keep * old.x : 0.0f;
+          old.y = pos + 1 < start && p.keep != 0.0f ? p.keep * old.y : 0.0f;
         }
+        if (pos + 1 < keys)
+          *reinterpret_cast<float2*>(wp + at) = make_float2(old.x + sum.x, old.y + sum.y);
+        else if (pos < keys)
+          wp[at] = old.x + sum.x;
       } else {
-        const float ks = p.ks[(int64_t)id * p.Hkv + h];
+        const float ks = __shfl_sync(0xffffffffu, ks_l, k & 31);
 #pragma unroll 1
-        for (int tile = 0; tile < kPage / 16; ++tile) {
-          float acc[NT][4];
-          score_tile(id, ks, (int64_t)pg * kPage + tile * 16, acc);
-          float sum[2] = {0.0f, 0.0f};
+        for (int t0 = 0; t0 < kPage / 16; t0 += BT) {
+          float acc[BT][NT][4];
+          score_tiles(id, ks, pg, t0, acc);
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
+          for (int t = 0; t < BT; ++t) {
+            float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              sum[e >> 1] += exp2f(acc[i][e] - row_lse[i * 8 + t4 * 2 + (e & 1)]);
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 1);
-            sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 2);
-            const int at = tile * 16 + g + 8 * half;
-            const int64_t pos = (int64_t)pg * kPage + at;
-            if (t4 == 0 && pos < keys) {
-              const float old = !fresh ? wp[at] : pos < start && p.keep != 0.0f ? p.keep * wp[at] : 0.0f;
-              wp[at] = old + sum[half];
+              for (int e = 0; e < 4; ++e)
+                sum[e >> 1] += ptx::ex2_approx(acc[t][i][e] - row_lse[i * 8 + t4 * 2 + (e & 1)]);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 1);
+              sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 2);
+              const int at = (t0 + t) * 16 + g + 8 * half, pos = pg * kPage + at;
+              if (t4 == 0 && pos < keys) {
+                const float old = !fresh ? wp[at] : pos < start && p.keep != 0.0f ? p.keep * wp[at] : 0.0f;
+                wp[at] = old + sum[half];
+              }
             }
           }
         }
       }
     }
+    if (kShare == kCluster) {
+      // the others have read this CTA's statistics: they may be written again, or the CTA leave
+      __syncwarp();
+      ptx::cluster_wait();
+    }
   }
+}
+
+// CTAs that share a unit's keys. Few units with long contexts take two launches: 16 units of 65536
+// tokens 106 us as clusters, 55 so; 16 units of 32768 with 16 query rows 90 and 48; but 32 units of
+// 32768 47 and 58, 32 of 8192 19 and 31. One CTA of a wave to a range: 6 per SM, 4 with more rows.
+struct Sharing {
+  bool cluster;
+  int cs;
+};
+Sharing sharing_of(int batch, int Hkv, int rows, int max_pages) {
+  const int64_t units = (int64_t)batch * Hkv;
+  if (units < 32 && max_pages >= 512) {
+    const int64_t most = 152 * (rows <= 8 ? 6 : 4) / units, cs = max_pages / 4;
+    return {false, (int)(cs < most ? cs : most)};
+  }
+  // a cluster: up to 2048 keys to a CTA (128 rows of 16384 tokens, 8 heads: 280 us; with 8192, 314;
+  // with 1024 the same as with 2048), fewer where the units are few
+  int cs = 1;
+  while (cs < 8 && max_pages > cs && ((int64_t)max_pages * kPage > (int64_t)cs * 2048 || units * cs < 128))
+    cs *= 2;
+  return {true, cs};
 }
 
 template <int D, int NT, int P, class T>
 kda_status launch_weigh_nt(const WeighParams& p, cudaStream_t s) {
   const int64_t units = (int64_t)p.batch * p.Hkv;
-  const int G = p.Hq / p.Hkv;
-  const int64_t rows64 = (int64_t)G * p.window;
+  const Sharing sh = sharing_of(p.batch, p.Hkv, p.max_rows, p.max_pages);
+  constexpr size_t frag = (size_t)P * NT * (D / 16) * 256;
+  static_assert(frag <= 32 * 1024, "shared memory");
+  static bool set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !set[dev]) {
+    const auto kernel = weigh_kernel<D, NT, P, T, kCluster>;
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
+    cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (dev >= 0 && dev < 64) set[dev] = true;
+  }
+  const unsigned grid = (unsigned)(units * sh.cs);
+  if (!sh.cluster) {
+    weigh_kernel<D, NT, P, T, kStats><<<grid, kWThreads, frag, s>>>(p, sh.cs, 0);
+    weigh_kernel<D, NT, P, T, kWeights><<<grid, kWThreads, frag, s>>>(p, sh.cs, 0);
+    count_launches(2);
+    return check_launch("kda_cache_weigh");
+  }
+  const int64_t rows64 = (int64_t)(p.Hq / p.Hkv) * p.window;
   const int rows = rows64 < NT * 8 ? (int)rows64 : NT * 8;
-  // about 2048 keys per CTA, more CTAs where the units are few
-  int cs = 1;
-  while (cs < 8 && ((int64_t)p.max_pages * kPage > (int64_t)cs * 2048 ||
-                    (units * cs < 152 && p.max_pages > cs)))
-    cs *= 2;
-  const int64_t per = (p.max_pages + cs - 1) / cs;
-  const size_t frag = (size_t)P * NT * (D / 16) * 256;
-  const size_t room = 100 * 1024 - frag;
-  int64_t cap = (int64_t)(room / ((size_t)rows * 4)) / kPage;
+  const int64_t per = (p.max_pages + sh.cs - 1) / sh.cs;
+  int64_t cap = (int64_t)((100 * 1024 - frag) / ((size_t)rows * 4) - 4) / kPage;
   if (cap > per) cap = per;
-  const size_t smem = frag + (size_t)cap * kPage * rows * 4;
-  auto kernel = weigh_kernel<D, NT, P, T>;
-  cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * cs));
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kWThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = frag + (size_t)(cap * kPage + 4) * rows * 4;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)cs;
+  at[0].val.clusterDim.x = (unsigned)sh.cs;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kernel, p, cs, (int)(cap * kPage));
+  cudaLaunchKernelEx(&cfg, weigh_kernel<D, NT, P, T, kCluster>, p, sh.cs, (int)(cap * kPage));
   count_launches(1);
   return check_launch("kda_cache_weigh");
 }
@@ -594,8 +731,11 @@ __global__ void __launch_bounds__(kMThreads) evict_move_kernel(const EvictParams
 
 }  // namespace
 
-size_t cache_weigh_workspace_bytes(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d) {
-  return weigh_tc_applies(dt, window, Hq, Hkv, d) ? cache_weigh_tc_workspace(batch, window, Hq, Hkv) : 0;
+size_t cache_weigh_workspace_bytes(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d,
+                                   int max_pages) {
+  if (weigh_tc_applies(dt, window, Hq, Hkv, d)) return cache_weigh_tc_workspace(batch, window, Hq, Hkv);
+  const Sharing sh = sharing_of(batch, Hkv, Hq / Hkv * window, max_pages);
+  return sh.cluster ? 0 : (size_t)batch * Hkv * sh.cs * (Hq / Hkv) * window * sizeof(float2);
 }
 
 kda_status launch_cache_weigh(const WeighParams& p, kda_dtype dt, int d, cudaStream_t s) {

@@ -236,9 +236,11 @@ struct WeighParams {
   const float* ks;
   float* weights;  // [n_pages, Hkv, 64]
   float2* stats;   // workspace: the query rows' statistics by ranges of keys
+  int max_rows;    // query rows per key/value head
   uint32_t* status;
 };
-size_t cache_weigh_workspace_bytes(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d);
+size_t cache_weigh_workspace_bytes(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d,
+                                   int max_pages);
 kda_status launch_cache_weigh(const WeighParams& p, kda_dtype dt, int d, cudaStream_t s);
 // bf16 at d = 128 with more than 64 query rows per key/value head: on the tensor cores' 8-bit path.
 bool weigh_tc_applies(kda_dtype dt, int window, int Hq, int Hkv, int d);

@@ -114,7 +114,7 @@ def lib():
     L.kda_cache_weigh.restype = I
     L.kda_cache_weigh.argtypes = [I, I, I, I, I, I, F, F, P, P, P, P, I, P, P, P, I64, P, Z, P, P]
     L.kda_cache_weigh_workspace.restype = Z
-    L.kda_cache_weigh_workspace.argtypes = [I, I, I, I, I, I]
+    L.kda_cache_weigh_workspace.argtypes = [I, I, I, I, I, I, I]
     L.kda_cache_evict.restype = I
     L.kda_cache_evict.argtypes = [I, I, I, P, P, I, P, I, P, P, P, P, P, I64, I, I, I, P, P, P, P]
     _lib = L
@@ -596,11 +596,10 @@ def decay_window(q, k, v, g, read_slots, write_slots, state_pool, scale=1.0, o=N
     return r
 
 
-def cache_weigh_workspace(dtype, batch, window, Hq, Hkv, d):
-    """kda_cache_weigh_workspace: scratch bytes of cache_weigh (0 for up to 64 query rows per
-    key/value head)."""
+def cache_weigh_workspace(dtype, batch, window, Hq, Hkv, d, max_pages):
+    """kda_cache_weigh_workspace: scratch bytes of cache_weigh (0 where it needs none)."""
     dt = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
-    return int(lib().kda_cache_weigh_workspace(dt, batch, window, Hq, Hkv, d))
+    return int(lib().kda_cache_weigh_workspace(dt, batch, window, Hq, Hkv, d, max_pages))
 
 
 def cache_weigh(q, start, page_table, k_cache, k_scale, weights, scale=1.0, lens=None, keep=1.0,

@@ -79,13 +79,16 @@ def test_weigh_refusals(L):
                 dict(cols=0), dict(q=P + 4), dict(w=P + 4), dict(kc=P + 1), dict(B=1 << 24)):
         assert _weigh(L, **bad) == A, bad
     assert "kda_cache_weigh" in kda.last_error()
-    need = kda.cache_weigh_workspace(torch.bfloat16, 2, 40, 8, 2, 128)
-    assert need > 0 and kda.cache_weigh_workspace(torch.bfloat16, 2, 16, 8, 2, 128) == 0
-    assert kda.cache_weigh_workspace(torch.float32, 2, 40, 8, 2, 128) == 0
+    need = kda.cache_weigh_workspace(torch.bfloat16, 2, 40, 8, 2, 128, 4)
+    assert need > 0 and kda.cache_weigh_workspace(torch.bfloat16, 2, 16, 8, 2, 128, 4) == 0
+    assert kda.cache_weigh_workspace(torch.float32, 2, 40, 8, 2, 128, 4) == 0
+    assert kda.cache_weigh_workspace(torch.float32, 2, 1, 8, 2, 128, 4000) > 0
     for x in (dict(), dict(ws=P + 16, ws_bytes=need), dict(ws=P, ws_bytes=need - 1)):
         assert _weigh(L, W=40, **x) == kda.KDA_ERR_WORKSPACE
-    for x in ((1, 0, 40, 8, 2, 128), (1, 2, 70000, 8, 2, 128), (1, 2, 40, 7, 2, 128),
-              (1, 2, 40, 8, 2, 96), (3, 2, 40, 8, 2, 128)):
+    assert _weigh(L, cols=4000) == kda.KDA_ERR_WORKSPACE
+    for x in ((1, 0, 40, 8, 2, 128, 4), (1, 2, 70000, 8, 2, 128, 4), (1, 2, 40, 7, 2, 128, 4),
+              (1, 2, 40, 8, 2, 96, 4), (3, 2, 40, 8, 2, 128, 4), (1, 2, 40, 8, 2, 128, 0),
+              (1, 2, 40, 8, 2, 128, 1 << 25)):
         assert L.kda_cache_weigh_workspace(*x) == 0
     assert _weigh(L, B=0) == kda.KDA_OK and _weigh(L, W=0) == kda.KDA_OK
 
