@@ -478,10 +478,17 @@ kda_status launch_weigh_t(const WeighParams& p, cudaStream_t s) {
 //
 // Two kernels. The first keeps, for each (row, head), the budget's positions: a cluster holds the
 // candidates' weights as order-preserving integers in shared memory and finds the smallest one that
-// is kept by four rounds of 256-bin counts, then writes the kept positions in order. The second
-// moves the kept tokens, one CTA per (new page, head).
+// is kept by three rounds of counts (digits of 11, 11 and 10 bits, the first counted as the weights
+// arrive), then writes the kept positions in order, each warp those of its own range. Latency: five
+// cluster barriers around passes over shared memory. (Four rounds of 8 bits, warps agreeing on
+// their distinct digits before they count, took 69 us for 32 rows of 16384 tokens and 8 heads;
+// EVICT_SELECT now.)
+// The second moves the kept tokens, one CTA per (new page, head). It is bound by the codes, read
+// and written once: all of a thread's loads are in flight before the page's scale is known.
 constexpr int kEThreads = 512;
 constexpr int kEWarps = kEThreads / 32;
+constexpr int kEBins = 2048;
+constexpr int kEMaxKeys = 49152;  // of a CTA in shared memory; later ones are read again
 
 // Orders like the weights; NaN lowest, zeros of both signs equal. 0 is no candidate.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -490,18 +497,31 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* p, uint32_t rank) {
-  uint32_t a, v;
+__device__ __forceinline__ uint4 ld_cluster_u32x4(const uint32_t* p, uint32_t rank) {
+  uint32_t a;
+  uint4 v;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t scan_lanes(uint32_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
   return v;
 }
 
 __global__ void __launch_bounds__(kEThreads) evict_select_kernel(const EvictParams p, int cs, int cap) {
-  extern __shared__ uint32_t s_key[];
-  __shared__ uint32_t hist[256], total[256];
-  __shared__ uint32_t s_count[2], s_pick[2];
-  __shared__ uint32_t warp_gt[kEWarps], warp_eq[kEWarps];
+  extern __shared__ __align__(16) uint32_t s_key[];
+  __shared__ __align__(16) uint32_t hist[3][kEBins];
+  __shared__ uint32_t warp_sum[kEWarps], s_pick[2];
+  __shared__ __align__(8) uint32_t s_count[2];
+  __shared__ uint2 warp_count[kEWarps];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int rank = blockIdx.x % cs, bh = blockIdx.x / cs;
   const int b = bh / p.Hkv, h = bh % p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -512,153 +532,191 @@ __global__ void __launch_bounds__(kEThreads) evict_select_kernel(const EvictPara
     if (rank == 0 && tid == 0 && h == 0) p.new_length[b] = raw;
     return;
   }
-  const int64_t most = (int64_t)p.max_pages * kPage;
+  for (int i = tid; i < 3 * kEBins / 4; i += kEThreads)
+    reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+  const int64_t most = (int64_t)p.max_pages * kPage;  // at most 2^30
   if (raw > most && rank == 0 && tid == 0 && h == 0 && p.status)
     atomicOr(p.status, KDA_STATUS_BAD_PAGE);
-  const int64_t len = raw < most ? raw : most;
-  const int pages = (int)((len + kPage - 1) / kPage), per = (pages + cs - 1) / cs;
+  const int len = (int)(raw < most ? raw : most);
+  const int pages = (len + kPage - 1) / kPage, per = (pages + cs - 1) / cs;
   const int pg0 = min(pages, rank * per), pg1 = min(pages, pg0 + per);
-  const int64_t first = (int64_t)pg0 * kPage;
-  const int n = (int)((int64_t)pg1 * kPage < len ? (pg1 - pg0) * kPage : len - first > 0 ? len - first : 0);
+  const int first = pg0 * kPage;
+  const int n = max(0, min(pg1 * kPage, len) - first);
   const int32_t* table = p.table + (int64_t)b * p.max_pages;
+  // the warp's positions: w0 .. w1 - 1 of the CTA's, four on end to a lane, 128 at a time
+  const int span = (n + kEWarps * 128 - 1) / (kEWarps * 128) * 128;
+  const int w0 = min(n, warp * span), w1 = min(n, w0 + span);
 
-  auto key_at = [&](int i) -> uint32_t {
-    const int64_t pos = first + i;
-    const int id = table[pos / kPage];
-    if (id < 0 || id >= p.n_pages) return 0u;
-    if (pos < p.sinks || pos >= len - p.recent) return 0xffffffffu;
-    return weight_key(p.weights[((int64_t)id * p.Hkv + h) * kPage + (pos & (kPage - 1))]);
+  // the keys of four positions i + .., from the weights
+  constexpr int kBatch = 4;
+  auto load = [&](int i0, int batch, uint4 (&k)[kBatch]) {
+    int id[kBatch];
+    float4 w[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * 128 + lane * 4;
+      id[u] = u < batch && i < w1 ? table[(first + i) / kPage] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int pos = first + i0 + u * 128 + lane * 4;
+      w[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (id[u] >= 0 && id[u] < p.n_pages)
+        w[u] = *reinterpret_cast<const float4*>(
+            p.weights + ((int64_t)id[u] * p.Hkv + h) * kPage + (pos & (kPage - 1)));
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int pos = first + i0 + u * 128 + lane * 4;
+      auto key = [&](int at, float x) -> uint32_t {
+        if (id[u] < 0 || id[u] >= p.n_pages || at >= len) return 0u;
+        return at < p.sinks || at >= len - p.recent ? 0xffffffffu : weight_key(x);
+      };
+      k[u] = make_uint4(key(pos, w[u].x), key(pos + 1, w[u].y), key(pos + 2, w[u].z),
+                        key(pos + 3, w[u].w));
+      if (id[u] >= p.n_pages && h == 0 && p.status) atomicOr(p.status, KDA_STATUS_BAD_PAGE);
+    }
   };
-  auto get = [&](int i) -> uint32_t { return i < cap ? s_key[i] : key_at(i); };
+  auto get = [&](int i0) -> uint4 {
+    const int i = i0 + lane * 4;
+    if (i0 + 128 <= cap) return i < w1 ? *reinterpret_cast<const uint4*>(s_key + i)
+                                       : make_uint4(0, 0, 0, 0);
+    uint4 k[kBatch];
+    load(i0, 1, k);
+    return k[0];
+  };
+  // counts the digits k >> shift & mask of the keys that agree with `prefix` in the bits `above`
+  auto count = [&](uint32_t* bins, const uint4& k4, uint32_t prefix, uint32_t above, int shift,
+                   uint32_t mask) {
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+    bool same = true;
+    const uint32_t lead = __shfl_sync(0xffffffffu, k4.x, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) same &= k[j] != 0u && ((k[j] ^ lead) >> shift) == 0u;
+    if (__all_sync(0xffffffffu, same)) {  // equal weights, kept ends: one addition
+      if (((lead ^ prefix) & above) == 0u && lane == 0) atomicAdd(&bins[(lead >> shift) & mask], 128u);
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (k[j] != 0u && ((k[j] ^ prefix) & above) == 0u) atomicAdd(&bins[(k[j] >> shift) & mask], 1u);
+  };
 
-  // keys, and how many candidates there are
-  if (tid < 2) s_count[tid] = 0;
   __syncthreads();
-  uint32_t mine = 0;
-  for (int i = tid; i < n; i += kEThreads) {
-    const uint32_t k = key_at(i);
-    if (i < cap) s_key[i] = k;
-    mine += k != 0u;
-    if (k == 0u && (i & (kPage - 1)) == 0 && h == 0 && p.status &&
-        table[(first + i) / kPage] >= p.n_pages)
-      atomicOr(p.status, KDA_STATUS_BAD_PAGE);
+#pragma unroll 1
+  for (int i0 = w0; i0 < w1; i0 += kBatch * 128) {
+    uint4 k[kBatch];
+    load(i0, kBatch, k);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * 128;
+      if (i >= w1) break;
+      if (i + 128 <= cap && i + lane * 4 < w1) *reinterpret_cast<uint4*>(s_key + i + lane * 4) = k[u];
+      count(hist[0], k[u], 0u, 0u, 21, 2047u);
+    }
   }
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  if (lane == 0) atomicAdd(&s_count[0], mine);
-  ptx::cluster_sync();
-  uint32_t all = 0;
-  for (int c = 0; c < cs; ++c) all += ld_cluster_u32(&s_count[0], c);
-  const uint32_t want = min(all, (uint32_t)p.budget);
 
   // the smallest kept key, and how many of that value are kept: digits from the top
-  uint32_t prefix = 0, left = want;
+  uint32_t prefix = 0, left = 0, want = 0;
+#pragma unroll 1
+  for (int round = 0; round < 3; ++round) {
+    const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
+    if (round > 0) {
+      const uint32_t above = 0xffffffffu << (round == 1 ? 21 : 10);
+#pragma unroll 1
+      for (int i0 = w0; i0 < w1; i0 += 128)
+        count(hist[round], get(i0), prefix, above, shift, round == 1 ? 2047u : 1023u);
+    }
+    ptx::cluster_sync();
+    // this thread's four bins, the highest digits to the first threads
+    const int bin = kEBins - 4 - 4 * tid;
+    uint32_t t[4] = {0, 0, 0, 0};
+    for (int c = 0; c < cs; ++c) {
+      const uint4 v = ld_cluster_u32x4(&hist[round][bin], c);
+      t[0] += v.w; t[1] += v.z; t[2] += v.y; t[3] += v.x;
+    }
+    const uint32_t sum = t[0] + t[1] + t[2] + t[3];
+    uint32_t upto = scan_lanes(sum, lane);
+    if (lane == 31) warp_sum[warp] = upto;
+    __syncthreads();
+    const uint32_t of_warps = scan_lanes(lane < kEWarps ? warp_sum[lane] : 0u, lane);
+    if (warp > 0) upto += __shfl_sync(0xffffffffu, of_warps, warp - 1);
+    if (round == 0) {
+      want = min(__shfl_sync(0xffffffffu, of_warps, 31), (uint32_t)p.budget);
+      left = want;
+      if (want == 0) break;  // (in the whole cluster)
+    }
+    uint32_t before = upto - sum;
+    if (before < left && left <= upto) {
+      int j = 0;
+      while (before + t[j] < left) before += t[j++];
+      s_pick[0] = (uint32_t)(bin + 3 - j);
+      s_pick[1] = left - before;
+    }
+    __syncthreads();
+    prefix |= s_pick[0] << shift;
+    left = s_pick[1];
+  }
+
+  // `prefix` is the smallest kept key; `left` of its positions are kept, the earliest ones.
+  // Where this warp's positions begin among the kept: counts of the warps and CTAs before it.
+  auto counts = [&](const uint4& k, uint32_t& gt, uint32_t& eq) {
+    gt = (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix);
+    eq = (k.x == prefix) + (k.y == prefix) + (k.z == prefix) + (k.w == prefix);
+  };
+  uint32_t gt = 0, eq = 0;
   if (want > 0) {
 #pragma unroll 1
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      const uint32_t above = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      for (int i0 = 0; i0 < n; i0 += kEThreads) {
-        const int i = i0 + tid;
-        const uint32_t k = i < n ? get(i) : 0u;
-        const bool in = k != 0u && ((k ^ prefix) & above) == 0u;
-        // one addition per distinct digit of the warp
-        const uint32_t digit = in ? (k >> shift) & 255u : 256u;
-        const uint32_t same = __match_any_sync(0xffffffffu, digit);
-        if (in && (int)(__ffs(same) - 1) == lane) atomicAdd(&hist[digit], __popc(same));
-      }
-      ptx::cluster_sync();
-      if (tid < 256) {
-        uint32_t sum = 0;
-        for (int c = 0; c < cs; ++c) sum += ld_cluster_u32(&hist[tid], c);
-        total[tid] = sum;
-      }
-      __syncthreads();
-      if (warp == 0) {
-        // lane l owns digits 255 - 8 l .. 248 - 8 l
-        uint32_t sum = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum += total[255 - 8 * lane - i];
-        uint32_t upto = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t u = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += u;
-        }
-        const uint32_t before = upto - sum;
-        if (before < left && left <= upto) {
-          uint32_t c = before;
-          int d = 255 - 8 * lane;
-          while (c + total[d] < left) c += total[d--];
-          s_pick[0] = (uint32_t)d;
-          s_pick[1] = left - c;
-        }
-      }
-      ptx::cluster_sync();  // counts are read before they are cleared
-      prefix |= s_pick[0] << shift;
-      left = s_pick[1];
-      __syncthreads();
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+      uint32_t g1, e1;
+      counts(get(i0), g1, e1);
+      gt += g1;
+      eq += e1;
     }
-  }
-  // `prefix` is the smallest kept key; `left` of its positions are kept, the earliest ones.
-  // Where this CTA's positions begin among the kept: counts of the CTAs before it.
-  uint32_t gt = 0, eq = 0;
-  for (int i = tid; i < n; i += kEThreads) {
-    const uint32_t k = get(i);
-    gt += want > 0 && k > prefix;
-    eq += want > 0 && k == prefix;
-  }
-  gt = __reduce_add_sync(0xffffffffu, gt);
-  eq = __reduce_add_sync(0xffffffffu, eq);
-  if (lane == 0) {
-    warp_gt[warp] = gt;
-    warp_eq[warp] = eq;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    gt = eq = 0;
-    for (int w = 0; w < kEWarps; ++w) {
-      gt += warp_gt[w];
-      eq += warp_eq[w];
-    }
-    s_count[0] = gt;
-    s_count[1] = eq;
-  }
-  ptx::cluster_sync();
-  uint32_t gt0 = 0, eq0 = 0;
-  for (int c = 0; c < rank; ++c) {
-    gt0 += ld_cluster_u32(&s_count[0], c);
-    eq0 += ld_cluster_u32(&s_count[1], c);
-  }
-  for (int i0 = 0; i0 < n && want > 0; i0 += kEThreads) {
-    const int i = i0 + tid;
-    const uint32_t k = i < n ? get(i) : 0u;
-    const bool is_gt = k > prefix, is_eq = k == prefix && k != 0u;
-    const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    if (lane == 0) warp_count[warp] = make_uint2(gt, eq);
     __syncthreads();
-    if (lane == 0) {
-      warp_gt[warp] = __popc(bg);
-      warp_eq[warp] = __popc(be);
+    const uint2 wc = lane < kEWarps ? warp_count[lane] : make_uint2(0, 0);
+    gt = __reduce_add_sync(0xffffffffu, lane < warp ? wc.x : 0u);
+    eq = __reduce_add_sync(0xffffffffu, lane < warp ? wc.y : 0u);
+    if (warp == kEWarps - 1 && lane == 0) {
+      s_count[0] = gt + warp_count[warp].x;
+      s_count[1] = eq + warp_count[warp].y;
     }
-    __syncthreads();
-    uint32_t g1 = gt0, e1 = eq0;
-    for (int w = 0; w < kEWarps; ++w) {
-      if (w < warp) {
-        g1 += warp_gt[w];
-        e1 += warp_eq[w];
-      }
-      gt0 += warp_gt[w];
-      eq0 += warp_eq[w];
-    }
-    const uint32_t below = (1u << lane) - 1u;
-    g1 += __popc(bg & below);
-    e1 += __popc(be & below);
-    if (is_gt || (is_eq && e1 < left)) kept[g1 + min(e1, left)] = (int32_t)(first + i);
+    ptx::cluster_sync();
+    uint64_t of_cta = 0;
+    if (lane < rank) of_cta = ptx::ld_cluster_u64(reinterpret_cast<const uint64_t*>(s_count), lane);
+    gt += __reduce_add_sync(0xffffffffu, (uint32_t)of_cta);
+    eq += __reduce_add_sync(0xffffffffu, (uint32_t)(of_cta >> 32));
   }
-  for (int64_t i = (int64_t)want + rank * kEThreads + tid; i < p.budget; i += cs * kEThreads)
-    kept[i] = -1;
+  __syncwarp();
+  ptx::cluster_arrive();  // this thread has read the others' counts; waited for below
+  if (want > 0) {
+#pragma unroll 1
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+      const uint4 k4 = get(i0);
+      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+      uint32_t g1, e1;
+      counts(k4, g1, e1);
+      const uint32_t own = g1 | e1 << 16, upto = scan_lanes(own, lane);
+      uint32_t g = gt + ((upto - own) & 0xffffu), e = eq + ((upto - own) >> 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool is_eq = k[j] == prefix;
+        if (k[j] > prefix || (is_eq && e < left)) kept[g + min(e, left)] = first + i0 + lane * 4 + j;
+        g += k[j] > prefix;
+        e += is_eq;
+      }
+      const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+      gt += all & 0xffffu;
+      eq += all >> 16;
+    }
+  }
+  for (int i = (int)want + rank * kEThreads + tid; i < p.budget; i += cs * kEThreads) kept[i] = -1;
   if (rank == 0 && tid == 0 && h == 0) p.new_length[b] = (int32_t)want;
-  ptx::cluster_sync();  // no CTA leaves while its counts are read
+  __syncwarp();
+  ptx::cluster_wait();  // no CTA leaves while its counts are read
 }
 
 // Moves 64 kept tokens of a head into a new page. The page's scale is the largest of the tokens'
@@ -668,54 +726,63 @@ constexpr int kMThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kMThreads) evict_move_kernel(const EvictParams p) {
   __shared__ int64_t src[kPage];      // row of the caches, -1: none
-  __shared__ float ratio[2][kPage];
+  __shared__ float scale[2][kPage];
   const int width = (p.budget + kPage - 1) / kPage;
   const int pg = blockIdx.x % width, h = blockIdx.y, b = blockIdx.x / width;
-  const int count = p.new_length[b];
-  if (count < 0 || (int64_t)pg * kPage >= count) return;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   int dst = -1;
   if (pg < p.new_max_pages) dst = p.new_table[(int64_t)b * p.new_max_pages + pg];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what is kept, of the kernel before
+  const int i = pg * kPage + tid;
+  int pos = 0;
+  if (tid < kPage && i < p.budget) pos = p.kept[((int64_t)b * p.Hkv + h) * p.budget + i];
+  const int count = p.new_length[b];
+  if (count < 0 || (int64_t)pg * kPage >= count) return;
   if (pg >= p.new_max_pages || dst >= p.n_pages) {
     if (tid == 0 && h == 0 && p.status) atomicOr(p.status, KDA_STATUS_BAD_PAGE);
     return;
   }
   if (dst < 0) return;
-  if (tid < 64) {
-    const int i = pg * kPage + tid;
-    int64_t row = -1;
-    float s[2] = {0.0f, 0.0f}, w = 0.0f;
+  int64_t slice = 0, row = -1;
+  if (tid < kPage) {
     if (i < count) {
-      const int pos = p.kept[((int64_t)b * p.Hkv + h) * p.budget + i];
-      const int64_t slice =
-          (int64_t)p.table[(int64_t)b * p.max_pages + pos / kPage] * p.Hkv + h;
+      slice = (int64_t)p.table[(int64_t)b * p.max_pages + pos / kPage] * p.Hkv + h;
       row = slice * kPage + (pos & (kPage - 1));
-      s[0] = p.scale[0][slice];
-      s[1] = p.scale[1][slice];
-      w = p.weights[row];
     }
     src[tid] = row;
-    ratio[0][tid] = s[0];
-    ratio[1][tid] = s[1];
-    p.weights[((int64_t)dst * p.Hkv + h) * kPage + tid] = w;
   }
   __syncthreads();
-  float top[2] = {0.0f, 0.0f};
-  for (int i = 0; i < kPage; ++i) {
-    top[0] = fmaxf(top[0], ratio[0][i]);
-    top[1] = fmaxf(top[1], ratio[1][i]);
+  constexpr int LPR = D / 16, ROWS = kMThreads / LPR, N = kPage / ROWS;
+  const int part = tid % LPR * 16, r0 = tid / LPR;
+  uint4 c[2][N];
+#pragma unroll
+  for (int side = 0; side < 2; ++side)
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int64_t at = src[r0 + k * ROWS];
+      if (at >= 0) c[side][k] = __ldcs(reinterpret_cast<const uint4*>(p.code[side] + at * D + part));
+    }
+  if (tid < kPage) {
+    scale[0][tid] = row < 0 ? 0.0f : p.scale[0][slice];
+    scale[1][tid] = row < 0 ? 0.0f : p.scale[1][slice];
+    p.weights[((int64_t)dst * p.Hkv + h) * kPage + tid] = row < 0 ? 0.0f : p.weights[row];
   }
-  constexpr int LPR = D / 16, ROWS = kMThreads / LPR;
+  __syncthreads();
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
-    uint8_t* out = p.code[side] + ((int64_t)dst * p.Hkv + h) * (int64_t)(kPage * D);
+    float top = fmaxf(scale[side][lane], scale[side][lane + 32]);
 #pragma unroll
-    for (int r = tid / LPR; r < kPage; r += ROWS) {
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    uint8_t* out = p.code[side] + ((int64_t)dst * p.Hkv + h) * (int64_t)(kPage * D) + part;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int r = r0 + k * ROWS;
       if (src[r] < 0) continue;
-      uint4 c = *reinterpret_cast<const uint4*>(p.code[side] + src[r] * D + (tid % LPR) * 16);
-      const float f = ratio[side][r] == top[side] ? 1.0f : ratio[side][r] / top[side];
-      if (f != 1.0f) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&c);
+      uint4 v = c[side][k];
+      const float old = scale[side][r];
+      if (old != top) {
+        const float f = old / top;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 x = f32x2_from_f16x2(f16x2_from_e4m3(w[j] & 0xffffu));
@@ -723,10 +790,10 @@ __global__ void __launch_bounds__(kMThreads) evict_move_kernel(const EvictParams
           w[j] = e4m3x2_from_f32(x.x * f, x.y * f) | e4m3x2_from_f32(y.x * f, y.y * f) << 16;
         }
       }
-      *reinterpret_cast<uint4*>(out + r * D + (tid % LPR) * 16) = c;
+      *reinterpret_cast<uint4*>(out + r * D) = v;
     }
+    if (tid == 0) p.scale[side][(int64_t)dst * p.Hkv + h] = top;
   }
-  if (tid < 2) p.scale[tid][(int64_t)dst * p.Hkv + h] = top[tid];
 }
 
 }  // namespace
@@ -751,8 +818,14 @@ kda_status launch_cache_evict(const EvictParams& p, int d, cudaStream_t s) {
   int cs = 1;
   while (cs < 8 && (int64_t)p.max_pages * kPage > (int64_t)cs * 8192) cs *= 2;
   const int64_t per = ((int64_t)p.max_pages + cs - 1) / cs * kPage;
-  const int cap = (int)(per < 49152 ? per : 49152);
-  cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, cap * 4);
+  const int cap = (int)(per < kEMaxKeys ? per : kEMaxKeys);
+  static bool set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !set[dev]) {
+    cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEMaxKeys * 4);
+    if (dev >= 0 && dev < 64) set[dev] = true;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * cs));
   cfg.blockDim = dim3(kEThreads);
@@ -765,12 +838,18 @@ kda_status launch_cache_evict(const EvictParams& p, int d, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   cudaLaunchKernelEx(&cfg, evict_select_kernel, p, cs, cap);
-  const dim3 grid((unsigned)p.batch * ((p.budget + kPage - 1) / kPage), (unsigned)p.Hkv);
-  if (grid.x > 0) {
-    if (d == 128) evict_move_kernel<128><<<grid, kMThreads, 0, s>>>(p);
-    else evict_move_kernel<64><<<grid, kMThreads, 0, s>>>(p);
+  count_launches(1);
+  if (p.budget > 0) {  // its CTAs start while the last of the selection run
+    cfg.gridDim = dim3((unsigned)p.batch * ((p.budget + kPage - 1) / kPage), (unsigned)p.Hkv);
+    cfg.blockDim = dim3(kMThreads);
+    cfg.dynamicSmemBytes = 0;
+    at[0] = {};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    if (d == 128) cudaLaunchKernelEx(&cfg, evict_move_kernel<128>, p);
+    else cudaLaunchKernelEx(&cfg, evict_move_kernel<64>, p);
+    count_launches(1);
   }
-  count_launches(grid.x > 0 ? 2 : 1);
   return check_launch("kda_cache_evict");
 }
 
