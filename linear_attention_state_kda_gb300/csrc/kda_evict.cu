@@ -481,13 +481,15 @@ kda_status launch_weigh_t(const WeighParams& p, cudaStream_t s) {
 // is kept by three rounds of counts (digits of 11, 11 and 10 bits, the first counted as the weights
 // arrive), then writes the kept positions in order, each warp those of its own range. Latency: five
 // cluster barriers around passes over shared memory. (Four rounds of 8 bits, warps agreeing on
-// their distinct digits before they count, took 69 us for 32 rows of 16384 tokens and 8 heads;
-// EVICT_SELECT now.)
+// their distinct digits before they count, took 69 us for 32 rows of 16384 tokens and 8 heads; this
+// takes 31. 3 rows of 500: 9 us, nearly all latency.)
 // The second moves the kept tokens, one CTA per (new page, head). It is bound by the codes, read
-// and written once: all of a thread's loads are in flight before the page's scale is known.
+// and written once: all of a thread's loads are in flight before the page's scale is known. 32 rows
+// of 4096 kept tokens: 88 us, 6.1 TB/s (102 us with the loads after the scale).
 constexpr int kEThreads = 512;
 constexpr int kEWarps = kEThreads / 32;
 constexpr int kEBins = 2048;
+static_assert(kEThreads * 4 >= kEBins, "a thread adds up four bins");
 constexpr int kEMaxKeys = 49152;  // of a CTA in shared memory; later ones are read again
 
 // Orders like the weights; NaN lowest, zeros of both signs equal. 0 is no candidate.
@@ -585,21 +587,21 @@ __global__ void __launch_bounds__(kEThreads) evict_select_kernel(const EvictPara
     load(i0, 1, k);
     return k[0];
   };
-  // counts the digits k >> shift & mask of the keys that agree with `prefix` in the bits `above`
-  auto count = [&](uint32_t* bins, const uint4& k4, uint32_t prefix, uint32_t above, int shift,
-                   uint32_t mask) {
+  // counts digits (k - prefix) >> shift of the keys in prefix .. prefix + 2^bits - 1
+  auto count = [&](uint32_t* bins, const uint4& k4, bool (&in)[4], uint32_t prefix, int shift) {
     const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-    bool same = true;
+    if (!__any_sync(0xffffffffu, in[0] | in[1] | in[2] | in[3])) return;
     const uint32_t lead = __shfl_sync(0xffffffffu, k4.x, 0);
+    bool same = in[0] & in[1] & in[2] & in[3];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) same &= k[j] != 0u && ((k[j] ^ lead) >> shift) == 0u;
+    for (int j = 0; j < 4; ++j) same &= (k[j] ^ lead) >> shift == 0u;
     if (__all_sync(0xffffffffu, same)) {  // equal weights, kept ends: one addition
-      if (((lead ^ prefix) & above) == 0u && lane == 0) atomicAdd(&bins[(lead >> shift) & mask], 128u);
+      if (lane == 0) atomicAdd(&bins[(lead - prefix) >> shift], 128u);
       return;
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (k[j] != 0u && ((k[j] ^ prefix) & above) == 0u) atomicAdd(&bins[(k[j] >> shift) & mask], 1u);
+      if (in[j]) atomicAdd(&bins[(k[j] - prefix) >> shift], 1u);
   };
 
   __syncthreads();
@@ -612,7 +614,8 @@ __global__ void __launch_bounds__(kEThreads) evict_select_kernel(const EvictPara
       const int i = i0 + u * 128;
       if (i >= w1) break;
       if (i + 128 <= cap && i + lane * 4 < w1) *reinterpret_cast<uint4*>(s_key + i + lane * 4) = k[u];
-      count(hist[0], k[u], 0u, 0u, 21, 2047u);
+      bool in[4] = {k[u].x != 0u, k[u].y != 0u, k[u].z != 0u, k[u].w != 0u};
+      count(hist[0], k[u], in, 0u, 21);
     }
   }
 
@@ -622,16 +625,21 @@ __global__ void __launch_bounds__(kEThreads) evict_select_kernel(const EvictPara
   for (int round = 0; round < 3; ++round) {
     const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
     if (round > 0) {
-      const uint32_t above = 0xffffffffu << (round == 1 ? 21 : 10);
+      // (keys 0 may be counted: they are below any that is kept)
+      const uint32_t range = round == 1 ? 1u << 21 : 1u << 10;
 #pragma unroll 1
-      for (int i0 = w0; i0 < w1; i0 += 128)
-        count(hist[round], get(i0), prefix, above, shift, round == 1 ? 2047u : 1023u);
+      for (int i0 = w0; i0 < w1; i0 += 128) {
+        const uint4 k = get(i0);
+        bool in[4] = {k.x - prefix < range, k.y - prefix < range, k.z - prefix < range,
+                      k.w - prefix < range};
+        count(hist[round], k, in, prefix, shift);
+      }
     }
     ptx::cluster_sync();
     // this thread's four bins, the highest digits to the first threads
     const int bin = kEBins - 4 - 4 * tid;
     uint32_t t[4] = {0, 0, 0, 0};
-    for (int c = 0; c < cs; ++c) {
+    for (int c = 0; c < cs && bin >= 0; ++c) {
       const uint4 v = ld_cluster_u32x4(&hist[round][bin], c);
       t[0] += v.w; t[1] += v.z; t[2] += v.y; t[3] += v.x;
     }
@@ -815,6 +823,8 @@ kda_status launch_cache_weigh(const WeighParams& p, kda_dtype dt, int d, cudaStr
 
 kda_status launch_cache_evict(const EvictParams& p, int d, cudaStream_t s) {
   const int64_t units = (int64_t)p.batch * p.Hkv;
+  // up to 8192 keys to a CTA. 32 rows of 16384, moves and read-back included: 243 us, as with 16384,
+  // and 263 with 4096; 8 rows of 32768: 133, 135 and 162 us.
   int cs = 1;
   while (cs < 8 && (int64_t)p.max_pages * kPage > (int64_t)cs * 8192) cs *= 2;
   const int64_t per = ((int64_t)p.max_pages + cs - 1) / cs * kPage;
