@@ -116,6 +116,15 @@ kda_status launch_window_t(const DecayParams& p, cudaStream_t s) {
 //     o_i = e^{gamma_i} scale S^T q_i + sum_{j <= i} e^{gamma_i - gamma_j} scale (q_i . k_j) v_j
 //     S'  = e^{gamma_C} S + sum_j e^{gamma_C - gamma_j} k_j v_j^T
 // The state is in registers (D/16 x 4 a thread), copied to shared memory for the first sum.
+#ifndef LB
+#define LB 512
+#endif
+#ifndef LF
+#define LF 256
+#endif
+#ifndef WF
+#define WF 304
+#endif
 constexpr int kC = 32;
 constexpr int kSimtThreads = 256;
 
@@ -143,8 +152,8 @@ decay_chunk_kernel(const DecayParams p, int seg, float* added, float* added_log)
 
   const int h = blockIdx.y, col0 = blockIdx.z * kCols, tid = threadIdx.x;
   Segment x;
-  if (!find_segment(p, seg, blockIdx.x, tid == 0 && h == 0 && blockIdx.z == 0, x)) return;
-  if (kStates && x.last) return;
+  if (!find_segment<kStates>(p, seg, blockIdx.x, tid & 31, tid == 0 && h == 0 && blockIdx.z == 0, x))
+    return;
   const int hk = h / (p.H / p.Hk);
   const int ty = tid >> 4, tx = tid & 15;
   const int r0 = ty * RPT, c0 = col0 + tx * 4;
@@ -249,22 +258,27 @@ decay_chunk_kernel(const DecayParams p, int seg, float* added, float* added_log)
         }
       }
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int row = i0 + m;
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) out[m][c] *= s_in[row];
-        for (int j = 0; j <= row; ++j) {  // later rows do not reach it, NaN included
-          const float w = sp[row * S::PP + j];
-          const float4 f = *reinterpret_cast<const float4*>(&sv[j * S::VP + tx * 4]);
-          out[m][0] = fmaf(w, f.x, out[m][0]); out[m][1] = fmaf(w, f.y, out[m][1]);
-          out[m][2] = fmaf(w, f.z, out[m][2]); out[m][3] = fmaf(w, f.w, out[m][3]);
-        }
-        if (row < n) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            st_elem((T*)p.o, ((t0 + row) * p.H + h) * D + c0 + c, p.scale * out[m][c]);
-        }
+        for (int c = 0; c < 4; ++c) out[m][c] *= s_in[i0 + m];
+      auto add = [&](float (&x)[4], float w, const float4& f) {
+        x[0] = fmaf(w, f.x, x[0]); x[1] = fmaf(w, f.y, x[1]);
+        x[2] = fmaf(w, f.z, x[2]); x[3] = fmaf(w, f.w, x[3]);
+      };
+      // later rows do not reach a row, NaN included
+      for (int j = 0; j <= i0; ++j) {
+        const float4 f = *reinterpret_cast<const float4*>(&sv[j * S::VP + tx * 4]);
+        add(out[0], sp[i0 * S::PP + j], f);
+        add(out[1], sp[(i0 + 1) * S::PP + j], f);
       }
+      add(out[1], sp[(i0 + 1) * S::PP + i0 + 1],
+          *reinterpret_cast<const float4*>(&sv[(i0 + 1) * S::VP + tx * 4]));
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        if (i0 + m < n)
+          *reinterpret_cast<float4*>((T*)p.o + ((t0 + i0 + m) * p.H + h) * D + c0) =
+              make_float4(p.scale * out[m][0], p.scale * out[m][1], p.scale * out[m][2],
+                          p.scale * out[m][3]);
     }
     const float a = s_total;
 #pragma unroll
@@ -275,12 +289,16 @@ decay_chunk_kernel(const DecayParams p, int seg, float* added, float* added_log)
       const float w = s_out[j];
       const float4 f = *reinterpret_cast<const float4*>(&sv[j * S::VP + tx * 4]);
       const float vv[4] = {f.x * w, f.y * w, f.z * w, f.w * w};
+      float kk[RPT];
 #pragma unroll
-      for (int i = 0; i < RPT; ++i) {
-        const float kk = sk[j * S::DP + r0 + i];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) st[i][c] = fmaf(kk, vv[c], st[i][c]);
+      for (int i = 0; i < RPT; i += 4) {
+        const float4 r = *reinterpret_cast<const float4*>(&sk[j * S::DP + r0 + i]);
+        kk[i] = r.x; kk[i + 1] = r.y; kk[i + 2] = r.z; kk[i + 3] = r.w;
       }
+#pragma unroll
+      for (int i = 0; i < RPT; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) st[i][c] = fmaf(kk[i], vv[c], st[i][c]);
     }
   }
   float* exit_state = nullptr;
@@ -304,13 +322,14 @@ template <int D>
 __global__ void __launch_bounds__(256)
 decay_scan_kernel(const DecayParams p, int seg, float* added, const float* added_log) {
   constexpr int kParts = D * D / 1024;
-  const int s = blockIdx.x / kParts, h = blockIdx.y;
-  const int64_t c0 = p.cu ? p.cu[s] : 0, c1 = p.cu ? p.cu[s + 1] : p.total;
-  if (c0 < 0 || c1 > p.total || c1 - c0 <= seg) return;
+  const int h = blockIdx.y;
+  Segment y;  // a sequence's first segment scans for all
+  if (!find_segment<true>(p, seg, blockIdx.x / kParts, threadIdx.x & 31, false, y) || !y.first) return;
+  const int64_t c0 = y.lo, c1 = p.cu ? p.cu[y.seq + 1] : p.total;
   const int e = (blockIdx.x % kParts * 256 + threadIdx.x) * 4;
   float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (p.init)
-    x = *reinterpret_cast<const float4*>(p.init + ((int64_t)s * p.H + h) * (D * D) + e);
+    x = *reinterpret_cast<const float4*>(p.init + ((int64_t)y.seq * p.H + h) * (D * D) + e);
   const int64_t first = c0 / seg, n = (c1 - c0 + seg - 1) / seg - 1;
   // four places at a time: their loads do not wait for one another
   for (int64_t j0 = first; j0 < first + n; j0 += 4) {
@@ -338,8 +357,8 @@ decay_scan_kernel(const DecayParams p, int seg, float* added, const float* added
 // a few chunks' worth of work outweighs the state that a segment has to write and read.
 int segment_tokens(kda_dtype dt, int total, int H, int d) {
   const int64_t units = (int64_t)H * (dt == KDA_BF16 ? 1 : d / kCols);
-  const int64_t want = units < 304 ? 304 / units : 1;
-  const int64_t seg = ((total + want - 1) / want + 63) / 64 * 64, least = dt == KDA_BF16 ? 512 : 256;
+  const int64_t all = dt == KDA_BF16 ? 304 : WF, want = units < all ? all / units : 1;
+  const int64_t seg = ((total + want - 1) / want + 63) / 64 * 64, least = dt == KDA_BF16 ? LB : LF;
   return (int)(seg < least ? least : seg);
 }
 
@@ -347,13 +366,20 @@ template <int D>
 kda_status launch_simt(const DecayParams& p, int seg, float* added, float* added_log,
                        cudaStream_t s) {
   const size_t smem = SimtShape<D>::floats * sizeof(float);
+  static bool set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !set[dev]) {
+    cudaFuncSetAttribute(decay_chunk_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         (int)smem);
+    cudaFuncSetAttribute(decay_chunk_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         (int)smem);
+    if (dev >= 0 && dev < 64) set[dev] = true;
+  }
   const dim3 grid((unsigned)(p.total / seg + p.n_seqs), (unsigned)p.H, D / kCols);
-  cudaFuncSetAttribute(decay_chunk_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       (int)smem);
-  cudaFuncSetAttribute(decay_chunk_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       (int)smem);
   if (p.total > seg) {
-    decay_chunk_kernel<D, true><<<grid, kSimtThreads, smem, s>>>(p, seg, added, added_log);
+    const dim3 places((unsigned)(p.total / seg), (unsigned)p.H, D / kCols);
+    decay_chunk_kernel<D, true><<<places, kSimtThreads, smem, s>>>(p, seg, added, added_log);
     launch_decay_scan(p, D, seg, added, added_log, s);
     count_launches(1);
   }
@@ -368,7 +394,7 @@ namespace decay {
 
 void launch_decay_scan(const DecayParams& p, int d, int seg, float* added, const float* added_log,
                        cudaStream_t s) {
-  const dim3 grid((unsigned)p.n_seqs * (unsigned)(d * d / 1024), (unsigned)p.H);
+  const dim3 grid((unsigned)(p.total / seg * (d * d / 1024)), (unsigned)p.H);
   if (d == 128) decay_scan_kernel<128><<<grid, 256, 0, s>>>(p, seg, added, added_log);
   else decay_scan_kernel<64><<<grid, 256, 0, s>>>(p, seg, added, added_log);
   count_launches(1);

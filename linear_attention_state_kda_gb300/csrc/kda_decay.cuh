@@ -22,20 +22,25 @@ struct Segment {
   bool first, last;    // of its sequence
 };
 
-// The segment in a slot; false: none. `flag`: report malformed offsets. (Offsets are at most 2^30, so
-// that 32 bits do; a negative one is malformed.)
-__device__ __forceinline__ bool find_segment(const DecayParams& p, int seg, int slot, bool flag,
-                                             Segment& x) {
-  int a = 0, b = p.n_seqs - 1;  // the last sequence whose first slot is <= slot
+// The segment in a slot, or (kPlaces) the one with a place, i.e. not its sequence's last; false: none.
+// `flag`: report malformed offsets. (Offsets are at most 2^30, so that 32 bits do; a negative one is
+// malformed.) By a whole warp, whose lanes probe 32 sequences at once.
+template <bool kPlaces>
+__device__ __forceinline__ bool find_segment(const DecayParams& p, int seg, int slot, int lane,
+                                             bool flag, Segment& x) {
+  int a = 0;  // the last sequence whose first slot (or place) is <= slot: among n from a on
   if (p.cu) {
-    while (a < b) {
-      const int m = (a + b + 1) >> 1;
-      if (p.cu[m] / seg + m <= slot) a = m;
-      else b = m - 1;
+    for (int n = p.n_seqs; n > 1;) {
+      const int step = (n + 31) / 32, off = lane * step, m = a + off;
+      bool upto = lane == 0;
+      if (lane > 0 && off < n) upto = p.cu[m] / seg + (kPlaces ? 0 : m) <= slot;
+      const int last = (31 - __clz(__ballot_sync(0xffffffffu, upto))) * step;
+      a += last;
+      n = min(step, n - last);
     }
   }
   int c0 = p.cu ? p.cu[a] : 0, c1 = p.cu ? p.cu[a + 1] : p.total;
-  const int j = slot - (c0 / seg + a);
+  const int j = slot - (c0 / seg + (kPlaces ? 0 : a));
   if (j < 0) return false;
   if (c0 < 0 || c1 > p.total || c1 < c0) {
     if (flag && p.status) atomicOr(p.status, KDA_STATUS_BAD_OFFSETS);
@@ -49,7 +54,7 @@ __device__ __forceinline__ bool find_segment(const DecayParams& p, int seg, int 
   x.first = j == 0;
   x.last = x.hi == c1;
   x.place = c0 / seg + j;
-  return x.first || x.lo < c1;
+  return kPlaces ? !x.last : x.first || x.lo < c1;
 }
 
 // Sums of log-decays, in base-2 exponents, as pairs of floats (high + low part): their error stays

@@ -58,7 +58,7 @@ struct Unit {
   int place;  // -1: there are no more units
 };
 struct UnitRing {
-  uint64_t full[kUnits], empty[kUnits], clc;
+  uint64_t full[kUnits], empty[kUnits], clc, ask;
   alignas(16) uint32_t response[4];
   Unit unit[kUnits];
 };
@@ -234,11 +234,6 @@ __device__ __forceinline__ void schedule(UnitRing& ring, const Waiter& wait, int
 #pragma unroll 1
   while (ok) {
     const bool more = block >= 0;
-    if (more && lane == 0) {  // the next one, while this one's segment is found
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive_expect_tx(&ring.clc, 16);
-      ptx::clc_try_cancel(ring.response, &ring.clc);
-    }
     Unit u;
     u.place = -1;
     if (!more || find(block, u)) {
@@ -248,9 +243,16 @@ __device__ __forceinline__ void schedule(UnitRing& ring, const Waiter& wait, int
         ring.unit[at] = u;
         ptx::mbar_arrive(&ring.full[at]);
       }
+      // the next is taken late, so that no CTA sits on units that another could begin
+      if (more && ok) ok = wait(&ring.ask, n & 1);
       ++n;
     }
-    if (!more) break;
+    if (!more || !ok) break;
+    if (lane == 0) {
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive_expect_tx(&ring.clc, 16);
+      ptx::clc_try_cancel(ring.response, &ring.clc);
+    }
     if (!wait(&ring.clc, asked++ & 1)) {
       ok = false;
       break;
@@ -304,6 +306,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
       ptx::mbar_init(&sm.units.empty[i], 2);
     }
     ptx::mbar_init(&sm.units.clc, 1);
+    ptx::mbar_init(&sm.units.ask, 1);
     ptx::mbar_init(&sm.sc_full, 1);
     ptx::mbar_init(&sm.sc_empty, 4);
     for (int i = 0; i < 2; ++i) {
@@ -448,6 +451,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
           c.tokens = (short)(u.hi - t < kC ? u.hi - t : kC);
           c.kind = (short)((t == u.lo ? kFirst : 0) | (u.hi - t <= kC ? kLast : 0));
           c.exit = c.kind & kLast ? u.exit : nullptr;
+          if ((c.kind & kLast) && lane == 0) ptx::mbar_arrive(&sm.units.ask);
           if (n >= kStages && !(ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1))) break;
           if (lane == 0) {
             sm.chunk[s] = c;
@@ -514,7 +518,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
       schedule(sm.units, wait, lane, [&](int block, Unit& u) {
         const int h = block % p.H;
         Segment x;
-        if (!find_segment(p, seg, block / p.H, lane == 0 && h == 0, x)) return false;
+        if (!find_segment<false>(p, seg, block / p.H, lane, lane == 0 && h == 0, x)) return false;
         u.lo = (int)x.lo;
         u.hi = (int)x.hi;
         u.head = h;
@@ -877,6 +881,7 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
       ptx::mbar_init(&sm.units.empty[i], 2);
     }
     ptx::mbar_init(&sm.units.clc, 1);
+    ptx::mbar_init(&sm.units.ask, 1);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sm.v_full[i], 2 * NQ);
       ptx::mbar_init(&sm.v_empty[i], 1);
@@ -919,6 +924,7 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
 #pragma unroll 1
       for (int i = 0; i < N; ++i, ++n) {
         const int s = n % kStages, t = u.lo + (N - 1 - i) * kC;
+        if (i == N - 1 && lane == 0) ptx::mbar_arrive(&sm.units.ask);
         if (n >= kStages && !(ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1))) break;
         if (lane == 0) {
           uint8_t* st = smem + s * M::STAGE;
@@ -984,7 +990,7 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
     // ------------------------------------------------------------------ the units
     schedule(sm.units, wait, lane, [&](int block, Unit& u) {
       Segment x;
-      if (!find_segment(p, seg, block / p.H, false, x) || x.last) return false;
+      if (!find_segment<true>(p, seg, block / p.H, lane, false, x)) return false;
       u.lo = (int)x.lo;
       u.hi = (int)x.hi;
       u.head = block % p.H;
@@ -1124,7 +1130,7 @@ kda_status launch_d(const DecayParams& p, int seg, float* added, float* added_lo
   }
   const int slots = p.total / seg + p.n_seqs;
   if (p.total > seg) {
-    decay_add_kernel<D><<<(unsigned)(slots * p.H), kAddThreads, add_bytes, s>>>(m, p, seg, added,
+    decay_add_kernel<D><<<(unsigned)(p.total / seg * p.H), kAddThreads, add_bytes, s>>>(m, p, seg, added,
                                                                                added_log);
     launch_decay_scan(p, D, seg, added, added_log, s);
     count_launches(1);
