@@ -361,33 +361,41 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
 #pragma unroll 1
       for (int n = 0;; ++n) {
         const int s = n % kStages;
-        if (!wait(&sm.full[s], (n / kStages) & 1) || (n > 0 && !wait(&sm.kv_done, (n - 1) & 1))) break;
-        ptx::tc_fence_after();
+        if (!wait(&sm.full[s], (n / kStages) & 1)) break;
         c = sm.chunk[s];
         const int kind = __shfl_sync(0xffffffffu, c.kind, 0);
         if (kind & (kFirst | kStop)) {
-          // the unit before ends: its state goes out, and the next one's comes in
+          // the unit before ends: its state goes out, and the next one's, asked for before, comes in
+          float f[D / 2];
+#pragma unroll
+          for (int b = 0; b < D / 2; ++b)
+            f[b] = kind != kStop && c.entry ? __ldg(c.entry + at + b * D) : 0.0f;
+          if (n > 0 && !wait(&sm.kv_done, (n - 1) & 1)) break;
+          ptx::tc_fence_after();
           if (exit_state) {
 #pragma unroll 1
             for (int b = 0; b < D / 2; b += 16) {
-              uint32_t f[16];
-              ptx::tmem_ld16_nowait(t_s + b, f);
+              uint32_t x[16];
+              ptx::tmem_ld16_nowait(t_s + b, x);
               ptx::tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(f[i]));
+              for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[i]));
 #pragma unroll
-              for (int i = 0; i < 16; ++i) exit_state[at + (b + i) * D] = __uint_as_float(f[i]);
+              for (int i = 0; i < 16; ++i) exit_state[at + (b + i) * D] = __uint_as_float(x[i]);
             }
           }
           if (kind == kStop) break;
-#pragma unroll 1
-          for (int b = 0; b < D / 2; b += 16) {
-            float f[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = c.entry ? __ldg(c.entry + at + (b + i) * D) : 0.0f;
-            ptx::tmem_st16(t_s + b, f);
+          for (int b = 0; b < D / 2; b += 16) {
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = f[b + i];
+            ptx::tmem_st16(t_s + b, x);
           }
           ptx::tmem_st_wait();
+        } else {
+          if (!wait(&sm.kv_done, (n - 1) & 1)) break;
+          ptx::tc_fence_after();
         }
         exit_state = c.exit;
         const float a = ptx::ex2_approx(sm.total[s].x + sm.total[s].y);
