@@ -116,15 +116,6 @@ kda_status launch_window_t(const DecayParams& p, cudaStream_t s) {
 //     o_i = e^{gamma_i} scale S^T q_i + sum_{j <= i} e^{gamma_i - gamma_j} scale (q_i . k_j) v_j
 //     S'  = e^{gamma_C} S + sum_j e^{gamma_C - gamma_j} k_j v_j^T
 // The state is in registers (D/16 x 4 a thread), copied to shared memory for the first sum.
-#ifndef LB
-#define LB 512
-#endif
-#ifndef LF
-#define LF 256
-#endif
-#ifndef WF
-#define WF 304
-#endif
 constexpr int kC = 32;
 constexpr int kSimtThreads = 256;
 
@@ -323,6 +314,8 @@ __global__ void __launch_bounds__(256)
 decay_scan_kernel(const DecayParams p, int seg, float* added, const float* added_log) {
   constexpr int kParts = D * D / 1024;
   const int h = blockIdx.y;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   Segment y;  // a sequence's first segment scans for all
   if (!find_segment<true>(p, seg, blockIdx.x / kParts, threadIdx.x & 31, false, y) || !y.first) return;
   const int64_t c0 = y.lo, c1 = p.cu ? p.cu[y.seq + 1] : p.total;
@@ -357,8 +350,8 @@ decay_scan_kernel(const DecayParams p, int seg, float* added, const float* added
 // a few chunks' worth of work outweighs the state that a segment has to write and read.
 int segment_tokens(kda_dtype dt, int total, int H, int d) {
   const int64_t units = (int64_t)H * (dt == KDA_BF16 ? 1 : d / kCols);
-  const int64_t all = dt == KDA_BF16 ? 304 : WF, want = units < all ? all / units : 1;
-  const int64_t seg = ((total + want - 1) / want + 63) / 64 * 64, least = dt == KDA_BF16 ? LB : LF;
+  const int64_t all = dt == KDA_BF16 ? 304 : 608, want = units < all ? all / units : 1;
+  const int64_t seg = ((total + want - 1) / want + 63) / 64 * 64, least = dt == KDA_BF16 ? 512 : 64;
   return (int)(seg < least ? least : seg);
 }
 
@@ -395,8 +388,17 @@ namespace decay {
 void launch_decay_scan(const DecayParams& p, int d, int seg, float* added, const float* added_log,
                        cudaStream_t s) {
   const dim3 grid((unsigned)(p.total / seg * (d * d / 1024)), (unsigned)p.H);
-  if (d == 128) decay_scan_kernel<128><<<grid, 256, 0, s>>>(p, seg, added, added_log);
-  else decay_scan_kernel<64><<<grid, 256, 0, s>>>(p, seg, added, added_log);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (d == 128) cudaLaunchKernelEx(&cfg, decay_scan_kernel<128>, p, seg, added, added_log);
+  else cudaLaunchKernelEx(&cfg, decay_scan_kernel<64>, p, seg, added, added_log);
   count_launches(1);
 }
 

@@ -358,6 +358,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
       const int at = half * (D / 2) * D + w * 32 + lane;  // of the state's matrix
       float* exit_state = nullptr;
       Chunk c;
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // the scan before this kernel, if any
 #pragma unroll 1
       for (int n = 0;; ++n) {
         const int s = n % kStages;
@@ -1143,7 +1144,18 @@ kda_status launch_d(const DecayParams& p, int seg, float* added, float* added_lo
     launch_decay_scan(p, D, seg, added, added_log, s);
     count_launches(1);
   }
-  decay_tc_kernel<D><<<(unsigned)(slots * p.H), kThreads, out_bytes, s>>>(m, p, seg, added);
+  // behind a scan, its CTAs start while the scan's last ones run
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(slots * p.H));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = out_bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.total > seg ? 1 : 0;
+  cudaLaunchKernelEx(&cfg, decay_tc_kernel<D>, m, p, seg, (const float*)added);
   count_launches(1);
   return check_launch("kda_decay_prefill");
 }
