@@ -346,12 +346,17 @@ decay_scan_kernel(const DecayParams p, int seg, float* added, const float* added
   }
 }
 
-// Tokens of a segment: so that the segments of all heads are at most two per SM, and no fewer than
-// a few chunks' worth of work outweighs the state that a segment has to write and read.
+// Tokens of a segment: so that all heads' segments are one per SM (bf16) or four (CUDA cores: 64 value
+// columns each), but not so few that the state that a segment has to write and read outweighs them.
+// bf16, 65536 tokens x 4 heads: 95 us, with two per SM 115; 16384 x 32: 178 and 175; 40 prompts up to
+// 1000 x 16: 87 and 107. At least 256 tokens: 2048 x 8 29 us, with 512 37; 8192 x 2 31 us, with 128 37. (But
+// 300 x 4 17 us in one, 23 in two.)
+// fp32, 5 prompts up to 1301 x 6: 51 us, with 256 tokens at least 91; 8192 x 16: 743, with half as
+// many 803, with twice as many 833.
 int segment_tokens(kda_dtype dt, int total, int H, int d) {
   const int64_t units = (int64_t)H * (dt == KDA_BF16 ? 1 : d / kCols);
-  const int64_t all = dt == KDA_BF16 ? 304 : 608, want = units < all ? all / units : 1;
-  const int64_t seg = ((total + want - 1) / want + 63) / 64 * 64, least = dt == KDA_BF16 ? 512 : 64;
+  const int64_t all = dt == KDA_BF16 ? 152 : 608, want = units < all ? all / units : 1;
+  const int64_t seg = ((total + want - 1) / want + 63) / 64 * 64, least = dt != KDA_BF16 ? 64 : total > 512 ? 256 : 512;
   return (int)(seg < least ? least : seg);
 }
 

@@ -78,15 +78,27 @@ __device__ __forceinline__ float2 log_add(float2 a, float2 b) {
 __device__ __forceinline__ float2 log_sub(float2 a, float2 b) {
   return log_add(a, make_float2(-b.x, -b.y));
 }
-// Sums over the lanes up to each.
-__device__ __forceinline__ float2 log_scan(float2 v, int lane) {
+// Sums over the lanes up to each, of N lists side by side (one alone waits for its own latencies).
+template <int N>
+__device__ __forceinline__ void log_scan(float2 (&v)[N], int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const float2 w = make_float2(__shfl_up_sync(0xffffffffu, v.x, o),
-                                 __shfl_up_sync(0xffffffffu, v.y, o));
-    if (lane >= o) v = log_add(v, w);
+    float2 w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      w[i] = make_float2(__shfl_up_sync(0xffffffffu, v[i].x, o),
+                         __shfl_up_sync(0xffffffffu, v[i].y, o));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 x = log_add(v[i], w[i]);
+      if (lane >= o) v[i] = x;
+    }
   }
-  return v;
+}
+__device__ __forceinline__ float2 log_scan(float2 v, int lane) {
+  float2 x[1] = {v};
+  log_scan(x, lane);
+  return x[0];
 }
 // 2^(a - b).
 __device__ __forceinline__ float decay_between(float2 a, float2 b) {

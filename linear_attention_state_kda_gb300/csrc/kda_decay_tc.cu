@@ -29,7 +29,7 @@ using namespace decay;
 constexpr int kC = 64;
 constexpr int kStages = 4;
 constexpr int kThreads = 896;
-constexpr int kAhead = 2;
+constexpr int kAhead = 2, kAddAhead = 8;  // chunks whose decays are asked for ahead (room; latency)
 constexpr uint32_t kTries = 1u << 19;  // of a wait inside a CTA: 2 s
 
 struct Maps {
@@ -172,6 +172,7 @@ __device__ __forceinline__ uint32_t tile_at(int i) {
 }
 // A ring of the next chunks' log-decays: lane l has tokens 2 l and 2 l + 1. Loaded kAhead chunks
 // before their use: the latency of one load is as long as a chunk.
+template <int kAhead>
 struct DecayRing {
   float (*ring)[kC];
   const float* g;
@@ -188,9 +189,12 @@ struct DecayRing {
     }
     ptx::cp_async_commit();
   }
-  // Chunk n's, once all but the latest kAhead - 1 groups have arrived.
-  __device__ __forceinline__ float2 take(int n) const {
-    ptx::cp_async_wait<kAhead - 1>();
+  // The next `chunks` of those asked for have arrived.
+  template <int chunks>
+  __device__ __forceinline__ void wait() const {
+    ptx::cp_async_wait<kAhead - chunks>();
+  }
+  __device__ __forceinline__ float2 get(int n) const {
     return *reinterpret_cast<const float2*>(&ring[n % kAhead][2 * lane]);
   }
 };
@@ -496,14 +500,15 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
       bool ok = true;
 #pragma unroll 1
       while (ok && next_unit(sm.units, wait, lane, unit, u)) {
-        const DecayRing ring{sm.g, p.g + u.head, p.gs, lane};
+        const DecayRing<kAhead> ring{sm.g, p.g + u.head, p.gs, lane};
 #pragma unroll 1
         for (int i = 0; i < kAhead; ++i) ring.ask(i, u.lo + i * kC, u.hi);
         int i = 0;
 #pragma unroll 1
         do {
           const int s = n % kStages;
-          const float2 g = ring.take(i);
+          ring.wait<1>();
+          const float2 g = ring.get(i);
           const bool nan = __any_sync(0xffffffffu, g.x != g.x || g.y != g.y);
           const float2 second = log_pair(g.y);
           float2 b = log_scan(log_add(log_pair(g.x), second), lane), a = log_sub(b, second);
@@ -860,7 +865,7 @@ struct AddSmall {
   uint64_t full[8], empty[8];
   uint64_t v_full[2], v_empty[2], acc_full[2], acc_empty[2], drain;
   float w[8][kC];
-  float g[kAhead][kC];
+  float g[kAddAhead][kC];
   float* out[8];  // of a chunk's unit
   int kind[8];
   uint32_t tmem;
@@ -963,31 +968,47 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
     bool ok = true;
 #pragma unroll 1
     while (ok && next_unit(sm.units, wait, lane, unit, u)) {
-      const DecayRing ring{sm.g, p.g + u.head, p.gs, lane};
+      const DecayRing<kAddAhead> ring{sm.g, p.g + u.head, p.gs, lane};
       auto ask = [&](int i) {
         const int t = i < N ? u.lo + (N - 1 - i) * kC : 0;
         ring.ask(i, t, i < N ? t + kC : 0);
       };
 #pragma unroll 1
-      for (int i = 0; i < kAhead; ++i) ask(i);
+      for (int i = 0; i < kAddAhead; ++i) ask(i);
       float2 later = make_float2(0.0f, 0.0f);
+      // two chunks side by side: one's sums alone took as long as everything else of a chunk
 #pragma unroll 1
-      for (int i = 0; i < N; ++i, ++n) {
-        const int s = n % kStages;
-        const float2 g = ring.take(i);
-        const bool nan = __any_sync(0xffffffffu, g.x != g.x || g.y != g.y);
-        const float2 second = log_pair(g.y);
-        const float2 sum = log_scan(log_add(log_pair(g.x), second), lane);
-        ask(i + kAhead);
-        const float2 all = make_float2(__shfl_sync(0xffffffffu, sum.x, 31),
-                                       __shfl_sync(0xffffffffu, sum.y, 31));
-        const float2 upto = log_add(later, all), b = log_sub(upto, sum), a = log_add(b, second);
-        float wa = ptx::ex2_approx(a.x + a.y), wb = ptx::ex2_approx(b.x + b.y);
-        if (nan) wa = wb = nan_f();
-        later = upto;
-        if (n >= kStages && !(ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1))) break;
-        *reinterpret_cast<float2*>(&sm.w[s][2 * lane]) = make_float2(wa, wb);
-        arrive(&sm.full[s]);
+      for (int i = 0; i < N; i += 2) {
+        float2 second[2], sum[2], all[2];
+        bool nan[2];
+        ring.wait<2>();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float2 g = ring.get(i + c);
+          nan[c] = __any_sync(0xffffffffu, g.x != g.x || g.y != g.y);
+          second[c] = log_pair(g.y);
+          sum[c] = log_add(log_pair(g.x), second[c]);
+        }
+        log_scan(sum, lane);
+        ask(i + kAddAhead);
+        ask(i + 1 + kAddAhead);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          all[c] = make_float2(__shfl_sync(0xffffffffu, sum[c].x, 31),
+                               __shfl_sync(0xffffffffu, sum[c].y, 31));
+#pragma unroll
+        for (int c = 0; c < 2 && i + c < N && ok; ++c, ++n) {
+          const int s = n % kStages;
+          const float2 upto = log_add(later, all[c]), b = log_sub(upto, sum[c]),
+                       a = log_add(b, second[c]);
+          float wa = ptx::ex2_approx(a.x + a.y), wb = ptx::ex2_approx(b.x + b.y);
+          if (nan[c]) wa = wb = nan_f();
+          later = upto;
+          if (n >= kStages && !(ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1))) break;
+          *reinterpret_cast<float2*>(&sm.w[s][2 * lane]) = make_float2(wa, wb);
+          arrive(&sm.full[s]);
+        }
+        if (!ok) break;
       }
       if (lane == 0) added_log[u.place] = later.x;
     }
