@@ -75,13 +75,13 @@ struct Out {
 };
 // Every wait is by parity, which tells a phase only from the one before it, so none may be two phases
 // behind. Each barrier's next phase needs, at some remove, what its waiters do after this one: a
-// stage's chunk is refilled once every role has left it; the next scores wait for sc_empty, the next
+// stage's chunk is refilled once every role has left it; the next scores wait for p_full, the next
 // state and V' for kv_done, the next rounded state for sq_done, the next V for o_full, the next
 // outputs for o_empty. P runs up to two chunks ahead of the products, so its barriers are by place.
 struct OutSmall {
   UnitRing units;
   uint64_t full[kStages], empty[kStages];
-  uint64_t sc_full, sc_empty, p_full[2], p_empty[2], v_full, vt_full, s_full, hi_full;
+  uint64_t sc_full, p_full[2], p_empty[2], v_full, vt_full, s_full, hi_full;
   uint64_t kv_done, sq_done, o_full, o_empty, drain;
   float ghi[kStages][kC], glo[kStages][kC];  // running sums of log2 decays, high and low parts
   float g[kAhead][kC];                       // log-decays of the next chunks
@@ -312,7 +312,6 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
     ptx::mbar_init(&sm.units.clc, 1);
     ptx::mbar_init(&sm.units.ask, 1);
     ptx::mbar_init(&sm.sc_full, 1);
-    ptx::mbar_init(&sm.sc_empty, 4);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sm.p_full[i], 4);
       ptx::mbar_init(&sm.p_empty[i], 1);
@@ -577,12 +576,6 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
           ptx::mma_commit(&sm.kv_done);
         }
         __syncwarp();
-        const bool more = take(n + 1, c);
-        if (more) {  // (once this chunk's have been read)
-          if (!wait(&sm.sc_empty, ph)) break;
-          ptx::tc_fence_after();
-          issue_qk(n + 1);
-        }
         if (n == 0 ? !wait(&sm.hi_full, 0) : !wait.both(&sm.hi_full, ph, &sm.o_empty, ph ^ 1)) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
@@ -608,6 +601,9 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
           ptx::mma_commit(&sm.p_empty[ph]);
         }
         __syncwarp();
+        // (P's warps have read this chunk's scores)
+        const bool more = take(n + 1, c);
+        if (more) issue_qk(n + 1);
         ok = more;
       }
       if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort)) {  // the products in flight end first
@@ -804,10 +800,6 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
         ptx::tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(r[j]));
-        if (c0 + 32 > w * 16) {  // all of them read
-          ptx::tc_fence_before();
-          arrive(&sm.sc_empty);
-        }
         uint32_t o[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -838,6 +830,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
                           o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
+      ptx::tc_fence_before();  // the scores are read, too
       ptx::fence_proxy_async_smem();
       arrive(&sm.p_full[n & 1]);
       if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
@@ -1031,13 +1024,14 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
     });
   } else if (warp == 17) {
     // ------------------------------------------------------------------ products
-    int kind;
+    // (a look at a barrier takes some 300 cycles: V' says that the chunk itself is there too)
     uint32_t unit = 0;
 #pragma unroll 1
-    for (int n = 0; take(n, kind); ++n) {
+    for (int n = 0; wait(&sm.v_full[n & 1], (n >> 1) & 1); ++n) {
       const int s = n % kStages, b = n & 1, acc = unit & 1;
+      const int kind = __shfl_sync(0xffffffffu, sm.kind[s], 0);
+      if (kind == kStop) break;
       if ((kind & kFirst) && unit >= 2 && !wait(&sm.acc_empty[acc], ((unit >> 1) - 1) & 1)) break;
-      if (!wait(&sm.v_full[b], (n >> 1) & 1)) break;
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
         issue_kv<D>(tmem + acc * 128, tmem + VP + b * 96, base + s * M::STAGE + M::K, kind & kFirst);
@@ -1060,13 +1054,19 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
     const int w = warp & 3, tok = ((warp >> 2) & 1) * 32, b = warp >> 3;
     if (w < NQ) {
       const uint32_t lanes = (uint32_t)(w * 32) << 16;
-      int kind;
 #pragma unroll 1
-      for (int n = 0; take(n, kind); ++n) {
+      for (int n = 0;; ++n) {
         const int s = n % kStages;
+        if (!wait(&sm.full[s], (n / kStages) & 1)) break;
+        const bool stop = __shfl_sync(0xffffffffu, sm.kind[s], 0) == kStop;
         if ((n & 1) != b) {  // (every warp sees every phase of a stage: parities do not run ahead)
+          if (stop) break;
           arrive(&sm.empty[s]);
           continue;
+        }
+        if (stop) {  // which the products learn from this barrier, once they have left its last phase
+          if (n < 2 || wait(&sm.v_empty[b], ((n >> 1) - 1) & 1)) arrive(&sm.v_full[b]);
+          break;
         }
         const uint32_t st = base + s * M::STAGE;
         uint32_t raw[2][8];
