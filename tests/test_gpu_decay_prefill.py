@@ -230,3 +230,33 @@ def test_long_prompt_many_segments():
         for h in (0, 17, 39):
             check(q[:, h // 2:h // 2 + 1], k[:, h // 2:h // 2 + 1], v[:, h:h + 1], g[:, h:h + 1], cu,
                   s0[:, h:h + 1], 0.1, o[:, h:h + 1], fin[:, h:h + 1], dtype)
+
+
+@pytest.mark.parametrize("dtype,d,H,T", [("bf16", 128, 4, 12160 + 13), ("bf16", 64, 3, 20160),
+                                         ("f32", 64, 2, 64 * 19 + 1)])
+def test_segments_of_an_odd_number_of_chunks(dtype, d, H, T):
+    """Segments of 5, 7 and (fp32) 2 chunks, several a block or one: the last one's end, too."""
+    x = make([T], H, 1, d, dtype, seed=13)
+    q, k, v, g, cu, s0 = x
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    o, fin = kda.decay_prefill(q, k, v, g, cu_seqlens=cu, init_state=s0, scale=0.1, status=status)
+    assert int(status) == 0
+    check(q, k, v[:, :1], g[:, :1], cu, s0[:, :1], 0.1, o[:, :1], fin[:, :1], dtype)
+    check(q, k, v[:, -1:], g[:, -1:], cu, s0[:, -1:], 0.1, o[:, -1:], fin[:, -1:], dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_two_calls_at_once(dtype):
+    """Two streams, a workspace each: the answers of one call after the other."""
+    xs = [make([1500, 70], 3, 3, 128, dtype, seed=20 + i) for i in range(2)]
+    want = [kda.decay_prefill(*x[:4], cu_seqlens=x[4], init_state=x[5]) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(3):
+        got = []
+        for x, s in zip(xs, streams):
+            with torch.cuda.stream(s):
+                got.append(kda.decay_prefill(*x[:4], cu_seqlens=x[4], init_state=x[5]))
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
