@@ -81,7 +81,7 @@ struct Out {
 struct OutSmall {
   UnitRing units;
   uint64_t full[kStages], empty[kStages];
-  uint64_t sc_full, p_full[2], p_empty[2], v_full, vt_full, s_full, hi_full;
+  uint64_t sc_full, p_full[2], p_empty[2], v_full, vt_full, u_empty, hi_full;
   uint64_t kv_done, sq_done, o_full, o_empty, drain;
   float ghi[kStages][kC], glo[kStages][kC];  // running sums of log2 decays, high and low parts
   float g[kAhead][kC];                       // log-decays of the next chunks
@@ -94,7 +94,7 @@ struct OutSmall {
 // a column), the scores, and the two sums of O, all 512 at D = 128.
 template <int D>
 struct Tm {
-  static constexpr int S = 0, HI = D, VP = HI + D / 2, VT = VP + 96, SC = VT + 32, OI = SC + 64,
+  static constexpr int U = 0, HI = D, VP = HI + D / 2, VT = VP + 96, SC = VT + 32, OI = SC + 64,
                        OA = OI + 64;
   static_assert(OA + 64 <= 512, "TMEM");
 };
@@ -151,17 +151,20 @@ __device__ __forceinline__ void load_tile(void* dst, const CUtensorMap* m, uint6
     ptx::tma_load_2d((uint8_t*)dst + i * 8192, m, bar, head * D + i * 64, t0);
 }
 
-// V'^T K of a chunk into the state: three parts of V' (TMEM), K (MN-major).
+// V'^T K of a chunk: three parts of V' (TMEM), K (MN-major). Products round their sums toward zero,
+// so the parts go from the smallest to the largest and each chunk into a sum of its own, which is
+// then added in registers: summed up over chunks in place, a slowly decaying state was off by 2e-6
+// after 500 tokens (and 4e-6 after 4000), now by 2e-7.
 template <int D>
-__device__ __forceinline__ void issue_kv(uint32_t tmem_s, uint32_t vp, uint32_t k, bool fresh) {
+__device__ __forceinline__ void issue_kv(uint32_t tmem_u, uint32_t vp, uint32_t k) {
   const uint32_t id = ptx::idesc_make(ptx::kFmtBF16, 128, D, false, true);
   const uint64_t b = ptx::sdesc_sw128(k, 8192, 1024);
 #pragma unroll 1
-  for (uint32_t part = 0; part < 3; ++part)
+  for (int part = 2; part >= 0; --part)
 #pragma unroll
     for (uint32_t i = 0; i < kC / 16; ++i)
-      ptx::mma_f16_ts(tmem_s, vp + part * 32 + i * 8, ptx::desc_add(b, i * 2048), id,
-                      !fresh || part + i > 0);
+      ptx::mma_f16_ts(tmem_u, vp + (uint32_t)part * 32 + i * 8, ptx::desc_add(b, i * 2048), id,
+                      part < 2 || i > 0);
 }
 
 // 16 bytes (8 channels) number i of a tile: row i / (D / 8), swizzled place.
@@ -318,7 +321,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
     }
     ptx::mbar_init(&sm.v_full, 2 * NQ);
     ptx::mbar_init(&sm.vt_full, 2 * NQ);
-    ptx::mbar_init(&sm.s_full, 2 * NQ);
+    ptx::mbar_init(&sm.u_empty, 2 * NQ);
     ptx::mbar_init(&sm.hi_full, 2 * NQ);
     ptx::mbar_init(&sm.kv_done, 1);
     ptx::mbar_init(&sm.sq_done, 1);
@@ -356,11 +359,12 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
     const int w = warp & 3, half = (warp - 4) >> 2;  // 32 value channels, half of the key channels
     if (w < NQ) {
       const uint32_t lanes = (uint32_t)(w * 32) << 16;
-      const uint32_t t_s = tmem + lanes + T::S + half * (D / 2);
-      const uint32_t t_part = tmem + lanes + half * (D / 4);
+      const uint32_t t_u = tmem + lanes + T::U + half * (D / 2);
+      const uint32_t t_hi = tmem + lanes + T::HI + half * (D / 4);
       const int at = half * (D / 2) * D + w * 32 + lane;  // of the state's matrix
       float* exit_state = nullptr;
       Chunk c;
+      ptx::f32x2 st[D / 4];
       asm volatile("griddepcontrol.wait;" ::: "memory");  // the scan before this kernel, if any
 #pragma unroll 1
       for (int n = 0;; ++n) {
@@ -368,75 +372,62 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
         if (!wait(&sm.full[s], (n / kStages) & 1)) break;
         c = sm.chunk[s];
         const int kind = __shfl_sync(0xffffffffu, c.kind, 0);
-        if (kind & (kFirst | kStop)) {
-          // the unit before ends: its state goes out, and the next one's, asked for before, comes in
-          float f[D / 2];
-#pragma unroll
-          for (int b = 0; b < D / 2; ++b)
-            f[b] = kind != kStop && c.entry ? __ldg(c.entry + at + b * D) : 0.0f;
-          if (n > 0 && !wait(&sm.kv_done, (n - 1) & 1)) break;
-          ptx::tc_fence_after();
+        if (kind & (kFirst | kStop)) {  // the unit before has ended
           if (exit_state) {
-#pragma unroll 1
-            for (int b = 0; b < D / 2; b += 16) {
-              uint32_t x[16];
-              ptx::tmem_ld16_nowait(t_s + b, x);
-              ptx::tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[i]));
-#pragma unroll
-              for (int i = 0; i < 16; ++i) exit_state[at + (b + i) * D] = __uint_as_float(x[i]);
+            for (int i = 0; i < D / 4; ++i) {
+              float x, y;
+              ptx::unpack2(st[i], x, y);
+              exit_state[at + (2 * i) * D] = x;
+              exit_state[at + (2 * i + 1) * D] = y;
             }
           }
           if (kind == kStop) break;
 #pragma unroll
-          for (int b = 0; b < D / 2; b += 16) {
-            float x[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = f[b + i];
-            ptx::tmem_st16(t_s + b, x);
+          for (int i = 0; i < D / 4; ++i) {
+            float x = 0.0f, y = 0.0f;
+            if (c.entry) {
+              x = __ldg(c.entry + at + (2 * i) * D);
+              y = __ldg(c.entry + at + (2 * i + 1) * D);
+            }
+            st[i] = ptx::pack2(x, y);
           }
-          ptx::tmem_st_wait();
-        } else {
-          if (!wait(&sm.kv_done, (n - 1) & 1)) break;
-          ptx::tc_fence_after();
         }
         exit_state = c.exit;
-        const float a = ptx::ex2_approx(sm.total[s].x + sm.total[s].y);
-        const ptx::f32x2 aa = ptx::pack2(a, a);
-        // decayed first, which is what the next sum waits for
-        float r[D / 32][8];
-#pragma unroll
-        for (int b = 0; b < D / 32; ++b) {
-          uint32_t f[16];
-          ptx::tmem_ld16_nowait(t_s + b * 16, f);
-          ptx::tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(f[i]));
-          float y[16];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float lo = __uint_as_float(f[2 * i]), hi = __uint_as_float(f[2 * i + 1]);
-            r[b][i] = __uint_as_float(pack_bf16(lo, hi));
-            ptx::unpack2(ptx::mul2(ptx::pack2(lo, hi), aa), y[2 * i], y[2 * i + 1]);
-          }
-          ptx::tmem_st16(t_s + b * 16, y);
-        }
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        arrive(&sm.s_full);
         if (n > 0 && !wait(&sm.sq_done, (n - 1) & 1)) break;
         ptx::tc_fence_after();
 #pragma unroll
-        for (int b = 0; b < D / 32; b += 2) {
+        for (int b = 0; b < D / 4; b += 16) {
           float h[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) h[i] = r[b + i / 8][i % 8];
-          ptx::tmem_st16(t_part + T::HI + b * 8, h);
+          for (int i = 0; i < 16; ++i) {
+            float x, y;
+            ptx::unpack2(st[b + i], x, y);
+            h[i] = __uint_as_float(pack_bf16(x, y));
+          }
+          ptx::tmem_st16(t_hi + b, h);
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         arrive(&sm.hi_full);
+        const float a = ptx::ex2_approx(sm.total[s].x + sm.total[s].y);
+        const ptx::f32x2 aa = ptx::pack2(a, a);
+        if (!wait(&sm.kv_done, n & 1)) break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int b = 0; b < D / 4; b += 8) {
+          uint32_t f[16];
+          ptx::tmem_ld16_nowait(t_u + 2 * b, f);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(f[i]));
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            st[b + i] = ptx::fma2(st[b + i], aa, ptx::pack2(__uint_as_float(f[2 * i]),
+                                                            __uint_as_float(f[2 * i + 1])));
+        }
+        ptx::tc_fence_before();
+        arrive(&sm.u_empty);
         if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
       }
     }
@@ -569,10 +560,10 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
       for (int n = 0; ok; ++n) {
         const int s = n % kStages;
         const uint32_t st = base + s * M::STAGE, ph = n & 1;
-        if (!wait.both(&sm.s_full, ph, &sm.v_full, ph)) break;
+        if (n == 0 ? !wait(&sm.v_full, 0) : !wait.both(&sm.u_empty, ph ^ 1, &sm.v_full, ph)) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
-          issue_kv<D>(tmem + T::S, tmem + T::VP, st + M::K, false);
+          issue_kv<D>(tmem + T::U, tmem + T::VP, st + M::K);
           ptx::mma_commit(&sm.kv_done);
         }
         __syncwarp();
@@ -864,7 +855,7 @@ struct AddSmall {
   uint32_t tmem;
   int abort;
 };
-constexpr int kAddThreads = 768;  // 16 + 2 + 4 + 2 warps
+constexpr int kAddThreads = 896;  // 16 + 8 + 4 warps
 
 template <int D>
 __global__ void __launch_bounds__(kAddThreads, 1)
@@ -872,7 +863,7 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
                  float* added_log) {
   using M = Add<D>;
   constexpr int NQ = D / 32, kStages = M::STAGES;
-  constexpr int VP = 256;  // TMEM: two sums in turn, then two sets of three parts of V'
+  constexpr int VP = 256;  // TMEM: two chunks' sums, then two sets of three parts of V'
   extern __shared__ __align__(1024) uint8_t smem[];
   AddSmall& sm = *reinterpret_cast<AddSmall*>(smem + M::SMALL);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -881,7 +872,7 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&sm.full[i], 2);
-      ptx::mbar_init(&sm.empty[i], 1 + 4 * NQ + NQ);
+      ptx::mbar_init(&sm.empty[i], 1 + 4 * NQ + 2 * NQ);
     }
     for (int i = 0; i < kUnits; ++i) {
       ptx::mbar_init(&sm.units.full[i], 1);
@@ -893,13 +884,13 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
       ptx::mbar_init(&sm.v_full[i], 2 * NQ);
       ptx::mbar_init(&sm.v_empty[i], 1);
       ptx::mbar_init(&sm.acc_full[i], 1);
-      ptx::mbar_init(&sm.acc_empty[i], NQ);
+      ptx::mbar_init(&sm.acc_empty[i], 2 * NQ);
     }
     ptx::mbar_init(&sm.drain, 1);
     ptx::fence_mbar_init();
     sm.abort = 0;
   }
-  if (warp == 17) {
+  if (warp == 25) {
     ptx::tmem_alloc(&sm.tmem, 512);
     ptx::tmem_relinquish();
   }
@@ -919,7 +910,110 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
     return kind != kStop;
   };
 
-  if (warp == 16) {
+  // registers of the seven warpgroups: 4 x 64 + 2 x 96 + 56 = 7 x 72
+  if (warp < 16) {
+    ptx::regs_give<64>();
+    // ------------------------------------------------------------------ V'
+    // two sets of 8 warps take chunks in turn: 32 channels, half of the tokens each
+    const int w = warp & 3, tok = ((warp >> 2) & 1) * 32, b = warp >> 3;
+    if (w < NQ) {
+      const uint32_t lanes = (uint32_t)(w * 32) << 16;
+#pragma unroll 1
+      for (int n = 0;; ++n) {
+        const int s = n % kStages;
+        if (!wait(&sm.full[s], (n / kStages) & 1)) break;
+        const bool stop = __shfl_sync(0xffffffffu, sm.kind[s], 0) == kStop;
+        if ((n & 1) != b) {  // (every warp sees every phase of a stage: parities do not run ahead)
+          if (stop) break;
+          arrive(&sm.empty[s]);
+          continue;
+        }
+        if (stop) {  // which the products learn from this barrier, once they have left its last phase
+          if (n < 2 || wait(&sm.v_empty[b], ((n >> 1) - 1) & 1)) arrive(&sm.v_full[b]);
+          break;
+        }
+        const uint32_t st = base + s * M::STAGE;
+        uint32_t raw[2][8];
+        load_vt(st + M::V, w * 32, tok, lane, raw[0]);
+        load_vt(st + M::V, w * 32 + 16, tok, lane, raw[1]);
+        ptx::f32x2 weight[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = *reinterpret_cast<const float2*>(&sm.w[s][tok + i * 8 + 2 * (lane & 3)]);
+          weight[i] = ptx::pack2(f.x, f.y);
+        }
+        arrive(&sm.empty[s]);
+        if (n >= 2 && !wait(&sm.v_empty[b], ((n >> 1) - 1) & 1)) break;
+        ptx::tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t part[3][8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t x[3];
+            weigh3(c ? raw[1][i] : raw[0][i], weight[i >> 1], x);
+            part[0][i] = x[0];
+            part[1][i] = x[1];
+            part[2][i] = x[2];
+          }
+#pragma unroll
+          for (int j = 0; j < 3; ++j)
+            ptx::tmem_st_rows16_nowait(
+                tmem + lanes + ((uint32_t)(c * 16) << 16) + VP + b * 96 + j * 32 + tok / 2, part[j]);
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        arrive(&sm.v_full[b]);
+      }
+    }
+  } else if (warp < 24) {
+    ptx::regs_take<96>();
+    // ------------------------------------------------------------------ sums over the chunks
+    const int w = warp & 3, half = (warp - 16) >> 2;  // 32 value channels, half of the key channels
+    if (w < NQ) {
+      const int at = half * (D / 2) * D + w * 32 + lane;
+      const uint32_t t_u = tmem + ((uint32_t)(w * 32) << 16) + half * (D / 2);
+      ptx::f32x2 sum[D / 4];
+      int kind;
+#pragma unroll 1
+      for (int n = 0; take(n, kind); ++n) {
+        const int s = n % kStages, b = n & 1;
+        float* out = sm.out[s] + at;
+        arrive(&sm.empty[s]);
+        if (kind & kFirst) {
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i) sum[i] = ptx::pack2(0.0f, 0.0f);
+        }
+        if (!wait(&sm.acc_full[b], (n >> 1) & 1)) break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < D / 4; c += 8) {
+          uint32_t f[16];
+          ptx::tmem_ld16_nowait(t_u + b * 128 + 2 * c, f);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(f[i]));
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            sum[c + i] = ptx::add2(sum[c + i], ptx::pack2(__uint_as_float(f[2 * i]),
+                                                          __uint_as_float(f[2 * i + 1])));
+        }
+        ptx::tc_fence_before();
+        arrive(&sm.acc_empty[b]);
+        if (kind & kLast) {
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i) {
+            float x, y;
+            ptx::unpack2(sum[i], x, y);
+            out[(2 * i) * D] = x;
+            out[(2 * i + 1) * D] = y;
+          }
+        }
+      }
+    }
+  } else {
+    ptx::regs_give<56>();
+    if (warp == 24) {
     // ------------------------------------------------------------------ loads
     int n = 0;
     uint32_t unit = 0;
@@ -953,7 +1047,7 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
       __nanosleep(1000000);
       __syncwarp();
     }
-  } else if (warp == 22) {
+    } else if (warp == 26) {
     // ------------------------------------------------------------------ sums of the decays
     int n = 0;
     uint32_t unit = 0;
@@ -1009,7 +1103,7 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
     if (ok && n >= kStages) ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1);
     if (ok) arrive(&sm.full[s]);
     ptx::cp_async_wait<0>();
-  } else if (warp == 23) {
+    } else if (warp == 27) {
     // ------------------------------------------------------------------ the units
     schedule(sm.units, wait, lane, [&](int block, Unit& u) {
       Segment x;
@@ -1022,25 +1116,24 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
       u.exit = added + (int64_t)u.place * (D * D);
       return true;
     });
-  } else if (warp == 17) {
+    } else {
     // ------------------------------------------------------------------ products
     // (a look at a barrier takes some 300 cycles: V' says that the chunk itself is there too)
-    uint32_t unit = 0;
 #pragma unroll 1
-    for (int n = 0; wait(&sm.v_full[n & 1], (n >> 1) & 1); ++n) {
-      const int s = n % kStages, b = n & 1, acc = unit & 1;
-      const int kind = __shfl_sync(0xffffffffu, sm.kind[s], 0);
-      if (kind == kStop) break;
-      if ((kind & kFirst) && unit >= 2 && !wait(&sm.acc_empty[acc], ((unit >> 1) - 1) & 1)) break;
+    for (int n = 0;; ++n) {
+      const int s = n % kStages, b = n & 1;
+      if (n < 2 ? !wait(&sm.v_full[b], 0)
+                : !wait.both(&sm.v_full[b], (n >> 1) & 1, &sm.acc_empty[b], ((n >> 1) - 1) & 1))
+        break;
+      if (__shfl_sync(0xffffffffu, sm.kind[s], 0) == kStop) break;
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
-        issue_kv<D>(tmem + acc * 128, tmem + VP + b * 96, base + s * M::STAGE + M::K, kind & kFirst);
+        issue_kv<D>(tmem + b * 128, tmem + VP + b * 96, base + s * M::STAGE + M::K);
         ptx::mma_commit(&sm.v_empty[b]);
         ptx::mma_commit(&sm.empty[s]);
-        if (kind & kLast) ptx::mma_commit(&sm.acc_full[acc]);
+        ptx::mma_commit(&sm.acc_full[b]);
       }
       __syncwarp();
-      if (kind & kLast) ++unit;
     }
     if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort)) {
       if (ptx::elect_one()) ptx::mma_commit(&sm.drain);
@@ -1048,92 +1141,12 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
       ptx::mbar_wait_tries(&sm.drain, 0, kTries);
       __syncwarp();
     }
-  } else if (warp < 16) {
-    // ------------------------------------------------------------------ V'
-    // two sets of 8 warps take chunks in turn: 32 channels, half of the tokens each
-    const int w = warp & 3, tok = ((warp >> 2) & 1) * 32, b = warp >> 3;
-    if (w < NQ) {
-      const uint32_t lanes = (uint32_t)(w * 32) << 16;
-#pragma unroll 1
-      for (int n = 0;; ++n) {
-        const int s = n % kStages;
-        if (!wait(&sm.full[s], (n / kStages) & 1)) break;
-        const bool stop = __shfl_sync(0xffffffffu, sm.kind[s], 0) == kStop;
-        if ((n & 1) != b) {  // (every warp sees every phase of a stage: parities do not run ahead)
-          if (stop) break;
-          arrive(&sm.empty[s]);
-          continue;
-        }
-        if (stop) {  // which the products learn from this barrier, once they have left its last phase
-          if (n < 2 || wait(&sm.v_empty[b], ((n >> 1) - 1) & 1)) arrive(&sm.v_full[b]);
-          break;
-        }
-        const uint32_t st = base + s * M::STAGE;
-        uint32_t raw[2][8];
-        load_vt(st + M::V, w * 32, tok, lane, raw[0]);
-        load_vt(st + M::V, w * 32 + 16, tok, lane, raw[1]);
-        ptx::f32x2 weight[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = *reinterpret_cast<const float2*>(&sm.w[s][tok + i * 8 + 2 * (lane & 3)]);
-          weight[i] = ptx::pack2(f.x, f.y);
-        }
-        arrive(&sm.empty[s]);
-        if (n >= 2 && !wait(&sm.v_empty[b], ((n >> 1) - 1) & 1)) break;
-        ptx::tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          uint32_t part[3][8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint32_t x[3];
-            weigh3(c ? raw[1][i] : raw[0][i], weight[i >> 1], x);
-            part[0][i] = x[0];
-            part[1][i] = x[1];
-            part[2][i] = x[2];
-          }
-#pragma unroll
-          for (int j = 0; j < 3; ++j)
-            ptx::tmem_st_rows16_nowait(
-                tmem + lanes + ((uint32_t)(c * 16) << 16) + VP + b * 96 + j * 32 + tok / 2, part[j]);
-        }
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        arrive(&sm.v_full[b]);
-      }
-    }
-  } else {
-    // ------------------------------------------------------------------ sums out (warps 18 .. 21)
-    const int w = warp & 3;
-    if (w < NQ) {
-      int kind;
-      uint32_t unit = 0;
-#pragma unroll 1
-      for (int n = 0; take(n, kind); ++n) {
-        const int s = n % kStages;
-        float* out = sm.out[s] + w * 32 + lane;
-        arrive(&sm.empty[s]);
-        if (!(kind & kLast)) continue;
-        const uint32_t acc = unit & 1;
-        if (!wait(&sm.acc_full[acc], (unit >> 1) & 1)) break;
-        ptx::tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float f[32];
-          ptx::tmem_ld32(tmem + ((uint32_t)(w * 32) << 16) + acc * 128 + c, f);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) out[(c + i) * D] = f[i];
-        }
-        ptx::tc_fence_before();
-        arrive(&sm.acc_empty[acc]);
-        ++unit;
-      }
     }
   }
   ptx::tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && sm.abort && p.status) atomicOr(p.status, KDA_STATUS_TIMEOUT);
-  if (warp == 17) ptx::tmem_dealloc(tmem, 512);
+  if (warp == 25) ptx::tmem_dealloc(tmem, 512);
 }
 
 template <int D>
