@@ -910,9 +910,8 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
     return kind != kStop;
   };
 
-  // registers of the seven warpgroups: 4 x 64 + 2 x 96 + 56 = 7 x 72
+  // registers of the seven warpgroups: 4 x 72 (as launched) + 2 x 88 + 40 = 7 x 72
   if (warp < 16) {
-    ptx::regs_give<64>();
     // ------------------------------------------------------------------ V'
     // two sets of 8 warps take chunks in turn: 32 channels, half of the tokens each
     const int w = warp & 3, tok = ((warp >> 2) & 1) * 32, b = warp >> 3;
@@ -943,31 +942,33 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
           weight[i] = ptx::pack2(f.x, f.y);
         }
         arrive(&sm.empty[s]);
-        if (n >= 2 && !wait(&sm.v_empty[b], ((n >> 1) - 1) & 1)) break;
-        ptx::tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          uint32_t part[3][8];
+        // all of V' before its room is free
+        uint32_t part[2][3][8];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             uint32_t x[3];
-            weigh3(c ? raw[1][i] : raw[0][i], weight[i >> 1], x);
-            part[0][i] = x[0];
-            part[1][i] = x[1];
-            part[2][i] = x[2];
+            weigh3(raw[c][i], weight[i >> 1], x);
+            part[c][0][i] = x[0];
+            part[c][1][i] = x[1];
+            part[c][2][i] = x[2];
           }
+        if (n >= 2 && !wait(&sm.v_empty[b], ((n >> 1) - 1) & 1)) break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int j = 0; j < 3; ++j)
             ptx::tmem_st_rows16_nowait(
-                tmem + lanes + ((uint32_t)(c * 16) << 16) + VP + b * 96 + j * 32 + tok / 2, part[j]);
-        }
+                tmem + lanes + ((uint32_t)(c * 16) << 16) + VP + b * 96 + j * 32 + tok / 2, part[c][j]);
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         arrive(&sm.v_full[b]);
       }
     }
   } else if (warp < 24) {
-    ptx::regs_take<96>();
+    ptx::regs_take<88>();
     // ------------------------------------------------------------------ sums over the chunks
     const int w = warp & 3, half = (warp - 16) >> 2;  // 32 value channels, half of the key channels
     if (w < NQ) {
@@ -1012,7 +1013,7 @@ decay_add_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg
       }
     }
   } else {
-    ptx::regs_give<56>();
+    ptx::regs_give<40>();
     if (warp == 24) {
     // ------------------------------------------------------------------ loads
     int n = 0;
