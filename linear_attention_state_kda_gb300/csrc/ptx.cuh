@@ -556,15 +556,6 @@ __device__ __forceinline__ void tmem_ld_frag32_nowait(uint32_t taddr, uint32_t* 
         "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-// The reverse.
-__device__ __forceinline__ void tmem_st_frag32_nowait(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
 // Four 8 x 8 matrices of 16-bit elements in that distribution (element (g, 2 t + e) in half e of the
 // word), stored transposed: lane 8 m + j gives the address of row j (16 bytes) of matrix m, which
 // gets the elements (0 .. 7, j).
