@@ -31,7 +31,7 @@ constexpr int kRows = 256;          // query rows at a time
 constexpr int kTile = 128;          // keys of a step: two pages
 constexpr int kStages = 4;
 constexpr int kParts = 3;
-constexpr int kThreads = 384;       // loads, products, two idle; 8 warps of exponentials
+constexpr int kThreads = 640;       // loads, products, two idle; 16 warps of exponentials
 constexpr int kSms = 152;           // ranges of keys are made for
 constexpr uint32_t kTries = 1u << 19;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -46,7 +46,7 @@ struct Small {
   float ks[kStages][2];             // of a step's pages; 0 where there is none
   int page[kStages][2];             // -1: none
   alignas(16) float2 row[kRows];    // scale log2(e) 2^e, and minus lse
-  float part[2][kTile];             // sums over the second half of the rows
+  float part[2][3][kTile];          // sums over the last three quarters of the rows
   uint32_t tmem;
   int abort;
 };
@@ -73,6 +73,7 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, co
   extern __shared__ __align__(1024) uint8_t smem[];
   Small& sm = *reinterpret_cast<Small*>(smem + Smem::SMALL);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (kStats) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int ranges = kStats ? cut.stat_ranges : cut.ranges;
   const int range = blockIdx.x % ranges;
   const int first_group = kStats ? blockIdx.x / ranges % cut.groups : 0;
@@ -97,11 +98,11 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, co
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&sm.full[i], 1);
-      ptx::mbar_init(&sm.empty[i], 1 + 8);
+      ptx::mbar_init(&sm.empty[i], 1 + 16);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sm.d_full[i], 1);
-      ptx::mbar_init(&sm.d_empty[i], 8);
+      ptx::mbar_init(&sm.d_empty[i], 16);
     }
     ptx::mbar_init(&sm.drain, 1);
     ptx::fence_mbar_init();
@@ -189,12 +190,13 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, co
     float lse = 0.0f;
     bool none = false;  // a row past the last, or that sees nothing, adds nothing
     const int mine = (int)threadIdx.x - 128;
+    if (!kStats && group == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!kStats && mine >= 0 && mine < tiles * 128) {
       const float2* ml =
-          p.stats + ((int64_t)bh * cut.groups + group) * cut.stat_ranges * kRows + mine;
+          p.stats + ((int64_t)bh * cut.groups + group) * (2 * cut.stat_ranges) * kRows + mine;
       float m = -INFINITY, l = 0.0f;
 #pragma unroll 4
-      for (int i = 0; i < cut.stat_ranges; ++i) {
+      for (int i = 0; i < 2 * cut.stat_ranges; ++i) {
         const float2 x = ml[(int64_t)i * kRows];
         const float top = fmaxf(m, x.x), at = top == -INFINITY ? 0.0f : top;
         l = l * exp2f(m - at) + x.y * exp2f(x.x - at);
@@ -229,8 +231,10 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, co
             }
             ks = id < 0 ? 0.0f : p.ks[(int64_t)id * p.Hkv + h];
           }
-          const int a = __shfl_sync(0xffffffffu, id, from), c = __shfl_sync(0xffffffffu, id, from + 1);
-          const float ka = __shfl_sync(0xffffffffu, ks, from), kc = __shfl_sync(0xffffffffu, ks, from + 1);
+          const int a = __shfl_sync(0xffffffffu, id, from);
+          const int c = __shfl_sync(0xffffffffu, id, from + 1);
+          const float ka = __shfl_sync(0xffffffffu, ks, from);
+          const float kc = __shfl_sync(0xffffffffu, ks, from + 1);
           if (at >= kStages && !wait(&sm.empty[s], ((at / kStages) - 1) & 1)) break;
           if (lane == 0) {
             sm.page[s][0] = a < 0 ? -1 : a;
@@ -264,14 +268,15 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, co
                 for (int t = 0; t < tiles; ++t)
 #pragma unroll
                   for (int j = 0; j < 4; ++j)
-                    ptx::mma_f8(d + t * kTile, ptx::desc_add(q, part * (kRows * D) + t * 128 * D + j * 32),
+                    ptx::mma_f8(d + t * kTile,
+                                ptx::desc_add(q, part * (kRows * D) + t * 128 * D + j * 32),
                                 ptx::desc_add(k, j * 32), id, part + j > 0);
               } else {
                 const uint32_t id = ptx::idesc_make2(ptx::kFmtE4M3, fmt, 128, (uint32_t)tiles * 128);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                  ptx::mma_f8(d, ptx::desc_add(k, j * 32), ptx::desc_add(q, part * (kRows * D) + j * 32),
-                              id, part + j > 0);
+                  ptx::mma_f8(d, ptx::desc_add(k, j * 32),
+                              ptx::desc_add(q, part * (kRows * D) + j * 32), id, part + j > 0);
               }
             }
             ptx::mma_commit(&sm.empty[s]);
@@ -281,10 +286,10 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, co
         }
       } else if (warp >= 4) {
         // ---------------------------------------------------------------- exponentials
-        const int w = warp & 3, g = (warp - 4) >> 2;
+        const int w = warp & 3, g = ((warp - 4) >> 2) & 1, half = (warp - 4) >> 3;
         const uint32_t lanes = (uint32_t)(w * 32) << 16;
         if (kStats) {
-          // a query row: row tile g, lane
+          // a query row: row tile g, lane; half of a step's keys
           const int r = g * 128 + w * 32 + lane;
           const float c = g < tiles ? sm.row[r].x : 0.0f;
           const int64_t vis = r < rows ? min(keys, (int64_t)start + (r0 + r) / G + 1) : 0;
@@ -296,7 +301,7 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, co
             if (g < tiles) {
               const int64_t pos0 = (int64_t)(s0 + i) * kTile;
 #pragma unroll 1
-              for (int q4 = 0; q4 < 4; ++q4) {  // 32 keys
+              for (int q4 = 2 * half; q4 < 2 * half + 2; ++q4) {  // 32 keys
                 float x[32];
                 ptx::tmem_ld32(tmem + lanes + buf * kRows + g * kTile + q4 * 32, x);
                 const float f = c * sm.ks[s][q4 >> 1];
@@ -338,10 +343,11 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, co
             }
           }
           if (g < tiles)
-            p.stats[(((int64_t)bh * cut.groups + group) * ranges + range) * kRows + r] =
+            p.stats[((((int64_t)bh * cut.groups + group) * ranges + range) * 2 + half) * kRows + r] =
                 make_float2(m, l);
         } else {
-          // a key: half g of the query rows
+          // a key: a quarter of the query rows, half of row tile g
+          const int quarter = g * 2 + half;
           for (int i = 0; i < count; ++i) {
             const int at = step + i, s = at % kStages, buf = at & 1;
             const bool ok = wait(&sm.d_full[buf], (at >> 1) & 1);
@@ -357,7 +363,7 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, co
             ptx::f32x2 sum = ptx::pack2(0.0f, 0.0f);
             if (ok && g < tiles) {
 #pragma unroll 1
-              for (int q4 = 0; q4 < 4; ++q4) {  // 32 rows
+              for (int q4 = 2 * half; q4 < 2 * half + 2; ++q4) {  // 32 rows
                 float x[32];
                 ptx::tmem_ld32(tmem + lanes + buf * kRows + g * 128 + q4 * 32, x);
                 const int rr = g * 128 + q4 * 32;
@@ -388,18 +394,19 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, co
             float a, e;
             ptx::unpack2(sum, a, e);
             a += e;
-            if (g == 1) sm.part[at & 1][w * 32 + lane] = a;
-            // both halves' warps of these keys
-            asm volatile("bar.sync %0, 64;" ::"r"(2 + w) : "memory");
-            if (g == 0 && ok && id >= 0 && pos < keys) {
-              a += sm.part[at & 1][w * 32 + lane];
+            if (quarter > 0) sm.part[at & 1][quarter - 1][w * 32 + lane] = a;
+            // the four warps of these keys
+            asm volatile("bar.sync %0, 128;" ::"r"(2 + w) : "memory");
+            if (quarter == 0 && ok && id >= 0 && pos < keys) {
+#pragma unroll
+              for (int j = 0; j < 3; ++j) a += sm.part[at & 1][j][w * 32 + lane];
               float* wp = p.weights + ((int64_t)id * p.Hkv + h) * kPage + (pos & (kPage - 1));
               const float old = r0 > 0 ? *wp : pos < start && p.keep != 0.0f ? p.keep * *wp : 0.0f;
               *wp = old + a;
             }
           }
           // (a part is written again two steps on, behind the next step's barrier)
-          if (r0 == 0 && g == 0) {
+          if (r0 == 0 && quarter == 0) {
             // positions that the window holds, but no row of this group sees, begin at zero
             for (int i = s1; i < w1; ++i) {
               const int64_t pos = (int64_t)i * kTile + w * 32 + lane;
@@ -449,7 +456,7 @@ bool weigh_tc_applies(kda_dtype dt, int window, int Hq, int Hkv, int d) {
 
 size_t cache_weigh_tc_workspace(int batch, int window, int Hq, int Hkv) {
   const Cut c = cut_of(batch, window, Hq, Hkv);
-  return (size_t)batch * Hkv * c.groups * c.stat_ranges * kRows * sizeof(float2);
+  return (size_t)batch * Hkv * c.groups * c.stat_ranges * 2 * kRows * sizeof(float2);
 }
 
 kda_status launch_cache_weigh_tc(const WeighParams& p, cudaStream_t s) {
@@ -472,8 +479,20 @@ kda_status launch_cache_weigh_tc(const WeighParams& p, cudaStream_t s) {
   }
   const Cut c = cut_of(p.batch, p.window, p.Hq, p.Hkv);
   const int64_t units = (int64_t)p.batch * p.Hkv;
-  weigh_tc_kernel<true><<<(unsigned)(units * c.groups * c.stat_ranges), kThreads, bytes, s>>>(map, p, c);
-  weigh_tc_kernel<false><<<(unsigned)(units * c.ranges), kThreads, bytes, s>>>(map, p, c);
+  const unsigned stats = (unsigned)(units * c.groups * c.stat_ranges);
+  weigh_tc_kernel<true><<<stats, kThreads, bytes, s>>>(map, p, c);
+  // its CTAs split their queries while the last statistics are taken
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * c.ranges));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, weigh_tc_kernel<false>, map, p, c);
   count_launches(2);
   return check_launch("kda_cache_weigh");
 }
