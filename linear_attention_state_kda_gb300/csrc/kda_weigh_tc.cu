@@ -16,9 +16,11 @@
 // reach; the third brings the error of entries below 2^-11 of the row's largest to 2^-22 of it.
 //
 // Bound by the exponentials (two for each query row and key, 16 a cycle and SM), then by the products
-// (three parts): one row of 32768 tokens, 64 query tokens x 32 heads, 8 key/value heads takes 72 us,
-// of which either kernel's exponentials are 15 and its products 11; the rest is splitting the queries
-// once per CTA, the ramp of short ranges (14 steps of 128 keys a CTA) and two launches.
+// (three parts). One row of 32768 tokens, 64 query tokens x 32 heads, 8 key/value heads: 62 us, of
+// which either kernel's exponentials are 15 and its products 11. A step of 128 keys x 256 rows takes
+// 2240 cycles of the first kernel (1750 of products, and two looks at barriers) and 3600 of the second
+// (2050 of exponentials; the rows' constants come from shared memory beside the products' operands).
+// Splitting the queries once per CTA and joining the statistics are 5 us together.
 #include "kda_internal.cuh"
 #include "kda_fp8.cuh"
 #include "ptx.cuh"
@@ -46,6 +48,7 @@ struct Small {
   float ks[kStages][2];             // of a step's pages; 0 where there is none
   int page[kStages][2];             // -1: none
   alignas(16) float2 row[kRows];    // scale log2(e) 2^e, and minus lse
+  float2 late[kRows];               // statistics of the second half of the ranges
   float part[2][3][kTile];          // sums over the last three quarters of the rows
   uint32_t tmem;
   int abort;
@@ -132,83 +135,98 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, co
     const int s0 = kStats ? min(all_steps, range * stat_per) : w0;
     const int s1 = kStats ? min(all_steps, s0 + stat_per) : max(w0, min(w1, all_steps));
     const int count = s1 - s0;
-    // the group's query rows: a warp takes four at a time, a lane four channels
-    constexpr int kWarps = kThreads / 32;
+    // the group's query rows: a warp takes four at a time, a lane 16 channels of one
+    const int piece = lane & 7;
 #pragma unroll 1
-    for (int q4 = warp; q4 < tiles * 128; q4 += 4 * kWarps) {
-      uint2 v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = q4 + i * kWarps, at = r0 + r, j = at / G;
-        v[i] = make_uint2(0u, 0u);
-        if (r < rows)
-          v[i] = *reinterpret_cast<const uint2*>(
-              (const __nv_bfloat16*)p.q +
-              (((int64_t)b * p.window + j) * p.Hq + h * G + (at - j * G)) * D + lane * 4);
+    for (int r = (int)threadIdx.x >> 3; r < tiles * 128; r += kThreads / 8) {
+      const int at = r0 + r, j = at / G;
+      uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+      if (r < rows) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            (const __nv_bfloat16*)p.q +
+            (((int64_t)b * p.window + j) * p.Hq + h * G + (at - j * G)) * D + piece * 16);
+        v[0] = src[0];
+        v[1] = src[1];
       }
+      const uint32_t u[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+      float f[16];
+      uint32_t m = 0;
+      bool bad = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = q4 + i * kWarps;
-        if (r >= tiles * 128) break;
-        float f[4] = {__uint_as_float(v[i].x << 16), __uint_as_float(v[i].x & 0xffff0000u),
-                      __uint_as_float(v[i].y << 16), __uint_as_float(v[i].y & 0xffff0000u)};
-        uint32_t m = 0;
-        bool bad = false;
+      for (int c = 0; c < 16; ++c) {
+        f[c] = __uint_as_float(c & 1 ? u[c / 2] & 0xffff0000u : u[c / 2] << 16);
+        m = max(m, finite_abs_bits(f[c]));
+        bad |= !(fabsf(f[c]) < INFINITY);
+      }
+      // (a row is within a warp's eight lanes, all of them here)
+      const uint32_t row_lanes = 0xffu << (lane & 24);
+      m = __reduce_max_sync(row_lanes, m);
+      bad = __any_sync(row_lanes, bad);
+      // 2^e, the smallest power of two with m <= 448 2^e, at least 2^-100
+      const int e = scale_exponent(m);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          m = max(m, finite_abs_bits(f[c]));
-          bad |= !(fabsf(f[c]) < INFINITY);
-        }
-        m = __reduce_max_sync(0xffffffffu, m);
-        bad = __any_sync(0xffffffffu, bad);
-        // 2^e, the smallest power of two with m <= 448 2^e, at least 2^-100
-        const int e = scale_exponent(m);
+      for (int c = 0; c < 16; ++c) f[c] *= pow2f(-e);
+      const uint32_t off = base + Smem::Q + (r >> 7) * (128 * D) + (r & 127) * D +
+                           ((piece ^ (r & 7)) << 4);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) f[c] *= pow2f(-e);
-        const uint32_t off = base + Smem::Q + (r >> 7) * (128 * D) + (r & 127) * D +
-                             (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+      for (int part = 0; part < kParts; ++part) {
+        uint32_t code[4];
 #pragma unroll
-        for (int part = 0; part < kParts; ++part) {
-          uint32_t code;
+        for (int c = 0; c < 16; c += 4) {
           if (part < 2) {
-            const uint32_t lo = e4m3x2_from_f32(f[0], f[1]), hi = e4m3x2_from_f32(f[2], f[3]);
-            const float2 a = f32x2_from_f16x2(f16x2_from_e4m3(lo));
-            const float2 c = f32x2_from_f16x2(f16x2_from_e4m3(hi));
-            f[0] -= a.x; f[1] -= a.y; f[2] -= c.x; f[3] -= c.y;
-            code = lo | hi << 16;
+            const uint32_t lo = e4m3x2_from_f32(f[c], f[c + 1]);
+            const uint32_t hi = e4m3x2_from_f32(f[c + 2], f[c + 3]);
+            const float2 x = f32x2_from_f16x2(f16x2_from_e4m3(lo));
+            const float2 y = f32x2_from_f16x2(f16x2_from_e4m3(hi));
+            f[c] -= x.x; f[c + 1] -= x.y; f[c + 2] -= y.x; f[c + 3] -= y.y;
+            code[c / 4] = lo | hi << 16;
           } else {
-            code = e5m2x2_from_f32(f[0], f[1]) | e5m2x2_from_f32(f[2], f[3]) << 16;
+            code[c / 4] = e5m2x2_from_f32(f[c], f[c + 1]) | e5m2x2_from_f32(f[c + 2], f[c + 3]) << 16;
           }
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(off + part * (kRows * D)), "r"(code)
-                       : "memory");
         }
-        // a row with an infinity or NaN has no weights but NaN
-        if (lane == 0)
-          sm.row[r].x = bad ? __int_as_float(0x7fffffff) : p.scale * kLog2e * pow2f(e);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(off + part * (kRows * D)),
+                     "r"(code[0]), "r"(code[1]), "r"(code[2]), "r"(code[3])
+                     : "memory");
       }
+      // a row with an infinity or NaN has no weights but NaN
+      if (piece == 0)
+        sm.row[r].x = bad ? __int_as_float(0x7fffffff) : p.scale * kLog2e * pow2f(e);
     }
-    float lse = 0.0f;
-    bool none = false;  // a row past the last, or that sees nothing, adds nothing
-    const int mine = (int)threadIdx.x - 128;
+    // the rows' statistics, by two threads a row
+    const int mine = (int)threadIdx.x - 128, row = mine & (kRows - 1);
+    float2 ml = make_float2(-INFINITY, 0.0f);
     if (!kStats && group == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!kStats && mine >= 0 && mine < tiles * 128) {
-      const float2* ml =
-          p.stats + ((int64_t)bh * cut.groups + group) * (2 * cut.stat_ranges) * kRows + mine;
-      float m = -INFINITY, l = 0.0f;
-#pragma unroll 4
-      for (int i = 0; i < 2 * cut.stat_ranges; ++i) {
-        const float2 x = ml[(int64_t)i * kRows];
-        const float top = fmaxf(m, x.x), at = top == -INFINITY ? 0.0f : top;
-        l = l * exp2f(m - at) + x.y * exp2f(x.x - at);
-        m = top;
+    if (!kStats && mine >= 0 && row < tiles * 128) {
+      const float2* src =
+          p.stats + ((int64_t)bh * cut.groups + group) * (2 * cut.stat_ranges) * kRows + row;
+      const int i0 = mine < kRows ? 0 : cut.stat_ranges, i1 = i0 + cut.stat_ranges;
+      constexpr int kBatch = 10;  // side by side
+#pragma unroll 1
+      for (int i = i0; i < i1; i += kBatch) {
+        float2 x[kBatch];
+        float top = ml.x;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          x[k] = i + k < i1 ? src[(int64_t)(i + k) * kRows] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) top = fmaxf(top, x[k].x);
+        const float at = top == -INFINITY ? 0.0f : top;
+        ml.y *= ptx::ex2_approx(ml.x - at);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) ml.y += x[k].y * ptx::ex2_approx(x[k].x - at);
+        ml.x = top;
       }
-      none = mine >= rows || (m == -INFINITY && !(l != l));
-      lse = none ? INFINITY : (m == -INFINITY ? 0.0f : m) + log2f(l);
+      if (mine >= kRows) sm.late[row] = ml;
     }
     __syncthreads();
     if (!kStats && mine >= 0 && mine < tiles * 128) {
-      sm.row[mine].y = -lse;
-      if (none) sm.row[mine].x = 0.0f;
+      const float2 x = sm.late[row];
+      const float m = fmaxf(ml.x, x.x), at = m == -INFINITY ? 0.0f : m;
+      const float l = ml.y * ptx::ex2_approx(ml.x - at) + x.y * ptx::ex2_approx(x.x - at);
+      // a row past the last, or that sees nothing, adds nothing
+      const bool none = row >= rows || (m == -INFINITY && !(l != l));
+      sm.row[row].y = none ? -INFINITY : -(at + log2f(l));
+      if (none) sm.row[row].x = 0.0f;
     }
     ptx::fence_proxy_async_smem();
     __syncthreads();
