@@ -3,8 +3,9 @@
 Tolerance, element by element. A score is an fp32 sum of at most 128 exact products (fp32 queries:
 known to 2^-22; windows of more than 64 query rows: to 2^-20 of the query's largest entry, 2^-17 of
 that sum for the queries here): |ds| <= 2^-16 of the sum of absolute products (3/2 of it in such
-windows), whose largest over the row's keys is top; a weight p = exp(s - lse) moves by at most 2 |ds| p, the exponentials, the sums of at most 2^13
-weights and of the old weight by 2^-18 of the result together."""
+windows), whose largest over the row's keys is top; a weight p = exp(s - lse) moves by at most
+2 |ds| p, the exponentials, the sums of at most 2^13 weights and of the old weight by 2^-18 of the
+result together."""
 import numpy as np
 import pytest
 import torch
@@ -208,3 +209,81 @@ def test_infinite_and_nan_queries():
             assert torch.isnan(mine).all()
             got[page, 1] = clean[page, 1]
             assert torch.equal(got, clean)
+
+
+@pytest.mark.parametrize("dtype,d,W,Hq", [("bf16", 128, 4, 8), ("bf16", 64, 4, 24), ("f32", 128, 4, 8),
+                                          ("f32", 64, 9, 16)])
+def test_wide_tables(dtype, d, W, Hq):
+    """Few rows with wide page tables: statistics and weights in a launch each, most ranges of keys
+    empty. Padding rows, windows of no token, absent pages, several groups of query rows; and two
+    captured graphs that share a workspace."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(10)
+    start, lens = [200, -1, 70, 30, 1000, 0], [2, 4, 0, W, W - 1, 1]
+    q, table, pool = _make(gen, start, W, Hq, 2, d, dtype)
+    table[0, 1] = -1
+    table[4, 3] = -7
+    wide = torch.full((6, 700), -1, dtype=torch.int32, device=DEV)
+    wide[:, :table.shape[1]] = table
+    wide[5, 690] = 0  # far behind what row 5 sees
+    need = kda.cache_weigh_workspace(q.dtype, 6, W, Hq, 2, d, 700)
+    assert need > 0
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device=DEV)
+    before = _weights(pool[0].shape[0], 2)
+    got = before.clone()
+    args = (_i32(start), wide, pool[0], pool[1])
+    kda.cache_weigh(q, *args, got, scale=0.04, lens=_i32(lens), keep=0.5, workspace=ws)
+    check(q, start, lens, table, pool, before, got, 0.04, 0.5)
+    q2, ln = q.flip(0).contiguous(), _i32(lens)
+    want = before.clone()
+    kda.cache_weigh(q2, *args, want, scale=0.04, lens=ln, keep=0.5)
+    a, b = before.clone(), before.clone()
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for gr, x, w in zip(graphs, (q, q2), (a, b)):
+        with torch.cuda.graph(gr):
+            kda.cache_weigh(x, *args, w, scale=0.04, lens=ln, keep=0.5, workspace=ws)
+    for _ in range(2):
+        a.copy_(before)
+        b.copy_(before)
+        graphs[0].replay()
+        graphs[1].replay()
+    assert torch.equal(a, got) and torch.equal(b, want)
+
+
+@pytest.mark.parametrize("dtype,d,W", [("bf16", 128, 1), ("f32", 64, 3)])
+def test_more_keys_than_a_cluster_has_room_for(dtype, d, W):
+    """Many rows (clusters), one of them longer than the scores have room for."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(11)
+    start = [40000] + [3 * i for i in range(19)]
+    q, table, pool = _make(gen, start, W, 16, 2, d, dtype)
+    before = _weights(pool[0].shape[0], 2)
+    got = before.clone()
+    scale = 0.3 * d ** -0.5
+    assert kda.cache_weigh_workspace(q.dtype, 20, W, 16, 2, d, table.shape[1]) == 0
+    kda.cache_weigh(q, _i32(start), table, pool[0], pool[1], got, scale=scale)
+    check(q, start, None, table, pool, before, got, scale, 1.0)
+
+
+def test_many_queries_in_two_graphs():
+    """Windows of more than 64 query rows, captured: two graphs that share a workspace."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(12)
+    start, W = [700, 3], 40
+    q, table, pool = _make(gen, start, W, 8, 2, 128, "bf16")
+    ws = torch.empty(kda.cache_weigh_workspace(q.dtype, 2, W, 8, 2, 128, table.shape[1]),
+                     dtype=torch.uint8, device=DEV)
+    qs, st = (q, q.flip(0).contiguous()), _i32(start)
+    before = _weights(pool[0].shape[0], 2)
+    want = [before.clone() for _ in qs]
+    for x, w in zip(qs, want):
+        kda.cache_weigh(x, st, table, pool[0], pool[1], w, scale=0.04)
+    got, graphs = [before.clone() for _ in qs], [torch.cuda.CUDAGraph() for _ in qs]
+    for gr, x, w in zip(graphs, qs, got):
+        with torch.cuda.graph(gr):
+            kda.cache_weigh(x, st, table, pool[0], pool[1], w, scale=0.04, workspace=ws)
+    for w in got:
+        w.copy_(before)
+    for gr in graphs:
+        gr.replay()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
