@@ -118,7 +118,8 @@ kda_status launch_window_t(const DecayParams& p, cudaStream_t s) {
 //     S'  = e^{gamma_C} S + sum_j e^{gamma_C - gamma_j} k_j v_j^T
 // The state is in registers (D/16 x 4 a thread), copied to shared memory for the first sum. Bound by
 // the fp32 units and, nearly as much, by shared memory: 5 prompts up to 1301 tokens x 6 heads of 64
-// 50 us (a sixth of them in each chunk's barriers), 8192 x 16 of 128 740 us, 13 TFLOP/s.
+// 49 us, 8192 x 16 of 128 606 us, 13 T multiply-adds/s in both passes (740 us with the rows asked for
+// only when they were needed).
 constexpr int kC = 32;
 constexpr int kSimtThreads = 256;
 
@@ -129,11 +130,11 @@ struct SimtShape {
 };
 
 template <int D, bool kStates>
-__global__ void __launch_bounds__(kSimtThreads)
+__global__ void __launch_bounds__(kSimtThreads, D == 64 ? 4 : 2)
 decay_chunk_kernel(const DecayParams p, int seg, float* added, float* added_log) {
   using S = SimtShape<D>;
   using T = float;
-  constexpr int RPT = D / 16, N = Vec16<T>::N;
+  constexpr int RPT = D / 16;
   extern __shared__ float smem[];
   float* sq = smem;
   float* sk = sq + kC * S::DP;
@@ -167,36 +168,42 @@ decay_chunk_kernel(const DecayParams p, int seg, float* added, float* added_log)
 
   const T *q = (const T*)p.q + (int64_t)hk * D, *k = (const T*)p.k + (int64_t)hk * D,
           *v = (const T*)p.v + (int64_t)h * D + col0;
+  // a chunk's rows, zeros past its end, are asked for while the chunk before is worked on
+  constexpr int NK = kC * (D / 4) / kSimtThreads, NV = kC * (kCols / 4) / kSimtThreads;
+  float4 fq[NK], fk[NK], fv[NV];
+  auto ask = [&](int64_t t0) {
+#pragma unroll
+    for (int j = 0; j < NK; ++j) {
+      const int i = tid + j * kSimtThreads, t = i / (D / 4), c = (i % (D / 4)) * 4;
+      fq[j] = fk[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (t0 + t < x.hi) {
+        if (!kStates) fq[j] = *reinterpret_cast<const float4*>(q + (t0 + t) * p.qs + c);
+        fk[j] = *reinterpret_cast<const float4*>(k + (t0 + t) * p.ks + c);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = tid + j * kSimtThreads, t = i / (kCols / 4), c = (i % (kCols / 4)) * 4;
+      fv[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (t0 + t < x.hi) fv[j] = *reinterpret_cast<const float4*>(v + (t0 + t) * p.vs + c);
+    }
+  };
+  if (x.lo < x.hi) ask(x.lo);
   for (int64_t t0 = x.lo; t0 < x.hi; t0 += kC) {
     const int n = (int)(x.hi - t0 < kC ? x.hi - t0 : kC);
     __syncthreads();
-    // rows of the chunk, zeros past its end
-    for (int i = tid; i < kC * (D / N); i += kSimtThreads) {
-      const int t = i / (D / N), c = (i % (D / N)) * N;
-      uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-      if (t < n) {
-        if (!kStates) a = *reinterpret_cast<const uint4*>(q + (t0 + t) * p.qs + c);
-        b = *reinterpret_cast<const uint4*>(k + (t0 + t) * p.ks + c);
-      }
-      float f[N];
-      if (!kStates) {
-        Vec16<T>::unpack(a, f);
 #pragma unroll
-        for (int e = 0; e < N; ++e) sq[t * S::DP + c + e] = f[e];
-      }
-      Vec16<T>::unpack(b, f);
-#pragma unroll
-      for (int e = 0; e < N; ++e) sk[t * S::DP + c + e] = f[e];
+    for (int j = 0; j < NK; ++j) {
+      const int i = tid + j * kSimtThreads, t = i / (D / 4), c = (i % (D / 4)) * 4;
+      if (!kStates) *reinterpret_cast<float4*>(&sq[t * S::DP + c]) = fq[j];
+      *reinterpret_cast<float4*>(&sk[t * S::DP + c]) = fk[j];
     }
-    for (int i = tid; i < kC * (kCols / N); i += kSimtThreads) {
-      const int t = i / (kCols / N), c = (i % (kCols / N)) * N;
-      uint4 a = make_uint4(0u, 0u, 0u, 0u);
-      if (t < n) a = *reinterpret_cast<const uint4*>(v + (t0 + t) * p.vs + c);
-      float f[N];
-      Vec16<T>::unpack(a, f);
 #pragma unroll
-      for (int e = 0; e < N; ++e) sv[t * S::VP + c + e] = f[e];
+    for (int j = 0; j < NV; ++j) {
+      const int i = tid + j * kSimtThreads, t = i / (kCols / 4), c = (i % (kCols / 4)) * 4;
+      *reinterpret_cast<float4*>(&sv[t * S::VP + c]) = fv[j];
     }
+    if (t0 + kC < x.hi) ask(t0 + kC);
     if (!kStates) {
 #pragma unroll
       for (int i = 0; i < RPT; ++i)
@@ -355,7 +362,7 @@ decay_scan_kernel(const DecayParams p, int seg, float* added, const float* added
 // 1000 x 16: 87 and 107. At least 256 tokens: 2048 x 8 29 us, with 512 37; 8192 x 2 31 us, with 128 37.
 // (But 300 x 4 17 us in one, 23 in two.)
 // fp32, 5 prompts up to 1301 x 6: 51 us, with 256 tokens at least 91; 8192 x 16: 743, with half as
-// many 803, with twice as many 833.
+// many 803, with twice as many 833 (before its rows were asked for ahead).
 int segment_tokens(kda_dtype dt, int total, int H, int d) {
   const int64_t units = (int64_t)H * (dt == KDA_BF16 ? 1 : d / kCols);
   const int64_t all = dt == KDA_BF16 ? 152 : 608, want = units < all ? all / units : 1;

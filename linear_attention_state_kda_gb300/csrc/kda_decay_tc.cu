@@ -83,8 +83,8 @@ struct Out {
 // Every wait is by parity, which tells a phase only from the one before it, so none may be two phases
 // behind. Each barrier's next phase needs, at some remove, what its waiters do after this one: a
 // stage's chunk is refilled once every role has left it; the next scores wait for p_full, the next
-// sum and V' for kv_done and u_empty, the next rounded state for sq_done, the next V for o_full, the next
-// outputs for o_empty. P runs up to two chunks ahead of the products, so its barriers are by place.
+// sum and V' for kv_done and u_empty, the next rounded state for sq_done, the next V for o_full, the
+// next outputs for o_empty. P runs up to two chunks ahead of the products, so its barriers are by place.
 struct OutSmall {
   UnitRing units;
   uint64_t full[kStages], empty[kStages];
