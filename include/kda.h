@@ -602,8 +602,9 @@ KDA_API kda_status kda_draft_verify(kda_dtype dt, int batch, int window, int voc
  *   n_seqs at most 2^24, total_tokens 2^30, H 65535, (total_tokens / 256 + n_seqs) * H below 2^31.
  *   status      optional device word (KDA_STATUS_BAD_OFFSETS, KDA_STATUS_TIMEOUT).
  * bf16 runs on the tensor cores (KDA_ERR_UNSUPPORTED when the driver lacks cuTensorMapEncodeTiled),
- * fp32 on CUDA cores. With bf16 the state and the weighted products q.k enter the outputs rounded to
- * bf16; new keys and values enter the state at 24 bits.
+ * fp32 on CUDA cores. With bf16 the state and the weighted products q.k enter the outputs in two bf16
+ * parts (2^-15 of a term), so that an output is off by little more than its own rounding; new keys and
+ * values enter the state at 24 bits.
  */
 KDA_API size_t kda_decay_prefill_workspace(kda_dtype dt, int n_seqs, int total_tokens, int H, int d);
 KDA_API kda_status kda_decay_prefill(kda_dtype dt, int n_seqs, int total_tokens,

@@ -4,26 +4,30 @@
 // the state before it (fp32, transposed: a thread has a value channel and half of the key channels),
 //     O^T = e^gamma_t * (S^T Q^T) + V^T P^T,   P_ts = [s <= t] e^(gamma_t - gamma_s) q_t . k_s
 //     S'^T = e^Gamma S^T + V'^T K,             V'_s = e^(Gamma - gamma_s) v_s
-// Every product is a tcgen05 bf16 product with fp32 sums. S and P enter theirs rounded to bf16, which
-// costs an output as much as its own rounding to bf16 (together 1.4 times the latter alone; in two
-// parts each they cost half of the issue slots, which bound the kernel then). What a token adds to
-// the state stays for the rest of the sequence, and states are fp32: V' is carried in three bf16
-// parts (24 bits), and each chunk's V'^T K is a sum of its own, added to the state in registers. The
-// two sums of O have accumulators of their own and meet in fp32, so that Q needs no decayed copy.
+// Every product is a tcgen05 bf16 product with fp32 sums. Operands that are not inputs are carried in
+// several bf16 parts, so that an output is as exact as its own rounding lets it be: S and P in two
+// (2^-15 of a term; rounded to one, outputs whose terms cancel were off by up to 16 times their own
+// rounding), V' in three (24 bits: states are fp32, and what a token adds stays for the rest of the
+// sequence). Each chunk's V'^T K is a sum of its own, added to the state in registers. The two sums of
+// O have accumulators of their own and meet in fp32, so that Q needs no decayed copy.
 //
 // Roles of a CTA (28 warps): one takes the units of work (segments of a head), one loads (TMA), one
 // sums the decays, one issues the products; 8 put V and V' into TMEM, transposed on the way; 4 turn
 // q.k into P; 8 keep the state; 4 write outputs. The chunks of all units run through them as one
-// stream, so that a unit's ends are covered by its neighbours. Order of the products per chunk:
-// V'^T K, which the state waits for, then S^T Q^T, V^T P^T and the next chunk's q.k.
+// stream, so that a unit's ends are covered by its neighbours. Order of the products per chunk: q.k,
+// V'^T K, which the state waits for, S^T Q^T and V^T P^T. The state's high part lies in TMEM, which is
+// full then, the low part in shared memory: three chunks of q, k and v fit beside it.
 //
-// 16384 tokens x 32 heads (d = 128): 164 us, of which what the segments add takes 54, the scan 7
-// and the outputs 105. The outputs move 537 MB in that, 5.1 TB/s; a chunk takes 3000 cycles of the
-// warp that issues: 1450 of products (three parts of V' are half of them), the rest its looks at
-// barriers, some 300 each. Measured and left: the states' products from a warp of their own (125 us:
-// products of two warps take turns and slow each other), all looks in one before the last three
-// products (115 us: they wait for the slowest), q.k before S^T Q^T (109 us). What a segment adds
-// takes 1350 cycles a chunk, 268 MB in 54 us, 5.0 TB/s.
+// 16384 tokens x 32 heads (d = 128): 180 us, of which what the segments add takes 55, the scan 7
+// and the outputs 120 (with S and P in one part each 163 and 105). The outputs move 537 MB in that, 4.5
+// TB/s; a chunk takes some 3500 cycles: 2300 in which the warp that issues has products to issue (44,
+// of which the three parts of V' are a third and half of the tensor time), the rest its looks at
+// barriers and its waits for the last chunk's outputs and the state's parts, whose warps share the issue
+// slots. Measured and left: both parts of the state in TMEM, the scores in the second sum's columns
+// (205 us: P and the outputs then wait for one another); the two parts of S^T Q^T behind barriers of
+// their own (188-208: more looks); V'^T K before q.k (189); all looks in one before the last products
+// (204: they wait for the slowest). What a segment adds takes 1350 cycles a chunk: three of four
+// segments a head, 201 MB, on 96 of the SMs.
 #include "kda_decay.cuh"
 #include "kda_fp8.cuh"
 #include "ptx.cuh"
@@ -34,7 +38,8 @@ namespace {
 using namespace decay;
 
 constexpr int kC = 64;
-constexpr int kStages = 4;
+constexpr int kStages = 4;  // chunks that the roles work on
+constexpr int kData = 3;    // of these, with their q, k and v in shared memory (released earlier)
 constexpr int kThreads = 896;
 constexpr int kAhead = 2, kAddAhead = 8;  // chunks whose decays are asked for ahead (room; latency)
 constexpr uint32_t kTries = 1u << 19;  // of a wait inside a CTA: 2 s
@@ -76,28 +81,31 @@ template <int D>
 struct Out {
   static constexpr int TILE = kC * D * 2, STAGE = 3 * TILE;
   static constexpr int Q = 0, K = TILE, V = 2 * TILE;
-  static constexpr int P = kStages * STAGE;  // two of 8 KB, in turn
-  static constexpr int O = P + 2 * 8192;     // outputs, as Q
-  static constexpr int SMALL = O + TILE;
+  static constexpr int P = kData * STAGE;  // two parts of 8 KB
+  static constexpr int O = P + 2 * 8192;   // outputs, as Q
+  static constexpr int LO = O + TILE;      // low part of the state: [128 value channels][64 key channels]
+  static constexpr int SMALL = LO + 128 * D * 2;
 };
 // Every wait is by parity, which tells a phase only from the one before it, so none may be two phases
 // behind. Each barrier's next phase needs, at some remove, what its waiters do after this one: a
-// stage's chunk is refilled once every role has left it; the next scores wait for p_full, the next
-// sum and V' for kv_done and u_empty, the next rounded state for sq_done, the next V for o_full, the
-// next outputs for o_empty. P runs up to two chunks ahead of the products, so its barriers are by place.
+// stage's chunk is replaced once every role has left it, its data once the products and V' have; the
+// next scores wait for p_full, the next P for sc_full (which comes behind V^T P^T of the last), the
+// next sum and V' for kv_done and u_empty, the next parts of the state for sq_done, the next V for
+// o_full, the next outputs for o_empty.
 struct OutSmall {
   UnitRing units;
-  uint64_t full[kStages], empty[kStages];
-  uint64_t sc_full, p_full[2], p_empty[2], v_full, vt_full, u_empty, hi_full;
+  uint64_t full[kStages], empty[kStages], data_full[kData], data_empty[kData];
+  uint64_t sc_full, p_full, v_full, vt_full, u_empty, hi_full;
   uint64_t kv_done, sq_done, o_full, o_empty, drain;
   float ghi[kStages][kC], glo[kStages][kC];  // running sums of log2 decays, high and low parts
+  float in[kStages][kC], out[kStages][kC];   // decays from the chunk's start, and to its end
   float g[kAhead][kC];                       // log-decays of the next chunks
-  float2 total[kStages];
+  float total[kStages];                      // decay of a whole chunk
   Chunk chunk[kStages];
   uint32_t tmem;
   int abort;
 };
-// TMEM columns: what a chunk adds to the state (fp32), the state's bf16 rounding, V' in three parts and
+// TMEM columns: what a chunk adds to the state (fp32), the state's high part, V' in three parts and
 // V (transposed, two tokens a column), the scores, and the two sums of O, all 512 at D = 128.
 template <int D>
 struct Tm {
@@ -123,9 +131,6 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t at) {
 __device__ __forceinline__ uint32_t tops(float a, float b) {
   return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
-__device__ __forceinline__ float top(float x) {
-  return __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -135,8 +140,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ uint32_t take_top(ptx::f32x2& x) {
   float a, b;
   ptx::unpack2(x, a, b);
-  x = ptx::fma2(ptx::pack2(top(a), top(b)), ptx::pack2(-1.0f, -1.0f), x);
-  return tops(a, b);
+  const uint32_t t = tops(a, b);
+  float ra, rb;
+  asm("{\n\t.reg .b16 lo, hi, m;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "mov.b16 m, 0xbf80;\n\t"
+      "fma.rn.f32.bf16 %0, lo, m, %3;\n\t"
+      "fma.rn.f32.bf16 %1, hi, m, %4;\n\t}"
+      : "=f"(ra), "=f"(rb)
+      : "r"(t), "f"(a), "f"(b));
+  x = ptx::pack2(ra, rb);
+  return t;
+}
+// A pair in two bf16 parts: the first cut (it never overflows), the rest rounded, 2^-15 in all. An
+// infinity or NaN stays one: its rest is NaN.
+__device__ __forceinline__ void split2(ptx::f32x2 x, uint32_t& hi, uint32_t& lo) {
+  hi = take_top(x);
+  float a, b;
+  ptx::unpack2(x, a, b);
+  lo = pack_bf16(a, b);
 }
 // Two bf16 values times two weights in three parts of 8 bits: the fp32 products exactly.
 __device__ __forceinline__ void weigh3(uint32_t v, ptx::f32x2 w, uint32_t part[3]) {
@@ -313,7 +335,11 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&sm.full[i], 2);
-      ptx::mbar_init(&sm.empty[i], 1 + 4 + 5 * NQ);
+      ptx::mbar_init(&sm.empty[i], 4 + 5 * NQ);
+    }
+    for (int i = 0; i < kData; ++i) {
+      ptx::mbar_init(&sm.data_full[i], 1);
+      ptx::mbar_init(&sm.data_empty[i], 1 + 2 * NQ);
     }
     for (int i = 0; i < kUnits; ++i) {
       ptx::mbar_init(&sm.units.full[i], 1);
@@ -322,10 +348,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
     ptx::mbar_init(&sm.units.clc, 1);
     ptx::mbar_init(&sm.units.ask, 1);
     ptx::mbar_init(&sm.sc_full, 1);
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&sm.p_full[i], 4);
-      ptx::mbar_init(&sm.p_empty[i], 1);
-    }
+    ptx::mbar_init(&sm.p_full, 4);
     ptx::mbar_init(&sm.v_full, 2 * NQ);
     ptx::mbar_init(&sm.vt_full, 2 * NQ);
     ptx::mbar_init(&sm.u_empty, 2 * NQ);
@@ -352,7 +375,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(bar);
   };
-  // The next chunk n, for every role but the one that loads it; false: none, or a wait gave up.
+  // The next chunk n, for P's warps; false: none, or a wait gave up.
   auto take = [&](int n, Chunk& c) {
     if (!wait(&sm.full[n % kStages], (n / kStages) & 1)) return false;
     c = sm.chunk[n % kStages];
@@ -368,6 +391,9 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
       const uint32_t lanes = (uint32_t)(w * 32) << 16;
       const uint32_t t_u = tmem + lanes + T::U + half * (D / 2);
       const uint32_t t_hi = tmem + lanes + T::HI + half * (D / 4);
+      // the row of the low part: blocks of 64 key channels, 128-byte swizzle
+      const uint32_t row = w * 32 + lane, lo = base + M::LO + row * 128 + (D == 128 ? half * 16384 : 0);
+      const uint32_t lo0 = D == 128 ? 0 : half * 4;
       const int at = half * (D / 2) * D + w * 32 + lane;  // of the state's matrix
       float* exit_state = nullptr;
       Chunk c;
@@ -404,20 +430,21 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
         if (n > 0 && !wait(&sm.sq_done, (n - 1) & 1)) break;
         ptx::tc_fence_after();
 #pragma unroll
-        for (int b = 0; b < D / 4; b += 16) {
-          float h[16];
+        for (int b = 0; b < D / 4; b += 8) {
+          uint32_t hi[8], l[8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x, y;
-            ptx::unpack2(st[b + i], x, y);
-            h[i] = __uint_as_float(pack_bf16(x, y));
-          }
-          ptx::tmem_st16(t_hi + b, h);
+          for (int i = 0; i < 8; ++i) split2(st[b + i], hi[i], l[i]);
+          ptx::tmem_st8(t_hi + b, hi);
+#pragma unroll
+          for (int i = 0; i < 8; i += 4)
+            st_shared(lo + ((((b + i) / 4 + lo0) ^ (row & 7)) << 4),
+                      make_uint4(l[i], l[i + 1], l[i + 2], l[i + 3]));
         }
+        ptx::fence_proxy_async_smem();
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         arrive(&sm.hi_full);
-        const float a = ptx::ex2_approx(sm.total[s].x + sm.total[s].y);
+        const float a = sm.total[s];
         const ptx::f32x2 aa = ptx::pack2(a, a);
         if (!wait(&sm.kv_done, n & 1)) break;
         ptx::tc_fence_after();
@@ -446,6 +473,10 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
       uint32_t unit = 0;
       Unit u;
       bool ok = true;
+      auto room = [&](int n) {
+        return (n < kStages || wait(&sm.empty[n % kStages], ((n / kStages) - 1) & 1)) &&
+               (n < kData || wait(&sm.data_empty[n % kData], ((n / kData) - 1) & 1));
+      };
 #pragma unroll 1
       while (ok && next_unit(sm.units, wait, lane, unit, u)) {
         const int hk = u.head / (p.H / p.Hk);
@@ -462,28 +493,29 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
           c.kind = (short)((t == u.lo ? kFirst : 0) | (u.hi - t <= kC ? kLast : 0));
           c.exit = c.kind & kLast ? u.exit : nullptr;
           if ((c.kind & kLast) && lane == 0) ptx::mbar_arrive(&sm.units.ask);
-          if (n >= kStages && !(ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1))) break;
+          if (!(ok = room(n))) break;
           if (lane == 0) {
             sm.chunk[s] = c;
-            uint8_t* st = smem + s * M::STAGE;
+            ptx::mbar_arrive(&sm.full[s]);
+            uint64_t* bar = &sm.data_full[n % kData];
+            uint8_t* st = smem + n % kData * M::STAGE;
             if (c.tokens > 0) {
-              ptx::mbar_arrive_expect_tx(&sm.full[s], M::STAGE);
-              load_tile<D>(st + M::K, &maps.k, &sm.full[s], hk, t);
-              load_tile<D>(st + M::Q, &maps.q, &sm.full[s], hk, t);
-              load_tile<D>(st + M::V, &maps.v, &sm.full[s], u.head, t);
+              ptx::mbar_arrive_expect_tx(bar, M::STAGE);
+              load_tile<D>(st + M::K, &maps.k, bar, hk, t);
+              load_tile<D>(st + M::Q, &maps.q, bar, hk, t);
+              load_tile<D>(st + M::V, &maps.v, bar, u.head, t);
             } else {  // an empty sequence: all rows are cleared, the state passes through
-              ptx::mbar_arrive(&sm.full[s]);
+              ptx::mbar_arrive(bar);
             }
           }
           ++n;
           t += kC;
         } while (t < u.hi);
       }
-      const int s = n % kStages;
-      if (ok && n >= kStages) ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1);
-      if (ok && lane == 0) {
-        sm.chunk[s].kind = kStop;
-        ptx::mbar_arrive(&sm.full[s]);
+      if (ok && room(n) && lane == 0) {
+        sm.chunk[n % kStages].kind = kStop;
+        ptx::mbar_arrive(&sm.full[n % kStages]);
+        ptx::mbar_arrive(&sm.data_full[n % kData]);
       }
       if (*(volatile int*)&sm.abort) {  // the loads in flight land before the CTA leaves
         __nanosleep(1000000);
@@ -514,7 +546,14 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
           if (n >= kStages && !(ok = wait(&sm.empty[s], ((n / kStages) - 1) & 1))) break;
           *reinterpret_cast<float2*>(&sm.ghi[s][2 * lane]) = make_float2(a.x, b.x);
           *reinterpret_cast<float2*>(&sm.glo[s][2 * lane]) = make_float2(a.y, b.y);
-          if (lane == 31) sm.total[s] = b;
+          const float ea = ptx::ex2_approx(a.x + a.y), eb = ptx::ex2_approx(b.x + b.y);
+          const float2 all = make_float2(__shfl_sync(0xffffffffu, b.x, 31),
+                                         __shfl_sync(0xffffffffu, b.y, 31));
+          *reinterpret_cast<float2*>(&sm.in[s][2 * lane]) = make_float2(ea, eb);
+          *reinterpret_cast<float2*>(&sm.out[s][2 * lane]) =
+              make_float2(ptx::ex2_approx((all.x - a.x) + (all.y - a.y)),
+                          ptx::ex2_approx((all.x - b.x) + (all.y - b.y)));
+          if (lane == 31) sm.total[s] = eb;
           arrive(&sm.full[s]);
           ++n;
           ++i;
@@ -545,8 +584,13 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
       // (loops rolled: unrolled, this role's code alone did not fit the instruction cache)
       const uint32_t id_o = ptx::idesc_make(ptx::kFmtBF16, 128, kC, false, false);
       const uint32_t id_sc = ptx::idesc_make(ptx::kFmtBF16, kC, kC, false, false);
-      auto issue_qk = [&](int n) {
-        const uint32_t st = base + (n % kStages) * M::STAGE;
+#pragma unroll 1
+      for (int n = 0;; ++n) {
+        const uint32_t st = base + n % kData * M::STAGE, ph = n & 1;
+        // (V' says that the chunk itself is there, or that there is none)
+        if (n == 0 ? !wait(&sm.v_full, 0) : !wait.both(&sm.u_empty, ph ^ 1, &sm.v_full, ph)) break;
+        if (__shfl_sync(0xffffffffu, (int)sm.chunk[n % kStages].kind, 0) == kStop) break;
+        ptx::tc_fence_after();
         if (ptx::elect_one()) {
           const uint64_t a = ptx::sdesc_sw128(st + M::Q, 16, 1024);
           const uint64_t b = ptx::sdesc_sw128(st + M::K, 16, 1024);
@@ -557,19 +601,6 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
               ptx::mma_f16(tmem + T::SC, ptx::desc_add(a, i * 8192 + j * 32),
                            ptx::desc_add(b, i * 8192 + j * 32), id_sc, i + j > 0);
           ptx::mma_commit(&sm.sc_full);
-        }
-        __syncwarp();
-      };
-      Chunk c;
-      bool ok = take(0, c);
-      if (ok) issue_qk(0);
-#pragma unroll 1
-      for (int n = 0; ok; ++n) {
-        const int s = n % kStages;
-        const uint32_t st = base + s * M::STAGE, ph = n & 1;
-        if (n == 0 ? !wait(&sm.v_full, 0) : !wait.both(&sm.u_empty, ph ^ 1, &sm.v_full, ph)) break;
-        ptx::tc_fence_after();
-        if (ptx::elect_one()) {
           issue_kv<D>(tmem + T::U, tmem + T::VP, st + M::K);
           ptx::mma_commit(&sm.kv_done);
         }
@@ -578,31 +609,36 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           const uint64_t b = ptx::sdesc_sw128(st + M::Q, 16, 1024);
+          const uint64_t lo = ptx::sdesc_sw128(base + M::LO, 16, 1024);
 #pragma unroll 1
           for (uint32_t i = 0; i < D / 64; ++i)
 #pragma unroll
             for (uint32_t j = 0; j < 4; ++j)
               ptx::mma_f16_ts(tmem + T::OI, tmem + T::HI + i * 32 + j * 8,
                               ptx::desc_add(b, i * 8192 + j * 32), id_o, i + j > 0);
+#pragma unroll 1
+          for (uint32_t i = 0; i < D / 64; ++i)
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+              ptx::mma_f16(tmem + T::OI, ptx::desc_add(lo, i * 16384 + j * 32),
+                           ptx::desc_add(b, i * 8192 + j * 32), id_o, 1);
           ptx::mma_commit(&sm.sq_done);
-          ptx::mma_commit(&sm.empty[s]);
+          ptx::mma_commit(&sm.data_empty[n % kData]);
         }
         __syncwarp();
-        if (!wait.both(&sm.p_full[ph], (n >> 1) & 1, &sm.vt_full, ph)) break;
+        if (!wait.both(&sm.p_full, ph, &sm.vt_full, ph)) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
-          const uint64_t b = ptx::sdesc_sw128(base + M::P + ph * 8192, 16, 1024);
+          const uint64_t b = ptx::sdesc_sw128(base + M::P, 16, 1024);
+#pragma unroll 1
+          for (uint32_t part = 0; part < 2; ++part)
 #pragma unroll
-          for (uint32_t i = 0; i < kC / 16; ++i)
-            ptx::mma_f16_ts(tmem + T::OA, tmem + T::VT + i * 8, ptx::desc_add(b, i * 32), id_o, i > 0);
+            for (uint32_t i = 0; i < kC / 16; ++i)
+              ptx::mma_f16_ts(tmem + T::OA, tmem + T::VT + i * 8,
+                              ptx::desc_add(b, part * 8192 + i * 32), id_o, part + i > 0);
           ptx::mma_commit(&sm.o_full);
-          ptx::mma_commit(&sm.p_empty[ph]);
         }
         __syncwarp();
-        // (P's warps have read this chunk's scores)
-        const bool more = take(n + 1, c);
-        if (more) issue_qk(n + 1);
-        ok = more;
       }
       if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort)) {  // the products in flight end first
         if (ptx::elect_one()) ptx::mma_commit(&sm.drain);
@@ -617,23 +653,25 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
     const int w = warp & 3, tok = ((warp - 16) >> 2) * 32;  // 32 channels, half of the tokens
     if (w < NQ) {
       const uint32_t lanes = (uint32_t)(w * 32) << 16;
-      Chunk c;
 #pragma unroll 1
-      for (int n = 0; take(n, c); ++n) {
-        const int s = n % kStages, m = c.tokens;
-        const uint32_t st = base + s * M::STAGE;
-        const float2 total = sm.total[s];
+      for (int n = 0;; ++n) {
+        const int s = n % kStages;
+        if (!wait.both(&sm.full[s], (n / kStages) & 1, &sm.data_full[n % kData], (n / kData) & 1)) break;
+        if (__shfl_sync(0xffffffffu, (int)sm.chunk[s].kind, 0) == kStop) {
+          // which the products learn from this barrier, once they have left its last phase
+          if (n == 0 || wait(&sm.kv_done, (n - 1) & 1)) arrive(&sm.v_full);
+          break;
+        }
+        const int m = sm.chunk[s].tokens;
+        const uint32_t st = base + n % kData * M::STAGE;
         ptx::f32x2 weight[4];
         uint32_t raw[2][8];
         load_vt(st + M::V, w * 32, tok, lane, raw[0]);
         load_vt(st + M::V, w * 32 + 16, tok, lane, raw[1]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int t = tok + i * 8 + 2 * (lane & 3);
-          const float2 h2 = *reinterpret_cast<const float2*>(&sm.ghi[s][t]);
-          const float2 l2 = *reinterpret_cast<const float2*>(&sm.glo[s][t]);
-          weight[i] = ptx::pack2(ptx::ex2_approx((total.x - h2.x) + (total.y - l2.x)),
-                                 ptx::ex2_approx((total.x - h2.y) + (total.y - l2.y)));
+          const float2 f = *reinterpret_cast<const float2*>(&sm.out[s][tok + i * 8 + 2 * (lane & 3)]);
+          weight[i] = ptx::pack2(f.x, f.y);
         }
         if (m < kC) {  // rows of the next sequence, whatever they hold: zeros, in K too
 #pragma unroll
@@ -651,6 +689,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
           ptx::fence_proxy_async_smem();
         }
         arrive(&sm.empty[s]);
+        if (lane == 0) ptx::mbar_arrive(&sm.data_empty[n % kData]);
         if (n > 0 && !wait(&sm.kv_done, (n - 1) & 1)) break;
         ptx::tc_fence_after();
 #pragma unroll 1
@@ -708,10 +747,8 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
           ptx::f32x2 ee[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int t = tok + i * 8 + 2 * (lane & 3);
-            const float2 h2 = *reinterpret_cast<const float2*>(&sm.ghi[s][t]);
-            const float2 l2 = *reinterpret_cast<const float2*>(&sm.glo[s][t]);
-            ee[i] = ptx::pack2(ptx::ex2_approx(h2.x + l2.x), ptx::ex2_approx(h2.y + l2.y));
+            const float2 f = *reinterpret_cast<const float2*>(&sm.in[s][tok + i * 8 + 2 * (lane & 3)]);
+            ee[i] = ptx::pack2(f.x, f.y);
           }
 #pragma unroll 1
           for (uint32_t ch0 = 0; ch0 < 32; ch0 += 16) {  // 16 channels x 32 tokens
@@ -783,8 +820,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
 #pragma unroll 1
     for (int n = 0; take(n, c); ++n) {
       const int s = n % kStages;
-      if (!wait(&sm.sc_full, n & 1) || (n >= 2 && !wait(&sm.p_empty[n & 1], ((n >> 1) - 1) & 1)))
-        break;
+      if (!wait(&sm.sc_full, n & 1)) break;  // (the last P has been read)
       ptx::tc_fence_after();
       const int row = w * 16 + g;
       const ptx::f32x2 gh[2] = {ptx::pack2(sm.ghi[s][row], sm.ghi[s][row]),
@@ -798,7 +834,7 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
         ptx::tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(r[j]));
-        uint32_t o[8];
+        uint32_t o[2][8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int col = c0 + 8 * i + 2 * t4;
@@ -816,21 +852,24 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
                          y0, y1);
             y0 = col <= row + 8 * e ? y0 : 0.0f;
             y1 = col < row + 8 * e ? y1 : 0.0f;
-            o[2 * i + e] = pack_bf16(y0, y1);
+            split2(ptx::pack2(y0, y1), o[0][2 * i + e], o[1][2 * i + e]);
           }
         }
         // matrices (rows 0-7, 8-15) x (two groups of 8 columns)
         const int at = w * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int blk = c0 / 8 + 2 * i + (lane >> 4);
-          ptx::st_matrix4(base + M::P + (n & 1) * 8192 + at * 128 + ((blk ^ (at & 7)) << 4), o[4 * i],
-                          o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        }
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int blk = c0 / 8 + 2 * i + (lane >> 4);
+            const uint32_t* x = &o[part][4 * i];
+            ptx::st_matrix4(base + M::P + part * 8192 + at * 128 + ((blk ^ (at & 7)) << 4), x[0], x[1],
+                            x[2], x[3]);
+          }
       }
       ptx::tc_fence_before();  // the scores are read, too
       ptx::fence_proxy_async_smem();
-      arrive(&sm.p_full[n & 1]);
+      arrive(&sm.p_full);
       if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
     }
   }
