@@ -419,9 +419,9 @@ decay_tc_kernel(const __grid_constant__ Maps maps, const DecayParams p, int seg,
 #pragma unroll
           for (int i = 0; i < D / 4; ++i) {
             float x = 0.0f, y = 0.0f;
-            if (c.entry) {
-              x = __ldg(c.entry + at + (2 * i) * D);
-              y = __ldg(c.entry + at + (2 * i + 1) * D);
+            if (c.entry) {  // (the scan may write it while this kernel runs: no read-only loads)
+              x = __ldcg(c.entry + at + (2 * i) * D);
+              y = __ldcg(c.entry + at + (2 * i + 1) * D);
             }
             st[i] = ptx::pack2(x, y);
           }
