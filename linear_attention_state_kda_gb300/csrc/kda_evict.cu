@@ -77,7 +77,7 @@ weigh_kernel(const WeighParams p, int cs, int cap_keys) {
   uint2* frag = reinterpret_cast<uint2*>(wsm);
   float* score = reinterpret_cast<float*>(wsm + (size_t)P * NT * KC * 256);
   const int stride = cap_keys + 4;
-  __shared__ float row_mul[ROWS];          // scale * log2 e * 2^e of a query row
+  __shared__ float row_mul[ROWS];          // 2^e of a query row
   __shared__ float2 part[kWMaxWarps][ROWS];
   __shared__ float2 cta_ml[ROWS];
   __shared__ float row_lse[ROWS];
@@ -100,7 +100,8 @@ weigh_kernel(const WeighParams p, int cs, int cap_keys) {
   const int pg0 = min(pages, rank * per), pg1 = min(pages, pg0 + per);
   const int32_t* table = p.table + (int64_t)b * p.max_pages;
 
-  // Ids and scales of the warp's pages pg0 + warp + warps * k: lane l has those of k = base + l.
+  // Ids and scales (times scale log2 e) of the warp's pages pg0 + warp + warps * k: lane l has those
+  // of k = base + l.
   int id_l = -1, have = -1;
   float ks_l = 0.0f;
   auto fetch = [&](int k) {  // (k the same in all lanes)
@@ -112,7 +113,7 @@ weigh_kernel(const WeighParams p, int cs, int cap_keys) {
       if (p.status) atomicOr(p.status, KDA_STATUS_BAD_PAGE);
       id_l = -1;
     }
-    ks_l = id_l < 0 ? 0.0f : p.ks[(int64_t)id_l * p.Hkv + h];
+    ks_l = id_l < 0 ? 0.0f : p.ks[(int64_t)id_l * p.Hkv + h] * (p.scale * kLog2e);
   };
   {  // (the first pages' ids on their way before the queries)
     const int pg = pg0 + warp + warps * lane;
@@ -157,10 +158,8 @@ weigh_kernel(const WeighParams p, int cs, int cap_keys) {
           dst[(size_t)NT * KC * 128 + el] = __float2half_rn(lo);
         }
       }
-      if (lane == 0) {
-        // scale and 2^e in two factors: e may be below the normal range
-        row_mul[r] = p.scale * kLog2e * pow2f(e < -126 ? -126 : e) * (e < -126 ? pow2f(e + 126) : 1.0f);
-      }
+      // (2^e may be below the normal numbers, and nothing but a power of two is exact there)
+      if (lane == 0) row_mul[r] = pow2f(e < -126 ? -126 : e) * (e < -126 ? pow2f(e + 126) : 1.0f);
     }
     __syncthreads();
 

@@ -43,10 +43,14 @@ __device__ __forceinline__ uint32_t finite_abs_bits(float x) {
   const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
   return b < 0x7f800000u ? b : 0u;
 }
-// Exponent of the smallest power of two s with m <= 448 s = 1.75 * 2^8 s, at least -100, from
-// the bits of m >= 0.
+// Exponent of the smallest power of two s with m <= 448 s = 1.75 * 2^8 s, from the bits of m >= 0
+// (for m below the normal numbers -135 or -134).
+__device__ __forceinline__ int exponent_of(uint32_t mbits) {
+  return (int)(mbits >> 23) - 127 - 8 + ((mbits & 0x7fffffu) > 0x600000u ? 1 : 0);
+}
+// The same of a page's scale: at least -100.
 __device__ __forceinline__ int scale_exponent(uint32_t mbits) {
-  const int e = (int)(mbits >> 23) - 127 - 8 + ((mbits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  const int e = exponent_of(mbits);
   return e < -100 ? -100 : e;
 }
 // 2^e for -126 <= e <= 127.

@@ -45,9 +45,9 @@ struct Smem {
 };
 struct Small {
   uint64_t full[kStages], empty[kStages], d_full[2], d_empty[2], drain;
-  float ks[kStages][2];             // of a step's pages; 0 where there is none
+  float ks[kStages][2];             // scale log2(e) times a step's pages' scales; 0 where there is none
   int page[kStages][2];             // -1: none
-  alignas(16) float2 row[kRows];    // scale log2(e) 2^e, and minus lse
+  alignas(16) float2 row[kRows];    // 2^e, and minus lse
   float2 late[kRows];               // statistics of the second half of the ranges
   float part[2][3][kTile];          // sums over the last three quarters of the rows
   uint32_t tmem;
@@ -162,8 +162,9 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, co
       const uint32_t row_lanes = 0xffu << (lane & 24);
       m = __reduce_max_sync(row_lanes, m);
       bad = __any_sync(row_lanes, bad);
-      // 2^e, the smallest power of two with m <= 448 2^e, at least 2^-100
-      const int e = scale_exponent(m);
+      // 2^e, the smallest power of two with m <= 448 2^e, at least 2^-126: bf16 ends at 2^-133, so that
+      // smaller rows are multiples of 2^-7 after it, which two parts hold
+      const int e = max(exponent_of(m), -126);
 #pragma unroll
       for (int c = 0; c < 16; ++c) f[c] *= pow2f(-e);
       const uint32_t off = base + Smem::Q + (r >> 7) * (128 * D) + (r & 127) * D +
@@ -190,7 +191,7 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, co
       }
       // a row with an infinity or NaN has no weights but NaN
       if (piece == 0)
-        sm.row[r].x = bad ? __int_as_float(0x7fffffff) : p.scale * kLog2e * pow2f(e);
+        sm.row[r].x = bad ? __int_as_float(0x7fffffff) : pow2f(e);
     }
     // the rows' statistics, by two threads a row
     const int mine = (int)threadIdx.x - 128, row = mine & (kRows - 1);
@@ -247,7 +248,8 @@ weigh_tc_kernel(const __grid_constant__ CUtensorMap map, const WeighParams p, co
               if (p.status) atomicOr(p.status, KDA_STATUS_BAD_PAGE);
               id = -1;
             }
-            ks = id < 0 ? 0.0f : p.ks[(int64_t)id * p.Hkv + h];
+            // (with the page's scale, not with 2^e, which it could bring below the normal numbers)
+            ks = id < 0 ? 0.0f : p.ks[(int64_t)id * p.Hkv + h] * (p.scale * kLog2e);
           }
           const int a = __shfl_sync(0xffffffffu, id, from);
           const int c = __shfl_sync(0xffffffffu, id, from + 1);

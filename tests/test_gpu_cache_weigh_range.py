@@ -1,4 +1,5 @@
-"""kda_cache_weigh where scores are far apart, key by key.
+"""kda_cache_weigh where scores are far apart, key by key, and at the ends of the ranges of queries and
+key scales.
 
 A score is off by at most ds = 2^-16 of its sum of absolute products (3/2 of that with more than 64
 query rows; their largest over the row's keys is taken for all), so a weight p = exp(s - lse) lies
@@ -14,7 +15,7 @@ import serving_ref as ref
 from kda_testutil import f64
 from linear_attention_state_kda_gb300 import kda
 from test_gpu_cache_attention import DEV, _i32, _make
-from test_gpu_cache_weigh import _weights
+from test_gpu_cache_weigh import _weights, check
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +69,22 @@ def test_one_key_takes_all(W, d, dtype):
     got = f64(got)
     off = 2.0 ** -18 * hi + 1e-37
     assert (got >= lo - off).all() and (got <= hi + off).all()
+
+
+@pytest.mark.parametrize("down,up", [(-126, 122), (-126, 110), (-120, 100), (-95, 60), (100, -90)])
+@pytest.mark.parametrize("W,d,dtype", [(2, 128, "bf16"), (40, 128, "bf16"), (5, 64, "bf16"),
+                                       (2, 128, "f32")])
+def test_small_queries_and_large_scales(W, d, dtype, down, up):
+    """Queries near the ends of fp32's range (bf16 entries below the normal range among them) and key
+    scales that bring the scores back."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(42)
+    start = [300, 65]
+    q, table, pool = _make(gen, start, W, 8, 2, d, dtype)
+    q = (q.double() * 2.0 ** down).to(q.dtype)
+    ks = (pool[1].double() * 2.0 ** up).float()
+    before = _weights(pool[0].shape[0], 2)
+    got = before.clone()
+    scale = 0.3 * d ** -0.5 * 2.0 ** (-down - up)
+    kda.cache_weigh(q, _i32(start), table, pool[0], ks, got, scale=scale)
+    check(q, start, None, table, [pool[0], ks], before, got, scale, 1.0)
