@@ -38,6 +38,9 @@ namespace {
 // of codes); 16 rows of 8192 with 4 query tokens 48 us; the same with 2 in fp32 35 us; 2 rows of 100
 // 8.9 us, which is latency: ids, codes, the cluster's two barriers.
 constexpr int kWThreads = 128, kWMaxWarps = kWThreads / 32;
+// Query rows whose statistics the two launches keep at a time (a window of more takes further pairs):
+// the workspace does not grow with the window past 8 KB for each range of keys. A multiple of 32.
+constexpr int kStatRows = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -62,11 +65,11 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
 
 // NT: tiles of 8 query rows scored at once. P: f16 parts of a query. How a unit's keys are shared:
 // by a cluster of `cs` CTAs, or by `cs` CTAs of a launch that takes the statistics and of one that sums
-// the weights.
+// the weights, each for query rows row0 .. row0 + stat_rows - 1 (a cluster takes all).
 enum Share { kCluster, kStats, kWeights };
 template <int D, int NT, int P, class T, Share kShare>
 __global__ void __launch_bounds__(kWThreads, NT == 1 ? 6 : 4)
-weigh_kernel(const WeighParams p, int cs, int cap_keys) {
+weigh_kernel(const WeighParams p, int cs, int cap_keys, int row0, int stat_rows) {
   constexpr int KC = D / 16;      // 16-channel steps
   constexpr int LB = D / 4;       // bytes of a key per lane
   constexpr int ROWS = NT * 8;
@@ -90,7 +93,7 @@ weigh_kernel(const WeighParams p, int cs, int cap_keys) {
   int n = start < 0 ? 0 : p.lens ? p.lens[b] : p.window;
   n = n < 0 ? 0 : n > p.window ? p.window : n;
   if (n == 0) return;  // the whole cluster
-  const int G = p.Hq / p.Hkv, R = n * G;
+  const int G = p.Hq / p.Hkv, R = kShare == kCluster ? n * G : min(n * G, row0 + stat_rows);
   const int64_t most = (int64_t)p.max_pages * kPage;  // at most 2^30
   const int keys = (int)((int64_t)start + n < most ? (int64_t)start + n : most);
   if (kShare != kWeights && rank == 0 && tid == 0 && h == 0 && p.status && (int64_t)start + n > most)
@@ -120,7 +123,7 @@ weigh_kernel(const WeighParams p, int cs, int cap_keys) {
     if (pg < pg1) asm volatile("prefetch.global.L1 [%0];" ::"l"(table + pg));
   }
 
-  for (int r0 = 0; r0 < R; r0 += ROWS) {
+  for (int r0 = kShare == kCluster ? 0 : row0; r0 < R; r0 += ROWS) {
     const int rows = min(ROWS, R - r0);
     __syncthreads();
     // the group's query rows: scale, then fragments. A warp takes a row.
@@ -291,7 +294,7 @@ weigh_kernel(const WeighParams p, int cs, int cap_keys) {
       const bool none = r >= rows || (s.x == -INFINITY && !(s.y != s.y));
       row_lse[r] = none ? INFINITY : (s.x == -INFINITY ? 0.0f : s.x) + log2f(s.y);
     };
-    float2* stats = kShare == kCluster ? nullptr : p.stats + (int64_t)bh * cs * p.max_rows + r0;
+    float2* stats = kShare == kCluster ? nullptr : p.stats + (int64_t)bh * cs * stat_rows + (r0 - row0);
     if (kShare != kWeights) {
 #pragma unroll
       for (int i = 0; i < NT; ++i)
@@ -310,7 +313,7 @@ weigh_kernel(const WeighParams p, int cs, int cap_keys) {
         const float2 s = of_row(w < kWMaxWarps ? part[w][r] : make_float2(-INFINITY, 0.0f));
         if (w == 0) {
           if (kShare == kCluster) cta_ml[r] = s;
-          else if (r < rows) stats[(int64_t)rank * p.max_rows + r] = s;
+          else if (r < rows) stats[(int64_t)rank * stat_rows + r] = s;
         }
       }
     }
@@ -329,7 +332,7 @@ weigh_kernel(const WeighParams p, int cs, int cap_keys) {
         const int r = i >> 4;
         float2 s = make_float2(-INFINITY, 0.0f);
         for (int c = i & 15; c < cs && r < rows; c += 16)
-          s = join(s, stats[(int64_t)c * p.max_rows + r]);
+          s = join(s, stats[(int64_t)c * stat_rows + r]);
         s = of_row(s);
         if ((i & 15) == 0) set_lse(r, s);
       }
@@ -442,9 +445,12 @@ kda_status launch_weigh_nt(const WeighParams& p, cudaStream_t s) {
   }
   const unsigned grid = (unsigned)(units * sh.cs);
   if (!sh.cluster) {
-    weigh_kernel<D, NT, P, T, kStats><<<grid, kWThreads, frag, s>>>(p, sh.cs, 0);
-    weigh_kernel<D, NT, P, T, kWeights><<<grid, kWThreads, frag, s>>>(p, sh.cs, 0);
-    count_launches(2);
+    const int at_once = p.max_rows < kStatRows ? p.max_rows : kStatRows;
+    for (int r = 0; r < p.max_rows; r += at_once) {
+      weigh_kernel<D, NT, P, T, kStats><<<grid, kWThreads, frag, s>>>(p, sh.cs, 0, r, at_once);
+      weigh_kernel<D, NT, P, T, kWeights><<<grid, kWThreads, frag, s>>>(p, sh.cs, 0, r, at_once);
+      count_launches(2);
+    }
     return check_launch("kda_cache_weigh");
   }
   const int64_t rows64 = (int64_t)(p.Hq / p.Hkv) * p.window;
@@ -463,7 +469,7 @@ kda_status launch_weigh_nt(const WeighParams& p, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, weigh_kernel<D, NT, P, T, kCluster>, p, sh.cs, (int)(cap * kPage));
+  cudaLaunchKernelEx(&cfg, weigh_kernel<D, NT, P, T, kCluster>, p, sh.cs, (int)(cap * kPage), 0, 0);
   count_launches(1);
   return check_launch("kda_cache_weigh");
 }
@@ -810,8 +816,9 @@ __global__ void __launch_bounds__(kMThreads) evict_move_kernel(const EvictParams
 size_t cache_weigh_workspace_bytes(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d,
                                    int max_pages) {
   if (weigh_tc_applies(dt, window, Hq, Hkv, d)) return cache_weigh_tc_workspace(batch, window, Hq, Hkv);
-  const Sharing sh = sharing_of(batch, Hkv, Hq / Hkv * window, max_pages);
-  return sh.cluster ? 0 : (size_t)batch * Hkv * sh.cs * (Hq / Hkv) * window * sizeof(float2);
+  const int rows = Hq / Hkv * window;
+  const Sharing sh = sharing_of(batch, Hkv, rows, max_pages);
+  return sh.cluster ? 0 : (size_t)batch * Hkv * sh.cs * (rows < kStatRows ? rows : kStatRows) * sizeof(float2);
 }
 
 kda_status launch_cache_weigh(const WeighParams& p, kda_dtype dt, int d, cudaStream_t s) {

@@ -1,5 +1,5 @@
 """kda_cache_weigh where scores are far apart, key by key, and at the ends of the ranges of queries and
-key scales.
+key scales; and windows of many query rows over wide tables.
 
 A score is off by at most ds = 2^-16 of its sum of absolute products (3/2 of that with more than 64
 query rows; their largest over the row's keys is taken for all), so a weight p = exp(s - lse) lies
@@ -88,3 +88,19 @@ def test_small_queries_and_large_scales(W, d, dtype, down, up):
     scale = 0.3 * d ** -0.5 * 2.0 ** (-down - up)
     kda.cache_weigh(q, _i32(start), table, pool[0], ks, got, scale=scale)
     check(q, start, None, table, [pool[0], ks], before, got, scale, 1.0)
+
+
+@pytest.mark.parametrize("W,Hq", [(150, 16), (21, 400)])
+def test_many_rows_in_two_launches(W, Hq):
+    """Wide tables, and more query rows than the statistics are kept of at a time."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(43)
+    start, lens = [130, -1, 64, 3], [W, 4, W - 1, 1]
+    q, table, pool = _make(gen, start, W, Hq, 2, 64, "f32")
+    wide = torch.full((4, 600), -1, dtype=torch.int32, device=DEV)
+    wide[:, :table.shape[1]] = table
+    assert kda.cache_weigh_workspace(q.dtype, 4, W, Hq, 2, 64, 600) > 0
+    before = _weights(pool[0].shape[0], 2)
+    got = before.clone()
+    kda.cache_weigh(q, _i32(start), wide, pool[0], pool[1], got, scale=0.04, lens=_i32(lens), keep=0.5)
+    check(q, start, lens, wide, pool, before, got, 0.04, 0.5)
