@@ -497,7 +497,8 @@ constexpr int kEThreads = 512;
 constexpr int kEWarps = kEThreads / 32;
 constexpr int kEBins = 2048;
 static_assert(kEThreads * 4 >= kEBins, "a thread adds up four bins");
-constexpr int kEMaxKeys = 49152;  // of a CTA in shared memory; later ones are read again
+constexpr int kEMaxKeys = 49152;  // of a CTA in shared memory, tiles of 128; later ones are read again
+static_assert(kEMaxKeys % 128 == 0, "whole tiles");
 
 // Orders like the weights; NaN lowest, zeros of both signs equal. 0 is no candidate.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -835,7 +836,8 @@ kda_status launch_cache_evict(const EvictParams& p, int d, cudaStream_t s) {
   // and 263 with 4096; 8 rows of 32768: 133, 135 and 162 us.
   int cs = 1;
   while (cs < 8 && (int64_t)p.max_pages * kPage > (int64_t)cs * 8192) cs *= 2;
-  const int64_t per = ((int64_t)p.max_pages + cs - 1) / cs * kPage;
+  // room for whole tiles of 128 keys (64 rows of one page: 34 us, with the keys read again 40)
+  const int64_t per = (((int64_t)p.max_pages + cs - 1) / cs * kPage + 127) / 128 * 128;
   const int cap = (int)(per < kEMaxKeys ? per : kEMaxKeys);
   static bool set[64] = {};
   int dev = 0;
