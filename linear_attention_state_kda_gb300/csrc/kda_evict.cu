@@ -166,6 +166,11 @@ weigh_kernel(const WeighParams p, int cs, int cap_keys, int row0, int stat_rows)
     }
     __syncthreads();
 
+    // Codes that the second launch reads again stay in L2 where they fit: 2 rows of 65536 tokens 48 us,
+    // marked to be evicted first 54; 64 fp32 tokens over one row of 32768 673 and 706. (The same for a
+    // cluster's further query rows, asked at run time: 64 tokens over 16 rows of 2048 at d = 64 169 us for
+    // 187, but 8 tokens over 16 rows of 8192, which have none, 99 for 93.)
+    constexpr bool read_again = kShare == kStats;
     // the last token of the group sees the most, its first token the least
     const int seen = (int)min((int64_t)keys, (int64_t)start + (r0 + rows - 1) / G + 1);
     const int64_t seen_by_all = (int64_t)start + r0 / G + 1;
@@ -194,8 +199,10 @@ weigh_kernel(const WeighParams p, int cs, int cap_keys, int row0, int stat_rows)
         for (int half = 0; half < 2; ++half)
 #pragma unroll
           for (int i = 0; i < LB / 16; ++i)
-            *reinterpret_cast<uint4*>(&w[t][half][4 * i]) = __ldcs(
-                reinterpret_cast<const uint4*>(base + (t * 16 + 8 * half) * D + 64 * i));
+          {
+            const uint4* src = reinterpret_cast<const uint4*>(base + (t * 16 + 8 * half) * D + 64 * i);
+            *reinterpret_cast<uint4*>(&w[t][half][4 * i]) = read_again ? *src : __ldcs(src);
+          }
 #pragma unroll
       for (int t = 0; t < BT; ++t) {
 #pragma unroll
