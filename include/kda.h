@@ -646,7 +646,7 @@ KDA_API kda_status kda_decay_window(kda_dtype dt, int batch, int window, int H, 
  *               none), 256-byte aligned; contents need not be initialised.
  *   Other arguments, limits and status as for kda_cache_attention.
  * Scores and sums are fp32 and the same on every run. bf16 queries enter at full precision (in windows
- * of more than 64 query rows per key/value head at d = 128: to 2^-20 of the query's largest entry),
+ * of more than 64 query rows per key/value head at d = 128: to 2^-21 of the query's largest entry),
  * fp32 ones as two 11-bit parts.
  */
 KDA_API size_t kda_cache_weigh_workspace(kda_dtype dt, int batch, int window, int Hq, int Hkv, int d,

@@ -1682,7 +1682,7 @@ bool make_map_rows(CUtensorMap* m, const void* ptr, bool f32, uint64_t cols, uin
 }
 
 bool make_map_tokens(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows,
-                     uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows, bool swizzle) {
+                     uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
@@ -1690,8 +1690,7 @@ bool make_map_tokens(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t ro
   cuuint32_t box[2] = {box_cols, box_rows};
   cuuint32_t estr[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE,
-             swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -356,16 +356,18 @@ decay_scan_kernel(const DecayParams p, int seg, float* added, const float* added
   }
 }
 
-// Tokens of a segment: so that all heads' segments are one per SM (bf16) or four (CUDA cores: 64 value
-// columns each), but not so few that the state that a segment has to write and read outweighs them.
-// bf16, 65536 tokens x 4 heads: 95 us, with two per SM 115; 16384 x 32: 178 and 175; 40 prompts up to
-// 1000 x 16: 87 and 107. At least 256 tokens: 2048 x 8 29 us, with 512 37; 8192 x 2 31 us, with 128 37.
-// (But 300 x 4 17 us in one, 23 in two.)
-// fp32, 5 prompts up to 1301 x 6: 51 us, with 256 tokens at least 91; 8192 x 16: 743, with half as
-// many 803, with twice as many 833 (before its rows were asked for ahead).
+// Tokens of a segment: so that all heads' segments are at most one per SM (bf16) or four (CUDA cores:
+// 64 value columns each), but not so few that the state that a segment has to write and read outweighs
+// them. bf16, with one per SM and with two: 65536 tokens x 4 heads 99 and 115 us, 40 prompts up to 1000
+// x 16 heads 95 and 112; where heads do not divide the SMs, segments are missing: 16384 x 32 180 and 178,
+// x 40 230 and 217, x 64 336 and 349, x 80 (one segment, half of the SMs) 456 and 452. At least 256
+// tokens: 2048 x 8 29 us, with 512 37; 8192 x 2 31 us, with 128 36, with 512 37. (But 300 x 4 17 us in
+// one, 22 in three.)
+// fp32, 5 prompts up to 1301 x 6: 50 us, with 256 tokens at least 84; 8192 x 16: 605, with half as
+// many segments 650, with twice as many 671.
 int segment_tokens(kda_dtype dt, int total, int H, int d) {
   const int64_t units = (int64_t)H * (dt == KDA_BF16 ? 1 : d / kCols);
-  const int64_t all = dt == KDA_BF16 ? 152 : 608, want = units < all ? all / units : 1;
+  const int64_t all = dt == KDA_BF16 ? kSms : 4 * kSms, want = units < all ? all / units : 1;
   const int64_t seg = ((total + want - 1) / want + 63) / 64 * 64;
   const int64_t least = dt != KDA_BF16 ? 64 : total > 512 ? 256 : 512;
   return (int)(seg < least ? least : seg);

@@ -1202,10 +1202,10 @@ kda_status launch_d(const DecayParams& p, int seg, float* added, float* added_lo
   const uint64_t rows = p.total > 0 ? (uint64_t)p.total : 1;
   // (without tokens nothing is loaded: the maps are not used)
   if (p.total > 0 &&
-      !(make_map_tokens(&m.q, p.q, (uint64_t)p.Hk * D, rows, (uint64_t)p.qs * 2, 64, kC, true) &&
-        make_map_tokens(&m.k, p.k, (uint64_t)p.Hk * D, rows, (uint64_t)p.ks * 2, 64, kC, true) &&
-        make_map_tokens(&m.v, p.v, (uint64_t)p.H * D, rows, (uint64_t)p.vs * 2, 64, kC, true) &&
-        make_map_tokens(&m.o, p.o, (uint64_t)p.H * D, rows, (uint64_t)p.H * D * 2, 64, kC, true)))
+      !(make_map_tokens(&m.q, p.q, (uint64_t)p.Hk * D, rows, (uint64_t)p.qs * 2, 64, kC) &&
+        make_map_tokens(&m.k, p.k, (uint64_t)p.Hk * D, rows, (uint64_t)p.ks * 2, 64, kC) &&
+        make_map_tokens(&m.v, p.v, (uint64_t)p.H * D, rows, (uint64_t)p.vs * 2, 64, kC) &&
+        make_map_tokens(&m.o, p.o, (uint64_t)p.H * D, rows, (uint64_t)p.H * D * 2, 64, kC)))
     return set_error(KDA_ERR_CUDA, "kda_decay_prefill: cuTensorMapEncodeTiled failed");
   constexpr int out_bytes = Out<D>::SMALL + (int)sizeof(OutSmall);
   constexpr int add_bytes = Add<D>::SMALL + (int)sizeof(AddSmall);

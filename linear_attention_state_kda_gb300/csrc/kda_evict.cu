@@ -423,7 +423,7 @@ struct Sharing {
 Sharing sharing_of(int batch, int Hkv, int rows, int max_pages) {
   const int64_t units = (int64_t)batch * Hkv;
   if (units < 32 && max_pages >= 512) {
-    const int64_t most = 152 * (rows <= 8 ? 6 : 4) / units, cs = max_pages / 4;
+    const int64_t most = kSms * (rows <= 8 ? 6 : 4) / units, cs = max_pages / 4;
     return {false, (int)(cs < most ? cs : most)};
   }
   // a cluster: up to 2048 keys to a CTA (128 rows of 16384 tokens, 8 heads: 280 us; with 8192, 314;

@@ -75,9 +75,9 @@ bool chunk_tc_available();
 bool make_map_rows(CUtensorMap* m, const void* ptr, bool f32, uint64_t cols, uint64_t rows,
                    uint32_t box_cols, uint32_t box_rows);
 // A bf16 array of `rows` rows of `cols` contiguous entries, row_bytes apart (a multiple of 16), as a
-// 2-D tensor map, box [box_rows][box_cols], plain or with the 128-byte swizzle (box_cols 64).
+// 2-D tensor map, box [box_rows][box_cols = 64] with the 128-byte swizzle.
 bool make_map_tokens(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows,
-                     uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows, bool swizzle);
+                     uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows);
 // The codes of a paged cache, [slices = n_pages * Hkv][64][d = 128] bytes, box one slice, with the
 // 128-byte swizzle.
 bool make_map_pages(CUtensorMap* m, const void* ptr, uint64_t d, uint64_t slices);
@@ -195,6 +195,10 @@ struct VerifyParams {
   uint32_t* status;
 };
 kda_status launch_verify(const VerifyParams& p, kda_dtype dt, cudaStream_t s);
+
+// SMs of a GB300, for the cuts of work that sizes of workspaces and the order of sums depend on: both
+// are the same whatever device, or none, is current. Where only the time depends on it, it is asked.
+constexpr int kSms = 152;
 
 // Linear attention with one decay per head: S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.
 struct DecayParams {
