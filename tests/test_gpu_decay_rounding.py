@@ -58,8 +58,10 @@ def test_terms_that_cancel(what, d):
 def test_largest_entries(d):
     """States and weighted products next to the end of bf16's range: no part overflows."""
     q, k, v, g, cu, s0 = make([130], 2, 2, d, "bf16", seed=34)
-    # (the largest state of these is about 2^127.8, which rounds to an infinity in one bf16)
-    s0 = s0 / s0.abs().amax() * 3.4e38 * (torch.arange(d, device=s0.device) % 7 == 0)[:, None]
+    # (the largest entry of these is past the largest bf16 by more than half a step)
+    s0 = s0 * (torch.arange(d, device=s0.device) % 7 == 0)[:, None]
+    s0 = s0 / s0.abs().amax() * 3.4e38
+    assert torch.isinf(s0.bfloat16()).any() and torch.isfinite(s0).all()
     q = (q.float() * 2.0 ** -40).bfloat16()
     g = g.clone()
     g[:, :] = -0.7
