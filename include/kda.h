@@ -639,7 +639,7 @@ KDA_API kda_status kda_decay_window(kda_dtype dt, int batch, int window, int H, 
  * (the window's own tokens) begin at the sum alone, and so does everything with keep = 0: what
  * their entries held does not matter.
  *   weights     [n_pages, Hkv, 64] fp32, 16-byte aligned, updated in place. Other entries are not
- *               touched. No page may be named by two rows of one call.
+ *               touched. No page may be named twice by the present positions of a call's rows.
  *   A query none of whose positions is present adds nothing. Codes that a query does not see do not
  *   reach its weights, NaN included.
  *   workspace   at least kda_cache_weigh_workspace(...) bytes (0 for sizes that are refused or need
