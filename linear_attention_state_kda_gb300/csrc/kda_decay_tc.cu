@@ -20,8 +20,8 @@
 //
 // 16384 tokens x 32 heads (d = 128): 180 us, of which what the segments add takes 55, the scan 7
 // and the outputs 120 (with S and P in one part each 163 and 105). The outputs move 537 MB in that, 4.5
-// TB/s; a chunk takes some 3500 cycles: 2300 in which the warp that issues has products to issue (44,
-// of which the three parts of V' are a third and half of the tensor time), the rest its looks at
+// TB/s; a chunk takes some 3500 cycles: 2300 in which the warp that issues has products to issue (44;
+// the three parts of V' are 12 of them and nearly half of the tensor time), the rest its looks at
 // barriers and its waits for the last chunk's outputs and the state's parts, whose warps share the issue
 // slots. Measured and left: both parts of the state in TMEM, the scores in the second sum's columns
 // (205 us: P and the outputs then wait for one another); the two parts of S^T Q^T behind barriers of

@@ -198,8 +198,7 @@ weigh_kernel(const WeighParams p, int cs, int cap_keys, int row0, int stat_rows)
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
-          for (int i = 0; i < LB / 16; ++i)
-          {
+          for (int i = 0; i < LB / 16; ++i) {
             const uint4* src = reinterpret_cast<const uint4*>(base + (t * 16 + 8 * half) * D + 64 * i);
             *reinterpret_cast<uint4*>(&w[t][half][4 * i]) = read_again ? *src : __ldcs(src);
           }
