@@ -413,8 +413,8 @@ weigh_kernel(const WeighParams p, int cs, int cap_keys, int row0, int stat_rows)
 }
 
 // CTAs that share a unit's keys. Few units with long contexts take two launches: 16 units of 65536
-// tokens 106 us as clusters, 55 so; 16 units of 32768 with 16 query rows 90 and 48; but 32 units of
-// 32768 47 and 58, 32 of 8192 19 and 31. One CTA of a wave to a range: 6 per SM, 4 with more rows.
+// tokens 106 us as clusters, 49 so; 16 units of 32768 with 16 query rows 90 and 40; but 32 units of
+// 32768 47 and 54, 32 of 8192 19 and 25, 8 of 8192 17 and 21. One CTA of a wave to a range: 6 per SM, 4 with more rows.
 struct Sharing {
   bool cluster;
   int cs;
